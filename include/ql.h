@@ -319,6 +319,86 @@ int ql_paged_attn_decode_kvq(const void* d_q, const void* d_pool, const int32_t*
                              float scale, void* d_out, void* d_workspace, size_t workspace_bytes,
                              void* stream);
 
+/* --------------------------------------------------------------- 4-bit KV pool
+ * Keys and values in 4 bits, 5 with their scales (f16: 16; q8_0 keys and q5_1 values: 7.25). A
+ * row of head_dim values (64 or 128) is cut into 32-element blocks; a block keeps
+ *   m = f16(min x), d = f16((max x - min x) / 15), codes c = clamp(rint((x - m) / d), 0, 15)
+ * (0 where d = 0): each of the three rounded once, to nearest even, from its exact value, with m
+ * and d the stored f16 values. The values it stands for are d c + m.
+ * Layout: one record of ql_kv4_record_bytes(head_dim) = 20 * head_dim bytes per (physical block,
+ * kv head), a layer's pool [num_blocks][n_kv][record], 16-byte aligned. With nb = head_dim / 32,
+ * slot s (0..15) of the block and element 32 b + e of a row (e < 32), a record holds:
+ *   key codes at byte 0, 16 rows of head_dim / 2: byte 4 (nb j + b) + i of a row has the codes of
+ *     e = 4 j + i (low four bits) and e = 4 j + i + 16 (high), i, j < 4;
+ *   value codes at 8 head_dim, 16 rows of head_dim / 2: the little-endian 16-bit word at byte
+ *     2 (nb u + b) of a row has the codes of e = w, w + 8, w + 16, w + 24 (lowest bits first) with
+ *     w < 8, u = w (head_dim 64) or w ^ (4 * bit 1 of s) (head_dim 128);
+ *   key d f16 [16][nb] at 16 head_dim, key m at 17 head_dim;
+ *   value d at 18 head_dim and value m at 19 head_dim, f16 number
+ *     4 nb (s % 4) + 2 nb (s / 8) + 2 b + (s / 4) % 2 each.
+ * (The order in which the attention's matrix instructions take them.) 0 for other head_dims.  */
+int64_t ql_kv4_record_bytes(int head_dim);
+/* Quantise rows of K and V into one layer's pool: row i of d_k / d_v, [n_kv_heads][head_dim] of
+ * dtype (QL_DTYPE_F32 or QL_DTYPE_F16), starts k_stride / v_stride elements after row i - 1 (a
+ * slice of a q|k|v projection, say), and goes to slot d_slots[i] % 16 of physical block
+ * d_slots[i] / 16 (int64 [n], device). A slot of -1 marks a row to leave out (a padded batch);
+ * any other slot outside the pool is skipped and recorded in the device error record, as is a
+ * non-finite value or an f16 overflow of a minimum or a scale (the row is still written). The
+ * slots of one call must differ from one another: of two rows for one slot, which bytes end
+ * there is not determined. d_k, d_v, d_pool and the strides' bytes are multiples of 16; strides
+ * at least n_kv_heads * head_dim (any when n is 1). n = 0 is allowed. Asynchronous on stream. */
+int ql_kv4_write(const void* d_k, const void* d_v, int dtype, int64_t k_stride, int64_t v_stride,
+                 const int64_t* d_slots, int64_t n, int n_kv_heads, int head_dim, void* d_pool,
+                 int64_t num_blocks, void* stream);
+/* The rows of d_slots read back, d c + m rounded once to dtype: row i to d_k / d_v
+ * (arguments as for ql_kv4_write; slots may repeat). Rows of slots outside the pool are left as
+ * they were, and recorded unless the slot is -1. Asynchronous on stream.                    */
+int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_heads, int head_dim,
+                int64_t num_blocks, void* d_k, void* d_v, int dtype, int64_t k_stride, int64_t v_stride,
+                void* stream);
+/* ql_paged_attn_decode over a 4-bit pool (d_pool: one layer, 16-byte aligned). Arguments and
+ * errors as for ql_paged_attn_decode, except that any group n_heads / n_kv_heads is taken, that
+ * keys of a block id outside the pool are left out of the softmax (and recorded), and that a
+ * sequence whose length is outside [0, max_blocks_per_seq * 16] (recorded) or 0 leaves its
+ * output row as it was. batch * n_heads < 2^31 / 128. Scores are exact f32 sums over the codes; the
+ * weights enter the value product as pairs of f16 (22 bits), all sums are f32.
+ * d_workspace: ql_paged_attn_kv4_workspace_bytes(...) bytes, 16-byte aligned, ZERO-FILLED before
+ * its first use; every call leaves it valid for a next call of any shape that it is large enough
+ * for. Calls (and captured graphs) that may run at the same time need workspaces of their own. */
+size_t ql_paged_attn_kv4_workspace_bytes(int64_t batch, int n_heads, int n_kv_heads, int head_dim,
+                                         int64_t max_blocks_per_seq);
+int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t* d_block_tables,
+                             const int32_t* d_context_lens, int64_t batch, int n_heads, int n_kv_heads,
+                             int head_dim, int block_size, int64_t max_blocks_per_seq, int64_t num_blocks,
+                             float scale, void* d_out, void* d_workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* --------------------------------------------------------------- token sampling
+ * The next token of each row of logits from one uniform number u in [0, 1) per row. Row b, with
+ * T = d_temperature[b], weights w_i = exp((l_i - max l) / T), tokens in order of falling logit
+ * (lowest index first on ties):
+ *   top-k  K = the first d_top_k[b] tokens of the order (0 or less: all);
+ *   top-p  P = the shortest prefix of K whose weight is at least d_top_p[b] times K's (1 or more:
+ *          all of K; always at least one token);
+ *   min-p  M = the tokens with l_i >= max l + T ln(d_min_p[b]) (0 or less: all; 1 or more: those
+ *          of the largest logit);
+ * the token drawn is the first index i at which the weight of the tokens of index <= i in K, P and
+ * M exceeds u times the weight of them all. T = 0 takes the arg max (lowest index). d_temperature,
+ * d_top_k, d_top_p and d_min_p are device arrays [batch] or NULL (T = 1, no filter).
+ * Logits: dtype (QL_DTYPE_F32 or QL_DTYPE_F16) [batch][vocab], rows row_stride elements apart, any
+ * alignment of their type. -inf and NaN are tokens that are never drawn, +inf counts as the
+ * largest finite value of f32. d_tokens int32 [batch]; d_probs f32 [batch] or NULL: the drawn token's
+ * share of the kept weight (1 where T = 0). A row with no token left gives token -1 and
+ * probability 0. So does a row whose T is negative, NaN or infinite, whose top_p or min_p is NaN
+ * or whose u is outside [0, 1), which is recorded in the device error record. d_active
+ * int32 [batch] or NULL: rows with 0 are left as they were. Weights are 40-bit fixed-point numbers
+ * (relative error 2^-30 before that rounding) and their sums exact, so that the outcome does not
+ * depend on the order of additions. 1 <= vocab <= 360448, batch < 2^31. Asynchronous on stream. */
+int ql_sample(const void* d_logits, int dtype, int64_t row_stride, int64_t batch, int64_t vocab,
+              const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+              const float* d_min_p, const float* d_uniform, const int32_t* d_active,
+              int32_t* d_tokens, float* d_probs, void* stream);
+
 /* How the context splits of a (sequence, kv head) are merged, for this process (every
  * attention entry point and the decode step; graphs keep the form they were captured with).
  * Both forms take the same online-softmax merge over the splits in order, so their outputs

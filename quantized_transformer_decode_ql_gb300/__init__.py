@@ -26,6 +26,8 @@ __all__ = [
     "ql_paged_attn_workspace_bytes", "ql_paged_attn_decode", "ql_paged_attn_decode_noalloc",
     "ql_paged_attn_chunk_workspace_bytes", "ql_paged_attn_chunk",
     "ql_kvq_record_bytes", "ql_kvq_write", "ql_paged_attn_decode_kvq",
+    "ql_kv4_record_bytes", "ql_kv4_write", "ql_kv4_read", "ql_paged_attn_kv4_workspace_bytes",
+    "ql_paged_attn_decode_kv4", "ql_sample",
     "ql_set_attn_merge_form", "ql_paged_attn_merge_form",
     "ql_kv_q8_0_row_bytes", "ql_kv_q5_1_row_bytes", "ql_kv_quantize_q8_0", "ql_kv_dequantize_q8_0",
     "ql_kv_quantize_q5_1", "ql_kv_dequantize_q5_1", "ql_kv_quantize_device", "ql_kv_dequantize_device",
@@ -215,6 +217,73 @@ def ql_paged_attn_decode_kvq(q, pool, block_tables, context_lens, batch, n_heads
                                          n_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
                                          ptr(out), ptr(workspace), workspace.numel() * workspace.element_size(),
                                          stream_ptr(stream)))
+
+
+def _dtype_of(name, *tensors):
+    """QL_DTYPE_* of tensors that have to share one type."""
+    import torch
+    types = {t.dtype for t in tensors}
+    if types == {torch.float32}:
+        return QL_DTYPE_F32
+    if types == {torch.float16}:
+        return QL_DTYPE_F16
+    raise QLError(QL_EINVAL, f"{name}: tensors must be all float32 or all float16, got {sorted(map(str, types))}")
+
+
+def _rows_of(name, t, n, n_kv_heads, head_dim):
+    """Row stride in elements of a [n, n_kv_heads, head_dim] (or [n, n_kv_heads * head_dim]) tensor whose rows are
+    contiguous."""
+    if t.numel() != n * n_kv_heads * head_dim or t.shape[0] != n:
+        raise QLError(QL_EINVAL, f"{name}: need {n} rows of {n_kv_heads} x {head_dim}, got {tuple(t.shape)}")
+    if n and not t[0].is_contiguous():
+        raise QLError(QL_EINVAL, f"{name}: the heads of a row must be contiguous")
+    return t.stride(0)
+
+
+def ql_kv4_record_bytes(head_dim):
+    return int(lib().ql_kv4_record_bytes(head_dim))
+
+
+def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=None):
+    """Quantise rows ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided) into one layer's 4-bit
+    pool at physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out)."""
+    n = slots.numel()
+    ks, vs = (_rows_of("ql_kv4_write", t, n, n_kv_heads, head_dim) for t in (k, v))
+    check(lib().ql_kv4_write(ptr(k), ptr(v), _dtype_of("ql_kv4_write", k, v), ks, vs, ptr(slots), n, n_kv_heads,
+                             head_dim, ptr(pool), num_blocks, stream_ptr(stream)))
+
+
+def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None):
+    """The values of ``slots`` read back into ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided)."""
+    n = slots.numel()
+    ks, vs = (_rows_of("ql_kv4_read", t, n, n_kv_heads, head_dim) for t in (k, v))
+    check(lib().ql_kv4_read(ptr(pool), ptr(slots), n, n_kv_heads, head_dim, num_blocks, ptr(k), ptr(v),
+                            _dtype_of("ql_kv4_read", k, v), ks, vs, stream_ptr(stream)))
+
+
+def ql_paged_attn_kv4_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_blocks_per_seq):
+    return int(lib().ql_paged_attn_kv4_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_blocks_per_seq))
+
+
+def ql_paged_attn_decode_kv4(q, pool, block_tables, context_lens, batch, n_heads, n_kv_heads, head_dim,
+                             block_size, max_blocks_per_seq, num_blocks, scale, out, workspace, stream=None):
+    """Single-token attention over a 4-bit pool; ``workspace``: a zero-filled byte tensor."""
+    check(lib().ql_paged_attn_decode_kv4(ptr(q), ptr(pool), ptr(block_tables), ptr(context_lens), batch, n_heads,
+                                         n_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
+                                         ptr(out), ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         stream_ptr(stream)))
+
+
+def ql_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
+              active=None, stream=None):
+    """Draw ``tokens`` (int32 [batch]) from ``logits`` (f32 or f16 [batch, vocab], rows may be strided) with one
+    ``uniform`` number (f32 [batch]) a row; the filters are device tensors [batch] (``top_k`` int32, the others
+    f32) or None. ``probs`` (f32 [batch]): the drawn tokens' probabilities."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise QLError(QL_EINVAL, "ql_sample: logits must be [batch, vocab] with contiguous rows")
+    check(lib().ql_sample(ptr(logits), _dtype_of("ql_sample", logits), logits.stride(0), logits.shape[0],
+                          logits.shape[1], ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(uniform),
+                          ptr(active), ptr(tokens), ptr(probs), stream_ptr(stream)))
 
 
 def ql_paged_attn_decode_noalloc(q, k_pool, v_pool, block_tables, context_lens, batch, n_heads,

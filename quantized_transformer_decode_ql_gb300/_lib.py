@@ -82,6 +82,16 @@ SIGNATURES = {
     "ql_kvq_write": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p, c_int64, c_void_p]),
     "ql_paged_attn_decode_kvq": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_int,
                                          c_int64, c_int64, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "ql_kv4_record_bytes": (c_int64, [c_int]),
+    "ql_kv4_write": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_int64, c_int, c_int, c_void_p,
+                             c_int64, c_void_p]),
+    "ql_kv4_read": (c_int, [c_void_p, c_void_p, c_int64, c_int, c_int, c_int64, c_void_p, c_void_p, c_int, c_int64,
+                            c_int64, c_void_p]),
+    "ql_paged_attn_kv4_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64]),
+    "ql_paged_attn_decode_kv4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_int,
+                                         c_int64, c_int64, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "ql_sample": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                          c_void_p, c_void_p, c_void_p, c_void_p]),
     "ql_paged_attn_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int, c_int64]),
     "ql_paged_attn_chunk_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int]),
     "ql_paged_attn_chunk": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int,

@@ -83,6 +83,8 @@ static const char* where_name(int w) {
         case kErrStepBarrier: return "persistent step: a grid barrier wait ran out (index = barrier, value = CTA)";
         case kErrKvNonFinite: return "KV row quantiser: non-finite value (index = row, value = block)";
         case kErrKvOverflow: return "KV row quantiser: block scale or minimum overflows f16 (index = row, value = block)";
+        case kErrKvSlot: return "KV rows: slot outside the pool (index = row, value = slot)";
+        case kErrSampleArg: return "sampling: temperature, top-p, min-p or uniform number out of range (index = row)";
         default: return "unknown";
     }
 }

@@ -48,6 +48,8 @@ enum DevErrWhere {
     kErrKvNonFinite = 10,
     kErrKvOverflow = 11,
     kErrMoeExpert = 12,
+    kErrKvSlot = 13,
+    kErrSampleArg = 14,
 };
 // The current device's record (allocated on first use, zero-filled).
 DevError* device_error_record();

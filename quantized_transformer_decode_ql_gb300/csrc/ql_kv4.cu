@@ -1,0 +1,232 @@
+// Rows of K and V quantised into the 4-bit pool as they are written, and read back.
+//
+// Both are bound by memory: a row of one kv head is 2 HD values in (or out) and 1.25 HD bytes out (or
+// in). HD / 8 neighbouring lanes share the (row, kv head): 8 key values and 8 value values a lane,
+// loaded before anything else, so that a full SM has 64 KB (f32) in flight.
+#include "ql_internal.h"
+#include "ql_kv4_rec.cuh"
+
+namespace ql {
+namespace {
+
+constexpr int kKv4Threads = 256;
+
+template <typename T>
+__device__ __forceinline__ void load2(const T* p, float& a, float& b);
+template <>
+__device__ __forceinline__ void load2<float>(const float* p, float& a, float& b) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+    a = v.x;
+    b = v.y;
+}
+template <>
+__device__ __forceinline__ void load2<__half>(const __half* p, float& a, float& b) {
+    const float2 v = __half22float2(__ldg(reinterpret_cast<const __half2*>(p)));
+    a = v.x;
+    b = v.y;
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* x);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, float* x) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void load4<__half>(const __half* p, float* x) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = b.x;
+    x[3] = b.y;
+}
+
+template <int HD, typename T>
+__global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const T* __restrict__ k, const T* __restrict__ v,
+                                                                long long ks, long long vs,
+                                                                const long long* __restrict__ slots, long long items,
+                                                                int n_kv, uint8_t* __restrict__ pool,
+                                                                long long num_blocks, DevError* err) {
+    using R = Kv4<HD>;
+    const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long item = at / R::LANES;
+    const int l = (int)(at % R::LANES), b = l >> 2, j = l & 3;
+    const bool in = item < items;   // the last warp's spare lanes still take part in its shuffles
+    const long long i = in ? item / n_kv : 0;
+    const int g = in ? (int)(item - i * n_kv) : 0;
+    float xk[8] = {}, xv[8] = {};
+    long long slot = -1;
+    if (in) {
+        slot = __ldg(slots + i);
+        const T* kr = k + i * ks + (size_t)g * HD + 32 * b;
+        const T* vr = v + i * vs + (size_t)g * HD + 32 * b;
+        load4(kr + 4 * j, xk);
+        load4(kr + 16 + 4 * j, xk + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load2(vr + 2 * j + 8 * q, xv[q], xv[4 + q]);
+    }
+    const long long blk = slot >> 4;
+    const bool live = slot >= 0 && blk < num_blocks;
+    if (in && !live && slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
+    uint8_t* rec = pool + ((size_t)(live ? blk : 0) * n_kv + g) * R::BYTES;
+    const bool ok = kv4_put_rows<HD>(xk, xv, rec, (int)(slot & 15), b, j, live);
+    bool finite = true;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) finite = finite && isfinite(xk[t]) && isfinite(xv[t]);
+    if (live && !finite) record_device_error(err, kErrKvNonFinite, i, g);
+    else if (live && !ok) record_device_error(err, kErrKvOverflow, i, g);
+}
+
+// 8 consecutive values d c + m, each rounded once. f16: one fused multiply-add of exact f16 codes
+// (1024 + c has the code in its low bits); f32: d c is exact, so is the fused multiply-add's rounding.
+__device__ __forceinline__ void put8(__half* o, const uint32_t (&c)[8], __half d, __half m) {
+    const __half2 dd = __half2half2(d), mm = __half2half2(m), k1024 = __float2half2_rn(1024.f);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t h = c[2 * i] | (c[2 * i + 1] << 16) | 0x64006400u;
+        const __half2 y = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&h), k1024), dd, mm);
+        w[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void put8(float* o, const uint32_t (&c)[8], __half d, __half m) {
+    const float df = __half2float(d), mf = __half2float(m);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = fmaf(df, (float)c[i], mf);
+    reinterpret_cast<float4*>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4*>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
+}
+
+// Lane (block b, w) writes elements 8 w .. 8 w + 7 of block b of the key row and of the value row.
+template <int HD, typename T>
+__global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __restrict__ pool,
+                                                               const long long* __restrict__ slots, long long items,
+                                                               int n_kv, long long num_blocks, T* __restrict__ k,
+                                                               T* __restrict__ v, long long ks, long long vs,
+                                                               DevError* err) {
+    using R = Kv4<HD>;
+    const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long item = at / R::LANES;
+    if (item >= items) return;
+    const int l = (int)(at % R::LANES), b = l >> 2, w = l & 3;
+    const long long i = item / n_kv;
+    const int g = (int)(item - i * n_kv);
+    const long long slot = __ldg(slots + i);
+    const long long blk = slot >> 4;
+    if (slot < 0 || blk >= num_blocks) {
+        if (slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
+        return;
+    }
+    const int s = (int)(slot & 15);
+    const uint8_t* rec = pool + ((size_t)blk * n_kv + g) * R::BYTES;
+    const uint8_t* krow = rec + R::KC + s * (HD / 2);
+    const uint8_t* vrow = rec + R::VC + s * (HD / 2) + 2 * b;
+    const int j0 = 2 * (w & 1);
+    const uint32_t k0 = *reinterpret_cast<const uint32_t*>(krow + 4 * (R::NB * j0 + b)) >> (4 * (w >> 1));
+    const uint32_t k1 = *reinterpret_cast<const uint32_t*>(krow + 4 * (R::NB * (j0 + 1) + b)) >> (4 * (w >> 1));
+    uint32_t ck[8], cv[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) cv[t] = (*reinterpret_cast<const uint16_t*>(vrow + R::vunit(s, t)) >> (4 * w)) & 15u;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        ck[t] = (k0 >> (8 * t)) & 15u;
+        ck[4 + t] = (k1 >> (8 * t)) & 15u;
+    }
+    const __half dk = reinterpret_cast<const __half*>(rec + R::KD)[s * R::NB + b];
+    const __half mk = reinterpret_cast<const __half*>(rec + R::KM)[s * R::NB + b];
+    const __half dv = reinterpret_cast<const __half*>(rec + R::VD)[R::vscale(s, b)];
+    const __half mv = reinterpret_cast<const __half*>(rec + R::VM)[R::vscale(s, b)];
+    put8(k + i * ks + (size_t)g * HD + 32 * b + 8 * w, ck, dk, mk);
+    put8(v + i * vs + (size_t)g * HD + 32 * b + 8 * w, cv, dv, mv);
+}
+
+// The checks that the writer and the reader share; `grid` for n > 0.
+int kv4_rows_check(const char* name, const void* k, const void* v, int dtype, int64_t ks, int64_t vs,
+                   const int64_t* slots, int64_t n, int n_kv, int hd, const void* pool, int64_t num_blocks,
+                   unsigned* grid) {
+    const std::string nm(name);
+    if (dtype != QL_DTYPE_F32 && dtype != QL_DTYPE_F16) return set_error(QL_EINVAL, nm + ": dtype must be f32 or f16");
+    if (hd != 64 && hd != 128) return set_error(QL_EINVAL, nm + ": head_dim must be 64 or 128");
+    if (n < 0 || n_kv <= 0 || num_blocks <= 0)
+        return set_error(QL_EINVAL, nm + ": need n >= 0, n_kv_heads and num_blocks > 0");
+    *grid = 0;
+    if (n == 0) return QL_OK;
+    if (!k || !v || !slots || !pool) return set_error(QL_EINVAL, nm + ": null pointer");
+    auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    if (!a16(k) || !a16(v) || !a16(pool))
+        return set_error(QL_EINVAL, nm + ": k, v and the pool must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slots) & 7) != 0) return set_error(QL_EINVAL, nm + ": slots must be 8-byte aligned");
+    const int64_t per = dtype == QL_DTYPE_F32 ? 4 : 8;
+    if (n > 1 && (ks < (int64_t)n_kv * hd || vs < (int64_t)n_kv * hd || ks % per || vs % per))
+        return set_error(QL_EINVAL, nm + ": row strides must be multiples of 16 bytes and at least n_kv_heads * head_dim");
+    const int64_t lanes = (int64_t)(hd / 8) * n_kv;
+    if (n > ((1ll << 31) - 1) * kKv4Threads / lanes) return set_error(QL_EINVAL, nm + ": too many rows");
+    *grid = (unsigned)((n * lanes + kKv4Threads - 1) / kKv4Threads);
+    return QL_OK;
+}
+
+}  // namespace
+}  // namespace ql
+
+extern "C" int64_t ql_kv4_record_bytes(int head_dim) {
+    return (head_dim == 64 || head_dim == 128) ? (int64_t)20 * head_dim : 0;
+}
+
+extern "C" int ql_kv4_write(const void* d_k, const void* d_v, int dtype, int64_t k_stride, int64_t v_stride,
+                            const int64_t* d_slots, int64_t n, int n_kv_heads, int head_dim, void* d_pool,
+                            int64_t num_blocks, void* stream) {
+    using namespace ql;
+    unsigned grid = 0;
+    if (int rc = kv4_rows_check("ql_kv4_write", d_k, d_v, dtype, k_stride, v_stride, d_slots, n, n_kv_heads, head_dim,
+                                d_pool, num_blocks, &grid))
+        return rc;
+    if (grid == 0) return QL_OK;
+    DevError* err = device_error_record();
+    if (!err) return set_error(QL_ECUDA, "ql_kv4_write: no device error record");
+    auto go = [&](auto kernel, auto zero) {
+        using T = decltype(zero);
+        return launch(kernel, dim3(grid), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
+                      static_cast<const T*>(d_k), static_cast<const T*>(d_v), (long long)k_stride, (long long)v_stride,
+                      reinterpret_cast<const long long*>(d_slots), (long long)(n * n_kv_heads), n_kv_heads,
+                      static_cast<uint8_t*>(d_pool), (long long)num_blocks, err);
+    };
+    const bool f32 = dtype == QL_DTYPE_F32;
+    const cudaError_t e = head_dim == 128 ? (f32 ? go(kv4_write_kernel<128, float>, 0.f)
+                                                 : go(kv4_write_kernel<128, __half>, __half()))
+                                          : (f32 ? go(kv4_write_kernel<64, float>, 0.f)
+                                                 : go(kv4_write_kernel<64, __half>, __half()));
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_kv4_write");
+}
+
+extern "C" int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_heads, int head_dim,
+                           int64_t num_blocks, void* d_k, void* d_v, int dtype, int64_t k_stride, int64_t v_stride,
+                           void* stream) {
+    using namespace ql;
+    unsigned grid = 0;
+    if (int rc = kv4_rows_check("ql_kv4_read", d_k, d_v, dtype, k_stride, v_stride, d_slots, n, n_kv_heads, head_dim,
+                                d_pool, num_blocks, &grid))
+        return rc;
+    if (grid == 0) return QL_OK;
+    DevError* err = device_error_record();
+    if (!err) return set_error(QL_ECUDA, "ql_kv4_read: no device error record");
+    auto go = [&](auto kernel, auto zero) {
+        using T = decltype(zero);
+        return launch(kernel, dim3(grid), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
+                      static_cast<const uint8_t*>(d_pool), reinterpret_cast<const long long*>(d_slots),
+                      (long long)(n * n_kv_heads), n_kv_heads, (long long)num_blocks, static_cast<T*>(d_k),
+                      static_cast<T*>(d_v), (long long)k_stride, (long long)v_stride, err);
+    };
+    const bool f32 = dtype == QL_DTYPE_F32;
+    const cudaError_t e = head_dim == 128 ? (f32 ? go(kv4_read_kernel<128, float>, 0.f)
+                                                 : go(kv4_read_kernel<128, __half>, __half()))
+                                          : (f32 ? go(kv4_read_kernel<64, float>, 0.f)
+                                                 : go(kv4_read_kernel<64, __half>, __half()));
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_kv4_read");
+}

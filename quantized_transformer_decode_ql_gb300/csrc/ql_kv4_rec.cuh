@@ -1,0 +1,131 @@
+// The 4-bit KV pool: where a record keeps its fields, and the row quantiser.
+//
+// A row of HD values is cut into 32-element blocks with m = f16(min x), d = f16((max x - min x) / 15)
+// and codes c = clamp(rint((x - m) / d), 0, 15); its values are d c + m. One record per (physical
+// block of 16 tokens, kv head), 20 HD bytes (160 B per token at HD 128, against 512 for f16), every
+// field 16-byte aligned, in the order in which the attention's matrix instructions take them:
+//   KC  u8  [16][HD / 2]  key codes: a lane of the score product reads its 8 elements of every
+//                         block as one word each, the words of one lane in a row
+//   VC  u8  [16][HD / 2]  value codes: 16-bit words of 4 elements 8 apart, the blocks' words of one
+//                         lane of the value product in a row; at HD 128 the lanes' units of two of
+//                         every four slots are swapped in halves, which keeps the shared-memory
+//                         reads of the four slots of a lane group on different banks
+//   KD, KM  f16 [16][HD / 32]             key scales and minima
+//   VD, VM  f16 [4][2][HD / 32][2]        value scales and minima of slot q + 4 e + 8 h at
+//                                         [q][h][block][e]: the pairs that a lane multiplies
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ql_internal.h"
+
+namespace ql {
+
+template <int HD>
+struct Kv4 {
+    static constexpr int NB = HD / 32;   // 32-element blocks per row
+    static constexpr int KC = 0, VC = 8 * HD, KD = 16 * HD, KM = 17 * HD, VD = 18 * HD, VM = 19 * HD;
+    static constexpr int BYTES = 20 * HD;
+    static constexpr int LANES = 4 * NB;   // lanes per row of the writer and the reader
+    // byte of a row's value unit w (the 4 NB-bit words of elements w, w + 8, w + 16, w + 24 of every block)
+    __host__ __device__ static constexpr int vunit(int slot, int w) {
+        return 2 * NB * (HD == 128 ? (w ^ (((slot >> 1) & 1) << 2)) : w);
+    }
+    // f16 index of (slot, block) in VD and VM
+    __host__ __device__ static constexpr int vscale(int slot, int b) {
+        return 4 * NB * (slot & 3) + 2 * NB * (slot >> 3) + 2 * b + ((slot >> 2) & 1);
+    }
+};
+
+#ifdef __CUDACC__
+// The code of x by its definition in f64. Kept out of line: one element in about 2^16 comes here.
+static __device__ __noinline__ float kv4_code_f64(float x, float m, float d) {
+    return (float)rint(((double)x - (double)m) / (double)d);
+}
+
+// One block of 32 elements, 8 in each of 4 neighbouring lanes (x: this lane's): the stored scale and
+// minimum, and this lane's codes. All 32 lanes of the warp take part. Each of m, d and the codes is
+// its exact value rounded once: d from the difference with its rounding error, compared with the
+// border between its two f16 neighbours; a code from f32, whose error is below 2^-18 for codes up to
+// 16 (three roundings of 2^-24 each), unless it lies within 2^-17 of a border, where f64 decides.
+// Returns false if the minimum or the scale overflows f16.
+__device__ __forceinline__ bool kv4_block(const float (&x)[8], uint32_t (&code)[8], __half& dh, __half& mh) {
+    float mn = x[0], mx = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        mn = fminf(mn, x[i]);
+        mx = fmaxf(mx, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    mh = __hadd(__float2half_rn(mn), __float2half_rn(0.f));   // a zero minimum is stored as +0
+    // mx - mn = s + e exactly
+    const float s = __fsub_rn(mx, mn);
+    const float t = __fsub_rn(s, mx);
+    const float e = __fadd_rn(__fsub_rn(mx, __fsub_rn(s, t)), __fsub_rn(-mn, t));
+    const __half lo = __float2half_rd(__fmul_rn(s, 1.0f / 15.0f));
+    const uint16_t lob = __half_as_ushort(lo);
+    const float lof = __half2float(lo);
+    // the next f16 after lo (65536 stands in for the one after the largest: the border is 65520)
+    const float hif = lob >= 0x7BFFu ? 65536.f : __half2float(__ushort_as_half((uint16_t)(lob + 1)));
+    const float border = 0.5f * (lof + hif);
+    const float over = __fadd_rn(__fsub_rn(s, 15.0f * border), e);   // 15 border has 16 bits: exact
+    const bool up = over > 0.f || (over == 0.f && (lob & 1));
+    dh = __ushort_as_half((uint16_t)(lob + (up && lob < 0x7C00u ? 1 : 0)));
+    const float d = __half2float(dh), m = __half2float(mh);
+    const float id = d > 0.f ? __fdiv_rn(1.0f, d) : 0.f;
+    bool near = false;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = __fmul_rn(__fsub_rn(x[i], m), id);
+        q[i] = rintf(f);
+        near = near || fabsf(f - q[i]) > 0.5f - 0x1p-17f;
+    }
+    if (near && d > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = kv4_code_f64(x[i], m, d);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) code[i] = (uint32_t)fminf(fmaxf(q[i], 0.f), 15.f);   // NaN: 0
+    return !__hisinf(dh) && !__hisinf(mh);
+}
+
+// Quantise a key row and a value row into slot `slot` of a record, by LANES neighbouring lanes: this
+// lane is word j (0..3) of block b. xk: elements 4 j + {0..3} and 16 + 4 j + {0..3} of the block of
+// the key row; xv: elements 2 j + 8 q and 2 j + 1 + 8 q (q = 0..3) of the value row, at q and 4 + q.
+// Stores only where `live`; all 32 lanes of the warp take part. False on an f16 overflow.
+template <int HD>
+__device__ __forceinline__ bool kv4_put_rows(const float (&xk)[8], const float (&xv)[8], uint8_t* rec, int slot, int b,
+                                             int j, bool live) {
+    using R = Kv4<HD>;
+    uint32_t ck[8], cv[8];
+    __half dk, mk, dv, mv;
+    const bool okk = kv4_block(xk, ck, dk, mk);
+    const bool okv = kv4_block(xv, cv, dv, mv);
+    if (live) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w |= (ck[i] | (ck[4 + i] << 4)) << (8 * i);
+        *reinterpret_cast<uint32_t*>(rec + R::KC + slot * (HD / 2) + 4 * (R::NB * j + b)) = w;
+        uint8_t* vrow = rec + R::VC + slot * (HD / 2) + 2 * b;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint16_t*>(vrow + R::vunit(slot, 2 * j + u)) =
+                (uint16_t)(cv[4 * u] | (cv[4 * u + 1] << 4) | (cv[4 * u + 2] << 8) | (cv[4 * u + 3] << 12));
+        if (j == 0) {
+            reinterpret_cast<__half*>(rec + R::KD)[slot * R::NB + b] = dk;
+            reinterpret_cast<__half*>(rec + R::KM)[slot * R::NB + b] = mk;
+            reinterpret_cast<__half*>(rec + R::VD)[R::vscale(slot, b)] = dv;
+            reinterpret_cast<__half*>(rec + R::VM)[R::vscale(slot, b)] = mv;
+        }
+    }
+    return okk && okv;
+}
+#endif
+
+}  // namespace ql
