@@ -1,10 +1,30 @@
 // Paged decode attention over the 4-bit pool: out = softmax(q . K scale) V for one query token per
 // sequence, each kv head shared by a group of query heads.
 //
-// One CTA of 4 warps per (sequence, kv head, up to 8 query heads of its group); a warp takes every
-// fourth key, a lane element 32 b + lane of each block b of a row, with a running maximum and sum
-// per head in f32; the warps' sums are joined in shared memory.
+// The bound is HBM: 20 HD bytes per 16 tokens and kv head. Both products run on mma.sync m16n8k16
+// with the 4-bit codes as the A operand and up to 8 query heads as the 8 columns, and no code is
+// ever decoded: (word & 0x000f000f) is a pair of subnormal f16 numbers c 2^-24, which the matrix unit
+// multiplies exactly, and (word & 0x00f000f0) a pair 16 times that. The scales stay outside:
+//   S^T = K Q^T: one f32 sum per (key, head) and 32-element block, sum_i q_i c_i, then
+//         s = sum_b d_b sum_b + sum_b m_b (sum_i q_i), the last product one m16n8k8 MMA of the minima
+//         with the q sums in two f16 parts. q is brought to [2^14, 2^15) by a power of two (exact),
+//         elements that meet the 16-fold codes are divided by 16.
+//   O^T = V^T P^T: p d_b takes the part of p, as two f16 numbers (22 bits; p alone in f16 would cost
+//         as much again as the rounding of the output), the minima are one more MMA whose fifth row
+//         of ones gives the sum of p.
+// Up to 4 heads: columns 4-7 repeat heads 0-3 and carry the low parts, so the second part is free;
+// otherwise each value product runs twice.
+//
+// The softmax reference is lazy: p = 2^(x - ref) with ref raised (and the sums rescaled) only when
+// some x exceeds it by 14 binades, so most tiles need one vote instead of a maximum over lanes.
+//
+// Work is a flat list of tiles (16 tokens of one kv head and one group of up to 8 heads), cut into
+// equal runs, one per CTA, whatever the lengths; the 8 warps of a CTA take its tiles in turn, each
+// through its own ring of bulk copies, which runs on across the borders of sequences. At a border the
+// warps' sums are joined in shared memory. A sequence's part that a CTA does not hold whole is written
+// to the workspace, and the CTA that takes the last ticket joins the parts in order.
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 
 #include "ql_internal.h"
@@ -14,8 +34,19 @@
 namespace ql {
 namespace {
 
-constexpr int kHeads = 8;    // query heads per CTA
-constexpr int kWarps = 4;
+constexpr int kHeads = 8;                 // query heads per tile
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kStages = 4;                // tiles of a warp in flight
+constexpr int kCtasPerSm = 2;
+constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+template <int HD>
+struct Part {                             // a lane's share of a state: sums, minima's sums, references
+    static constexpr int MT = HD / 16;    // 16-row tiles of the value product
+    static constexpr int N = 4 * MT + 4;
+};
+constexpr size_t kSlotBytes = (size_t)Part<128>::N * 32 * sizeof(float);
 
 struct Params {
     const __half* q;
@@ -24,99 +55,575 @@ struct Params {
     const int32_t* context_lens;
     const int32_t* positions;
     const int32_t* active;
-    int n_heads, n_kv, group, chunks;
+    int batch, n_heads, n_kv, group, chunks;   // chunks: parts of up to 8 heads of a group
     long long maxb, num_blocks;
     float scale_log2;
     __half* out;
+    float* slots;       // [2 gridDim.x][Part<HD>::N][32]
+    int* tickets;       // [gridDim.x], zero between launches
 };
 
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(b0));
+}
+// The transpose of an 8 x 8 f16 matrix held one row pair per lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ T lds(uint32_t a);
+template <>
+__device__ __forceinline__ uint32_t lds<uint32_t>(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+template <>
+__device__ __forceinline__ uint2 lds<uint2>(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+template <>
+__device__ __forceinline__ uint4 lds<uint4>(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+// N consecutive words of a row: one load
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
+    if constexpr (N == 4) {
+        const uint4 v = lds<uint4>(a);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = lds<uint2>(a);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = lds<uint32_t>(a);
+    }
+}
+
+// Wait for phase `parity` of an mbarrier: false after 2 s.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2, %3;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(2000u) : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        if (bar_test(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < kWaitNs);
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    return bar_test(bar, parity) || bar_wait_slow(bar, parity);
+}
+
+// A warp's running state: the value sums (units of 2^-24, odd row halves 16 times that), the minima's
+// sums (row b < NB) and the weights' sum (row 4), and the references of this lane's two heads.
 template <int HD>
-__global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(Params p, DevError* err) {
+struct State {
+    float o[HD / 16][4];
+    float z[4];
+    float ref[2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        z[0] = z[1] = z[2] = z[3] = 0.f;
+        ref[0] = ref[1] = -FLT_MAX;
+    }
+    __device__ __forceinline__ void scale(float f0, float f1) {
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+            o[i][0] *= f0;
+            o[i][1] *= f1;
+            o[i][2] *= f0;
+            o[i][3] *= f1;
+        }
+        z[0] *= f0;
+        z[1] *= f1;
+    }
+    template <typename Put>
+    __device__ __forceinline__ void put(Put st) const {
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) st(i, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
+        st(HD / 16, make_float4(z[0], z[1], ref[0], ref[1]));
+    }
+    // add a state stored by put
+    template <typename Get>
+    __device__ __forceinline__ void join(Get ld) {
+        const float4 t = ld(HD / 16);
+        const float r0 = fmaxf(ref[0], t.z), r1 = fmaxf(ref[1], t.w);
+        const float a0 = exp2_fast(ref[0] - r0), a1 = exp2_fast(ref[1] - r1);
+        const float b0 = exp2_fast(t.z - r0), b1 = exp2_fast(t.w - r1);
+        ref[0] = r0;
+        ref[1] = r1;
+        z[0] = fmaf(t.x, b0, z[0] * a0);
+        z[1] = fmaf(t.y, b1, z[1] * a1);
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+            const float4 v = ld(i);
+            o[i][0] = fmaf(v.x, b0, o[i][0] * a0);
+            o[i][1] = fmaf(v.y, b1, o[i][1] * a1);
+            o[i][2] = fmaf(v.z, b0, o[i][2] * a0);
+            o[i][3] = fmaf(v.w, b1, o[i][3] * a1);
+        }
+    }
+};
+
+// Tiles of sequence b: 0 for an idle or inactive one or one whose length does not fit its table.
+__device__ __forceinline__ int seq_len(const Params& p, int b) {
+    if (p.active && p.active[b] == 0) return 0;
+    const long long len = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
+    return len < 0 || len > p.maxb * 16 ? 0 : (int)len;
+}
+
+// Where a tile of the flat list lies. All fields are the same in every lane of the warp.
+struct Place {
+    long long seg0;   // the list's number of this segment's first tile
+    int b, s;         // sequence; kv head * chunks + chunk
+    int len, nb;      // the sequence's length and tiles
+};
+
+template <int HD, bool DUP>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p, DevError* err) {
     using R = Kv4<HD>;
-    constexpr int NB = R::NB;
-    __shared__ float sm[kWarps][kHeads], sl[kWarps][kHeads], so[kWarps][kHeads][HD];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = blockIdx.x / p.chunks, c = blockIdx.x % p.chunks, b = blockIdx.y;
+    using St = State<HD>;
+    constexpr int NB = R::NB, MT = HD / 16, REC = R::BYTES;
+    extern __shared__ __align__(128) unsigned char smem[];   // [warp][stage] records, then 4 states
+    __shared__ __align__(8) unsigned long long bars[kWarps * kStages];
+    __shared__ int last_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gq = lane >> 2, tq = lane & 3;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * REC;
+    const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars) + warp * kStages * 8;
+    float4* const joins = reinterpret_cast<float4*>(smem + kWarps * kStages * REC);
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar0 + 8 * i) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
-    if (p.active && p.active[b] == 0) return;
-    const long long len = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
-    if (len < 0 || len > p.maxb * 16) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) record_device_error(err, kErrAttnLength, b, len);
-        return;
+
+    // the whole list's length, then this CTA's run [lo, hi)
+    const int S = p.n_kv * p.chunks;
+    long long total = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int nb = b < p.batch ? (seq_len(p, b) + 15) >> 4 : 0;
+        if (b < p.batch && nb == 0 && blockIdx.x == 0 && warp == 0 && !(p.active && p.active[b] == 0)) {
+            const long long len = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
+            if (len != 0) record_device_error(err, kErrAttnLength, b, len);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) nb += __shfl_xor_sync(0xffffffffu, nb, o);
+        total += nb;
     }
-    if (len == 0) return;
-    const int h0 = g * p.group + c * kHeads;
-    const int nh = min(kHeads, p.group - c * kHeads);
-    float q[kHeads][NB], o[kHeads][NB], m[kHeads], l[kHeads];
-    for (int h = 0; h < kHeads; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-        for (int k = 0; k < NB; ++k) {
-            q[h][k] = h < nh ? __half2float(p.q[((size_t)b * p.n_heads + h0 + h) * HD + 32 * k + lane]) : 0.f;
-            o[h][k] = 0.f;
+    total *= S;
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    per = per < kWarps ? kWarps : per;
+    const long long lo = blockIdx.x * per, hi = lo + per < total ? lo + per : total;
+    if (lo >= hi) return;
+
+    // the segment of tile t at or after place `pl` (whose segment starts at or before t)
+    auto seek = [&](Place& pl, long long t) {
+        while (t >= pl.seg0 + pl.nb) {
+            pl.seg0 += pl.nb;
+            if (++pl.s < S && pl.nb > 0) continue;
+            pl.s = 0;
+            ++pl.b;
+            pl.len = seq_len(p, pl.b);
+            pl.nb = (pl.len + 15) >> 4;
+        }
+    };
+    Place pl = {0, 0, 0, 0, 0};
+    {
+        long long before = 0;
+        for (int b0 = 0;; b0 += 32) {
+            const int b = b0 + lane;
+            const int len = b < p.batch ? seq_len(p, b) : 0, nb = (len + 15) >> 4;
+            long long incl = (long long)nb * S;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, before + incl > lo);
+            if (here) {
+                const int l = __ffs(here) - 1;
+                pl.b = b0 + l;
+                pl.len = __shfl_sync(0xffffffffu, len, l);
+                pl.nb = (pl.len + 15) >> 4;
+                const long long first = before + __shfl_sync(0xffffffffu, incl, l) - (long long)pl.nb * S;
+                pl.s = (int)((lo - first) / pl.nb);
+                pl.seg0 = first + (long long)pl.s * pl.nb;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
-    for (long long t = warp; t < len; t += kWarps) {
-        const long long blk = p.block_tables[(size_t)b * p.maxb + (t >> 4)];
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) record_device_error(err, kErrAttnBlock, (long long)b * p.maxb + (t >> 4), blk);
-            continue;
-        }
-        const int s = (int)(t & 15);
-        const uint8_t* rec = p.pool + ((size_t)blk * p.n_kv + g) * R::BYTES;
-        float kx[NB], vx[NB];
-        for (int k = 0; k < NB; ++k) {
-            const int j = (lane & 15) >> 2, i = lane & 3;
-            const int kc = rec[R::KC + s * (HD / 2) + 4 * (NB * j + k) + i] >> (4 * (lane >> 4)) & 15;
-            const int vc = rec[R::VC + s * (HD / 2) + R::vunit(s, lane & 7) + 2 * k + (lane >> 4)] >> (4 * ((lane >> 3) & 1)) & 15;
-            kx[k] = fmaf(__half2float(reinterpret_cast<const __half*>(rec + R::KD)[s * NB + k]), (float)kc,
-                         __half2float(reinterpret_cast<const __half*>(rec + R::KM)[s * NB + k]));
-            vx[k] = fmaf(__half2float(reinterpret_cast<const __half*>(rec + R::VD)[R::vscale(s, k)]), (float)vc,
-                         __half2float(reinterpret_cast<const __half*>(rec + R::VM)[R::vscale(s, k)]));
-        }
-        for (int h = 0; h < kHeads; ++h) {
-            float x = 0.f;
-            for (int k = 0; k < NB; ++k) x = fmaf(q[h][k], kx[k], x);
-            for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-            x *= p.scale_log2;
-            const float mn = fmaxf(m[h], x), a = exp2f(m[h] - mn), w = exp2f(x - mn);
-            m[h] = mn;
-            l[h] = l[h] * a + w;
-            for (int k = 0; k < NB; ++k) o[h][k] = fmaf(w, vx[k], o[h][k] * a);
-        }
-    }
-    for (int h = 0; h < kHeads; ++h) {
+
+    // ---- the ring: tile k of this warp (number lo + warp + 8 k) goes to stage k % kStages
+    Place pp = pl;                     // the place of the next tile whose block id is loaded
+    long long pt = lo + warp;
+    int phys = -1, pseg = 0;           // its block id, its kv head
+    auto fetch_id = [&]() {
+        if (pt >= hi) return;
+        seek(pp, pt);
+        const int blk = (int)(pt - pp.seg0);
+        phys = __ldg(p.block_tables + (size_t)pp.b * p.maxb + blk);
+        pseg = p.chunks == 1 ? pp.s : pp.s / p.chunks;
+    };
+    unsigned okm = 0;                  // stages that hold a record
+    int issued = 0;
+    bool dead = false;                 // a wait ran out: no more copies
+    auto issue = [&]() {               // copy the tile whose id is loaded, then load the next id
+        if (pt >= hi) return;
+        const int st = issued % kStages;
+        const bool ok = phys >= 0 && phys < p.num_blocks && !dead;
+        okm = (okm & ~(1u << st)) | ((ok ? 1u : 0u) << st);
         if (lane == 0) {
-            sm[warp][h] = m[h];
-            sl[warp][h] = l[h];
+            if (ok) {
+                const uint8_t* src = p.pool + ((size_t)phys * p.n_kv + pseg) * REC;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar0 + 8 * st), "r"(REC)
+                             : "memory");
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
+                    "[%3], %4;" ::"r"(ring + st * REC), "l"(src), "r"(REC), "r"(bar0 + 8 * st), "l"(l2_evict_first())
+                    : "memory");
+            } else {
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar0 + 8 * st) : "memory");
+                if (!dead) record_device_error(err, kErrAttnBlock, (long long)pp.b * p.maxb + (pt - pp.seg0), phys);
+            }
         }
-        for (int k = 0; k < NB; ++k) so[warp][h][32 * k + lane] = o[h][k];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nh * HD; i += kWarps * 32) {
-        const int h = i / HD, e = i % HD;
-        float mx = -INFINITY, ls = 0.f, os = 0.f;
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w][h]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = sm[w][h] == -INFINITY ? 0.f : exp2f(sm[w][h] - mx);
-            ls += sl[w][h] * f;
-            os += so[w][h][e] * f;
+        ++issued;
+        pt += kWarps;
+        fetch_id();
+    };
+    fetch_id();
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) issue();
+
+    int used = 0;                      // tiles consumed
+    long long tn = lo + warp;          // this warp's next tile
+    St st;
+    // lane constants: shared-memory offsets within a record
+    const int krow = ((gq >> 1) & 3) | ((gq & 1) << 2);   // the key of this lane's row of the score product
+    const uint32_t offK = R::KC + krow * (HD / 2) + 4 * NB * tq;
+    const uint32_t offKD = R::KD + krow * NB * 2, offKM = R::KM + krow * NB * 2 + (NB == 4 ? 4 * (tq & 1) : 0);
+    const uint32_t offV = R::VC + tq * (HD / 2) + R::vunit(tq, gq);
+    const uint32_t offVD = R::VD + tq * NB * 8, offVM = R::VM + tq * NB * 8 + 4 * (gq & (NB - 1));
+
+    for (;;) {
+        const long long seg1 = pl.seg0 + pl.nb;
+        const long long t0 = pl.seg0 > lo ? pl.seg0 : lo, t1 = seg1 < hi ? seg1 : hi;
+        const int g = pl.s / p.chunks, c = pl.s - g * p.chunks;
+        const int nh = min(kHeads, p.group - c * kHeads);
+        const int h0 = g * p.group + c * kHeads;
+        st.clear();
+        float top = kTop;
+        // ---- q as the B operand of the score product
+        uint32_t ql[NB][2], qh[NB][2], qz = 0;
+        float fac[2];
+        if (tn < t1) {
+            const int h = DUP ? gq & 3 : gq;
+            const __half* qr = p.q + ((size_t)pl.b * p.n_heads + h0 + (h < nh ? h : 0)) * HD + 4 * tq;
+            float v[NB][8];
+            float mx = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = __half22float2(
+                        __ldg(reinterpret_cast<const __half2*>(qr + 32 * b + 16 * (k >> 1) + 2 * (k & 1))));
+                    v[b][2 * k] = h < nh ? f.x : 0.f;
+                    v[b][2 * k + 1] = h < nh ? f.y : 0.f;
+                    mx = fmaxf(mx, fmaxf(fabsf(v[b][2 * k]), fabsf(v[b][2 * k + 1])));
+                }
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // 2^e brings the largest |q| of the head to [2^14, 2^15)
+            const int e = mx > 0.f && mx < INFINITY ? 14 - ((int)(__float_as_uint(mx) >> 23) - 127) : 0;
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            float qs[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    v[b][k] *= up;
+                    s += v[b][k];
+                }
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                qs[b] = s * 0x1p-5f;
+                ql[b][0] = u32(__floats2half2_rn(v[b][0], v[b][2]));
+                ql[b][1] = u32(__floats2half2_rn(v[b][1], v[b][3]));
+                qh[b][0] = u32(__floats2half2_rn(v[b][4] * 0.0625f, v[b][6] * 0.0625f));
+                qh[b][1] = u32(__floats2half2_rn(v[b][5] * 0.0625f, v[b][7] * 0.0625f));
+            }
+            // the sums' high and low f16 parts, opposite the minima of blocks 2 (tq & 1), 2 (tq & 1) + 1
+            const float sa = NB == 4 && (tq & 1) ? qs[NB - 2] : qs[0], sb = NB == 4 && (tq & 1) ? qs[NB - 1] : qs[1];
+            const __half2 hi2 = __floats2half2_rn(sa, sb);
+            const float2 hf = __half22float2(hi2);
+            const __half2 lo2 = __floats2half2_rn(sa - hf.x, sb - hf.y);
+            qz = NB == 4 ? u32(tq < 2 ? hi2 : lo2) : tq == 0 ? u32(hi2) : tq == 1 ? u32(lo2) : 0u;
+            const float f = p.scale_log2 * __uint_as_float((uint32_t)(24 - e + 127) << 23);
+            fac[0] = __shfl_sync(0xffffffffu, f, 8 * tq);
+            fac[1] = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
         }
-        p.out[((size_t)b * p.n_heads + h0 + h) * HD + e] = __float2half_rn(ls > 0.f ? os / ls : 0.f);
+        // ---- this warp's tiles of the segment
+        for (; tn < t1; tn += kWarps, ++used) {
+            const int sg = used % kStages;
+            if (!dead && !bar_wait(bar0 + 8 * sg, (used / kStages) & 1)) {
+                dead = true;
+                if (lane == 0) record_device_error(err, kErrGemvStage, pl.b, tn - pl.seg0);
+            }
+            const int valid = dead || !((okm >> sg) & 1u) ? 0 : min(16, pl.len - 16 * (int)(tn - pl.seg0));
+            const uint32_t rec = ring + sg * REC;
+            // S^T: rows are keys krow, krow + 8 of this lane, columns heads 2 tq, 2 tq + 1
+            uint32_t wa[NB], wb[NB], da[NB / 2], db[NB / 2];
+            lds_words(wa, rec + offK);
+            lds_words(wb, rec + offK + 8 * (HD / 2));
+            lds_words(da, rec + offKD);
+            lds_words(db, rec + offKD + 16 * NB);
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            mma8(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] *= 0x1p-19f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float a[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint32_t wa8 = wa[b] >> 8, wb8 = wb[b] >> 8;
+                mma16(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu, ql[b][0], ql[b][1]);
+                mma16(a, wa[b] & 0x00f000f0u, wb[b] & 0x00f000f0u, wa8 & 0x00f000f0u, wb8 & 0x00f000f0u, qh[b][0], qh[b][1]);
+                const float2 d0 = __half22float2(h2(da[b / 2])), d1 = __half22float2(h2(db[b / 2]));
+                const float x0 = b & 1 ? d0.y : d0.x, x1 = b & 1 ? d1.y : d1.x;
+                s[0] = fmaf(x0, a[0], s[0]);
+                s[1] = fmaf(x0, a[1], s[1]);
+                s[2] = fmaf(x1, a[2], s[2]);
+                s[3] = fmaf(x1, a[3], s[3]);
+            }
+            // the value scales of slots tq, tq + 4 (vd[0]) and tq + 8, tq + 12 (vd[1]), the minima of block gq
+            uint32_t vd[2][NB], vm[2];
+            lds_words(vd[0], rec + offVD);
+            lds_words(vd[1], rec + offVD + 4 * NB);
+            vm[0] = lds<uint32_t>(rec + offVM);
+            vm[1] = lds<uint32_t>(rec + offVM + 4 * NB);
+            s[0] *= fac[0];
+            s[1] *= fac[1];
+            s[2] *= fac[0];
+            s[3] *= fac[1];
+            if (valid < 16) {   // slots past the context, or a block that is not there: any bytes
+                if (krow >= valid) s[0] = s[1] = -INFINITY;
+                if (krow + 8 >= valid) s[2] = s[3] = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t keep = (tq + 8 * k < valid ? 0x0000ffffu : 0u) | (tq + 4 + 8 * k < valid ? 0xffff0000u : 0u);
+                    vm[k] &= keep;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) vd[k][b] &= keep;
+                }
+            }
+            __half2 dmax = __hmax2(h2(vd[0][0]), h2(vd[1][0]));
+#pragma unroll
+            for (int b = 1; b < NB; ++b) dmax = __hmax2(dmax, __hmax2(h2(vd[0][b]), h2(vd[1][b])));
+            const float dm = fmaxf(__low2float(dmax), __high2float(dmax));
+            const float over = fmaxf(fmaxf(s[0], s[2]) - st.ref[0], fmaxf(s[1], s[3]) - st.ref[1]);
+            // p 2^top and p d stay below 2^16: with scales above 2 the largest weight is smaller
+            if (__any_sync(0xffffffffu, over > top || dm > __uint_as_float((uint32_t)(127 + 15 - (int)top) << 23))) {
+                float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]), dw = dm;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                }
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) dw = fmaxf(dw, __shfl_xor_sync(0xffffffffu, dw, o));
+                // the largest scale below 2^(15 - top); top may be 0 at least (scales below 2^14)
+                const float old = top;
+                while (top > 1.f && dw > __uint_as_float((uint32_t)(127 + 15 - (int)top) << 23)) top -= 1.f;
+                // the largest weight so far becomes 2^(top - 6): room for 6 binades before the next move
+                const float r0 = fmaxf(st.ref[0] + (old - top), m0 - top + 6.f), r1 = fmaxf(st.ref[1] + (old - top), m1 - top + 6.f);
+                st.scale(exp2_fast(st.ref[0] - r0), exp2_fast(st.ref[1] - r1));
+                st.ref[0] = r0;
+                st.ref[1] = r1;
+            }
+            // p, in two f16 parts, keys down the columns of the B operand
+            uint32_t ph[2], plo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float p0 = exp2_fast(s[2 * k] - st.ref[0]), p1 = exp2_fast(s[2 * k + 1] - st.ref[1]);
+                const __half2 hi2 = __floats2half2_rn(p0, p1);
+                const float2 hf = __half22float2(hi2);
+                ph[k] = transposed(u32(hi2));
+                plo[k] = transposed(u32(__floats2half2_rn(p0 - hf.x, p1 - hf.y)));
+            }
+            // O^T: A rows are elements gq (+ 8, 16 times) of a 16-element half block, its columns the slots
+            uint32_t v[4][NB / 2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) lds_words(v[k], rec + offV + k * 4 * (HD / 2));
+            const bool low = DUP && gq >= 4;
+            {
+                const uint32_t one = gq == 4 ? 0x3c003c00u : 0u;
+                const uint32_t a0 = gq < NB ? vm[0] : one, a2 = gq < NB ? vm[1] : one;
+                mma16(st.z, a0, 0u, a2, 0u, low ? plo[0] : ph[0], low ? plo[1] : ph[1]);
+                if (!DUP) mma16(st.z, a0, 0u, a2, 0u, plo[0], plo[1]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t ph_[2], pl_[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const __half2 d = h2(vd[k][b]);
+                    const __half2 hi2 = __hmul2(h2(ph[k]), d);
+                    // the product's rounding, exactly, and the low part's product
+                    const __half2 lo2 = __hfma2(h2(plo[k]), d, __hfma2(h2(ph[k]), d, __hneg2(hi2)));
+                    ph_[k] = low ? u32(lo2) : u32(hi2);
+                    pl_[k] = u32(lo2);
+                }
+                const uint32_t x = __byte_perm(v[0][b / 2], v[1][b / 2], b & 1 ? 0x7632 : 0x5410);
+                const uint32_t y = __byte_perm(v[2][b / 2], v[3][b / 2], b & 1 ? 0x7632 : 0x5410);
+                const uint32_t x8 = x >> 8, y8 = y >> 8;
+                mma16(st.o[2 * b], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, ph_[0], ph_[1]);
+                mma16(st.o[2 * b + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, ph_[0], ph_[1]);
+                if (!DUP) {
+                    mma16(st.o[2 * b], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, pl_[0], pl_[1]);
+                    mma16(st.o[2 * b + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, pl_[0], pl_[1]);
+                }
+            }
+            __syncwarp();   // every lane is done with the record
+            issue();
+        }
+        if (DUP) {   // the low parts' columns join the high ones
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) st.o[i][k] += __shfl_xor_sync(0xffffffffu, st.o[i][k], 2);
+            st.z[0] += __shfl_xor_sync(0xffffffffu, st.z[0], 2);
+            st.z[1] += __shfl_xor_sync(0xffffffffu, st.z[1], 2);
+        }
+        // ---- the warps' states join in warp 0: 4 to 7 with 0 to 3, then 2 and 3, then 1
+        auto tree = [&]() {
+#pragma unroll 1
+            for (int n = kWarps / 2; n; n >>= 1) {
+                float4* mine = joins + (size_t)(warp & (n - 1)) * (MT + 1) * 32 + lane;
+                __syncthreads();
+                if (warp >= n && warp < 2 * n) st.put([&](int i, float4 x) { mine[i * 32] = x; });
+                __syncthreads();
+                if (warp < n) st.join([&](int i) { return mine[i * 32]; });
+            }
+        };
+        tree();
+        const bool whole = t0 == pl.seg0 && t1 == seg1;
+        bool write = whole;
+        if (!whole) {
+            const long long c0 = pl.seg0 / per, c1 = (seg1 - 1) / per;   // the CTAs that hold parts
+            float4* slots = reinterpret_cast<float4*>(p.slots);
+            constexpr size_t SLOT = (size_t)(MT + 1) * 32;
+            if (warp == 0) {
+                float4* mine = slots + (2 * (size_t)blockIdx.x + (t0 == pl.seg0 ? 1 : 0)) * SLOT + lane;
+                st.put([&](int i, float4 x) { __stcg(mine + i * 32, x); });
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) {
+                    const int n = atomicAdd(p.tickets + c0, 1);
+                    last_flag = n == (int)(c1 - c0);
+                    if (last_flag) p.tickets[c0] = 0;   // armed for the next launch
+                    __threadfence();
+                }
+            }
+            __syncthreads();
+            if (last_flag) {   // the last part is there: all of them, in order, warp w those of c0 + w, c0 + w + 8, ...
+                st.clear();
+                for (long long k = c0 + warp; k <= c1; k += kWarps) {
+                    const float4* part = slots + (2 * (size_t)k + (k == c0 ? 1 : 0)) * SLOT + lane;
+                    st.join([&](int i) { return __ldcg(part + i * 32); });
+                }
+                tree();
+                write = true;
+            }
+        }
+        if (write && warp == 0) {
+            const int hc = 2 * tq;
+            const float l0 = __shfl_sync(0xffffffffu, st.z[0], 16 + tq), l1 = __shfl_sync(0xffffffffu, st.z[1], 16 + tq);
+            const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+            __half* o = p.out + ((size_t)pl.b * p.n_heads + h0 + hc) * HD + gq;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float z0 = __shfl_sync(0xffffffffu, st.z[0], 4 * b + tq), z1 = __shfl_sync(0xffffffffu, st.z[1], 4 * b + tq);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = k & 1 ? 0x1p20f : 0x1p24f;
+                    const float y0 = fmaf(st.o[2 * b + (k >> 1)][2 * (k & 1)], f, z0) * i0;
+                    const float y1 = fmaf(st.o[2 * b + (k >> 1)][2 * (k & 1) + 1], f, z1) * i1;
+                    if (hc < nh) o[32 * b + 8 * k] = __float2half_rn(y0);
+                    if (hc + 1 < nh) o[HD + 32 * b + 8 * k] = __float2half_rn(y1);
+                }
+            }
+        }
+        if (t1 >= hi) break;
+        seek(pl, t1);
     }
+    if (dead) {   // copies may still be in flight: wait for them (again with a limit) before leaving
+        for (; used < issued; ++used) bar_wait(bar0 + 8 * (used % kStages), (used / kStages) & 1);
+    }
+}
+
+template <int HD>
+constexpr size_t attn_smem() {
+    return (size_t)kWarps * kStages * Kv4<HD>::BYTES + (size_t)(kWarps / 2) * (HD / 16 + 1) * 32 * sizeof(float4);
+}
+
+int attn_grid() { return kCtasPerSm * num_sms(); }
+
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 }  // namespace
 
-size_t kv4_attn_workspace_bytes(int64_t batch, int n_heads, int n_kv, int head_dim, int64_t maxb) {
-    (void)batch, (void)n_heads, (void)n_kv, (void)head_dim, (void)maxb;
-    return 16;
+size_t kv4_attn_workspace_bytes() {
+    const size_t g = (size_t)attn_grid();
+    return 2 * g * kSlotBytes + g * sizeof(int);
 }
 
 int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl) {
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "4-bit attention: no device error record");
+    const int grid = attn_grid();
     Params p = {};
     p.q = a.q;
     p.pool = a.pool;
@@ -124,6 +631,7 @@ int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl) {
     p.context_lens = a.context_lens;
     p.positions = a.positions;
     p.active = a.active;
+    p.batch = a.batch;
     p.n_heads = a.n_heads;
     p.n_kv = a.n_kv_heads;
     p.group = a.n_heads / a.n_kv_heads;
@@ -132,9 +640,16 @@ int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl) {
     p.num_blocks = a.num_blocks;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     p.out = a.out;
-    const dim3 grid((unsigned)(a.n_kv_heads * p.chunks), (unsigned)a.batch);
-    const cudaError_t e = a.head_dim == 128 ? launch(kv4_attn_kernel<128>, grid, dim3(kWarps * 32), 0, s, pdl, p, err)
-                                            : launch(kv4_attn_kernel<64>, grid, dim3(kWarps * 32), 0, s, pdl, p, err);
+    p.slots = static_cast<float*>(a.workspace);
+    p.tickets = reinterpret_cast<int*>(static_cast<char*>(a.workspace) + 2 * (size_t)grid * kSlotBytes);
+    auto go = [&](auto kernel, size_t smem) {
+        const cudaError_t e = allow_smem(kernel, smem);
+        return e == cudaSuccess ? launch(kernel, dim3((unsigned)grid), dim3(kThreads), smem, s, pdl, p, err) : e;
+    };
+    const bool dup = p.group <= 4;
+    const cudaError_t e = a.head_dim == 128
+                              ? (dup ? go(kv4_attn_kernel<128, true>, attn_smem<128>()) : go(kv4_attn_kernel<128, false>, attn_smem<128>()))
+                              : (dup ? go(kv4_attn_kernel<64, true>, attn_smem<64>()) : go(kv4_attn_kernel<64, false>, attn_smem<64>()));
     return e == cudaSuccess ? QL_OK : cuda_error(e, "4-bit attention launch");
 }
 
@@ -145,7 +660,7 @@ extern "C" size_t ql_paged_attn_kv4_workspace_bytes(int64_t batch, int n_heads, 
     if (batch < 1 || n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || (head_dim != 64 && head_dim != 128) ||
         max_blocks_per_seq < 1)
         return 0;
-    return ql::kv4_attn_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_blocks_per_seq);
+    return ql::kv4_attn_workspace_bytes();
 }
 
 extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t* d_block_tables,
@@ -166,7 +681,7 @@ extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, con
     QL_REQUIRE((reinterpret_cast<uintptr_t>(d_pool) & 15) == 0 && (reinterpret_cast<uintptr_t>(d_workspace) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(d_q) & 3) == 0 && (reinterpret_cast<uintptr_t>(d_out) & 3) == 0,
                std::string(nm) + ": the pool and the workspace must be 16-byte aligned, q and the output 4-byte aligned");
-    QL_REQUIRE(workspace_bytes >= kv4_attn_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_blocks_per_seq),
+    QL_REQUIRE(workspace_bytes >= kv4_attn_workspace_bytes(),
                std::string(nm) + ": workspace too small");
     Kv4AttnArgs a = {};
     a.q = static_cast<const __half*>(d_q);

@@ -22,7 +22,7 @@ struct Kv4AttnArgs {
     size_t workspace_bytes;
 };
 
-size_t kv4_attn_workspace_bytes(int64_t batch, int n_heads, int n_kv_heads, int head_dim, int64_t max_blocks_per_seq);
+size_t kv4_attn_workspace_bytes();   // of any shape, on the current device
 int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl);
 
 }  // namespace ql
