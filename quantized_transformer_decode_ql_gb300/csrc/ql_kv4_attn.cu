@@ -41,12 +41,7 @@ constexpr int kCtasPerSm = 2;
 constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-template <int HD>
-struct Part {                             // a lane's share of a state: sums, minima's sums, references
-    static constexpr int MT = HD / 16;    // 16-row tiles of the value product
-    static constexpr int N = 4 * MT + 4;
-};
-constexpr size_t kSlotBytes = (size_t)Part<128>::N * 32 * sizeof(float);
+constexpr size_t kSlotBytes = (size_t)(128 / 16 + 1) * 32 * sizeof(float4);   // a stored state at HD 128
 
 struct Params {
     const __half* q;
@@ -59,7 +54,7 @@ struct Params {
     long long maxb, num_blocks;
     float scale_log2;
     __half* out;
-    float* slots;       // [2 gridDim.x][Part<HD>::N][32]
+    float* slots;       // [2 gridDim.x] stored states: a CTA's part of the segment it starts in and of the one it ends in
     int* tickets;       // [gridDim.x], zero between launches
 };
 
@@ -171,16 +166,15 @@ struct State {
         z[0] *= f0;
         z[1] *= f1;
     }
-    template <typename Put>
-    __device__ __forceinline__ void put(Put st) const {
+    // rows of float4 per lane: 0 .. HD / 16 - 1 the value sums, then minima's sums and references
+    __device__ __forceinline__ void put(float4* to) const {
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) st(i, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
-        st(HD / 16, make_float4(z[0], z[1], ref[0], ref[1]));
+        for (int i = 0; i < HD / 16; ++i) to[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        to[HD / 16 * 32] = make_float4(z[0], z[1], ref[0], ref[1]);
     }
     // add a state stored by put
-    template <typename Get>
-    __device__ __forceinline__ void join(Get ld) {
-        const float4 t = ld(HD / 16);
+    __device__ __forceinline__ void join(const float4* from) {
+        const float4 t = from[HD / 16 * 32];
         const float r0 = fmaxf(ref[0], t.z), r1 = fmaxf(ref[1], t.w);
         const float a0 = exp2_fast(ref[0] - r0), a1 = exp2_fast(ref[1] - r1);
         const float b0 = exp2_fast(t.z - r0), b1 = exp2_fast(t.w - r1);
@@ -190,7 +184,7 @@ struct State {
         z[1] = fmaf(t.y, b1, z[1] * a1);
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
-            const float4 v = ld(i);
+            const float4 v = from[i * 32];
             o[i][0] = fmaf(v.x, b0, o[i][0] * a0);
             o[i][1] = fmaf(v.y, b1, o[i][1] * a1);
             o[i][2] = fmaf(v.z, b0, o[i][2] * a0);
@@ -199,27 +193,53 @@ struct State {
     }
 };
 
-// Tiles of sequence b: 0 for an idle or inactive one or one whose length does not fit its table.
+// One row of several states joined: value sums v, minima's sums and references t.
+struct Slice {
+    float4 v, t;
+    __device__ __forceinline__ void join(float4 w, float4 u) {
+        const float r0 = fmaxf(t.z, u.z), r1 = fmaxf(t.w, u.w);
+        const float a0 = exp2_fast(t.z - r0), a1 = exp2_fast(t.w - r1);
+        const float b0 = exp2_fast(u.z - r0), b1 = exp2_fast(u.w - r1);
+        t = make_float4(fmaf(u.x, b0, t.x * a0), fmaf(u.y, b1, t.y * a1), r0, r1);
+        v = make_float4(fmaf(w.x, b0, v.x * a0), fmaf(w.y, b1, v.y * a1), fmaf(w.z, b0, v.z * a0), fmaf(w.w, b1, v.w * a1));
+    }
+};
+
+// The length of sequence b: 0 for an inactive one or one that does not fit its table.
 __device__ __forceinline__ int seq_len(const Params& p, int b) {
     if (p.active && p.active[b] == 0) return 0;
     const long long len = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
     return len < 0 || len > p.maxb * 16 ? 0 : (int)len;
 }
 
-// Where a tile of the flat list lies. All fields are the same in every lane of the warp.
-struct Place {
-    long long seg0;   // the list's number of this segment's first tile
-    int b, s;         // sequence; kv head * chunks + chunk
-    int len, nb;      // the sequence's length and tiles
+// A segment: the tiles of one (sequence, kv head, chunk of heads) that lie in a CTA's run, numbers rel ..
+// of the run being tiles blk0 .. blk1 - 1 of the sequence's nb. The same in every lane.
+struct Segment {
+    int b, s, len, nb, blk0, blk1, rel;
+    __device__ __forceinline__ void next(const Params& p, int S, int run) {
+        rel += blk1 - blk0;
+        if (++s == S) {
+            s = 0;
+            do {
+                ++b;
+                len = seq_len(p, b);
+            } while (len == 0);
+            nb = (len + 15) >> 4;
+        }
+        blk0 = 0;
+        blk1 = min(nb, run - rel);
+    }
 };
 
 template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p, DevError* err) {
     using R = Kv4<HD>;
     using St = State<HD>;
-    constexpr int NB = R::NB, MT = HD / 16, REC = R::BYTES;
+    constexpr int NB = R::NB, MT = HD / 16, REC = R::BYTES, ROWS = (MT + 1) * 32;
+    static_assert((kStages & (kStages - 1)) == 0 && MT <= kWarps, "");
     extern __shared__ __align__(128) unsigned char smem[];   // [warp][stage] records, then 4 states
     __shared__ __align__(8) unsigned long long bars[kWarps * kStages];
+    __shared__ Segment ahead[kWarps];                        // where each warp's copies are
     __shared__ int last_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, tq = lane & 3;
@@ -235,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     pdl_wait();
     pdl_trigger();
 
-    // the whole list's length, then this CTA's run [lo, hi)
+    // the whole list's length, then this CTA's run of it
     const int S = p.n_kv * p.chunks;
     long long total = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -245,34 +265,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             const long long len = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
             if (len != 0) record_device_error(err, kErrAttnLength, b, len);
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) nb += __shfl_xor_sync(0xffffffffu, nb, o);
-        total += nb;
+        total += __reduce_add_sync(0xffffffffu, nb);
     }
     total *= S;
     long long per = (total + gridDim.x - 1) / gridDim.x;
     per = per < kWarps ? kWarps : per;
-    const long long lo = blockIdx.x * per, hi = lo + per < total ? lo + per : total;
-    if (lo >= hi) return;
-
-    // the segment of tile t at or after place `pl` (whose segment starts at or before t)
-    auto seek = [&](Place& pl, long long t) {
-        while (t >= pl.seg0 + pl.nb) {
-            pl.seg0 += pl.nb;
-            if (++pl.s < S && pl.nb > 0) continue;
-            pl.s = 0;
-            ++pl.b;
-            pl.len = seq_len(p, pl.b);
-            pl.nb = (pl.len + 15) >> 4;
-        }
-    };
-    Place pl = {0, 0, 0, 0, 0};
+    const long long lo = blockIdx.x * per;
+    if (lo >= total) return;
+    const int run = (int)(lo + per < total ? per : total - lo);
+    Segment sg;
     {
         long long before = 0;
         for (int b0 = 0;; b0 += 32) {
             const int b = b0 + lane;
-            const int len = b < p.batch ? seq_len(p, b) : 0, nb = (len + 15) >> 4;
-            long long incl = (long long)nb * S;
+            const int len = b < p.batch ? seq_len(p, b) : 0;
+            long long incl = (long long)((len + 15) >> 4) * S;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -281,62 +288,84 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             const unsigned here = __ballot_sync(0xffffffffu, before + incl > lo);
             if (here) {
                 const int l = __ffs(here) - 1;
-                pl.b = b0 + l;
-                pl.len = __shfl_sync(0xffffffffu, len, l);
-                pl.nb = (pl.len + 15) >> 4;
-                const long long first = before + __shfl_sync(0xffffffffu, incl, l) - (long long)pl.nb * S;
-                pl.s = (int)((lo - first) / pl.nb);
-                pl.seg0 = first + (long long)pl.s * pl.nb;
+                sg.b = b0 + l;
+                sg.len = __shfl_sync(0xffffffffu, len, l);
+                sg.nb = (sg.len + 15) >> 4;
+                const long long in = lo - (before + __shfl_sync(0xffffffffu, incl, l) - (long long)sg.nb * S);
+                sg.s = (int)(in / sg.nb);
+                sg.blk0 = (int)(in - (long long)sg.s * sg.nb);
+                sg.blk1 = (int)min((long long)sg.nb, (long long)sg.blk0 + run);
+                sg.rel = 0;
                 break;
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
 
-    // ---- the ring: tile k of this warp (number lo + warp + 8 k) goes to stage k % kStages
-    Place pp = pl;                     // the place of the next tile whose block id is loaded
-    long long pt = lo + warp;
-    int phys = -1, pseg = 0;           // its block id, its kv head
-    auto fetch_id = [&]() {
-        if (pt >= hi) return;
-        seek(pp, pt);
-        const int blk = (int)(pt - pp.seg0);
-        phys = __ldg(p.block_tables + (size_t)pp.b * p.maxb + blk);
-        pseg = p.chunks == 1 ? pp.s : pp.s / p.chunks;
+    // ---- the ring: the tiles of this warp (numbers warp, warp + 8, ... of the run), in order
+    int pblk, pend;                    // the next tile to copy and the end of its segment; pend 0: none left
+    const int32_t* prow;               // its sequence's block table
+    const uint8_t* ppool;              // the pool at its kv head
+    int phys = -1;                     // its block, loaded a tile ahead of the copy
+    const long long rec_stride = (long long)p.n_kv * REC;
+    auto enter = [&](const Segment& g) {   // the warp's first tile in segment g, if it has one
+        pblk = g.blk0 + ((warp - g.rel) & (kWarps - 1));
+        pend = g.blk1;
+        prow = p.block_tables + (size_t)g.b * p.maxb;
+        ppool = p.pool + (size_t)(p.chunks == 1 ? g.s : g.s / p.chunks) * REC;
     };
-    unsigned okm = 0;                  // stages that hold a record
-    int issued = 0;
+    auto settle = [&]() {              // past the segment's end: the next one with a tile of this warp
+        if (pblk >= pend && pend != 0) {
+            Segment g = ahead[warp];
+            do {
+                if (g.rel + g.blk1 - g.blk0 >= run) {
+                    pblk = pend = 0;
+                    return;
+                }
+                g.next(p, S, run);
+                enter(g);
+            } while (pblk >= pend);
+            __syncwarp();
+            if (lane == 0) ahead[warp] = g;
+            __syncwarp();
+        }
+        if (pend != 0) phys = __ldg(prow + pblk);
+    };
+    unsigned bad = 0;                  // stages without a record (a block id outside the pool, or a failed wait)
     bool dead = false;                 // a wait ran out: no more copies
-    auto issue = [&]() {               // copy the tile whose id is loaded, then load the next id
-        if (pt >= hi) return;
-        const int st = issued % kStages;
-        const bool ok = phys >= 0 && phys < p.num_blocks && !dead;
-        okm = (okm & ~(1u << st)) | ((ok ? 1u : 0u) << st);
-        if (lane == 0) {
-            if (ok) {
-                const uint8_t* src = p.pool + ((size_t)phys * p.n_kv + pseg) * REC;
+    auto issue = [&](int st) {         // copy the tile whose block is loaded into stage st, then load the next one
+        if (pend == 0) return;
+        if ((unsigned)phys < (unsigned)p.num_blocks && !dead) {
+            if (lane == 0) {
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar0 + 8 * st), "r"(REC)
                              : "memory");
                 asm volatile(
                     "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(ring + st * REC), "l"(src), "r"(REC), "r"(bar0 + 8 * st), "l"(l2_evict_first())
+                    "[%3], %4;" ::"r"(ring + st * REC), "l"(ppool + phys * rec_stride), "r"(REC), "r"(bar0 + 8 * st),
+                    "l"(l2_evict_first())
                     : "memory");
-            } else {
+            }
+            if (bad) bad &= ~(1u << st);
+        } else {
+            bad |= 1u << st;
+            if (lane == 0) {
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar0 + 8 * st) : "memory");
-                if (!dead) record_device_error(err, kErrAttnBlock, (long long)pp.b * p.maxb + (pt - pp.seg0), phys);
+                if (!dead) record_device_error(err, kErrAttnBlock, (long long)ahead[warp].b * p.maxb + pblk, phys);
             }
         }
-        ++issued;
-        pt += kWarps;
-        fetch_id();
+        pblk += kWarps;
+        settle();
     };
-    fetch_id();
+    if (lane == 0) ahead[warp] = sg;
+    __syncwarp();
+    enter(sg);
+    settle();
 #pragma unroll 1
-    for (int i = 0; i < kStages; ++i) issue();
+    for (int i = 0; i < kStages; ++i) issue(i);
 
-    int used = 0;                      // tiles consumed
-    long long tn = lo + warp;          // this warp's next tile
     St st;
+    int stage = 0;
+    uint32_t parity = 0;
     // lane constants: shared-memory offsets within a record
     const int krow = ((gq >> 1) & 3) | ((gq & 1) << 2);   // the key of this lane's row of the score product
     const uint32_t offK = R::KC + krow * (HD / 2) + 4 * NB * tq;
@@ -345,19 +374,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     const uint32_t offVD = R::VD + tq * NB * 8, offVM = R::VM + tq * NB * 8 + 4 * (gq & (NB - 1));
 
     for (;;) {
-        const long long seg1 = pl.seg0 + pl.nb;
-        const long long t0 = pl.seg0 > lo ? pl.seg0 : lo, t1 = seg1 < hi ? seg1 : hi;
-        const int g = pl.s / p.chunks, c = pl.s - g * p.chunks;
+        const int g = p.chunks == 1 ? sg.s : sg.s / p.chunks, c = sg.s - g * p.chunks;
         const int nh = min(kHeads, p.group - c * kHeads);
         const int h0 = g * p.group + c * kHeads;
         st.clear();
-        float top = kTop;
+        float top = kTop, dlim = 2.f;   // the largest weight's log2; the largest value scale that goes with it
+        int blk = sg.blk0 + ((warp - sg.rel) & (kWarps - 1));
         // ---- q as the B operand of the score product
         uint32_t ql[NB][2], qh[NB][2], qz = 0;
         float fac[2];
-        if (tn < t1) {
+        if (blk < sg.blk1) {
             const int h = DUP ? gq & 3 : gq;
-            const __half* qr = p.q + ((size_t)pl.b * p.n_heads + h0 + (h < nh ? h : 0)) * HD + 4 * tq;
+            const __half* qr = p.q + ((size_t)sg.b * p.n_heads + h0 + (h < nh ? h : 0)) * HD + 4 * tq;
             float v[NB][8];
             float mx = 0.f;
 #pragma unroll
@@ -404,14 +432,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             fac[1] = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
         }
         // ---- this warp's tiles of the segment
-        for (; tn < t1; tn += kWarps, ++used) {
-            const int sg = used % kStages;
-            if (!dead && !bar_wait(bar0 + 8 * sg, (used / kStages) & 1)) {
+#pragma unroll 1
+        for (; blk < sg.blk1; blk += kWarps) {
+            if (!bar_wait(bar0 + 8 * stage, parity) && !dead) {
                 dead = true;
-                if (lane == 0) record_device_error(err, kErrGemvStage, pl.b, tn - pl.seg0);
+                if (lane == 0) record_device_error(err, kErrGemvStage, sg.b, blk);
             }
-            const int valid = dead || !((okm >> sg) & 1u) ? 0 : min(16, pl.len - 16 * (int)(tn - pl.seg0));
-            const uint32_t rec = ring + sg * REC;
+            const uint32_t rec = ring + stage * REC;
             // S^T: rows are keys krow, krow + 8 of this lane, columns heads 2 tq, 2 tq + 1
             uint32_t wa[NB], wb[NB], da[NB / 2], db[NB / 2];
             lds_words(wa, rec + offK);
@@ -445,7 +472,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             s[1] *= fac[1];
             s[2] *= fac[0];
             s[3] *= fac[1];
-            if (valid < 16) {   // slots past the context, or a block that is not there: any bytes
+            const int left = sg.len - 16 * blk;
+            if (left < 16 || bad || dead) {   // slots past the context, or a block that is not there: any bytes
+                const int valid = dead || ((bad >> stage) & 1u) ? 0 : left;
                 if (krow >= valid) s[0] = s[1] = -INFINITY;
                 if (krow + 8 >= valid) s[2] = s[3] = -INFINITY;
 #pragma unroll
@@ -461,8 +490,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             for (int b = 1; b < NB; ++b) dmax = __hmax2(dmax, __hmax2(h2(vd[0][b]), h2(vd[1][b])));
             const float dm = fmaxf(__low2float(dmax), __high2float(dmax));
             const float over = fmaxf(fmaxf(s[0], s[2]) - st.ref[0], fmaxf(s[1], s[3]) - st.ref[1]);
-            // p 2^top and p d stay below 2^16: with scales above 2 the largest weight is smaller
-            if (__any_sync(0xffffffffu, over > top || dm > __uint_as_float((uint32_t)(127 + 15 - (int)top) << 23))) {
+            if (__any_sync(0xffffffffu, over > top || dm > dlim)) {
                 float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]), dw = dm;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
@@ -471,9 +499,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 }
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) dw = fmaxf(dw, __shfl_xor_sync(0xffffffffu, dw, o));
-                // the largest scale below 2^(15 - top); top may be 0 at least (scales below 2^14)
+                // p and p d stay below 2^15: the largest scale is at most 2^(15 - top)
                 const float old = top;
-                while (top > 1.f && dw > __uint_as_float((uint32_t)(127 + 15 - (int)top) << 23)) top -= 1.f;
+                while (top > 1.f && dw > dlim) {
+                    top -= 1.f;
+                    dlim *= 2.f;
+                }
                 // the largest weight so far becomes 2^(top - 6): room for 6 binades before the next move
                 const float r0 = fmaxf(st.ref[0] + (old - top), m0 - top + 6.f), r1 = fmaxf(st.ref[1] + (old - top), m1 - top + 6.f);
                 st.scale(exp2_fast(st.ref[0] - r0), exp2_fast(st.ref[1] - r1));
@@ -524,7 +555,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 }
             }
             __syncwarp();   // every lane is done with the record
-            issue();
+            issue(stage);
+            stage = (stage + 1) & (kStages - 1);
+            parity ^= stage == 0 ? 1u : 0u;
         }
         if (DUP) {   // the low parts' columns join the high ones
 #pragma unroll
@@ -534,70 +567,73 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             st.z[0] += __shfl_xor_sync(0xffffffffu, st.z[0], 2);
             st.z[1] += __shfl_xor_sync(0xffffffffu, st.z[1], 2);
         }
-        // ---- the warps' states join in warp 0: 4 to 7 with 0 to 3, then 2 and 3, then 1
-        auto tree = [&]() {
-#pragma unroll 1
-            for (int n = kWarps / 2; n; n >>= 1) {
-                float4* mine = joins + (size_t)(warp & (n - 1)) * (MT + 1) * 32 + lane;
-                __syncthreads();
-                if (warp >= n && warp < 2 * n) st.put([&](int i, float4 x) { mine[i * 32] = x; });
-                __syncthreads();
-                if (warp < n) st.join([&](int i) { return mine[i * 32]; });
-            }
-        };
-        tree();
-        const bool whole = t0 == pl.seg0 && t1 == seg1;
-        bool write = whole;
-        if (!whole) {
-            const long long c0 = pl.seg0 / per, c1 = (seg1 - 1) / per;   // the CTAs that hold parts
+        // ---- the warps' states join: 4 to 7 with 0 to 3, then row w of those four by warp w
+        float4* mine = joins + (size_t)(warp & 3) * ROWS + lane;
+        __syncthreads();
+        if (warp >= 4) st.put(mine);
+        __syncthreads();
+        if (warp < 4) {
+            st.join(mine);
+            __syncwarp();
+            st.put(mine);
+        }
+        __syncthreads();
+        Slice sl;
+        const bool has = warp < MT;
+        const int row = has ? warp : 0;
+        sl.v = joins[row * 32 + lane];
+        sl.t = joins[MT * 32 + lane];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) sl.join(joins[k * ROWS + row * 32 + lane], joins[k * ROWS + MT * 32 + lane]);
+        bool write = sg.blk1 - sg.blk0 == sg.nb;
+        if (!write) {
+            const long long seg0 = lo + sg.rel - sg.blk0;                       // the list's number of its first tile
+            const long long c0 = seg0 / per, c1 = (seg0 + sg.nb - 1) / per;     // the CTAs that hold parts
             float4* slots = reinterpret_cast<float4*>(p.slots);
-            constexpr size_t SLOT = (size_t)(MT + 1) * 32;
-            if (warp == 0) {
-                float4* mine = slots + (2 * (size_t)blockIdx.x + (t0 == pl.seg0 ? 1 : 0)) * SLOT + lane;
-                st.put([&](int i, float4 x) { __stcg(mine + i * 32, x); });
+            float4* to = slots + (2 * (size_t)blockIdx.x + (sg.blk0 == 0 ? 1 : 0)) * ROWS + lane;
+            if (has) __stcg(to + row * 32, sl.v);
+            if (warp == 0) __stcg(to + MT * 32, sl.t);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int n = atomicAdd(p.tickets + c0, 1);
+                last_flag = n == (int)(c1 - c0);
+                if (last_flag) p.tickets[c0] = 0;   // armed for the next launch
                 __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const int n = atomicAdd(p.tickets + c0, 1);
-                    last_flag = n == (int)(c1 - c0);
-                    if (last_flag) p.tickets[c0] = 0;   // armed for the next launch
-                    __threadfence();
-                }
             }
             __syncthreads();
-            if (last_flag) {   // the last part is there: all of them, in order, warp w those of c0 + w, c0 + w + 8, ...
-                st.clear();
-                for (long long k = c0 + warp; k <= c1; k += kWarps) {
-                    const float4* part = slots + (2 * (size_t)k + (k == c0 ? 1 : 0)) * SLOT + lane;
-                    st.join([&](int i) { return __ldcg(part + i * 32); });
-                }
-                tree();
+            if (last_flag) {   // the last part is there: all of them, in order
                 write = true;
-            }
-        }
-        if (write && warp == 0) {
-            const int hc = 2 * tq;
-            const float l0 = __shfl_sync(0xffffffffu, st.z[0], 16 + tq), l1 = __shfl_sync(0xffffffffu, st.z[1], 16 + tq);
-            const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-            __half* o = p.out + ((size_t)pl.b * p.n_heads + h0 + hc) * HD + gq;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const float z0 = __shfl_sync(0xffffffffu, st.z[0], 4 * b + tq), z1 = __shfl_sync(0xffffffffu, st.z[1], 4 * b + tq);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float f = k & 1 ? 0x1p20f : 0x1p24f;
-                    const float y0 = fmaf(st.o[2 * b + (k >> 1)][2 * (k & 1)], f, z0) * i0;
-                    const float y1 = fmaf(st.o[2 * b + (k >> 1)][2 * (k & 1) + 1], f, z1) * i1;
-                    if (hc < nh) o[32 * b + 8 * k] = __float2half_rn(y0);
-                    if (hc + 1 < nh) o[HD + 32 * b + 8 * k] = __float2half_rn(y1);
+                const float4* part = slots + (2 * (size_t)c0 + 1) * ROWS + lane;
+                sl.v = __ldcg(part + row * 32);
+                sl.t = __ldcg(part + MT * 32);
+#pragma unroll 4
+                for (long long k = c0 + 1; k <= c1; ++k) {
+                    part = slots + 2 * (size_t)k * ROWS + lane;
+                    sl.join(__ldcg(part + row * 32), __ldcg(part + MT * 32));
                 }
             }
         }
-        if (t1 >= hi) break;
-        seek(pl, t1);
+        if (write && has) {
+            const int hc = 2 * tq, b = warp >> 1;
+            const float l0 = __shfl_sync(0xffffffffu, sl.t.x, 16 + tq), l1 = __shfl_sync(0xffffffffu, sl.t.y, 16 + tq);
+            const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+            const float z0 = __shfl_sync(0xffffffffu, sl.t.x, 4 * b + tq), z1 = __shfl_sync(0xffffffffu, sl.t.y, 4 * b + tq);
+            __half* o = p.out + ((size_t)sg.b * p.n_heads + h0 + hc) * HD + 16 * warp + gq;
+            if (hc < nh) {
+                o[0] = __float2half_rn(fmaf(sl.v.x, 0x1p24f, z0) * i0);
+                o[8] = __float2half_rn(fmaf(sl.v.z, 0x1p20f, z0) * i0);
+            }
+            if (hc + 1 < nh) {
+                o[HD] = __float2half_rn(fmaf(sl.v.y, 0x1p24f, z1) * i1);
+                o[HD + 8] = __float2half_rn(fmaf(sl.v.w, 0x1p20f, z1) * i1);
+            }
+        }
+        if (sg.rel + sg.blk1 - sg.blk0 >= run) break;
+        sg.next(p, S, run);
     }
     if (dead) {   // copies may still be in flight: wait for them (again with a limit) before leaving
-        for (; used < issued; ++used) bar_wait(bar0 + 8 * (used % kStages), (used / kStages) & 1);
+        for (int i = 0; i < kStages; ++i) bar_wait(bar0 + 8 * ((stage + i) & (kStages - 1)), parity ^ (stage + i >= kStages ? 1u : 0u));
     }
 }
 
@@ -678,6 +714,7 @@ extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, con
     QL_REQUIRE(batch >= 1 && batch <= 65535 && batch * n_heads < (1ll << 31) / 128, std::string(nm) + ": batch out of range");
     QL_REQUIRE(max_blocks_per_seq >= 1 && max_blocks_per_seq < (1ll << 27) && num_blocks >= 1 && num_blocks < (1ll << 31),
                std::string(nm) + ": bad table or pool size");
+    QL_REQUIRE(batch * max_blocks_per_seq < (1ll << 38) / n_heads, std::string(nm) + ": batch * max_blocks_per_seq out of range");
     QL_REQUIRE((reinterpret_cast<uintptr_t>(d_pool) & 15) == 0 && (reinterpret_cast<uintptr_t>(d_workspace) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(d_q) & 3) == 0 && (reinterpret_cast<uintptr_t>(d_out) & 3) == 0,
                std::string(nm) + ": the pool and the workspace must be 16-byte aligned, q and the output 4-byte aligned");
