@@ -50,6 +50,7 @@ enum DevErrWhere {
     kErrMoeExpert = 12,
     kErrKvSlot = 13,
     kErrSampleArg = 14,
+    kErrAttnStage = 15,
 };
 // The current device's record (allocated on first use, zero-filled).
 DevError* device_error_record();

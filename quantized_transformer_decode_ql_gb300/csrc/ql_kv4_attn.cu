@@ -40,6 +40,7 @@ constexpr int kStages = 4;                // tiles of a warp in flight
 constexpr int kCtasPerSm = 2;
 constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
 constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kNone = -0x7fffffff - 1;    // no tile left to copy
 
 constexpr size_t kSlotBytes = (size_t)(128 / 16 + 1) * 32 * sizeof(float4);   // a stored state at HD 128
 
@@ -65,10 +66,18 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(b0));
+__device__ __forceinline__ void mma8_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+// The same with C = 0.
+__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // The transpose of an 8 x 8 f16 matrix held one row pair per lane.
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
@@ -125,8 +134,8 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t a) {
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2, %3;\n selp.u32 %0, 1, 0, q;\n}"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(2000u) : "memory");
+        "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
@@ -241,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     __shared__ __align__(8) unsigned long long bars[kWarps * kStages];
     __shared__ Segment ahead[kWarps];                        // where each warp's copies are
     __shared__ int last_flag;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane, and known to be
     const int gq = lane >> 2, tq = lane & 3;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * REC;
     const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars) + warp * kStages * 8;
@@ -306,60 +316,68 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     int pblk, pend;                    // the next tile to copy and the end of its segment; pend 0: none left
     const int32_t* prow;               // its sequence's block table
     const uint8_t* ppool;              // the pool at its kv head
-    int phys = -1;                     // its block, loaded a tile ahead of the copy
+    int phys = -1;                     // its block, loaded a tile ahead of the copy (kNone: no tile)
     const long long rec_stride = (long long)p.n_kv * REC;
+    const uint32_t elected = lane == 0;
+    const unsigned long long policy = l2_evict_first();
     auto enter = [&](const Segment& g) {   // the warp's first tile in segment g, if it has one
         pblk = g.blk0 + ((warp - g.rel) & (kWarps - 1));
         pend = g.blk1;
         prow = p.block_tables + (size_t)g.b * p.maxb;
         ppool = p.pool + (size_t)(p.chunks == 1 ? g.s : g.s / p.chunks) * REC;
     };
-    auto settle = [&]() {              // past the segment's end: the next one with a tile of this warp
-        if (pblk >= pend && pend != 0) {
-            Segment g = ahead[warp];
-            do {
-                if (g.rel + g.blk1 - g.blk0 >= run) {
-                    pblk = pend = 0;
-                    return;
-                }
-                g.next(p, S, run);
-                enter(g);
-            } while (pblk >= pend);
-            __syncwarp();
-            if (lane == 0) ahead[warp] = g;
-            __syncwarp();
-        }
-        if (pend != 0) phys = __ldg(prow + pblk);
+    auto cross = [&]() {               // past the segment's end: the next one with a tile of this warp
+        Segment g = ahead[warp];
+        do {
+            if (g.rel + g.blk1 - g.blk0 >= run) {
+                phys = kNone;
+                return;
+            }
+            g.next(p, S, run);
+            enter(g);
+        } while (pblk >= pend);
+        __syncwarp();
+        if (lane == 0) ahead[warp] = g;
+        __syncwarp();
+        phys = __ldg(prow + pblk);
     };
     unsigned bad = 0;                  // stages without a record (a block id outside the pool, or a failed wait)
     bool dead = false;                 // a wait ran out: no more copies
     auto issue = [&](int st) {         // copy the tile whose block is loaded into stage st, then load the next one
-        if (pend == 0) return;
-        if ((unsigned)phys < (unsigned)p.num_blocks && !dead) {
-            if (lane == 0) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar0 + 8 * st), "r"(REC)
-                             : "memory");
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(ring + st * REC), "l"(ppool + phys * rec_stride), "r"(REC), "r"(bar0 + 8 * st),
-                    "l"(l2_evict_first())
-                    : "memory");
-            }
-            if (bad) bad &= ~(1u << st);
+        const bool in = (unsigned)phys < (unsigned)p.num_blocks;
+        if (in && bad == 0) {
+            asm volatile(
+                "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
+                "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+                "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%2], [%3], %1, [%0], %4;\n}"
+                ::"r"(bar0 + 8 * st), "r"(REC), "r"(ring + st * REC), "l"(ppool + phys * rec_stride), "l"(policy), "r"(elected)
+                : "memory");
         } else {
-            bad |= 1u << st;
+            if (phys == kNone) return;
+            bad = in && !dead ? bad & ~(1u << st) : bad | (1u << st);
             if (lane == 0) {
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar0 + 8 * st) : "memory");
-                if (!dead) record_device_error(err, kErrAttnBlock, (long long)ahead[warp].b * p.maxb + pblk, phys);
+                if (in && !dead) {
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar0 + 8 * st), "r"(REC)
+                                 : "memory");
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
+                        "[%3], %4;" ::"r"(ring + st * REC), "l"(ppool + phys * rec_stride), "r"(REC), "r"(bar0 + 8 * st), "l"(policy)
+                        : "memory");
+                } else {
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar0 + 8 * st) : "memory");
+                    if (!dead) record_device_error(err, kErrAttnBlock, (long long)ahead[warp].b * p.maxb + pblk, phys);
+                }
             }
         }
         pblk += kWarps;
-        settle();
+        if (pblk < pend) phys = __ldg(prow + pblk);
+        else cross();
     };
     if (lane == 0) ahead[warp] = sg;
     __syncwarp();
     enter(sg);
-    settle();
+    if (pblk < pend) phys = __ldg(prow + pblk);
+    else cross();
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) issue(i);
 
@@ -434,9 +452,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         // ---- this warp's tiles of the segment
 #pragma unroll 1
         for (; blk < sg.blk1; blk += kWarps) {
-            if (!bar_wait(bar0 + 8 * stage, parity) && !dead) {
+            if (!bar_wait(bar0 + 8 * stage, parity)) {
+                if (!dead && lane == 0) record_device_error(err, kErrAttnStage, sg.b, blk);
                 dead = true;
-                if (lane == 0) record_device_error(err, kErrGemvStage, sg.b, blk);
+                bad = ~0u;
             }
             const uint32_t rec = ring + stage * REC;
             // S^T: rows are keys krow, krow + 8 of this lane, columns heads 2 tq, 2 tq + 1
@@ -445,15 +464,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             lds_words(wb, rec + offK + 8 * (HD / 2));
             lds_words(da, rec + offKD);
             lds_words(db, rec + offKD + 16 * NB);
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            mma8(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz);
+            float s[4];
+            mma8_first(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz);
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[i] *= 0x1p-19f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float a[4] = {0.f, 0.f, 0.f, 0.f};
+                float a[4];
                 const uint32_t wa8 = wa[b] >> 8, wb8 = wb[b] >> 8;
-                mma16(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu, ql[b][0], ql[b][1]);
+                mma16_first(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu, ql[b][0], ql[b][1]);
                 mma16(a, wa[b] & 0x00f000f0u, wb[b] & 0x00f000f0u, wa8 & 0x00f000f0u, wb8 & 0x00f000f0u, qh[b][0], qh[b][1]);
                 const float2 d0 = __half22float2(h2(da[b / 2])), d1 = __half22float2(h2(db[b / 2]));
                 const float x0 = b & 1 ? d0.y : d0.x, x1 = b & 1 ? d1.y : d1.x;
@@ -473,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             s[2] *= fac[0];
             s[3] *= fac[1];
             const int left = sg.len - 16 * blk;
-            if (left < 16 || bad || dead) {   // slots past the context, or a block that is not there: any bytes
-                const int valid = dead || ((bad >> stage) & 1u) ? 0 : left;
+            if (left < 16 || bad != 0) {   // slots past the context, or a block that is not there: any bytes
+                const int valid = (bad >> stage) & 1u ? 0 : left;
                 if (krow >= valid) s[0] = s[1] = -INFINITY;
                 if (krow + 8 >= valid) s[2] = s[3] = -INFINITY;
 #pragma unroll
