@@ -38,8 +38,8 @@ constexpr int kHeads = 8;                 // query heads per tile
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStages = 4;                // tiles of a warp in flight
 constexpr int kCtasPerSm = 2;
-constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
 constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
 constexpr int kNone = -0x7fffffff - 1;    // no tile left to copy
 
 constexpr size_t kSlotBytes = (size_t)(128 / 16 + 1) * 32 * sizeof(float4);   // a stored state at HD 128
@@ -59,6 +59,7 @@ struct Params {
     int* tickets;       // [gridDim.x], zero between launches
 };
 
+// The matrix instructions are volatile: a plain asm may be moved into a branch that some lanes take.
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
     asm volatile(
@@ -245,20 +246,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     using R = Kv4<HD>;
     using St = State<HD>;
     constexpr int NB = R::NB, MT = HD / 16, REC = R::BYTES, ROWS = (MT + 1) * 32;
-    static_assert((kStages & (kStages - 1)) == 0 && MT <= kWarps, "");
-    extern __shared__ __align__(128) unsigned char smem[];   // [warp][stage] records, then 4 states
-    __shared__ __align__(8) unsigned long long bars[kWarps * kStages];
+    constexpr int STAGE = REC + 16;                          // a record and the barrier that its copy completes on
+    static_assert(MT <= kWarps, "");
+    extern __shared__ __align__(128) unsigned char smem[];   // [warp][stage], then 4 states
     __shared__ Segment ahead[kWarps];                        // where each warp's copies are
     __shared__ int last_flag;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane, and known to be
     const int gq = lane >> 2, tq = lane & 3;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * REC;
-    const uint32_t bar0 = (uint32_t)__cvta_generic_to_shared(bars) + warp * kStages * 8;
-    float4* const joins = reinterpret_cast<float4*>(smem + kWarps * kStages * REC);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * STAGE, ring_end = ring + kStages * STAGE;
+    float4* const joins = reinterpret_cast<float4*>(smem + kWarps * kStages * STAGE);
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar0 + 8 * i) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(ring + i * STAGE + REC) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
@@ -317,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     const int32_t* prow;               // its sequence's block table
     const uint8_t* ppool;              // the pool at its kv head
     int phys = -1;                     // its block, loaded a tile ahead of the copy (kNone: no tile)
-    const long long rec_stride = (long long)p.n_kv * REC;
+    const uint32_t rec_stride = (uint32_t)p.n_kv * REC;
     const uint32_t elected = lane == 0;
-    const unsigned long long policy = l2_evict_first();
+    const unsigned long long policy = l2_evict_first();   // the context is read once per step
     auto enter = [&](const Segment& g) {   // the warp's first tile in segment g, if it has one
         pblk = g.blk0 + ((warp - g.rel) & (kWarps - 1));
         pend = g.blk1;
@@ -343,31 +343,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     };
     unsigned bad = 0;                  // stages without a record (a block id outside the pool, or a failed wait)
     bool dead = false;                 // a wait ran out: no more copies
-    auto issue = [&](int st) {         // copy the tile whose block is loaded into stage st, then load the next one
+    // copy the tile whose block is loaded to the stage at rec, then load the next one's block
+    auto issue = [&](uint32_t rec) {
         const bool in = (unsigned)phys < (unsigned)p.num_blocks;
         if (in && bad == 0) {
             asm volatile(
                 "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
                 "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%2], [%3], %1, [%0], %4;\n}"
-                ::"r"(bar0 + 8 * st), "r"(REC), "r"(ring + st * REC), "l"(ppool + phys * rec_stride), "l"(policy), "r"(elected)
+                ::"r"(rec + REC), "r"(REC), "r"(rec), "l"(ppool + (size_t)(unsigned)phys * rec_stride), "l"(policy), "r"(elected)
                 : "memory");
         } else {
             if (phys == kNone) return;
-            bad = in && !dead ? bad & ~(1u << st) : bad | (1u << st);
+            const unsigned bit = 1u << ((rec - ring) / STAGE);
+            bad = in && !dead ? bad & ~bit : bad | bit;
             if (lane == 0) {
                 if (in && !dead) {
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar0 + 8 * st), "r"(REC)
-                                 : "memory");
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(rec + REC), "r"(REC) : "memory");
                     asm volatile(
                         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                        "[%3], %4;" ::"r"(ring + st * REC), "l"(ppool + phys * rec_stride), "r"(REC), "r"(bar0 + 8 * st), "l"(policy)
+                        "[%3], %4;" ::"r"(rec), "l"(ppool + (size_t)(unsigned)phys * rec_stride), "r"(REC), "r"(rec + REC), "l"(policy)
                         : "memory");
                 } else {
-                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar0 + 8 * st) : "memory");
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(rec + REC) : "memory");
                     if (!dead) record_device_error(err, kErrAttnBlock, (long long)ahead[warp].b * p.maxb + pblk, phys);
                 }
             }
+            __syncwarp();
         }
         pblk += kWarps;
         if (pblk < pend) phys = __ldg(prow + pblk);
@@ -379,11 +381,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     if (pblk < pend) phys = __ldg(prow + pblk);
     else cross();
 #pragma unroll 1
-    for (int i = 0; i < kStages; ++i) issue(i);
+    for (int i = 0; i < kStages; ++i) issue(ring + i * STAGE);
 
     St st;
-    int stage = 0;
-    uint32_t parity = 0;
+    uint32_t rec = ring, parity = 0;   // the stage of this warp's next tile, and its barrier's phase
     // lane constants: shared-memory offsets within a record
     const int krow = ((gq >> 1) & 3) | ((gq & 1) << 2);   // the key of this lane's row of the score product
     const uint32_t offK = R::KC + krow * (HD / 2) + 4 * NB * tq;
@@ -396,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         const int nh = min(kHeads, p.group - c * kHeads);
         const int h0 = g * p.group + c * kHeads;
         st.clear();
-        float top = kTop, dlim = 2.f;   // the largest weight's log2; the largest value scale that goes with it
+        float top = kTop;               // log2 of the largest weight
+        __half2 dlim = __float2half2_rn(2.f);   // the largest value scale that goes with it
         int blk = sg.blk0 + ((warp - sg.rel) & (kWarps - 1));
         // ---- q as the B operand of the score product
         uint32_t ql[NB][2], qh[NB][2], qz = 0;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                qs[b] = s * 0x1p-5f;
+                qs[b] = s * 0x1p-24f;
                 ql[b][0] = u32(__floats2half2_rn(v[b][0], v[b][2]));
                 ql[b][1] = u32(__floats2half2_rn(v[b][1], v[b][3]));
                 qh[b][0] = u32(__floats2half2_rn(v[b][4] * 0.0625f, v[b][6] * 0.0625f));
@@ -449,25 +451,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             fac[0] = __shfl_sync(0xffffffffu, f, 8 * tq);
             fac[1] = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
         }
-        // ---- this warp's tiles of the segment
-#pragma unroll 1
-        for (; blk < sg.blk1; blk += kWarps) {
-            if (!bar_wait(bar0 + 8 * stage, parity)) {
-                if (!dead && lane == 0) record_device_error(err, kErrAttnStage, sg.b, blk);
-                dead = true;
-                bad = ~0u;
-            }
-            const uint32_t rec = ring + stage * REC;
-            // S^T: rows are keys krow, krow + 8 of this lane, columns heads 2 tq, 2 tq + 1
+        // ---- the tiles, each in three steps
+        // scores: S^T of the record at rec, rows keys krow, krow + 8 of this lane, columns heads 2 tq, 2 tq + 1
+        auto score = [&](uint32_t rec, float (&s)[4]) {
             uint32_t wa[NB], wb[NB], da[NB / 2], db[NB / 2];
             lds_words(wa, rec + offK);
             lds_words(wb, rec + offK + 8 * (HD / 2));
             lds_words(da, rec + offKD);
             lds_words(db, rec + offKD + 16 * NB);
-            float s[4];
             mma8_first(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] *= 0x1p-19f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float a[4];
@@ -481,36 +473,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 s[2] = fmaf(x1, a[2], s[2]);
                 s[3] = fmaf(x1, a[3], s[3]);
             }
-            // the value scales of slots tq, tq + 4 (vd[0]) and tq + 8, tq + 12 (vd[1]), the minima of block gq
-            uint32_t vd[2][NB], vm[2];
+        };
+        // weights: p = 2^(s fac - ref) in two f16 parts, keys down the columns of the B operand
+        uint32_t ph[2], plo[2];
+        auto weigh = [&](uint32_t rec, int blk_, float (&s)[4]) {
+            float t[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = fmaf(s[k], fac[k & 1], -st.ref[k & 1]);
+            const int left = sg.len - 16 * blk_;
+            if (left < 16 || bad != 0) {   // slots past the context, or a block that is not there: any bytes
+                const int valid = (bad >> ((rec - ring) / STAGE)) & 1u ? 0 : left;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if ((k < 2 ? krow : krow + 8) >= valid) {
+                        t[k] = -INFINITY;
+                        s[k] = NAN;   // left out of every maximum
+                    }
+                }
+                // their value scales and minima become 0 (slot lane & 15: VD for lanes 0-15, VM for the others)
+                const uint32_t at = rec + (lane < 16 ? R::VD : R::VM) + 2 * R::vscale(lane & 15, 0);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %1, %2;\n @q st.shared.u16 [%0], %3;\n}" ::"r"(at + 4 * b),
+                                 "r"(lane & 15), "r"(valid), "h"((uint16_t)0) : "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy into this stage
+                __syncwarp();
+            }
+            // the value scales of slots tq, tq + 4 and tq + 8, tq + 12
+            uint32_t vd[2][NB];
             lds_words(vd[0], rec + offVD);
             lds_words(vd[1], rec + offVD + 4 * NB);
-            vm[0] = lds<uint32_t>(rec + offVM);
-            vm[1] = lds<uint32_t>(rec + offVM + 4 * NB);
-            s[0] *= fac[0];
-            s[1] *= fac[1];
-            s[2] *= fac[0];
-            s[3] *= fac[1];
-            const int left = sg.len - 16 * blk;
-            if (left < 16 || bad != 0) {   // slots past the context, or a block that is not there: any bytes
-                const int valid = (bad >> stage) & 1u ? 0 : left;
-                if (krow >= valid) s[0] = s[1] = -INFINITY;
-                if (krow + 8 >= valid) s[2] = s[3] = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t keep = (tq + 8 * k < valid ? 0x0000ffffu : 0u) | (tq + 4 + 8 * k < valid ? 0xffff0000u : 0u);
-                    vm[k] &= keep;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) vd[k][b] &= keep;
-                }
-            }
             __half2 dmax = __hmax2(h2(vd[0][0]), h2(vd[1][0]));
 #pragma unroll
             for (int b = 1; b < NB; ++b) dmax = __hmax2(dmax, __hmax2(h2(vd[0][b]), h2(vd[1][b])));
-            const float dm = fmaxf(__low2float(dmax), __high2float(dmax));
-            const float over = fmaxf(fmaxf(s[0], s[2]) - st.ref[0], fmaxf(s[1], s[3]) - st.ref[1]);
-            if (__any_sync(0xffffffffu, over > top || dm > dlim)) {
-                float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]), dw = dm;
+            const float over = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            if (__any_sync(0xffffffffu, over > top || !__hble2(dmax, dlim))) {
+                float m0 = fmaxf(s[0] * fac[0], s[2] * fac[0]), m1 = fmaxf(s[1] * fac[1], s[3] * fac[1]);
+                float dw = fmaxf(__low2float(dmax), __high2float(dmax));
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
@@ -520,34 +519,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 for (int o = 1; o < 32; o <<= 1) dw = fmaxf(dw, __shfl_xor_sync(0xffffffffu, dw, o));
                 // p and p d stay below 2^15: the largest scale is at most 2^(15 - top)
                 const float old = top;
-                while (top > 1.f && dw > dlim) {
+                float lim = __low2float(dlim);
+                while (top > 1.f && dw > lim) {
                     top -= 1.f;
-                    dlim *= 2.f;
+                    lim *= 2.f;
                 }
+                dlim = __float2half2_rn(lim);
                 // the largest weight so far becomes 2^(top - 6): room for 6 binades before the next move
                 const float r0 = fmaxf(st.ref[0] + (old - top), m0 - top + 6.f), r1 = fmaxf(st.ref[1] + (old - top), m1 - top + 6.f);
                 st.scale(exp2_fast(st.ref[0] - r0), exp2_fast(st.ref[1] - r1));
                 st.ref[0] = r0;
                 st.ref[1] = r1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (t[k] != -INFINITY) t[k] = fmaf(s[k], fac[k & 1], -st.ref[k & 1]);
             }
-            // p, in two f16 parts, keys down the columns of the B operand
-            uint32_t ph[2], plo[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float p0 = exp2_fast(s[2 * k] - st.ref[0]), p1 = exp2_fast(s[2 * k + 1] - st.ref[1]);
+                const float p0 = exp2_fast(t[2 * k]), p1 = exp2_fast(t[2 * k + 1]);
                 const __half2 hi2 = __floats2half2_rn(p0, p1);
                 const float2 hf = __half22float2(hi2);
                 ph[k] = transposed(u32(hi2));
                 plo[k] = transposed(u32(__floats2half2_rn(p0 - hf.x, p1 - hf.y)));
             }
-            // O^T: A rows are elements gq (+ 8, 16 times) of a 16-element half block, its columns the slots
-            uint32_t v[4][NB / 2];
+        };
+        // values: O^T, A rows elements gq (+ 8, 16 times) of a 16-element half block, its columns the slots
+        auto value = [&](uint32_t rec) {
+            uint32_t v[4][NB / 2], vd[2][NB];
+            lds_words(vd[0], rec + offVD);
+            lds_words(vd[1], rec + offVD + 4 * NB);
+            const uint32_t vm0 = lds<uint32_t>(rec + offVM), vm1 = lds<uint32_t>(rec + offVM + 4 * NB);   // minima of block gq
 #pragma unroll
             for (int k = 0; k < 4; ++k) lds_words(v[k], rec + offV + k * 4 * (HD / 2));
             const bool low = DUP && gq >= 4;
             {
                 const uint32_t one = gq == 4 ? 0x3c003c00u : 0u;
-                const uint32_t a0 = gq < NB ? vm[0] : one, a2 = gq < NB ? vm[1] : one;
+                const uint32_t a0 = gq < NB ? vm0 : one, a2 = gq < NB ? vm1 : one;
                 mma16(st.z, a0, 0u, a2, 0u, low ? plo[0] : ph[0], low ? plo[1] : ph[1]);
                 if (!DUP) mma16(st.z, a0, 0u, a2, 0u, plo[0], plo[1]);
             }
@@ -573,10 +580,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                     mma16(st.o[2 * b + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, pl_[0], pl_[1]);
                 }
             }
-            __syncwarp();   // every lane is done with the record
-            issue(stage);
-            stage = (stage + 1) & (kStages - 1);
-            parity ^= stage == 0 ? 1u : 0u;
+        };
+        auto arrived = [&]() {   // the record at rec
+            if (!bar_wait(rec + REC, parity)) {
+                if (!dead && lane == 0) record_device_error(err, kErrAttnStage, sg.b, blk);
+                dead = true;
+                bad = ~0u;
+            }
+            __syncwarp();
+        };
+        auto advance = [&]() {
+            rec += STAGE;
+            if (rec == ring_end) {
+                rec = ring;
+                parity ^= 1u;
+            }
+        };
+        // the scores of a tile beside the values of the one before it: two independent chains
+        if (blk < sg.blk1) {
+            float s[4];
+            arrived();
+            score(rec, s);
+            weigh(rec, blk, s);
+#pragma unroll 1
+            for (blk += kWarps; blk < sg.blk1; blk += kWarps) {
+                const uint32_t old = rec;
+                advance();
+                arrived();
+                score(rec, s);
+                value(old);
+                __syncwarp();   // every lane is done with the record
+                issue(old);
+                weigh(rec, blk, s);
+            }
+            value(rec);
+            __syncwarp();
+            issue(rec);
+            advance();
         }
         if (DUP) {   // the low parts' columns join the high ones
 #pragma unroll
@@ -652,13 +692,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         sg.next(p, S, run);
     }
     if (dead) {   // copies may still be in flight: wait for them (again with a limit) before leaving
-        for (int i = 0; i < kStages; ++i) bar_wait(bar0 + 8 * ((stage + i) & (kStages - 1)), parity ^ (stage + i >= kStages ? 1u : 0u));
+        for (int i = 0; i < kStages; ++i) {
+            bar_wait(rec + REC, parity);
+            rec += STAGE;
+            if (rec == ring_end) {
+                rec = ring;
+                parity ^= 1u;
+            }
+        }
     }
 }
 
 template <int HD>
 constexpr size_t attn_smem() {
-    return (size_t)kWarps * kStages * Kv4<HD>::BYTES + (size_t)(kWarps / 2) * (HD / 16 + 1) * 32 * sizeof(float4);
+    return (size_t)kWarps * kStages * (Kv4<HD>::BYTES + 16) + (size_t)(kWarps / 2) * (HD / 16 + 1) * 32 * sizeof(float4);
 }
 
 int attn_grid() { return kCtasPerSm * num_sms(); }

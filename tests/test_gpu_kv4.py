@@ -220,6 +220,20 @@ def test_attention_long_contexts_split_over_the_gpu(heads, n_kv, hd):
     check(got.cpu().numpy(), q, rec, bt, lens, 1 / math.sqrt(hd))
 
 
+@pytest.mark.parametrize("heads,hd", [(8, 128), (32, 128), (8, 64)])
+def test_attention_with_many_tiles_per_warp(heads, hd):
+    """More tiles than a warp's ring has stages, borders of sequences among them."""
+    ql = lib()
+    rng = np.random.default_rng(heads + hd)
+    lens = np.array([31007, 1234, 16010], np.int32)
+    bt, blocks = tables(rng, lens, 2000)
+    rec = random_records(rng, blocks, 4, hd)
+    q = rng.standard_normal((3, heads, hd)).astype(np.float16)
+    got = attend(ql, dev(q), dev(rec), dev(bt), dev(lens), 1 / math.sqrt(hd))
+    ql.ql_check_device_error()
+    check(got.cpu().numpy(), q, rec, bt, lens, 1 / math.sqrt(hd))
+
+
 def test_attention_many_short_sequences():
     ql = lib()
     rng = np.random.default_rng(8)
