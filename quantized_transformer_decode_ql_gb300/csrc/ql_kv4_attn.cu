@@ -67,18 +67,18 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
-}
-// The same with C = 0.
+// The same with C = z (a quad of zeros).
 __device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1) {
+                                            uint32_t b0, uint32_t b1, const float (&z)[4]) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
+}
+__device__ __forceinline__ void mma8_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0, const float (&z)[4]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%8,%9,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
 }
 // The transpose of an 8 x 8 f16 matrix held one row pair per lane.
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     extern __shared__ __align__(128) unsigned char smem[];   // [warp][stage], then 4 states
     __shared__ Segment ahead[kWarps];                        // where each warp's copies are
     __shared__ int last_flag;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
+    int lane;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));       // kept in a register, not read again and again
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane, and known to be
     const int gq = lane >> 2, tq = lane & 3;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * STAGE, ring_end = ring + kStages * STAGE;
@@ -265,17 +267,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     pdl_wait();
     pdl_trigger();
 
-    // the whole list's length, then this CTA's run of it
+    // the whole list's length, then this CTA's run of it and the segment that it starts in; a batch of up to
+    // 32 takes one round of loads
     const int S = p.n_kv * p.chunks;
+    int len0 = 0;
     long long total = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
-        int nb = b < p.batch ? (seq_len(p, b) + 15) >> 4 : 0;
-        if (b < p.batch && nb == 0 && blockIdx.x == 0 && warp == 0 && !(p.active && p.active[b] == 0)) {
-            const long long len = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
-            if (len != 0) record_device_error(err, kErrAttnLength, b, len);
+        const int len = b < p.batch ? seq_len(p, b) : 0;
+        if (b0 == 0) len0 = len;
+        if (b < p.batch && len == 0 && blockIdx.x == 0 && warp == 0 && !(p.active && p.active[b] == 0)) {
+            const long long l = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
+            if (l != 0) record_device_error(err, kErrAttnLength, b, l);
         }
-        total += __reduce_add_sync(0xffffffffu, nb);
+        total += __reduce_add_sync(0xffffffffu, (len + 15) >> 4);
     }
     total *= S;
     long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         long long before = 0;
         for (int b0 = 0;; b0 += 32) {
             const int b = b0 + lane;
-            const int len = b < p.batch ? seq_len(p, b) : 0;
+            const int len = b0 == 0 ? len0 : b < p.batch ? seq_len(p, b) : 0;
             long long incl = (long long)((len + 15) >> 4) * S;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -384,6 +389,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     for (int i = 0; i < kStages; ++i) issue(ring + i * STAGE);
 
     St st;
+    float zero[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
     uint32_t rec = ring, parity = 0;   // the stage of this warp's next tile, and its barrier's phase
     // lane constants: shared-memory offsets within a record
     const int krow = ((gq >> 1) & 3) | ((gq & 1) << 2);   // the key of this lane's row of the score product
@@ -459,12 +467,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             lds_words(wb, rec + offK + 8 * (HD / 2));
             lds_words(da, rec + offKD);
             lds_words(db, rec + offKD + 16 * NB);
-            mma8_first(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz);
+            mma8_first(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz, zero);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float a[4];
                 const uint32_t wa8 = wa[b] >> 8, wb8 = wb[b] >> 8;
-                mma16_first(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu, ql[b][0], ql[b][1]);
+                mma16_first(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu, ql[b][0], ql[b][1], zero);
                 mma16(a, wa[b] & 0x00f000f0u, wb[b] & 0x00f000f0u, wa8 & 0x00f000f0u, wb8 & 0x00f000f0u, qh[b][0], qh[b][1]);
                 const float2 d0 = __half22float2(h2(da[b / 2])), d1 = __half22float2(h2(db[b / 2]));
                 const float x0 = b & 1 ? d0.y : d0.x, x1 = b & 1 ? d1.y : d1.x;
@@ -652,13 +660,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             float4* to = slots + (2 * (size_t)blockIdx.x + (sg.blk0 == 0 ? 1 : 0)) * ROWS + lane;
             if (has) __stcg(to + row * 32, sl.v);
             if (warp == 0) __stcg(to + MT * 32, sl.t);
-            __threadfence();
             __syncthreads();
-            if (tid == 0) {
-                const int n = atomicAdd(p.tickets + c0, 1);
+            if (tid == 0) {   // releases the CTA's part (ordered by the barrier), acquires the others'
+                int n;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(p.tickets + c0) : "memory");
                 last_flag = n == (int)(c1 - c0);
                 if (last_flag) p.tickets[c0] = 0;   // armed for the next launch
-                __threadfence();
             }
             __syncthreads();
             if (last_flag) {   // the last part is there: all of them, in order
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 const float4* part = slots + (2 * (size_t)c0 + 1) * ROWS + lane;
                 sl.v = __ldcg(part + row * 32);
                 sl.t = __ldcg(part + MT * 32);
-#pragma unroll 4
+#pragma unroll 8
                 for (long long k = c0 + 1; k <= c1; ++k) {
                     part = slots + 2 * (size_t)k * ROWS + lane;
                     sl.join(__ldcg(part + row * 32), __ldcg(part + MT * 32));
