@@ -5,12 +5,15 @@
 // index order. Weights w = 2^((l - max) log2(e) / T) are 40-bit fixed-point integers and sums 64-bit
 // ones: exact, whatever the order of additions, and the same in every pass.
 //
-// The border of top-k (a count) or top-p (a weight) is found by digits, the histogram of 256 bins
-// naming the bin that the border falls into and the next round dividing that bin: first 8 bits at a
-// time of the distance from the largest logit on a 24-bit scale of 24 T, then of the logit's ordered
-// bits, then of the index, until 32 candidates or fewer are left, which one warp ranks.
+// The border of top-k (a count) or top-p (a weight) is found by digits, the histogram of 128 bins
+// naming the bin that the border falls into and the next round dividing that bin: 7 bits at a time of
+// the distance from the largest logit on a 24-bit scale of 24 T, then of the logit's ordered bits, then
+// of the index, until few enough candidates are left, which are ranked against one another.
 //
-// One CTA per row, the row read from L2 in every pass.
+// A row is read once: a thread-block cluster holds it in shared memory, each CTA a run of tokens, and
+// sums, histograms and candidates are exchanged through distributed shared memory, one cluster
+// barrier each; every CTA then draws the same conclusions. A histogram has a column per lane, so that
+// a warp's additions never meet; its weights are split into 20-bit halves that 32-bit sums hold.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>
@@ -22,9 +25,12 @@ namespace ql {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 256, kList = 32;
+constexpr int kBins = 128, kDigit = 7;
+constexpr int kList = 128;                      // candidates that are ranked directly
+constexpr int kMaxCluster = 8;
 constexpr int kScale = 40;                      // fixed-point bits of a weight of 1
 constexpr uint32_t kQMax = (1u << 24) - 1;      // the distance scale's last value: all that is farther
+constexpr uint32_t kKeyMin = 0x00800000u;       // the key after -inf's
 
 // 2^(j / 64) in 30 bits after the point
 __device__ const uint32_t kExp2[64] = {
@@ -43,7 +49,7 @@ typedef unsigned long long u64;
 struct Params {
     const void* logits;
     long long stride;
-    int vocab;
+    int vocab, per;               // tokens of a row, and of a CTA (a multiple of 8)
     const float* temperature;
     const int32_t* top_k;
     const float* top_p;
@@ -56,12 +62,41 @@ struct Params {
     float* probs;
 };
 
+// ---- the cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address of this CTA's shared variable in the CTA of rank r
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t r) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(r));
+    return a;
+}
+__device__ __forceinline__ u64 remote_u64(const void* p, uint32_t r) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, r)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t r) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, r)) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float canonical(float l) {
     l = l == l ? l : -INFINITY;          // NaN: never drawn
     return fminf(l, FLT_MAX) + 0.0f;     // -0 and +0 tie
 }
-__device__ __forceinline__ float load(const float* p, long long i) { return canonical(__ldg(p + i)); }
-__device__ __forceinline__ float load(const __half* p, long long i) { return canonical(__half2float(__ldg(p + i))); }
 
 // Bits that order as the logits do.
 __device__ __forceinline__ uint32_t key_of(float l) {
@@ -73,6 +108,18 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 struct RowScale {
     float ref, c_hi, c_lo, magic, low;   // (l - ref) (c_hi + c_lo): the exponent in 64ths
     float top, dist;                     // distance (top - l) dist
+    __device__ __forceinline__ void set(float t, float temp) {
+        constexpr float k_hi = 92.332482616893656754f, k_lo = (float)(92.332482616893656754 - (double)k_hi);   // 64 log2(e)
+        c_hi = __fdiv_rn(k_hi, temp);
+        c_lo = __fdiv_rn(fmaf(-c_hi, temp, k_hi) + k_lo, temp);
+        top = t;
+        // exponents of logits near the largest stay below 2^21 in magnitude, where the floor is exact
+        ref = fabsf(t * c_hi) > 0x1p20f ? t : 0.f;
+        const float x = t - ref;
+        magic = 12582912.0f - floorf(__fmul_rd(x, c_hi));
+        low = fmaxf(x - __fdiv_rn(3200.f, c_hi), -FLT_MAX);            // 2^-50 of the largest: weight 0
+        dist = fminf(__fdiv_rn(16777216.f / 24.f, temp), FLT_MAX);     // finite: 0 dist is 0
+    }
 };
 
 // The weight of logit l: 2^(40 + e / 64), e = (l - ref) 64 log2(e) / T minus its floor at the largest
@@ -105,78 +152,161 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// inclusive sum over the lanes up to this one
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
+// A token's place in the order: kept are the tokens up to and with the border's.
+struct Border {
+    uint32_t key;
+    int idx;
+    __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= idx); }
+    __device__ __forceinline__ void tighten(const Border& o) {
+        if (o.key > key || (o.key == key && o.idx < idx)) *this = o;
+    }
+};
+
+struct Entry {
+    u64 w;
+    uint32_t key;
+    int idx;
+};
 
 struct Shared {
     uint32_t table[64];
-    u64 mass[kBins];
-    uint32_t count[kBins];
+    u64 mine[2][kBins];          // this CTA's sums of a histogram's bins; every second round in turn
+    u64 all[kBins];              // the cluster's
+    float top;                   // this CTA's largest logit
+    float wtop[kWarps];
     u64 part[kWarps];
-    uint32_t wkey[kWarps];
-    int widx[kWarps];
-    uint32_t lkey[kList];
-    int lidx[kList];
-    u64 lw[kList];
+    u64 whole;
     uint32_t nlist;
-    RowScale row;
-    uint32_t bkey;
-    int bidx;
-    int bin;
-    uint32_t bin_count;
-    u64 base, total;
-    int token;
+    int first;
+    float least;
+    Border border;
+    u64 scan[kWarps];
 };
 
-// The border of the shortest prefix of the order with at least `target` tokens (mass false) or weight
-// (mass true): its last token's key and index, in sh.bkey and sh.bidx.
-template <typename T>
-__device__ void find_border(const T* lg, int vocab, bool mass, u64 target, Shared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const RowScale row = sh.row;
-    uint32_t qa = 0, qb = kQMax, ka = 0, kb = 0xFFFFFFFFu, ia = 0, ib = (uint32_t)vocab - 1;
+// A CTA's run of a row: token i at data[sh + i - base]; the places before and after hold -inf.
+struct Run {
+    const float4* data;
+    int base;        // the token at data[0], negative where the first row starts inside its vector
+    int v0, v1;      // this warp's vectors
+};
+template <typename F>
+__device__ __forceinline__ void each(const Run& r, int lane, F f) {
+    for (int v = r.v0 + lane; v < r.v1; v += 32) {
+        const float4 x = r.data[v];
+        const int i = r.base + 4 * v;
+        f(x.x, i);
+        f(x.y, i + 1);
+        f(x.z, i + 2);
+        f(x.w, i + 3);
+    }
+}
+
+// The border of the shortest prefix of the order, within `in`, that has `target` tokens (MASS false) or at
+// least the share `share` of the weight within `in` (MASS true). Returns `in` where there are fewer tokens.
+template <bool MASS>
+__device__ Border find_border(const Run& run, const RowScale& row, int vocab, const Border in, u64 target, float share,
+                              uint32_t* hist, Shared& sh, uint32_t ranks, int& turn) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    Entry *list = reinterpret_cast<Entry*>(hist), *ranked = list + kList;   // once a histogram has been read
+    uint32_t qa = 0, qb = kQMax, ka = kKeyMin, kb = key_of(row.top), ia = 0, ib = (uint32_t)vocab - 1;
     u64 base = 0;
-    for (;;) {
-        // the digit that this round divides: 8 bits of the widest interval still open
+    auto member = [&](float l, int i, uint32_t& q, uint32_t& k) {
+        q = distance(l, row);
+        k = key_of(l);
+        return q >= qa && q <= qb && k >= ka && k <= kb && (uint32_t)i >= ia && (uint32_t)i <= ib && in.keeps(k, i);
+    };
+    for (int round = 0;; ++round) {
+        // the digit that this round divides: the highest 7 bits of the first interval still open
         const int level = qa < qb ? 0 : ka < kb ? 1 : 2;
         const uint32_t a = level == 0 ? qa : level == 1 ? ka : ia, b = level == 0 ? qb : level == 1 ? kb : ib;
         const int bits = 32 - __clz((int)(b - a));
-        const int shift = bits > 8 ? bits - 8 : 0;
-        for (int i = tid; i < kBins; i += kThreads) {
-            sh.mass[i] = 0;
-            sh.count[i] = 0;
-        }
+        const int shift = bits > kDigit ? bits - kDigit : 0;
+        for (int i = tid; i < kBins * 32 * (MASS ? 2 : 1) / 4; i += kThreads)
+            reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid == 0) sh.nlist = 0;
         __syncthreads();
-        for (int i = tid; i < vocab; i += kThreads) {
-            const float l = load(lg, i);
-            const uint32_t q = distance(l, row), k = key_of(l);
-            if (q < qa || q > qb || k < ka || k > kb || (uint32_t)i < ia || (uint32_t)i > ib) continue;
+        each(run, lane, [&](float l, int i) {
+            uint32_t q, k;
+            if (!member(l, i, q, k)) return;
             const uint32_t v = level == 0 ? q - a : level == 1 ? b - k : (uint32_t)i - a;
-            atomicAdd(&sh.count[v >> shift], 1u);
-            if (mass) atomicAdd(&sh.mass[v >> shift], weight(l, row, sh.table));
-        }
-        __syncthreads();
-        if (tid == 0) {
-            u64 c = base;
-            int bin = kBins - 1;
-            for (int i = 0; i < kBins; ++i) {
-                const u64 v = mass ? sh.mass[i] : sh.count[i];
-                if (c + v >= target) {
-                    bin = i;
-                    break;
+            uint32_t* h = hist + (v >> shift) * 32 + lane;
+            if (MASS) {
+                const u64 w = weight(l, row, sh.table);
+                if (w != 0) {
+                    atomicAdd(h, (uint32_t)w & 0xfffffu);
+                    atomicAdd(h + kBins * 32, (uint32_t)(w >> 20));
                 }
-                c += v;
+            } else {
+                atomicAdd(h, 1u);
             }
-            sh.bin = bin;
-            sh.bin_count = sh.count[bin];
-            sh.base = c;
-            sh.nlist = 0;
-        }
+        });
         __syncthreads();
-        base = sh.base;
-        const uint32_t lo = (uint32_t)sh.bin << shift, hi = lo + ((1u << shift) - 1);
+        {   // four threads a bin, eight columns each, taken so that a warp's reads are on different banks
+            const int bin = tid >> 2, c0 = (tid & 3) * 8;
+            u64 v = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {   // a column holds at most 2^11 tokens of 2^20 each: below 2^32
+                const int c = c0 + ((j + bin) & 7);
+                v += hist[bin * 32 + c];
+                if (MASS) v += (u64)hist[(kBins + bin) * 32 + c] << 20;
+            }
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if ((tid & 3) == 0) sh.mine[turn][bin] = v;
+        }
+        cluster_sync();
+        if (tid < kBins) {
+            u64 v = 0;
+            for (uint32_t r = 0; r < ranks; ++r) v += remote_u64(&sh.mine[turn][tid], r);
+            sh.all[tid] = v;
+        }
+        turn ^= 1;
+        __syncthreads();
+        // every warp: the bin in which the running sum reaches the target
+        u64 v[kBins / 32], mine = 0;
+#pragma unroll
+        for (int j = 0; j < kBins / 32; ++j) {
+            v[j] = sh.all[lane * (kBins / 32) + j];
+            mine += v[j];
+        }
+        const u64 upto = warp_scan(mine, lane);
+        if (round == 0) {
+            const u64 sum = __shfl_sync(0xffffffffu, upto, 31);
+            if (MASS) {   // ceil(share * sum), exactly; 1 at least
+                const u64 s64 = share > 0.f ? __float2ull_rz(share * 0x1p64f) : 0;
+                target = __umul64hi(s64, sum) + (s64 * sum != 0 ? 1 : 0);
+                target = target == 0 ? 1 : target;
+            }
+            if (sum < target) return in;
+        }
+        const unsigned reach = __ballot_sync(0xffffffffu, base + upto >= target);
+        const int l = reach ? __ffs(reach) - 1 : 31;
+        u64 c = base + upto - mine;
+        int bin = lane * (kBins / 32);
+#pragma unroll
+        for (int j = 0; j < kBins / 32 - 1; ++j) {
+            if (bin == lane * (kBins / 32) + j && c + v[j] < target) {
+                c += v[j];
+                ++bin;
+            }
+        }
+        bin = __shfl_sync(0xffffffffu, bin, l);
+        base = __shfl_sync(0xffffffffu, c, l);
+        const uint32_t lo = (uint32_t)bin << shift, hi = lo + ((1u << shift) - 1);
         if (level == 1) {   // keys: bins fall from the largest
-            const uint32_t top = kb;
-            kb = top - lo;
-            ka = hi < top - ka ? top - hi : ka;
+            const uint32_t last = kb;
+            kb = last - lo;
+            ka = hi < last - ka ? last - hi : ka;
         } else if (level == 0) {
             qb = hi < qb - qa ? qa + hi : qb;
             qa += lo;
@@ -184,84 +314,122 @@ __device__ void find_border(const T* lg, int vocab, bool mass, u64 target, Share
             ib = hi < ib - ia ? ia + hi : ib;
             ia += lo;
         }
-        const uint32_t left = sh.bin_count;
-        __syncthreads();
-        if (left > kList) continue;
-        for (int i = tid; i < vocab; i += kThreads) {
-            const float l = load(lg, i);
-            const uint32_t q = distance(l, row), k = key_of(l);
-            if (q < qa || q > qb || k < ka || k > kb || (uint32_t)i < ia || (uint32_t)i > ib) continue;
+        if (!MASS) {
+            const u64 left = sh.all[bin];
+            if (left > kList) {
+                __syncthreads();   // sh.all is read before the next round writes it
+                continue;
+            }
+        } else if (round == 0 && vocab > 16 * kList) {   // rarely few enough after one digit
+            __syncthreads();
+            continue;
+        }
+        // the candidates: this CTA's, then everybody's
+        each(run, lane, [&](float l2, int i) {
+            uint32_t q, k;
+            if (!member(l2, i, q, k)) return;
             const uint32_t n = atomicAdd(&sh.nlist, 1u);
-            sh.lkey[n] = k;
-            sh.lidx[n] = i;
-            sh.lw[n] = mass ? weight(l, row, sh.table) : 1;
+            if (n < kList) list[n] = Entry{MASS ? weight(l2, row, sh.table) : 1ull, k, i};
+        });
+        cluster_sync();
+        uint32_t total = 0;
+        for (uint32_t r = 0; r < ranks; ++r) {
+            const uint32_t n = remote_u32(&sh.nlist, r);
+            if ((uint32_t)tid >= total && (uint32_t)tid < total + n && total + n <= kList) {
+                const Entry* e = &list[tid - total];
+                ranked[tid].w = remote_u64(&e->w, r);
+                const u64 ki = remote_u64(&e->key, r);
+                ranked[tid].key = (uint32_t)ki;
+                ranked[tid].idx = (int)(ki >> 32);
+            }
+            total += n;
+        }
+        if (tid == 0) sh.border = in;
+        cluster_sync();   // the lists may be written again
+        if (total > kList) continue;
+        if ((uint32_t)tid < total) {
+            const Entry e = ranked[tid];
+            u64 cum = base;
+            for (uint32_t j = 0; j < total; ++j) {
+                const Entry o = ranked[j];
+                if (o.key > e.key || (o.key == e.key && o.idx <= e.idx)) cum += o.w;
+            }
+            if (cum >= target && cum - e.w < target) sh.border = Border{e.key, e.idx};
         }
         __syncthreads();
-        if (warp == 0) {
-            const uint32_t n = sh.nlist;
-            const uint32_t k = lane < n ? sh.lkey[lane] : 0;
-            const int idx = lane < n ? sh.lidx[lane] : 0x7FFFFFFF;
-            u64 cum = 0;
-            for (uint32_t j = 0; j < n; ++j) {
-                const uint32_t kj = sh.lkey[j];
-                if (kj > k || (kj == k && sh.lidx[j] <= idx)) cum += sh.lw[j];
-            }
-            // the border: the first of the order whose running sum reaches the target, else the last
-            const bool reach = lane < n && base + cum >= target;
-            bool best = lane < n;
-            for (uint32_t j = 0; j < n; ++j) {
-                const bool rj = __shfl_sync(0xffffffffu, (int)reach, j);
-                const uint32_t kj = sh.lkey[j];
-                const bool before = kj > k || (kj == k && sh.lidx[j] < idx);
-                if (rj && (!reach || before)) best = false;
-                if (!rj && !reach && (kj < k || (kj == k && sh.lidx[j] > idx))) best = false;
-            }
-            if (best) {
-                sh.bkey = k;
-                sh.bidx = idx;
-            }
-        }
+        const Border found = sh.border;
         __syncthreads();
-        return;
+        return found;
     }
 }
 
-// The weight of the kept tokens of [lo, hi), all threads; the sum goes to sh.total.
 template <typename T>
-__device__ u64 kept_weight(const T* lg, int i, uint32_t bkey, int bidx, const RowScale& row, const uint32_t* table) {
-    const float l = load(lg, i);
-    const uint32_t k = key_of(l);
-    return (k > bkey || (k == bkey && i <= bidx)) ? weight(l, row, table) : 0;
-}
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
 
+// The CTA's run of the row into shared memory, sh places further on so that 16-byte loads are aligned at
+// both ends; returns this thread's largest logit.
 template <typename T>
-__device__ void sum_kept(const T* lg, int vocab, uint32_t bkey, int bidx, Shared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const RowScale row = sh.row;
-    const int per = (vocab + kWarps - 1) / kWarps;
-    u64 w = 0;
-    const int end = min(vocab, (warp + 1) * per);
-    for (int i = warp * per + lane; i < end; i += 32) w += kept_weight(lg, i, bkey, bidx, row, sh.table);
-    w = warp_sum(w);
-    if (lane == 0) sh.part[warp] = w;
-    __syncthreads();
-    if (tid == 0) {
-        u64 t = 0;
-        for (int i = 0; i < kWarps; ++i) t += sh.part[i];
-        sh.total = t;
+__device__ __forceinline__ float load_run(const T* src, int n, int off, float* data, int nvec) {
+    constexpr int W = 16 / (int)sizeof(T);   // tokens of a 16-byte load
+    float mx = -INFINITY;
+    auto put = [&](int at, float l) {
+        l = canonical(l);
+        data[at] = l;
+        mx = fmaxf(mx, l);
+    };
+    const int head = min(n, (W - off) % W);            // tokens before the first whole vector
+    const int body = (n - head) / W;
+    const uint4* v = reinterpret_cast<const uint4*>(src + head);
+    float4* to = reinterpret_cast<float4*>(data + off + head);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < body; i += kThreads) {
+        const uint4 x = __ldg(v + i);
+        float l[W];
+        if constexpr (W == 4) {
+            l[0] = __uint_as_float(x.x);
+            l[1] = __uint_as_float(x.y);
+            l[2] = __uint_as_float(x.z);
+            l[3] = __uint_as_float(x.w);
+        } else {
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+                l[2 * j] = f.x;
+                l[2 * j + 1] = f.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            l[j] = canonical(l[j]);
+            mx = fmaxf(mx, l[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) to[i * (W / 4) + j] = make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
     }
-    __syncthreads();
+    const int tail = head + body * W;
+    for (int i = threadIdx.x; i < head; i += kThreads) put(off + i, to_float(src[i]));
+    for (int i = tail + threadIdx.x; i < n; i += kThreads) put(off + i, to_float(src[i]));
+    for (int i = threadIdx.x; i < off; i += kThreads) data[i] = -INFINITY;
+    for (int i = off + n + threadIdx.x; i < 4 * nvec; i += kThreads) data[i] = -INFINITY;
+    return mx;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* err) {
+    extern __shared__ __align__(16) float dyn[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long b = blockIdx.x;
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const long long b = blockIdx.x / ranks;
     pdl_wait();
     pdl_trigger();
+    // every decision below is the same in all CTAs of the cluster
     if (p.active && p.active[b] == 0) return;
-    const T* lg = static_cast<const T*>(p.logits) + b * p.stride;
     const float temp = p.temperature ? p.temperature[b] : 1.0f;
     const float topp = p.top_p ? p.top_p[b] : 1.0f;
     const float minp = p.min_p ? p.min_p[b] : 0.0f;
@@ -271,135 +439,143 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
     const float u = p.uniform[at];
     const bool ok = temp >= 0.f && temp < INFINITY && topp == topp && minp == minp && u >= 0.f && u < 1.f;
     if (!ok) {
-        if (tid == 0) {
+        if (tid == 0 && rank == 0) {
             record_device_error(err, kErrSampleArg, b, 0);
             p.tokens[b] = -1;
             if (p.probs) p.probs[b] = 0.f;
         }
         return;
     }
+    const int first = (int)rank * p.per;
+    const int n = max(0, min(p.vocab - first, p.per));
+    const T* src = static_cast<const T*>(p.logits) + b * p.stride + first;
+    const int off = (int)((reinterpret_cast<uintptr_t>(src) % 16) / sizeof(T));
+    const int nvec = (off + n + 3) / 4;
+    uint32_t* hist = reinterpret_cast<uint32_t*>(dyn + p.per + 8);
     if (tid < 64) sh.table[tid] = kExp2[tid];
-    // the largest logit, at its lowest index
-    uint32_t bk = 0;
-    int bi = 0x7FFFFFFF;
-    for (int i = tid; i < p.vocab; i += kThreads) {
-        const uint32_t k = key_of(load(lg, i));
-        if (k > bk) {
-            bk = k;
-            bi = i;
-        }
-    }
+    float top = load_run(src, n, off, dyn, nvec);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const uint32_t k = __shfl_xor_sync(0xffffffffu, bk, o);
-        const int i = __shfl_xor_sync(0xffffffffu, bi, o);
-        if (k > bk || (k == bk && i < bi)) {
-            bk = k;
-            bi = i;
-        }
-    }
-    if (lane == 0) {
-        sh.wkey[warp] = bk;
-        sh.widx[warp] = bi;
-    }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.wtop[warp] = top;
     __syncthreads();
-    bk = sh.wkey[0];
-    bi = sh.widx[0];
-    for (int w = 1; w < kWarps; ++w) {
-        if (sh.wkey[w] > bk || (sh.wkey[w] == bk && sh.widx[w] < bi)) {
-            bk = sh.wkey[w];
-            bi = sh.widx[w];
-        }
+    if (tid == 0) {
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.wtop[w]);
+        sh.top = top;
     }
-    const bool none = bk <= 0x007FFFFFu;   // the key of -inf
-    if (none || temp < kMinTemperature) {
-        if (tid == 0) {
-            p.tokens[b] = none ? -1 : bi;
-            if (p.probs) p.probs[b] = none ? 0.f : 1.f;
+    cluster_sync();
+    top = lane < (int)ranks ? __uint_as_float(remote_u32(&sh.top, (uint32_t)lane)) : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -INFINITY) {
+        cluster_sync();   // nobody leaves while its shared memory may be read
+        if (tid == 0 && rank == 0) {
+            p.tokens[b] = -1;
+            if (p.probs) p.probs[b] = 0.f;
         }
         return;
     }
-    const float top = __uint_as_float(bk & 0x80000000u ? bk ^ 0x80000000u : ~bk);
-    if (tid == 0) {
-        const double c = 64.0 * 1.4426950408889634 / (double)temp;
-        RowScale r;
-        // exponents of logits near the largest stay below 2^21 in magnitude, where the floor is exact
-        r.ref = fabs((double)top * c) > 0x1p20 ? top : 0.f;
-        r.c_hi = (float)c;
-        r.c_lo = (float)(c - (double)r.c_hi);
-        const float x = top - r.ref;
-        r.magic = 12582912.0f - floorf(__fmul_rd(x, r.c_hi));
-        r.low = fmaxf(x - (float)(3200.0 / c), -FLT_MAX);       // 2^-50 of the largest: weight 0
-        r.top = top;
-        r.dist = (float)fmin(16777216.0 / (24.0 * (double)temp), (double)FLT_MAX);   // finite: 0 r.dist is 0
-        sh.row = r;
+    Run run;
+    run.data = reinterpret_cast<const float4*>(dyn);
+    run.base = first - off;
+    const int vpw = (nvec + kWarps - 1) / kWarps;
+    run.v0 = warp * vpw;
+    run.v1 = min(nvec, run.v0 + vpw);
+    int turn = 0;
+    if (temp < kMinTemperature) {   // the arg max: the lowest index of the largest logit
+        int idx = 0x7FFFFFFF;
+        each(run, lane, [&](float l, int i) { idx = l == top && i < idx ? i : idx; });
+        idx = __reduce_min_sync(0xffffffffu, idx);
+        if (tid == 0) sh.first = 0x7FFFFFFF;
+        __syncthreads();
+        if (lane == 0) atomicMin(&sh.first, idx);
+        cluster_sync();
+        if (tid == 0 && rank == 0) {
+            int best = 0x7FFFFFFF;
+            for (uint32_t r = 0; r < ranks; ++r) best = min(best, (int)remote_u32(&sh.first, r));
+            p.tokens[b] = best;
+            if (p.probs) p.probs[b] = 1.f;
+        }
+        cluster_sync();
+        return;
     }
-    __syncthreads();
-    uint32_t bkey = 0x00800000u;   // above -inf
-    int bidx = 0x7FFFFFFF;
+    RowScale row;
+    row.set(top, temp);
+    Border border = {kKeyMin, 0x7FFFFFFF};   // all that is above -inf
     if (minp > 0.f) {
-        // the least f32 at or above top + T ln(min_p)
-        const float thr = minp >= 1.f ? top : __double2float_ru((double)top + (double)temp * log((double)minp));
-        const uint32_t k = key_of(thr + 0.0f);
-        bkey = k > bkey ? k : bkey;
+        if (tid == 0)   // the least f32 at or above top + T ln(min_p)
+            sh.least = minp >= 1.f ? top : __double2float_ru((double)top + (double)temp * log((double)minp));
+        __syncthreads();
+        border.tighten(Border{max(kKeyMin, key_of(sh.least + 0.0f)), 0x7FFFFFFF});
     }
-    auto tighten = [&]() {
-        if (sh.bkey > bkey || (sh.bkey == bkey && sh.bidx < bidx)) {
-            bkey = sh.bkey;
-            bidx = sh.bidx;
-        }
-    };
-    uint32_t kkey = 0x00800000u;
-    int kidx = 0x7FFFFFFF;
+    Border prefix = {kKeyMin, 0x7FFFFFFF};
     if (topk > 0 && topk < p.vocab) {
-        find_border(lg, p.vocab, false, (u64)topk, sh);
-        kkey = sh.bkey;
-        kidx = sh.bidx;
-        tighten();
-        __syncthreads();
+        prefix = find_border<false>(run, row, p.vocab, prefix, (u64)topk, 0.f, hist, sh, ranks, turn);
+        border.tighten(prefix);
     }
-    if (topp < 1.f) {
-        sum_kept(lg, p.vocab, kkey, kidx, sh);
-        const double want = ceil((double)topp * (double)sh.total);
-        find_border(lg, p.vocab, true, want < 1.0 ? 1ull : (u64)want, sh);
-        tighten();
-        __syncthreads();
+    if (topp < 1.f) border.tighten(find_border<true>(run, row, p.vocab, prefix, 0, topp, hist, sh, ranks, turn));
+
+    // ---- the draw: the kept weight of every warp's tokens, then of every CTA's
+    u64 w = 0;
+    each(run, lane, [&](float l, int i) {
+        if (border.keeps(key_of(l), i)) w += weight(l, row, sh.table);
+    });
+    w = warp_sum(w);
+    if (lane == 0) sh.part[warp] = w;
+    __syncthreads();
+    if (tid == 0) {
+        u64 t = 0;
+        for (int i = 0; i < kWarps; ++i) t += sh.part[i];
+        sh.whole = t;
     }
-    // the draw: the warp whose range the running sum passes the target in, then that warp's tokens
-    sum_kept(lg, p.vocab, bkey, bidx, sh);
-    if (warp == 0) {
-        const RowScale row = sh.row;
-        const double target = (double)u * (double)sh.total;
-        u64 c = 0;
-        int w = 0;
-        while (w < kWarps - 1 && (double)(c + sh.part[w]) <= target) c += sh.part[w++];
-        const int per = (p.vocab + kWarps - 1) / kWarps;
-        const int end = min(p.vocab, (w + 1) * per);
-        int token = bi;
-        u64 tw = 0;
-        for (int i0 = w * per; i0 < end; i0 += 32) {
-            const int i = i0 + lane;
-            const u64 wt = i < end ? kept_weight(lg, i, bkey, bidx, row, sh.table) : 0;
-            u64 s = wt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 v = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += v;
-            }
-            const unsigned pass = __ballot_sync(0xffffffffu, wt > 0 && (double)(c + s) > target);
-            if (pass) {
-                const int n = __ffs(pass) - 1;
-                token = i0 + n;
-                tw = __shfl_sync(0xffffffffu, wt, n);
-                break;
-            }
-            c += __shfl_sync(0xffffffffu, s, 31);
+    cluster_sync();
+    u64 total = 0, before = 0;
+    {
+        const u64 t = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
+        const u64 upto = warp_scan(t, lane);
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        before = __shfl_sync(0xffffffffu, upto - t, (int)rank);
+    }
+    // the first token at which the running sum exceeds u total: reaches floor(u total) + 1, exactly
+    const u64 target = __umul64hi(__float2ull_rz(u * 0x1p64f), total) + 1;
+    if (target > before && target <= before + sh.whole) {   // in this CTA
+        u64 c = before;
+        int ow = 0;
+        while (ow < kWarps - 1 && c + sh.part[ow] < target) c += sh.part[ow++];
+        // that warp's tokens over all threads, a few consecutive ones each
+        const int t0 = 4 * ow * vpw, t1 = 4 * min(nvec, (ow + 1) * vpw);
+        const int each_n = (t1 - t0 + kThreads - 1) / kThreads;
+        const int a = t0 + tid * each_n, e = min(t1, a + each_n);
+        u64 s = 0;
+        for (int j = a; j < e; ++j) {
+            const float l = dyn[j];
+            if (border.keeps(key_of(l), run.base + j)) s += weight(l, row, sh.table);
         }
-        if (lane == 0) {
-            p.tokens[b] = token;
-            if (p.probs) p.probs[b] = (float)((double)tw / (double)sh.total);
+        const u64 incl = warp_scan(s, lane);
+        if (lane == 31) sh.scan[warp] = incl;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) c += sh.scan[k];
+        c += incl - s;
+        if (c < target && c + s >= target) {
+            for (int j = a; j < e; ++j) {
+                const float l = dyn[j];
+                const u64 x = border.keeps(key_of(l), run.base + j) ? weight(l, row, sh.table) : 0;
+                c += x;
+                if (x != 0 && c >= target) {
+                    p.tokens[b] = run.base + j;
+                    if (p.probs) p.probs[b] = (float)((double)x / (double)total);
+                    break;
+                }
+            }
         }
     }
+    cluster_sync();   // as above
+}
+
+// CTAs of a row: enough that its run fits beside the histogram twice per SM, more while the batch leaves SMs idle
+int cluster_for(int64_t batch, int64_t vocab) {
+    int c = 1;
+    while (c < kMaxCluster && (vocab > 20000ll * c || (batch * c * 2 <= num_sms() && vocab > 2048ll * c))) c *= 2;
+    return c;
 }
 
 }  // namespace
@@ -407,10 +583,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
 int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "sampling: no device error record");
+    const int c = cluster_for(a.batch, a.vocab);
+    if (a.batch * c >= (1ll << 31)) return set_error(QL_EINVAL, "sampling: batch out of range");
     Params p = {};
     p.logits = a.logits;
     p.stride = a.row_stride;
     p.vocab = (int)a.vocab;
+    p.per = (int)(((a.vocab + c - 1) / c + 7) / 8 * 8);
     p.temperature = a.temperature;
     p.top_k = a.top_k;
     p.top_p = a.top_p;
@@ -421,10 +600,26 @@ int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     p.active = a.active;
     p.tokens = a.tokens;
     p.probs = a.probs;
-    const dim3 grid((unsigned)a.batch);
-    const cudaError_t e = a.dtype == QL_DTYPE_F32
-                              ? launch(sample_kernel<float>, grid, dim3(kThreads), 0, s, pdl, p, err)
-                              : launch(sample_kernel<__half>, grid, dim3(kThreads), 0, s, pdl, p, err);
+    const size_t smem = (size_t)(p.per + 8) * 4 +
+                        (a.top_p ? (size_t)kBins * 32 * 8 : a.top_k ? (size_t)kBins * 32 * 4 : 0);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.batch * c));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    auto go = [&](auto kernel) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, p, err) : e;
+    };
+    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? go(sample_kernel<float>) : go(sample_kernel<__half>);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "sampling launch");
 }
 
