@@ -28,7 +28,6 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 128, kDigit = 7;
 constexpr int kList = 128;                      // candidates that are ranked directly
 constexpr int kMaxCluster = 8;
-constexpr int kScale = 40;                      // fixed-point bits of a weight of 1
 constexpr uint32_t kQMax = (1u << 24) - 1;      // the distance scale's last value: all that is farther
 constexpr uint32_t kKeyMin = 0x00800000u;       // the key after -inf's
 
@@ -94,8 +93,7 @@ __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t r) {
 }
 
 __device__ __forceinline__ float canonical(float l) {
-    l = l == l ? l : -INFINITY;          // NaN: never drawn
-    return fminf(l, FLT_MAX) + 0.0f;     // -0 and +0 tie
+    return fminf(fmaxf(l, -INFINITY), FLT_MAX) + 0.0f;   // NaN: -inf, never drawn; -0 and +0 tie
 }
 
 // Bits that order as the logits do.
@@ -117,7 +115,7 @@ struct RowScale {
         ref = fabsf(t * c_hi) > 0x1p20f ? t : 0.f;
         const float x = t - ref;
         magic = 12582912.0f - floorf(__fmul_rd(x, c_hi));
-        low = fmaxf(x - __fdiv_rn(3200.f, c_hi), -FLT_MAX);            // 2^-50 of the largest: weight 0
+        low = fmaxf(x - __fdiv_rn(2624.f, c_hi), -FLT_MAX);            // 2^-41 of the largest: weight 0
         dist = fminf(__fdiv_rn(16777216.f / 24.f, temp), FLT_MAX);     // finite: 0 dist is 0
     }
 };
@@ -131,16 +129,17 @@ __device__ __forceinline__ u64 weight(float l, const RowScale& r, const uint32_t
     const float z = __fmaf_rd(x, r.c_hi, r.magic);
     float f = __fmaf_rn(x, r.c_hi, r.magic - z);
     f = __fmaf_rn(x, r.c_lo, f);
-    const int k = __float_as_int(z) - 0x4B400000;
+    const uint32_t bits = __float_as_uint(z);    // 0x4B400000 + e, e >= -41 * 64 - 1
     constexpr float y = 0.010830424696249145f;   // ln 2 / 64
     constexpr float s = 4294967296.0f;
     float q = fmaf(f, s * y * y * y * y / 24.f, s * y * y * y / 6.f);
     q = fmaf(f, q, s * y * y / 2.f);
     q = fmaf(f, q, s * y);
-    const int t = (int)table[k & 63];
-    const uint32_t m = (uint32_t)(t + __mulhi(t, __float2int_rn(f * q)));
-    const int sh = min(-(k >> 6), 63);
-    return ((u64)m << (kScale - 30)) >> sh;
+    const int t = (int)table[bits & 63];
+    const uint32_t m = (uint32_t)(t + __mulhi(t, __float2int_rn(f * q)));   // 30 bits after the point
+    // m 2^(40 - 30 + e / 64) = (m 2^32) >> (22 - e / 64); the shift is below 64 but for e = -41 * 64 - 1, all of whose bits go
+    const uint32_t sh = min(22u + 0x4B400000u / 64 - (bits >> 6), 63u);
+    return ((u64)m << 32) >> sh;
 }
 
 __device__ __forceinline__ uint32_t distance(float l, const RowScale& r) {
@@ -167,6 +166,7 @@ struct Border {
     uint32_t key;
     int idx;
     __device__ __forceinline__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= idx); }
+    __device__ __forceinline__ bool all() const { return key == kKeyMin && idx == 0x7FFFFFFF; }
     __device__ __forceinline__ void tighten(const Border& o) {
         if (o.key > key || (o.key == key && o.idx < idx)) *this = o;
     }
@@ -186,8 +186,9 @@ struct Shared {
     float wtop[kWarps];
     u64 part[kWarps];
     u64 whole;
-    uint32_t nlist;
+    uint32_t nlist, found;
     int first;
+    u64 sum;                     // this CTA's weight of all tokens
     float least;
     Border border;
     u64 scan[kWarps];
@@ -211,34 +212,45 @@ __device__ __forceinline__ void each(const Run& r, int lane, F f) {
     }
 }
 
-// The border of the shortest prefix of the order, within `in`, that has `target` tokens (MASS false) or at
-// least the share `share` of the weight within `in` (MASS true). Returns `in` where there are fewer tokens.
-template <bool MASS>
+// What a search looks for: the border of the first `target` tokens of the order; that of the shortest
+// prefix, within `in`, with at least the share `share` of the weight within `in`; or the first `target`
+// tokens themselves (at most kList), which then lie in `ranked`, sh.found of them with a few more.
+enum { kCount = 0, kMass = 1, kFirst = 2 };
+
+// Returns `in` where there are fewer tokens.
+template <int KIND>
 __device__ Border find_border(const Run& run, const RowScale& row, int vocab, const Border in, u64 target, float share,
                               uint32_t* hist, Shared& sh, uint32_t ranks, int& turn) {
+    constexpr bool MASS = KIND == kMass;
     const int tid = threadIdx.x, lane = tid & 31;
     Entry *list = reinterpret_cast<Entry*>(hist), *ranked = list + kList;   // once a histogram has been read
     uint32_t qa = 0, qb = kQMax, ka = kKeyMin, kb = key_of(row.top), ia = 0, ib = (uint32_t)vocab - 1;
     u64 base = 0;
-    auto member = [&](float l, int i, uint32_t& q, uint32_t& k) {
-        q = distance(l, row);
-        k = key_of(l);
-        return q >= qa && q <= qb && k >= ka && k <= kb && (uint32_t)i >= ia && (uint32_t)i <= ib && in.keeps(k, i);
+    const bool all = in.all();
+    // the digit's value of a token, above `b - a` where it is not one of those left. Tokens of -inf are
+    // left in until the keys are divided: they weigh nothing, and come last in a count.
+    auto digit = [&](int level, float l, int i) -> uint32_t {
+        const uint32_t q = distance(l, row);
+        if (level == 0) return all || in.keeps(key_of(l), i) ? q - qa : ~0u;
+        const uint32_t k = key_of(l);
+        const bool ok = q == qa && k <= kb && k >= ka && (all || in.keeps(k, i));
+        if (level == 1) return ok ? kb - k : ~0u;
+        return ok ? (uint32_t)i - ia : ~0u;
     };
     for (int round = 0;; ++round) {
         // the digit that this round divides: the highest 7 bits of the first interval still open
         const int level = qa < qb ? 0 : ka < kb ? 1 : 2;
         const uint32_t a = level == 0 ? qa : level == 1 ? ka : ia, b = level == 0 ? qb : level == 1 ? kb : ib;
-        const int bits = 32 - __clz((int)(b - a));
+        const uint32_t span = b - a;
+        const int bits = 32 - __clz((int)span);
         const int shift = bits > kDigit ? bits - kDigit : 0;
         for (int i = tid; i < kBins * 32 * (MASS ? 2 : 1) / 4; i += kThreads)
             reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
         if (tid == 0) sh.nlist = 0;
         __syncthreads();
         each(run, lane, [&](float l, int i) {
-            uint32_t q, k;
-            if (!member(l, i, q, k)) return;
-            const uint32_t v = level == 0 ? q - a : level == 1 ? b - k : (uint32_t)i - a;
+            const uint32_t v = digit(level, l, i);
+            if (v > span) return;
             uint32_t* h = hist + (v >> shift) * 32 + lane;
             if (MASS) {
                 const u64 w = weight(l, row, sh.table);
@@ -287,9 +299,9 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
                 target = __umul64hi(s64, sum) + (s64 * sum != 0 ? 1 : 0);
                 target = target == 0 ? 1 : target;
             }
-            if (sum < target) return in;
         }
         const unsigned reach = __ballot_sync(0xffffffffu, base + upto >= target);
+        if (!reach && KIND != kFirst) return in;   // fewer tokens
         const int l = reach ? __ffs(reach) - 1 : 31;
         u64 c = base + upto - mine;
         int bin = lane * (kBins / 32);
@@ -315,21 +327,25 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
             ia += lo;
         }
         if (!MASS) {
-            const u64 left = sh.all[bin];
-            if (left > kList) {
-                __syncthreads();   // sh.all is read before the next round writes it
-                continue;
-            }
+            if ((KIND == kFirst ? base : 0) + sh.all[bin] > kList) continue;
         } else if (round == 0 && vocab > 16 * kList) {   // rarely few enough after one digit
-            __syncthreads();
             continue;
         }
         // the candidates: this CTA's, then everybody's
+        const int at = qa < qb ? 0 : ka < kb ? 1 : 2;
+        const uint32_t rest = at == 0 ? qb - qa : at == 1 ? kb - ka : ib - ia;
+        __syncthreads();   // the histogram has been read
         each(run, lane, [&](float l2, int i) {
-            uint32_t q, k;
-            if (!member(l2, i, q, k)) return;
+            if (KIND == kFirst) {   // all up to the interval's last
+                const uint32_t k = key_of(l2);
+                if (at == 0 ? distance(l2, row) > qb : at == 1 ? k < ka : !(Border{ka, (int)ib}.keeps(k, i))) return;
+            } else if (digit(at, l2, i) > rest) {
+                return;
+            }
+            const u64 w = KIND == kCount ? 1 : weight(l2, row, sh.table);
+            if (KIND != kCount && w == 0) return;
             const uint32_t n = atomicAdd(&sh.nlist, 1u);
-            if (n < kList) list[n] = Entry{MASS ? weight(l2, row, sh.table) : 1ull, k, i};
+            if (n < kList) list[n] = Entry{w, key_of(l2), i};
         });
         cluster_sync();
         uint32_t total = 0;
@@ -346,6 +362,11 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
         }
         if (tid == 0) sh.border = in;
         cluster_sync();   // the lists may be written again
+        if (KIND == kFirst) {
+            if (tid == 0) sh.found = total;
+            __syncthreads();
+            return in;
+        }
         if (total > kList) continue;
         if ((uint32_t)tid < total) {
             const Entry e = ranked[tid];
@@ -360,6 +381,55 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
         const Border found = sh.border;
         __syncthreads();
         return found;
+    }
+}
+
+// The draw among the n <= kList entries of the first top_k tokens and a few after them, by one CTA.
+__device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t least, float u, int32_t* token, float* prob,
+                           Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    static_assert(kList == 4 * 32, "four warps hold the entries");
+    const Entry me = tid < n ? e[tid] : Entry{0, 0, 0x7FFFFFFF};
+    u64 before = 0;
+    int place = 0;
+    if (tid < kList) {
+        for (int j = 0; j < n; ++j) {
+            const Entry o = e[j];
+            if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) {
+                before += o.w;
+                ++place;
+            }
+        }
+    }
+    const bool in = tid < n && place < topk;
+    auto total_of = [&](u64 w) {
+        w = warp_sum(w);
+        if (lane == 0) sh.part[warp] = w;
+        __syncthreads();
+        const u64 t = sh.part[0] + sh.part[1] + sh.part[2] + sh.part[3];
+        __syncthreads();
+        return t;
+    };
+    bool keep = in && me.key >= least;
+    if (topp < 1.f) {
+        const u64 whole = total_of(in ? me.w : 0);
+        const u64 s64 = topp > 0.f ? __float2ull_rz(topp * 0x1p64f) : 0;
+        u64 target = __umul64hi(s64, whole) + (s64 * whole != 0 ? 1 : 0);
+        target = target == 0 ? 1 : target;
+        keep = keep && before < target;
+    }
+    const u64 total = total_of(keep ? me.w : 0);
+    const u64 target = __umul64hi(__float2ull_rz(u * 0x1p64f), total) + 1;
+    if (tid < kList) sh.all[tid] = keep ? me.w : 0;
+    __syncthreads();
+    if (keep) {
+        u64 c = 0;
+        for (int j = 0; j < n; ++j)
+            if (e[j].idx <= me.idx) c += sh.all[j];
+        if (c >= target && c - me.w < target) {
+            *token = me.idx;
+            if (prob) *prob = (float)((double)me.w / (double)total);
+        }
     }
 }
 
@@ -505,29 +575,70 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
         if (tid == 0)   // the least f32 at or above top + T ln(min_p)
             sh.least = minp >= 1.f ? top : __double2float_ru((double)top + (double)temp * log((double)minp));
         __syncthreads();
-        border.tighten(Border{max(kKeyMin, key_of(sh.least + 0.0f)), 0x7FFFFFFF});
+        border.key = max(kKeyMin, key_of(sh.least + 0.0f));
     }
-    Border prefix = {kKeyMin, 0x7FFFFFFF};
+    const Border every = {kKeyMin, 0x7FFFFFFF};
+    if (topk > 0 && topk <= kList && topk < p.vocab) {
+        find_border<kFirst>(run, row, p.vocab, every, (u64)topk, 0.f, hist, sh, ranks, turn);
+        if (rank == 0)
+            draw_small(reinterpret_cast<const Entry*>(hist) + kList, (int)sh.found, topk, topp, border.key, u, p.tokens + b,
+                       p.probs ? p.probs + b : nullptr, sh);
+        return;   // no CTA reads another's shared memory any more
+    }
+    // this warp's tokens' kept weight, the CTA's to sh.whole; with `all_too` the CTA's weight of all to sh.sum
+    auto kept_sums = [&](bool all_too) {
+        u64 w = 0, s = 0;
+        const float least = __uint_as_float(border.key & 0x80000000u ? border.key ^ 0x80000000u : ~border.key);
+        if (all_too) {
+            each(run, lane, [&](float l, int) {
+                const u64 x = weight(l, row, sh.table);
+                s += x;
+                w += l >= least ? x : 0;
+            });
+        } else if (border.idx == 0x7FFFFFFF) {
+            each(run, lane, [&](float l, int) { w += l >= least ? weight(l, row, sh.table) : 0; });
+        } else {
+            each(run, lane, [&](float l, int i) { w += border.keeps(key_of(l), i) ? weight(l, row, sh.table) : 0; });
+        }
+        w = warp_sum(w);
+        s = warp_sum(s);
+        if (lane == 0) {
+            sh.part[warp] = w;
+            sh.scan[warp] = s;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            u64 t = 0, a = 0;
+            for (int i = 0; i < kWarps; ++i) {
+                t += sh.part[i];
+                a += sh.scan[i];
+            }
+            sh.whole = t;
+            sh.sum = a;
+        }
+        cluster_sync();
+    };
+    Border prefix = every;
     if (topk > 0 && topk < p.vocab) {
-        prefix = find_border<false>(run, row, p.vocab, prefix, (u64)topk, 0.f, hist, sh, ranks, turn);
+        prefix = find_border<kCount>(run, row, p.vocab, prefix, (u64)topk, 0.f, hist, sh, ranks, turn);
         border.tighten(prefix);
     }
-    if (topp < 1.f) border.tighten(find_border<true>(run, row, p.vocab, prefix, 0, topp, hist, sh, ranks, turn));
-
-    // ---- the draw: the kept weight of every warp's tokens, then of every CTA's
-    u64 w = 0;
-    each(run, lane, [&](float l, int i) {
-        if (border.keeps(key_of(l), i)) w += weight(l, row, sh.table);
-    });
-    w = warp_sum(w);
-    if (lane == 0) sh.part[warp] = w;
-    __syncthreads();
-    if (tid == 0) {
-        u64 t = 0;
-        for (int i = 0; i < kWarps; ++i) t += sh.part[i];
-        sh.whole = t;
+    bool ready = false;   // the kept sums are there
+    if (topp < 1.f && minp > 0.f && prefix.all()) {
+        // where min-p keeps less weight than top-p asks for, it is the border
+        kept_sums(true);
+        u64 kept = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
+        u64 all = lane < (int)ranks ? remote_u64(&sh.sum, (uint32_t)lane) : 0;
+        kept = warp_sum(kept);
+        all = warp_sum(all);
+        const u64 s64 = topp > 0.f ? __float2ull_rz(topp * 0x1p64f) : 0;
+        ready = kept < __umul64hi(s64, all) + (s64 * all != 0 ? 1 : 0);
     }
-    cluster_sync();
+    if (!ready) {
+        if (topp < 1.f) border.tighten(find_border<kMass>(run, row, p.vocab, prefix, 0, topp, hist, sh, ranks, turn));
+        kept_sums(false);
+    }
+    // ---- the draw: the CTA, then the warp, then the thread in whose tokens the running sum reaches the target
     u64 total = 0, before = 0;
     {
         const u64 t = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
