@@ -489,8 +489,9 @@ __device__ __forceinline__ float load_run(const T* src, int n, int off, float* d
     return mx;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* err) {
+// FILTER: top-k or top-p may be asked for; without, fewer registers let three CTAs share an SM.
+template <typename T, bool FILTER>
+__global__ void __launch_bounds__(kThreads, FILTER ? 2 : 3) sample_kernel(Params p, DevError* err) {
     extern __shared__ __align__(16) float dyn[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -501,9 +502,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
     // every decision below is the same in all CTAs of the cluster
     if (p.active && p.active[b] == 0) return;
     const float temp = p.temperature ? p.temperature[b] : 1.0f;
-    const float topp = p.top_p ? p.top_p[b] : 1.0f;
+    const float topp = FILTER && p.top_p ? p.top_p[b] : 1.0f;
     const float minp = p.min_p ? p.min_p[b] : 0.0f;
-    const int topk = p.top_k ? p.top_k[b] : 0;
+    const int topk = FILTER && p.top_k ? p.top_k[b] : 0;
     // a decode loop's numbers, one per position (a negative position has been recorded by the step)
     const long long at = p.uniform_stride <= 1 ? b : b * p.uniform_stride + max(p.positions[b], 0) % p.uniform_stride;
     const float u = p.uniform[at];
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
         border.key = max(kKeyMin, key_of(sh.least + 0.0f));
     }
     const Border every = {kKeyMin, 0x7FFFFFFF};
-    if (topk > 0 && topk <= kList && topk < p.vocab) {
+    if (FILTER && topk > 0 && topk <= kList && topk < p.vocab) {
         find_border<kFirst>(run, row, p.vocab, every, (u64)topk, 0.f, hist, sh, ranks, turn);
         if (rank == 0)
             draw_small(reinterpret_cast<const Entry*>(hist) + kList, (int)sh.found, topk, topp, border.key, u, p.tokens + b,
@@ -593,12 +594,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
             each(run, lane, [&](float l, int) {
                 const u64 x = weight(l, row, sh.table);
                 s += x;
-                w += l >= least ? x : 0;
+                w += x & -(u64)(l >= least);
             });
+        } else if (border.all()) {
+            each(run, lane, [&](float l, int) { w += weight(l, row, sh.table); });   // -inf weighs nothing
         } else if (border.idx == 0x7FFFFFFF) {
-            each(run, lane, [&](float l, int) { w += l >= least ? weight(l, row, sh.table) : 0; });
+            each(run, lane, [&](float l, int) { w += weight(l, row, sh.table) & -(u64)(l >= least); });
         } else {
-            each(run, lane, [&](float l, int i) { w += border.keeps(key_of(l), i) ? weight(l, row, sh.table) : 0; });
+            each(run, lane, [&](float l, int i) { w += weight(l, row, sh.table) & -(u64)border.keeps(key_of(l), i); });
         }
         w = warp_sum(w);
         s = warp_sum(s);
@@ -619,12 +622,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
         cluster_sync();
     };
     Border prefix = every;
-    if (topk > 0 && topk < p.vocab) {
+    if (FILTER && topk > 0 && topk < p.vocab) {
         prefix = find_border<kCount>(run, row, p.vocab, prefix, (u64)topk, 0.f, hist, sh, ranks, turn);
         border.tighten(prefix);
     }
     bool ready = false;   // the kept sums are there
-    if (topp < 1.f && minp > 0.f && prefix.all()) {
+    if (FILTER && topp < 1.f && minp > 0.f && prefix.all()) {
         // where min-p keeps less weight than top-p asks for, it is the border
         kept_sums(true);
         u64 kept = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(Params p, DevError* er
         ready = kept < __umul64hi(s64, all) + (s64 * all != 0 ? 1 : 0);
     }
     if (!ready) {
-        if (topp < 1.f) border.tighten(find_border<kMass>(run, row, p.vocab, prefix, 0, topp, hist, sh, ranks, turn));
+        if (FILTER && topp < 1.f) border.tighten(find_border<kMass>(run, row, p.vocab, prefix, 0, topp, hist, sh, ranks, turn));
         kept_sums(false);
     }
     // ---- the draw: the CTA, then the warp, then the thread in whose tokens the running sum reaches the target
@@ -730,7 +733,9 @@ int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, p, err) : e;
     };
-    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? go(sample_kernel<float>) : go(sample_kernel<__half>);
+    const bool filter = a.top_k || a.top_p;
+    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? (filter ? go(sample_kernel<float, true>) : go(sample_kernel<float, false>))
+                                                  : (filter ? go(sample_kernel<__half, true>) : go(sample_kernel<__half, false>));
     return e == cudaSuccess ? QL_OK : cuda_error(e, "sampling launch");
 }
 
