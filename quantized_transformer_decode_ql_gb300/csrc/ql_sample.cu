@@ -191,7 +191,7 @@ struct Shared {
     u64 sum;                     // this CTA's weight of all tokens
     float least;
     Border border;
-    u64 scan[kWarps];
+    u64 scan[kWarps], wsum[kWarps];
 };
 
 // A CTA's run of a row: token i at data[sh + i - base]; the places before and after hold -inf.
@@ -210,6 +210,59 @@ __device__ __forceinline__ void each(const Run& r, int lane, F f) {
         f(x.z, i + 2);
         f(x.w, i + 3);
     }
+}
+
+// The same run read from memory: token i at src[i - first], this warp's at from .. to - 1 of src, of which
+// those from v0 on lie in nv aligned vectors.
+template <typename T>
+struct Stream {
+    static constexpr int W = 16 / (int)sizeof(T);
+    const T* src;
+    int from, to, v0, nv;
+    __device__ __forceinline__ Stream(const T* s, int n, int warp) : src(s) {
+        const int off = (int)((reinterpret_cast<uintptr_t>(s) % 16) / sizeof(T));
+        const int head = min(n, (W - off) % W), body = (n - head) / W;
+        const int per = (body + kWarps - 1) / kWarps, a = min(body, warp * per);
+        nv = min(body, a + per) - a;
+        v0 = head + a * W;
+        from = warp == 0 ? 0 : v0;
+        to = warp == kWarps - 1 ? n : v0 + nv * W;
+        if (nv == 0 && warp != kWarps - 1) to = warp == 0 ? head : from;
+    }
+};
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+// the canonical logits of a 16-byte load
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 x, float (&l)[16 / sizeof(T)]) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+            l[j] = canonical(__uint_as_float(u[j]));
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            l[2 * j] = canonical(f.x);
+            l[2 * j + 1] = canonical(f.y);
+        }
+    }
+}
+template <typename T, typename F>
+__device__ __forceinline__ void each(const Stream<T>& s, int lane, F f) {
+    const uint4* v = reinterpret_cast<const uint4*>(s.src + s.v0);
+#pragma unroll 4
+    for (int i = lane; i < s.nv; i += 32) {
+        float l[Stream<T>::W];
+        unpack<T>(__ldg(v + i), l);
+#pragma unroll
+        for (int j = 0; j < Stream<T>::W; ++j) f(l[j]);
+    }
+    for (int i = s.from + lane; i < s.v0; i += 32) f(canonical(to_float(__ldg(s.src + i))));
+    for (int i = s.v0 + s.nv * Stream<T>::W + lane; i < s.to; i += 32) f(canonical(to_float(__ldg(s.src + i))));
 }
 
 // What a search looks for: the border of the first `target` tokens of the order; that of the shortest
@@ -248,7 +301,9 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
             reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
         if (tid == 0) sh.nlist = 0;
         __syncthreads();
-        each(run, lane, [&](float l, int i) {
+        if (KIND != kMass && round == 0 && all) {   // every token counts
+            each(run, lane, [&](float l, int) { atomicAdd(hist + (distance(l, row) >> shift) * 32 + lane, 1u); });
+        } else each(run, lane, [&](float l, int i) {
             const uint32_t v = digit(level, l, i);
             if (v > span) return;
             uint32_t* h = hist + (v >> shift) * 32 + lane;
@@ -279,7 +334,8 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
         cluster_sync();
         if (tid < kBins) {
             u64 v = 0;
-            for (uint32_t r = 0; r < ranks; ++r) v += remote_u64(&sh.mine[turn][tid], r);
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r) v += r < ranks ? remote_u64(&sh.mine[turn][tid], r) : 0;
             sh.all[tid] = v;
         }
         turn ^= 1;
@@ -348,17 +404,25 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
             if (n < kList) list[n] = Entry{w, key_of(l2), i};
         });
         cluster_sync();
-        uint32_t total = 0;
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const uint32_t n = remote_u32(&sh.nlist, r);
-            if ((uint32_t)tid >= total && (uint32_t)tid < total + n && total + n <= kList) {
-                const Entry* e = &list[tid - total];
-                ranked[tid].w = remote_u64(&e->w, r);
-                const u64 ki = remote_u64(&e->key, r);
-                ranked[tid].key = (uint32_t)ki;
-                ranked[tid].idx = (int)(ki >> 32);
+        // thread t takes the t-th of all candidates: the CTA in whose list it is, and its place there
+        const uint32_t len = lane < (int)ranks ? remote_u32(&sh.nlist, (uint32_t)lane) : 0;
+        const uint32_t ends = (uint32_t)warp_scan(len, lane);
+        const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
+        if (total <= kList) {
+            uint32_t r = 0, start = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < kMaxCluster; ++k) {
+                const uint32_t end = __shfl_sync(0xffffffffu, ends, k);
+                if ((uint32_t)tid >= end) {
+                    r = k + 1;
+                    start = end;
+                }
             }
-            total += n;
+            if ((uint32_t)tid < total) {
+                const Entry* e = &list[tid - start];
+                const u64 w = remote_u64(&e->w, r), ki = remote_u64(&e->key, r);
+                ranked[tid] = Entry{w, (uint32_t)ki, (int)(ki >> 32)};
+            }
         }
         if (tid == 0) sh.border = in;
         cluster_sync();   // the lists may be written again
@@ -433,13 +497,6 @@ __device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-
 // The CTA's run of the row into shared memory, sh places further on so that 16-byte loads are aligned at
 // both ends; returns this thread's largest logit.
 template <typename T>
@@ -457,27 +514,10 @@ __device__ __forceinline__ float load_run(const T* src, int n, int off, float* d
     float4* to = reinterpret_cast<float4*>(data + off + head);
 #pragma unroll 4
     for (int i = threadIdx.x; i < body; i += kThreads) {
-        const uint4 x = __ldg(v + i);
         float l[W];
-        if constexpr (W == 4) {
-            l[0] = __uint_as_float(x.x);
-            l[1] = __uint_as_float(x.y);
-            l[2] = __uint_as_float(x.z);
-            l[3] = __uint_as_float(x.w);
-        } else {
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        unpack<T>(__ldg(v + i), l);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-                l[2 * j] = f.x;
-                l[2 * j + 1] = f.y;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            l[j] = canonical(l[j]);
-            mx = fmaxf(mx, l[j]);
-        }
+        for (int j = 0; j < W; ++j) mx = fmaxf(mx, l[j]);
 #pragma unroll
         for (int j = 0; j < W / 4; ++j) to[i * (W / 4) + j] = make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
     }
@@ -489,9 +529,197 @@ __device__ __forceinline__ float load_run(const T* src, int n, int off, float* d
     return mx;
 }
 
-// FILTER: top-k or top-p may be asked for; without, fewer registers let three CTAs share an SM.
-template <typename T, bool FILTER>
-__global__ void __launch_bounds__(kThreads, FILTER ? 2 : 3) sample_kernel(Params p, DevError* err) {
+// A row's arguments. Every decision that follows from them is the same in all CTAs of the cluster.
+struct RowArgs {
+    float temp, topp, minp, u;
+    int topk;
+};
+// False where nothing is to be drawn: an inactive row, or one whose arguments are out of range (recorded).
+__device__ __forceinline__ bool row_args(const Params& p, long long b, uint32_t rank, RowArgs& a, DevError* err) {
+    if (p.active && p.active[b] == 0) return false;
+    a.temp = p.temperature ? p.temperature[b] : 1.0f;
+    a.topp = p.top_p ? p.top_p[b] : 1.0f;
+    a.minp = p.min_p ? p.min_p[b] : 0.0f;
+    a.topk = p.top_k ? p.top_k[b] : 0;
+    // a decode loop's numbers, one per position (a negative position has been recorded by the step)
+    const long long at = p.uniform_stride <= 1 ? b : b * p.uniform_stride + max(p.positions[b], 0) % p.uniform_stride;
+    a.u = p.uniform[at];
+    if (a.temp >= 0.f && a.temp < INFINITY && a.topp == a.topp && a.minp == a.minp && a.u >= 0.f && a.u < 1.f) return true;
+    if (threadIdx.x == 0 && rank == 0) {
+        record_device_error(err, kErrSampleArg, b, 0);
+        p.tokens[b] = -1;
+        if (p.probs) p.probs[b] = 0.f;
+    }
+    return false;
+}
+
+// The row's largest logit from every thread's. False where the row has no token, which is written.
+__device__ __forceinline__ bool row_top(const Params& p, long long b, uint32_t rank, uint32_t ranks, float& top, Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.wtop[warp] = top;
+    __syncthreads();
+    if (warp == 0) {
+        top = sh.wtop[lane & (kWarps - 1)];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) sh.top = top;
+    }
+    cluster_sync();
+    top = lane < (int)ranks ? __uint_as_float(remote_u32(&sh.top, (uint32_t)lane)) : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top != -INFINITY) return true;
+    cluster_sync();   // nobody leaves while its shared memory may be read
+    if (tid == 0 && rank == 0) {
+        p.tokens[b] = -1;
+        if (p.probs) p.probs[b] = 0.f;
+    }
+    return false;
+}
+
+// The arg max: the lowest of the threads' indices of the largest logit.
+__device__ __forceinline__ void row_first(const Params& p, long long b, uint32_t rank, uint32_t ranks, int idx, Shared& sh) {
+    const int tid = threadIdx.x;
+    idx = __reduce_min_sync(0xffffffffu, idx);
+    if (tid == 0) sh.first = 0x7FFFFFFF;
+    __syncthreads();
+    if ((tid & 31) == 0) atomicMin(&sh.first, idx);
+    cluster_sync();
+    if (tid == 0 && rank == 0) {
+        int best = 0x7FFFFFFF;
+        for (uint32_t r = 0; r < ranks; ++r) best = min(best, (int)remote_u32(&sh.first, r));
+        p.tokens[b] = best;
+        if (p.probs) p.probs[b] = 1.f;
+    }
+    cluster_sync();
+}
+
+// The least f32 at or above top + T ln(min_p), by thread 0 (a barrier must follow); its key.
+__device__ __forceinline__ float min_p_least(const RowArgs& a, float top) {
+    return (a.minp >= 1.f ? top : __double2float_ru((double)top + (double)a.temp * log((double)a.minp))) + 0.0f;
+}
+
+// The warps' sums w (and s) to sh.part (and sh.scan), the CTA's to sh.whole (and sh.sum), for all CTAs to read.
+__device__ __forceinline__ void share_sums(u64 w, u64 s, Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    w = warp_sum(w);
+    s = warp_sum(s);
+    if (lane == 0) {
+        sh.part[warp] = w;
+        sh.scan[warp] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        w = warp_sum(lane < kWarps ? sh.part[lane] : 0);
+        s = warp_sum(lane < kWarps ? sh.scan[lane] : 0);
+        if (lane == 0) {
+            sh.whole = w;
+            sh.sum = s;
+        }
+    }
+    cluster_sync();
+}
+
+// The draw from the shared sums: the CTA, then the warp, then the thread in whose tokens the running sum
+// reaches the target. tokens(warp, from, to): a warp's places; kept(place): its kept weight; index(place).
+template <typename R, typename K, typename I>
+__device__ __forceinline__ void draw(const Params& p, long long b, uint32_t rank, uint32_t ranks, float u, Shared& sh, R tokens,
+                                     K kept, I index) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const u64 t = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
+    const u64 upto = warp_scan(t, lane);
+    const u64 total = __shfl_sync(0xffffffffu, upto, 31), before = __shfl_sync(0xffffffffu, upto - t, (int)rank);
+    // the first token at which the running sum exceeds u total: reaches floor(u total) + 1, exactly
+    const u64 target = __umul64hi(__float2ull_rz(u * 0x1p64f), total) + 1;
+    if (target > before && target <= before + sh.whole) {   // in this CTA
+        const u64 mine = lane < kWarps ? sh.part[lane] : 0;
+        const u64 ends = before + warp_scan(mine, lane);
+        const int ow = __ffs(__ballot_sync(0xffffffffu, lane < kWarps && ends >= target)) - 1;
+        u64 c = __shfl_sync(0xffffffffu, ends - mine, ow);
+        // that warp's tokens over all threads, a few consecutive ones each
+        int from, to;
+        tokens(ow, from, to);
+        const int n = (to - from + kThreads - 1) / kThreads;
+        const int a = min(to, from + tid * n), e = min(to, a + n);
+        u64 s = 0;
+        for (int j = a; j < e; ++j) s += kept(j);
+        const u64 incl = warp_scan(s, lane);
+        if (lane == 31) sh.wsum[warp] = incl;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) c += sh.wsum[k];
+        c += incl - s;
+        if (c < target && c + s >= target) {
+            for (int j = a; j < e; ++j) {
+                const u64 x = kept(j);
+                c += x;
+                if (x != 0 && c >= target) {
+                    p.tokens[b] = index(j);
+                    if (p.probs) p.probs[b] = (float)((double)x / (double)total);
+                    break;
+                }
+            }
+        }
+    }
+    cluster_sync();   // nobody leaves while its shared memory may be read
+}
+
+// No top-k or top-p: two passes over the row, the second from L2, so that shared memory does not bound the
+// CTAs of an SM.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, DevError* err) {
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const long long b = blockIdx.x / ranks;
+    pdl_wait();
+    pdl_trigger();
+    RowArgs a;
+    if (!row_args(p, b, rank, a, err)) return;
+    const int first = (int)rank * p.per;
+    const int n = max(0, min(p.vocab - first, p.per));
+    const T* src = static_cast<const T*>(p.logits) + b * p.stride + first;
+    const Stream<T> run(src, n, warp);
+    if (tid < 64) sh.table[tid] = kExp2[tid];
+    float top = -INFINITY;
+    each(run, lane, [&](float l) { top = fmaxf(top, l); });
+    if (!row_top(p, b, rank, ranks, top, sh)) return;
+    auto at = [&](int j) { return canonical(to_float(__ldg(src + j))); };
+    if (a.temp < kMinTemperature) {
+        int idx = 0x7FFFFFFF;
+        for (int j = run.from + lane; j < run.to; j += 32)
+            if (at(j) == top) idx = min(idx, first + j);
+        row_first(p, b, rank, ranks, idx, sh);
+        return;
+    }
+    RowScale row;
+    row.set(top, a.temp);
+    float least = -INFINITY;   // -inf weighs nothing
+    if (a.minp > 0.f) {
+        if (tid == 0) sh.least = min_p_least(a, top);
+        __syncthreads();
+        least = sh.least;
+    }
+    u64 w = 0;
+    if (least == -INFINITY) each(run, lane, [&](float l) { w += weight(l, row, sh.table); });
+    else each(run, lane, [&](float l) { w += weight(l, row, sh.table) & -(u64)(l >= least); });
+    share_sums(w, 0, sh);
+    draw(p, b, rank, ranks, a.u, sh,
+         [&](int ow, int& from, int& to) {
+             const Stream<T> r(src, n, ow);
+             from = r.from;
+             to = r.to;
+         },
+         [&](int j) {
+             const float l = at(j);
+             return weight(l, row, sh.table) & -(u64)(l >= least);
+         },
+         [&](int j) { return first + j; });
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError* err) {
     extern __shared__ __align__(16) float dyn[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -499,24 +727,8 @@ __global__ void __launch_bounds__(kThreads, FILTER ? 2 : 3) sample_kernel(Params
     const long long b = blockIdx.x / ranks;
     pdl_wait();
     pdl_trigger();
-    // every decision below is the same in all CTAs of the cluster
-    if (p.active && p.active[b] == 0) return;
-    const float temp = p.temperature ? p.temperature[b] : 1.0f;
-    const float topp = FILTER && p.top_p ? p.top_p[b] : 1.0f;
-    const float minp = p.min_p ? p.min_p[b] : 0.0f;
-    const int topk = FILTER && p.top_k ? p.top_k[b] : 0;
-    // a decode loop's numbers, one per position (a negative position has been recorded by the step)
-    const long long at = p.uniform_stride <= 1 ? b : b * p.uniform_stride + max(p.positions[b], 0) % p.uniform_stride;
-    const float u = p.uniform[at];
-    const bool ok = temp >= 0.f && temp < INFINITY && topp == topp && minp == minp && u >= 0.f && u < 1.f;
-    if (!ok) {
-        if (tid == 0 && rank == 0) {
-            record_device_error(err, kErrSampleArg, b, 0);
-            p.tokens[b] = -1;
-            if (p.probs) p.probs[b] = 0.f;
-        }
-        return;
-    }
+    RowArgs a;
+    if (!row_args(p, b, rank, a, err)) return;
     const int first = (int)rank * p.per;
     const int n = max(0, min(p.vocab - first, p.per));
     const T* src = static_cast<const T*>(p.logits) + b * p.stride + first;
@@ -525,26 +737,7 @@ __global__ void __launch_bounds__(kThreads, FILTER ? 2 : 3) sample_kernel(Params
     uint32_t* hist = reinterpret_cast<uint32_t*>(dyn + p.per + 8);
     if (tid < 64) sh.table[tid] = kExp2[tid];
     float top = load_run(src, n, off, dyn, nvec);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sh.wtop[warp] = top;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sh.wtop[w]);
-        sh.top = top;
-    }
-    cluster_sync();
-    top = lane < (int)ranks ? __uint_as_float(remote_u32(&sh.top, (uint32_t)lane)) : -INFINITY;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top == -INFINITY) {
-        cluster_sync();   // nobody leaves while its shared memory may be read
-        if (tid == 0 && rank == 0) {
-            p.tokens[b] = -1;
-            if (p.probs) p.probs[b] = 0.f;
-        }
-        return;
-    }
+    if (!row_top(p, b, rank, ranks, top, sh)) return;
     Run run;
     run.data = reinterpret_cast<const float4*>(dyn);
     run.base = first - off;
@@ -552,143 +745,75 @@ __global__ void __launch_bounds__(kThreads, FILTER ? 2 : 3) sample_kernel(Params
     run.v0 = warp * vpw;
     run.v1 = min(nvec, run.v0 + vpw);
     int turn = 0;
-    if (temp < kMinTemperature) {   // the arg max: the lowest index of the largest logit
+    if (a.temp < kMinTemperature) {
         int idx = 0x7FFFFFFF;
         each(run, lane, [&](float l, int i) { idx = l == top && i < idx ? i : idx; });
-        idx = __reduce_min_sync(0xffffffffu, idx);
-        if (tid == 0) sh.first = 0x7FFFFFFF;
-        __syncthreads();
-        if (lane == 0) atomicMin(&sh.first, idx);
-        cluster_sync();
-        if (tid == 0 && rank == 0) {
-            int best = 0x7FFFFFFF;
-            for (uint32_t r = 0; r < ranks; ++r) best = min(best, (int)remote_u32(&sh.first, r));
-            p.tokens[b] = best;
-            if (p.probs) p.probs[b] = 1.f;
-        }
-        cluster_sync();
+        row_first(p, b, rank, ranks, idx, sh);
         return;
     }
     RowScale row;
-    row.set(top, temp);
-    Border border = {kKeyMin, 0x7FFFFFFF};   // all that is above -inf
-    if (minp > 0.f) {
-        if (tid == 0)   // the least f32 at or above top + T ln(min_p)
-            sh.least = minp >= 1.f ? top : __double2float_ru((double)top + (double)temp * log((double)minp));
+    row.set(top, a.temp);
+    const Border every = {kKeyMin, 0x7FFFFFFF};   // all that is above -inf
+    Border border = every, prefix = every;
+    if (a.minp > 0.f) {
+        if (tid == 0) sh.least = min_p_least(a, top);
         __syncthreads();
-        border.key = max(kKeyMin, key_of(sh.least + 0.0f));
+        border.key = max(kKeyMin, key_of(sh.least));
     }
-    const Border every = {kKeyMin, 0x7FFFFFFF};
-    if (FILTER && topk > 0 && topk <= kList && topk < p.vocab) {
-        find_border<kFirst>(run, row, p.vocab, every, (u64)topk, 0.f, hist, sh, ranks, turn);
+    if (a.topk > 0 && a.topk <= kList && a.topk < p.vocab) {
+        find_border<kFirst>(run, row, p.vocab, every, (u64)a.topk, 0.f, hist, sh, ranks, turn);
         if (rank == 0)
-            draw_small(reinterpret_cast<const Entry*>(hist) + kList, (int)sh.found, topk, topp, border.key, u, p.tokens + b,
+            draw_small(reinterpret_cast<const Entry*>(hist) + kList, (int)sh.found, a.topk, a.topp, border.key, a.u, p.tokens + b,
                        p.probs ? p.probs + b : nullptr, sh);
         return;   // no CTA reads another's shared memory any more
     }
-    // this warp's tokens' kept weight, the CTA's to sh.whole; with `all_too` the CTA's weight of all to sh.sum
-    auto kept_sums = [&](bool all_too) {
-        u64 w = 0, s = 0;
-        const float least = __uint_as_float(border.key & 0x80000000u ? border.key ^ 0x80000000u : ~border.key);
-        if (all_too) {
-            each(run, lane, [&](float l, int) {
-                const u64 x = weight(l, row, sh.table);
-                s += x;
-                w += x & -(u64)(l >= least);
-            });
-        } else if (border.all()) {
-            each(run, lane, [&](float l, int) { w += weight(l, row, sh.table); });   // -inf weighs nothing
-        } else if (border.idx == 0x7FFFFFFF) {
-            each(run, lane, [&](float l, int) { w += weight(l, row, sh.table) & -(u64)(l >= least); });
-        } else {
-            each(run, lane, [&](float l, int i) { w += weight(l, row, sh.table) & -(u64)border.keeps(key_of(l), i); });
-        }
-        w = warp_sum(w);
-        s = warp_sum(s);
-        if (lane == 0) {
-            sh.part[warp] = w;
-            sh.scan[warp] = s;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            u64 t = 0, a = 0;
-            for (int i = 0; i < kWarps; ++i) {
-                t += sh.part[i];
-                a += sh.scan[i];
-            }
-            sh.whole = t;
-            sh.sum = a;
-        }
-        cluster_sync();
-    };
-    Border prefix = every;
-    if (FILTER && topk > 0 && topk < p.vocab) {
-        prefix = find_border<kCount>(run, row, p.vocab, prefix, (u64)topk, 0.f, hist, sh, ranks, turn);
+    if (a.topk > 0 && a.topk < p.vocab) {
+        prefix = find_border<kCount>(run, row, p.vocab, prefix, (u64)a.topk, 0.f, hist, sh, ranks, turn);
         border.tighten(prefix);
     }
     bool ready = false;   // the kept sums are there
-    if (FILTER && topp < 1.f && minp > 0.f && prefix.all()) {
+    if (a.topp < 1.f && a.minp > 0.f && prefix.all()) {
         // where min-p keeps less weight than top-p asks for, it is the border
-        kept_sums(true);
-        u64 kept = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
-        u64 all = lane < (int)ranks ? remote_u64(&sh.sum, (uint32_t)lane) : 0;
-        kept = warp_sum(kept);
-        all = warp_sum(all);
-        const u64 s64 = topp > 0.f ? __float2ull_rz(topp * 0x1p64f) : 0;
+        const float least = sh.least;
+        u64 w = 0, s = 0;
+        each(run, lane, [&](float l, int) {
+            const u64 x = weight(l, row, sh.table);
+            s += x;
+            w += x & -(u64)(l >= least);
+        });
+        share_sums(w, s, sh);
+        const u64 kept = warp_sum(lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0);
+        const u64 all = warp_sum(lane < (int)ranks ? remote_u64(&sh.sum, (uint32_t)lane) : 0);
+        const u64 s64 = a.topp > 0.f ? __float2ull_rz(a.topp * 0x1p64f) : 0;
         ready = kept < __umul64hi(s64, all) + (s64 * all != 0 ? 1 : 0);
     }
     if (!ready) {
-        if (FILTER && topp < 1.f) border.tighten(find_border<kMass>(run, row, p.vocab, prefix, 0, topp, hist, sh, ranks, turn));
-        kept_sums(false);
-    }
-    // ---- the draw: the CTA, then the warp, then the thread in whose tokens the running sum reaches the target
-    u64 total = 0, before = 0;
-    {
-        const u64 t = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
-        const u64 upto = warp_scan(t, lane);
-        total = __shfl_sync(0xffffffffu, upto, 31);
-        before = __shfl_sync(0xffffffffu, upto - t, (int)rank);
-    }
-    // the first token at which the running sum exceeds u total: reaches floor(u total) + 1, exactly
-    const u64 target = __umul64hi(__float2ull_rz(u * 0x1p64f), total) + 1;
-    if (target > before && target <= before + sh.whole) {   // in this CTA
-        u64 c = before;
-        int ow = 0;
-        while (ow < kWarps - 1 && c + sh.part[ow] < target) c += sh.part[ow++];
-        // that warp's tokens over all threads, a few consecutive ones each
-        const int t0 = 4 * ow * vpw, t1 = 4 * min(nvec, (ow + 1) * vpw);
-        const int each_n = (t1 - t0 + kThreads - 1) / kThreads;
-        const int a = t0 + tid * each_n, e = min(t1, a + each_n);
-        u64 s = 0;
-        for (int j = a; j < e; ++j) {
-            const float l = dyn[j];
-            if (border.keeps(key_of(l), run.base + j)) s += weight(l, row, sh.table);
+        if (a.topp < 1.f) border.tighten(find_border<kMass>(run, row, p.vocab, prefix, 0, a.topp, hist, sh, ranks, turn));
+        u64 w = 0;
+        if (border.all()) {
+            each(run, lane, [&](float l, int) { w += weight(l, row, sh.table); });   // -inf weighs nothing
+        } else {
+            each(run, lane, [&](float l, int i) { w += weight(l, row, sh.table) & -(u64)border.keeps(key_of(l), i); });
         }
-        const u64 incl = warp_scan(s, lane);
-        if (lane == 31) sh.scan[warp] = incl;
-        __syncthreads();
-        for (int k = 0; k < warp; ++k) c += sh.scan[k];
-        c += incl - s;
-        if (c < target && c + s >= target) {
-            for (int j = a; j < e; ++j) {
-                const float l = dyn[j];
-                const u64 x = border.keeps(key_of(l), run.base + j) ? weight(l, row, sh.table) : 0;
-                c += x;
-                if (x != 0 && c >= target) {
-                    p.tokens[b] = run.base + j;
-                    if (p.probs) p.probs[b] = (float)((double)x / (double)total);
-                    break;
-                }
-            }
-        }
+        share_sums(w, 0, sh);
     }
-    cluster_sync();   // as above
+    draw(p, b, rank, ranks, a.u, sh,
+         [&](int ow, int& from, int& to) {
+             from = 4 * min(nvec, ow * vpw);
+             to = 4 * min(nvec, (ow + 1) * vpw);
+         },
+         [&](int j) {
+             const float l = dyn[j];
+             return weight(l, row, sh.table) & -(u64)border.keeps(key_of(l), run.base + j);
+         },
+         [&](int j) { return run.base + j; });
 }
 
-// CTAs of a row: enough that its run fits beside the histogram twice per SM, more while the batch leaves SMs idle
-int cluster_for(int64_t batch, int64_t vocab) {
+// CTAs of a row. Staged in shared memory (top-k, top-p): enough that two runs fit an SM beside their
+// histograms. Otherwise one, as long as a batch has enough rows. More while the batch leaves SMs idle.
+int cluster_for(int64_t batch, int64_t vocab, bool staged) {
     int c = 1;
-    while (c < kMaxCluster && (vocab > 20000ll * c || (batch * c * 2 <= num_sms() && vocab > 2048ll * c))) c *= 2;
+    while (c < kMaxCluster && ((staged && vocab > 20000ll * c) || (batch * c * 2 <= 3 * num_sms() && vocab > 2048ll * c))) c *= 2;
     return c;
 }
 
@@ -697,7 +822,8 @@ int cluster_for(int64_t batch, int64_t vocab) {
 int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "sampling: no device error record");
-    const int c = cluster_for(a.batch, a.vocab);
+    const bool staged = a.top_k || a.top_p;
+    const int c = cluster_for(a.batch, a.vocab, staged);
     if (a.batch * c >= (1ll << 31)) return set_error(QL_EINVAL, "sampling: batch out of range");
     Params p = {};
     p.logits = a.logits;
@@ -714,8 +840,7 @@ int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     p.active = a.active;
     p.tokens = a.tokens;
     p.probs = a.probs;
-    const size_t smem = (size_t)(p.per + 8) * 4 +
-                        (a.top_p ? (size_t)kBins * 32 * 8 : a.top_k ? (size_t)kBins * 32 * 4 : 0);
+    const size_t smem = staged ? (size_t)(p.per + 8) * 4 + (size_t)kBins * 32 * (a.top_p ? 8 : 4) : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.batch * c));
     cfg.blockDim = dim3(kThreads);
@@ -730,12 +855,12 @@ int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
     auto go = [&](auto kernel) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e =
+            staged ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
         return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, p, err) : e;
     };
-    const bool filter = a.top_k || a.top_p;
-    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? (filter ? go(sample_kernel<float, true>) : go(sample_kernel<float, false>))
-                                                  : (filter ? go(sample_kernel<__half, true>) : go(sample_kernel<__half, false>));
+    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? (staged ? go(sample_kernel<float>) : go(sample_plain_kernel<float>))
+                                                  : (staged ? go(sample_kernel<__half>) : go(sample_plain_kernel<__half>));
     return e == cudaSuccess ? QL_OK : cuda_error(e, "sampling launch");
 }
 
