@@ -115,7 +115,7 @@ struct RowScale {
         ref = fabsf(t * c_hi) > 0x1p20f ? t : 0.f;
         const float x = t - ref;
         magic = 12582912.0f - floorf(__fmul_rd(x, c_hi));
-        low = fmaxf(x - __fdiv_rn(2624.f, c_hi), -FLT_MAX);            // 2^-41 of the largest: weight 0
+        low = fmaxf(x - __fdiv_rn(2600.f, c_hi), -FLT_MAX);            // 2^-40.6 of the largest: weight 0
         dist = fminf(__fdiv_rn(16777216.f / 24.f, temp), FLT_MAX);     // finite: 0 dist is 0
     }
 };
@@ -124,12 +124,15 @@ struct RowScale {
 // logit. The floor and the fraction come from fused multiply-adds of l itself, each rounded once, so
 // that the error of a large l does not enter; 2^(fraction / 64) - 1 is the series of exp to the fourth
 // power (the next term is below 2^-40), the product with the table is an integer one.
+// The clamp keeps e / 64 above -42 and takes a NaN to weight 0.
+// REF false: r.ref is 0.
+template <bool REF = true>
 __device__ __forceinline__ u64 weight(float l, const RowScale& r, const uint32_t* table) {
-    const float x = fmaxf(l - r.ref, r.low);
+    const float x = fmaxf(REF ? l - r.ref : l, r.low);
     const float z = __fmaf_rd(x, r.c_hi, r.magic);
     float f = __fmaf_rn(x, r.c_hi, r.magic - z);
     f = __fmaf_rn(x, r.c_lo, f);
-    const uint32_t bits = __float_as_uint(z);    // 0x4B400000 + e, e >= -41 * 64 - 1
+    const uint32_t bits = __float_as_uint(z);    // 0x4B400000 + e
     constexpr float y = 0.010830424696249145f;   // ln 2 / 64
     constexpr float s = 4294967296.0f;
     float q = fmaf(f, s * y * y * y * y / 24.f, s * y * y * y / 6.f);
@@ -137,9 +140,8 @@ __device__ __forceinline__ u64 weight(float l, const RowScale& r, const uint32_t
     q = fmaf(f, q, s * y);
     const int t = (int)table[bits & 63];
     const uint32_t m = (uint32_t)(t + __mulhi(t, __float2int_rn(f * q)));   // 30 bits after the point
-    // m 2^(40 - 30 + e / 64) = (m 2^32) >> (22 - e / 64); the shift is below 64 but for e = -41 * 64 - 1, all of whose bits go
-    const uint32_t sh = min(22u + 0x4B400000u / 64 - (bits >> 6), 63u);
-    return ((u64)m << 32) >> sh;
+    // m 2^(40 - 30 + e / 64) = (m 2^32) >> (22 - e / 64), the shift at most 63
+    return ((u64)m << 32) >> (22u + 0x4B400000u / 64 - (bits >> 6));
 }
 
 __device__ __forceinline__ uint32_t distance(float l, const RowScale& r) {
@@ -236,33 +238,37 @@ template <>
 __device__ __forceinline__ float to_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-// the canonical logits of a 16-byte load
-template <typename T>
+// the logits of a 16-byte load, canonical or as they are
+template <typename T, bool RAW = false>
 __device__ __forceinline__ void unpack(const uint4 x, float (&l)[16 / sizeof(T)]) {
     const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if constexpr (sizeof(T) == 4) {
-            l[j] = canonical(__uint_as_float(u[j]));
+            l[j] = RAW ? __uint_as_float(u[j]) : canonical(__uint_as_float(u[j]));
         } else {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-            l[2 * j] = canonical(f.x);
-            l[2 * j + 1] = canonical(f.y);
+            l[2 * j] = RAW ? f.x : canonical(f.x);
+            l[2 * j + 1] = RAW ? f.y : canonical(f.y);
         }
     }
 }
-template <typename T, typename F>
+template <bool RAW, typename T, typename F>
 __device__ __forceinline__ void each(const Stream<T>& s, int lane, F f) {
     const uint4* v = reinterpret_cast<const uint4*>(s.src + s.v0);
 #pragma unroll 4
     for (int i = lane; i < s.nv; i += 32) {
         float l[Stream<T>::W];
-        unpack<T>(__ldg(v + i), l);
+        unpack<T, RAW>(__ldg(v + i), l);
 #pragma unroll
         for (int j = 0; j < Stream<T>::W; ++j) f(l[j]);
     }
-    for (int i = s.from + lane; i < s.v0; i += 32) f(canonical(to_float(__ldg(s.src + i))));
-    for (int i = s.v0 + s.nv * Stream<T>::W + lane; i < s.to; i += 32) f(canonical(to_float(__ldg(s.src + i))));
+    auto one = [&](int i) {
+        const float l = to_float(__ldg(s.src + i));
+        f(RAW ? l : canonical(l));
+    };
+    for (int i = s.from + lane; i < s.v0; i += 32) one(i);
+    for (int i = s.v0 + s.nv * Stream<T>::W + lane; i < s.to; i += 32) one(i);
 }
 
 // What a search looks for: the border of the first `target` tokens of the order; that of the shortest
@@ -683,8 +689,10 @@ __global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, Dev
     const Stream<T> run(src, n, warp);
     if (tid < 64) sh.table[tid] = kExp2[tid];
     float top = -INFINITY;
-    each(run, lane, [&](float l) { top = fmaxf(top, l); });
+    each<true>(run, lane, [&](float l) { top = fmaxf(top, l); });   // passes over NaN
     if (!row_top(p, b, rank, ranks, top, sh)) return;
+    const bool infinite = top == INFINITY;
+    top = canonical(top);
     auto at = [&](int j) { return canonical(to_float(__ldg(src + j))); };
     if (a.temp < kMinTemperature) {
         int idx = 0x7FFFFFFF;
@@ -702,8 +710,13 @@ __global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, Dev
         least = sh.least;
     }
     u64 w = 0;
-    if (least == -INFINITY) each(run, lane, [&](float l) { w += weight(l, row, sh.table); });
-    else each(run, lane, [&](float l) { w += weight(l, row, sh.table) & -(u64)(l >= least); });
+    if (row.ref != 0.f || infinite) {
+        each<false>(run, lane, [&](float l) { w += weight(l, row, sh.table) & -(u64)(l >= least); });
+    } else if (least == -INFINITY) {
+        each<true>(run, lane, [&](float l) { w += weight<false>(l, row, sh.table); });
+    } else {
+        each<true>(run, lane, [&](float l) { w += weight<false>(l, row, sh.table) & -(u64)(l >= least); });
+    }
     share_sums(w, 0, sh);
     draw(p, b, rank, ranks, a.u, sh,
          [&](int ow, int& from, int& to) {
