@@ -219,25 +219,32 @@ def ql_paged_attn_decode_kvq(q, pool, block_tables, context_lens, batch, n_heads
                                          stream_ptr(stream)))
 
 
-def _dtype_of(name, *tensors):
+def _dtype_of(name, a, b=None):
     """QL_DTYPE_* of tensors that have to share one type."""
-    import torch
-    types = {t.dtype for t in tensors}
-    if types == {torch.float32}:
-        return QL_DTYPE_F32
-    if types == {torch.float16}:
-        return QL_DTYPE_F16
-    raise QLError(QL_EINVAL, f"{name}: tensors must be all float32 or all float16, got {sorted(map(str, types))}")
+    t = a.dtype
+    if b is None or b.dtype == t:
+        code = _DTYPES.get(str(t))
+        if code is not None:
+            return code
+    raise QLError(QL_EINVAL, f"{name}: tensors must be all float32 or all float16")
 
 
-def _rows_of(name, t, n, n_kv_heads, head_dim):
+_DTYPES = {"torch.float32": QL_DTYPE_F32, "torch.float16": QL_DTYPE_F16}
+
+
+def _row_stride(name, t, n, n_kv_heads, head_dim):
     """Row stride in elements of a [n, n_kv_heads, head_dim] (or [n, n_kv_heads * head_dim]) tensor whose rows are
     contiguous."""
-    if t.numel() != n * n_kv_heads * head_dim or t.shape[0] != n:
-        raise QLError(QL_EINVAL, f"{name}: need {n} rows of {n_kv_heads} x {head_dim}, got {tuple(t.shape)}")
-    if n and not t[0].is_contiguous():
-        raise QLError(QL_EINVAL, f"{name}: the heads of a row must be contiguous")
-    return t.stride(0)
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = (shape[0] == n and shape[1] == n_kv_heads and shape[2] == head_dim and
+              strides[2] == 1 and (strides[1] == head_dim or n_kv_heads == 1))
+    else:
+        ok = len(shape) == 2 and shape[0] == n and shape[1] == n_kv_heads * head_dim and strides[1] == 1
+    if not ok:
+        raise QLError(QL_EINVAL, f"{name}: need {n} rows of {n_kv_heads} x {head_dim} with contiguous heads, got "
+                                 f"{tuple(shape)} with strides {tuple(strides)}")
+    return strides[0]
 
 
 def ql_kv4_record_bytes(head_dim):
@@ -248,7 +255,8 @@ def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=Non
     """Quantise rows ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided) into one layer's 4-bit
     pool at physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out)."""
     n = slots.numel()
-    ks, vs = (_rows_of("ql_kv4_write", t, n, n_kv_heads, head_dim) for t in (k, v))
+    ks = _row_stride("ql_kv4_write", k, n, n_kv_heads, head_dim)
+    vs = _row_stride("ql_kv4_write", v, n, n_kv_heads, head_dim)
     check(lib().ql_kv4_write(ptr(k), ptr(v), _dtype_of("ql_kv4_write", k, v), ks, vs, ptr(slots), n, n_kv_heads,
                              head_dim, ptr(pool), num_blocks, stream_ptr(stream)))
 
@@ -256,7 +264,8 @@ def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=Non
 def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None):
     """The values of ``slots`` read back into ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided)."""
     n = slots.numel()
-    ks, vs = (_rows_of("ql_kv4_read", t, n, n_kv_heads, head_dim) for t in (k, v))
+    ks = _row_stride("ql_kv4_read", k, n, n_kv_heads, head_dim)
+    vs = _row_stride("ql_kv4_read", v, n, n_kv_heads, head_dim)
     check(lib().ql_kv4_read(ptr(pool), ptr(slots), n, n_kv_heads, head_dim, num_blocks, ptr(k), ptr(v),
                             _dtype_of("ql_kv4_read", k, v), ks, vs, stream_ptr(stream)))
 

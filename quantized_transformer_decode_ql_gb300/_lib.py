@@ -177,10 +177,25 @@ def ptr(x) -> int | None:
     return x.data_ptr()
 
 
-def stream_ptr(stream=None) -> int | None:
+_current_stream = None   # () -> the current stream's address
+
+
+def _find_current_stream():
+    """The address of the current stream without a stream object around it, where this PyTorch offers it."""
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
+
+
+def stream_ptr(stream=None) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

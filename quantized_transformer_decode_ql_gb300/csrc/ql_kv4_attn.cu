@@ -717,9 +717,12 @@ constexpr size_t attn_smem() {
 
 int attn_grid() { return kCtasPerSm * num_sms(); }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+template <int HD, bool DUP>
+cudaError_t attn_go(const Params& p, int grid, cudaStream_t s, bool pdl, DevError* err) {
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem_once(kv4_attn_kernel<HD, DUP>, attn_smem<HD>(), done);
+    return e == cudaSuccess ? launch(kv4_attn_kernel<HD, DUP>, dim3((unsigned)grid), dim3(kThreads), attn_smem<HD>(), s, pdl, p, err)
+                            : e;
 }
 
 }  // namespace
@@ -751,14 +754,10 @@ int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl) {
     p.out = a.out;
     p.slots = static_cast<float*>(a.workspace);
     p.tickets = reinterpret_cast<int*>(static_cast<char*>(a.workspace) + 2 * (size_t)grid * kSlotBytes);
-    auto go = [&](auto kernel, size_t smem) {
-        const cudaError_t e = allow_smem(kernel, smem);
-        return e == cudaSuccess ? launch(kernel, dim3((unsigned)grid), dim3(kThreads), smem, s, pdl, p, err) : e;
-    };
     const bool dup = p.group <= 4;
     const cudaError_t e = a.head_dim == 128
-                              ? (dup ? go(kv4_attn_kernel<128, true>, attn_smem<128>()) : go(kv4_attn_kernel<128, false>, attn_smem<128>()))
-                              : (dup ? go(kv4_attn_kernel<64, true>, attn_smem<64>()) : go(kv4_attn_kernel<64, false>, attn_smem<64>()));
+                              ? (dup ? attn_go<128, true>(p, grid, s, pdl, err) : attn_go<128, false>(p, grid, s, pdl, err))
+                              : (dup ? attn_go<64, true>(p, grid, s, pdl, err) : attn_go<64, false>(p, grid, s, pdl, err));
     return e == cudaSuccess ? QL_OK : cuda_error(e, "4-bit attention launch");
 }
 

@@ -830,6 +830,15 @@ int cluster_for(int64_t batch, int64_t vocab, bool staged) {
     return c;
 }
 
+template <typename T>
+cudaError_t sample_go(bool staged, const cudaLaunchConfig_t& cfg, const Params& p, DevError* err) {
+    static std::atomic<unsigned long long> done{0};
+    if (!staged) return cudaLaunchKernelEx(&cfg, sample_plain_kernel<T>, p, err);
+    const size_t most = (size_t)(kMaxSampleVocab / kMaxCluster + 8) * 4 + (size_t)kBins * 32 * 8;   // of any call
+    const cudaError_t e = allow_smem_once(sample_kernel<T>, most, done);
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, sample_kernel<T>, p, err) : e;
+}
+
 }  // namespace
 
 int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
@@ -867,13 +876,7 @@ int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    auto go = [&](auto kernel) {
-        const cudaError_t e =
-            staged ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
-        return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, p, err) : e;
-    };
-    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? (staged ? go(sample_kernel<float>) : go(sample_plain_kernel<float>))
-                                                  : (staged ? go(sample_kernel<__half>) : go(sample_plain_kernel<__half>));
+    const cudaError_t e = a.dtype == QL_DTYPE_F32 ? sample_go<float>(staged, cfg, p, err) : sample_go<__half>(staged, cfg, p, err);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "sampling launch");
 }
 
