@@ -2,7 +2,8 @@
 //
 // Both are bound by memory: a row of one kv head is 2 HD values in (or out) and 1.25 HD bytes out (or
 // in). HD / 8 neighbouring lanes share the (row, kv head): 8 key values and 8 value values a lane,
-// loaded before anything else, so that a full SM has 64 KB (f32) in flight.
+// loaded before anything else, so that a full SM has 64 KB (f32) in flight. A CTA stays with one kv head
+// (no division by the heads); its rows' pieces are at least 128 bytes each.
 #include "ql_internal.h"
 #include "ql_kv4_rec.cuh"
 
@@ -49,16 +50,13 @@ __device__ __forceinline__ void load4<__half>(const __half* p, float* x) {
 template <int HD, typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const T* __restrict__ k, const T* __restrict__ v,
                                                                 long long ks, long long vs,
-                                                                const long long* __restrict__ slots, long long items,
-                                                                int n_kv, uint8_t* __restrict__ pool,
-                                                                long long num_blocks, DevError* err) {
+                                                                const long long* __restrict__ slots, long long n,
+                                                                uint8_t* __restrict__ pool, long long num_blocks,
+                                                                DevError* err) {
     using R = Kv4<HD>;
-    const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long item = at / R::LANES;
-    const int l = (int)(at % R::LANES), b = l >> 2, j = l & 3;
-    const bool in = item < items;   // the last warp's spare lanes still take part in its shuffles
-    const long long i = in ? item / n_kv : 0;
-    const int g = in ? (int)(item - i * n_kv) : 0;
+    const long long i = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) / R::LANES;
+    const int l = threadIdx.x % R::LANES, b = l >> 2, j = l & 3, g = blockIdx.y;
+    const bool in = i < n;   // the last warp's spare lanes still take part in its shuffles
     float xk[8] = {}, xv[8] = {};
     long long slot = -1;
     if (in) {
@@ -73,76 +71,79 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const T* __restr
     const long long blk = slot >> 4;
     const bool live = slot >= 0 && blk < num_blocks;
     if (in && !live && slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
-    uint8_t* rec = pool + ((size_t)(live ? blk : 0) * n_kv + g) * R::BYTES;
+    uint8_t* rec = pool + ((size_t)(live ? blk : 0) * gridDim.y + g) * R::BYTES;
     const bool ok = kv4_put_rows<HD>(xk, xv, rec, (int)(slot & 15), b, j, live);
-    bool finite = true;
+    float odd = 0.f;   // NaN from a value that is not finite
 #pragma unroll
-    for (int t = 0; t < 8; ++t) finite = finite && isfinite(xk[t]) && isfinite(xv[t]);
-    if (live && !finite) record_device_error(err, kErrKvNonFinite, i, g);
+    for (int t = 0; t < 8; ++t) odd = fmaf(xk[t], 0.f, fmaf(xv[t], 0.f, odd));
+    if (live && odd != 0.f) record_device_error(err, kErrKvNonFinite, i, g);
     else if (live && !ok) record_device_error(err, kErrKvOverflow, i, g);
 }
 
-// 8 consecutive values d c + m, each rounded once. f16: one fused multiply-add of exact f16 codes
-// (1024 + c has the code in its low bits); f32: d c is exact, so is the fused multiply-add's rounding.
-__device__ __forceinline__ void put8(__half* o, const uint32_t (&c)[8], __half d, __half m) {
+// 8 consecutive values d c + m, each rounded once, from their codes in the bytes of c[0], c[1]. f16: one
+// fused multiply-add of exact f16 codes (1024 + c has the code in its low byte); f32: d c is exact, and so
+// the fused multiply-add rounds once.
+__device__ __forceinline__ void put8(__half* o, const uint32_t (&c)[2], __half d, __half m) {
     const __half2 dd = __half2half2(d), mm = __half2half2(m), k1024 = __float2half2_rn(1024.f);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t h = c[2 * i] | (c[2 * i + 1] << 16) | 0x64006400u;
+        const uint32_t h = __byte_perm(c[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140);
         const __half2 y = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&h), k1024), dd, mm);
         w[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
     *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void put8(float* o, const uint32_t (&c)[8], __half d, __half m) {
+__device__ __forceinline__ void put8(float* o, const uint32_t (&c)[2], __half d, __half m) {
     const float df = __half2float(d), mf = __half2float(m);
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(df, (float)c[i], mf);
+    for (int i = 0; i < 8; ++i)   // 2^23 + c, minus 2^23
+        y[i] = fmaf(df, __uint_as_float(__byte_perm(c[i >> 2], 0x4B000000u, 0x7650 + (i & 3))) - 8388608.f, mf);
     reinterpret_cast<float4*>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
     reinterpret_cast<float4*>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
 
-// Lane (block b, w) writes elements 8 w .. 8 w + 7 of block b of the key row and of the value row.
+// A lane writes elements 8 w .. 8 w + 7 of block b of the key row and of the value row. The value codes of
+// those 8 elements lie in 8 units: each lane loads one word (a unit's two blocks), and the 8 lanes of a
+// pair of blocks transpose their 8 words of 8 codes by three exchanges (halves, bytes, nibbles).
 template <int HD, typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __restrict__ pool,
-                                                               const long long* __restrict__ slots, long long items,
-                                                               int n_kv, long long num_blocks, T* __restrict__ k,
+                                                               const long long* __restrict__ slots, long long n,
+                                                               long long num_blocks, T* __restrict__ k,
                                                                T* __restrict__ v, long long ks, long long vs,
                                                                DevError* err) {
     using R = Kv4<HD>;
-    const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long item = at / R::LANES;
-    if (item >= items) return;
-    const int l = (int)(at % R::LANES), b = l >> 2, w = l & 3;
-    const long long i = item / n_kv;
-    const int g = (int)(item - i * n_kv);
-    const long long slot = __ldg(slots + i);
+    constexpr int P = R::NB / 2;           // pairs of blocks
+    const long long i = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) / R::LANES;
+    const int l = threadIdx.x % R::LANES, pair = l % P, u = l / P, g = blockIdx.y;
+    const int b = 2 * pair + (u >> 2), w = u & 3;
+    const bool in = i < n;
+    const long long slot = in ? __ldg(slots + i) : -1;
     const long long blk = slot >> 4;
-    if (slot < 0 || blk >= num_blocks) {
-        if (slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
-        return;
-    }
+    const bool live = slot >= 0 && blk < num_blocks;   // the others still take part in the exchanges
+    if (in && !live && slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
     const int s = (int)(slot & 15);
-    const uint8_t* rec = pool + ((size_t)blk * n_kv + g) * R::BYTES;
-    const uint8_t* krow = rec + R::KC + s * (HD / 2);
-    const uint8_t* vrow = rec + R::VC + s * (HD / 2) + 2 * b;
-    const int j0 = 2 * (w & 1);
-    const uint32_t k0 = *reinterpret_cast<const uint32_t*>(krow + 4 * (R::NB * j0 + b)) >> (4 * (w >> 1));
-    const uint32_t k1 = *reinterpret_cast<const uint32_t*>(krow + 4 * (R::NB * (j0 + 1) + b)) >> (4 * (w >> 1));
-    uint32_t ck[8], cv[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) cv[t] = (*reinterpret_cast<const uint16_t*>(vrow + R::vunit(s, t)) >> (4 * w)) & 15u;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        ck[t] = (k0 >> (8 * t)) & 15u;
-        ck[4 + t] = (k1 >> (8 * t)) & 15u;
-    }
+    const uint8_t* rec = pool + ((size_t)(live ? blk : 0) * gridDim.y + g) * R::BYTES;
+    const uint8_t* krow = rec + R::KC + s * (HD / 2) + 4 * (R::NB * 2 * (w & 1) + b);
+    const uint32_t k0 = __ldg(reinterpret_cast<const uint32_t*>(krow));
+    const uint32_t k1 = __ldg(reinterpret_cast<const uint32_t*>(krow + 4 * R::NB));
+    uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(rec + R::VC + s * (HD / 2) + R::vunit(s, u) + 4 * pair));
     const __half dk = reinterpret_cast<const __half*>(rec + R::KD)[s * R::NB + b];
     const __half mk = reinterpret_cast<const __half*>(rec + R::KM)[s * R::NB + b];
     const __half dv = reinterpret_cast<const __half*>(rec + R::VD)[R::vscale(s, b)];
     const __half mv = reinterpret_cast<const __half*>(rec + R::VM)[R::vscale(s, b)];
+    uint32_t y = __shfl_xor_sync(0xffffffffu, x, 4 * P);
+    x = __byte_perm(x, y, u & 4 ? 0x3276 : 0x5410);
+    y = __shfl_xor_sync(0xffffffffu, x, 2 * P);
+    x = __byte_perm(x, y, u & 2 ? 0x3715 : 0x6240);
+    y = __shfl_xor_sync(0xffffffffu, x, P);
+    x = u & 1 ? ((y >> 4) & 0x0f0f0f0fu) | (x & 0xf0f0f0f0u) : (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+    if (!live) return;
+    const int sh = 4 * (w >> 1);
+    const uint32_t ck[2] = {(k0 >> sh) & 0x0f0f0f0fu, (k1 >> sh) & 0x0f0f0f0fu};
+    const uint32_t even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
+    const uint32_t cv[2] = {__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362)};
     put8(k + i * ks + (size_t)g * HD + 32 * b + 8 * w, ck, dk, mk);
     put8(v + i * vs + (size_t)g * HD + 32 * b + 8 * w, cv, dv, mv);
 }
@@ -166,9 +167,9 @@ int kv4_rows_check(const char* name, const void* k, const void* v, int dtype, in
     const int64_t per = dtype == QL_DTYPE_F32 ? 4 : 8;
     if (n > 1 && (ks < (int64_t)n_kv * hd || vs < (int64_t)n_kv * hd || ks % per || vs % per))
         return set_error(QL_EINVAL, nm + ": row strides must be multiples of 16 bytes and at least n_kv_heads * head_dim");
-    const int64_t lanes = (int64_t)(hd / 8) * n_kv;
-    if (n > ((1ll << 31) - 1) * kKv4Threads / lanes) return set_error(QL_EINVAL, nm + ": too many rows");
-    *grid = (unsigned)((n * lanes + kKv4Threads - 1) / kKv4Threads);
+    const int64_t rows = kKv4Threads / (hd / 8);   // of a CTA
+    if (n > ((1ll << 31) - 1) * rows || n_kv > 65535) return set_error(QL_EINVAL, nm + ": too many rows or heads");
+    *grid = (unsigned)((n + rows - 1) / rows);
     return QL_OK;
 }
 
@@ -192,9 +193,9 @@ extern "C" int ql_kv4_write(const void* d_k, const void* d_v, int dtype, int64_t
     if (!err) return set_error(QL_ECUDA, "ql_kv4_write: no device error record");
     auto go = [&](auto kernel, auto zero) {
         using T = decltype(zero);
-        return launch(kernel, dim3(grid), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
+        return launch(kernel, dim3(grid, (unsigned)n_kv_heads), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
                       static_cast<const T*>(d_k), static_cast<const T*>(d_v), (long long)k_stride, (long long)v_stride,
-                      reinterpret_cast<const long long*>(d_slots), (long long)(n * n_kv_heads), n_kv_heads,
+                      reinterpret_cast<const long long*>(d_slots), (long long)n,
                       static_cast<uint8_t*>(d_pool), (long long)num_blocks, err);
     };
     const bool f32 = dtype == QL_DTYPE_F32;
@@ -218,9 +219,9 @@ extern "C" int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n
     if (!err) return set_error(QL_ECUDA, "ql_kv4_read: no device error record");
     auto go = [&](auto kernel, auto zero) {
         using T = decltype(zero);
-        return launch(kernel, dim3(grid), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
+        return launch(kernel, dim3(grid, (unsigned)n_kv_heads), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
                       static_cast<const uint8_t*>(d_pool), reinterpret_cast<const long long*>(d_slots),
-                      (long long)(n * n_kv_heads), n_kv_heads, (long long)num_blocks, static_cast<T*>(d_k),
+                      (long long)n, (long long)num_blocks, static_cast<T*>(d_k),
                       static_cast<T*>(d_v), (long long)k_stride, (long long)v_stride, err);
     };
     const bool f32 = dtype == QL_DTYPE_F32;

@@ -45,11 +45,12 @@ static __device__ __noinline__ float kv4_code_f64(float x, float m, float d) {
 }
 
 // One block of 32 elements, 8 in each of 4 neighbouring lanes (x: this lane's): the stored scale and
-// minimum, and this lane's codes. All 32 lanes of the warp take part. Each of m, d and the codes is
-// its exact value rounded once: d from the difference with its rounding error, compared with the
-// border between its two f16 neighbours; a code from f32, whose error is below 2^-18 for codes up to
-// 16 (three roundings of 2^-24 each), unless it lies within 2^-17 of a border, where f64 decides.
-// Returns false if the minimum or the scale overflows f16.
+// minimum, and this lane's codes, code[i] = 0x4B400000 + the code of x[i]. All 32 lanes of the warp take
+// part. Each of m, d and the codes is its exact value rounded once: d from the difference with its
+// rounding error, compared with the border between its two f16 neighbours; a code from f32, whose error
+// is below 2^-18 for codes up to 16 (two roundings of 2^-24 and a reciprocal good to 2^-23), unless it
+// lies within 2^-17 of a border, where f64 decides. The sum with 1.5 2^23 rounds to the nearest integer
+// and leaves it in the low bits. Returns false if the minimum or the scale overflows f16.
 __device__ __forceinline__ bool kv4_block(const float (&x)[8], uint32_t (&code)[8], __half& dh, __half& mh) {
     float mn = x[0], mx = x[0];
 #pragma unroll
@@ -77,23 +78,28 @@ __device__ __forceinline__ bool kv4_block(const float (&x)[8], uint32_t (&code)[
     const bool up = over > 0.f || (over == 0.f && (lob & 1));
     dh = __ushort_as_half((uint16_t)(lob + (up && lob < 0x7C00u ? 1 : 0)));
     const float d = __half2float(dh), m = __half2float(mh);
-    const float id = d > 0.f ? __fdiv_rn(1.0f, d) : 0.f;
+    float id;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(id) : "f"(d));
+    id = d > 0.f ? id : 0.f;
     bool near = false;
-    float q[8];
+    float r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float f = __fmul_rn(__fsub_rn(x[i], m), id);
-        q[i] = rintf(f);
-        near = near || fabsf(f - q[i]) > 0.5f - 0x1p-17f;
+        // clamped first: the ends are integers, and NaN becomes 0
+        const float f = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], m), id), 0.f), 15.f);
+        r[i] = __fadd_rn(f, 12582912.0f);
+        near = near || fabsf(__fsub_rn(f, __fsub_rn(r[i], 12582912.0f))) > 0.5f - 0x1p-17f;
     }
-    if (near && d > 0.f) {
+    if (near) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = kv4_code_f64(x[i], m, d);
+        for (int i = 0; i < 8; ++i) r[i] = fminf(fmaxf(kv4_code_f64(x[i], m, d), 0.f), 15.f) + 12582912.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = (uint32_t)fminf(fmaxf(q[i], 0.f), 15.f);   // NaN: 0
+    for (int i = 0; i < 8; ++i) code[i] = __float_as_uint(r[i]);
     return !__hisinf(dh) && !__hisinf(mh);
 }
+
+constexpr uint32_t kCodeOne = 0x4B400000u;   // the constant part of a code
 
 // Quantise a key row and a value row into slot `slot` of a record, by LANES neighbouring lanes: this
 // lane is word j (0..3) of block b. xk: elements 4 j + {0..3} and 16 + 4 j + {0..3} of the block of
@@ -108,15 +114,16 @@ __device__ __forceinline__ bool kv4_put_rows(const float (&xk)[8], const float (
     const bool okk = kv4_block(xk, ck, dk, mk);
     const bool okv = kv4_block(xv, cv, dv, mv);
     if (live) {
-        uint32_t w = 0;
+        // the codes' constant parts add up to a constant each
+        uint32_t w = 0u - kCodeOne * 0x11111111u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w |= (ck[i] | (ck[4 + i] << 4)) << (8 * i);
+        for (int i = 0; i < 4; ++i) w += ck[i] * (1u << (8 * i)) + ck[4 + i] * (16u << (8 * i));
         *reinterpret_cast<uint32_t*>(rec + R::KC + slot * (HD / 2) + 4 * (R::NB * j + b)) = w;
         uint8_t* vrow = rec + R::VC + slot * (HD / 2) + 2 * b;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             *reinterpret_cast<uint16_t*>(vrow + R::vunit(slot, 2 * j + u)) =
-                (uint16_t)(cv[4 * u] | (cv[4 * u + 1] << 4) | (cv[4 * u + 2] << 8) | (cv[4 * u + 3] << 12));
+                (uint16_t)(cv[4 * u] + cv[4 * u + 1] * 16u + cv[4 * u + 2] * 256u + cv[4 * u + 3] * 4096u - kCodeOne * 0x1111u);
         if (j == 0) {
             reinterpret_cast<__half*>(rec + R::KD)[slot * R::NB + b] = dk;
             reinterpret_cast<__half*>(rec + R::KM)[slot * R::NB + b] = mk;
