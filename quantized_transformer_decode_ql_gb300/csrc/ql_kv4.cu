@@ -72,12 +72,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const T* __restr
     const bool live = slot >= 0 && blk < num_blocks;
     if (in && !live && slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
     uint8_t* rec = pool + ((size_t)(live ? blk : 0) * gridDim.y + g) * R::BYTES;
-    const bool ok = kv4_put_rows<HD>(xk, xv, rec, (int)(slot & 15), b, j, live);
-    float odd = 0.f;   // NaN from a value that is not finite
-#pragma unroll
-    for (int t = 0; t < 8; ++t) odd = fmaf(xk[t], 0.f, fmaf(xv[t], 0.f, odd));
-    if (live && odd != 0.f) record_device_error(err, kErrKvNonFinite, i, g);
-    else if (live && !ok) record_device_error(err, kErrKvOverflow, i, g);
+    const int fault = kv4_put_rows<HD>(xk, xv, rec, (int)(slot & 15), b, j, live);
+    if (live && fault) record_device_error(err, fault == 2 ? kErrKvNonFinite : kErrKvOverflow, i, g);
 }
 
 // 8 consecutive values d c + m, each rounded once, from their codes in the bytes of c[0], c[1]. f16: one
@@ -106,7 +102,9 @@ __device__ __forceinline__ void put8(float* o, const uint32_t (&c)[2], __half d,
 
 // A lane writes elements 8 w .. 8 w + 7 of block b of the key row and of the value row. The value codes of
 // those 8 elements lie in 8 units: each lane loads one word (a unit's two blocks), and the 8 lanes of a
-// pair of blocks transpose their 8 words of 8 codes by three exchanges (halves, bytes, nibbles).
+// pair of blocks transpose their 8 words of 8 codes by three exchanges (halves, bytes, nibbles). A warp's
+// life is two round trips (slots, records), so a thread takes two rows at once.
+constexpr int kReadRows = 2;
 template <int HD, typename T>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __restrict__ pool,
                                                                const long long* __restrict__ slots, long long n,
@@ -114,44 +112,56 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __
                                                                T* __restrict__ v, long long ks, long long vs,
                                                                DevError* err) {
     using R = Kv4<HD>;
-    constexpr int P = R::NB / 2;           // pairs of blocks
-    const long long i = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) / R::LANES;
+    constexpr int P = R::NB / 2;                        // pairs of blocks
+    constexpr int ROWS = kKv4Threads / R::LANES;        // rows of a CTA at a time
     const int l = threadIdx.x % R::LANES, pair = l % P, u = l / P, g = blockIdx.y;
     const int b = 2 * pair + (u >> 2), w = u & 3;
-    const bool in = i < n;
-    const long long slot = in ? __ldg(slots + i) : -1;
-    const long long blk = slot >> 4;
-    const bool live = slot >= 0 && blk < num_blocks;   // the others still take part in the exchanges
-    if (in && !live && slot != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i, slot);
-    const int s = (int)(slot & 15);
-    const uint8_t* rec = pool + ((size_t)(live ? blk : 0) * gridDim.y + g) * R::BYTES;
-    const uint8_t* krow = rec + R::KC + s * (HD / 2) + 4 * (R::NB * 2 * (w & 1) + b);
-    const uint32_t k0 = __ldg(reinterpret_cast<const uint32_t*>(krow));
-    const uint32_t k1 = __ldg(reinterpret_cast<const uint32_t*>(krow + 4 * R::NB));
-    uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(rec + R::VC + s * (HD / 2) + R::vunit(s, u) + 4 * pair));
-    const __half dk = reinterpret_cast<const __half*>(rec + R::KD)[s * R::NB + b];
-    const __half mk = reinterpret_cast<const __half*>(rec + R::KM)[s * R::NB + b];
-    const __half dv = reinterpret_cast<const __half*>(rec + R::VD)[R::vscale(s, b)];
-    const __half mv = reinterpret_cast<const __half*>(rec + R::VM)[R::vscale(s, b)];
-    uint32_t y = __shfl_xor_sync(0xffffffffu, x, 4 * P);
-    x = __byte_perm(x, y, u & 4 ? 0x3276 : 0x5410);
-    y = __shfl_xor_sync(0xffffffffu, x, 2 * P);
-    x = __byte_perm(x, y, u & 2 ? 0x3715 : 0x6240);
-    y = __shfl_xor_sync(0xffffffffu, x, P);
-    x = u & 1 ? ((y >> 4) & 0x0f0f0f0fu) | (x & 0xf0f0f0f0u) : (x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
-    if (!live) return;
-    const int sh = 4 * (w >> 1);
-    const uint32_t ck[2] = {(k0 >> sh) & 0x0f0f0f0fu, (k1 >> sh) & 0x0f0f0f0fu};
-    const uint32_t even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
-    const uint32_t cv[2] = {__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362)};
-    put8(k + i * ks + (size_t)g * HD + 32 * b + 8 * w, ck, dk, mk);
-    put8(v + i * vs + (size_t)g * HD + 32 * b + 8 * w, cv, dv, mv);
+    const long long i0 = (long long)blockIdx.x * (kReadRows * ROWS) + threadIdx.x / R::LANES;
+    long long slot[kReadRows];
+    bool live[kReadRows];                               // the others still take part in the exchanges
+    uint32_t k0[kReadRows], k1[kReadRows], x[kReadRows];
+    __half dk[kReadRows], mk[kReadRows], dv[kReadRows], mv[kReadRows];
+#pragma unroll
+    for (int r = 0; r < kReadRows; ++r) slot[r] = i0 + r * ROWS < n ? __ldg(slots + i0 + r * ROWS) : -1;
+#pragma unroll
+    for (int r = 0; r < kReadRows; ++r) {
+        const long long blk = slot[r] >> 4;
+        live[r] = slot[r] >= 0 && blk < num_blocks;
+        if (!live[r] && slot[r] != -1 && g == 0 && l == 0) record_device_error(err, kErrKvSlot, i0 + r * ROWS, slot[r]);
+        const int s = (int)(slot[r] & 15);
+        const uint8_t* rec = pool + ((size_t)(live[r] ? blk : 0) * gridDim.y + g) * R::BYTES;
+        const uint8_t* krow = rec + R::KC + s * (HD / 2) + 4 * (R::NB * 2 * (w & 1) + b);
+        k0[r] = __ldg(reinterpret_cast<const uint32_t*>(krow));
+        k1[r] = __ldg(reinterpret_cast<const uint32_t*>(krow + 4 * R::NB));
+        x[r] = __ldg(reinterpret_cast<const uint32_t*>(rec + R::VC + s * (HD / 2) + R::vunit(s, u) + 4 * pair));
+        dk[r] = reinterpret_cast<const __half*>(rec + R::KD)[s * R::NB + b];
+        mk[r] = reinterpret_cast<const __half*>(rec + R::KM)[s * R::NB + b];
+        dv[r] = reinterpret_cast<const __half*>(rec + R::VD)[R::vscale(s, b)];
+        mv[r] = reinterpret_cast<const __half*>(rec + R::VM)[R::vscale(s, b)];
+    }
+#pragma unroll
+    for (int r = 0; r < kReadRows; ++r) {
+        uint32_t y = __shfl_xor_sync(0xffffffffu, x[r], 4 * P);
+        uint32_t z = __byte_perm(x[r], y, u & 4 ? 0x3276 : 0x5410);
+        y = __shfl_xor_sync(0xffffffffu, z, 2 * P);
+        z = __byte_perm(z, y, u & 2 ? 0x3715 : 0x6240);
+        y = __shfl_xor_sync(0xffffffffu, z, P);
+        z = u & 1 ? ((y >> 4) & 0x0f0f0f0fu) | (z & 0xf0f0f0f0u) : (z & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u);
+        if (!live[r]) continue;
+        const int sh = 4 * (w >> 1);
+        const uint32_t ck[2] = {(k0[r] >> sh) & 0x0f0f0f0fu, (k1[r] >> sh) & 0x0f0f0f0fu};
+        const uint32_t even = z & 0x0f0f0f0fu, odd = (z >> 4) & 0x0f0f0f0fu;
+        const uint32_t cv[2] = {__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362)};
+        const long long i = i0 + r * ROWS;
+        put8(k + i * ks + (size_t)g * HD + 32 * b + 8 * w, ck, dk[r], mk[r]);
+        put8(v + i * vs + (size_t)g * HD + 32 * b + 8 * w, cv, dv[r], mv[r]);
+    }
 }
 
-// The checks that the writer and the reader share; `grid` for n > 0.
+// The checks that the writer and the reader share; `grid` for n > 0, each CTA `times` as many rows as its threads hold.
 int kv4_rows_check(const char* name, const void* k, const void* v, int dtype, int64_t ks, int64_t vs,
                    const int64_t* slots, int64_t n, int n_kv, int hd, const void* pool, int64_t num_blocks,
-                   unsigned* grid) {
+                   int times, unsigned* grid) {
     const std::string nm(name);
     if (dtype != QL_DTYPE_F32 && dtype != QL_DTYPE_F16) return set_error(QL_EINVAL, nm + ": dtype must be f32 or f16");
     if (hd != 64 && hd != 128) return set_error(QL_EINVAL, nm + ": head_dim must be 64 or 128");
@@ -167,7 +177,7 @@ int kv4_rows_check(const char* name, const void* k, const void* v, int dtype, in
     const int64_t per = dtype == QL_DTYPE_F32 ? 4 : 8;
     if (n > 1 && (ks < (int64_t)n_kv * hd || vs < (int64_t)n_kv * hd || ks % per || vs % per))
         return set_error(QL_EINVAL, nm + ": row strides must be multiples of 16 bytes and at least n_kv_heads * head_dim");
-    const int64_t rows = kKv4Threads / (hd / 8);   // of a CTA
+    const int64_t rows = (int64_t)times * kKv4Threads / (hd / 8);   // of a CTA
     if (n > ((1ll << 31) - 1) * rows || n_kv > 65535) return set_error(QL_EINVAL, nm + ": too many rows or heads");
     *grid = (unsigned)((n + rows - 1) / rows);
     return QL_OK;
@@ -186,7 +196,7 @@ extern "C" int ql_kv4_write(const void* d_k, const void* d_v, int dtype, int64_t
     using namespace ql;
     unsigned grid = 0;
     if (int rc = kv4_rows_check("ql_kv4_write", d_k, d_v, dtype, k_stride, v_stride, d_slots, n, n_kv_heads, head_dim,
-                                d_pool, num_blocks, &grid))
+                                d_pool, num_blocks, 1, &grid))
         return rc;
     if (grid == 0) return QL_OK;
     DevError* err = device_error_record();
@@ -212,7 +222,7 @@ extern "C" int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n
     using namespace ql;
     unsigned grid = 0;
     if (int rc = kv4_rows_check("ql_kv4_read", d_k, d_v, dtype, k_stride, v_stride, d_slots, n, n_kv_heads, head_dim,
-                                d_pool, num_blocks, &grid))
+                                d_pool, num_blocks, kReadRows, &grid))
         return rc;
     if (grid == 0) return QL_OK;
     DevError* err = device_error_record();

@@ -39,29 +39,32 @@ struct Kv4 {
 };
 
 #ifdef __CUDACC__
-// The code of x by its definition in f64. Kept out of line: one element in about 2^16 comes here.
-static __device__ __noinline__ float kv4_code_f64(float x, float m, float d) {
-    return (float)rint(((double)x - (double)m) / (double)d);
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // One block of 32 elements, 8 in each of 4 neighbouring lanes (x: this lane's): the stored scale and
 // minimum, and this lane's codes, code[i] = 0x4B400000 + the code of x[i]. All 32 lanes of the warp take
-// part. Each of m, d and the codes is its exact value rounded once: d from the difference with its
-// rounding error, compared with the border between its two f16 neighbours; a code from f32, whose error
-// is below 2^-18 for codes up to 16 (two roundings of 2^-24 and a reciprocal good to 2^-23), unless it
-// lies within 2^-17 of a border, where f64 decides. The sum with 1.5 2^23 rounds to the nearest integer
-// and leaves it in the low bits. Returns false if the minimum or the scale overflows f16.
-__device__ __forceinline__ bool kv4_block(const float (&x)[8], uint32_t (&code)[8], __half& dh, __half& mh) {
+// part. Each of m, d and the codes is its exact value rounded once:
+//   d  from the difference with its rounding error, compared with the border between its f16 neighbours;
+//   a code from g = (x - m) / (15 d) clamped to [0, 1] in f32, 15 g + 1.5 2^23 leaving the nearest integer
+//      in the low bits. 15 g is off by at most 16 * 6 * 2^-24 < 2^-17 (a difference, a reciprocal good to
+//      2^-23, three products); within 2^-17 of a border the exact difference is compared with it.
+// A block with a value that is not finite decodes to NaN. Returns 0, 1 if the minimum or the scale
+// overflows f16, 2 if a value is not finite.
+__device__ __forceinline__ int kv4_block(const float (&x)[8], uint32_t (&code)[8], __half& dh, __half& mh) {
     float mn = x[0], mx = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
         mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
+        mx = max_nan(mx, x[i]);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
     mh = __hadd(__float2half_rn(mn), __float2half_rn(0.f));   // a zero minimum is stored as +0
     // mx - mn = s + e exactly
@@ -80,23 +83,29 @@ __device__ __forceinline__ bool kv4_block(const float (&x)[8], uint32_t (&code)[
     const float d = __half2float(dh), m = __half2float(mh);
     float id;
     asm("rcp.approx.f32 %0, %1;" : "=f"(id) : "f"(d));
-    id = d > 0.f ? id : 0.f;
-    bool near = false;
-    float r[8];
+    id = d > 0.f ? __fmul_rn(id, 1.0f / 15.0f) : 0.f;
+    float off = 0.f, g[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        // clamped first: the ends are integers, and NaN becomes 0
-        const float f = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], m), id), 0.f), 15.f);
-        r[i] = __fadd_rn(f, 12582912.0f);
-        near = near || fabsf(__fsub_rn(f, __fsub_rn(r[i], 12582912.0f))) > 0.5f - 0x1p-17f;
+        g[i] = __saturatef(__fmul_rn(__fsub_rn(x[i], m), id));
+        const float r = __fmaf_rn(g[i], 15.0f, 12582912.0f);
+        code[i] = __float_as_uint(r);
+        off = fmaxf(off, fabsf(__fmaf_rn(g[i], 15.0f, -__fsub_rn(r, 12582912.0f))));
     }
-    if (near) {
+    if (off > 0.5f - 0x1p-17f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = fminf(fmaxf(kv4_code_f64(x[i], m, d), 0.f), 15.f) + 12582912.0f;
+        for (int i = 0; i < 8; ++i) {
+            // x - m = y + ye exactly, against the border (k + 1/2) d, which has 16 bits
+            const float k = floorf(15.0f * g[i]);
+            const float y = __fsub_rn(x[i], m), z = __fsub_rn(y, x[i]);
+            const float ye = __fadd_rn(__fsub_rn(x[i], __fsub_rn(y, z)), __fsub_rn(-m, z));
+            const float v = __fadd_rn(__fsub_rn(y, __fmul_rn(k + 0.5f, d)), ye);
+            const bool odd = ((int)k & 1) != 0;
+            if (fabsf(__fmaf_rn(g[i], 15.0f, -k) - 0.5f) < 0x1p-16f)
+                code[i] = 0x4B400000u + (uint32_t)k + (v > 0.f || (v == 0.f && odd) ? 1u : 0u);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = __float_as_uint(r[i]);
-    return !__hisinf(dh) && !__hisinf(mh);
+    return !(mx - mn < INFINITY) ? 2 : __hisinf(dh) || __hisinf(mh) ? 1 : 0;
 }
 
 constexpr uint32_t kCodeOne = 0x4B400000u;   // the constant part of a code
@@ -104,15 +113,14 @@ constexpr uint32_t kCodeOne = 0x4B400000u;   // the constant part of a code
 // Quantise a key row and a value row into slot `slot` of a record, by LANES neighbouring lanes: this
 // lane is word j (0..3) of block b. xk: elements 4 j + {0..3} and 16 + 4 j + {0..3} of the block of
 // the key row; xv: elements 2 j + 8 q and 2 j + 1 + 8 q (q = 0..3) of the value row, at q and 4 + q.
-// Stores only where `live`; all 32 lanes of the warp take part. False on an f16 overflow.
+// Stores only where `live`; all 32 lanes of the warp take part. Returns what kv4_block does, the larger.
 template <int HD>
-__device__ __forceinline__ bool kv4_put_rows(const float (&xk)[8], const float (&xv)[8], uint8_t* rec, int slot, int b,
+__device__ __forceinline__ int kv4_put_rows(const float (&xk)[8], const float (&xv)[8], uint8_t* rec, int slot, int b,
                                              int j, bool live) {
     using R = Kv4<HD>;
     uint32_t ck[8], cv[8];
     __half dk, mk, dv, mv;
-    const bool okk = kv4_block(xk, ck, dk, mk);
-    const bool okv = kv4_block(xv, cv, dv, mv);
+    const int fk = kv4_block(xk, ck, dk, mk), fv = kv4_block(xv, cv, dv, mv);
     if (live) {
         // the codes' constant parts add up to a constant each
         uint32_t w = 0u - kCodeOne * 0x11111111u;
@@ -131,7 +139,7 @@ __device__ __forceinline__ bool kv4_put_rows(const float (&xk)[8], const float (
             reinterpret_cast<__half*>(rec + R::VM)[R::vscale(slot, b)] = mv;
         }
     }
-    return okk && okv;
+    return fk > fv ? fk : fv;
 }
 #endif
 
