@@ -483,8 +483,8 @@ typedef struct {
     int block_size;             /* 16 */
     int64_t max_batch;          /* largest batch any step will use */
     int64_t max_blocks_per_seq; /* block-table row length; max context = this * block_size */
-    int kv_format;              /* QL_KV_F16 (k_pool / v_pool) or QL_KV_Q8_0_Q5_1 (kvq_pool) */
-    void* kvq_pool;             /* QL_KV_Q8_0_Q5_1: u8 [n_layers][num_blocks][n_kv][ql_kvq_record_bytes] */
+    int kv_format;              /* QL_KV_F16 (k_pool / v_pool), QL_KV_Q8_0_Q5_1 or QL_KV_Q4_1 (kvq_pool) */
+    void* kvq_pool;             /* u8 [n_layers][num_blocks][n_kv][ql_kvq_record_bytes or ql_kv4_record_bytes] */
     /* Routed experts ([IL] Cfg: num_experts, topk, moe_inter, norm_topk; 0 experts = dense).
      * Every layer's feed-forward block is then: router logits = router . rms(x) w_ffn (f32),
      * the softmax over all experts, the topk largest (lowest index first on ties), their weights
@@ -499,8 +499,12 @@ typedef struct {
 /* KV cache formats of a model (ql_model_desc.kv_format). QL_KV_Q8_0_Q5_1: the quantised pool of
  * ql_paged_attn_decode_kvq; the decode step quantises each appended K row as q8_0 and V row as
  * q5_1 (ql_kvq_write's rule) and reads every record back through the quantised attention. The
- * persistent step kernel takes only QL_KV_F16.                                            */
-enum { QL_KV_F16 = 0, QL_KV_Q8_0_Q5_1 = 1 };
+ * persistent step kernel takes only QL_KV_F16. QL_KV_Q4_1: the 4-bit pool of
+ * ql_paged_attn_decode_kv4; each step quantises its K and V rows (f32, K after norm and rotation)
+ * by ql_kv4_write's rule in a kernel before the attention; prefill chunks do the same and attend to
+ * the context's values as f16 (ql_kv4_read's, in a buffer of one layer that the handle owns:
+ * max_blocks_per_seq * 64 * n_kv_heads * head_dim bytes).                                   */
+enum { QL_KV_F16 = 0, QL_KV_Q8_0_Q5_1 = 1, QL_KV_Q4_1 = 2 };
 
 typedef struct ql_model ql_model;
 
@@ -560,6 +564,22 @@ enum { QL_STEP_AUTO = 0, QL_STEP_LAUNCHES = 1, QL_STEP_PERSISTENT = 2 };
 enum { QL_OPT_STEP_KERNEL = 1, QL_OPT_BARRIER_TIMEOUT_NS = 2, QL_OPT_TEST_BARRIER_EXTRA = 3,
        QL_OPT_STEP_TRACE = 4, QL_OPT_MERGE_TRACE = 5 };
 int ql_model_set_option(ql_model* m, int option, int64_t value);
+/* Sampling in place of the arg max for the decode steps issued (or graphs captured) afterwards;
+ * NULL: the arg max again. Device arrays of at least the steps' batch, owned by the caller, read by
+ * every step (a captured graph reads what they hold at its replay): temperature, top_k, top_p,
+ * min_p [batch] or NULL as for ql_sample; uniform f32 [batch][uniform_stride], of which a step at
+ * position p of slot b takes number p % uniform_stride (stride 1: numbers that the caller renews
+ * between steps). next_tokens and out_tokens then hold the drawn tokens (-1 where ql_sample gives
+ * -1). Prefill chunks keep their greedy next token; the persistent step kernel is QL_EINVAL.  */
+typedef struct {
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* uniform;
+    int64_t uniform_stride;
+} ql_sampling;
+int ql_model_set_sampling(ql_model* m, const ql_sampling* sampling);
 /* When the persistent kernel is available, ql_model_create also keeps a copy of every q4_0
  * matrix re-laid as a tile stream (16 rows x 4 blocks of codes and their scales contiguous,
  * 1152 B per unit) for the kernel's bulk copies: device memory equal to the weights again.
@@ -624,7 +644,8 @@ int ql_decode_graph_step_host(ql_model* m, int64_t batch, const int32_t* h_token
  * [max_blocks_per_seq] of the sequence (blocks for every position of the chunk assigned);
  * d_position: int32 [1], advanced by n_tokens; d_logits: f32 [vocab] of the chunk's last token,
  * or NULL; d_next_token: int32 [1], its greedy argmax, or NULL. 1 <= n_tokens <= min(256,
- * max_batch); dense models with the f16 KV format. Asynchronous on stream; not for capture. */
+ * max_batch); dense models with the f16 or the 4-bit KV format. Asynchronous on stream; not for
+ * capture. */
 int ql_prefill_chunk(ql_model* m, const int32_t* d_tokens, int64_t n_tokens, int32_t* d_position,
                      const int32_t* d_block_table, float* d_logits, int32_t* d_next_token, void* stream);
 /* Synchronizes the device and reads (and clears) its error record: QL_OK, or QL_EDEVICE

@@ -14,10 +14,10 @@ from ._lib import (QLError, QL_OK, QL_EINVAL, QL_ENOMEM, QL_ECUDA, QL_EPOOL, QL_
                    QL_EPI_ADD_RESIDUAL, QL_EPI_SILU_MUL, QL_STEP_AUTO, QL_STEP_LAUNCHES,
                    QL_STEP_PERSISTENT, QL_OPT_STEP_KERNEL, QL_OPT_BARRIER_TIMEOUT_NS,
                    QL_OPT_TEST_BARRIER_EXTRA, QL_OPT_STEP_TRACE, QL_OPT_MERGE_TRACE, QL_BATCHED_MMA_SYNC, QL_BATCHED_TCGEN05,
-                   QL_GEMV_ACT_INT16, QL_GEMV_ACT_INT8, QL_KV_F16, QL_KV_Q8_0_Q5_1,
+                   QL_GEMV_ACT_INT16, QL_GEMV_ACT_INT8, QL_KV_F16, QL_KV_Q8_0_Q5_1, QL_KV_Q4_1,
                    QL_ATTN_MERGE_TICKET, QL_ATTN_MERGE_CLUSTER,
                    Q4Matrix, LayerDesc, ModelDesc,
-                   StepArgs, SIGNATURES, LIB_PATH, lib, check, ptr, stream_ptr)
+                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, ptr, stream_ptr)
 
 __all__ = [
     "QLError", "lib", "ql_q4_0_pack", "ql_q4_0_unpack", "ql_q4_0_pack_device", "ql_gemv_q4_0",

@@ -21,7 +21,7 @@ QL_OPT_STEP_KERNEL, QL_OPT_BARRIER_TIMEOUT_NS, QL_OPT_TEST_BARRIER_EXTRA, QL_OPT
 QL_OPT_MERGE_TRACE = 5
 QL_BATCHED_MMA_SYNC, QL_BATCHED_TCGEN05 = 0, 1
 QL_GEMV_ACT_INT16, QL_GEMV_ACT_INT8 = 0, 1
-QL_KV_F16, QL_KV_Q8_0_Q5_1 = 0, 1
+QL_KV_F16, QL_KV_Q8_0_Q5_1, QL_KV_Q4_1 = 0, 1, 2
 QL_ATTN_MERGE_TICKET, QL_ATTN_MERGE_CLUSTER = 0, 1
 
 
@@ -57,6 +57,11 @@ class StepArgs(ctypes.Structure):
     _fields_ = [("batch", c_int64), ("tokens", c_void_p), ("positions", c_void_p),
                 ("block_tables", c_void_p), ("active", c_void_p), ("logits", c_void_p),
                 ("next_tokens", c_void_p), ("out_tokens", c_void_p), ("out_stride", c_int64)]
+
+
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", c_void_p), ("top_k", c_void_p), ("top_p", c_void_p), ("min_p", c_void_p),
+                ("uniform", c_void_p), ("uniform_stride", c_int64)]
 
 
 # name -> (restype, argtypes); the complete exported surface of include/ql.h
@@ -123,6 +128,7 @@ SIGNATURES = {
     "ql_model_create": (c_int, [POINTER(ModelDesc), POINTER(c_void_p)]),
     "ql_model_destroy": (c_int, [c_void_p]),
     "ql_model_set_option": (c_int, [c_void_p, c_int, c_int64]),
+    "ql_model_set_sampling": (c_int, [c_void_p, POINTER(Sampling)]),
     "ql_model_persistent_max_batch": (c_int64, [c_void_p]),
     "ql_decode_step": (c_int, [c_void_p, POINTER(StepArgs), c_void_p]),
     "ql_decode_graph_capture": (c_int, [c_void_p, POINTER(StepArgs), c_void_p]),

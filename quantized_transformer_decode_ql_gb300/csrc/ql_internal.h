@@ -235,6 +235,11 @@ struct RopeArgs {
     NextWeights next;
 };
 int rope_launch(const RopeArgs& a, cudaStream_t s, bool pdl);
+// The same into a layer's 4-bit pool (ql_kv4.cu; k_pool and v_pool are not used).
+int kv4_norm_rope_launch(const RopeArgs& a, uint8_t* pool, cudaStream_t s, bool pdl);
+// Rows of the slots of a 4-bit pool (-1: left out) as f16 pools [n / 16][n_kv][16][head_dim], n a multiple of 16.
+int kv4_read_blocks_launch(const uint8_t* pool, const long long* slots, long long n, int n_kv, int head_dim,
+                           long long num_blocks, __half* k, __half* v, cudaStream_t s);
 
 // ---------------------------------------------------------------- persistent decode step
 // The whole step of a small batch as one cooperative kernel (one CTA per SM); see

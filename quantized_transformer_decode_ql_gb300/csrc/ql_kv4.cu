@@ -104,8 +104,9 @@ __device__ __forceinline__ void put8(float* o, const uint32_t (&c)[2], __half d,
 // those 8 elements lie in 8 units: each lane loads one word (a unit's two blocks), and the 8 lanes of a
 // pair of blocks transpose their 8 words of 8 codes by three exchanges (halves, bytes, nibbles). A warp's
 // life is two round trips (slots, records), so a thread takes two rows at once.
+// BLOCKS: row i goes to slot i % 16 of block i / 16 of a pool [blocks][n_kv][16][HD] instead.
 constexpr int kReadRows = 2;
-template <int HD, typename T>
+template <int HD, typename T, bool BLOCKS>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __restrict__ pool,
                                                                const long long* __restrict__ slots, long long n,
                                                                long long num_blocks, T* __restrict__ k,
@@ -153,9 +154,106 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __
         const uint32_t even = z & 0x0f0f0f0fu, odd = (z >> 4) & 0x0f0f0f0fu;
         const uint32_t cv[2] = {__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362)};
         const long long i = i0 + r * ROWS;
-        put8(k + i * ks + (size_t)g * HD + 32 * b + 8 * w, ck, dk[r], mk[r]);
-        put8(v + i * vs + (size_t)g * HD + 32 * b + 8 * w, cv, dv[r], mv[r]);
+        const long long at = 32 * b + 8 * w + (BLOCKS ? ((i >> 4) * gridDim.y + g) * (16ll * HD) + (i & 15) * HD : (long long)g * HD);
+        put8(k + (BLOCKS ? 0 : i * ks) + at, ck, dk[r], mk[r]);
+        put8(v + (BLOCKS ? 0 : i * vs) + at, cv, dv[r], mv[r]);
     }
+}
+
+// The decode step's q and new K / V rows: per-head RMSNorm and NeoX rotation (pairs i, i + HD / 2) of the f32
+// q | k | v projection, q to f16, the key row and the value row of a kv head quantised into the pool at the
+// position's slot. As in the writer, HD / 8 lanes share a head, a lane holding 8 elements; it loads their
+// rotation partners too, which are another lane's.
+struct Kv4RopeParams {
+    const float* qkv;
+    const float* q_norm;
+    const float* k_norm;
+    const float* cos_t;
+    const float* sin_t;
+    const int32_t* positions;
+    const int32_t* active;
+    const int32_t* block_tables;
+    float eps;
+    int n_heads, n_kv;
+    long long items, maxb, num_blocks, max_position;
+    __half* q_out;
+    uint8_t* pool;
+};
+template <int HD>
+__global__ void __launch_bounds__(kKv4Threads) kv4_norm_rope_kernel(Kv4RopeParams p, DevError* err) {
+    using R = Kv4<HD>;
+    constexpr int H2 = HD / 2;
+    const long long item = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) / R::LANES;
+    const int l = threadIdx.x % R::LANES, b = l >> 2, j = l & 3;
+    pdl_wait();
+    pdl_trigger();
+    const int heads = p.n_heads + p.n_kv;
+    const bool in = item < p.items;   // all lanes take part in the shuffles
+    const long long t = in ? item / heads : 0;
+    const int h = in ? (int)(item - t * heads) : 0;
+    const bool act = in && (p.active == nullptr || p.active[t] != 0);
+    const int pos = act ? p.positions[t] : 0;
+    const bool ok = act && pos >= 0 && pos < p.max_position;
+    if (act && !ok && h == 0 && l == 0) record_device_error(err, kErrRopePosition, t, pos);
+    const bool is_q = h < p.n_heads;
+    const float* src = p.qkv + (t * (p.n_heads + 2 * p.n_kv) + h) * HD;
+    const float* w = is_q ? p.q_norm : p.k_norm;
+    const float* c = p.cos_t + (size_t)(ok ? pos : 0) * H2;
+    const float* s = p.sin_t + (size_t)(ok ? pos : 0) * H2;
+    // elements e, e + 1, ... of this lane's two quads and their partners
+    const int e0 = 32 * b + 4 * j;
+    const bool low = e0 < H2;
+    float x[8], y[8];
+    float ss = 0.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int e = e0 + 16 * q, o = low ? e + H2 : e - H2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[4 * q + i] = ok ? __ldcg(src + e + i) : 0.f;
+            y[4 * q + i] = ok ? __ldcg(src + o + i) : 0.f;
+            ss = fmaf(x[4 * q + i], x[4 * q + i], ss);
+        }
+    }
+#pragma unroll
+    for (int o = R::LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(fmaf(ss, 1.0f / (float)HD, p.eps));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int e = e0 + 16 * q, o = low ? e + H2 : e - H2, a = low ? e : o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float xn = x[4 * q + i] * r * __ldg(w + e + i), yn = y[4 * q + i] * r * __ldg(w + o + i);
+            const float cc = __ldg(c + a + i), sn = __ldg(s + a + i);
+            x[4 * q + i] = low ? xn * cc - yn * sn : yn * sn + xn * cc;
+        }
+    }
+    if (ok && is_q) {
+        __half* qo = p.q_out + (t * p.n_heads + h) * HD;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const __half2 a = __floats2half2_rn(x[4 * q], x[4 * q + 1]), d = __floats2half2_rn(x[4 * q + 2], x[4 * q + 3]);
+            *reinterpret_cast<uint2*>(qo + e0 + 16 * q) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&d));
+        }
+    }
+    const int g = h - p.n_heads;
+    const long long lb = pos >> 4;
+    const int phys = ok && !is_q ? p.block_tables[t * p.maxb + lb] : -1;   // max_position is 16 maxb at most
+    const bool live = phys >= 0 && phys < p.num_blocks;
+    if (ok && !is_q && !live && l == 0) record_device_error(err, kErrRopeBlock, t * p.maxb + lb, phys);
+    float v[8] = {};
+    if (live) {
+        const float* vs = src + (size_t)p.n_kv * HD + 32 * b + 2 * j;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = __ldcg(vs + 8 * q);
+            v[4 + q] = __ldcg(vs + 8 * q + 1);
+        }
+    }
+    uint8_t* rec = p.pool + ((size_t)(live ? phys : 0) * p.n_kv + (live ? g : 0)) * R::BYTES;
+    const int fault = kv4_put_rows<HD>(x, v, rec, pos & 15, b, j, live);
+    if (live && fault) record_device_error(err, fault == 2 ? kErrKvNonFinite : kErrKvOverflow, t, g);
 }
 
 // The checks that the writer and the reader share; `grid` for n > 0, each CTA `times` as many rows as its threads hold.
@@ -184,6 +282,48 @@ int kv4_rows_check(const char* name, const void* k, const void* v, int dtype, in
 }
 
 }  // namespace
+
+int kv4_norm_rope_launch(const RopeArgs& a, uint8_t* pool, cudaStream_t s, bool pdl) {
+    DevError* err = device_error_record();
+    if (!err) return set_error(QL_ECUDA, "4-bit norm_rope: no device error record");
+    Kv4RopeParams p = {};
+    p.qkv = a.qkv;
+    p.q_norm = a.q_norm;
+    p.k_norm = a.k_norm;
+    p.cos_t = a.cos_t;
+    p.sin_t = a.sin_t;
+    p.positions = a.positions;
+    p.active = a.active;
+    p.block_tables = a.block_tables;
+    p.eps = a.eps;
+    p.n_heads = a.n_heads;
+    p.n_kv = a.n_kv_heads;
+    p.items = (long long)a.batch * (a.n_heads + a.n_kv_heads);
+    p.maxb = a.max_blocks_per_seq;
+    p.num_blocks = a.num_blocks;
+    p.max_position = a.max_position;
+    p.q_out = a.q_out;
+    p.pool = pool;
+    const long long grid = (p.items * (a.head_dim / 8) + kKv4Threads - 1) / kKv4Threads;
+    const cudaError_t e = a.head_dim == 128
+                              ? launch(kv4_norm_rope_kernel<128>, dim3((unsigned)grid), dim3(kKv4Threads), 0, s, pdl, p, err)
+                              : launch(kv4_norm_rope_kernel<64>, dim3((unsigned)grid), dim3(kKv4Threads), 0, s, pdl, p, err);
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "4-bit norm_rope launch");
+}
+
+int kv4_read_blocks_launch(const uint8_t* pool, const long long* slots, long long n, int n_kv, int head_dim, long long num_blocks,
+                           __half* k, __half* v, cudaStream_t s) {
+    DevError* err = device_error_record();
+    if (!err) return set_error(QL_ECUDA, "4-bit read: no device error record");
+    const long long rows = kReadRows * kKv4Threads / (head_dim / 8);
+    const dim3 grid((unsigned)((n + rows - 1) / rows), (unsigned)n_kv);
+    auto go = [&](auto kernel) {
+        return launch(kernel, grid, dim3(kKv4Threads), 0, s, false, pool, slots, n, num_blocks, k, v, 0ll, 0ll, err);
+    };
+    const cudaError_t e = head_dim == 128 ? go(kv4_read_kernel<128, __half, true>) : go(kv4_read_kernel<64, __half, true>);
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "4-bit read launch");
+}
+
 }  // namespace ql
 
 extern "C" int64_t ql_kv4_record_bytes(int head_dim) {
@@ -235,9 +375,9 @@ extern "C" int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n
                       static_cast<T*>(d_v), (long long)k_stride, (long long)v_stride, err);
     };
     const bool f32 = dtype == QL_DTYPE_F32;
-    const cudaError_t e = head_dim == 128 ? (f32 ? go(kv4_read_kernel<128, float>, 0.f)
-                                                 : go(kv4_read_kernel<128, __half>, __half()))
-                                          : (f32 ? go(kv4_read_kernel<64, float>, 0.f)
-                                                 : go(kv4_read_kernel<64, __half>, __half()));
+    const cudaError_t e = head_dim == 128 ? (f32 ? go(kv4_read_kernel<128, float, false>, 0.f)
+                                                 : go(kv4_read_kernel<128, __half, false>, __half()))
+                                          : (f32 ? go(kv4_read_kernel<64, float, false>, 0.f)
+                                                 : go(kv4_read_kernel<64, __half, false>, __half()));
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_kv4_read");
 }

@@ -30,6 +30,8 @@
 #include "ql_batched.h"
 #include "ql_chunk_attn.h"
 #include "ql_internal.h"
+#include "ql_kv4_attn.h"
+#include "ql_sample.h"
 
 struct ql_model {
     ql_model_desc d;
@@ -92,6 +94,18 @@ struct ql_model {
     int32_t* plen = nullptr;     // [max_batch]
     void* cws = nullptr;         // prefill chunk attention: the splits' partials
     size_t cws_bytes = 0;
+    // 4-bit KV (kv_format QL_KV_Q4_1): the attention's workspace; for prefill chunks one layer's context read
+    // back as f16 blocks in order, with its slots and the table of that order
+    void* k4_ws = nullptr;
+    size_t k4_ws_bytes = 0;
+    long long* k4_slots = nullptr;   // [max_blocks_per_seq * 16]
+    int32_t* k4_order = nullptr;     // [max_blocks_per_seq]: 0, 1, 2, ...
+    __half* k4_k = nullptr;          // [max_blocks_per_seq][n_kv][16][hd]
+    __half* k4_v = nullptr;
+    // sampling of the decode step (ql_model_set_sampling); greedy without
+    bool sampling = false;
+    ql_sampling sample = {};
+    int32_t* stok = nullptr;         // [maxB]: the drawn tokens
     void* gws = nullptr;         // prefill GEMM: the K parts' sums of matrices with few row blocks
     size_t gws_bytes = 0;
 };
@@ -120,15 +134,14 @@ __global__ void embed_kernel(const float* __restrict__ E, const int32_t* __restr
 
 __global__ void finalize_kernel(unsigned long long* keys, const int32_t* active, int32_t* positions,
                                 int32_t* next_tokens, int32_t* out_tokens, long long out_stride,
-                                float* logits_dummy, int batch) {
-    (void)logits_dummy;
+                                const int32_t* drawn, int batch) {
     pdl_wait();
     pdl_trigger();
     for (int b = threadIdx.x; b < batch; b += blockDim.x) {
         const unsigned long long k = keys[b];
         keys[b] = 0ull;
         if (active && active[b] == 0) continue;
-        const int tok = (int)(0xFFFFFFFFu - (uint32_t)(k & 0xFFFFFFFFull));
+        const int tok = drawn ? drawn[b] : (int)(0xFFFFFFFFu - (uint32_t)(k & 0xFFFFFFFFull));
         const int pos = positions[b];
         next_tokens[b] = tok;
         if (out_tokens && pos + 1 >= 0 && pos + 1 < out_stride)
@@ -139,11 +152,15 @@ __global__ void finalize_kernel(unsigned long long* keys, const int32_t* active,
 
 // Chunked prefill: token t of the chunk sits at position p0 + t (p0 = *position) and attends
 // to positions 0 .. p0 + t; every token uses the sequence's block table row.
+// slots (4-bit KV, else null): the pool slot of every position up to the chunk's last, -1 behind it.
 __global__ void prefill_setup_kernel(const int32_t* position, const int32_t* block_table, int maxb, int T,
-                                     int32_t* bt, int32_t* pos, int32_t* len) {
+                                     int32_t* bt, int32_t* pos, int32_t* len, long long* slots) {
     pdl_wait();
     pdl_trigger();
     const int p0 = *position;
+    if (slots != nullptr)
+        for (long long i = threadIdx.x; i < 16ll * maxb; i += blockDim.x)
+            slots[i] = i < (long long)p0 + T ? (long long)block_table[i >> 4] * 16 + (i & 15) : -1;
     for (int i = threadIdx.x; i < T * maxb; i += blockDim.x) bt[i] = block_table[i % maxb];
     for (int t = threadIdx.x; t < T; t += blockDim.x) {
         pos[t] = p0 + t;
@@ -255,13 +272,81 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
         return set_error(QL_EINVAL, "decode step: routed experts decode at batch 1");
     if (m->d.num_experts > 0 && m->hmats.empty())
         return set_error(QL_EINVAL, "decode step: routed experts need the tile stream copies (matrix widths multiples of 128)");
+    if (m->step_kernel == QL_STEP_PERSISTENT && m->sampling)
+        return set_error(QL_EINVAL, "decode step: the persistent step kernel takes the arg max only");
     if (m->step_kernel == QL_STEP_PERSISTENT) return run_persist(m, a, s);
     const bool pdl = true;
     const int hd = (int)d.head_dim, nh = (int)d.n_heads, nkv = (int)d.n_kv_heads;
     const size_t layer_pool = (size_t)d.num_blocks * nkv * d.block_size * hd;
     const bool kvq = d.kv_format == QL_KV_Q8_0_Q5_1;
     const size_t kvq_layer = (size_t)d.num_blocks * nkv * (size_t)ql_kvq_record_bytes(hd);
+    const bool kv4 = d.kv_format == QL_KV_Q4_1;
     int rc;
+    // 4-bit KV: q normalised and rotated, the new rows quantised into layer li's pool, then the attention over it
+    auto attend4 = [&](int li, const ql_layer_desc& L) -> int {
+        RopeArgs ra = {};
+        ra.qkv = m->qkv;
+        ra.q_norm = L.q_norm;
+        ra.k_norm = L.k_norm;
+        ra.cos_t = m->cos_t;
+        ra.sin_t = m->sin_t;
+        ra.positions = a->positions;
+        ra.active = a->active;
+        ra.eps = d.eps;
+        ra.batch = B;
+        ra.n_heads = nh;
+        ra.n_kv_heads = nkv;
+        ra.head_dim = hd;
+        ra.q_out = m->q16;
+        ra.block_tables = a->block_tables;
+        ra.max_blocks_per_seq = d.max_blocks_per_seq;
+        ra.num_blocks = d.num_blocks;
+        ra.max_position = d.max_blocks_per_seq * d.block_size;
+        uint8_t* pool = static_cast<uint8_t*>(d.kvq_pool) + (size_t)d.num_blocks * nkv * (size_t)ql_kv4_record_bytes(hd) * li;
+        if (int rc4 = kv4_norm_rope_launch(ra, pool, s, pdl)) return rc4;
+        Kv4AttnArgs ka = {};
+        ka.q = m->q16;
+        ka.pool = pool;
+        ka.block_tables = a->block_tables;
+        ka.positions = a->positions;
+        ka.active = a->active;
+        ka.batch = B;
+        ka.n_heads = nh;
+        ka.n_kv_heads = nkv;
+        ka.head_dim = hd;
+        ka.max_blocks_per_seq = d.max_blocks_per_seq;
+        ka.num_blocks = d.num_blocks;
+        ka.scale = 1.0f / sqrtf((float)hd);
+        ka.out = m->attn;
+        ka.workspace = m->k4_ws;
+        ka.workspace_bytes = m->k4_ws_bytes;
+        return kv4_attn_launch(ka, s, pdl);
+    };
+    // the step's end: the drawn tokens (or the arg max of the lm_head's keys), positions advanced
+    auto finish = [&]() -> int {
+        if (m->sampling) {
+            SampleArgs sa = {};
+            sa.logits = a->logits ? a->logits : m->logits;
+            sa.dtype = QL_DTYPE_F32;
+            sa.row_stride = d.vocab;
+            sa.batch = B;
+            sa.vocab = d.vocab;
+            sa.temperature = m->sample.temperature;
+            sa.top_k = m->sample.top_k;
+            sa.top_p = m->sample.top_p;
+            sa.min_p = m->sample.min_p;
+            sa.uniform = m->sample.uniform;
+            sa.uniform_stride = m->sample.uniform_stride;
+            sa.positions = a->positions;
+            sa.active = a->active;
+            sa.tokens = m->stok;
+            if (int rcs = sample_launch(sa, s, pdl)) return rcs;
+        }
+        const cudaError_t ef = launch(finalize_kernel, dim3(1), dim3(64), 0, s, pdl, m->keys, a->active, a->positions,
+                                      a->next_tokens, a->out_tokens, (long long)a->out_stride,
+                                      (const int32_t*)(m->sampling ? m->stok : nullptr), B);
+        return ef == cudaSuccess ? QL_OK : cuda_error(ef, "finalize launch");
+    };
 
     // Each kernel asks L2 to fetch the weights of a GEMV that follows it, so that HBM keeps
     // streaming weights through kernel boundaries, launches and the small kernels:
@@ -346,7 +431,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
             at.eps = d.eps;
             at.max_position = d.max_blocks_per_seq * d.block_size;
             if (kvq) at.kvq = static_cast<uint8_t*>(d.kvq_pool) + kvq_layer * li;
-            else {
+            else if (!kv4) {
                 at.k_pool = static_cast<__half*>(d.k_pool) + layer_pool * li;
                 at.v_pool = static_cast<__half*>(d.v_pool) + layer_pool * li;
             }
@@ -368,7 +453,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
                 at.trace = m->trace + (size_t)(4 * d.n_layers + 1 + li) * num_sms() * persist_trace_words();
                 at.trace_ctas = num_sms();
             }
-            if ((rc = attn_launch(at, s, pdl)) != QL_OK) return rc;
+            if ((rc = kv4 ? attend4(li, L) : attn_launch(at, s, pdl)) != QL_OK) return rc;
             // the o GEMV leaves out one SM per attention merge (one CTA per sequence and kv head
             // merges the splits, ending after the others): every o CTA then starts on an SM
             // freed early, while the CTA with the most tiles keeps the same count
@@ -440,7 +525,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
         at.eps = d.eps;
         at.max_position = d.max_blocks_per_seq * d.block_size;
         if (kvq) at.kvq = static_cast<uint8_t*>(d.kvq_pool) + kvq_layer * li;
-        else {
+        else if (!kv4) {
             at.k_pool = static_cast<__half*>(d.k_pool) + layer_pool * li;
             at.v_pool = static_cast<__half*>(d.v_pool) + layer_pool * li;
         }
@@ -459,7 +544,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
         at.out = m->attn;
         at.workspace = m->attn_ws;
         at.workspace_bytes = m->attn_ws_bytes;
-        if ((rc = attn_launch(at, s, pdl)) != QL_OK) return rc;
+        if ((rc = kv4 ? attend4(li, L) : attn_launch(at, s, pdl)) != QL_OK) return rc;
 
         GemvArgs go = {};
         go.batch = B;
@@ -515,10 +600,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
                      a->logits ? a->logits : m->logits, (int)d.vocab, first_norm, 0,
                      fold_lm ? m->ssq : nullptr)) != QL_OK)
             return rc;
-        e = launch(finalize_kernel, dim3(1), dim3(64), 0, s, pdl, m->keys, a->active, a->positions,
-                   a->next_tokens, a->out_tokens, (long long)a->out_stride, (float*)nullptr, B);
-        if (e != cudaSuccess) return cuda_error(e, "finalize launch");
-        return QL_OK;
+        return finish();
     }
     GemvArgs gl = {};
     gl.batch = B;
@@ -537,10 +619,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
     gl.active = a->active;
     if ((rc = gemv_launch(gl, s, pdl)) != QL_OK) return rc;
 
-    e = launch(finalize_kernel, dim3(1), dim3(64), 0, s, pdl, m->keys, a->active, a->positions,
-               a->next_tokens, a->out_tokens, (long long)a->out_stride, (float*)nullptr, B);
-    if (e != cudaSuccess) return cuda_error(e, "finalize launch");
-    return QL_OK;
+    return finish();
 }
 
 // A chunk of T prompt tokens of one sequence through every layer together: the step's GEMVs at
@@ -555,9 +634,10 @@ int run_prefill(ql_model* m, const int32_t* tokens, int T, int32_t* position, co
     const int hd = (int)d.head_dim, nh = (int)d.n_heads, nkv = (int)d.n_kv_heads;
     const size_t layer_pool = (size_t)d.num_blocks * nkv * d.block_size * hd;
     const int maxb = (int)d.max_blocks_per_seq;
+    const bool kv4 = d.kv_format == QL_KV_Q4_1;
     int rc;
     cudaError_t e = launch(prefill_setup_kernel, dim3(1), dim3(256), 0, s, pdl, position, block_table, maxb, T, m->pbt,
-                           m->ppos, m->plen);
+                           m->ppos, m->plen, m->k4_slots);
     if (e != cudaSuccess) return cuda_error(e, "prefill setup launch");
     const NextWeights none = {{nullptr, nullptr}, {0, 0}};
     e = launch(embed_kernel, dim3(T), dim3(256), 0, s, pdl, d.embed, tokens, (const int32_t*)nullptr, m->x,
@@ -620,27 +700,38 @@ int run_prefill(ql_model* m, const int32_t* tokens, int T, int32_t* position, co
         ra.n_kv_heads = nkv;
         ra.head_dim = hd;
         ra.q_out = m->q16;
-        ra.k_pool = static_cast<__half*>(d.k_pool) + layer_pool * li;
-        ra.v_pool = static_cast<__half*>(d.v_pool) + layer_pool * li;
+        ra.k_pool = kv4 ? nullptr : static_cast<__half*>(d.k_pool) + layer_pool * li;
+        ra.v_pool = kv4 ? nullptr : static_cast<__half*>(d.v_pool) + layer_pool * li;
         ra.block_tables = m->pbt;
         ra.max_blocks_per_seq = maxb;
         ra.block_size = d.block_size;
         ra.num_blocks = d.num_blocks;
         ra.max_position = d.max_blocks_per_seq * d.block_size;
-        if ((rc = rope_launch(ra, s, pdl)) != QL_OK) return rc;
         // the chunk's T tokens against the cache in one pass (each K/V block read once)
         ChunkAttnArgs ca = {};
         ca.q = m->q16;
-        ca.k_pool = ra.k_pool;
-        ca.v_pool = ra.v_pool;
-        ca.block_table = m->pbt;   // row 0: the sequence's table
+        if (kv4) {
+            // the rows quantised as the decode step does, then the context's values read back as f16 blocks
+            uint8_t* pool = static_cast<uint8_t*>(d.kvq_pool) + (size_t)d.num_blocks * nkv * (size_t)ql_kv4_record_bytes(hd) * li;
+            if ((rc = kv4_norm_rope_launch(ra, pool, s, pdl)) != QL_OK) return rc;
+            if ((rc = kv4_read_blocks_launch(pool, m->k4_slots, 16ll * maxb, nkv, hd, d.num_blocks, m->k4_k, m->k4_v, s)) != QL_OK)
+                return rc;
+            ca.k_pool = m->k4_k;
+            ca.v_pool = m->k4_v;
+            ca.block_table = m->k4_order;
+        } else {
+            if ((rc = rope_launch(ra, s, pdl)) != QL_OK) return rc;
+            ca.k_pool = ra.k_pool;
+            ca.v_pool = ra.v_pool;
+            ca.block_table = m->pbt;   // row 0: the sequence's table
+        }
         ca.position = m->ppos;     // [0] = the chunk's first position
         ca.T = T;
         ca.n_heads = nh;
         ca.n_kv_heads = nkv;
         ca.head_dim = hd;
         ca.max_blocks_per_seq = maxb;
-        ca.num_blocks = (int)d.num_blocks;
+        ca.num_blocks = kv4 ? maxb : (int)d.num_blocks;
         ca.scale = 1.0f / sqrtf((float)hd);
         ca.out = m->attn;
         ca.workspace = m->cws;
@@ -852,9 +943,10 @@ extern "C" int ql_model_create(const ql_model_desc* desc, ql_model** out) {
     QL_REQUIRE((d.n_heads * d.head_dim) % 32 == 0, "ql_model_create: n_heads*head_dim must be a multiple of 32");
     QL_REQUIRE(d.vocab > 0 && d.embed && d.final_norm, "ql_model_create: need vocab, embed, final_norm");
     QL_REQUIRE(d.block_size == 16, "ql_model_create: block_size must be 16");
-    QL_REQUIRE(d.kv_format == QL_KV_F16 || d.kv_format == QL_KV_Q8_0_Q5_1, "ql_model_create: unknown kv_format");
+    QL_REQUIRE(d.kv_format == QL_KV_F16 || d.kv_format == QL_KV_Q8_0_Q5_1 || d.kv_format == QL_KV_Q4_1,
+               "ql_model_create: unknown kv_format");
     QL_REQUIRE(d.num_blocks > 0 && (d.kv_format == QL_KV_F16 ? (d.k_pool && d.v_pool) : d.kvq_pool != nullptr),
-               "ql_model_create: need KV pools (k_pool and v_pool, or kvq_pool for the quantised format)");
+               "ql_model_create: need KV pools (k_pool and v_pool, or kvq_pool for the quantised formats)");
     QL_REQUIRE(d.kv_format == QL_KV_F16 || (reinterpret_cast<uintptr_t>(d.kvq_pool) & 15) == 0,
                "ql_model_create: kvq_pool must be 16-byte aligned");
     QL_REQUIRE(d.max_batch >= 1 && d.max_batch <= 4096, "ql_model_create: max_batch out of range");
@@ -920,6 +1012,24 @@ extern "C" int ql_model_create(const ql_model_desc* desc, ql_model** out) {
         if (rc == QL_OK && cudaMemset(m->meidx, 0, d.topk * 4) != cudaSuccess) rc = set_error(QL_ECUDA, "ql_model_create: memset");
     }
     A((void**)&m->logits, B * d.vocab * 4);
+    A((void**)&m->stok, B * 4);
+    if (d.kv_format == QL_KV_Q4_1) {
+        m->k4_ws_bytes = kv4_attn_workspace_bytes();
+        A(&m->k4_ws, m->k4_ws_bytes);
+        if (rc == QL_OK && cudaMemset(m->k4_ws, 0, m->k4_ws_bytes) != cudaSuccess) rc = set_error(QL_ECUDA, "ql_model_create: memset");
+        if (d.num_experts == 0) {   // prefill chunks
+            const size_t rows = (size_t)max_pos * d.n_kv_heads * d.head_dim * 2;
+            A((void**)&m->k4_slots, max_pos * 8);
+            A((void**)&m->k4_order, d.max_blocks_per_seq * 4);
+            A((void**)&m->k4_k, rows);
+            A((void**)&m->k4_v, rows);
+            std::vector<int32_t> order(d.max_blocks_per_seq);
+            for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
+            if (rc == QL_OK && (cudaMemcpy(m->k4_order, order.data(), order.size() * 4, cudaMemcpyHostToDevice) != cudaSuccess ||
+                                cudaMemset(m->k4_k, 0, rows) != cudaSuccess || cudaMemset(m->k4_v, 0, rows) != cudaSuccess))
+                rc = set_error(QL_ECUDA, "ql_model_create: 4-bit prefill buffers");
+        }
+    }
     A((void**)&m->keys, B * 8);
     A((void**)&m->cos_t, max_pos * (d.head_dim / 2) * 4);
     A((void**)&m->sin_t, max_pos * (d.head_dim / 2) * 4);
@@ -999,6 +1109,23 @@ extern "C" int ql_model_set_option(ql_model* m, int option, int64_t value) {
     }
 }
 
+extern "C" int ql_model_set_sampling(ql_model* m, const ql_sampling* sampling) {
+    if (!m) return set_error(QL_EINVAL, "ql_model_set_sampling: null model");
+    if (!sampling) {
+        m->sampling = false;
+        return QL_OK;
+    }
+    if (!sampling->uniform) return set_error(QL_EINVAL, "ql_model_set_sampling: uniform numbers are required");
+    if (sampling->uniform_stride < 1) return set_error(QL_EINVAL, "ql_model_set_sampling: uniform_stride must be at least 1");
+    if (m->d.vocab > kMaxSampleVocab) return set_error(QL_EINVAL, "ql_model_set_sampling: vocab above 360448");
+    auto a4 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3) == 0; };
+    if (!a4(sampling->temperature) || !a4(sampling->top_k) || !a4(sampling->top_p) || !a4(sampling->min_p) || !a4(sampling->uniform))
+        return set_error(QL_EINVAL, "ql_model_set_sampling: misaligned array");
+    m->sample = *sampling;
+    m->sampling = true;
+    return QL_OK;
+}
+
 extern "C" int64_t ql_model_persistent_max_batch(const ql_model* m) { return m ? m->persist_max_b : 0; }
 
 extern "C" int ql_decode_step(ql_model* m, const ql_step_args* args, void* stream) {
@@ -1011,8 +1138,8 @@ extern "C" int ql_prefill_chunk(ql_model* m, const int32_t* d_tokens, int64_t n_
                                 const int32_t* d_block_table, float* d_logits, int32_t* d_next_token, void* stream) {
     if (!m || !d_tokens || !d_position || !d_block_table) return set_error(QL_EINVAL, "ql_prefill_chunk: null pointer");
     const ql_model_desc& d = m->d;
-    if (d.num_experts > 0 || d.kv_format != QL_KV_F16)
-        return set_error(QL_EINVAL, "ql_prefill_chunk: dense models with the f16 KV cache only");
+    if (d.num_experts > 0 || d.kv_format == QL_KV_Q8_0_Q5_1)
+        return set_error(QL_EINVAL, "ql_prefill_chunk: dense models with the f16 or the 4-bit KV cache only");
     if (n_tokens < 1 || n_tokens > kPrefillMax || n_tokens > d.max_batch)
         return set_error(QL_EINVAL, "ql_prefill_chunk: n_tokens must be in [1, min(256, max_batch)]");
     if (m->hmats.empty() || (n_tokens > kPersistMaxBatch && n_tokens <= kPrefillGemvMax && !m->batched_ok))

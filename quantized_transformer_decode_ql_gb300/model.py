@@ -11,7 +11,8 @@ import ctypes
 
 import torch
 
-from ._lib import (LayerDesc, ModelDesc, Q4Matrix, QL_KV_F16, StepArgs, check, lib, ptr, stream_ptr)
+from ._lib import (LayerDesc, ModelDesc, Q4Matrix, QL_DTYPE_F32, QL_KV_F16, QL_KV_Q4_1, Sampling, StepArgs, check, lib, ptr,
+                   stream_ptr)
 
 BLOCK = 16
 
@@ -85,7 +86,7 @@ class DeviceModel:
 
     def _alloc_pools(self):
         """KV pools: f16 K and V [n_layers, num_blocks, n_kv, 16, hd], or the quantised records
-        [n_layers, num_blocks, n_kv, ql_kvq_record_bytes(hd)] (u8)."""
+        [n_layers, num_blocks, n_kv, ql_kvq_record_bytes(hd) or ql_kv4_record_bytes(hd)] (u8)."""
         cfg = self.cfg
         if self.kv_format == QL_KV_F16:
             shape = (cfg.n_layers, self.num_blocks, cfg.n_kv_heads, BLOCK, cfg.head_dim)
@@ -93,7 +94,8 @@ class DeviceModel:
             self.v_pool = torch.zeros(shape, dtype=torch.float16, device=self.device)
             self.kvq_pool = None
         else:
-            rec = int(lib().ql_kvq_record_bytes(cfg.head_dim))
+            size = lib().ql_kv4_record_bytes if self.kv_format == QL_KV_Q4_1 else lib().ql_kvq_record_bytes
+            rec = int(size(cfg.head_dim))
             self.k_pool = self.v_pool = None
             self.kvq_pool = torch.zeros((cfg.n_layers, self.num_blocks, cfg.n_kv_heads, rec), dtype=torch.uint8,
                                         device=self.device)
@@ -204,6 +206,18 @@ class DeviceModel:
     def ql_model_set_option(self, option: int, value: int):
         check(lib().ql_model_set_option(self.handle, option, value))
 
+    def ql_model_set_sampling(self, uniform=None, temperature=None, top_k=None, top_p=None, min_p=None):
+        """Decode steps issued (or graphs captured) from now on draw their next tokens with the device tensors
+        ``uniform`` (f32 [batch] or [batch, numbers]: one per position in turn), ``temperature``, ``top_p``,
+        ``min_p`` (f32 [batch]) and ``top_k`` (int32 [batch]); without ``uniform`` they take the arg max again."""
+        self._sampling_tensors = (uniform, temperature, top_k, top_p, min_p)   # the steps read them
+        if uniform is None:
+            check(lib().ql_model_set_sampling(self.handle, None))
+            return
+        s = Sampling(ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(uniform),
+                     uniform.shape[1] if uniform.dim() == 2 else 1)
+        check(lib().ql_model_set_sampling(self.handle, ctypes.byref(s)))
+
     def ql_model_persistent_max_batch(self) -> int:
         return int(lib().ql_model_persistent_max_batch(self.handle))
 
@@ -236,7 +250,7 @@ class DeviceModel:
     def write_context(self, slot_blocks, k_ctx, v_ctx):
         """Place a pre-filled context ``[n_layers, n_kv, n_pos, hd]`` into the pools through a
         slot's block list (stands in for prefill): f16 pools take the values as f16; the quantised
-        pool takes them quantised on the device (``ql_kvq_write``, per layer)."""
+        pools take them quantised on the device (``ql_kvq_write`` or ``ql_kv4_write``, per layer)."""
         n = k_ctx.shape[2]
         if self.kv_format != QL_KV_F16:
             cfg = self.cfg
@@ -246,8 +260,13 @@ class DeviceModel:
             for li in range(cfg.n_layers):
                 kl = torch.as_tensor(k_ctx[li], device=self.device).float().permute(1, 0, 2).contiguous()
                 vl = torch.as_tensor(v_ctx[li], device=self.device).float().permute(1, 0, 2).contiguous()
-                check(lib().ql_kvq_write(ptr(kl), ptr(vl), ptr(slots), n, cfg.n_kv_heads, cfg.head_dim,
-                                         ptr(self.kvq_pool[li]), self.num_blocks, stream_ptr(None)))
+                if self.kv_format == QL_KV_Q4_1:
+                    row = cfg.n_kv_heads * cfg.head_dim
+                    check(lib().ql_kv4_write(ptr(kl), ptr(vl), QL_DTYPE_F32, row, row, ptr(slots), n, cfg.n_kv_heads,
+                                             cfg.head_dim, ptr(self.kvq_pool[li]), self.num_blocks, stream_ptr(None)))
+                else:
+                    check(lib().ql_kvq_write(ptr(kl), ptr(vl), ptr(slots), n, cfg.n_kv_heads, cfg.head_dim,
+                                             ptr(self.kvq_pool[li]), self.num_blocks, stream_ptr(None)))
             return
         kc = torch.as_tensor(k_ctx, dtype=torch.float16, device=self.device)
         vc = torch.as_tensor(v_ctx, dtype=torch.float16, device=self.device)
