@@ -40,6 +40,7 @@ constexpr int kStages = 4;                // tiles of a warp in flight
 constexpr int kCtasPerSm = 2;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
+constexpr int kSettle = 8;                // tiles of a warp between two settlings of the sums, a power of two
 constexpr int kNone = -0x7fffffff - 1;    // no tile left to copy
 
 constexpr size_t kSlotBytes = (size_t)(128 / 16 + 1) * 32 * sizeof(float4);   // a stored state at HD 128
@@ -175,6 +176,22 @@ struct State {
         }
         z[0] *= f0;
         z[1] *= f1;
+    }
+    // The minima's sums move to the value sums. Codes are not negative, so both grow where the values they
+    // stand for cancel; the matrix unit truncates what it adds, by more the larger the sum.
+    __device__ __forceinline__ void settle(int lane) {
+#pragma unroll
+        for (int b = 0; b < HD / 32; ++b) {
+            const float z0 = __shfl_sync(0xffffffffu, z[0], 4 * b + (lane & 3)), z1 = __shfl_sync(0xffffffffu, z[1], 4 * b + (lane & 3));
+#pragma unroll
+            for (int i = 2 * b; i < 2 * b + 2; ++i) {
+                o[i][0] = fmaf(z0, 0x1p-24f, o[i][0]);
+                o[i][1] = fmaf(z1, 0x1p-24f, o[i][1]);
+                o[i][2] = fmaf(z0, 0x1p-20f, o[i][2]);
+                o[i][3] = fmaf(z1, 0x1p-20f, o[i][3]);
+            }
+        }
+        if (lane < HD / 8) z[0] = z[1] = 0.f;
     }
     // rows of float4 per lane: 0 .. HD / 16 - 1 the value sums, then minima's sums and references
     __device__ __forceinline__ void put(float4* to) const {
@@ -620,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 __syncwarp();   // every lane is done with the record
                 issue(old);
                 weigh(rec, blk, s);
+                if ((blk & (kSettle * kWarps - kWarps)) == 0) st.settle(lane);
             }
             value(rec);
             __syncwarp();
