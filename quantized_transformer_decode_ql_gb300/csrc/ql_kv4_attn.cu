@@ -41,7 +41,8 @@ constexpr int kCtasPerSm = 2;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
 constexpr int kSettle = 8;                // tiles of a warp between two settlings of the sums, a power of two
-constexpr int kNone = -0x7fffffff - 1;    // no tile left to copy
+constexpr int kEntry = 20;                // what a segment costs besides its tiles, in tiles (about 3 us; 10: 6% slower on ragged batches)
+constexpr int kLeast = 2 * kWarps;            // the shortest run of a CTA
 
 constexpr size_t kSlotBytes = (size_t)(128 / 16 + 1) * 32 * sizeof(float4);   // a stored state at HD 128
 
@@ -239,12 +240,16 @@ __device__ __forceinline__ int seq_len(const Params& p, int b) {
     return len < 0 || len > p.maxb * 16 ? 0 : (int)len;
 }
 
-// A segment: the tiles of one (sequence, kv head, chunk of heads) that lie in a CTA's run, numbers rel ..
-// of the run being tiles blk0 .. blk1 - 1 of the sequence's nb. The same in every lane.
+// A segment: the tiles blk0 .. blk1 - 1 (of nb) of one (sequence, kv head, chunk of heads) that lie in a
+// CTA's window of the list, the CTA's tiles rel and on. In the list a segment is kEntry places for entering
+// and leaving it, then its tiles; at: the place of tile 0 in the window (negative where the window starts
+// behind it). The same in every lane.
 struct Segment {
-    int b, s, len, nb, blk0, blk1, rel;
-    __device__ __forceinline__ void next(const Params& p, int S, int run) {
+    int b, s, len, nb, blk0, blk1, rel, at;
+    __device__ __forceinline__ bool last(int window) const { return at + nb + kEntry >= window; }
+    __device__ __forceinline__ void next(const Params& p, int S, int window) {
         rel += blk1 - blk0;
+        at += nb + kEntry;
         if (++s == S) {
             s = 0;
             do {
@@ -254,9 +259,17 @@ struct Segment {
             nb = (len + 15) >> 4;
         }
         blk0 = 0;
-        blk1 = min(nb, run - rel);
+        blk1 = min(nb, window - at);
     }
 };
+
+// a / b below 2^20, without the call that a division of 64 bits is
+__device__ __forceinline__ int quotient(long long a, long long b) {
+    int q = (int)__fdividef((float)a, (float)b);
+    while (q * b > a) --q;
+    while ((q + 1) * b <= a) ++q;
+    return q;
+}
 
 template <int HD, bool DUP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p, DevError* err) {
@@ -264,10 +277,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     using St = State<HD>;
     constexpr int NB = R::NB, MT = HD / 16, REC = R::BYTES, ROWS = (MT + 1) * 32;
     constexpr int STAGE = REC + 16;                          // a record and the barrier that its copy completes on
+    constexpr int MERGE = 9;                                 // parts loaded at a time
     static_assert(MT <= kWarps, "");
     extern __shared__ __align__(128) unsigned char smem[];   // [warp][stage], then 4 states
     __shared__ Segment ahead[kWarps];                        // where each warp's copies are
-    __shared__ int last_flag;
+    __shared__ struct {                                      // a part written: its CTAs, its (sequence, s)
+        int c0, c1, b, s;
+    } part[2];                                               // of the segment that the window starts in, of the one it ends in
+    __shared__ int complete[2];                              // the part was its segment's last
     const int tid = threadIdx.x;
     int lane;
     asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));       // kept in a register, not read again and again
@@ -297,21 +314,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             const long long l = p.context_lens ? (long long)p.context_lens[b] : (long long)p.positions[b] + 1;
             if (l != 0) record_device_error(err, kErrAttnLength, b, l);
         }
-        total += __reduce_add_sync(0xffffffffu, (len + 15) >> 4);
+        total += __reduce_add_sync(0xffffffffu, len > 0 ? kEntry + ((len + 15) >> 4) : 0);
     }
     total *= S;
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    per = per < kWarps ? kWarps : per;
-    const long long lo = blockIdx.x * per;
+    // the CTAs' windows: total / gridDim.x places, rounded up (by a little more where that is past 32 bits)
+    int per = (total >> 31) == 0 ? (int)(((uint32_t)total + gridDim.x - 1) / gridDim.x) : (int)__fdividef((float)total, (float)gridDim.x);
+    if ((total >> 31) != 0) per += (per >> 18) + 1;
+    per = max(per, kLeast);
+    const long long lo = (long long)blockIdx.x * per;
     if (lo >= total) return;
-    const int run = (int)(lo + per < total ? per : total - lo);
+    const int window = (int)(lo + per < total ? per : total - lo);
     Segment sg;
     {
         long long before = 0;
         for (int b0 = 0;; b0 += 32) {
             const int b = b0 + lane;
             const int len = b0 == 0 ? len0 : b < p.batch ? seq_len(p, b) : 0;
-            long long incl = (long long)((len + 15) >> 4) * S;
+            long long incl = (long long)(len > 0 ? kEntry + ((len + 15) >> 4) : 0) * S;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -323,10 +342,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 sg.b = b0 + l;
                 sg.len = __shfl_sync(0xffffffffu, len, l);
                 sg.nb = (sg.len + 15) >> 4;
-                const long long in = lo - (before + __shfl_sync(0xffffffffu, incl, l) - (long long)sg.nb * S);
-                sg.s = (int)(in / sg.nb);
-                sg.blk0 = (int)(in - (long long)sg.s * sg.nb);
-                sg.blk1 = (int)min((long long)sg.nb, (long long)sg.blk0 + run);
+                const long long in = lo - (before + __shfl_sync(0xffffffffu, incl, l) - (long long)(kEntry + sg.nb) * S);
+                sg.s = quotient(in, kEntry + sg.nb);
+                sg.at = kEntry - (int)(in - (long long)sg.s * (kEntry + sg.nb));
+                sg.blk0 = max(0, -sg.at);
+                sg.blk1 = min(sg.nb, window - sg.at);
                 sg.rel = 0;
                 break;
             }
@@ -334,49 +354,77 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         }
     }
 
+    if (sg.blk1 <= sg.blk0) return;   // no tile in the window
+
+    // ---- q's rows for the products' columns
+    uint2 qr[NB][2];
+    auto load_q = [&](const Segment& g) {
+        const int kv = p.chunks == 1 ? g.s : g.s / p.chunks, c = g.s - kv * p.chunks;
+        const int nh = min(kHeads, p.group - c * kHeads), h = DUP ? gq & 3 : gq;
+        const __half* src = p.q + ((size_t)g.b * p.n_heads + kv * p.group + c * kHeads + (h < nh ? h : 0)) * HD + 4 * tq;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            qr[b][0] = __ldg(reinterpret_cast<const uint2*>(src + 32 * b));
+            qr[b][1] = __ldg(reinterpret_cast<const uint2*>(src + 32 * b + 16));
+        }
+    };
+
     // ---- the ring: the tiles of this warp (numbers warp, warp + 8, ... of the run), in order
     int pblk, pend;                    // the next tile to copy and the end of its segment; pend 0: none left
-    const int32_t* prow;               // its sequence's block table
-    const uint8_t* ppool;              // the pool at its kv head
-    int phys = -1;                     // its block, loaded a tile ahead of the copy (kNone: no tile)
+    uint32_t pofs;                     // its kv head's place in a block
+    int ids, later;                    // block ids: lane l has that of the warp's tile with number 8 l + warp's part in pblk's 256; the next 256
     const uint32_t rec_stride = (uint32_t)p.n_kv * REC;
     const uint32_t elected = lane == 0;
     const unsigned long long policy = l2_evict_first();   // the context is read once per step
+    auto blocks = [&](int from) {
+        const int at = (from & ~(32 * kWarps - 1)) + kWarps * lane + (from & (kWarps - 1));
+        return at < pend ? __ldg(p.block_tables + (size_t)ahead[warp].b * p.maxb + at) : -1;
+    };
     auto enter = [&](const Segment& g) {   // the warp's first tile in segment g, if it has one
         pblk = g.blk0 + ((warp - g.rel) & (kWarps - 1));
         pend = g.blk1;
-        prow = p.block_tables + (size_t)g.b * p.maxb;
-        ppool = p.pool + (size_t)(p.chunks == 1 ? g.s : g.s / p.chunks) * REC;
+        pofs = (uint32_t)(p.chunks == 1 ? g.s : g.s / p.chunks) * REC;
+    };
+    auto look = [&]() {
+        const Segment& g = ahead[warp];   // its q rows on their way to L2
+        const int kv = p.chunks == 1 ? g.s : g.s / p.chunks, c = g.s - kv * p.chunks;
+        if (c * kHeads + (lane >> 2) < p.group)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                p.q + ((size_t)g.b * p.n_heads + kv * p.group + c * kHeads + (lane >> 2)) * HD + (lane & 3) * (HD / 4)));
+        ids = blocks(pblk);
+        later = blocks(pblk + 32 * kWarps);
     };
     auto cross = [&]() {               // past the segment's end: the next one with a tile of this warp
         Segment g = ahead[warp];
         do {
-            if (g.rel + g.blk1 - g.blk0 >= run) {
-                phys = kNone;
+            if (g.last(window)) {
+                pend = 0;
+                ids = -1;
                 return;
             }
-            g.next(p, S, run);
+            g.next(p, S, window);
             enter(g);
         } while (pblk >= pend);
         __syncwarp();
         if (lane == 0) ahead[warp] = g;
         __syncwarp();
-        phys = __ldg(prow + pblk);
+        look();
     };
     unsigned bad = 0;                  // stages without a record (a block id outside the pool, or a failed wait)
     bool dead = false;                 // a wait ran out: no more copies
-    // copy the tile whose block is loaded to the stage at rec, then load the next one's block
+    // copy the next tile to the stage at rec
     auto issue = [&](uint32_t rec) {
+        const int phys = __shfl_sync(0xffffffffu, ids, pblk / kWarps);
         const bool in = (unsigned)phys < (unsigned)p.num_blocks;
         if (in && bad == 0) {
             asm volatile(
                 "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
                 "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%2], [%3], %1, [%0], %4;\n}"
-                ::"r"(rec + REC), "r"(REC), "r"(rec), "l"(ppool + (size_t)(unsigned)phys * rec_stride), "l"(policy), "r"(elected)
+                ::"r"(rec + REC), "r"(REC), "r"(rec), "l"(p.pool + ((size_t)(unsigned)phys * rec_stride + pofs)), "l"(policy), "r"(elected)
                 : "memory");
         } else {
-            if (phys == kNone) return;
+            if (pend == 0) return;
             const unsigned bit = 1u << ((rec - ring) / STAGE);
             bad = in && !dead ? bad & ~bit : bad | bit;
             if (lane == 0) {
@@ -384,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(rec + REC), "r"(REC) : "memory");
                     asm volatile(
                         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                        "[%3], %4;" ::"r"(rec), "l"(ppool + (size_t)(unsigned)phys * rec_stride), "r"(REC), "r"(rec + REC), "l"(policy)
+                        "[%3], %4;" ::"r"(rec), "l"(p.pool + ((size_t)(unsigned)phys * rec_stride + pofs)), "r"(REC), "r"(rec + REC), "l"(policy)
                         : "memory");
                 } else {
                     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(rec + REC) : "memory");
@@ -394,13 +442,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             __syncwarp();
         }
         pblk += kWarps;
-        if (pblk < pend) phys = __ldg(prow + pblk);
-        else cross();
+        if (pblk >= pend) cross();
+        else if ((pblk & (31 * kWarps)) == 0) {
+            ids = later;
+            later = blocks(pblk + 32 * kWarps);
+        }
     };
     if (lane == 0) ahead[warp] = sg;
     __syncwarp();
     enter(sg);
-    if (pblk < pend) phys = __ldg(prow + pblk);
+    if (pblk < pend) look();
     else cross();
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) issue(ring + i * STAGE);
@@ -417,10 +468,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     const uint32_t offV = R::VC + tq * (HD / 2) + R::vunit(tq, gq);
     const uint32_t offVD = R::VD + tq * NB * 8, offVM = R::VM + tq * NB * 8 + 4 * (gq & (NB - 1));
 
+    // ---- the end of a segment: row w of the joined state (value sums of 16 elements) is warp w's
+    const bool has = warp < MT;
+    const int row = has ? warp : 0;
+    int parts = 0, arrival = 0;   // parts written (1: of the segment the window starts in, 2: of the one it ends in); the first's ticket (thread 0)
+    auto emit = [&](const Slice& sl, int b, int s) {
+        if (!has) return;
+        const int kv = p.chunks == 1 ? s : s / p.chunks, c = s - kv * p.chunks;
+        const int nh = min(kHeads, p.group - c * kHeads), hc = 2 * tq, eb = warp >> 1;
+        const float l0 = __shfl_sync(0xffffffffu, sl.t.x, 16 + tq), l1 = __shfl_sync(0xffffffffu, sl.t.y, 16 + tq);
+        const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+        const float z0 = __shfl_sync(0xffffffffu, sl.t.x, 4 * eb + tq), z1 = __shfl_sync(0xffffffffu, sl.t.y, 4 * eb + tq);
+        __half* o = p.out + ((size_t)b * p.n_heads + kv * p.group + c * kHeads + hc) * HD + 16 * warp + gq;
+        if (hc < nh) {
+            o[0] = __float2half_rn(fmaf(sl.v.x, 0x1p24f, z0) * i0);
+            o[8] = __float2half_rn(fmaf(sl.v.z, 0x1p20f, z0) * i0);
+        }
+        if (hc + 1 < nh) {
+            o[HD] = __float2half_rn(fmaf(sl.v.y, 0x1p24f, z1) * i1);
+            o[HD + 8] = __float2half_rn(fmaf(sl.v.w, 0x1p20f, z1) * i1);
+        }
+    };
+
     for (;;) {
-        const int g = p.chunks == 1 ? sg.s : sg.s / p.chunks, c = sg.s - g * p.chunks;
-        const int nh = min(kHeads, p.group - c * kHeads);
-        const int h0 = g * p.group + c * kHeads;
+        const int nh = min(kHeads, p.group - (p.chunks == 1 ? 0 : sg.s % p.chunks) * kHeads);
         st.clear();
         float top = kTop;               // log2 of the largest weight
         __half2 dlim = __float2half2_rn(2.f);   // the largest value scale that goes with it
@@ -430,41 +501,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         float fac[2];
         if (blk < sg.blk1) {
             const int h = DUP ? gq & 3 : gq;
-            const __half* qr = p.q + ((size_t)sg.b * p.n_heads + h0 + (h < nh ? h : 0)) * HD + 4 * tq;
-            float v[NB][8];
-            float mx = 0.f;
+            load_q(sg);
+            __half2 m2 = __float2half2_rn(0.f);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __half22float2(
-                        __ldg(reinterpret_cast<const __half2*>(qr + 32 * b + 16 * (k >> 1) + 2 * (k & 1))));
-                    v[b][2 * k] = h < nh ? f.x : 0.f;
-                    v[b][2 * k + 1] = h < nh ? f.y : 0.f;
-                    mx = fmaxf(mx, fmaxf(fabsf(v[b][2 * k]), fabsf(v[b][2 * k + 1])));
+                for (int k = 0; k < 2; ++k) {
+                    qr[b][k].x = h < nh ? qr[b][k].x : 0u;
+                    qr[b][k].y = h < nh ? qr[b][k].y : 0u;
+                    m2 = __hmax2(m2, __hmax2(__habs2(h2(qr[b][k].x)), __habs2(h2(qr[b][k].y))));
                 }
             }
+            float mx = fmaxf(__low2float(m2), __high2float(m2));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // 2^e brings the largest |q| of the head to [2^14, 2^15)
+            // 2^e brings the largest |q| of the head to [2^14, 2^15): two factors, each an f16 number; exact but
+            // for what e = -1 (a largest |q| of 2^15 or more) takes from numbers below 2^-13
             const int e = mx > 0.f && mx < INFINITY ? 14 - ((int)(__float_as_uint(mx) >> 23) - 127) : 0;
-            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            const int e0 = min(e, 14);
+            const __half2 up0 = __float2half2_rn(__uint_as_float((uint32_t)(e0 + 127) << 23));
+            const __half2 up1 = __float2half2_rn(__uint_as_float((uint32_t)(min(e - e0, 14) + 127) << 23));
+            const __half2 up2 = __float2half2_rn(__uint_as_float((uint32_t)(max(e - 28, 0) + 127) << 23));
+            const __half2 sixteenth = __float2half2_rn(0.0625f);
             float qs[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float s = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    v[b][k] *= up;
-                    s += v[b][k];
+                for (int k = 0; k < 2; ++k) {
+                    const __half2 x = __hmul2(__hmul2(__hmul2(h2(qr[b][k].x), up0), up1), up2);
+                    const __half2 y = __hmul2(__hmul2(__hmul2(h2(qr[b][k].y), up0), up1), up2);
+                    s += __low2float(x) + __high2float(x) + (__low2float(y) + __high2float(y));
+                    const __half2 lo = __lows2half2(x, y), hi = __highs2half2(x, y);
+                    (k ? qh : ql)[b][0] = u32(k ? __hmul2(lo, sixteenth) : lo);
+                    (k ? qh : ql)[b][1] = u32(k ? __hmul2(hi, sixteenth) : hi);
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
                 qs[b] = s * 0x1p-24f;
-                ql[b][0] = u32(__floats2half2_rn(v[b][0], v[b][2]));
-                ql[b][1] = u32(__floats2half2_rn(v[b][1], v[b][3]));
-                qh[b][0] = u32(__floats2half2_rn(v[b][4] * 0.0625f, v[b][6] * 0.0625f));
-                qh[b][1] = u32(__floats2half2_rn(v[b][5] * 0.0625f, v[b][7] * 0.0625f));
             }
             // the sums' high and low f16 parts, opposite the minima of blocks 2 (tq & 1), 2 (tq & 1) + 1
             const float sa = NB == 4 && (tq & 1) ? qs[NB - 2] : qs[0], sb = NB == 4 && (tq & 1) ? qs[NB - 1] : qs[1];
@@ -664,57 +738,65 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         }
         __syncthreads();
         Slice sl;
-        const bool has = warp < MT;
-        const int row = has ? warp : 0;
         sl.v = joins[row * 32 + lane];
         sl.t = joins[MT * 32 + lane];
 #pragma unroll
         for (int k = 1; k < 4; ++k) sl.join(joins[k * ROWS + row * 32 + lane], joins[k * ROWS + MT * 32 + lane]);
-        bool write = sg.blk1 - sg.blk0 == sg.nb;
-        if (!write) {
-            const long long seg0 = lo + sg.rel - sg.blk0;                       // the list's number of its first tile
-            const long long c0 = seg0 / per, c1 = (seg0 + sg.nb - 1) / per;     // the CTAs that hold parts
-            float4* slots = reinterpret_cast<float4*>(p.slots);
-            float4* to = slots + (2 * (size_t)blockIdx.x + (sg.blk0 == 0 ? 1 : 0)) * ROWS + lane;
+        if (sg.blk1 - sg.blk0 == sg.nb) emit(sl, sg.b, sg.s);
+        else {
+            const int end = sg.blk0 == 0 ? 1 : 0;
+            float4* to = reinterpret_cast<float4*>(p.slots) + (2 * (size_t)blockIdx.x + end) * ROWS + lane;
             if (has) __stcg(to + row * 32, sl.v);
             if (warp == 0) __stcg(to + MT * 32, sl.t);
             __syncthreads();
-            if (tid == 0) {   // releases the CTA's part (ordered by the barrier), acquires the others'
+            if (tid == 0) {   // releases the CTA's part (ordered by the barrier); the answer is not looked at before the end
+                const int c0 = quotient(lo + sg.at, per), c1 = quotient(lo + sg.at + sg.nb - 1, per);
+                part[end] = {c0, c1, sg.b, sg.s};
                 int n;
-                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(p.tickets + c0) : "memory");
-                last_flag = n == (int)(c1 - c0);
-                if (last_flag) p.tickets[c0] = 0;   // armed for the next launch
+                asm volatile("atom.add.release.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(p.tickets + c0) : "memory");
+                if (end) complete[1] = n == c1 - c0;
+                else arrival = n;
             }
-            __syncthreads();
-            if (last_flag) {   // the last part is there: all of them, in order
-                write = true;
-                const float4* part = slots + (2 * (size_t)c0 + 1) * ROWS + lane;
-                sl.v = __ldcg(part + row * 32);
-                sl.t = __ldcg(part + MT * 32);
-#pragma unroll 8
-                for (long long k = c0 + 1; k <= c1; ++k) {
-                    part = slots + 2 * (size_t)k * ROWS + lane;
-                    sl.join(__ldcg(part + row * 32), __ldcg(part + MT * 32));
+            parts |= 1 + end;
+        }
+        if (sg.last(window)) break;
+        sg.next(p, S, window);
+    }
+    if (parts) {   // (the same in every thread)
+        if (tid == 0) {
+            if (parts & 1) complete[0] = arrival == part[0].c1 - part[0].c0;
+            asm volatile("fence.acq_rel.gpu;" ::: "memory");   // the others' parts, where theirs came before
+            if ((parts & 1) && complete[0]) p.tickets[part[0].c0] = 0;   // armed for the next launch
+            if ((parts & 2) && complete[1]) p.tickets[part[1].c0] = 0;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (!(parts >> i & 1) || !complete[i]) continue;
+            // this CTA's part came last: all of them, in order
+            const int c0 = part[i].c0, c1 = part[i].c1;
+            Slice sl;
+#pragma unroll 1
+            for (int k0 = c0; k0 <= c1; k0 += MERGE) {
+                float4 v[MERGE], t[MERGE];
+#pragma unroll
+                for (int k = 0; k < MERGE; ++k) {
+                    const int c = min(k0 + k, c1);
+                    const float4* from = reinterpret_cast<const float4*>(p.slots) + (2 * (size_t)c + (c == c0 ? 1 : 0)) * ROWS + lane;
+                    v[k] = __ldcg(from + row * 32);
+                    t[k] = __ldcg(from + MT * 32);
+                }
+#pragma unroll
+                for (int k = 0; k < MERGE; ++k) {
+                    if (k0 + k > c1) break;
+                    if (k0 + k == c0) {
+                        sl.v = v[k];
+                        sl.t = t[k];
+                    } else sl.join(v[k], t[k]);
                 }
             }
+            emit(sl, part[i].b, part[i].s);
         }
-        if (write && has) {
-            const int hc = 2 * tq, b = warp >> 1;
-            const float l0 = __shfl_sync(0xffffffffu, sl.t.x, 16 + tq), l1 = __shfl_sync(0xffffffffu, sl.t.y, 16 + tq);
-            const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-            const float z0 = __shfl_sync(0xffffffffu, sl.t.x, 4 * b + tq), z1 = __shfl_sync(0xffffffffu, sl.t.y, 4 * b + tq);
-            __half* o = p.out + ((size_t)sg.b * p.n_heads + h0 + hc) * HD + 16 * warp + gq;
-            if (hc < nh) {
-                o[0] = __float2half_rn(fmaf(sl.v.x, 0x1p24f, z0) * i0);
-                o[8] = __float2half_rn(fmaf(sl.v.z, 0x1p20f, z0) * i0);
-            }
-            if (hc + 1 < nh) {
-                o[HD] = __float2half_rn(fmaf(sl.v.y, 0x1p24f, z1) * i1);
-                o[HD + 8] = __float2half_rn(fmaf(sl.v.w, 0x1p20f, z1) * i1);
-            }
-        }
-        if (sg.rel + sg.blk1 - sg.blk0 >= run) break;
-        sg.next(p, S, run);
     }
     if (dead) {   // copies may still be in flight: wait for them (again with a limit) before leaving
         for (int i = 0; i < kStages; ++i) {
