@@ -7,7 +7,7 @@
 //
 // The border of top-k (a count) or top-p (a weight) is found by digits, the histogram of 128 bins
 // naming the bin that the border falls into and the next round dividing that bin: 7 bits at a time of
-// the distance from the largest logit on a 24-bit scale of 24 T, then of the logit's ordered bits, then
+// the distance from the largest logit on a 23-bit scale of 24 T, then of the logit's ordered bits, then
 // of the index, until few enough candidates are left, which are ranked against one another.
 //
 // A row is read once: a thread-block cluster holds it in shared memory, each CTA a run of tokens, and
@@ -28,7 +28,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 128, kDigit = 7;
 constexpr int kList = 128;                      // candidates that are ranked directly
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kQMax = (1u << 24) - 1;      // the distance scale's last value: all that is farther
+constexpr uint32_t kQMax = (1u << 23) - 1;      // the distance scale's last value: all that is farther
 constexpr uint32_t kKeyMin = 0x00800000u;       // the key after -inf's
 
 // 2^(j / 64) in 30 bits after the point
@@ -116,7 +116,7 @@ struct RowScale {
         const float x = t - ref;
         magic = 12582912.0f - floorf(__fmul_rd(x, c_hi));
         low = fmaxf(x - __fdiv_rn(2600.f, c_hi), -FLT_MAX);            // 2^-40.6 of the largest: weight 0
-        dist = fminf(__fdiv_rn(16777216.f / 24.f, temp), FLT_MAX);     // finite: 0 dist is 0
+        dist = fminf(__fdiv_rn(8388608.f / 24.f, temp), FLT_MAX);     // finite: 0 dist is 0
     }
 };
 
@@ -145,7 +145,7 @@ __device__ __forceinline__ u64 weight(float l, const RowScale& r, const uint32_t
 }
 
 __device__ __forceinline__ uint32_t distance(float l, const RowScale& r) {
-    return (uint32_t)fminf((r.top - l) * r.dist, (float)kQMax);
+    return __float_as_uint(__fadd_rz(fminf((r.top - l) * r.dist, (float)kQMax), 8388608.f)) - 0x4B000000u;   // truncated
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -454,29 +454,122 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
     }
 }
 
-// The draw among the n <= kList entries of the first top_k tokens and a few after them, by one CTA.
-__device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t least, float u, int32_t* token, float* prob,
-                           Shared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    static_assert(kList == 4 * 32, "four warps hold the entries");
-    const Entry me = tid < n ? e[tid] : Entry{0, 0, 0x7FFFFFFF};
-    u64 before = 0;
-    int place = 0;
-    if (tid < kList) {
-        for (int j = 0; j < n; ++j) {
-            const Entry o = e[j];
-            if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) {
-                before += o.w;
-                ++place;
+// The first topk (<= kList) tokens of the order and a few more, sh.found of them, to hist + kList entries of rank 0;
+// false (nothing found) where the few would be too many. At least topk tokens lie as near as topk threads'
+// largest logits (mine) do, so that the threshold comes from a histogram of one value a thread.
+__device__ bool list_first(const Run& run, const RowScale& row, float mine, int topk, uint32_t* hist, Shared& sh, uint32_t rank,
+                           uint32_t ranks) {
+    constexpr int kShift = 23 - kDigit;
+    const int tid = threadIdx.x, lane = tid & 31;
+    Entry *list = reinterpret_cast<Entry*>(hist), *ranked = list + kList;
+    uint32_t* bins = reinterpret_cast<uint32_t*>(ranked);
+    if (tid < kBins) bins[tid] = 0;
+    if (tid == 0) sh.nlist = 0;
+    __syncthreads();
+    if (mine > -INFINITY) atomicAdd(bins + (distance(mine, row) >> kShift), 1u);
+    __syncthreads();
+    if (tid < kBins) sh.mine[0][tid] = bins[tid];
+    cluster_sync();
+    if (tid < kBins) {
+        u64 v = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) v += r < ranks ? remote_u64(&sh.mine[0][tid], r) : 0;
+        sh.all[tid] = v;
+    }
+    __syncthreads();
+    uint32_t v[kBins / 32], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kBins / 32; ++j) {
+        v[j] = (uint32_t)sh.all[lane * (kBins / 32) + j];
+        sum += v[j];
+    }
+    uint32_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += t;
+    }
+    const unsigned reach = __ballot_sync(0xffffffffu, upto >= (uint32_t)topk);
+    uint32_t far = kQMax;
+    if (reach) {
+        uint32_t c = upto - sum;
+        int bin = lane * (kBins / 32);
+#pragma unroll
+        for (int j = 0; j < kBins / 32 - 1; ++j) {
+            if (bin == lane * (kBins / 32) + j && c + v[j] < (uint32_t)topk) {
+                c += v[j];
+                ++bin;
             }
         }
+        bin = __shfl_sync(0xffffffffu, bin, __ffs(reach) - 1);
+        far = ((uint32_t)(bin + 1) << kShift) - 1;
     }
-    const bool in = tid < n && place < topk;
+    for (int i = run.v0 + lane; i < run.v1; i += 32) {
+        const float4 x = run.data[i];
+        if (distance(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), row) > far) continue;
+        const float l[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (distance(l[j], row) > far) continue;
+            const u64 w = weight(l[j], row, sh.table);
+            if (w == 0) continue;
+            const uint32_t n = atomicAdd(&sh.nlist, 1u);
+            if (n < kList) list[n] = Entry{w, key_of(l[j]), run.base + 4 * i + j};
+        }
+    }
+    cluster_sync();
+    const uint32_t len = lane < (int)ranks ? remote_u32(&sh.nlist, (uint32_t)lane) : 0;
+    const uint32_t ends = (uint32_t)warp_scan(len, lane);
+    const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
+    if (total <= kList && rank == 0) {   // thread t takes the t-th of all: the CTA in whose list it is, and its place there
+        uint32_t r = 0, start = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kMaxCluster; ++k) {
+            const uint32_t end = __shfl_sync(0xffffffffu, ends, k);
+            if ((uint32_t)tid >= end) {
+                r = k + 1;
+                start = end;
+            }
+        }
+        if ((uint32_t)tid < total) {
+            const Entry* e = &list[tid - start];
+            const u64 w = remote_u64(&e->w, r), ki = remote_u64(&e->key, r);
+            ranked[tid] = Entry{w, (uint32_t)ki, (int)(ki >> 32)};
+        }
+        if (tid == 0) sh.found = total;
+    }
+    cluster_sync();   // the lists have been read
+    return total <= kList;
+}
+
+// The draw among the n <= kList entries of the first top_k tokens and a few after them, by one CTA, four threads an
+// entry.
+__device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t least, float u, int32_t* token, float* prob,
+                           Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = tid >> 2, part = tid & 3;
+    static_assert(4 * kList == kThreads, "four threads an entry");
+    const Entry me = at < n ? e[at] : Entry{0, 0, 0x7FFFFFFF};
+    auto quad = [](u64 v) {
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        return v + __shfl_xor_sync(0xffffffffu, v, 2);
+    };
+    u64 before = 0;
+    int place = 0;
+    for (int j = part; j < n; j += 4) {
+        const Entry o = e[j];
+        if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) {
+            before += o.w;
+            ++place;
+        }
+    }
+    before = quad(before);
+    place = (int)quad((u64)place);
+    const bool in = at < n && place < topk;
     auto total_of = [&](u64 w) {
-        w = warp_sum(w);
+        w = warp_sum(part == 0 ? w : 0);
         if (lane == 0) sh.part[warp] = w;
         __syncthreads();
-        const u64 t = sh.part[0] + sh.part[1] + sh.part[2] + sh.part[3];
+        const u64 t = warp_sum(lane < kWarps ? sh.part[lane] : 0);
         __syncthreads();
         return t;
     };
@@ -488,18 +581,16 @@ __device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t
         target = target == 0 ? 1 : target;
         keep = keep && before < target;
     }
+    if (part == 0) sh.all[at] = keep ? me.w : 0;
     const u64 total = total_of(keep ? me.w : 0);
     const u64 target = __umul64hi(__float2ull_rz(u * 0x1p64f), total) + 1;
-    if (tid < kList) sh.all[tid] = keep ? me.w : 0;
-    __syncthreads();
-    if (keep) {
-        u64 c = 0;
-        for (int j = 0; j < n; ++j)
-            if (e[j].idx <= me.idx) c += sh.all[j];
-        if (c >= target && c - me.w < target) {
-            *token = me.idx;
-            if (prob) *prob = (float)((double)me.w / (double)total);
-        }
+    u64 c = 0;
+    for (int j = part; j < n; j += 4)
+        if (e[j].idx <= me.idx) c += sh.all[j];
+    c = quad(c);
+    if (keep && part == 0 && c >= target && c - me.w < target) {
+        *token = me.idx;
+        if (prob) *prob = (float)((double)me.w / (double)total);
     }
 }
 
@@ -540,9 +631,9 @@ struct RowArgs {
     float temp, topp, minp, u;
     int topk;
 };
-// False where nothing is to be drawn: an inactive row, or one whose arguments are out of range (recorded).
-__device__ __forceinline__ bool row_args(const Params& p, long long b, uint32_t rank, RowArgs& a, DevError* err) {
-    if (p.active && p.active[b] == 0) return false;
+// Their loads, not waited for before row_args looks at them; false for an inactive row.
+__device__ __forceinline__ bool row_loads(const Params& p, long long b, RowArgs& a) {
+    const bool active = !p.active || p.active[b] != 0;
     a.temp = p.temperature ? p.temperature[b] : 1.0f;
     a.topp = p.top_p ? p.top_p[b] : 1.0f;
     a.minp = p.min_p ? p.min_p[b] : 0.0f;
@@ -550,6 +641,10 @@ __device__ __forceinline__ bool row_args(const Params& p, long long b, uint32_t 
     // a decode loop's numbers, one per position (a negative position has been recorded by the step)
     const long long at = p.uniform_stride <= 1 ? b : b * p.uniform_stride + max(p.positions[b], 0) % p.uniform_stride;
     a.u = p.uniform[at];
+    return active;
+}
+// False where the arguments are out of range (recorded).
+__device__ __forceinline__ bool row_args(const Params& p, long long b, uint32_t rank, const RowArgs& a, DevError* err) {
     if (a.temp >= 0.f && a.temp < INFINITY && a.topp == a.topp && a.minp == a.minp && a.u >= 0.f && a.u < 1.f) return true;
     if (threadIdx.x == 0 && rank == 0) {
         record_device_error(err, kErrSampleArg, b, 0);
@@ -682,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, Dev
     pdl_wait();
     pdl_trigger();
     RowArgs a;
-    if (!row_args(p, b, rank, a, err)) return;
+    if (!row_loads(p, b, a)) return;
     const int first = (int)rank * p.per;
     const int n = max(0, min(p.vocab - first, p.per));
     const T* src = static_cast<const T*>(p.logits) + b * p.stride + first;
@@ -690,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, Dev
     if (tid < 64) sh.table[tid] = kExp2[tid];
     float top = -INFINITY;
     each<true>(run, lane, [&](float l) { top = fmaxf(top, l); });   // passes over NaN
+    if (!row_args(p, b, rank, a, err)) return;
     if (!row_top(p, b, rank, ranks, top, sh)) return;
     const bool infinite = top == INFINITY;
     top = canonical(top);
@@ -741,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
     pdl_wait();
     pdl_trigger();
     RowArgs a;
-    if (!row_args(p, b, rank, a, err)) return;
+    if (!row_loads(p, b, a)) return;
     const int first = (int)rank * p.per;
     const int n = max(0, min(p.vocab - first, p.per));
     const T* src = static_cast<const T*>(p.logits) + b * p.stride + first;
@@ -749,7 +845,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
     const int nvec = (off + n + 3) / 4;
     uint32_t* hist = reinterpret_cast<uint32_t*>(dyn + p.per + 8);
     if (tid < 64) sh.table[tid] = kExp2[tid];
-    float top = load_run(src, n, off, dyn, nvec);
+    const float mine = load_run(src, n, off, dyn, nvec);
+    float top = mine;
+    if (!row_args(p, b, rank, a, err)) return;
     if (!row_top(p, b, rank, ranks, top, sh)) return;
     Run run;
     run.data = reinterpret_cast<const float4*>(dyn);
@@ -774,7 +872,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         border.key = max(kKeyMin, key_of(sh.least));
     }
     if (a.topk > 0 && a.topk <= kList && a.topk < p.vocab) {
-        find_border<kFirst>(run, row, p.vocab, every, (u64)a.topk, 0.f, hist, sh, ranks, turn);
+        if (!list_first(run, row, mine, a.topk, hist, sh, rank, ranks))
+            find_border<kFirst>(run, row, p.vocab, every, (u64)a.topk, 0.f, hist, sh, ranks, turn);
         if (rank == 0)
             draw_small(reinterpret_cast<const Entry*>(hist) + kList, (int)sh.found, a.topk, a.topp, border.key, a.u, p.tokens + b,
                        p.probs ? p.probs + b : nullptr, sh);
