@@ -72,6 +72,8 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -174,7 +176,7 @@ struct Border {
     }
 };
 
-struct Entry {
+struct __align__(16) Entry {
     u64 w;
     uint32_t key;
     int idx;
@@ -184,8 +186,9 @@ struct Shared {
     uint32_t table[64];
     u64 mine[2][kBins];          // this CTA's sums of a histogram's bins; every second round in turn
     u64 all[kBins];              // the cluster's
-    float top;                   // this CTA's largest logit
-    float wtop[kWarps];
+    uint32_t keys[kBins];
+    uint32_t top;                // the key of this CTA's largest logit
+    uint32_t wtop[kWarps];
     u64 part[kWarps];
     u64 whole;
     uint32_t nlist, found;
@@ -454,15 +457,16 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
     }
 }
 
-// The first topk (<= kList) tokens of the order and a few more, sh.found of them, to hist + kList entries of rank 0;
-// false (nothing found) where the few would be too many. At least topk tokens lie as near as topk threads'
+// The first topk (<= kList) tokens of the order and a few more, sh.nlist of them, to `list` of rank 0; false
+// where the few would be too many. At least topk tokens lie as near as topk threads'
 // largest logits (mine) do, so that the threshold comes from a histogram of one value a thread.
-__device__ bool list_first(const Run& run, const RowScale& row, float mine, int topk, uint32_t* hist, Shared& sh, uint32_t rank,
+__device__ bool list_first(const Run& run, const RowScale& row, float mine, int topk, uint32_t* hist, Shared& sh,
                            uint32_t ranks) {
     constexpr int kShift = 23 - kDigit;
     const int tid = threadIdx.x, lane = tid & 31;
-    Entry *list = reinterpret_cast<Entry*>(hist), *ranked = list + kList;
-    uint32_t* bins = reinterpret_cast<uint32_t*>(ranked);
+    Entry* list = reinterpret_cast<Entry*>(hist);
+    uint32_t* bins = reinterpret_cast<uint32_t*>(list + kList);
+    const uint32_t count = remote(&sh.nlist, 0), entries = remote(list, 0);
     if (tid < kBins) bins[tid] = 0;
     if (tid == 0) sh.nlist = 0;
     __syncthreads();
@@ -513,48 +517,31 @@ __device__ bool list_first(const Run& run, const RowScale& row, float mine, int 
             if (distance(l[j], row) > far) continue;
             const u64 w = weight(l[j], row, sh.table);
             if (w == 0) continue;
-            const uint32_t n = atomicAdd(&sh.nlist, 1u);
-            if (n < kList) list[n] = Entry{w, key_of(l[j]), run.base + 4 * i + j};
+            uint32_t n;
+            asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(count) : "memory");
+            if (n < kList)
+                asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(entries + n * 16), "r"((uint32_t)w),
+                             "r"((uint32_t)(w >> 32)), "r"(key_of(l[j])), "r"(run.base + 4 * i + j) : "memory");
         }
     }
     cluster_sync();
-    const uint32_t len = lane < (int)ranks ? remote_u32(&sh.nlist, (uint32_t)lane) : 0;
-    const uint32_t ends = (uint32_t)warp_scan(len, lane);
-    const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
-    if (total <= kList && rank == 0) {   // thread t takes the t-th of all: the CTA in whose list it is, and its place there
-        uint32_t r = 0, start = 0;
-#pragma unroll
-        for (uint32_t k = 0; k < kMaxCluster; ++k) {
-            const uint32_t end = __shfl_sync(0xffffffffu, ends, k);
-            if ((uint32_t)tid >= end) {
-                r = k + 1;
-                start = end;
-            }
-        }
-        if ((uint32_t)tid < total) {
-            const Entry* e = &list[tid - start];
-            const u64 w = remote_u64(&e->w, r), ki = remote_u64(&e->key, r);
-            ranked[tid] = Entry{w, (uint32_t)ki, (int)(ki >> 32)};
-        }
-        if (tid == 0) sh.found = total;
-    }
-    cluster_sync();   // the lists have been read
-    return total <= kList;
+    return remote_u32(&sh.nlist, 0) <= kList;
 }
 
 // The draw among the n <= kList entries of the first top_k tokens and a few after them, by one CTA, four threads an
-// entry.
+// entry. What is kept is a prefix of the order, so the entry at its end knows the kept weight.
 __device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t least, float u, int32_t* token, float* prob,
                            Shared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = tid >> 2, part = tid & 3;
-    static_assert(4 * kList == kThreads, "four threads an entry");
+    const int tid = threadIdx.x, at = tid >> 2, part = tid & 3;
+    static_assert(4 * kList == kThreads && kList <= kBins, "four threads an entry");
     const Entry me = at < n ? e[at] : Entry{0, 0, 0x7FFFFFFF};
     auto quad = [](u64 v) {
         v += __shfl_xor_sync(0xffffffffu, v, 1);
         return v + __shfl_xor_sync(0xffffffffu, v, 2);
     };
     u64 before = 0;
-    int place = 0;
+    uint32_t place = 0;
+#pragma unroll 4
     for (int j = part; j < n; j += 4) {
         const Entry o = e[j];
         if (o.key > me.key || (o.key == me.key && o.idx < me.idx)) {
@@ -563,30 +550,35 @@ __device__ void draw_small(const Entry* e, int n, int topk, float topp, uint32_t
         }
     }
     before = quad(before);
-    place = (int)quad((u64)place);
-    const bool in = at < n && place < topk;
-    auto total_of = [&](u64 w) {
-        w = warp_sum(part == 0 ? w : 0);
-        if (lane == 0) sh.part[warp] = w;
-        __syncthreads();
-        const u64 t = warp_sum(lane < kWarps ? sh.part[lane] : 0);
-        __syncthreads();
-        return t;
-    };
-    bool keep = in && me.key >= least;
-    if (topp < 1.f) {
-        const u64 whole = total_of(in ? me.w : 0);
-        const u64 s64 = topp > 0.f ? __float2ull_rz(topp * 0x1p64f) : 0;
-        u64 target = __umul64hi(s64, whole) + (s64 * whole != 0 ? 1 : 0);
-        target = target == 0 ? 1 : target;
-        keep = keep && before < target;
+    place += __shfl_xor_sync(0xffffffffu, place, 1);
+    place += __shfl_xor_sync(0xffffffffu, place, 2);
+    const int m = min(n, topk);
+    if (part == 0 && at < n) {   // sums and keys in the order's places
+        sh.all[place] = before + me.w;
+        sh.keys[place] = me.key;
     }
-    if (part == 0) sh.all[at] = keep ? me.w : 0;
-    const u64 total = total_of(keep ? me.w : 0);
+    __syncthreads();
+    u64 within = ~0ull;   // top-p: kept while less than this lies before
+    if (topp < 1.f) {
+        const u64 whole = sh.all[m - 1];
+        const u64 s64 = topp > 0.f ? __float2ull_rz(topp * 0x1p64f) : 0;
+        within = __umul64hi(s64, whole) + (s64 * whole != 0 ? 1 : 0);
+        within = within == 0 ? 1 : within;
+    }
+    auto kept = [&](int q, u64 b, uint32_t key) { return q < m && b < within && key >= least; };
+    const bool keep = at < n && kept((int)place, before, me.key);
+    const u64 upto = before + me.w;
+    if (part == 0) {
+        sh.mine[0][at] = keep ? me.w : 0;
+        if (keep && !((int)place + 1 < m && kept((int)place + 1, upto, sh.keys[place + 1]))) sh.whole = upto;
+    }
+    __syncthreads();
+    const u64 total = sh.whole;
     const u64 target = __umul64hi(__float2ull_rz(u * 0x1p64f), total) + 1;
     u64 c = 0;
+#pragma unroll 4
     for (int j = part; j < n; j += 4)
-        if (e[j].idx <= me.idx) c += sh.all[j];
+        if (e[j].idx <= me.idx) c += sh.mine[0][j];
     c = quad(c);
     if (keep && part == 0 && c >= target && c - me.w < target) {
         *token = me.idx;
@@ -657,20 +649,16 @@ __device__ __forceinline__ bool row_args(const Params& p, long long b, uint32_t 
 // The row's largest logit from every thread's. False where the row has no token, which is written.
 __device__ __forceinline__ bool row_top(const Params& p, long long b, uint32_t rank, uint32_t ranks, float& top, Shared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sh.wtop[warp] = top;
+    uint32_t key = __reduce_max_sync(0xffffffffu, key_of(top));
+    if (lane == 0) sh.wtop[warp] = key;
     __syncthreads();
     if (warp == 0) {
-        top = sh.wtop[lane & (kWarps - 1)];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) sh.top = top;
+        key = __reduce_max_sync(0xffffffffu, sh.wtop[lane & (kWarps - 1)]);
+        if (lane == 0) sh.top = key;
     }
     cluster_sync();
-    top = lane < (int)ranks ? __uint_as_float(remote_u32(&sh.top, (uint32_t)lane)) : -INFINITY;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    key = __reduce_max_sync(0xffffffffu, lane < (int)ranks ? remote_u32(&sh.top, (uint32_t)lane) : 0u);
+    top = __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
     if (top != -INFINITY) return true;
     cluster_sync();   // nobody leaves while its shared memory may be read
     if (tid == 0 && rank == 0) {
@@ -730,6 +718,7 @@ __device__ __forceinline__ void draw(const Params& p, long long b, uint32_t rank
                                      K kept, I index) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const u64 t = lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0;
+    cluster_arrive();   // what this CTA reads of the others is read
     const u64 upto = warp_scan(t, lane);
     const u64 total = __shfl_sync(0xffffffffu, upto, 31), before = __shfl_sync(0xffffffffu, upto - t, (int)rank);
     // the first token at which the running sum exceeds u total: reaches floor(u total) + 1, exactly
@@ -745,6 +734,7 @@ __device__ __forceinline__ void draw(const Params& p, long long b, uint32_t rank
         const int n = (to - from + kThreads - 1) / kThreads;
         const int a = min(to, from + tid * n), e = min(to, a + n);
         u64 s = 0;
+#pragma unroll 4
         for (int j = a; j < e; ++j) s += kept(j);
         const u64 incl = warp_scan(s, lane);
         if (lane == 31) sh.wsum[warp] = incl;
@@ -763,7 +753,7 @@ __device__ __forceinline__ void draw(const Params& p, long long b, uint32_t rank
             }
         }
     }
-    cluster_sync();   // nobody leaves while its shared memory may be read
+    cluster_wait();   // nobody leaves while its shared memory may be read
 }
 
 // No top-k or top-p: two passes over the row, the second from L2, so that shared memory does not bound the
@@ -872,11 +862,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         border.key = max(kKeyMin, key_of(sh.least));
     }
     if (a.topk > 0 && a.topk <= kList && a.topk < p.vocab) {
-        if (!list_first(run, row, mine, a.topk, hist, sh, rank, ranks))
+        const Entry* e = reinterpret_cast<const Entry*>(hist);
+        const bool listed = list_first(run, row, mine, a.topk, hist, sh, ranks);
+        cluster_arrive();   // this CTA has read rank 0's count
+        if (!listed) {
+            cluster_wait();
             find_border<kFirst>(run, row, p.vocab, every, (u64)a.topk, 0.f, hist, sh, ranks, turn);
+            e += kList;
+        }
         if (rank == 0)
-            draw_small(reinterpret_cast<const Entry*>(hist) + kList, (int)sh.found, a.topk, a.topp, border.key, a.u, p.tokens + b,
+            draw_small(e, (int)(listed ? sh.nlist : sh.found), a.topk, a.topp, border.key, a.u, p.tokens + b,
                        p.probs ? p.probs + b : nullptr, sh);
+        if (listed) cluster_wait();
         return;   // no CTA reads another's shared memory any more
     }
     if (a.topk > 0 && a.topk < p.vocab) {
@@ -891,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         each(run, lane, [&](float l, int) {
             const u64 x = weight(l, row, sh.table);
             s += x;
-            w += x & -(u64)(l >= least);
+            if (l >= least) w += x;
         });
         share_sums(w, s, sh);
         const u64 kept = warp_sum(lane < (int)ranks ? remote_u64(&sh.whole, (uint32_t)lane) : 0);
