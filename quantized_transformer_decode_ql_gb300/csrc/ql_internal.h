@@ -137,18 +137,21 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Dynamic shared memory beyond 48 KB: allowed once per kernel and device (`done`: a bit per device of one
-// kernel), not at every launch.
-template <typename K>
-cudaError_t allow_smem_once(K kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+// A kernel's attribute set once per kernel and device (`done`: a bit per device of one kernel), not at every launch.
+inline cudaError_t allow_once(const void* kernel, cudaFuncAttribute attr, int value, std::atomic<unsigned long long>& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    e = cudaFuncSetAttribute(kernel, attr, value);
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
+}
+// Dynamic shared memory beyond 48 KB.
+template <typename K>
+cudaError_t allow_smem_once(K kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+    return allow_once(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes, done);
 }
 
 // ---------------------------------------------------------------- GEMV (internal form)

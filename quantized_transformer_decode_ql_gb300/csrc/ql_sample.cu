@@ -27,7 +27,8 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 128, kDigit = 7;
 constexpr int kList = 128;                      // candidates that are ranked directly
-constexpr int kMaxCluster = 8;
+constexpr int kFewRows = 4;
+constexpr int kMaxCluster = 16, kPortableCluster = 8;
 constexpr uint32_t kQMax = (1u << 23) - 1;      // the distance scale's last value: all that is farther
 constexpr uint32_t kKeyMin = 0x00800000u;       // the key after -inf's
 
@@ -191,7 +192,7 @@ struct Shared {
     uint32_t wtop[kWarps];
     u64 part[kWarps];
     u64 whole;
-    uint32_t nlist, found;
+    uint32_t nlist, found, nlong;
     int first;
     u64 sum;                     // this CTA's weight of all tokens
     float least;
@@ -274,137 +275,175 @@ __device__ __forceinline__ void each(const Stream<T>& s, int lane, F f) {
     for (int i = s.v0 + s.nv * Stream<T>::W + lane; i < s.to; i += 32) one(i);
 }
 
+// What a search passes over: the CTA's run, or a list of its entries.
+struct Tokens {
+    Run run;
+    template <typename F>
+    __device__ __forceinline__ void pass(F f) const {
+        each(run, threadIdx.x & 31, f);
+    }
+};
+__device__ __forceinline__ float logit_of(uint32_t key) {
+    return __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+struct Listed {
+    const Entry* e;
+    int n;
+    template <typename F>
+    __device__ __forceinline__ void pass(F f) const {
+        for (int j = threadIdx.x; j < n; j += kThreads) f(logit_of(e[j].key), e[j].idx);
+    }
+};
+
 // What a search looks for: the border of the first `target` tokens of the order; that of the shortest
 // prefix, within `in`, with at least the share `share` of the weight within `in`; or the first `target`
 // tokens themselves (at most kList), which then lie in `ranked`, sh.found of them with a few more.
 enum { kCount = 0, kMass = 1, kFirst = 2 };
 
-// Returns `in` where there are fewer tokens.
-template <int KIND>
-__device__ Border find_border(const Run& run, const RowScale& row, int vocab, const Border in, u64 target, float share,
+// The interval that the border lies in, by what is open: distances qa .. qb, of one distance keys ka .. kb, of
+// one key indices ia .. ib; what of the target lies before it.
+struct Search {
+    uint32_t qa, qb, ka, kb, ia, ib;
+    u64 base, target;
+    bool all;        // in: every token above -inf
+    __device__ __forceinline__ Search(const RowScale& row, int vocab, const Border& in, u64 t)
+        : qa(0), qb(kQMax), ka(kKeyMin), kb(key_of(row.top)), ia(0), ib((uint32_t)vocab - 1), base(0), target(t), all(in.all()) {}
+    __device__ __forceinline__ int level() const { return qa < qb ? 0 : ka < kb ? 1 : 2; }
+    // the digit's value of a token, above the interval's span where it is not one of those left. Tokens of -inf
+    // are left in until the keys are divided: they weigh nothing, and come last in a count.
+    __device__ __forceinline__ uint32_t digit(int lv, float l, int i, const RowScale& row, const Border& in) const {
+        const uint32_t q = distance(l, row), k = key_of(l);
+        if (lv == 0) return all || in.keeps(k, i) ? q - qa : ~0u;
+        const bool ok = q == qa && k <= kb && k >= ka && (all || in.keeps(k, i));
+        if (lv == 1) return ok ? kb - k : ~0u;
+        return ok ? (uint32_t)i - ia : ~0u;
+    }
+};
+
+// One round: the highest 7 bits of the first interval still open are divided; false where the target is not
+// reached. COLS: the histogram's columns, one per lane where all tokens are passed over.
+template <int KIND, int COLS, typename S>
+__device__ bool divide(const S& src, Search& f, const RowScale& row, const Border& in, float share, bool first, uint32_t* hist,
+                       Shared& sh, uint32_t ranks, int& turn, u64& in_bin) {
+    constexpr bool MASS = KIND == kMass;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int level = f.level();
+    const uint32_t a = level == 0 ? f.qa : level == 1 ? f.ka : f.ia, b = level == 0 ? f.qb : level == 1 ? f.kb : f.ib;
+    const uint32_t span = b - a;
+    const int bits = 32 - __clz((int)span);
+    const int shift = bits > kDigit ? bits - kDigit : 0;
+    for (int i = tid; i < kBins * COLS * (MASS ? 2 : 1) / 4; i += kThreads)
+        reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) sh.nlist = 0;
+    __syncthreads();
+    if (KIND != kMass && first && f.all) {   // every token counts
+        src.pass([&](float l, int) { atomicAdd(hist + (distance(l, row) >> shift) * COLS + lane % COLS, 1u); });
+    } else src.pass([&](float l, int i) {
+        const uint32_t v = f.digit(level, l, i, row, in);
+        if (v > span) return;
+        uint32_t* h = hist + (v >> shift) * COLS + lane % COLS;
+        if (MASS) {
+            const u64 w = weight(l, row, sh.table);
+            if (w != 0) {
+                atomicAdd(h, (uint32_t)w & 0xfffffu);
+                atomicAdd(h + kBins * COLS, (uint32_t)(w >> 20));
+            }
+        } else {
+            atomicAdd(h, 1u);
+        }
+    });
+    __syncthreads();
+    {   // four threads a bin, a quarter of the columns each, taken so that a warp's reads are on different banks
+        const int bin = tid >> 2, c0 = (tid & 3) * (COLS / 4);
+        u64 v = 0;
+#pragma unroll
+        for (int j = 0; j < COLS / 4; ++j) {   // a column holds at most 2^11 tokens of 2^20 each: below 2^32
+            const int c = c0 + ((j + bin) & (COLS / 4 - 1));
+            v += hist[bin * COLS + c];
+            if (MASS) v += (u64)hist[(kBins + bin) * COLS + c] << 20;
+        }
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if ((tid & 3) == 0) sh.mine[turn][bin] = v;
+    }
+    cluster_sync();
+    if (tid < kBins) {
+        u64 v = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) v += r < ranks ? remote_u64(&sh.mine[turn][tid], r) : 0;
+        sh.all[tid] = v;
+    }
+    turn ^= 1;
+    __syncthreads();
+    // every warp: the bin in which the running sum reaches the target
+    u64 v[kBins / 32], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kBins / 32; ++j) {
+        v[j] = sh.all[lane * (kBins / 32) + j];
+        mine += v[j];
+    }
+    const u64 upto = warp_scan(mine, lane);
+    if (MASS && first) {   // ceil(share * sum), exactly; 1 at least
+        const u64 sum = __shfl_sync(0xffffffffu, upto, 31);
+        const u64 s64 = share > 0.f ? __float2ull_rz(share * 0x1p64f) : 0;
+        f.target = __umul64hi(s64, sum) + (s64 * sum != 0 ? 1 : 0);
+        f.target = f.target == 0 ? 1 : f.target;
+    }
+    const unsigned reach = __ballot_sync(0xffffffffu, f.base + upto >= f.target);
+    if (!reach && KIND != kFirst) return false;   // fewer tokens
+    const int l = reach ? __ffs(reach) - 1 : 31;
+    u64 c = f.base + upto - mine;
+    int bin = lane * (kBins / 32);
+#pragma unroll
+    for (int j = 0; j < kBins / 32 - 1; ++j) {
+        if (bin == lane * (kBins / 32) + j && c + v[j] < f.target) {
+            c += v[j];
+            ++bin;
+        }
+    }
+    bin = __shfl_sync(0xffffffffu, bin, l);
+    f.base = __shfl_sync(0xffffffffu, c, l);
+    in_bin = sh.all[bin];
+    const uint32_t lo = (uint32_t)bin << shift, hi = lo + ((1u << shift) - 1);
+    if (level == 1) {   // keys: bins fall from the largest
+        const uint32_t last = f.kb;
+        f.kb = last - lo;
+        f.ka = hi < last - f.ka ? last - hi : f.ka;
+    } else if (level == 0) {
+        f.qb = hi < f.qb - f.qa ? f.qa + hi : f.qb;
+        f.qa += lo;
+    } else {
+        f.ib = hi < f.ib - f.ia ? f.ia + hi : f.ib;
+        f.ia += lo;
+    }
+    return true;
+}
+
+// The border, from the interval that f has come to (`rounds` of them done); `in` where there are fewer tokens.
+template <int KIND, int COLS, typename S>
+__device__ Border find_border(const S& src, Search f, const RowScale& row, int vocab, const Border in, float share, int rounds,
                               uint32_t* hist, Shared& sh, uint32_t ranks, int& turn) {
     constexpr bool MASS = KIND == kMass;
     const int tid = threadIdx.x, lane = tid & 31;
     Entry *list = reinterpret_cast<Entry*>(hist), *ranked = list + kList;   // once a histogram has been read
-    uint32_t qa = 0, qb = kQMax, ka = kKeyMin, kb = key_of(row.top), ia = 0, ib = (uint32_t)vocab - 1;
-    u64 base = 0;
-    const bool all = in.all();
-    // the digit's value of a token, above `b - a` where it is not one of those left. Tokens of -inf are
-    // left in until the keys are divided: they weigh nothing, and come last in a count.
-    auto digit = [&](int level, float l, int i) -> uint32_t {
-        const uint32_t q = distance(l, row);
-        if (level == 0) return all || in.keeps(key_of(l), i) ? q - qa : ~0u;
-        const uint32_t k = key_of(l);
-        const bool ok = q == qa && k <= kb && k >= ka && (all || in.keeps(k, i));
-        if (level == 1) return ok ? kb - k : ~0u;
-        return ok ? (uint32_t)i - ia : ~0u;
-    };
-    for (int round = 0;; ++round) {
-        // the digit that this round divides: the highest 7 bits of the first interval still open
-        const int level = qa < qb ? 0 : ka < kb ? 1 : 2;
-        const uint32_t a = level == 0 ? qa : level == 1 ? ka : ia, b = level == 0 ? qb : level == 1 ? kb : ib;
-        const uint32_t span = b - a;
-        const int bits = 32 - __clz((int)span);
-        const int shift = bits > kDigit ? bits - kDigit : 0;
-        for (int i = tid; i < kBins * 32 * (MASS ? 2 : 1) / 4; i += kThreads)
-            reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0) sh.nlist = 0;
-        __syncthreads();
-        if (KIND != kMass && round == 0 && all) {   // every token counts
-            each(run, lane, [&](float l, int) { atomicAdd(hist + (distance(l, row) >> shift) * 32 + lane, 1u); });
-        } else each(run, lane, [&](float l, int i) {
-            const uint32_t v = digit(level, l, i);
-            if (v > span) return;
-            uint32_t* h = hist + (v >> shift) * 32 + lane;
-            if (MASS) {
-                const u64 w = weight(l, row, sh.table);
-                if (w != 0) {
-                    atomicAdd(h, (uint32_t)w & 0xfffffu);
-                    atomicAdd(h + kBins * 32, (uint32_t)(w >> 20));
-                }
-            } else {
-                atomicAdd(h, 1u);
-            }
-        });
-        __syncthreads();
-        {   // four threads a bin, eight columns each, taken so that a warp's reads are on different banks
-            const int bin = tid >> 2, c0 = (tid & 3) * 8;
-            u64 v = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {   // a column holds at most 2^11 tokens of 2^20 each: below 2^32
-                const int c = c0 + ((j + bin) & 7);
-                v += hist[bin * 32 + c];
-                if (MASS) v += (u64)hist[(kBins + bin) * 32 + c] << 20;
-            }
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            if ((tid & 3) == 0) sh.mine[turn][bin] = v;
-        }
-        cluster_sync();
-        if (tid < kBins) {
-            u64 v = 0;
-#pragma unroll
-            for (uint32_t r = 0; r < kMaxCluster; ++r) v += r < ranks ? remote_u64(&sh.mine[turn][tid], r) : 0;
-            sh.all[tid] = v;
-        }
-        turn ^= 1;
-        __syncthreads();
-        // every warp: the bin in which the running sum reaches the target
-        u64 v[kBins / 32], mine = 0;
-#pragma unroll
-        for (int j = 0; j < kBins / 32; ++j) {
-            v[j] = sh.all[lane * (kBins / 32) + j];
-            mine += v[j];
-        }
-        const u64 upto = warp_scan(mine, lane);
-        if (round == 0) {
-            const u64 sum = __shfl_sync(0xffffffffu, upto, 31);
-            if (MASS) {   // ceil(share * sum), exactly; 1 at least
-                const u64 s64 = share > 0.f ? __float2ull_rz(share * 0x1p64f) : 0;
-                target = __umul64hi(s64, sum) + (s64 * sum != 0 ? 1 : 0);
-                target = target == 0 ? 1 : target;
-            }
-        }
-        const unsigned reach = __ballot_sync(0xffffffffu, base + upto >= target);
-        if (!reach && KIND != kFirst) return in;   // fewer tokens
-        const int l = reach ? __ffs(reach) - 1 : 31;
-        u64 c = base + upto - mine;
-        int bin = lane * (kBins / 32);
-#pragma unroll
-        for (int j = 0; j < kBins / 32 - 1; ++j) {
-            if (bin == lane * (kBins / 32) + j && c + v[j] < target) {
-                c += v[j];
-                ++bin;
-            }
-        }
-        bin = __shfl_sync(0xffffffffu, bin, l);
-        base = __shfl_sync(0xffffffffu, c, l);
-        const uint32_t lo = (uint32_t)bin << shift, hi = lo + ((1u << shift) - 1);
-        if (level == 1) {   // keys: bins fall from the largest
-            const uint32_t last = kb;
-            kb = last - lo;
-            ka = hi < last - ka ? last - hi : ka;
-        } else if (level == 0) {
-            qb = hi < qb - qa ? qa + hi : qb;
-            qa += lo;
-        } else {
-            ib = hi < ib - ia ? ia + hi : ib;
-            ia += lo;
-        }
+    static_assert(kBins * COLS * 4 * (MASS ? 2 : 1) >= 2 * kList * (int)sizeof(Entry), "");
+    for (int round = rounds;; ++round) {
+        u64 in_bin;
+        if (!divide<KIND, COLS>(src, f, row, in, share, round == 0, hist, sh, ranks, turn, in_bin)) return in;
         if (!MASS) {
-            if ((KIND == kFirst ? base : 0) + sh.all[bin] > kList) continue;
+            if ((KIND == kFirst ? f.base : 0) + in_bin > kList) continue;
         } else if (round == 0 && vocab > 16 * kList) {   // rarely few enough after one digit
             continue;
         }
         // the candidates: this CTA's, then everybody's
-        const int at = qa < qb ? 0 : ka < kb ? 1 : 2;
-        const uint32_t rest = at == 0 ? qb - qa : at == 1 ? kb - ka : ib - ia;
+        const int at = f.level();
+        const uint32_t rest = at == 0 ? f.qb - f.qa : at == 1 ? f.kb - f.ka : f.ib - f.ia;
         __syncthreads();   // the histogram has been read
-        each(run, lane, [&](float l2, int i) {
+        src.pass([&](float l2, int i) {
             if (KIND == kFirst) {   // all up to the interval's last
                 const uint32_t k = key_of(l2);
-                if (at == 0 ? distance(l2, row) > qb : at == 1 ? k < ka : !(Border{ka, (int)ib}.keeps(k, i))) return;
-            } else if (digit(at, l2, i) > rest) {
+                if (at == 0 ? distance(l2, row) > f.qb : at == 1 ? k < f.ka : !(Border{f.ka, (int)f.ib}.keeps(k, i))) return;
+            } else if (f.digit(at, l2, i, row, in) > rest) {
                 return;
             }
             const u64 w = KIND == kCount ? 1 : weight(l2, row, sh.table);
@@ -443,18 +482,69 @@ __device__ Border find_border(const Run& run, const RowScale& row, int vocab, co
         if (total > kList) continue;
         if ((uint32_t)tid < total) {
             const Entry e = ranked[tid];
-            u64 cum = base;
+            u64 cum = f.base;
             for (uint32_t j = 0; j < total; ++j) {
                 const Entry o = ranked[j];
                 if (o.key > e.key || (o.key == e.key && o.idx <= e.idx)) cum += o.w;
             }
-            if (cum >= target && cum - e.w < target) sh.border = Border{e.key, e.idx};
+            if (cum >= f.target && cum - e.w < f.target) sh.border = Border{e.key, e.idx};
         }
         __syncthreads();
         const Border found = sh.border;
         __syncthreads();
         return found;
     }
+}
+
+// Top-p by two passes over the tokens: a histogram of weights, then this warp's sum of what lies before the bin
+// that the border falls into and a list of the bin's tokens, which the rest is done with. sh.part: the warps'
+// kept weights, of tokens with keys from `least` on. False (nothing done) where a list would be too long.
+constexpr int kLong = 1024;
+__device__ bool nucleus(const Run& run, const RowScale& row, int vocab, const Border in, uint32_t least, float share, uint32_t* hist,
+                        Shared& sh, uint32_t ranks, int& turn, int vectors, Border& border) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Search f(row, vocab, in, 0);
+    u64 in_bin;
+    if (tid == 0) sh.nlong = 0;
+    divide<kMass, 32>(Tokens{run}, f, row, in, share, true, hist, sh, ranks, turn, in_bin);
+    Entry* list = reinterpret_cast<Entry*>(hist);
+    u64 w = 0;
+    for (int v = run.v0 + lane; v < run.v1; v += 32) {
+        const float4 x = run.data[v];
+        if (distance(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), row) > f.qb) continue;
+        const float l[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t q = distance(l[j], row), k = key_of(l[j]);
+            const int i = run.base + 4 * v + j;
+            if (q > f.qb || !(f.all || in.keeps(k, i))) continue;
+            const u64 x1 = weight(l[j], row, sh.table);
+            if (q < f.qa) {
+                if (k >= least) w += x1;
+            } else if (x1 != 0) {
+                const uint32_t n = atomicAdd(&sh.nlong, 1u);
+                if (n < kLong) list[n] = Entry{x1, k, i};
+            }
+        }
+    }
+    w = warp_sum(w);
+    if (lane == 0) sh.part[warp] = w;
+    cluster_sync();
+    const uint32_t longest = __reduce_max_sync(0xffffffffu, lane < (int)ranks ? remote_u32(&sh.nlong, (uint32_t)lane) : 0u);
+    if (longest > kLong) return false;
+    const int n = (int)sh.nlong;
+    border = find_border<kMass, 8>(Listed{list, n}, f, row, vocab, in, share, 1, reinterpret_cast<uint32_t*>(list + kLong), sh, ranks, turn);
+    for (int j = tid; j < n; j += kThreads) {
+        const Entry e = list[j];
+        if (border.keeps(e.key, e.idx) && e.key >= least) atomicAdd(&sh.part[(e.idx - run.base) / 4 / vectors], e.w);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        w = warp_sum(lane < kWarps ? sh.part[lane] : 0);
+        if (lane == 0) sh.whole = w;
+    }
+    cluster_sync();
+    return true;
 }
 
 // The first topk (<= kList) tokens of the order and a few more, sh.nlist of them, to `list` of rank 0; false
@@ -658,7 +748,7 @@ __device__ __forceinline__ bool row_top(const Params& p, long long b, uint32_t r
     }
     cluster_sync();
     key = __reduce_max_sync(0xffffffffu, lane < (int)ranks ? remote_u32(&sh.top, (uint32_t)lane) : 0u);
-    top = __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
+    top = logit_of(key);
     if (top != -INFINITY) return true;
     cluster_sync();   // nobody leaves while its shared memory may be read
     if (tid == 0 && rank == 0) {
@@ -867,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         cluster_arrive();   // this CTA has read rank 0's count
         if (!listed) {
             cluster_wait();
-            find_border<kFirst>(run, row, p.vocab, every, (u64)a.topk, 0.f, hist, sh, ranks, turn);
+            find_border<kFirst, 32>(Tokens{run}, Search(row, p.vocab, every, (u64)a.topk), row, p.vocab, every, 0.f, 0, hist, sh, ranks, turn);
             e += kList;
         }
         if (rank == 0)
@@ -877,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         return;   // no CTA reads another's shared memory any more
     }
     if (a.topk > 0 && a.topk < p.vocab) {
-        prefix = find_border<kCount>(run, row, p.vocab, prefix, (u64)a.topk, 0.f, hist, sh, ranks, turn);
+        prefix = find_border<kCount, 32>(Tokens{run}, Search(row, p.vocab, every, (u64)a.topk), row, p.vocab, every, 0.f, 0, hist, sh, ranks, turn);
         border.tighten(prefix);
     }
     bool ready = false;   // the kept sums are there
@@ -896,8 +986,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         const u64 s64 = a.topp > 0.f ? __float2ull_rz(a.topp * 0x1p64f) : 0;
         ready = kept < __umul64hi(s64, all) + (s64 * all != 0 ? 1 : 0);
     }
+    if (!ready && a.topp < 1.f) {
+        Border mass = prefix;
+        ready = nucleus(run, row, p.vocab, prefix, border.key, a.topp, hist, sh, ranks, turn, vpw, mass);
+        if (!ready)
+            mass = find_border<kMass, 32>(Tokens{run}, Search(row, p.vocab, prefix, 0), row, p.vocab, prefix, a.topp, 0, hist, sh, ranks,
+                                          turn);
+        border.tighten(mass);
+    }
     if (!ready) {
-        if (a.topp < 1.f) border.tighten(find_border<kMass>(run, row, p.vocab, prefix, 0, a.topp, hist, sh, ranks, turn));
         u64 w = 0;
         if (border.all()) {
             each(run, lane, [&](float l, int) { w += weight(l, row, sh.table); });   // -inf weighs nothing
@@ -922,15 +1019,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
 // histograms. Otherwise one, as long as a batch has enough rows. More while the batch leaves SMs idle.
 int cluster_for(int64_t batch, int64_t vocab, bool staged) {
     int c = 1;
-    while (c < kMaxCluster && ((staged && vocab > 20000ll * c) || (batch * c * 2 <= 3 * num_sms() && vocab > 2048ll * c))) c *= 2;
+    while (c < kPortableCluster && ((staged && vocab > 20000ll * c) || (batch * c * 2 <= 3 * num_sms() && vocab > 2048ll * c))) c *= 2;
+    if (batch <= kFewRows && vocab > 4096ll * kMaxCluster) c = kMaxCluster;
     return c;
 }
 
 template <typename T>
 cudaError_t sample_go(bool staged, const cudaLaunchConfig_t& cfg, const Params& p, DevError* err) {
-    static std::atomic<unsigned long long> done{0};
+    static std::atomic<unsigned long long> done{0}, large[2] = {};
+    if (cfg.attrs[0].val.clusterDim.x > kPortableCluster) {
+        const void* k = staged ? reinterpret_cast<const void*>(sample_kernel<T>) : reinterpret_cast<const void*>(sample_plain_kernel<T>);
+        const cudaError_t e = allow_once(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, large[staged]);
+        if (e != cudaSuccess) return e;
+    }
     if (!staged) return cudaLaunchKernelEx(&cfg, sample_plain_kernel<T>, p, err);
-    const size_t most = (size_t)(kMaxSampleVocab / kMaxCluster + 8) * 4 + (size_t)kBins * 32 * 8;   // of any call
+    const size_t most = (size_t)(kMaxSampleVocab / kPortableCluster + 8) * 4 + (size_t)kBins * 32 * 8;   // of any call
     const cudaError_t e = allow_smem_once(sample_kernel<T>, most, done);
     return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, sample_kernel<T>, p, err) : e;
 }
