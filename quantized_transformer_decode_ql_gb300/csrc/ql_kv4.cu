@@ -10,7 +10,7 @@
 namespace ql {
 namespace {
 
-constexpr int kKv4Threads = 256;
+constexpr int kKv4Threads = 128;
 
 template <typename T>
 __device__ __forceinline__ void load2(const T* p, float& a, float& b);

@@ -45,17 +45,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
     return r;
 }
 
-// One block of 32 elements, 8 in each of 4 neighbouring lanes (x: this lane's): the stored scale and
-// minimum, and this lane's codes, code[i] = 0x4B400000 + the code of x[i]. All 32 lanes of the warp take
-// part. Each of m, d and the codes is its exact value rounded once:
-//   d  from the difference with its rounding error, compared with the border between its f16 neighbours;
-//   a code from g = (x - m) / (15 d) clamped to [0, 1] in f32, 15 g + 1.5 2^23 leaving the nearest integer
-//      in the low bits. 15 g is off by at most 16 * 6 * 2^-24 < 2^-17 (a difference, a reciprocal good to
-//      2^-23, three products); within 2^-17 of a border the exact difference is compared with it.
-// A block with a value that is not finite decodes to NaN. Returns 0, 1 if the minimum or the scale
-// overflows f16, 2 if a value is not finite.
-__device__ __forceinline__ int kv4_block(const float (&x)[8], uint32_t (&code)[8], __half& dh, __half& mh) {
-    float mn = x[0], mx = x[0];
+// The largest and the smallest of a block of 32 elements, 8 in each of 4 neighbouring lanes.
+__device__ __forceinline__ void kv4_range(const float (&x)[8], float& mn, float& mx) {
+    mn = x[0];
+    mx = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
         mn = fminf(mn, x[i]);
@@ -66,6 +59,13 @@ __device__ __forceinline__ int kv4_block(const float (&x)[8], uint32_t (&code)[8
         mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
         mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
+}
+
+// The stored scale and minimum of a block, each its exact value rounded once: d from the difference with its
+// rounding error, compared with the border between its f16 neighbours. id: 1 / (15 d), 0 where d is.
+// A block with a value that is not finite decodes to NaN. Returns 0, 1 if the minimum or the scale
+// overflows f16, 2 if a value is not finite.
+__device__ __forceinline__ int kv4_scale(float mn, float mx, __half& dh, __half& mh, float& id) {
     mh = __hadd(__float2half_rn(mn), __float2half_rn(0.f));   // a zero minimum is stored as +0
     // mx - mn = s + e exactly
     const float s = __fsub_rn(mx, mn);
@@ -80,19 +80,30 @@ __device__ __forceinline__ int kv4_block(const float (&x)[8], uint32_t (&code)[8
     const float over = __fadd_rn(__fsub_rn(s, 15.0f * border), e);   // 15 border has 16 bits: exact
     const bool up = over > 0.f || (over == 0.f && (lob & 1));
     dh = __ushort_as_half((uint16_t)(lob + (up && lob < 0x7C00u ? 1 : 0)));
-    const float d = __half2float(dh), m = __half2float(mh);
-    float id;
+    const float d = __half2float(dh);
     asm("rcp.approx.f32 %0, %1;" : "=f"(id) : "f"(d));
     id = d > 0.f ? __fmul_rn(id, 1.0f / 15.0f) : 0.f;
-    float off = 0.f, g[8];
+    return !(s < INFINITY) ? 2 : __hisinf(dh) || __hisinf(mh) ? 1 : 0;
+}
+
+// The codes of this lane's 8 elements, code[i] = kCodeOne + the code of x[i], its exact value rounded once: from
+// g = (x - m) / (15 d) clamped to [0, 1] in f32, 15 g + 1.5 2^23 leaving the nearest integer in the low bits.
+// Every step's error is relative: 15 g is off by at most 6 2^-24 of itself (a difference, a reciprocal good to
+// 2^-23, three products). Where 15 g (1 - 2^-20) and 15 g (1 + 2^-20) do not round alike, the exact difference
+// is compared with the border.
+constexpr uint32_t kCodeOne = 0x4B400000u;   // the constant part of a code
+__device__ __forceinline__ void kv4_codes(const float (&x)[8], __half dh, __half mh, float id, uint32_t (&code)[8]) {
+    const float m = __half2float(mh);
+    float g[8];
+    uint32_t apart = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         g[i] = __saturatef(__fmul_rn(__fsub_rn(x[i], m), id));
-        const float r = __fmaf_rn(g[i], 15.0f, 12582912.0f);
-        code[i] = __float_as_uint(r);
-        off = fmaxf(off, fabsf(__fmaf_rn(g[i], 15.0f, -__fsub_rn(r, 12582912.0f))));
+        code[i] = __float_as_uint(__fmaf_rn(g[i], 15.0f * (1.0f + 0x1p-20f), 12582912.0f));
+        apart |= code[i] ^ __float_as_uint(__fmaf_rn(g[i], 15.0f * (1.0f - 0x1p-20f), 12582912.0f));
     }
-    if (off > 0.5f - 0x1p-17f) {
+    if (apart != 0) {
+        const float d = __half2float(dh);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             // x - m = y + ye exactly, against the border (k + 1/2) d, which has 16 bits
@@ -101,26 +112,36 @@ __device__ __forceinline__ int kv4_block(const float (&x)[8], uint32_t (&code)[8
             const float ye = __fadd_rn(__fsub_rn(x[i], __fsub_rn(y, z)), __fsub_rn(-m, z));
             const float v = __fadd_rn(__fsub_rn(y, __fmul_rn(k + 0.5f, d)), ye);
             const bool odd = ((int)k & 1) != 0;
-            if (fabsf(__fmaf_rn(g[i], 15.0f, -k) - 0.5f) < 0x1p-16f)
-                code[i] = 0x4B400000u + (uint32_t)k + (v > 0.f || (v == 0.f && odd) ? 1u : 0u);
+            if (fabsf(__fmaf_rn(g[i], 15.0f, -k) - 0.5f) < 0x1p-15f)
+                code[i] = kCodeOne + (uint32_t)k + (v > 0.f || (v == 0.f && odd) ? 1u : 0u);
         }
     }
-    return !(mx - mn < INFINITY) ? 2 : __hisinf(dh) || __hisinf(mh) ? 1 : 0;
 }
-
-constexpr uint32_t kCodeOne = 0x4B400000u;   // the constant part of a code
 
 // Quantise a key row and a value row into slot `slot` of a record, by LANES neighbouring lanes: this
 // lane is word j (0..3) of block b. xk: elements 4 j + {0..3} and 16 + 4 j + {0..3} of the block of
 // the key row; xv: elements 2 j + 8 q and 2 j + 1 + 8 q (q = 0..3) of the value row, at q and 4 + q.
-// Stores only where `live`; all 32 lanes of the warp take part. Returns what kv4_block does, the larger.
+// Of the 4 lanes of a block two work out the key block's scale, two the value block's.
+// Stores only where `live`; all 32 lanes of the warp take part. Returns what kv4_scale does, the larger.
 template <int HD>
 __device__ __forceinline__ int kv4_put_rows(const float (&xk)[8], const float (&xv)[8], uint8_t* rec, int slot, int b,
                                              int j, bool live) {
     using R = Kv4<HD>;
+    float nk, tk, nv, tv, id;
+    kv4_range(xk, nk, tk);
+    kv4_range(xv, nv, tv);
+    const bool val = j & 1;
+    __half d, m;
+    const int fault = kv4_scale(val ? nv : nk, val ? tv : tk, d, m, id);
+    // the other block's, from the neighbour
+    const __half2 dm = __halves2half2(d, m);
+    const uint32_t own = *reinterpret_cast<const uint32_t*>(&dm), their = __shfl_xor_sync(0xffffffffu, own, 1);
+    const float id2 = __shfl_xor_sync(0xffffffffu, id, 1);
+    const uint32_t wk = val ? their : own, wv = val ? own : their;
+    const __half2 k2 = *reinterpret_cast<const __half2*>(&wk), v2 = *reinterpret_cast<const __half2*>(&wv);
     uint32_t ck[8], cv[8];
-    __half dk, mk, dv, mv;
-    const int fk = kv4_block(xk, ck, dk, mk), fv = kv4_block(xv, cv, dv, mv);
+    kv4_codes(xk, __low2half(k2), __high2half(k2), val ? id2 : id, ck);
+    kv4_codes(xv, __low2half(v2), __high2half(v2), val ? id : id2, cv);
     if (live) {
         // the codes' constant parts add up to a constant each
         uint32_t w = 0u - kCodeOne * 0x11111111u;
@@ -132,14 +153,11 @@ __device__ __forceinline__ int kv4_put_rows(const float (&xk)[8], const float (&
         for (int u = 0; u < 2; ++u)
             *reinterpret_cast<uint16_t*>(vrow + R::vunit(slot, 2 * j + u)) =
                 (uint16_t)(cv[4 * u] + cv[4 * u + 1] * 16u + cv[4 * u + 2] * 256u + cv[4 * u + 3] * 4096u - kCodeOne * 0x1111u);
-        if (j == 0) {
-            reinterpret_cast<__half*>(rec + R::KD)[slot * R::NB + b] = dk;
-            reinterpret_cast<__half*>(rec + R::KM)[slot * R::NB + b] = mk;
-            reinterpret_cast<__half*>(rec + R::VD)[R::vscale(slot, b)] = dv;
-            reinterpret_cast<__half*>(rec + R::VM)[R::vscale(slot, b)] = mv;
-        }
+        // lane 0 the key scale, 1 the value scale, 2 the key minimum, 3 the value minimum
+        const int at = val ? R::VD + 2 * R::vscale(slot, b) : R::KD + 2 * (slot * R::NB + b);
+        *reinterpret_cast<uint16_t*>(rec + at + (j & 2 ? R::KM - R::KD : 0)) = (uint16_t)(j & 2 ? own >> 16 : own);
     }
-    return fk > fv ? fk : fv;
+    return fault;
 }
 #endif
 
