@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const T* __restr
     using R = Kv4<HD>;
     const long long i = ((long long)blockIdx.x * kKv4Threads + threadIdx.x) / R::LANES;
     const int l = threadIdx.x % R::LANES, b = l >> 2, j = l & 3, g = blockIdx.y;
+    pdl_wait();
+    pdl_trigger();
     const bool in = i < n;   // the last warp's spare lanes still take part in its shuffles
     float xk[8] = {}, xv[8] = {};
     long long slot = -1;
@@ -122,6 +124,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __
     bool live[kReadRows];                               // the others still take part in the exchanges
     uint32_t k0[kReadRows], k1[kReadRows], x[kReadRows];
     __half dk[kReadRows], mk[kReadRows], dv[kReadRows], mv[kReadRows];
+    pdl_wait();
+    pdl_trigger();
 #pragma unroll
     for (int r = 0; r < kReadRows; ++r) slot[r] = i0 + r * ROWS < n ? __ldg(slots + i0 + r * ROWS) : -1;
 #pragma unroll
@@ -343,7 +347,7 @@ extern "C" int ql_kv4_write(const void* d_k, const void* d_v, int dtype, int64_t
     if (!err) return set_error(QL_ECUDA, "ql_kv4_write: no device error record");
     auto go = [&](auto kernel, auto zero) {
         using T = decltype(zero);
-        return launch(kernel, dim3(grid, (unsigned)n_kv_heads), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
+        return launch(kernel, dim3(grid, (unsigned)n_kv_heads), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), true,
                       static_cast<const T*>(d_k), static_cast<const T*>(d_v), (long long)k_stride, (long long)v_stride,
                       reinterpret_cast<const long long*>(d_slots), (long long)n,
                       static_cast<uint8_t*>(d_pool), (long long)num_blocks, err);
@@ -369,7 +373,7 @@ extern "C" int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n
     if (!err) return set_error(QL_ECUDA, "ql_kv4_read: no device error record");
     auto go = [&](auto kernel, auto zero) {
         using T = decltype(zero);
-        return launch(kernel, dim3(grid, (unsigned)n_kv_heads), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), false,
+        return launch(kernel, dim3(grid, (unsigned)n_kv_heads), dim3(kKv4Threads), 0, static_cast<cudaStream_t>(stream), true,
                       static_cast<const uint8_t*>(d_pool), reinterpret_cast<const long long*>(d_slots),
                       (long long)n, (long long)num_blocks, static_cast<T*>(d_k),
                       static_cast<T*>(d_v), (long long)k_stride, (long long)v_stride, err);

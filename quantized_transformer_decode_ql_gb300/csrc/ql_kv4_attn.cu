@@ -907,5 +907,5 @@ extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, con
     a.out = static_cast<__half*>(d_out);
     a.workspace = d_workspace;
     a.workspace_bytes = workspace_bytes;
-    return kv4_attn_launch(a, static_cast<cudaStream_t>(stream), false);
+    return kv4_attn_launch(a, static_cast<cudaStream_t>(stream), true);
 }
