@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     }
     __syncwarp();
     pdl_wait();
-    pdl_trigger();
 
     // the whole list's length, then this CTA's run of it and the segment that it starts in; a batch of up to
     // 32 takes one round of loads
@@ -472,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     const bool has = warp < MT;
     const int row = has ? warp : 0;
     int parts = 0, arrival = 0;   // parts written (1: of the segment the window starts in, 2: of the one it ends in); the first's ticket (thread 0)
+    bool deferred = false;        // that ticket is still to be looked at
     auto emit = [&](const Slice& sl, int b, int s) {
         if (!has) return;
         const int kv = p.chunks == 1 ? s : s / p.chunks, c = s - kv * p.chunks;
@@ -748,24 +748,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             float4* to = reinterpret_cast<float4*>(p.slots) + (2 * (size_t)blockIdx.x + end) * ROWS + lane;
             if (has) __stcg(to + row * 32, sl.v);
             if (warp == 0) __stcg(to + MT * 32, sl.t);
+            const bool more = !sg.last(window);
+            const int c0 = quotient(lo + sg.at, per), c1 = quotient(lo + sg.at + sg.nb - 1, per);
             __syncthreads();
-            if (tid == 0) {   // releases the CTA's part (ordered by the barrier); the answer is not looked at before the end
-                const int c0 = quotient(lo + sg.at, per), c1 = quotient(lo + sg.at + sg.nb - 1, per);
+            if (tid == 0) {   // releases the CTA's part (ordered by the barrier)
                 part[end] = {c0, c1, sg.b, sg.s};
                 int n;
-                asm volatile("atom.add.release.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(p.tickets + c0) : "memory");
-                if (end) complete[1] = n == c1 - c0;
-                else arrival = n;
+                if (more) {   // the answer is not looked at before the end
+                    asm volatile("atom.add.release.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(p.tickets + c0) : "memory");
+                    arrival = n;
+                } else {      // acquires the others' parts, where theirs came before
+                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(p.tickets + c0) : "memory");
+                    complete[end] = n == c1 - c0;
+                }
             }
+            if (more) deferred = true;
             parts |= 1 + end;
         }
         if (sg.last(window)) break;
         sg.next(p, S, window);
     }
+    pdl_trigger();   // not before: the next grid's CTAs would take the room of this one's (a decode step of 36 layers 26 us longer)
     if (parts) {   // (the same in every thread)
         if (tid == 0) {
-            if (parts & 1) complete[0] = arrival == part[0].c1 - part[0].c0;
-            asm volatile("fence.acq_rel.gpu;" ::: "memory");   // the others' parts, where theirs came before
+            if (deferred) {
+                complete[0] = arrival == part[0].c1 - part[0].c0;
+                asm volatile("fence.acq_rel.gpu;" ::: "memory");
+            }
             if ((parts & 1) && complete[0]) p.tickets[part[0].c0] = 0;   // armed for the next launch
             if ((parts & 2) && complete[1]) p.tickets[part[1].c0] = 0;
         }
