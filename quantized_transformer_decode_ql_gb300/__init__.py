@@ -17,7 +17,7 @@ from ._lib import (QLError, QL_OK, QL_EINVAL, QL_ENOMEM, QL_ECUDA, QL_EPOOL, QL_
                    QL_GEMV_ACT_INT16, QL_GEMV_ACT_INT8, QL_KV_F16, QL_KV_Q8_0_Q5_1, QL_KV_Q4_1,
                    QL_ATTN_MERGE_TICKET, QL_ATTN_MERGE_CLUSTER,
                    Q4Matrix, LayerDesc, ModelDesc,
-                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, ptr, stream_ptr)
+                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, check_array, check_sampling, ptr, stream_ptr)
 
 __all__ = [
     "QLError", "lib", "ql_q4_0_pack", "ql_q4_0_unpack", "ql_q4_0_pack_device", "ql_gemv_q4_0",
@@ -255,6 +255,7 @@ def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=Non
     """Quantise rows ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided) into one layer's 4-bit
     pool at physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out)."""
     n = slots.numel()
+    check_array("ql_kv4_write", "slots", slots, "torch.int64", 0)
     ks = _row_stride("ql_kv4_write", k, n, n_kv_heads, head_dim)
     vs = _row_stride("ql_kv4_write", v, n, n_kv_heads, head_dim)
     check(lib().ql_kv4_write(ptr(k), ptr(v), _dtype_of("ql_kv4_write", k, v), ks, vs, ptr(slots), n, n_kv_heads,
@@ -264,6 +265,7 @@ def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=Non
 def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None):
     """The values of ``slots`` read back into ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided)."""
     n = slots.numel()
+    check_array("ql_kv4_read", "slots", slots, "torch.int64", 0)
     ks = _row_stride("ql_kv4_read", k, n, n_kv_heads, head_dim)
     vs = _row_stride("ql_kv4_read", v, n, n_kv_heads, head_dim)
     check(lib().ql_kv4_read(ptr(pool), ptr(slots), n, n_kv_heads, head_dim, num_blocks, ptr(k), ptr(v),
@@ -290,6 +292,11 @@ def ql_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None,
     f32) or None. ``probs`` (f32 [batch]): the drawn tokens' probabilities."""
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise QLError(QL_EINVAL, "ql_sample: logits must be [batch, vocab] with contiguous rows")
+    B = logits.shape[0]
+    check_array("ql_sample", "tokens", tokens, "torch.int32", B)
+    check_sampling("ql_sample", B, uniform, temperature, top_k, top_p, min_p)
+    check_array("ql_sample", "probs", probs, "torch.float32", B)
+    check_array("ql_sample", "active", active, "torch.int32", B)
     check(lib().ql_sample(ptr(logits), _dtype_of("ql_sample", logits), logits.stride(0), logits.shape[0],
                           logits.shape[1], ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(uniform),
                           ptr(active), ptr(tokens), ptr(probs), stream_ptr(stream)))

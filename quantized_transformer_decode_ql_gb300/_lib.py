@@ -183,6 +183,22 @@ def ptr(x) -> int | None:
     return x.data_ptr()
 
 
+def check_array(name, what, t, dtype, n):
+    """Refuse what is not None or a contiguous tensor of ``dtype`` with at least ``n`` numbers."""
+    if t is not None and (str(t.dtype) != dtype or t.numel() < n or not t.is_contiguous()):
+        raise QLError(QL_EINVAL, f"{name}: {what} must be a contiguous {dtype} tensor of at least {n} numbers, got "
+                                 f"{tuple(t.shape)} of {t.dtype}")
+
+
+def check_sampling(name, batch, uniform, temperature, top_k, top_p, min_p):
+    """The sampling arrays of a batch."""
+    check_array(name, "uniform", uniform, "torch.float32", batch)
+    check_array(name, "temperature", temperature, "torch.float32", batch)
+    check_array(name, "top_k", top_k, "torch.int32", batch)
+    check_array(name, "top_p", top_p, "torch.float32", batch)
+    check_array(name, "min_p", min_p, "torch.float32", batch)
+
+
 _current_stream = None   # () -> the current stream's address
 
 

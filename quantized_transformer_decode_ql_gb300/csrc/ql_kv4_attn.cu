@@ -363,8 +363,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         const __half* src = p.q + ((size_t)g.b * p.n_heads + kv * p.group + c * kHeads + (h < nh ? h : 0)) * HD + 4 * tq;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            qr[b][0] = __ldg(reinterpret_cast<const uint2*>(src + 32 * b));
-            qr[b][1] = __ldg(reinterpret_cast<const uint2*>(src + 32 * b + 16));
+            for (int k = 0; k < 2; ++k) {   // q is 4-byte aligned
+                const uint32_t* at = reinterpret_cast<const uint32_t*>(src + 32 * b + 16 * k);
+                qr[b][k] = make_uint2(__ldg(at), __ldg(at + 1));
+            }
         }
     };
 

@@ -949,6 +949,9 @@ extern "C" int ql_model_create(const ql_model_desc* desc, ql_model** out) {
                "ql_model_create: need KV pools (k_pool and v_pool, or kvq_pool for the quantised formats)");
     QL_REQUIRE(d.kv_format == QL_KV_F16 || (reinterpret_cast<uintptr_t>(d.kvq_pool) & 15) == 0,
                "ql_model_create: kvq_pool must be 16-byte aligned");
+    QL_REQUIRE(d.kv_format != QL_KV_Q4_1 || (d.num_blocks < (1ll << 31) && d.n_heads > 0 && d.max_blocks_per_seq < (1ll << 27) &&
+                                             d.max_batch * d.max_blocks_per_seq < (1ll << 38) / d.n_heads),
+               "ql_model_create: tables or pool too large for the 4-bit format");
     QL_REQUIRE(d.max_batch >= 1 && d.max_batch <= 4096, "ql_model_create: max_batch out of range");
     QL_REQUIRE(d.max_blocks_per_seq >= 1, "ql_model_create: bad max_blocks_per_seq");
     QL_REQUIRE(d.eps > 0.f && d.rope_theta > 0.0, "ql_model_create: eps and rope_theta must be positive");

@@ -11,8 +11,8 @@ import ctypes
 
 import torch
 
-from ._lib import (LayerDesc, ModelDesc, Q4Matrix, QL_DTYPE_F32, QL_KV_F16, QL_KV_Q4_1, Sampling, StepArgs, check, lib, ptr,
-                   stream_ptr)
+from ._lib import (LayerDesc, ModelDesc, Q4Matrix, QL_DTYPE_F32, QL_EINVAL, QL_KV_F16, QL_KV_Q4_1, QLError, Sampling, StepArgs,
+                   check, check_sampling, lib, ptr, stream_ptr)
 
 BLOCK = 16
 
@@ -167,6 +167,8 @@ class DeviceModel:
         d.num_experts, d.topk, d.moe_inter = cfg.num_experts, cfg.topk, cfg.moe_inter
         d.norm_topk = 1 if cfg.norm_topk else 0
         self._desc = d
+        self._sampling = None          # the arrays of ql_model_set_sampling; those of each captured batch
+        self._graph_sampling = {}
         h = ctypes.c_void_p()
         check(lib().ql_model_create(ctypes.byref(d), ctypes.byref(h)))
         self.handle = h.value
@@ -210,29 +212,40 @@ class DeviceModel:
         """Decode steps issued (or graphs captured) from now on draw their next tokens with the device tensors
         ``uniform`` (f32 [batch] or [batch, numbers]: one per position in turn), ``temperature``, ``top_p``,
         ``min_p`` (f32 [batch]) and ``top_k`` (int32 [batch]); without ``uniform`` they take the arg max again."""
-        self._sampling_tensors = (uniform, temperature, top_k, top_p, min_p)   # the steps read them
         if uniform is None:
             check(lib().ql_model_set_sampling(self.handle, None))
+            self._sampling = None
             return
+        check_sampling("ql_model_set_sampling", uniform.shape[0] if uniform.dim() else 0, uniform, temperature, top_k, top_p, min_p)
+        if uniform.dim() not in (1, 2):
+            raise QLError(QL_EINVAL, "ql_model_set_sampling: uniform must be [batch] or [batch, numbers]")
         s = Sampling(ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(uniform),
                      uniform.shape[1] if uniform.dim() == 2 else 1)
         check(lib().ql_model_set_sampling(self.handle, ctypes.byref(s)))
+        self._sampling = (uniform, temperature, top_k, top_p, min_p)   # the steps read them
+
+    def _sampling_rows(self, args: StepArgs):
+        if self._sampling is not None and args.batch > self._sampling[0].shape[0]:
+            raise QLError(QL_EINVAL, f"a step of batch {args.batch} draws with arrays of {self._sampling[0].shape[0]} rows")
 
     def ql_model_persistent_max_batch(self) -> int:
         return int(lib().ql_model_persistent_max_batch(self.handle))
 
     def ql_decode_step(self, args: StepArgs, stream=None):
+        self._sampling_rows(args)
         check(lib().ql_decode_step(self.handle, ctypes.byref(args), stream_ptr(stream)))
 
     def ql_decode_graph_capture(self, args: StepArgs, stream):
+        self._sampling_rows(args)
         check(lib().ql_decode_graph_capture(self.handle, ctypes.byref(args), stream_ptr(stream)))
+        self._graph_sampling[int(args.batch)] = self._sampling   # its replays read them
 
     def ql_decode_graph_replay(self, batch: int, n_steps: int, stream=None):
         check(lib().ql_decode_graph_replay(self.handle, batch, n_steps, stream_ptr(stream)))
 
     def ql_decode_graph_step_host(self, batch: int, h_tokens, h_next_tokens, stream=None):
         """One replayed step from host buffers (int32 CPU tensors, pinned for asynchronous
-        copies): h_tokens in, the step's greedy tokens out in h_next_tokens on return."""
+        copies): h_tokens in, the step's tokens out in h_next_tokens on return."""
         assert h_tokens.device.type == "cpu" and h_next_tokens.device.type == "cpu"
         check(lib().ql_decode_graph_step_host(self.handle, batch, h_tokens.data_ptr(), h_next_tokens.data_ptr(),
                                               stream_ptr(stream)))
