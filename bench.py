@@ -329,7 +329,7 @@ def attn_alone(B, lo, hi, s, g, seed=6, iters=10, kvq=False):
 def prefill_context(gm, cfg, ids, n_pos, g):
     """Synthetic pre-filled context (stands in for prefill): N(0,1) K and V written straight
     into a slot's blocks of every layer and kv head: as f16 into an f16 pool, quantised on the
-    device (ql_kvq_write) into a quantised one."""
+    device (ql_kvq_write, ql_kv4_write) into a quantised one."""
     import torch
     import quantized_transformer_decode_ql_gb300 as ql
     nb = (n_pos + 15) // 16
@@ -340,7 +340,8 @@ def prefill_context(gm, cfg, ids, n_pos, g):
         for li in range(cfg.n_layers):
             k = torch.randn((n_pos, cfg.n_kv_heads, cfg.head_dim), generator=g, device="cuda")
             v = torch.randn((n_pos, cfg.n_kv_heads, cfg.head_dim), generator=g, device="cuda")
-            ql.ql_kvq_write(k, v, slots, cfg.n_kv_heads, cfg.head_dim, gm.kvq_pool[li], gm.num_blocks)
+            write = ql.ql_kv4_write if gm.kv_format == ql.QL_KV_Q4_1 else ql.ql_kvq_write
+            write(k, v, slots, cfg.n_kv_heads, cfg.head_dim, gm.kvq_pool[li], gm.num_blocks)
         return
     shape = (cfg.n_layers, nb, cfg.n_kv_heads, 16, cfg.head_dim)
     gm.k_pool[:, idx] = torch.randn(shape, generator=g, device="cuda").half()
@@ -349,11 +350,11 @@ def prefill_context(gm, cfg, ids, n_pos, g):
 
 def kv_bytes_per_token(gm, cfg):
     """KV bytes one cached position costs over all layers: f16 K and V, or its share of the
-    quantised records (29 head_dim bytes per 16 positions and kv head)."""
+    quantised records (29 or, in 4 bits, 20 head_dim bytes per 16 positions and kv head)."""
     import quantized_transformer_decode_ql_gb300 as ql
     if gm.kv_format == ql.QL_KV_F16:
         return cfg.n_layers * 2 * cfg.n_kv_heads * cfg.head_dim * 2
-    return cfg.n_layers * cfg.n_kv_heads * 29 * cfg.head_dim / 16
+    return cfg.n_layers * cfg.n_kv_heads * (20 if gm.kv_format == ql.QL_KV_Q4_1 else 29) * cfg.head_dim / 16
 
 
 def build_e1(cfg, steps, warmup):
@@ -744,7 +745,7 @@ def e32_run(gm, cfg, steps, warmup, s, local_rank, world):
                           "frac": round(gbs / peak, 4), "peak": peak, "peak_source": peak_src,
                           "roofline_tokens_s": round(B * peak * 1e9 / float(np.mean(step_bytes)), 1)},
         "replacement_s_excluded": round(repl_s, 3), "replacements": int((finish < steps).sum()),
-        "clocks": clocks, "gpu_launches": launches_per_step(cfg, B) * steps,
+        "clocks": clocks, "gpu_launches": launches_per_step(cfg, B, gm.kv_format) * steps,
         **({"step_phases_us": phases} if phases else {}),
     }
 
@@ -764,7 +765,7 @@ def gpu_arm_e32(args, rank, world, local_rank):
     t_setup = time.time()
     import quantized_transformer_decode_ql_gb300 as ql
     gm = DeviceModel.from_layer_fn(cfg, device_tensor_fn(cfg, seed=0), **e32_pool(cfg, args.steps, args.warmup),
-                                   kv_format=ql.QL_KV_Q8_0_Q5_1 if args.kv == "q8q5" else ql.QL_KV_F16)
+                                   kv_format={"f16": ql.QL_KV_F16, "q8q5": ql.QL_KV_Q8_0_Q5_1, "q4": ql.QL_KV_Q4_1}[args.kv])
     setup_s = time.time() - t_setup
     s = torch.cuda.Stream()
     r = e32_run(gm, cfg, args.steps, args.warmup, s, local_rank, world)
@@ -827,12 +828,15 @@ def gemv_passes(cols, batch):
     return -(-batch // nb_max)
 
 
-def launches_per_step(cfg, B):
+def launches_per_step(cfg, B, kv_format=0):
     """Kernel launches of one step in the one-launch-per-phase form. Batch 1-2: embed, per layer
     qkv / attention / o / gate_up / down GEMVs over the tile stream layout, lm_head, finalize.
     Batch 3-32 (the mma.sync form): each GEMV is the split-K kernel plus its merge kernel; the
     RMSNorm is folded into the merges, so only layer 0's q|k|v GEMV gets an RMSNorm kernel first
-    (every RMSNorm'd GEMV does with QL_BATCHED_NORM_FOLD=0). Above 32: row-major passes."""
+    (every RMSNorm'd GEMV does with QL_BATCHED_NORM_FOLD=0). Above 32: row-major passes. A 4-bit
+    cache (format 2) adds a kernel per layer: the rows normalised, rotated and stored."""
+    if kv_format == 2:
+        return launches_per_step(cfg, B) + cfg.n_layers
     if B <= 2:
         return 3 + 5 * cfg.n_layers
     if B <= 32:
@@ -1302,7 +1306,7 @@ def main():
     ap.add_argument("--config", default="e1", choices=["e1", "e32", "prefill"])
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-e32", action="store_true", help="leave the batch-32 sub-results out of the default line")
-    ap.add_argument("--kv", default="f16", choices=["f16", "q8q5"], help="--config e32: KV cache format")
+    ap.add_argument("--kv", default="f16", choices=["f16", "q8q5", "q4"], help="--config e32: KV cache format")
     ap.add_argument("--no-moe", action="store_true", help="leave the routed-expert sub-result out of the default line")
     ap.add_argument("--no-prefill", action="store_true", help="leave the prefill sub-result out of the default line")
     ap.add_argument("--chunk", type=int, default=256, help="--config prefill: prompt tokens per chunk (1-256)")

@@ -342,8 +342,9 @@ int64_t ql_kv4_record_bytes(int head_dim);
  * dtype (QL_DTYPE_F32 or QL_DTYPE_F16), starts k_stride / v_stride elements after row i - 1 (a
  * slice of a q|k|v projection, say), and goes to slot d_slots[i] % 16 of physical block
  * d_slots[i] / 16 (int64 [n], device). A slot of -1 marks a row to leave out (a padded batch);
- * any other slot outside the pool is skipped and recorded in the device error record, as is a
- * non-finite value or an f16 overflow of a minimum or a scale (the row is still written). The
+ * any other slot outside the pool is skipped and recorded in the device error record. A value that
+ * is not finite (its block then reads back as NaN) and an f16 overflow of a minimum or a scale are
+ * recorded too; the row is still written. The
  * slots of one call must differ from one another: of two rows for one slot, which bytes end
  * there is not determined. d_k, d_v, d_pool and the strides' bytes are multiples of 16; strides
  * at least n_kv_heads * head_dim (any when n is 1). n = 0 is allowed. Asynchronous on stream. */
@@ -360,7 +361,8 @@ int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_
  * errors as for ql_paged_attn_decode, except that any group n_heads / n_kv_heads is taken, that
  * keys of a block id outside the pool are left out of the softmax (and recorded), and that a
  * sequence whose length is outside [0, max_blocks_per_seq * 16] (recorded) or 0 leaves its
- * output row as it was. batch * n_heads < 2^31 / 128. Scores are exact f32 sums over the codes; the
+ * output row as it was. batch <= 65535, batch * n_heads < 2^24, max_blocks_per_seq < 2^27, batch *
+ * max_blocks_per_seq * n_heads < 2^38, num_blocks < 2^31; q and the output 4-byte aligned. Scores are exact f32 sums over the codes; the
  * weights enter the value product as pairs of f16 (22 bits), all sums are f32.
  * d_workspace: ql_paged_attn_kv4_workspace_bytes(...) bytes, 16-byte aligned, ZERO-FILLED before
  * its first use; every call leaves it valid for a next call of any shape that it is large enough
@@ -392,7 +394,8 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  * probability 0. So does a row whose T is negative, NaN or infinite, whose top_p or min_p is NaN
  * or whose u is outside [0, 1), which is recorded in the device error record. d_active
  * int32 [batch] or NULL: rows with 0 are left as they were. Weights are 40-bit fixed-point numbers
- * (relative error 2^-30 before that rounding) and their sums exact, so that the outcome does not
+ * (relative error 2^-29 before that rounding; a token 2^-40 times as likely as the largest is never
+ * drawn) and their sums exact, so that the outcome does not
  * depend on the order of additions. 1 <= vocab <= 360448, batch < 2^31. Asynchronous on stream. */
 int ql_sample(const void* d_logits, int dtype, int64_t row_stride, int64_t batch, int64_t vocab,
               const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,

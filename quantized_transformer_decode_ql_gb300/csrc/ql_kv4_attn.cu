@@ -18,11 +18,22 @@
 // The softmax reference is lazy: p = 2^(x - ref) with ref raised (and the sums rescaled) only when
 // some x exceeds it by 14 binades, so most tiles need one vote instead of a maximum over lanes.
 //
-// Work is a flat list of tiles (16 tokens of one kv head and one group of up to 8 heads), cut into
-// equal runs, one per CTA, whatever the lengths; the 8 warps of a CTA take its tiles in turn, each
-// through its own ring of bulk copies, which runs on across the borders of sequences. At a border the
-// warps' sums are joined in shared memory. A sequence's part that a CTA does not hold whole is written
-// to the workspace, and the CTA that takes the last ticket joins the parts in order.
+// Codes are not negative: the sums of scaled codes and of minima grow while the values that they stand
+// for cancel, and the matrix unit truncates what it adds. Every 8 tiles the minima's sums therefore move
+// into the value sums (settle), which keeps the error at that of the output's rounding at any length.
+//
+// Work is a flat list of places: the tiles (16 tokens of one kv head and one group of up to 8 heads) of
+// each segment (a sequence's kv head and group) and kEntry places for entering and leaving it. The list is
+// cut into equal windows, one per CTA (two on an SM), whatever the lengths; the 8 warps of a CTA take its
+// tiles in turn, each through its own ring of bulk copies, which runs on across the borders of sequences.
+// At a border the warps' sums are joined in shared memory. A segment's part that a CTA does not hold whole
+// is written to the workspace, and the CTA that takes the last ticket joins the parts in order.
+//
+// Measured (HD 128, contexts 128 - 8192, 32 heads on 8, batch 32): 47 us, 3.6 TB/s; 8 heads per kv head and
+// contexts of 20000 - 40960, batch 16: 73 us, 4.3 TB/s (a copy reaches 6.8). About 370 instructions a tile,
+// 55% of the issue slots, 16 warps on an SM (128 registers each): what bounds it is the latency of the
+// instructions of a tile and, for a few tiles a warp, the chain length - table - record - join - parts
+// (9.5 us for 2048 tokens). Copies alone take 36 and 59 us.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>

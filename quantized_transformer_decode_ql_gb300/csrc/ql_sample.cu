@@ -8,12 +8,21 @@
 // The border of top-k (a count) or top-p (a weight) is found by digits, the histogram of 128 bins
 // naming the bin that the border falls into and the next round dividing that bin: 7 bits at a time of
 // the distance from the largest logit on a 23-bit scale of 24 T, then of the logit's ordered bits, then
-// of the index, until few enough candidates are left, which are ranked against one another.
+// of the index, until few enough candidates are left, which are ranked against one another. Two shorter
+// ways, where the lists that they need are long enough: a top-k of up to 128 takes its threshold from the
+// threads' largest logits (list_first), and top-p divides a list of the first histogram's border bin
+// (nucleus), so that two passes over the tokens are all.
 //
 // A row is read once: a thread-block cluster holds it in shared memory, each CTA a run of tokens, and
 // sums, histograms and candidates are exchanged through distributed shared memory, one cluster
 // barrier each; every CTA then draws the same conclusions. A histogram has a column per lane, so that
 // a warp's additions never meet; its weights are split into 20-bit halves that 32-bit sums hold.
+//
+// Measured (vocab 151936): one row with top-k 50 and top-p 0.95 9.4 us, of which the load is 1.3, the
+// largest logit 1.1, the threshold 1.1, the list 2.6 and the draw 2.4: barriers and latency, not memory.
+// Top-p 0.9 alone 21.8 us; 32 rows with top-p 0.9 and min-p 0.02 17 us, no filter 13 us. 256 rows of
+// 50021 without a filter 27.5 us (1.9 TB/s): both passes are near their bounds, memory (8.7 us) and 28
+// instructions a token (8.5 us), on the SMs that hold two rows of the 1.7 there are to each.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>
