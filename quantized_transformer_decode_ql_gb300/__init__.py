@@ -223,24 +223,27 @@ def _dtype_of(name, a, b=None):
     """QL_DTYPE_* of tensors that have to share one type."""
     t = a.dtype
     if b is None or b.dtype == t:
-        code = _DTYPES.get(str(t))
+        code = _CODES.get(t)
+        if code is None:
+            code = _DTYPES.get(str(t))
         if code is not None:
+            _CODES[t] = code
             return code
     raise QLError(QL_EINVAL, f"{name}: tensors must be all float32 or all float16")
 
 
 _DTYPES = {"torch.float32": QL_DTYPE_F32, "torch.float16": QL_DTYPE_F16}
+_CODES = {}   # by the type itself, as they come
 
 
 def _row_stride(name, t, n, n_kv_heads, head_dim):
     """Row stride in elements of a [n, n_kv_heads, head_dim] (or [n, n_kv_heads * head_dim]) tensor whose rows are
     contiguous."""
     shape, strides = t.shape, t.stride()
-    if len(shape) == 3:
-        ok = (shape[0] == n and shape[1] == n_kv_heads and shape[2] == head_dim and
-              strides[2] == 1 and (strides[1] == head_dim or n_kv_heads == 1))
+    if shape == (n, n_kv_heads, head_dim):
+        ok = strides[2] == 1 and (strides[1] == head_dim or n_kv_heads == 1)
     else:
-        ok = len(shape) == 2 and shape[0] == n and shape[1] == n_kv_heads * head_dim and strides[1] == 1
+        ok = shape == (n, n_kv_heads * head_dim) and strides[1] == 1
     if not ok:
         raise QLError(QL_EINVAL, f"{name}: need {n} rows of {n_kv_heads} x {head_dim} with contiguous heads, got "
                                  f"{tuple(shape)} with strides {tuple(strides)}")
@@ -258,8 +261,10 @@ def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=Non
     check_array("ql_kv4_write", "slots", slots, "torch.int64", 0)
     ks = _row_stride("ql_kv4_write", k, n, n_kv_heads, head_dim)
     vs = _row_stride("ql_kv4_write", v, n, n_kv_heads, head_dim)
-    check(lib().ql_kv4_write(ptr(k), ptr(v), _dtype_of("ql_kv4_write", k, v), ks, vs, ptr(slots), n, n_kv_heads,
-                             head_dim, ptr(pool), num_blocks, stream_ptr(stream)))
+    status = lib().ql_kv4_write(k.data_ptr(), v.data_ptr(), _dtype_of("ql_kv4_write", k, v), ks, vs, slots.data_ptr(), n,
+                                n_kv_heads, head_dim, ptr(pool), num_blocks, stream_ptr(stream))
+    if status:
+        check(status)
 
 
 def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None):
@@ -268,8 +273,10 @@ def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None
     check_array("ql_kv4_read", "slots", slots, "torch.int64", 0)
     ks = _row_stride("ql_kv4_read", k, n, n_kv_heads, head_dim)
     vs = _row_stride("ql_kv4_read", v, n, n_kv_heads, head_dim)
-    check(lib().ql_kv4_read(ptr(pool), ptr(slots), n, n_kv_heads, head_dim, num_blocks, ptr(k), ptr(v),
-                            _dtype_of("ql_kv4_read", k, v), ks, vs, stream_ptr(stream)))
+    status = lib().ql_kv4_read(ptr(pool), slots.data_ptr(), n, n_kv_heads, head_dim, num_blocks, k.data_ptr(), v.data_ptr(),
+                               _dtype_of("ql_kv4_read", k, v), ks, vs, stream_ptr(stream))
+    if status:
+        check(status)
 
 
 def ql_paged_attn_kv4_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_blocks_per_seq):

@@ -183,9 +183,17 @@ def ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_NAMES = {}   # a type's name by the type
+
+
 def check_array(name, what, t, dtype, n):
     """Refuse what is not None or a contiguous tensor of ``dtype`` with at least ``n`` numbers."""
-    if t is not None and (str(t.dtype) != dtype or t.numel() < n or not t.is_contiguous()):
+    if t is None:
+        return
+    have = _NAMES.get(t.dtype)
+    if have is None:
+        have = _NAMES[t.dtype] = str(t.dtype)
+    if have != dtype or t.numel() < n or not t.is_contiguous():
         raise QLError(QL_EINVAL, f"{name}: {what} must be a contiguous {dtype} tensor of at least {n} numbers, got "
                                  f"{tuple(t.shape)} of {t.dtype}")
 
