@@ -361,7 +361,7 @@ int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_
  * errors as for ql_paged_attn_decode, except that any group n_heads / n_kv_heads is taken, that
  * keys of a block id outside the pool are left out of the softmax (and recorded), and that a
  * sequence whose length is outside [0, max_blocks_per_seq * 16] (recorded) or 0 leaves its
- * output row as it was. batch <= 65535, batch * n_heads < 2^24, max_blocks_per_seq < 2^27, batch *
+ * output row as it was. batch <= 65535, batch * n_heads < 2^24, max_blocks_per_seq < 2^25, batch *
  * max_blocks_per_seq * n_heads < 2^38, num_blocks < 2^31; q and the output 4-byte aligned. Scores are exact f32 sums over the codes; the
  * weights enter the value product as pairs of f16 (22 bits), all sums are f32.
  * d_workspace: ql_paged_attn_kv4_workspace_bytes(...) bytes, 16-byte aligned, ZERO-FILLED before

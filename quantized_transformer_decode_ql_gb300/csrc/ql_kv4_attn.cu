@@ -906,7 +906,7 @@ extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, con
     QL_REQUIRE(n_heads > 0 && n_kv_heads > 0 && n_heads % n_kv_heads == 0,
                std::string(nm) + ": n_heads must be a multiple of n_kv_heads");
     QL_REQUIRE(batch >= 1 && batch <= 65535 && batch * n_heads < (1ll << 31) / 128, std::string(nm) + ": batch out of range");
-    QL_REQUIRE(max_blocks_per_seq >= 1 && max_blocks_per_seq < (1ll << 27) && num_blocks >= 1 && num_blocks < (1ll << 31),
+    QL_REQUIRE(max_blocks_per_seq >= 1 && max_blocks_per_seq < kKv4MaxBlocks && num_blocks >= 1 && num_blocks < (1ll << 31),
                std::string(nm) + ": bad table or pool size");
     QL_REQUIRE(batch * max_blocks_per_seq < (1ll << 38) / n_heads, std::string(nm) + ": batch * max_blocks_per_seq out of range");
     QL_REQUIRE((reinterpret_cast<uintptr_t>(d_pool) & 15) == 0 && (reinterpret_cast<uintptr_t>(d_workspace) & 15) == 0 &&

@@ -22,6 +22,8 @@ struct Kv4AttnArgs {
     size_t workspace_bytes;
 };
 
+constexpr int64_t kKv4MaxBlocks = 1ll << 25;   // of a table row: the tiles of 32 sequences fit 31 bits
+
 size_t kv4_attn_workspace_bytes();   // of any shape, on the current device
 int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl);
 

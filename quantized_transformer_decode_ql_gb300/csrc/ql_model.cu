@@ -949,7 +949,7 @@ extern "C" int ql_model_create(const ql_model_desc* desc, ql_model** out) {
                "ql_model_create: need KV pools (k_pool and v_pool, or kvq_pool for the quantised formats)");
     QL_REQUIRE(d.kv_format == QL_KV_F16 || (reinterpret_cast<uintptr_t>(d.kvq_pool) & 15) == 0,
                "ql_model_create: kvq_pool must be 16-byte aligned");
-    QL_REQUIRE(d.kv_format != QL_KV_Q4_1 || (d.num_blocks < (1ll << 31) && d.n_heads > 0 && d.max_blocks_per_seq < (1ll << 27) &&
+    QL_REQUIRE(d.kv_format != QL_KV_Q4_1 || (d.num_blocks < (1ll << 31) && d.n_heads > 0 && d.max_blocks_per_seq < kKv4MaxBlocks &&
                                              d.max_batch * d.max_blocks_per_seq < (1ll << 38) / d.n_heads),
                "ql_model_create: tables or pool too large for the 4-bit format");
     QL_REQUIRE(d.max_batch >= 1 && d.max_batch <= 4096, "ql_model_create: max_batch out of range");
