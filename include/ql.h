@@ -347,7 +347,8 @@ int64_t ql_kv4_record_bytes(int head_dim);
  * recorded too; the row is still written. The
  * slots of one call must differ from one another: of two rows for one slot, which bytes end
  * there is not determined. d_k, d_v, d_pool and the strides' bytes are multiples of 16; strides
- * at least n_kv_heads * head_dim (any when n is 1). n = 0 is allowed. Asynchronous on stream. */
+ * at least n_kv_heads * head_dim (any when n is 1); n_kv_heads <= 65535. n = 0 is allowed.
+ * Asynchronous on stream.                                                                    */
 int ql_kv4_write(const void* d_k, const void* d_v, int dtype, int64_t k_stride, int64_t v_stride,
                  const int64_t* d_slots, int64_t n, int n_kv_heads, int head_dim, void* d_pool,
                  int64_t num_blocks, void* stream);
@@ -361,7 +362,7 @@ int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_
  * errors as for ql_paged_attn_decode, except that any group n_heads / n_kv_heads is taken, that
  * keys of a block id outside the pool are left out of the softmax (and recorded), and that a
  * sequence whose length is outside [0, max_blocks_per_seq * 16] (recorded) or 0 leaves its
- * output row as it was. batch <= 65535, batch * n_heads < 2^24, max_blocks_per_seq < 2^25, batch *
+ * output row as it was. batch <= 65535, n_heads <= 2^20, batch * n_heads < 2^24, max_blocks_per_seq < 2^25, batch *
  * max_blocks_per_seq * n_heads < 2^38, num_blocks < 2^31; q and the output 4-byte aligned. Scores are exact f32 sums over the codes; the
  * weights enter the value product as pairs of f16 (22 bits), all sums are f32.
  * d_workspace: ql_paged_attn_kv4_workspace_bytes(...) bytes, 16-byte aligned, ZERO-FILLED before

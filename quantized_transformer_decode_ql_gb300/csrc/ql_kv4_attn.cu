@@ -903,8 +903,8 @@ extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, con
     QL_REQUIRE(d_q && d_pool && d_block_tables && d_context_lens && d_out && d_workspace, std::string(nm) + ": null pointer");
     QL_REQUIRE(head_dim == 64 || head_dim == 128, std::string(nm) + ": head_dim must be 64 or 128");
     QL_REQUIRE(block_size == 16, std::string(nm) + ": block_size must be 16");
-    QL_REQUIRE(n_heads > 0 && n_kv_heads > 0 && n_heads % n_kv_heads == 0,
-               std::string(nm) + ": n_heads must be a multiple of n_kv_heads");
+    QL_REQUIRE(n_heads > 0 && n_heads <= (1 << 20) && n_kv_heads > 0 && n_heads % n_kv_heads == 0,
+               std::string(nm) + ": n_heads must be a multiple of n_kv_heads, 2^20 at most");
     QL_REQUIRE(batch >= 1 && batch <= 65535 && batch * n_heads < (1ll << 31) / 128, std::string(nm) + ": batch out of range");
     QL_REQUIRE(max_blocks_per_seq >= 1 && max_blocks_per_seq < kKv4MaxBlocks && num_blocks >= 1 && num_blocks < (1ll << 31),
                std::string(nm) + ": bad table or pool size");

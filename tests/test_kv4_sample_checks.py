@@ -53,5 +53,5 @@ def test_library_refusals():
     s = ql.Sampling(None, None, None, None, 64, 1)
     assert L.ql_model_set_sampling(None, ctypes.byref(s)) == ql.QL_EINVAL
     assert L.ql_model_set_sampling(None, None) == ql.QL_EINVAL
-    for batch, heads, maxb in ((1, 8, 1 << 27), (1, 8, 1 << 25), (60000, 32, 1 << 26), (65536, 8, 4), (65535, 512, 4)):
+    for batch, heads, maxb in ((1, 8, 1 << 27), (1, 8, 1 << 25), (60000, 32, 1 << 26), (65536, 8, 4), (65535, 512, 4), (1, (1 << 20) + 8, 4)):
         assert L.ql_paged_attn_decode_kv4(64, 1024, 64, 64, batch, heads, 8, 128, 16, maxb, 9, 0.1, 64, 64, 1 << 40, None) == ql.QL_EINVAL
