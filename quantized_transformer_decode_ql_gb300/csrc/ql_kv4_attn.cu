@@ -165,7 +165,8 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     return bar_test(bar, parity) || bar_wait_slow(bar, parity);
 }
 
-// A warp's running state: the value sums (units of 2^-24, odd row halves 16 times that), the minima's
+// A warp's running state: the value sums in units of 2^-24 (rows of the lower half c, of the upper half
+// c + 16 c' with the code c' of their own: whole bytes, which need no mask), the minima's
 // sums (row b < NB) and the weights' sum (row 4), and the references of this lane's two heads.
 template <int HD>
 struct State {
@@ -199,8 +200,8 @@ struct State {
             for (int i = 2 * b; i < 2 * b + 2; ++i) {
                 o[i][0] = fmaf(z0, 0x1p-24f, o[i][0]);
                 o[i][1] = fmaf(z1, 0x1p-24f, o[i][1]);
-                o[i][2] = fmaf(z0, 0x1p-20f, o[i][2]);
-                o[i][3] = fmaf(z1, 0x1p-20f, o[i][3]);
+                o[i][2] = fmaf(z0, 0x1p-20f + 0x1p-24f, o[i][2]);
+                o[i][3] = fmaf(z1, 0x1p-20f + 0x1p-24f, o[i][3]);
             }
         }
         if (lane < HD / 8) z[0] = z[1] = 0.f;
@@ -495,11 +496,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         __half* o = p.out + ((size_t)b * p.n_heads + kv * p.group + c * kHeads + hc) * HD + 16 * warp + gq;
         if (hc < nh) {
             o[0] = __float2half_rn(fmaf(sl.v.x, 0x1p24f, z0) * i0);
-            o[8] = __float2half_rn(fmaf(sl.v.z, 0x1p20f, z0) * i0);
+            o[8] = __float2half_rn(fmaf(sl.v.z - sl.v.x, 0x1p20f, z0) * i0);
         }
         if (hc + 1 < nh) {
             o[HD] = __float2half_rn(fmaf(sl.v.y, 0x1p24f, z1) * i1);
-            o[HD + 8] = __float2half_rn(fmaf(sl.v.w, 0x1p20f, z1) * i1);
+            o[HD + 8] = __float2half_rn(fmaf(sl.v.w - sl.v.y, 0x1p20f, z1) * i1);
         }
     };
 
@@ -575,9 +576,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float a[4];
-                const uint32_t wa8 = wa[b] >> 8, wb8 = wb[b] >> 8;
-                mma16_first(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, wa8 & 0x000f000fu, wb8 & 0x000f000fu, ql[b][0], ql[b][1], zero);
-                mma16(a, wa[b] & 0x00f000f0u, wb[b] & 0x00f000f0u, wa8 & 0x00f000f0u, wb8 & 0x00f000f0u, qh[b][0], qh[b][1]);
+                const uint32_t wa8 = __byte_perm(wa[b], 0u, 0x4341), wb8 = __byte_perm(wb[b], 0u, 0x4341);
+                const uint32_t la8 = wa8 & 0x000f000fu, lb8 = wb8 & 0x000f000fu;
+                mma16_first(a, wa[b] & 0x000f000fu, wb[b] & 0x000f000fu, la8, lb8, ql[b][0], ql[b][1], zero);
+                // the upper codes of the upper bytes as a difference (exact): another pipe than the masks'
+                mma16(a, wa[b] & 0x00f000f0u, wb[b] & 0x00f000f0u, u32(__hsub2(h2(wa8), h2(la8))), u32(__hsub2(h2(wb8), h2(lb8))), qh[b][0], qh[b][1]);
                 const float2 d0 = __half22float2(h2(da[b / 2])), d1 = __half22float2(h2(db[b / 2]));
                 const float x0 = b & 1 ? d0.y : d0.x, x1 = b & 1 ? d1.y : d1.x;
                 s[0] = fmaf(x0, a[0], s[0]);
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 plo[k] = transposed(u32(__floats2half2_rn(p0 - hf.x, p1 - hf.y)));
             }
         };
-        // values: O^T, A rows elements gq (+ 8, 16 times) of a 16-element half block, its columns the slots
+        // values: O^T, A rows elements gq (+ 8, as whole bytes) of a 16-element half block, its columns the slots
         auto value = [&](uint32_t rec) {
             uint32_t v[4][NB / 2], vd[2][NB];
             lds_words(vd[0], rec + offVD);
@@ -684,12 +687,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 }
                 const uint32_t x = __byte_perm(v[0][b / 2], v[1][b / 2], b & 1 ? 0x7632 : 0x5410);
                 const uint32_t y = __byte_perm(v[2][b / 2], v[3][b / 2], b & 1 ? 0x7632 : 0x5410);
-                const uint32_t x8 = x >> 8, y8 = y >> 8;
-                mma16(st.o[2 * b], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, ph_[0], ph_[1]);
-                mma16(st.o[2 * b + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, ph_[0], ph_[1]);
+                const uint32_t x8 = __byte_perm(x, 0u, 0x4341), y8 = __byte_perm(y, 0u, 0x4341);
+                const uint32_t x0 = x & 0x000f000fu, x1 = x & 0x00ff00ffu, y0 = y & 0x000f000fu, y1 = y & 0x00ff00ffu;
+                const uint32_t x2 = x8 & 0x000f000fu, y2 = y8 & 0x000f000fu;
+                mma16(st.o[2 * b], x0, x1, y0, y1, ph_[0], ph_[1]);
+                mma16(st.o[2 * b + 1], x2, x8, y2, y8, ph_[0], ph_[1]);
                 if (!DUP) {
-                    mma16(st.o[2 * b], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, pl_[0], pl_[1]);
-                    mma16(st.o[2 * b + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, pl_[0], pl_[1]);
+                    mma16(st.o[2 * b], x0, x1, y0, y1, pl_[0], pl_[1]);
+                    mma16(st.o[2 * b + 1], x2, x8, y2, y8, pl_[0], pl_[1]);
                 }
             }
         };
