@@ -425,19 +425,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     };
     unsigned bad = 0;                  // stages without a record (a block id outside the pool, or a failed wait)
     bool dead = false;                 // a wait ran out: no more copies
-    // copy the next tile to the stage at rec
+    // copy the next tile to the stage at rec; what is rare is behind one vote
     auto issue = [&](uint32_t rec) {
+        if (pend == 0) return;   // none left
         const int phys = __shfl_sync(0xffffffffu, ids, pblk / kWarps);
-        const bool in = (unsigned)phys < (unsigned)p.num_blocks;
-        if (in && bad == 0) {
-            asm volatile(
-                "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
-                "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-                "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%2], [%3], %1, [%0], %4;\n}"
-                ::"r"(rec + REC), "r"(REC), "r"(rec), "l"(p.pool + ((size_t)(unsigned)phys * rec_stride + pofs)), "l"(policy), "r"(elected)
-                : "memory");
-        } else {
-            if (pend == 0) return;
+        const bool in = (unsigned)phys < (unsigned)p.num_blocks, go = in && bad == 0;
+        const uint8_t* const from = p.pool + ((size_t)(unsigned)phys * rec_stride + pofs);
+        asm volatile(
+            "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
+            "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+            "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%2], [%3], %1, [%0], %4;\n}" ::"r"(
+                rec + REC),
+            "r"(REC), "r"(rec), "l"(from), "l"(policy), "r"(go ? elected : 0u)
+            : "memory");
+        pblk += kWarps;
+        if (!__any_sync(0xffffffffu, !go || pblk >= pend || (pblk & (31 * kWarps)) == 0)) return;
+        if (!go) {
             const unsigned bit = 1u << ((rec - ring) / STAGE);
             bad = in && !dead ? bad & ~bit : bad | bit;
             if (lane == 0) {
@@ -445,16 +448,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(rec + REC), "r"(REC) : "memory");
                     asm volatile(
                         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                        "[%3], %4;" ::"r"(rec), "l"(p.pool + ((size_t)(unsigned)phys * rec_stride + pofs)), "r"(REC), "r"(rec + REC), "l"(policy)
+                        "[%3], %4;" ::"r"(rec), "l"(from), "r"(REC), "r"(rec + REC), "l"(policy)
                         : "memory");
                 } else {
                     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(rec + REC) : "memory");
-                    if (!dead) record_device_error(err, kErrAttnBlock, (long long)ahead[warp].b * p.maxb + pblk, phys);
+                    if (!dead) record_device_error(err, kErrAttnBlock, (long long)ahead[warp].b * p.maxb + pblk - kWarps, phys);
                 }
             }
             __syncwarp();
         }
-        pblk += kWarps;
         if (pblk >= pend) cross();
         else if ((pblk & (31 * kWarps)) == 0) {
             ids = later;
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     if (pblk < pend) look();
     else cross();
 #pragma unroll 1
-    for (int i = 0; i < kStages; ++i) issue(ring + i * STAGE);
+    for (int i = 0; i < kStages && pend != 0; ++i) issue(ring + i * STAGE);
 
     St st;
     float zero[4];
@@ -618,36 +620,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             uint32_t vd[2][NB];
             lds_words(vd[0], rec + offVD);
             lds_words(vd[1], rec + offVD + 4 * NB);
-            __half2 dmax = __hmax2(h2(vd[0][0]), h2(vd[1][0]));
+            uint32_t large = 0;   // a scale of 2 or more (or a NaN) has bit 14 set
 #pragma unroll
-            for (int b = 1; b < NB; ++b) dmax = __hmax2(dmax, __hmax2(h2(vd[0][b]), h2(vd[1][b])));
+            for (int b = 0; b < NB; ++b) large |= vd[0][b] | vd[1][b];
             const float over = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-            if (__any_sync(0xffffffffu, over > top || !__hble2(dmax, dlim))) {
-                float m0 = fmaxf(s[0] * fac[0], s[2] * fac[0]), m1 = fmaxf(s[1] * fac[1], s[3] * fac[1]);
-                float dw = fmaxf(__low2float(dmax), __high2float(dmax));
+            if (__any_sync(0xffffffffu, over > top || (large & 0x40004000u) != 0)) {
+                __half2 dmax = __hmax2(h2(vd[0][0]), h2(vd[1][0]));
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                for (int b = 1; b < NB; ++b) dmax = __hmax2(dmax, __hmax2(h2(vd[0][b]), h2(vd[1][b])));
+                if (__any_sync(0xffffffffu, over > top || !__hble2(dmax, dlim))) {
+                    float m0 = fmaxf(s[0] * fac[0], s[2] * fac[0]), m1 = fmaxf(s[1] * fac[1], s[3] * fac[1]);
+                    float dw = fmaxf(__low2float(dmax), __high2float(dmax));
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) dw = fmaxf(dw, __shfl_xor_sync(0xffffffffu, dw, o));
+                    // p and p d stay below 2^15: the largest scale is at most 2^(15 - top)
+                    const float old = top;
+                    float lim = __low2float(dlim);
+                    while (top > 1.f && dw > lim) {
+                        top -= 1.f;
+                        lim *= 2.f;
+                    }
+                    dlim = __float2half2_rn(lim);
+                    // the largest weight so far becomes 2^(top - 6): room for 6 binades before the next move
+                    const float r0 = fmaxf(st.ref[0] + (old - top), m0 - top + 6.f), r1 = fmaxf(st.ref[1] + (old - top), m1 - top + 6.f);
+                    st.scale(exp2_fast(st.ref[0] - r0), exp2_fast(st.ref[1] - r1));
+                    st.ref[0] = r0;
+                    st.ref[1] = r1;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (t[k] != -INFINITY) t[k] = fmaf(s[k], fac[k & 1], -st.ref[k & 1]);
                 }
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) dw = fmaxf(dw, __shfl_xor_sync(0xffffffffu, dw, o));
-                // p and p d stay below 2^15: the largest scale is at most 2^(15 - top)
-                const float old = top;
-                float lim = __low2float(dlim);
-                while (top > 1.f && dw > lim) {
-                    top -= 1.f;
-                    lim *= 2.f;
-                }
-                dlim = __float2half2_rn(lim);
-                // the largest weight so far becomes 2^(top - 6): room for 6 binades before the next move
-                const float r0 = fmaxf(st.ref[0] + (old - top), m0 - top + 6.f), r1 = fmaxf(st.ref[1] + (old - top), m1 - top + 6.f);
-                st.scale(exp2_fast(st.ref[0] - r0), exp2_fast(st.ref[1] - r1));
-                st.ref[0] = r0;
-                st.ref[1] = r1;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (t[k] != -INFINITY) t[k] = fmaf(s[k], fac[k & 1], -st.ref[k & 1]);
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             }
         };
         auto arrived = [&]() {   // the record at rec
-            if (!bar_wait(rec + REC, parity)) {
+            if (!__all_sync(0xffffffffu, bar_test(rec + REC, parity)) && !__all_sync(0xffffffffu, bar_wait_slow(rec + REC, parity))) {
                 if (!dead && lane == 0) record_device_error(err, kErrAttnStage, sg.b, blk);
                 dead = true;
                 bad = ~0u;
