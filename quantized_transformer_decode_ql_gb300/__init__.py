@@ -299,14 +299,20 @@ def ql_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None,
     f32) or None. ``probs`` (f32 [batch]): the drawn tokens' probabilities."""
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise QLError(QL_EINVAL, "ql_sample: logits must be [batch, vocab] with contiguous rows")
-    B = logits.shape[0]
+    B, V = logits.shape
+    check_array("ql_sample", "uniform", uniform, "torch.float32", B)
     check_array("ql_sample", "tokens", tokens, "torch.int32", B)
-    check_sampling("ql_sample", B, uniform, temperature, top_k, top_p, min_p)
-    check_array("ql_sample", "probs", probs, "torch.float32", B)
-    check_array("ql_sample", "active", active, "torch.int32", B)
-    check(lib().ql_sample(ptr(logits), _dtype_of("ql_sample", logits), logits.stride(0), logits.shape[0],
-                          logits.shape[1], ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(uniform),
-                          ptr(active), ptr(tokens), ptr(probs), stream_ptr(stream)))
+    real, whole = uniform.dtype, tokens.dtype
+    for t, kind in ((temperature, real), (top_k, whole), (top_p, real), (min_p, real), (probs, real), (active, whole)):
+        if t is not None and (t.dtype is not kind or t.numel() < B or not t.is_contiguous()):
+            check_sampling("ql_sample", B, uniform, temperature, top_k, top_p, min_p)
+            check_array("ql_sample", "probs", probs, "torch.float32", B)
+            check_array("ql_sample", "active", active, "torch.int32", B)
+    status = lib().ql_sample(logits.data_ptr(), _dtype_of("ql_sample", logits), logits.stride(0), B, V, ptr(temperature),
+                             ptr(top_k), ptr(top_p), ptr(min_p), uniform.data_ptr(), ptr(active), tokens.data_ptr(),
+                             ptr(probs), stream_ptr(stream))
+    if status:
+        check(status)
 
 
 def ql_paged_attn_decode_noalloc(q, k_pool, v_pool, block_tables, context_lens, batch, n_heads,

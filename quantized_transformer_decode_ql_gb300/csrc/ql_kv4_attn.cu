@@ -4,7 +4,8 @@
 // The bound is HBM: 20 HD bytes per 16 tokens and kv head. Both products run on mma.sync m16n8k16
 // with the 4-bit codes as the A operand and up to 8 query heads as the 8 columns, and no code is
 // ever decoded: (word & 0x000f000f) is a pair of subnormal f16 numbers c 2^-24, which the matrix unit
-// multiplies exactly, and (word & 0x00f000f0) a pair 16 times that. The scales stay outside:
+// multiplies exactly, (word & 0x00f000f0) a pair 16 times that and (word & 0x00ff00ff) the sum of both;
+// the upper bytes come down by a byte permutation. The scales stay outside:
 //   S^T = K Q^T: one f32 sum per (key, head) and 32-element block, sum_i q_i c_i, then
 //         s = sum_b d_b sum_b + sum_b m_b (sum_i q_i), the last product one m16n8k8 MMA of the minima
 //         with the q sums in two f16 parts. q is brought to [2^14, 2^15) by a power of two (exact),
@@ -29,11 +30,11 @@
 // At a border the warps' sums are joined in shared memory. A segment's part that a CTA does not hold whole
 // is written to the workspace, and the CTA that takes the last ticket joins the parts in order.
 //
-// Measured (HD 128, contexts 128 - 8192, 32 heads on 8, batch 32): 47 us, 3.6 TB/s; 8 heads per kv head and
-// contexts of 20000 - 40960, batch 16: 73 us, 4.3 TB/s (a copy reaches 6.8). About 370 instructions a tile,
-// 55% of the issue slots, 16 warps on an SM (128 registers each): what bounds it is the latency of the
-// instructions of a tile and, for a few tiles a warp, the chain length - table - record - join - parts
-// (9.5 us for 2048 tokens). Copies alone take 36 and 59 us.
+// Measured (HD 128, contexts 128 - 8192, 32 heads on 8, batch 32): 47 us, 3.7 TB/s; 8 heads per kv head and
+// contexts of 20000 - 40960, batch 16: 70 us, 4.4 TB/s (a copy reaches 6.8). About 370 instructions a tile,
+// half of them on the pipe that takes one in two cycles, 55% of the issue slots, 16 warps on an SM (128
+// registers each): what bounds it is the latency of a tile's instructions and, for a few tiles a warp, the
+// chain length - table - record - join - parts (9.3 us for 2048 tokens). Copies alone take 36 and 59 us.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <math.h>

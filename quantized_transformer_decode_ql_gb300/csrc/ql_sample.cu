@@ -1027,7 +1027,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
 // histograms. Otherwise one, as long as a batch has enough rows. More while the batch leaves SMs idle.
 int cluster_for(int64_t batch, int64_t vocab, bool staged) {
     int c = 1;
-    while (c < kPortableCluster && ((staged && vocab > 20000ll * c) || (batch * c * 2 <= 3 * num_sms() && vocab > 2048ll * c))) c *= 2;
+    const int sms = num_sms();
+    while (c < kPortableCluster && ((staged && vocab > 20000ll * c) || (batch * c * 2 <= 3 * sms && vocab > 2048ll * c))) c *= 2;
     if (batch <= kFewRows && vocab > 4096ll * kMaxCluster) c = kMaxCluster;
     return c;
 }
