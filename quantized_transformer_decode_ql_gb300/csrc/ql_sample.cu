@@ -69,6 +69,8 @@ struct Params {
     const int32_t* active;
     int32_t* tokens;
     float* probs;
+    bool early;   // the next grid may start at once: this one leaves it half of the SMs (on shared ones its CTAs
+                  // would come to lie unevenly: 256 rows after 256 rows 34.0 us against 27.5)
 };
 
 // ---- the cluster
@@ -286,6 +288,7 @@ __device__ __forceinline__ void each(const Stream<T>& s, int lane, F f) {
 
 // What a search passes over: the CTA's run, or a list of its entries.
 struct Tokens {
+    static constexpr bool kAll = true;
     Run run;
     template <typename F>
     __device__ __forceinline__ void pass(F f) const {
@@ -296,6 +299,7 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
 }
 struct Listed {
+    static constexpr bool kAll = false;
     const Entry* e;
     int n;
     template <typename F>
@@ -347,6 +351,22 @@ __device__ bool divide(const S& src, Search& f, const RowScale& row, const Borde
     __syncthreads();
     if (KIND != kMass && first && f.all) {   // every token counts
         src.pass([&](float l, int) { atomicAdd(hist + (distance(l, row) >> shift) * COLS + lane % COLS, 1u); });
+    } else if (MASS && S::kAll && first && f.all) {
+        if constexpr (S::kAll) {   // four tokens at a time and no branches: their chains overlap (a weight of 0 adds nothing)
+            for (int v = src.run.v0 + lane; v < src.run.v1; v += 32) {
+                const float4 x = src.run.data[v];
+                const float l[4] = {x.x, x.y, x.z, x.w};
+                u64 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = weight(l[j], row, sh.table);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t* h = hist + (distance(l[j], row) >> shift) * COLS + lane % COLS;
+                    atomicAdd(h, (uint32_t)w[j] & 0xfffffu);
+                    atomicAdd(h + kBins * COLS, (uint32_t)(w[j] >> 20));
+                }
+            }
+        }
     } else src.pass([&](float l, int i) {
         const uint32_t v = f.digit(level, l, i, row, in);
         if (v > span) return;
@@ -429,21 +449,25 @@ __device__ bool divide(const S& src, Search& f, const RowScale& row, const Borde
 }
 
 // The border, from the interval that f has come to (`rounds` of them done); `in` where there are fewer tokens.
+// few: what is left fits the lists already.
 template <int KIND, int COLS, typename S>
 __device__ Border find_border(const S& src, Search f, const RowScale& row, int vocab, const Border in, float share, int rounds,
-                              uint32_t* hist, Shared& sh, uint32_t ranks, int& turn) {
+                              uint32_t* hist, Shared& sh, uint32_t ranks, int& turn, bool few = false) {
     constexpr bool MASS = KIND == kMass;
     const int tid = threadIdx.x, lane = tid & 31;
     Entry *list = reinterpret_cast<Entry*>(hist), *ranked = list + kList;   // once a histogram has been read
     static_assert(kBins * COLS * 4 * (MASS ? 2 : 1) >= 2 * kList * (int)sizeof(Entry), "");
     for (int round = rounds;; ++round) {
-        u64 in_bin;
-        if (!divide<KIND, COLS>(src, f, row, in, share, round == 0, hist, sh, ranks, turn, in_bin)) return in;
-        if (!MASS) {
-            if ((KIND == kFirst ? f.base : 0) + in_bin > kList) continue;
-        } else if (round == 0 && vocab > 16 * kList) {   // rarely few enough after one digit
-            continue;
+        if (!few) {
+            u64 in_bin;
+            if (!divide<KIND, COLS>(src, f, row, in, share, round == 0, hist, sh, ranks, turn, in_bin)) return in;
+            if (!MASS) {
+                if ((KIND == kFirst ? f.base : 0) + in_bin > kList) continue;
+            } else if (round == 0 && vocab > 16 * kList) {   // rarely few enough after one digit
+                continue;
+            }
         }
+        few = false;
         // the candidates: this CTA's, then everybody's
         const int at = f.level();
         const uint32_t rest = at == 0 ? f.qb - f.qa : at == 1 ? f.kb - f.ka : f.ib - f.ia;
@@ -489,15 +513,18 @@ __device__ Border find_border(const S& src, Search f, const RowScale& row, int v
             return in;
         }
         if (total > kList) continue;
-        if ((uint32_t)tid < total) {
-            const Entry e = ranked[tid];
-            u64 cum = f.base;
-            for (uint32_t j = 0; j < total; ++j) {
-                const Entry o = ranked[j];
-                if (o.key > e.key || (o.key == e.key && o.idx <= e.idx)) cum += o.w;
-            }
-            if (cum >= f.target && cum - e.w < f.target) sh.border = Border{e.key, e.idx};
+        static_assert(4 * kList == kThreads, "four threads a candidate");
+        const Entry e = (uint32_t)tid / 4 < total ? ranked[tid / 4] : Entry{0, 0, 0};
+        u64 cum = 0;
+#pragma unroll 4
+        for (uint32_t j = tid & 3; j < total; j += 4) {
+            const Entry o = ranked[j];
+            if (o.key > e.key || (o.key == e.key && o.idx <= e.idx)) cum += o.w;
         }
+        cum += __shfl_xor_sync(0xffffffffu, cum, 1);
+        cum += __shfl_xor_sync(0xffffffffu, cum, 2);
+        cum += f.base;
+        if ((uint32_t)tid / 4 < total && (tid & 3) == 0 && cum >= f.target && cum - e.w < f.target) sh.border = Border{e.key, e.idx};
         __syncthreads();
         const Border found = sh.border;
         __syncthreads();
@@ -518,31 +545,35 @@ __device__ bool nucleus(const Run& run, const RowScale& row, int vocab, const Bo
     divide<kMass, 32>(Tokens{run}, f, row, in, share, true, hist, sh, ranks, turn, in_bin);
     Entry* list = reinterpret_cast<Entry*>(hist);
     u64 w = 0;
-    for (int v = run.v0 + lane; v < run.v1; v += 32) {
-        const float4 x = run.data[v];
-        if (distance(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), row) > f.qb) continue;
+    for (int v0 = run.v0; v0 < run.v1; v0 += 32) {
+        const int v = v0 + lane;
+        const float4 x = v < run.v1 ? run.data[v] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (!__any_sync(0xffffffffu, distance(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), row) <= f.qb)) continue;
         const float l[4] = {x.x, x.y, x.z, x.w};
+        u64 x1[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x1[j] = weight(l[j], row, sh.table);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t q = distance(l[j], row), k = key_of(l[j]);
             const int i = run.base + 4 * v + j;
-            if (q > f.qb || !(f.all || in.keeps(k, i))) continue;
-            const u64 x1 = weight(l[j], row, sh.table);
-            if (q < f.qa) {
-                if (k >= least) w += x1;
-            } else if (x1 != 0) {
+            const bool here = f.all || in.keeps(k, i);
+            w += here && q < f.qa && k >= least ? x1[j] : 0;
+            if (here && q >= f.qa && q <= f.qb && x1[j] != 0) {
                 const uint32_t n = atomicAdd(&sh.nlong, 1u);
-                if (n < kLong) list[n] = Entry{x1, k, i};
+                if (n < kLong) list[n] = Entry{x1[j], k, i};
             }
         }
     }
     w = warp_sum(w);
     if (lane == 0) sh.part[warp] = w;
     cluster_sync();
-    const uint32_t longest = __reduce_max_sync(0xffffffffu, lane < (int)ranks ? remote_u32(&sh.nlong, (uint32_t)lane) : 0u);
-    if (longest > kLong) return false;
+    const uint32_t len = lane < (int)ranks ? remote_u32(&sh.nlong, (uint32_t)lane) : 0u;
+    if (__reduce_max_sync(0xffffffffu, len) > kLong) return false;
+    const bool few = __reduce_add_sync(0xffffffffu, len) <= kList;
     const int n = (int)sh.nlong;
-    border = find_border<kMass, 8>(Listed{list, n}, f, row, vocab, in, share, 1, reinterpret_cast<uint32_t*>(list + kLong), sh, ranks, turn);
+    border = find_border<kMass, 8>(Listed{list, n}, f, row, vocab, in, share, 1, reinterpret_cast<uint32_t*>(list + kLong), sh, ranks, turn,
+                                    few);
     for (int j = tid; j < n; j += kThreads) {
         const Entry e = list[j];
         if (border.keeps(e.key, e.idx) && e.key >= least) atomicAdd(&sh.part[(e.idx - run.base) / 4 / vectors], e.w);
@@ -863,7 +894,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, Dev
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const long long b = blockIdx.x / ranks;
-    pdl_wait();   // and no trigger: the next grid's CTAs would come to SMs unevenly (256 rows after 256 rows: 34.0 us against 27.5)
+    pdl_wait();
+    if (p.early) pdl_trigger();
     RowArgs a;
     if (!row_loads(p, b, a)) return;
     const int first = (int)rank * p.per;
@@ -923,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const long long b = blockIdx.x / ranks;
     pdl_wait();
-    pdl_trigger();
+    if (p.early) pdl_trigger();
     RowArgs a;
     if (!row_loads(p, b, a)) return;
     const int first = (int)rank * p.per;
@@ -1070,6 +1102,7 @@ int sample_launch(const SampleArgs& a, cudaStream_t s, bool pdl) {
     p.active = a.active;
     p.tokens = a.tokens;
     p.probs = a.probs;
+    p.early = a.batch * c * 2 <= num_sms();
     const size_t smem = staged ? (size_t)(p.per + 8) * 4 + (size_t)kBins * 32 * (a.top_p ? 8 : 4) : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.batch * c));
