@@ -20,7 +20,7 @@
 //
 // Measured (vocab 151936): one row with top-k 50 and top-p 0.95 9.4 us, of which the load is 1.3, the
 // largest logit 1.1, the threshold 1.1, the list 2.6 and the draw 2.4: barriers and latency, not memory.
-// Top-p 0.9 alone 21.8 us; 32 rows with top-p 0.9 and min-p 0.02 17 us, no filter 13 us. 256 rows of
+// Top-p 0.9 alone 20.5 us (15.0 at T 0.3), 34 us for 32 rows; 32 rows with min-p 0.02 too 17 us, no filter 13 us. 256 rows of
 // 50021 without a filter 27.5 us (1.9 TB/s): both passes are near their bounds, memory (8.7 us) and 28
 // instructions a token (8.5 us), on the SMs that hold two rows of the 1.7 there are to each.
 #include <cuda_fp16.h>
@@ -545,23 +545,21 @@ __device__ bool nucleus(const Run& run, const RowScale& row, int vocab, const Bo
     divide<kMass, 32>(Tokens{run}, f, row, in, share, true, hist, sh, ranks, turn, in_bin);
     Entry* list = reinterpret_cast<Entry*>(hist);
     u64 w = 0;
-    for (int v0 = run.v0; v0 < run.v1; v0 += 32) {
-        const int v = v0 + lane;
-        const float4 x = v < run.v1 ? run.data[v] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (!__any_sync(0xffffffffu, distance(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), row) <= f.qb)) continue;
+    for (int v = run.v0 + lane; v < run.v1; v += 32) {
+        const float4 x = run.data[v];
+        if (distance(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)), row) > f.qb) continue;
         const float l[4] = {x.x, x.y, x.z, x.w};
-        u64 x1[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x1[j] = weight(l[j], row, sh.table);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t q = distance(l[j], row), k = key_of(l[j]);
             const int i = run.base + 4 * v + j;
-            const bool here = f.all || in.keeps(k, i);
-            w += here && q < f.qa && k >= least ? x1[j] : 0;
-            if (here && q >= f.qa && q <= f.qb && x1[j] != 0) {
+            if (q > f.qb || !(f.all || in.keeps(k, i))) continue;
+            const u64 x1 = weight(l[j], row, sh.table);
+            if (q < f.qa) {
+                if (k >= least) w += x1;
+            } else if (x1 != 0) {
                 const uint32_t n = atomicAdd(&sh.nlong, 1u);
-                if (n < kLong) list[n] = Entry{x1[j], k, i};
+                if (n < kLong) list[n] = Entry{x1, k, i};
             }
         }
     }
