@@ -14,7 +14,7 @@
 namespace ql {
 namespace {
 
-constexpr int kKv4Threads = 128;
+constexpr int kKv4Threads = 128;   // with 256 a prompt written and read back takes 25.4 us instead of 24.5, a long context read 41.6 instead of 39.3
 
 template <typename T>
 __device__ __forceinline__ void load2(const T* p, float& a, float& b);

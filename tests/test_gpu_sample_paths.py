@@ -64,3 +64,26 @@ def test_fewer_tokens_than_top_k(vocab):
     for k in (30, 128, 4000):
         check(ql, x, rng.random(10), k=np.full(10, k), p=np.full(10, 0.95))
         check(ql, x, rng.random(10), k=np.full(10, k))
+
+
+@pytest.mark.parametrize("top_k", [None, 3, 300])
+def test_more_rows_than_a_grid_dimension_of_16_bits(top_k):
+    """Row by row the same as a call of those rows alone, and the arg max where the temperature is 0."""
+    import torch
+    from gpu_util import dev
+    ql = lib()
+    rng = np.random.default_rng(9)
+    B, V = 70001, 41
+    x = dev(logits_of(rng, B, V))
+    t = dev((np.arange(B) % 3).astype(np.float32))
+    u = dev(rng.random(B).astype(np.float32))
+    k = None if top_k is None else torch.full((B,), top_k, dtype=torch.int32, device="cuda")
+    tokens = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    ql.ql_sample(x, u, tokens, temperature=t, top_k=k)
+    ql.ql_check_device_error()
+    assert torch.equal(tokens[::3].long(), x[::3].argmax(1))
+    assert bool(((tokens >= 0) & (tokens < V)).all())
+    for a in (0, 33333, B - 5):
+        part = torch.full((5,), -7, dtype=torch.int32, device="cuda")
+        ql.ql_sample(x[a:a + 5], u[a:a + 5], part, temperature=t[a:a + 5], top_k=None if k is None else k[a:a + 5])
+        assert torch.equal(part, tokens[a:a + 5])
