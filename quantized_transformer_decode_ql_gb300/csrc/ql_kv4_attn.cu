@@ -68,6 +68,7 @@ struct Params {
     int batch, n_heads, n_kv, group, chunks;   // chunks: parts of up to 8 heads of a group
     long long maxb, num_blocks;
     float scale_log2;
+    bool early;
     __half* out;
     float* slots;       // [2 gridDim.x] stored states: a CTA's part of the segment it starts in and of the one it ends in
     int* tickets;       // [gridDim.x], zero between launches
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
-    pdl_wait();
+    if (!p.early) pdl_wait();   // every CTA waits before it ends, so that what follows is behind what went before
 
     // the whole list's length, then this CTA's run of it and the segment that it starts in; a batch of up to
     // 32 takes one round of loads
@@ -334,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     if ((total >> 31) != 0) per += (per >> 18) + 1;
     per = max(per, kLeast);
     const long long lo = (long long)blockIdx.x * per;
-    if (lo >= total) return;
+    if (lo >= total) {
+        pdl_wait();
+        return;
+    }
     const int window = (int)(lo + per < total ? per : total - lo);
     Segment sg;
     {
@@ -366,7 +370,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
         }
     }
 
-    if (sg.blk1 <= sg.blk0) return;   // no tile in the window
+    if (sg.blk1 <= sg.blk0) {   // no tile in the window
+        pdl_wait();
+        return;
+    }
 
     // ---- q's rows for the products' columns
     uint2 qr[NB][2];
@@ -469,8 +476,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
     enter(sg);
     if (pblk < pend) look();
     else cross();
+    bool waited = !p.early;
 #pragma unroll 1
-    for (int i = 0; i < kStages && pend != 0; ++i) issue(ring + i * STAGE);
+    for (int i = 0; i < kStages && pend != 0; ++i) {
+        if (!waited && pblk >= ahead[warp].nb - 1) {   // the block that holds the newest row
+            pdl_wait();
+            waited = true;
+        }
+        issue(ring + i * STAGE);
+    }
+    if (!waited) pdl_wait();
 
     St st;
     float zero[4];
@@ -886,6 +901,7 @@ int kv4_attn_launch(const Kv4AttnArgs& a, cudaStream_t s, bool pdl) {
     p.maxb = a.max_blocks_per_seq;
     p.num_blocks = a.num_blocks;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+    p.early = pdl && a.early;
     p.out = a.out;
     p.slots = static_cast<float*>(a.workspace);
     p.tickets = reinterpret_cast<int*>(static_cast<char*>(a.workspace) + 2 * (size_t)grid * kSlotBytes);

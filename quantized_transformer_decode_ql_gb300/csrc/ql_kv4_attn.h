@@ -17,6 +17,8 @@ struct Kv4AttnArgs {
     int batch, n_heads, n_kv_heads, head_dim;
     int64_t max_blocks_per_seq, num_blocks;
     float scale;
+    bool early;                   // only q and the rows in a sequence's last block may come from the preceding kernel:
+                                  // lengths, tables and the other blocks are read before it has ended (decode step)
     __half* out;                  // [batch][n_heads * head_dim]
     void* workspace;              // kv4_attn_workspace_bytes, zero-filled once
     size_t workspace_bytes;

@@ -317,6 +317,7 @@ int run_step(ql_model* m, const ql_step_args* a, cudaStream_t s) {
         ka.max_blocks_per_seq = d.max_blocks_per_seq;
         ka.num_blocks = d.num_blocks;
         ka.scale = 1.0f / sqrtf((float)hd);
+        ka.early = pdl;
         ka.out = m->attn;
         ka.workspace = m->k4_ws;
         ka.workspace_bytes = m->k4_ws_bytes;
