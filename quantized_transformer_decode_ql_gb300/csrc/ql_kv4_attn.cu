@@ -31,7 +31,7 @@
 // is written to the workspace, and the CTA that takes the last ticket joins the parts in order.
 //
 // Measured (HD 128, contexts 128 - 8192, 32 heads on 8, batch 32): 47 us, 3.7 TB/s; 8 heads per kv head and
-// contexts of 20000 - 40960, batch 16: 70 us, 4.4 TB/s (a copy reaches 6.8). About 370 instructions a tile,
+// contexts of 20000 - 40960, batch 16: 70 us, 4.4 TB/s (a copy reaches 6.8). About 360 instructions a tile,
 // half of them on the pipe that takes one in two cycles, 55% of the issue slots, 16 warps on an SM (128
 // registers each): what bounds it is the latency of a tile's instructions and, for a few tiles a warp, the
 // chain length - table - record - join - parts (9.3 us for 2048 tokens). Copies alone take 36 and 59 us.
