@@ -102,7 +102,9 @@ __global__ void __launch_bounds__(kCT) chunk_attn_kernel(CParams p, DevError* er
     }
     const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(csm));
     // stage block blk into buffer b (every thread a share of the 16-byte copies); a bad block
-    // id is recorded and its tiles left as they are (the keys are then masked)
+    // id is recorded and its tiles left as they are (the keys are then masked). Rows behind the
+    // chunk's last position are filled with zeros, not read: a masked key has p = 0, and 0 times a
+    // NaN or an infinity that the block's last owner left there would be NaN in O += P V
     auto stage = [&](int blk, int b) -> bool {
         const int phys = blk < p.maxb ? __ldg(p.block_table + blk) : -1;   // past the table: invalid
         const bool ok = phys >= 0 && phys < p.num_blocks;
@@ -112,10 +114,11 @@ __global__ void __launch_bounds__(kCT) chunk_attn_kernel(CParams p, DevError* er
             const uint32_t kd = sbase + (uint32_t)(b * 2 * TILE), vd = kd + TILE;
             for (int c = tid; c < kBSk * CHUNKS; c += kCT) {
                 const int row = c / CHUNKS, col = c - row * CHUNKS;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(kd + row * PITCH + col * 16),
-                             "l"(ks + row * HD + col * 8) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(vd + row * PITCH + col * 16),
-                             "l"(vs + row * HD + col * 8) : "memory");
+                const int bytes = blk * kBSk + row < L ? 16 : 0;   // the rest of the 16 is zeros
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(kd + row * PITCH + col * 16),
+                             "l"(ks + row * HD + col * 8), "r"(bytes) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(vd + row * PITCH + col * 16),
+                             "l"(vs + row * HD + col * 8), "r"(bytes) : "memory");
             }
         } else if (tid == 0) {
             record_device_error(err, kErrAttnBlock, blk, phys);

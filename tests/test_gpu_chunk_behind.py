@@ -1,0 +1,77 @@
+"""What lies behind a prompt chunk's last position.
+
+A block that a sequence takes over holds whatever its last owner left there: rows behind the chunk must not
+reach the output, not even as 0 x NaN. The same for the buffer that a 4-bit model reads a context back into,
+which all sequences share.
+"""
+import numpy as np
+import pytest
+import torch
+
+import ql_inputs
+
+from gpu_util import lib, dev
+from test_gpu_kv4_model import model
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("p0,T", [(0, 1), (0, 5), (21, 20), (40, 30)])
+@pytest.mark.parametrize("stale", [float("nan"), float("inf")])
+def test_chunk_attention_over_blocks_with_stale_rows(hd, p0, T, stale):
+    """The output is bit for bit that over zeros in the same places."""
+    ql = lib()
+    rng = np.random.default_rng(p0 + T + hd)
+    n_heads, n_kv = 8, 2
+    L = p0 + T
+    nb = (L + 15) // 16
+    assert L % 16
+    k, v = (rng.standard_normal((nb, n_kv, 16, hd)).astype(np.float16) for _ in range(2))
+    table = rng.permutation(nb).astype(np.int32)
+    q = rng.standard_normal((T, n_heads, hd)).astype(np.float16)
+    ws = torch.empty(ql.ql_paged_attn_chunk_workspace_bytes(T, n_heads, n_kv, hd), dtype=torch.uint8, device="cuda")
+    outs = []
+    for behind in (0.0, stale):
+        k[table[-1], :, L % 16:], v[table[-1], :, L % 16:] = behind, behind
+        out = torch.full((T, n_heads * hd), 7.0, dtype=torch.float16, device="cuda")
+        ql.ql_paged_attn_chunk(dev(q), dev(k), dev(v), dev(table), dev(np.array([p0], np.int32)), T, n_heads, n_kv, hd, 16, nb,
+                               nb, 0.1, out, ws)
+        ql.ql_check_device_error()
+        outs.append(out.cpu().numpy())
+    assert np.all(np.isfinite(outs[0])) and np.array_equal(*outs)
+
+
+def prompt(gm, cfg, tokens, position, table):
+    logits = torch.zeros(cfg.vocab, dtype=torch.float32, device="cuda")
+    gm.ql_prefill_chunk(dev(tokens.astype(np.int32)), dev(np.array([position], np.int32)), dev(table), logits=logits)
+    torch.cuda.synchronize()
+    return logits.cpu().numpy()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 2e5])
+def test_a_sequence_does_not_reach_the_next_one_s_prompt(value):
+    """A first sequence's context holds a value that is not finite (or not as f16) at position 30; a second one's
+    prompt of 20 tokens gives the same logits as on a fresh handle."""
+    ql = lib()
+    cfg = ql_inputs.TINY
+    one, two = np.array([0, 1, 2, 3], np.int32), np.array([7, 5, 4, 6], np.int32)
+    tokens = ql_inputs.prompt_tokens(60, cfg.vocab, seed=3)
+    got = []
+    for spoiled in (False, True):
+        gm, _ = model(cfg, 8, 40, 4)
+        try:
+            if spoiled:
+                rows = torch.ones((32, cfg.n_kv_heads, cfg.head_dim), device="cuda")
+                rows[30, :, ::3] = value
+                for li in range(cfg.n_layers):
+                    ql.ql_kv4_write(torch.ones_like(rows), rows, torch.arange(32, device="cuda"), cfg.n_kv_heads, cfg.head_dim,
+                                    gm.kvq_pool[li], 8)
+                prompt(gm, cfg, tokens[20:28], 32, one)
+                with pytest.raises(ql.QLError):          # recorded, and cleared
+                    gm.ql_check_device_error()
+            got.append(prompt(gm, cfg, tokens[:20], 0, two))
+            gm.ql_check_device_error()
+        finally:
+            gm.close()
+    assert np.all(np.isfinite(got[0])) and np.array_equal(*got)
