@@ -99,7 +99,7 @@ struct ql_model {
     void* k4_ws = nullptr;
     size_t k4_ws_bytes = 0;
     long long* k4_slots = nullptr;   // [max_blocks_per_seq * 16]
-    int32_t* k4_order = nullptr;     // [max_blocks_per_seq]: 0, 1, 2, ...
+    int32_t* k4_order = nullptr;     // [max_blocks_per_seq]: 0, 1, 2, ..., -1 for a block that the pool does not have
     __half* k4_k = nullptr;          // [max_blocks_per_seq][n_kv][16][hd]
     __half* k4_v = nullptr;
     // sampling of the decode step (ql_model_set_sampling); greedy without
@@ -152,15 +152,21 @@ __global__ void finalize_kernel(unsigned long long* keys, const int32_t* active,
 
 // Chunked prefill: token t of the chunk sits at position p0 + t (p0 = *position) and attends
 // to positions 0 .. p0 + t; every token uses the sequence's block table row.
-// slots (4-bit KV, else null): the pool slot of every position up to the chunk's last, -1 behind it.
+// 4-bit KV (else null): slots, the pool slot of every position up to the chunk's last, -1 behind it; order, the
+// table of the context read back: block i at i, -1 where the pool has no such block (those rows of the buffer are
+// not written, and the chunk attention leaves the keys out as it does for such an id in a table of its own).
 __global__ void prefill_setup_kernel(const int32_t* position, const int32_t* block_table, int maxb, int T,
-                                     int32_t* bt, int32_t* pos, int32_t* len, long long* slots) {
+                                     int32_t* bt, int32_t* pos, int32_t* len, long long* slots, int32_t* order,
+                                     long long num_blocks) {
     pdl_wait();
     pdl_trigger();
     const int p0 = *position;
-    if (slots != nullptr)
+    if (slots != nullptr) {
         for (long long i = threadIdx.x; i < 16ll * maxb; i += blockDim.x)
             slots[i] = i < (long long)p0 + T ? (long long)block_table[i >> 4] * 16 + (i & 15) : -1;
+        for (int i = threadIdx.x; i < maxb; i += blockDim.x)
+            order[i] = block_table[i] >= 0 && block_table[i] < num_blocks ? i : -1;
+    }
     for (int i = threadIdx.x; i < T * maxb; i += blockDim.x) bt[i] = block_table[i % maxb];
     for (int t = threadIdx.x; t < T; t += blockDim.x) {
         pos[t] = p0 + t;
@@ -638,7 +644,7 @@ int run_prefill(ql_model* m, const int32_t* tokens, int T, int32_t* position, co
     const bool kv4 = d.kv_format == QL_KV_Q4_1;
     int rc;
     cudaError_t e = launch(prefill_setup_kernel, dim3(1), dim3(256), 0, s, pdl, position, block_table, maxb, T, m->pbt,
-                           m->ppos, m->plen, m->k4_slots);
+                           m->ppos, m->plen, m->k4_slots, m->k4_order, (long long)d.num_blocks);
     if (e != cudaSuccess) return cuda_error(e, "prefill setup launch");
     const NextWeights none = {{nullptr, nullptr}, {0, 0}};
     e = launch(embed_kernel, dim3(T), dim3(256), 0, s, pdl, d.embed, tokens, (const int32_t*)nullptr, m->x,
@@ -1027,11 +1033,6 @@ extern "C" int ql_model_create(const ql_model_desc* desc, ql_model** out) {
             A((void**)&m->k4_order, d.max_blocks_per_seq * 4);
             A((void**)&m->k4_k, rows);
             A((void**)&m->k4_v, rows);
-            std::vector<int32_t> order(d.max_blocks_per_seq);
-            for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
-            if (rc == QL_OK && (cudaMemcpy(m->k4_order, order.data(), order.size() * 4, cudaMemcpyHostToDevice) != cudaSuccess ||
-                                cudaMemset(m->k4_k, 0, rows) != cudaSuccess || cudaMemset(m->k4_v, 0, rows) != cudaSuccess))
-                rc = set_error(QL_ECUDA, "ql_model_create: 4-bit prefill buffers");
         }
     }
     A((void**)&m->keys, B * 8);

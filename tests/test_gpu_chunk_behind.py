@@ -1,17 +1,18 @@
-"""What lies behind a prompt chunk's last position.
+"""What lies behind a prompt chunk's last position, and blocks that a table does not have.
 
 A block that a sequence takes over holds whatever its last owner left there: rows behind the chunk must not
 reach the output, not even as 0 x NaN. The same for the buffer that a 4-bit model reads a context back into,
-which all sequences share.
+which all sequences share. Keys of an id outside the pool are left out of the softmax, by every path.
 """
 import numpy as np
 import pytest
 import torch
 
 import ql_inputs
+from oracle import decode
 
 from gpu_util import lib, dev
-from test_gpu_kv4_model import model
+from test_gpu_kv4_model import Following, model
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,38 @@ def test_a_sequence_does_not_reach_the_next_one_s_prompt(value):
         finally:
             gm.close()
     assert np.all(np.isfinite(got[0])) and np.array_equal(*got)
+
+
+@pytest.mark.parametrize("bad", [-1, 8, 2 ** 31 - 1, -2 ** 31])
+def test_a_chunk_leaves_out_the_keys_of_a_block_that_the_pool_does_not_have(bad, monkeypatch):
+    """After another sequence's prompt, a chunk at position 48 whose table's second id is outside the pool: the oracle's
+    logits over positions 0 - 15 and 32 on."""
+    ql = lib()
+    cfg = ql_inputs.TINY
+    gm, om = model(cfg, 8, 64, 4)
+    try:
+        good = np.array([7, 5, 4, 6], np.int32)
+        prompt(gm, cfg, ql_inputs.prompt_tokens(64, cfg.vocab, seed=5), 0, np.array([0, 1, 2, 3], np.int32))
+        gm.ql_check_device_error()
+        k, v = ql_inputs.kv_context(cfg.n_layers, cfg.n_kv_heads, cfg.head_dim, 48, seed=6)
+        gm.write_context(good, k, v)
+        broken = good.copy()
+        broken[1] = bad
+        tokens = ql_inputs.prompt_tokens(10, cfg.vocab, seed=7)
+        got = prompt(gm, cfg, tokens, 48, broken).astype(np.float64)
+        with pytest.raises(ql.QLError) as e:
+            gm.ql_check_device_error()
+        assert e.value.status == ql.QL_EDEVICE
+        cache = Following(cfg, 1, 64, gm, good.reshape(1, -1))
+        for li in range(cfg.n_layers):
+            rows = cache.rows(li, 0, np.arange(48))
+            cache.k[0, li, :, :48], cache.v[0, li, :, :48] = rows[0], rows[1]
+        plain = decode.ops.gqa_attention
+        monkeypatch.setattr(decode.ops, "gqa_attention",
+                            lambda q, k, v, s: plain(q, np.delete(k, np.s_[16:32], 1), np.delete(v, np.s_[16:32], 1), s))
+        for t in range(10):
+            cache.begin([48 + t])
+            want = decode.decode_step(om, cache, [int(tokens[t])], [48 + t])[0]
+        assert decode.logits_close(got, want).all(), float(np.abs(got - want).max())
+    finally:
+        gm.close()
