@@ -507,7 +507,8 @@ typedef struct {
  * ql_paged_attn_decode_kv4; each step quantises its K and V rows (f32, K after norm and rotation)
  * by ql_kv4_write's rule in a kernel before the attention; prefill chunks do the same and attend to
  * the context's values as f16 (ql_kv4_read's, in a buffer of one layer that the handle owns:
- * max_blocks_per_seq * 64 * n_kv_heads * head_dim bytes).                                   */
+ * max_blocks_per_seq * 64 * n_kv_heads * head_dim bytes; a value of the format that f16 does not hold,
+ * 65520 or more in magnitude, is infinite there and recorded in the device error record).   */
 enum { QL_KV_F16 = 0, QL_KV_Q8_0_Q5_1 = 1, QL_KV_Q4_1 = 2 };
 
 typedef struct ql_model ql_model;

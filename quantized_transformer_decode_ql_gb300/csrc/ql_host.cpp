@@ -82,7 +82,7 @@ static const char* where_name(int w) {
         case kErrGemvStage: return "gemv: a staged weight copy did not arrive (bounded wait expired)";
         case kErrStepBarrier: return "persistent step: a grid barrier wait ran out (index = barrier, value = CTA)";
         case kErrKvNonFinite: return "KV row quantiser: non-finite value (index = row, value = block)";
-        case kErrKvOverflow: return "KV row quantiser: block scale or minimum overflows f16 (index = row, value = block)";
+        case kErrKvOverflow: return "KV rows: a block scale or minimum, or a value read back for a prompt chunk, overflows f16 (index = row, value = block or kv head)";
         case kErrKvSlot: return "KV rows: slot outside the pool (index = row, value = slot)";
         case kErrAttnStage: return "4-bit attention: a staged record did not arrive (bounded wait expired; index = sequence, value = block)";
         case kErrSampleArg: return "sampling: temperature, top-p, min-p or uniform number out of range (index = row)";

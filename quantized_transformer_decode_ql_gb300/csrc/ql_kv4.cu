@@ -106,11 +106,22 @@ __device__ __forceinline__ void put8(float* o, const uint32_t (&c)[2], __half d,
     reinterpret_cast<float4*>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
 
+// Whether one of those values overflows f16, d and m being finite: the largest code would have to first.
+__device__ __forceinline__ bool overflows8(const uint32_t (&c)[2], __half d, __half m) {
+    const float df = __half2float(d), mf = __half2float(m);
+    if (!(fabsf(df) < INFINITY && fabsf(mf) < INFINITY && fabsf(fmaf(df, 15.f, mf)) >= 65520.f)) return false;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) any |= fabsf(fmaf(df, (float)((c[i >> 2] >> (8 * (i & 3))) & 15u), mf)) >= 65520.f;
+    return any;
+}
+
 // A lane writes elements 8 w .. 8 w + 7 of block b of the key row and of the value row. The value codes of
 // those 8 elements lie in 8 units: each lane loads one word (a unit's two blocks), and the 8 lanes of a
 // pair of blocks transpose their 8 words of 8 codes by three exchanges (halves, bytes, nibbles). A warp's
 // life is two round trips (slots, records), so a thread takes two rows at once.
-// BLOCKS: row i goes to slot i % 16 of block i / 16 of a pool [blocks][n_kv][16][HD] instead.
+// BLOCKS: row i goes to slot i % 16 of block i / 16 of a pool [blocks][n_kv][16][HD] instead, and a finite value that
+// is none as f16 is recorded (the format holds values up to 1e6, the attention that reads this pool does not).
 constexpr int kReadRows = 2;
 template <int HD, typename T, bool BLOCKS>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __restrict__ pool,
@@ -165,6 +176,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const uint8_t* __
         const long long at = 32 * b + 8 * w + (BLOCKS ? ((i >> 4) * gridDim.y + g) * (16ll * HD) + (i & 15) * HD : (long long)g * HD);
         put8(k + (BLOCKS ? 0 : i * ks) + at, ck, dk[r], mk[r]);
         put8(v + (BLOCKS ? 0 : i * vs) + at, cv, dv[r], mv[r]);
+        if (BLOCKS && (overflows8(ck, dk[r], mk[r]) || overflows8(cv, dv[r], mv[r]))) record_device_error(err, kErrKvOverflow, i, g);
     }
 }
 

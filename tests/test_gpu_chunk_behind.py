@@ -111,3 +111,27 @@ def test_a_chunk_leaves_out_the_keys_of_a_block_that_the_pool_does_not_have(bad,
         assert decode.logits_close(got, want).all(), float(np.abs(got - want).max())
     finally:
         gm.close()
+
+
+def test_a_context_s_value_above_f16_is_recorded():
+    """The format holds it (m + 15 d up to 1e6), the chunk's attention reads it as f16."""
+    ql = lib()
+    cfg = ql_inputs.TINY
+    gm, _ = model(cfg, 8, 40, 4)
+    try:
+        table, tokens = np.array([3, 0, 1, 2], np.int32), ql_inputs.prompt_tokens(8, cfg.vocab, seed=3)
+        for value, fits in ((65000.0, True), (65504.0 * 1.2, False)):
+            rows = torch.ones((16, cfg.n_kv_heads, cfg.head_dim), device="cuda")
+            rows[9, 1, 40] = value
+            ql.ql_kv4_write(torch.ones_like(rows), rows, 48 + torch.arange(16, device="cuda"), cfg.n_kv_heads, cfg.head_dim,
+                            gm.kvq_pool[1], 8)
+            gm.ql_check_device_error()                     # the row itself fits the format
+            prompt(gm, cfg, tokens, 16, table)
+            if fits:
+                gm.ql_check_device_error()
+            else:
+                with pytest.raises(ql.QLError) as e:
+                    gm.ql_check_device_error()
+                assert e.value.status == ql.QL_EDEVICE
+    finally:
+        gm.close()
