@@ -386,7 +386,7 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  *   min-p  M = the tokens with l_i >= max l + T ln(d_min_p[b]) (0 or less: all; 1 or more: those
  *          of the largest logit);
  * the token drawn is the first index i at which the weight of the tokens of index <= i in K, P and
- * M exceeds u times the weight of them all. T = 0 takes the arg max (lowest index). d_temperature,
+ * M exceeds u times the weight of them all. T = 0 (any below 1e-36) takes the arg max (lowest index). d_temperature,
  * d_top_k, d_top_p and d_min_p are device arrays [batch] or NULL (T = 1, no filter).
  * Logits: dtype (QL_DTYPE_F32 or QL_DTYPE_F16) [batch][vocab], rows row_stride elements apart, any
  * alignment of their type. -inf and NaN are tokens that are never drawn, +inf counts as the
@@ -395,7 +395,7 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  * probability 0. So does a row whose T is negative, NaN or infinite, whose top_p or min_p is NaN
  * or whose u is outside [0, 1), which is recorded in the device error record. d_active
  * int32 [batch] or NULL: rows with 0 are left as they were. Weights are 40-bit fixed-point numbers
- * (relative error 2^-29 before that rounding; a token 2^-40 times as likely as the largest is never
+ * (relative error 2^-29 before that rounding, 2^-28 at T above 1e36; a token 2^-40 times as likely as the largest is never
  * drawn) and their sums exact, so that the outcome does not
  * depend on the order of additions. 1 <= vocab <= 360448, batch < 2^31. Asynchronous on stream. */
 int ql_sample(const void* d_logits, int dtype, int64_t row_stride, int64_t batch, int64_t vocab,

@@ -129,16 +129,20 @@ struct RowScale {
         ref = fabsf(t * c_hi) > 0x1p20f ? t : 0.f;
         const float x = t - ref;
         magic = 12582912.0f - floorf(__fmul_rd(x, c_hi));
-        low = fmaxf(x - __fdiv_rn(2600.f, c_hi), -FLT_MAX);            // 2^-40.6 of the largest: weight 0
+        low = fmaxf(x - __fdiv_rn(2600.f, c_hi), -FLT_MAX);            // 2^-40.6 of the largest: weight 0 (see hot)
         dist = fminf(__fdiv_rn(8388608.f / 24.f, temp), FLT_MAX);     // finite: 0 dist is 0
     }
+    // No finite logit is so far below the largest (T of 1.2e37 and more): weight() takes -inf for the least finite
+    // one, which weighs something. Passes over such a row look at each token's key (a border that is not all()) or
+    // compare its logit with the least one kept.
+    __device__ __forceinline__ bool hot() const { return low == -FLT_MAX; }
 };
 
 // The weight of logit l: 2^(40 + e / 64), e = (l - ref) 64 log2(e) / T minus its floor at the largest
 // logit. The floor and the fraction come from fused multiply-adds of l itself, each rounded once, so
 // that the error of a large l does not enter; 2^(fraction / 64) - 1 is the series of exp to the fourth
 // power (the next term is below 2^-40), the product with the table is an integer one.
-// The clamp keeps e / 64 above -42 and takes a NaN to weight 0.
+// The clamp keeps e / 64 above -42 and takes a NaN and -inf to weight 0, in a row that is not hot().
 // REF false: r.ref is 0.
 template <bool REF = true>
 __device__ __forceinline__ u64 weight(float l, const RowScale& r, const uint32_t* table) {
@@ -480,7 +484,7 @@ __device__ Border find_border(const S& src, Search f, const RowScale& row, int v
                 return;
             }
             const u64 w = KIND == kCount ? 1 : weight(l2, row, sh.table);
-            if (KIND != kCount && w == 0) return;
+            if (KIND != kCount && (w == 0 || l2 == -INFINITY)) return;
             const uint32_t n = atomicAdd(&sh.nlist, 1u);
             if (n < kList) list[n] = Entry{w, key_of(l2), i};
         });
@@ -644,7 +648,7 @@ __device__ bool list_first(const Run& run, const RowScale& row, float mine, int 
         for (int j = 0; j < 4; ++j) {
             if (distance(l[j], row) > far) continue;
             const u64 w = weight(l[j], row, sh.table);
-            if (w == 0) continue;
+            if (w == 0 || l[j] == -INFINITY) continue;
             uint32_t n;
             asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(count) : "memory");
             if (n < kList)
@@ -917,11 +921,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_plain_kernel(Params p, Dev
     }
     RowScale row;
     row.set(top, a.temp);
-    float least = -INFINITY;   // -inf weighs nothing
+    float least = row.hot() ? -FLT_MAX : -INFINITY;   // -inf weighs nothing
     if (a.minp > 0.f) {
         if (tid == 0) sh.least = min_p_least(a, top);
         __syncthreads();
-        least = sh.least;
+        least = fmaxf(least, sh.least);
     }
     u64 w = 0;
     if (row.ref != 0.f || infinite) {
@@ -982,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
     }
     RowScale row;
     row.set(top, a.temp);
-    const Border every = {kKeyMin, 0x7FFFFFFF};   // all that is above -inf
+    const Border every = {kKeyMin, row.hot() ? 0x7FFFFFFE : 0x7FFFFFFF};   // all that is above -inf
     Border border = every, prefix = every;
     if (a.minp > 0.f) {
         if (tid == 0) sh.least = min_p_least(a, top);
