@@ -363,8 +363,10 @@ int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_
  * keys of a block id outside the pool are left out of the softmax (and recorded), and that a
  * sequence whose length is outside [0, max_blocks_per_seq * 16] (recorded) or 0 leaves its
  * output row as it was. batch <= 65535, n_heads <= 2^20, batch * n_heads < 2^24, max_blocks_per_seq < 2^25, batch *
- * max_blocks_per_seq * n_heads < 2^38, num_blocks < 2^31; q and the output 4-byte aligned. Scores are exact f32 sums over the codes; the
- * weights enter the value product as pairs of f16 (22 bits), all sums are f32.
+ * max_blocks_per_seq * n_heads < 2^38, num_blocks < 2^31; q and the output 4-byte aligned. Scores are f32 sums: of the
+ * codes times q exactly as they are, and of the minima times q's sum over a block, which enters as a pair of f16 (22 bits).
+ * The weights enter the value product as pairs of f16 too (22 bits, in steps of 2^-33 of the largest weight or finer; where
+ * value scales d above 2 are met, d 2^-34, and 2^-20 at most); all sums are f32.
  * d_workspace: ql_paged_attn_kv4_workspace_bytes(...) bytes, 16-byte aligned, ZERO-FILLED before
  * its first use; every call leaves it valid for a next call of any shape that it is large enough
  * for. Calls (and captured graphs) that may run at the same time need workspaces of their own. */

@@ -8,8 +8,10 @@
 // the upper bytes come down by a byte permutation. The scales stay outside:
 //   S^T = K Q^T: one f32 sum per (key, head) and 32-element block, sum_i q_i c_i, then
 //         s = sum_b d_b sum_b + sum_b m_b (sum_i q_i), the last product one m16n8k8 MMA of the minima
-//         with the q sums in two f16 parts. q is brought to [2^14, 2^15) by a power of two (exact),
-//         elements that meet the 16-fold codes are divided by 16.
+//         with the q sums in two f16 parts, in units (kSumUnit) that keep both in the normal range: 22 bits
+//         of every sum, however small beside the head's largest |q| (as subnormal parts, in the codes'
+//         units, a score of small sums was off by 2^-8 of itself; the times are the same). q is brought to
+//         [2^14, 2^15) by a power of two (exact), elements that meet the 16-fold codes are divided by 16.
 //   O^T = V^T P^T: p d_b takes the part of p, as two f16 numbers (22 bits; p alone in f16 would cost
 //         as much again as the rounding of the output), the minima are one more MMA whose fifth row
 //         of ones gives the sum of p.
@@ -52,6 +54,7 @@ constexpr int kStages = 4;                // tiles of a warp in flight
 constexpr int kCtasPerSm = 2;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kTop = 14.f;              // log2 of the largest weight before the reference moves
+constexpr float kSumUnit = 0x1p-5f;       // of a block's sum of q as an f16 operand: up to 2^20 units, and both of its parts in the normal range
 constexpr int kSettle = 8;                // tiles of a warp between two settlings of the sums, a power of two
 constexpr int kEntry = 20;                // what a segment costs besides its tiles, in tiles (about 3 us; 10: 6% slower on ragged batches)
 constexpr int kLeast = 2 * kWarps;            // the shortest window (2048 tokens on 8 kv heads: 9.5 us, with kWarps 10.2)
@@ -570,9 +573,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                qs[b] = s * 0x1p-24f;
+                qs[b] = s * kSumUnit;   // 2^15 at most
             }
-            // the sums' high and low f16 parts, opposite the minima of blocks 2 (tq & 1), 2 (tq & 1) + 1
+            // the sums' high and low f16 parts (22 bits, but 2^-25 at least), opposite the minima of blocks 2 (tq & 1),
+            // 2 (tq & 1) + 1
             const float sa = NB == 4 && (tq & 1) ? qs[NB - 2] : qs[0], sb = NB == 4 && (tq & 1) ? qs[NB - 1] : qs[1];
             const __half2 hi2 = __floats2half2_rn(sa, sb);
             const float2 hf = __half22float2(hi2);
@@ -591,6 +595,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
             lds_words(da, rec + offKD);
             lds_words(db, rec + offKD + 16 * NB);
             mma8_first(s, lds<uint32_t>(rec + offKM), lds<uint32_t>(rec + offKM + 16 * NB), qz, zero);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] *= 0x1p-24f / kSumUnit;   // to the codes' units
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float a[4];
