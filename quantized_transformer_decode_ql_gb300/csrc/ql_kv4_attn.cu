@@ -660,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv4_attn_kernel(Params p
                     }
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) dw = fmaxf(dw, __shfl_xor_sync(0xffffffffu, dw, o));
-                    // p and p d stay below 2^15: the largest scale is at most 2^(15 - top)
+                    // p and p d stay below 2^15: the largest scale is at most 2^(15 - top). Above 2^14 (top = 1) every tile
+                    // with such a scale comes here, and has weights of 2^-5 at most then
                     const float old = top;
                     float lim = __low2float(dlim);
                     while (top > 1.f && dw > lim) {

@@ -1,5 +1,5 @@
 """Scores of the 4-bit attention whose weight lies in the minima: m times a sum of q that is small beside the head's
-largest |q|.
+largest |q|; and value scales near the end of f16.
 
 A score is scale sum_b (d_b sum_i q_i c_i + m_b Q_b), Q_b = sum_i q_i of block b. Q_b enters as two f16 numbers at a scale
 that brings the head's largest |q| to 2^9 .. 2^10: off by 2^-22 |Q_b|, or by the spacing there, 2^-25 of 2^9 (2^-34 of the
@@ -68,3 +68,28 @@ def test_small_sums_of_q_beside_a_large_element(heads, n_kv, hd, largest):
     got = attend(ql, dev(q), dev(rec), dev(bt), dev(np.array([n, n], np.int32)), scale)
     ql.ql_check_device_error()
     check(got.cpu().numpy(), q, rec, n, scale)
+
+
+@pytest.mark.parametrize("size", [16000.0, 33000.0, 40000.0, 60000.0, 65504.0])
+@pytest.mark.parametrize("rise", [4.0, 5.5, 5.97, 6.5])
+@pytest.mark.parametrize("heads,n_kv", [(4, 1), (8, 1)])
+def test_value_scales_near_the_end_of_f16(heads, n_kv, rise, size):
+    """Codes 0 and 1 of a scale of up to 65504, and weights that rise by `rise` binades from a warp's first tile to its
+    second: outputs are finite f16 numbers."""
+    ql = lib()
+    hd, blocks = 128, 24
+    rng = np.random.default_rng(int(size))
+    rec = np.zeros((blocks, n_kv, 20 * hd), np.uint8)
+    w = rec.view(np.float16)
+    rec[..., 8 * hd:16 * hd] = rng.integers(0, 2, (blocks, n_kv, 8 * hd)) * 0x10 + rng.integers(0, 2, (blocks, n_kv, 8 * hd))
+    w[..., 9 * hd:9 * hd + hd // 2] = size                                      # d of the values; m = 0
+    for blk in range(blocks):                                                   # keys: m alone, the same in all blocks of a row
+        w[blk, :, 8 * hd + hd // 2:9 * hd] = rise * (blk // 8)
+    q = np.full((1, heads, hd), 1.0 / 128, np.float16)
+    n = blocks * 16 - 3
+    bt = np.arange(blocks, dtype=np.int32)[None]
+    scale = float(np.log(2.0))                                                  # a key of x: 2^x
+    got = attend(ql, dev(q), dev(rec), dev(bt), dev(np.array([n], np.int32)), scale).cpu().numpy()
+    ql.ql_check_device_error()
+    assert np.all(np.isfinite(got))
+    check(got, q, rec, n, scale)
