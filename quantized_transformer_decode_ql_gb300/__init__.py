@@ -17,7 +17,8 @@ from ._lib import (QLError, QL_OK, QL_EINVAL, QL_ENOMEM, QL_ECUDA, QL_EPOOL, QL_
                    QL_GEMV_ACT_INT16, QL_GEMV_ACT_INT8, QL_KV_F16, QL_KV_Q8_0_Q5_1, QL_KV_Q4_1,
                    QL_ATTN_MERGE_TICKET, QL_ATTN_MERGE_CLUSTER,
                    Q4Matrix, LayerDesc, ModelDesc,
-                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, check_array, check_sampling, ptr, stream_ptr)
+                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, check_array, check_device, check_pool,
+                   check_sampling, ptr, stream_ptr)
 
 __all__ = [
     "QLError", "lib", "ql_q4_0_pack", "ql_q4_0_unpack", "ql_q4_0_pack_device", "ql_gemv_q4_0",
@@ -259,6 +260,8 @@ def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=Non
     pool at physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out)."""
     n = slots.numel()
     check_array("ql_kv4_write", "slots", slots, "torch.int64", 0)
+    check_device("ql_kv4_write", k, v, slots, pool)
+    check_pool("ql_kv4_write", pool, num_blocks * n_kv_heads * 20 * head_dim)
     ks = _row_stride("ql_kv4_write", k, n, n_kv_heads, head_dim)
     vs = _row_stride("ql_kv4_write", v, n, n_kv_heads, head_dim)
     status = lib().ql_kv4_write(k.data_ptr(), v.data_ptr(), _dtype_of("ql_kv4_write", k, v), ks, vs, slots.data_ptr(), n,
@@ -271,6 +274,8 @@ def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None
     """The values of ``slots`` read back into ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided)."""
     n = slots.numel()
     check_array("ql_kv4_read", "slots", slots, "torch.int64", 0)
+    check_device("ql_kv4_read", k, v, slots, pool)
+    check_pool("ql_kv4_read", pool, num_blocks * n_kv_heads * 20 * head_dim)
     ks = _row_stride("ql_kv4_read", k, n, n_kv_heads, head_dim)
     vs = _row_stride("ql_kv4_read", v, n, n_kv_heads, head_dim)
     status = lib().ql_kv4_read(ptr(pool), slots.data_ptr(), n, n_kv_heads, head_dim, num_blocks, k.data_ptr(), v.data_ptr(),
@@ -285,7 +290,19 @@ def ql_paged_attn_kv4_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_
 
 def ql_paged_attn_decode_kv4(q, pool, block_tables, context_lens, batch, n_heads, n_kv_heads, head_dim,
                              block_size, max_blocks_per_seq, num_blocks, scale, out, workspace, stream=None):
-    """Single-token attention over a 4-bit pool; ``workspace``: a zero-filled byte tensor."""
+    """Single-token attention over a 4-bit pool: ``q``, ``out`` f16 [batch, n_heads, head_dim], ``block_tables`` int32
+    [batch, max_blocks_per_seq], ``context_lens`` int32 [batch], all contiguous; ``workspace``: a zero-filled byte tensor."""
+    name = "ql_paged_attn_decode_kv4"
+    rows = batch * n_heads * head_dim
+    for what, t, dtype, n in (("q", q, "torch.float16", rows), ("out", out, "torch.float16", rows),
+                              ("block_tables", block_tables, "torch.int32", batch * max_blocks_per_seq),
+                              ("context_lens", context_lens, "torch.int32", batch)):
+        if not isinstance(t, int):
+            check_array(name, what, t, dtype, n)
+    if not workspace.is_contiguous():
+        raise QLError(QL_EINVAL, f"{name}: the workspace must be contiguous")
+    check_device(name, q, pool, block_tables, context_lens, out, workspace)
+    check_pool(name, pool, num_blocks * n_kv_heads * 20 * head_dim)
     check(lib().ql_paged_attn_decode_kv4(ptr(q), ptr(pool), ptr(block_tables), ptr(context_lens), batch, n_heads,
                                          n_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
                                          ptr(out), ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -308,6 +325,7 @@ def ql_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None,
             check_sampling("ql_sample", B, uniform, temperature, top_k, top_p, min_p)
             check_array("ql_sample", "probs", probs, "torch.float32", B)
             check_array("ql_sample", "active", active, "torch.int32", B)
+    check_device("ql_sample", logits, uniform, tokens, temperature, top_k, top_p, min_p, probs, active)
     status = lib().ql_sample(logits.data_ptr(), _dtype_of("ql_sample", logits), logits.stride(0), B, V, ptr(temperature),
                              ptr(top_k), ptr(top_p), ptr(min_p), uniform.data_ptr(), ptr(active), tokens.data_ptr(),
                              ptr(probs), stream_ptr(stream))

@@ -198,6 +198,33 @@ def check_array(name, what, t, dtype, n):
                                  f"{tuple(t.shape)} of {t.dtype}")
 
 
+_current_device = None   # () -> the current GPU's index
+
+
+def _find_current_device():
+    import torch
+    if not torch.cuda.is_available():
+        return lambda: -2   # no tensor's
+    return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def check_device(name, *tensors):
+    """Refuse tensors that are not on the current GPU (None and plain addresses pass)."""
+    global _current_device
+    if _current_device is None:
+        _current_device = _find_current_device()
+    here = _current_device()
+    for t in tensors:
+        if t is not None and t.__class__ is not int and t.get_device() != here:
+            raise QLError(QL_EINVAL, f"{name}: tensors must be on the current GPU, got one on {t.device}")
+
+
+def check_pool(name, pool, nbytes):
+    """Refuse a pool tensor that is not contiguous or has fewer than ``nbytes`` bytes (a plain address passes)."""
+    if pool.__class__ is not int and (pool is None or pool.nbytes < nbytes or not pool.is_contiguous()):
+        raise QLError(QL_EINVAL, f"{name}: the pool must be a contiguous tensor of at least {nbytes} bytes")
+
+
 def check_sampling(name, batch, uniform, temperature, top_k, top_p, min_p):
     """The sampling arrays of a batch."""
     check_array(name, "uniform", uniform, "torch.float32", batch)

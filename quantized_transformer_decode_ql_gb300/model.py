@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from ._lib import (LayerDesc, ModelDesc, Q4Matrix, QL_DTYPE_F32, QL_EINVAL, QL_KV_F16, QL_KV_Q4_1, QLError, Sampling, StepArgs,
-                   check, check_sampling, lib, ptr, stream_ptr)
+                   check, check_device, check_sampling, lib, ptr, stream_ptr)
 
 BLOCK = 16
 
@@ -219,6 +219,7 @@ class DeviceModel:
         check_sampling("ql_model_set_sampling", uniform.shape[0] if uniform.dim() else 0, uniform, temperature, top_k, top_p, min_p)
         if uniform.dim() not in (1, 2):
             raise QLError(QL_EINVAL, "ql_model_set_sampling: uniform must be [batch] or [batch, numbers]")
+        check_device("ql_model_set_sampling", uniform, temperature, top_k, top_p, min_p)
         s = Sampling(ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), ptr(uniform),
                      uniform.shape[1] if uniform.dim() == 2 else 1)
         check(lib().ql_model_set_sampling(self.handle, ctypes.byref(s)))
