@@ -948,6 +948,8 @@ extern "C" int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, con
     QL_REQUIRE((reinterpret_cast<uintptr_t>(d_pool) & 15) == 0 && (reinterpret_cast<uintptr_t>(d_workspace) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(d_q) & 3) == 0 && (reinterpret_cast<uintptr_t>(d_out) & 3) == 0,
                std::string(nm) + ": the pool and the workspace must be 16-byte aligned, q and the output 4-byte aligned");
+    QL_REQUIRE((reinterpret_cast<uintptr_t>(d_block_tables) & 3) == 0 && (reinterpret_cast<uintptr_t>(d_context_lens) & 3) == 0,
+               std::string(nm) + ": misaligned block tables or lengths");
     QL_REQUIRE(workspace_bytes >= kv4_attn_workspace_bytes(),
                std::string(nm) + ": workspace too small");
     Kv4AttnArgs a = {};

@@ -123,3 +123,9 @@ def test_addresses_pass_the_checks(gpu, monkeypatch):
     ql.ql_kv4_read(4096, slots, 2, 64, 1 << 20, k, k, stream=5)
     ql.ql_kv4_write(k, k, slots, 2, 64, gpu(torch.zeros((2, 2, 1280), dtype=torch.uint8)), 2, stream=5)
     assert Library.called == 4
+
+
+def test_misaligned_tables_and_lengths():
+    for table, lens in ((66, 64), (64, 65), (67, 66)):
+        assert ql.lib().ql_paged_attn_decode_kv4(64, 1024, table, lens, 1, 8, 8, 128, 16, 4, 9, 0.1, 64, 64, 1 << 40, None) == ql.QL_EINVAL
+        assert "misaligned" in ql.lib().ql_last_error().decode()
