@@ -396,7 +396,8 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  * share of the kept weight (1 where T = 0). A row with no token left gives token -1 and
  * probability 0. So does a row whose T is negative, NaN or infinite, whose top_p or min_p is NaN
  * or whose u is outside [0, 1), which is recorded in the device error record. d_active
- * int32 [batch] or NULL: rows with 0 are left as they were. Weights are 40-bit fixed-point numbers
+ * int32 [batch] or NULL: rows with 0 are left as they were. The outputs overlap neither each other nor an
+ * input (QL_EINVAL). Weights are 40-bit fixed-point numbers
  * (relative error 2^-29 before that rounding, 2^-28 at T above 1e36; a token 2^-40 times as likely as the largest is never
  * drawn) and their sums exact, so that the outcome does not
  * depend on the order of additions. 1 <= vocab <= 360448, batch < 2^31. Asynchronous on stream. */

@@ -1143,6 +1143,23 @@ extern "C" int ql_sample(const void* d_logits, int dtype, int64_t row_stride, in
     QL_REQUIRE(a4(d_temperature) && a4(d_top_k) && a4(d_top_p) && a4(d_min_p) && a4(d_uniform) && a4(d_active) &&
                    a4(d_tokens) && a4(d_probs),
                "ql_sample: misaligned array");
+    // The CTAs of a row read its arguments on their own and have to find the same ones: an output in their place would
+    // send them different ways.
+    const uintptr_t rows = (uintptr_t)batch * 4;
+    auto apart = [](const void* p, uintptr_t np, const void* q, uintptr_t nq) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+        return !p || !q || a + np <= b || b + nq <= a;
+    };
+    const uintptr_t all = ((uintptr_t)(batch - 1) * (uintptr_t)(batch > 1 ? row_stride : 0) + (uintptr_t)vocab) * size;
+    for (const void* out : {static_cast<const void*>(d_tokens), static_cast<const void*>(d_probs)}) {
+        bool ok = apart(out, rows, d_logits, all);
+        for (const void* in : {static_cast<const void*>(d_temperature), static_cast<const void*>(d_top_k),
+                               static_cast<const void*>(d_top_p), static_cast<const void*>(d_min_p),
+                               static_cast<const void*>(d_uniform), static_cast<const void*>(d_active)})
+            ok = ok && apart(out, rows, in, rows);
+        QL_REQUIRE(ok, "ql_sample: the outputs must not overlap the inputs");
+    }
+    QL_REQUIRE(apart(d_tokens, rows, d_probs, rows), "ql_sample: the outputs must not overlap");
     SampleArgs a = {};
     a.logits = d_logits;
     a.dtype = dtype;

@@ -129,3 +129,20 @@ def test_misaligned_tables_and_lengths():
     for table, lens in ((66, 64), (64, 65), (67, 66)):
         assert ql.lib().ql_paged_attn_decode_kv4(64, 1024, table, lens, 1, 8, 8, 128, 16, 4, 9, 0.1, 64, 64, 1 << 40, None) == ql.QL_EINVAL
         assert "misaligned" in ql.lib().ql_last_error().decode()
+
+
+def test_sampled_outputs_that_overlap():
+    """(Pointers only: nothing is launched.)"""
+    L, B, V = ql.lib(), 8, 100
+
+    def status(**over):
+        a = dict(logits=1 << 20, temperature=0x1000, top_k=0x2000, top_p=0x3000, min_p=0x4000, uniform=0x5000, active=0x6000,
+                 tokens=0x7000, probs=0x8000)
+        a.update(over)
+        return L.ql_sample(a["logits"], ql.QL_DTYPE_F32, V + 3, B, V, a["temperature"], a["top_k"], a["top_p"], a["min_p"], a["uniform"],
+                           a["active"], a["tokens"], a["probs"], None)
+    end = (1 << 20) + ((B - 1) * (V + 3) + V) * 4
+    for out in ("tokens", "probs"):
+        for at in [0x1000 * i + d for i in range(1, 7) for d in (-28, 0, 28)] + [(1 << 20) - 28, end - 4]:
+            assert status(**{out: at}) == ql.QL_EINVAL and "overlap" in L.ql_last_error().decode(), (out, hex(at))
+    assert status(tokens=0x8000) == ql.QL_EINVAL and status(probs=0x7000 + 28) == ql.QL_EINVAL
