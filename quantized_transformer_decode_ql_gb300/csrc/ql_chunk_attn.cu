@@ -57,8 +57,25 @@ __device__ __forceinline__ void split_of(int L, int nsplit, int& nblocks, int& s
     n_active = (nblocks + spb - 1) / spb;
 }
 
+// The value rows behind the chunk's last position, in the staged last block, become zeros: a masked key has p = 0, and 0
+// times a NaN or an infinity that the block's last owner left there would be NaN in O += P V. By every thread of the
+// CTA; the chunk's end and the thread's number are read again, for the loop has no register to keep them.
 template <int HD>
-__global__ void __launch_bounds__(kCT) chunk_attn_kernel(CParams p, DevError* err) {
+__device__ __forceinline__ void clear_behind(const int32_t* position, int T, uint32_t vsm) {
+    constexpr int PITCH = HD * 2 + 16, CHUNKS = HD * 2 / 16;
+    int p0, tid;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(p0) : "l"(position) : "memory");
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+#pragma unroll 1
+    for (int c = (p0 + T) % kBSk * CHUNKS + tid; c < kBSk * CHUNKS; c += kCT)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vsm + c / CHUNKS * PITCH + c % CHUNKS * 16), "r"(0u) : "memory");
+    __syncthreads();
+}
+
+// Three and two CTAs an SM: left to itself the compiler takes 150 registers a thread at HD 128, which leaves room for one
+// (a 16384-token prompt of the 8B shape 17250 tokens/s instead of 19170).
+template <int HD>
+__global__ void __launch_bounds__(kCT, HD == 64 ? 3 : 2) chunk_attn_kernel(CParams p, DevError* err) {
     constexpr int KSTEPS = HD / 16, NT = HD / 8;
     constexpr int PITCH = HD * 2 + 16;            // bytes per staged row (ldmatrix without bank conflicts)
     constexpr int TILE = kBSk * PITCH;
@@ -102,9 +119,7 @@ __global__ void __launch_bounds__(kCT) chunk_attn_kernel(CParams p, DevError* er
     }
     const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(csm));
     // stage block blk into buffer b (every thread a share of the 16-byte copies); a bad block
-    // id is recorded and its tiles left as they are (the keys are then masked). Rows behind the
-    // chunk's last position are filled with zeros, not read: a masked key has p = 0, and 0 times a
-    // NaN or an infinity that the block's last owner left there would be NaN in O += P V
+    // id is recorded and its tiles left as they are (the keys are then masked)
     auto stage = [&](int blk, int b) -> bool {
         const int phys = blk < p.maxb ? __ldg(p.block_table + blk) : -1;   // past the table: invalid
         const bool ok = phys >= 0 && phys < p.num_blocks;
@@ -114,11 +129,10 @@ __global__ void __launch_bounds__(kCT) chunk_attn_kernel(CParams p, DevError* er
             const uint32_t kd = sbase + (uint32_t)(b * 2 * TILE), vd = kd + TILE;
             for (int c = tid; c < kBSk * CHUNKS; c += kCT) {
                 const int row = c / CHUNKS, col = c - row * CHUNKS;
-                const int bytes = blk * kBSk + row < L ? 16 : 0;   // the rest of the 16 is zeros
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(kd + row * PITCH + col * 16),
-                             "l"(ks + row * HD + col * 8), "r"(bytes) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(vd + row * PITCH + col * 16),
-                             "l"(vs + row * HD + col * 8), "r"(bytes) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(kd + row * PITCH + col * 16),
+                             "l"(ks + row * HD + col * 8) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(vd + row * PITCH + col * 16),
+                             "l"(vs + row * HD + col * 8) : "memory");
             }
         } else if (tid == 0) {
             record_device_error(err, kErrAttnBlock, blk, phys);
@@ -139,84 +153,92 @@ __global__ void __launch_bounds__(kCT) chunk_attn_kernel(CParams p, DevError* er
     for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float ma = -INFINITY, mb_ = -INFINITY, la = 0.f, lb = 0.f;
     const int lm = lane >> 3, lr = lane & 7;
-    for (int i = 0; i < nb; ++i) {
-        // groups committed: blocks 0 .. i + kNS - 2; block i has landed when at most kNS - 2 pend
-        asm volatile("cp.async.wait_group %0;" ::"n"(kNS - 2) : "memory");
+    // a last block that ends behind the chunk's last position takes a round of its own, its rows there cleared
+    int i = 0;
+    for (int stop = nb > 0 && blk_end * kBSk > L ? nb - 1 : nb;; stop = nb) {
+        for (; i < stop; ++i) {
+            // groups committed: blocks 0 .. i + kNS - 2; block i has landed when at most kNS - 2 pend
+            asm volatile("cp.async.wait_group %0;" ::"n"(kNS - 2) : "memory");
+            __syncthreads();
+            const int blk = blk0 + i, b = i % kNS;
+            if (warp_live && ((okm >> b) & 1u)) {
+                const uint32_t ksm = sbase + (uint32_t)(b * 2 * TILE), vsm = ksm + TILE;
+                // ---- S = Q K^T for the block's 16 keys
+                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < KSTEPS; ++kk) {
+                    uint32_t b0, b1, b2, b3;
+                    const uint32_t addr = ksm + (uint32_t)(((lm >> 1) * 8 + lr) * PITCH + (16 * kk + (lm & 1) * 8) * 2);
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(addr));
+                    mma16816(s0, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
+                    mma16816(s1, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b2, b3);
+                }
+                // ---- causal mask and online softmax of rows ra (s*[0..1]) and rb (s*[2..3])
+                const int k0 = blk * kBSk + 2 * tq;
+                const float xa0 = va && k0 <= posa ? s0[0] * p.scale_log2 : -INFINITY;
+                const float xa1 = va && k0 + 1 <= posa ? s0[1] * p.scale_log2 : -INFINITY;
+                const float xa2 = va && k0 + 8 <= posa ? s1[0] * p.scale_log2 : -INFINITY;
+                const float xa3 = va && k0 + 9 <= posa ? s1[1] * p.scale_log2 : -INFINITY;
+                const float xb0 = vb && k0 <= posb ? s0[2] * p.scale_log2 : -INFINITY;
+                const float xb1 = vb && k0 + 1 <= posb ? s0[3] * p.scale_log2 : -INFINITY;
+                const float xb2 = vb && k0 + 8 <= posb ? s1[2] * p.scale_log2 : -INFINITY;
+                const float xb3 = vb && k0 + 9 <= posb ? s1[3] * p.scale_log2 : -INFINITY;
+                float mxa = fmaxf(fmaxf(xa0, xa1), fmaxf(xa2, xa3));
+                float mxb = fmaxf(fmaxf(xb0, xb1), fmaxf(xb2, xb3));
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+                const float mna = fmaxf(ma, mxa), mnb = fmaxf(mb_, mxb);
+                // a row with no key so far keeps its zero sums (reference 0 instead of -inf)
+                const float ra_ = mna == -INFINITY ? 0.f : mna, rb_ = mnb == -INFINITY ? 0.f : mnb;
+                const float aa = exp2f(ma - ra_), ab = exp2f(mb_ - rb_);
+                const float pa0 = exp2f(xa0 - ra_), pa1 = exp2f(xa1 - ra_), pa2 = exp2f(xa2 - ra_), pa3 = exp2f(xa3 - ra_);
+                const float pb0 = exp2f(xb0 - rb_), pb1 = exp2f(xb1 - rb_), pb2 = exp2f(xb2 - rb_), pb3 = exp2f(xb3 - rb_);
+                float sa = (pa0 + pa1) + (pa2 + pa3), sb = (pb0 + pb1) + (pb2 + pb3);
+                sa += __shfl_xor_sync(0xffffffffu, sa, 1);
+                sa += __shfl_xor_sync(0xffffffffu, sa, 2);
+                sb += __shfl_xor_sync(0xffffffffu, sb, 1);
+                sb += __shfl_xor_sync(0xffffffffu, sb, 2);
+                la = la * aa + sa;
+                lb = lb * ab + sb;
+                ma = mna;
+                mb_ = mnb;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    o[n][0] *= aa;
+                    o[n][1] *= aa;
+                    o[n][2] *= ab;
+                    o[n][3] *= ab;
+                }
+                const __half2 h0 = __floats2half2_rn(pa0, pa1), h1 = __floats2half2_rn(pb0, pb1);
+                const __half2 h2 = __floats2half2_rn(pa2, pa3), h3 = __floats2half2_rn(pb2, pb3);
+                const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&h0), u1 = *reinterpret_cast<const uint32_t*>(&h1);
+                const uint32_t u2 = *reinterpret_cast<const uint32_t*>(&h2), u3 = *reinterpret_cast<const uint32_t*>(&h3);
+                // ---- O += P V (V^T fragments by transposing ldmatrix)
+#pragma unroll
+                for (int pp = 0; pp < NT / 2; ++pp) {
+                    uint32_t v0, v1, v2, v3;
+                    const uint32_t addr = vsm + (uint32_t)(((lm & 1) * 8 + lr) * PITCH + (16 * pp + (lm >> 1) * 8) * 2);
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3) : "r"(addr));
+                    mma16816(o[2 * pp], u0, u1, u2, u3, v0, v1);
+                    mma16816(o[2 * pp + 1], u0, u1, u2, u3, v2, v3);
+                }
+            }
+            __syncthreads();   // every warp is done with buffer b
+            if (i + kNS - 1 < nb) {
+                const int nbuf = (i + kNS - 1) % kNS;
+                okm = (okm & ~(1u << nbuf)) | ((stage(blk0 + i + kNS - 1, nbuf) ? 1u : 0u) << nbuf);
+            } else {
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+        }
+        if (stop == nb) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kNS - 2) : "memory");   // it has landed
         __syncthreads();
-        const int blk = blk0 + i, b = i % kNS;
-        if (warp_live && ((okm >> b) & 1u)) {
-            const uint32_t ksm = sbase + (uint32_t)(b * 2 * TILE), vsm = ksm + TILE;
-            // ---- S = Q K^T for the block's 16 keys
-            float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < KSTEPS; ++kk) {
-                uint32_t b0, b1, b2, b3;
-                const uint32_t addr = ksm + (uint32_t)(((lm >> 1) * 8 + lr) * PITCH + (16 * kk + (lm & 1) * 8) * 2);
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(addr));
-                mma16816(s0, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
-                mma16816(s1, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b2, b3);
-            }
-            // ---- causal mask and online softmax of rows ra (s*[0..1]) and rb (s*[2..3])
-            const int k0 = blk * kBSk + 2 * tq;
-            const float xa0 = va && k0 <= posa ? s0[0] * p.scale_log2 : -INFINITY;
-            const float xa1 = va && k0 + 1 <= posa ? s0[1] * p.scale_log2 : -INFINITY;
-            const float xa2 = va && k0 + 8 <= posa ? s1[0] * p.scale_log2 : -INFINITY;
-            const float xa3 = va && k0 + 9 <= posa ? s1[1] * p.scale_log2 : -INFINITY;
-            const float xb0 = vb && k0 <= posb ? s0[2] * p.scale_log2 : -INFINITY;
-            const float xb1 = vb && k0 + 1 <= posb ? s0[3] * p.scale_log2 : -INFINITY;
-            const float xb2 = vb && k0 + 8 <= posb ? s1[2] * p.scale_log2 : -INFINITY;
-            const float xb3 = vb && k0 + 9 <= posb ? s1[3] * p.scale_log2 : -INFINITY;
-            float mxa = fmaxf(fmaxf(xa0, xa1), fmaxf(xa2, xa3));
-            float mxb = fmaxf(fmaxf(xb0, xb1), fmaxf(xb2, xb3));
-            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
-            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
-            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-            const float mna = fmaxf(ma, mxa), mnb = fmaxf(mb_, mxb);
-            // a row with no key so far keeps its zero sums (reference 0 instead of -inf)
-            const float ra_ = mna == -INFINITY ? 0.f : mna, rb_ = mnb == -INFINITY ? 0.f : mnb;
-            const float aa = exp2f(ma - ra_), ab = exp2f(mb_ - rb_);
-            const float pa0 = exp2f(xa0 - ra_), pa1 = exp2f(xa1 - ra_), pa2 = exp2f(xa2 - ra_), pa3 = exp2f(xa3 - ra_);
-            const float pb0 = exp2f(xb0 - rb_), pb1 = exp2f(xb1 - rb_), pb2 = exp2f(xb2 - rb_), pb3 = exp2f(xb3 - rb_);
-            float sa = (pa0 + pa1) + (pa2 + pa3), sb = (pb0 + pb1) + (pb2 + pb3);
-            sa += __shfl_xor_sync(0xffffffffu, sa, 1);
-            sa += __shfl_xor_sync(0xffffffffu, sa, 2);
-            sb += __shfl_xor_sync(0xffffffffu, sb, 1);
-            sb += __shfl_xor_sync(0xffffffffu, sb, 2);
-            la = la * aa + sa;
-            lb = lb * ab + sb;
-            ma = mna;
-            mb_ = mnb;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                o[n][0] *= aa;
-                o[n][1] *= aa;
-                o[n][2] *= ab;
-                o[n][3] *= ab;
-            }
-            const __half2 h0 = __floats2half2_rn(pa0, pa1), h1 = __floats2half2_rn(pb0, pb1);
-            const __half2 h2 = __floats2half2_rn(pa2, pa3), h3 = __floats2half2_rn(pb2, pb3);
-            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&h0), u1 = *reinterpret_cast<const uint32_t*>(&h1);
-            const uint32_t u2 = *reinterpret_cast<const uint32_t*>(&h2), u3 = *reinterpret_cast<const uint32_t*>(&h3);
-            // ---- O += P V (V^T fragments by transposing ldmatrix)
-#pragma unroll
-            for (int pp = 0; pp < NT / 2; ++pp) {
-                uint32_t v0, v1, v2, v3;
-                const uint32_t addr = vsm + (uint32_t)(((lm & 1) * 8 + lr) * PITCH + (16 * pp + (lm >> 1) * 8) * 2);
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3) : "r"(addr));
-                mma16816(o[2 * pp], u0, u1, u2, u3, v0, v1);
-                mma16816(o[2 * pp + 1], u0, u1, u2, u3, v2, v3);
-            }
-        }
-        __syncthreads();   // every warp is done with buffer b
-        if (i + kNS - 1 < nb) {
-            const int nbuf = (i + kNS - 1) % kNS;
-            okm = (okm & ~(1u << nbuf)) | ((stage(blk0 + i + kNS - 1, nbuf) ? 1u : 0u) << nbuf);
-        } else {
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
+        clear_behind<HD>(p.position, p.T, sbase + (uint32_t)(i % kNS * 2 * TILE) + TILE);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     // this split's partial of rows ra, rb: sums, max and the unnormalised output
