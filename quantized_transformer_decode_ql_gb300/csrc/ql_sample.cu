@@ -986,7 +986,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
     }
     RowScale row;
     row.set(top, a.temp);
-    const Border every = {kKeyMin, row.hot() ? 0x7FFFFFFE : 0x7FFFFFFF};   // all that is above -inf
+    // all that is above -inf; in a count -inf comes last and does no harm
+    const Border any = {kKeyMin, 0x7FFFFFFF}, every = {kKeyMin, row.hot() ? 0x7FFFFFFE : 0x7FFFFFFF};
     Border border = every, prefix = every;
     if (a.minp > 0.f) {
         if (tid == 0) sh.least = min_p_least(a, top);
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         cluster_arrive();   // this CTA has read rank 0's count
         if (!listed) {
             cluster_wait();
-            find_border<kFirst, 32>(Tokens{run}, Search(row, p.vocab, every, (u64)a.topk), row, p.vocab, every, 0.f, 0, hist, sh, ranks, turn);
+            find_border<kFirst, 32>(Tokens{run}, Search(row, p.vocab, any, (u64)a.topk), row, p.vocab, any, 0.f, 0, hist, sh, ranks, turn);
             e += kList;
         }
         if (rank == 0)
@@ -1009,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(Params p, DevError*
         return;   // no CTA reads another's shared memory any more
     }
     if (a.topk > 0 && a.topk < p.vocab) {
-        prefix = find_border<kCount, 32>(Tokens{run}, Search(row, p.vocab, every, (u64)a.topk), row, p.vocab, every, 0.f, 0, hist, sh, ranks, turn);
+        prefix.tighten(find_border<kCount, 32>(Tokens{run}, Search(row, p.vocab, any, (u64)a.topk), row, p.vocab, any, 0.f, 0, hist, sh, ranks, turn));
         border.tighten(prefix);
     }
     bool ready = false;   // the kept sums are there
