@@ -17,7 +17,7 @@ from ._lib import (QLError, QL_OK, QL_EINVAL, QL_ENOMEM, QL_ECUDA, QL_EPOOL, QL_
                    QL_GEMV_ACT_INT16, QL_GEMV_ACT_INT8, QL_KV_F16, QL_KV_Q8_0_Q5_1, QL_KV_Q4_1,
                    QL_ATTN_MERGE_TICKET, QL_ATTN_MERGE_CLUSTER,
                    Q4Matrix, LayerDesc, ModelDesc,
-                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, check_array, check_device, check_pool,
+                   StepArgs, Sampling, SIGNATURES, LIB_PATH, lib, check, check_array, check_device, check_pool, device_index,
                    check_sampling, ptr, stream_ptr)
 
 __all__ = [
@@ -255,31 +255,49 @@ def ql_kv4_record_bytes(head_dim):
     return int(lib().ql_kv4_record_bytes(head_dim))
 
 
+_types = None   # float16, int32, int64
+
+
+def _torch_types():
+    global _types
+    import torch
+    _types = (torch.float16, torch.int32, torch.int64)
+    return _types
+
+
+def _kv4_rows(name, k, v, slots, n_kv_heads, head_dim, pool, num_blocks):
+    """The tensors of a write or a read checked: the number of rows, k's and v's type and row strides, the pool's address."""
+    here, size = device_index(), num_blocks * n_kv_heads * 20 * head_dim
+    address = pool
+    if pool.__class__ is not int:
+        if pool is None or pool.get_device() != here or pool.nbytes < size or not pool.is_contiguous():
+            check_pool(name, pool, size)
+            check_device(name, pool)
+        address = pool.data_ptr()
+    n = slots.numel()
+    if (k.get_device() != here or v.get_device() != here or slots.get_device() != here
+            or slots.dtype is not (_types or _torch_types())[2] or not slots.is_contiguous()):
+        check_array(name, "slots", slots, "torch.int64", 0)
+        check_device(name, k, v, slots)
+    return (n, _dtype_of(name, k, v), _row_stride(name, k, n, n_kv_heads, head_dim), _row_stride(name, v, n, n_kv_heads, head_dim),
+            address)
+
+
 def ql_kv4_write(k, v, slots, n_kv_heads, head_dim, pool, num_blocks, stream=None):
     """Quantise rows ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided) into one layer's 4-bit
     pool at physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out)."""
-    n = slots.numel()
-    check_array("ql_kv4_write", "slots", slots, "torch.int64", 0)
-    check_device("ql_kv4_write", k, v, slots, pool)
-    check_pool("ql_kv4_write", pool, num_blocks * n_kv_heads * 20 * head_dim)
-    ks = _row_stride("ql_kv4_write", k, n, n_kv_heads, head_dim)
-    vs = _row_stride("ql_kv4_write", v, n, n_kv_heads, head_dim)
-    status = lib().ql_kv4_write(k.data_ptr(), v.data_ptr(), _dtype_of("ql_kv4_write", k, v), ks, vs, slots.data_ptr(), n,
-                                n_kv_heads, head_dim, ptr(pool), num_blocks, stream_ptr(stream))
+    n, kind, ks, vs, address = _kv4_rows("ql_kv4_write", k, v, slots, n_kv_heads, head_dim, pool, num_blocks)
+    status = lib().ql_kv4_write(k.data_ptr(), v.data_ptr(), kind, ks, vs, slots.data_ptr(), n, n_kv_heads, head_dim, address,
+                                num_blocks, stream_ptr(stream))
     if status:
         check(status)
 
 
 def ql_kv4_read(pool, slots, n_kv_heads, head_dim, num_blocks, k, v, stream=None):
     """The values of ``slots`` read back into ``k``, ``v`` (f32 or f16 [n, n_kv, hd], rows may be strided)."""
-    n = slots.numel()
-    check_array("ql_kv4_read", "slots", slots, "torch.int64", 0)
-    check_device("ql_kv4_read", k, v, slots, pool)
-    check_pool("ql_kv4_read", pool, num_blocks * n_kv_heads * 20 * head_dim)
-    ks = _row_stride("ql_kv4_read", k, n, n_kv_heads, head_dim)
-    vs = _row_stride("ql_kv4_read", v, n, n_kv_heads, head_dim)
-    status = lib().ql_kv4_read(ptr(pool), slots.data_ptr(), n, n_kv_heads, head_dim, num_blocks, k.data_ptr(), v.data_ptr(),
-                               _dtype_of("ql_kv4_read", k, v), ks, vs, stream_ptr(stream))
+    n, kind, ks, vs, address = _kv4_rows("ql_kv4_read", k, v, slots, n_kv_heads, head_dim, pool, num_blocks)
+    status = lib().ql_kv4_read(address, slots.data_ptr(), n, n_kv_heads, head_dim, num_blocks, k.data_ptr(), v.data_ptr(), kind,
+                               ks, vs, stream_ptr(stream))
     if status:
         check(status)
 
@@ -293,20 +311,30 @@ def ql_paged_attn_decode_kv4(q, pool, block_tables, context_lens, batch, n_heads
     """Single-token attention over a 4-bit pool: ``q``, ``out`` f16 [batch, n_heads, head_dim], ``block_tables`` int32
     [batch, max_blocks_per_seq], ``context_lens`` int32 [batch], all contiguous; ``workspace``: a zero-filled byte tensor."""
     name = "ql_paged_attn_decode_kv4"
-    rows = batch * n_heads * head_dim
-    for what, t, dtype, n in (("q", q, "torch.float16", rows), ("out", out, "torch.float16", rows),
-                              ("block_tables", block_tables, "torch.int32", batch * max_blocks_per_seq),
-                              ("context_lens", context_lens, "torch.int32", batch)):
-        if not isinstance(t, int):
-            check_array(name, what, t, dtype, n)
-    if not workspace.is_contiguous():
+    half, whole, _ = _types or _torch_types()
+    here, rows, size = device_index(), batch * n_heads * head_dim, num_blocks * n_kv_heads * 20 * head_dim
+    entries = batch * max_blocks_per_seq
+    for t, kind, n in ((q, half, rows), (out, half, rows), (block_tables, whole, entries), (context_lens, whole, batch)):
+        if t.__class__ is not int and (t is None or t.dtype is not kind or t.numel() < n or t.get_device() != here
+                                       or not t.is_contiguous()):
+            for what, x, dtype, m in (("q", q, "torch.float16", rows), ("out", out, "torch.float16", rows),
+                                      ("block_tables", block_tables, "torch.int32", entries),
+                                      ("context_lens", context_lens, "torch.int32", batch)):
+                if not isinstance(x, int):
+                    check_array(name, what, x, dtype, m)
+            check_device(name, q, out, block_tables, context_lens)
+            break
+    if pool.__class__ is not int and (pool is None or pool.nbytes < size or pool.get_device() != here or not pool.is_contiguous()):
+        check_pool(name, pool, size)
+        check_device(name, pool)
+    if workspace.get_device() != here or not workspace.is_contiguous():
+        check_device(name, workspace)
         raise QLError(QL_EINVAL, f"{name}: the workspace must be contiguous")
-    check_device(name, q, pool, block_tables, context_lens, out, workspace)
-    check_pool(name, pool, num_blocks * n_kv_heads * 20 * head_dim)
-    check(lib().ql_paged_attn_decode_kv4(ptr(q), ptr(pool), ptr(block_tables), ptr(context_lens), batch, n_heads,
-                                         n_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, scale,
-                                         ptr(out), ptr(workspace), workspace.numel() * workspace.element_size(),
-                                         stream_ptr(stream)))
+    status = lib().ql_paged_attn_decode_kv4(ptr(q), ptr(pool), ptr(block_tables), ptr(context_lens), batch, n_heads, n_kv_heads,
+                                            head_dim, block_size, max_blocks_per_seq, num_blocks, scale, ptr(out),
+                                            workspace.data_ptr(), workspace.nbytes, stream_ptr(stream))
+    if status:
+        check(status)
 
 
 def ql_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,

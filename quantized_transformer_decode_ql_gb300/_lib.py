@@ -208,12 +208,16 @@ def _find_current_device():
     return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def check_device(name, *tensors):
-    """Refuse tensors that are not on the current GPU (None and plain addresses pass)."""
+def device_index() -> int:
     global _current_device
     if _current_device is None:
         _current_device = _find_current_device()
-    here = _current_device()
+    return _current_device()
+
+
+def check_device(name, *tensors):
+    """Refuse tensors that are not on the current GPU (None and plain addresses pass)."""
+    here = device_index()
     for t in tensors:
         if t is not None and t.__class__ is not int and t.get_device() != here:
             raise QLError(QL_EINVAL, f"{name}: tensors must be on the current GPU, got one on {t.device}")
@@ -243,7 +247,8 @@ def _find_current_stream():
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    device = torch.cuda.current_device
+    torch.cuda.current_device()   # initialises CUDA
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return lambda: raw(device())
 
 

@@ -146,3 +146,12 @@ def test_sampled_outputs_that_overlap():
         for at in [0x1000 * i + d for i in range(1, 7) for d in (-28, 0, 28)] + [(1 << 20) - 28, end - 4]:
             assert status(**{out: at}) == ql.QL_EINVAL and "overlap" in L.ql_last_error().decode(), (out, hex(at))
     assert status(tokens=0x8000) == ql.QL_EINVAL and status(probs=0x7000 + 28) == ql.QL_EINVAL
+
+
+def test_rows_of_another_type(gpu, no_library):
+    slots, pool = gpu(torch.zeros(3, dtype=torch.int64)), gpu(torch.zeros((2, 2, 1280), dtype=torch.uint8))
+    k = torch.zeros((3, 2, 64))
+    for a, b in ((k.long(), k.long()), (k, k.half()), (k.bfloat16(), k.bfloat16()), (k.double(), k.double())):
+        for _ in range(2):
+            refused("float32", ql.ql_kv4_write, gpu(a), gpu(b), slots, 2, 64, pool, 2)
+            refused("float32", ql.ql_kv4_read, pool, slots, 2, 64, 2, gpu(a), gpu(b))
