@@ -477,9 +477,10 @@ __device__ Border find_border(const S& src, Search f, const RowScale& row, int v
         const uint32_t rest = at == 0 ? f.qb - f.qa : at == 1 ? f.kb - f.ka : f.ib - f.ia;
         __syncthreads();   // the histogram has been read
         src.pass([&](float l2, int i) {
-            if (KIND == kFirst) {   // all up to the interval's last
-                const uint32_t k = key_of(l2);
-                if (at == 0 ? distance(l2, row) > f.qb : at == 1 ? k < f.ka : !(Border{f.ka, (int)f.ib}.keeps(k, i))) return;
+            if (KIND == kFirst) {   // all up to the interval's last: f.base and in_bin, kList at most
+                const uint32_t k = key_of(l2), q = distance(l2, row);
+                // (while keys are divided f.ka may be lower than any of this distance, and tokens of the next one lie above it)
+                if (at == 0 ? q > f.qb : at == 1 ? q > f.qa || (q == f.qa && k < f.ka) : !(Border{f.ka, (int)f.ib}.keeps(k, i))) return;
             } else if (f.digit(at, l2, i, row, in) > rest) {
                 return;
             }
@@ -512,7 +513,7 @@ __device__ Border find_border(const S& src, Search f, const RowScale& row, int v
         if (tid == 0) sh.border = in;
         cluster_sync();   // the lists may be written again
         if (KIND == kFirst) {
-            if (tid == 0) sh.found = total;
+            if (tid == 0) sh.found = min(total, (uint32_t)kList);
             __syncthreads();
             return in;
         }
