@@ -359,7 +359,8 @@ int ql_kv4_read(const void* d_pool, const int64_t* d_slots, int64_t n, int n_kv_
                 int64_t num_blocks, void* d_k, void* d_v, int dtype, int64_t k_stride, int64_t v_stride,
                 void* stream);
 /* ql_paged_attn_decode over a 4-bit pool (d_pool: one layer, 16-byte aligned). Arguments and
- * errors as for ql_paged_attn_decode, except that any group n_heads / n_kv_heads is taken, that
+ * errors as for ql_paged_attn_decode, except that any group n_heads / n_kv_heads is taken (the
+ * records are read once per 8 heads of it), that
  * keys of a block id outside the pool are left out of the softmax (and recorded), and that a
  * sequence whose length is outside [0, max_blocks_per_seq * 16] (recorded) or 0 leaves its
  * output row as it was. batch <= 65535, n_heads <= 2^20, batch * n_heads < 2^24, max_blocks_per_seq < 2^25, batch *

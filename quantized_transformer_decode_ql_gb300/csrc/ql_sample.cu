@@ -20,8 +20,8 @@
 //
 // Measured (vocab 151936): one row with top-k 50 and top-p 0.95 9.4 us, of which the load is 1.3, the
 // largest logit 1.1, the threshold 1.1, the list 2.6 and the draw 2.4: barriers and latency, not memory.
-// Top-p 0.9 alone 20.5 us (15.0 at T 0.3), 34 us for 32 rows; 32 rows with min-p 0.02 too 17 us, no filter 13 us. 256 rows of
-// 50021 without a filter 27.5 us (1.9 TB/s): both passes are near their bounds, memory (8.7 us) and 28
+// Top-p 0.9 alone 21 us at T 0.6 - 1.2 (15.3 at T 0.3), 38 us for 32 rows; 32 rows with min-p 0.02 too 17 us, no filter 13 us. 256 rows of
+// 50021 without a filter 27.5 us (1.9 TB/s): a pass at memory speed (8.7 us), a barrier, and one of 28
 // instructions a token (8.5 us), on the SMs that hold two rows of the 1.7 there are to each.
 #include <cuda_fp16.h>
 #include <float.h>
