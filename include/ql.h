@@ -256,7 +256,8 @@ int ql_paged_attn_decode(const void* d_q, const void* d_k_pool, const void* d_v_
  * are the MMA rows); the block table's splits are merged by a second kernel. d_out f16
  * [n_tokens][n_heads * head_dim]. d_workspace: ql_paged_attn_chunk_workspace_bytes, contents
  * need not be initialised. Tolerance as ql_paged_attn_decode. Block ids out of range are
- * recorded in the device error record and their keys skipped. 1 <= n_tokens <= 256.       */
+ * recorded in the device error record and their keys skipped (a token that none is left for has
+ * an output of 0). What the last block holds behind the chunk does not matter. 1 <= n_tokens <= 256. */
 size_t ql_paged_attn_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int n_kv_heads, int head_dim);
 int ql_paged_attn_chunk(const void* d_q, const void* d_k_pool, const void* d_v_pool, const int32_t* d_block_table,
                         const int32_t* d_position, int64_t n_tokens, int n_heads, int n_kv_heads, int head_dim,

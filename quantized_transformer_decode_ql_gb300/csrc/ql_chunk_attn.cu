@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(CParams p) {
             }
         }
         if (lane < HD / 4) {
-            const float inv = 1.0f / Ls;
+            const float inv = Ls == 0.f ? 0.f : 1.0f / Ls;   // no key at all (ids outside the pool): zeros
             __half2* dst = reinterpret_cast<__half2*>(p.out + (size_t)row * HD) + 2 * lane;
             dst[0] = __floats2half2_rn(A.x * inv, A.y * inv);
             dst[1] = __floats2half2_rn(A.z * inv, A.w * inv);

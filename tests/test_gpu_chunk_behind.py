@@ -43,6 +43,30 @@ def test_chunk_attention_over_blocks_with_stale_rows(hd, p0, T, stale):
     assert np.all(np.isfinite(outs[0])) and np.array_equal(*outs)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_tokens_without_a_key_are_zero(hd):
+    """The first block's id is outside the pool: tokens 0 - 15 see nothing, the others the second block."""
+    ql = lib()
+    rng = np.random.default_rng(hd)
+    T, n_heads, n_kv = 24, 8, 2
+    k, v = (rng.standard_normal((2, n_kv, 16, hd)).astype(np.float16) for _ in range(2))
+    q = rng.standard_normal((T, n_heads, hd)).astype(np.float16)
+    ws = torch.empty(ql.ql_paged_attn_chunk_workspace_bytes(T, n_heads, n_kv, hd), dtype=torch.uint8, device="cuda")
+    out = torch.full((T, n_heads * hd), 7.0, dtype=torch.float16, device="cuda")
+    ql.ql_paged_attn_chunk(dev(q), dev(k), dev(v), dev(np.array([-1, 1], np.int32)), dev(np.zeros(1, np.int32)), T, n_heads, n_kv, hd,
+                           16, 2, 2, 0.1, out, ws)
+    with pytest.raises(ql.QLError):
+        ql.ql_check_device_error()
+    got = out.cpu().numpy().reshape(T, n_heads, hd).astype(np.float64)
+    assert np.all(got[:16] == 0)
+    for t in range(16, T):
+        for h in range(n_heads):
+            x = k[1, h // 4, :t - 15].astype(np.float64) @ q[t, h].astype(np.float64) * 0.1
+            p = np.exp(x - x.max())
+            want = p @ v[1, h // 4, :t - 15].astype(np.float64) / p.sum()
+            assert np.all(np.abs(got[t, h] - want) <= 2e-3 + 1e-2 * np.abs(want))
+
+
 def prompt(gm, cfg, tokens, position, table):
     logits = torch.zeros(cfg.vocab, dtype=torch.float32, device="cuda")
     gm.ql_prefill_chunk(dev(tokens.astype(np.int32)), dev(np.array([position], np.int32)), dev(table), logits=logits)
