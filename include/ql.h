@@ -380,6 +380,66 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
                              float scale, void* d_out, void* d_workspace, size_t workspace_bytes,
                              void* stream);
 
+/* --------------------------------------------------------------- latent attention
+ * Attention whose cache keeps one row a token for all heads: a normalised latent vector c of `rank`
+ * values and a rotated key part r of rope_dim values (f16, 2 (rank + rope_dim) bytes a token whatever
+ * the heads). Head h has key [Wk_h c | r] and value Wv_h c, Wk_h and Wv_h of head_dim rows each.
+ * head_dim 64 or 128, rank 256 or 512, rope_dim 64, block_size 16, n_heads 1..1024 (any number).
+ * Layout: one layer's pool is f16 [num_blocks][16][rank + rope_dim]; d_w_kv is f16
+ * [n_heads][2 head_dim][rank], a head's key rows before its value rows; a query is f16
+ * [n_heads][head_dim + rope_dim], the rotated part last. num_blocks < 2^27.
+ *
+ * ql_mla_append: n tokens' projections into the cache and the queries made ready. Row i of d_kv
+ * ([rank + rope_dim] of dtype, QL_DTYPE_F32 or QL_DTYPE_F16, kv_stride elements after the row before) goes to slot
+ * d_slots[i] % 16 of block d_slots[i] / 16 as f16( x / sqrt(mean x^2 + eps) * d_norm_w | rot ), the mean over
+ * the first rank values, rot the rotation of the last rope_dim: pairs (j, j + rope_dim / 2) by the angle of
+ * position d_positions[i] (int32 [n]) in the tables d_cos / d_sin, f32 [max_position][rope_dim / 2]
+ * (ql_rope_tables with head_dim = rope_dim). Row i of d_q ([n_heads][head_dim + rope_dim] of dtype, q_stride
+ * elements apart) is written to row i of d_q_out, f16, contiguous, the last rope_dim values of each head rotated alike. d_q and
+ * d_q_out may both be NULL. A slot of -1 marks a row to leave out (a padded batch): neither its
+ * cache row nor its query is written. Any other slot outside the pool, or a position outside the tables, leaves
+ * the row out too and is recorded in the device error record, as is a cache row with a value that f16 does
+ * not hold (the row is written). The slots of one call must differ from one another (-1 may repeat).
+ * d_q_out overlaps no input. Rows, norm weights, d_q_out and the pool 16-byte aligned, strides multiples
+ * of 16 bytes and at least a row (any when n is 1), below 2^31 elements. n = 0 is allowed, n < 2^31. Asynchronous on stream. */
+int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride, int64_t kv_stride, const float* d_norm_w,
+                  const float* d_cos, const float* d_sin, const int32_t* d_positions, const int64_t* d_slots, float eps,
+                  int64_t n, int n_heads, int head_dim, int rank, int rope_dim, void* d_q_out, void* d_pool,
+                  int64_t num_blocks, int64_t max_position, void* stream);
+/* One new token of each sequence (the absorbed form):
+ *   out[b][h] = Wv_h sum_{t < context_lens[b]} softmax_t((Wk_h^T q[b][h][0:head_dim] . c_t + q[b][h][head_dim:] . r_t) scale) c_t
+ * with row t of sequence b in slot t % 16 of block d_block_tables[b][t / 16]. The weights are multiplied into the query
+ * (rounded to f16) and into the sum (rounded to f16), so that the cache is read once, as it is, for up to 64 heads.
+ * d_q f16 [batch][n_heads][head_dim + rope_dim]; d_block_tables int32 [batch][max_blocks_per_seq]; d_context_lens int32
+ * [batch], each in [0, max_blocks_per_seq * 16]: 0 marks an idle slot, whose output row is left as it was, as is
+ * that of a length outside the range (recorded). A block id outside the pool is recorded and its keys left out
+ * of the softmax (an output of 0 where none is left). What a sequence's last block holds behind its length does
+ * not matter. An absorbed query that f16 does not hold is recorded (its outputs are then not finite).
+ * d_out f16 [batch][n_heads * head_dim]. batch <= 65535, batch * n_heads < 2^22, max_blocks_per_seq <= 2^20.
+ * q, the weights, the pool and the output 16-byte aligned. d_workspace: ql_mla_decode_workspace_bytes(...)
+ * bytes, 128-byte aligned, any contents; calls and captured graphs that may run at the same time need
+ * workspaces of their own. The split of the work over the SMs is made from the lengths on the
+ * device, so that a captured call serves any lengths. */
+size_t ql_mla_decode_workspace_bytes(int64_t batch, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq);
+int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_tables,
+                       const int32_t* d_context_lens, int64_t batch, int n_heads, int head_dim, int rank, int rope_dim,
+                       int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
+                       void* d_workspace, size_t workspace_bytes, void* stream);
+/* A chunk of a prompt (the expanded form): query i of d_q, f16 [n_tokens][n_heads][head_dim + rope_dim], is at
+ * position p + i, p = *d_position (int32 [1], device), and attends to rows 0 .. p + i of the sequence whose table is
+ * d_block_table (int32 [max_blocks_per_seq]); all of them are in the cache already. Keys and values are made from the
+ * latents of the whole context, as f16, in the workspace. Worth it from about 170 tokens (head_dim 128,
+ * rank 512) on; few tokens behind a long context are cheaper as a batch of ql_mla_attn_decode that
+ * repeats the table. d_out f16 [n_tokens][n_heads * head_dim]. Block ids as for ql_mla_attn_decode (an
+ * output of 0 for a query that no key is left for); a position below 0 or a chunk that ends behind the table is recorded
+ * and leaves the output as it was. 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22, max_blocks_per_seq <= 2^16.
+ * Alignments and workspace (ql_mla_chunk_workspace_bytes) as for ql_mla_attn_decode. */
+size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq);
+int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
+                      const int32_t* d_position, int64_t n_tokens, int n_heads, int head_dim, int rank, int rope_dim,
+                      int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
+                      void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* --------------------------------------------------------------- token sampling
  * The next token of each row of logits from one uniform number u in [0, 1) per row. Row b, with
  * T = d_temperature[b], weights w_i = exp((l_i - max l) / T), tokens in order of falling logit

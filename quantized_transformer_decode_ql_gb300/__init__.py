@@ -28,7 +28,8 @@ __all__ = [
     "ql_paged_attn_chunk_workspace_bytes", "ql_paged_attn_chunk",
     "ql_kvq_record_bytes", "ql_kvq_write", "ql_paged_attn_decode_kvq",
     "ql_kv4_record_bytes", "ql_kv4_write", "ql_kv4_read", "ql_paged_attn_kv4_workspace_bytes",
-    "ql_paged_attn_decode_kv4", "ql_sample",
+    "ql_paged_attn_decode_kv4", "ql_mla_append", "ql_mla_decode_workspace_bytes", "ql_mla_attn_decode",
+    "ql_mla_chunk_workspace_bytes", "ql_mla_attn_chunk", "ql_sample",
     "ql_set_attn_merge_form", "ql_paged_attn_merge_form",
     "ql_kv_q8_0_row_bytes", "ql_kv_q5_1_row_bytes", "ql_kv_quantize_q8_0", "ql_kv_dequantize_q8_0",
     "ql_kv_quantize_q5_1", "ql_kv_dequantize_q5_1", "ql_kv_quantize_device", "ql_kv_dequantize_device",
@@ -333,6 +334,95 @@ def ql_paged_attn_decode_kv4(q, pool, block_tables, context_lens, batch, n_heads
     status = lib().ql_paged_attn_decode_kv4(ptr(q), ptr(pool), ptr(block_tables), ptr(context_lens), batch, n_heads, n_kv_heads,
                                             head_dim, block_size, max_blocks_per_seq, num_blocks, scale, ptr(out),
                                             workspace.data_ptr(), workspace.nbytes, stream_ptr(stream))
+    if status:
+        check(status)
+
+
+def ql_mla_append(q, kv, norm_w, cos_t, sin_t, positions, slots, eps, n_heads, head_dim, rank, rope_dim, q_out, pool, num_blocks,
+                  max_position, stream=None):
+    """Latent rows ``kv`` (f32 or f16 [n, rank + rope_dim], rows may be strided) normalised and rotated into the paged ``pool`` (f16) at
+    physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out), queries ``q`` ([n, n_heads, head_dim + rope_dim] of the same
+    type, or None) rotated into ``q_out`` (f16, contiguous); ``positions`` int32 [n], the tables f32 [max_position, rope_dim / 2]."""
+    name = "ql_mla_append"
+    n, row, width = slots.numel(), rank + rope_dim, head_dim + rope_dim
+    half, whole, long = _types or _torch_types()
+    here, turns = device_index(), max_position * (rope_dim // 2)
+    for what, t, kind, size in (("norm_w", norm_w, norm_w.dtype, rank), ("cos_t", cos_t, norm_w.dtype, turns),
+                                ("sin_t", sin_t, norm_w.dtype, turns), ("positions", positions, whole, n), ("slots", slots, long, n),
+                                ("q_out", q_out, half, n * n_heads * width)):
+        if t is None and what == "q_out":
+            continue
+        if t.dtype is not kind or t.numel() < size or t.get_device() != here or not t.is_contiguous():
+            check_array(name, what, t, str(kind), size)
+            check_device(name, t)
+    if str(norm_w.dtype) != "torch.float32":
+        raise QLError(QL_EINVAL, f"{name}: norm_w must be float32")
+    if pool is None or pool.dtype is not half or pool.numel() < num_blocks * 16 * row or pool.get_device() != here or not pool.is_contiguous():
+        check_array(name, "pool", pool, "torch.float16", num_blocks * 16 * row)
+        check_device(name, pool)
+        raise QLError(QL_EINVAL, f"{name}: the pool must be a contiguous float16 tensor")
+    check_device(name, kv, q)
+    if (q is None) != (q_out is None):
+        raise QLError(QL_EINVAL, f"{name}: q and q_out come together")
+    status = lib().ql_mla_append(ptr(q), kv.data_ptr(), _dtype_of(name, kv, q), _row_stride(name, q, n, n_heads, width) if q is not None else 0,
+                                 _row_stride(name, kv, n, 1, row), norm_w.data_ptr(), cos_t.data_ptr(), sin_t.data_ptr(),
+                                 positions.data_ptr(), slots.data_ptr(), eps, n, n_heads, head_dim, rank, rope_dim, ptr(q_out),
+                                 pool.data_ptr(), num_blocks, max_position, stream_ptr(stream))
+    if status:
+        check(status)
+
+
+def _mla_tensors(name, q, w_kv, pool, table, lens, rows, tables, n_lens, n_heads, head_dim, rank, rope_dim, max_blocks_per_seq,
+                 num_blocks, out, workspace):
+    """The tensors of a latent attention checked."""
+    half, whole, _ = _types or _torch_types()
+    here = device_index()
+    arrays = (("q", q, half, rows * n_heads * (head_dim + rope_dim)), ("w_kv", w_kv, half, n_heads * 2 * head_dim * rank),
+              ("pool", pool, half, num_blocks * 16 * (rank + rope_dim)), ("table", table, whole, tables * max_blocks_per_seq),
+              ("lengths", lens, whole, n_lens), ("out", out, half, rows * n_heads * head_dim))
+    for what, t, kind, size in arrays:
+        if t is None or t.dtype is not kind or t.numel() < size or t.get_device() != here or not t.is_contiguous():
+            if t is None:
+                raise QLError(QL_EINVAL, f"{name}: {what} is missing")
+            check_array(name, what, t, str(kind), size)
+            check_device(name, t)
+    if workspace.get_device() != here or not workspace.is_contiguous():
+        check_device(name, workspace)
+        raise QLError(QL_EINVAL, f"{name}: the workspace must be contiguous")
+
+
+def ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq):
+    return int(lib().ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq))
+
+
+def ql_mla_attn_decode(q, w_kv, pool, block_tables, context_lens, batch, n_heads, head_dim, rank, rope_dim, block_size,
+                       max_blocks_per_seq, num_blocks, scale, out, workspace, stream=None):
+    """Single-token latent attention over the paged pool of ql_mla_append: ``q`` f16 [batch, n_heads, head_dim + rope_dim], ``w_kv`` f16
+    [n_heads, 2 head_dim, rank], ``block_tables`` int32 [batch, max_blocks_per_seq], ``context_lens`` int32 [batch], ``out`` f16
+    [batch, n_heads, head_dim], all contiguous; ``workspace``: a byte tensor of ql_mla_decode_workspace_bytes, any contents."""
+    _mla_tensors("ql_mla_attn_decode", q, w_kv, pool, block_tables, context_lens, batch, batch, batch, n_heads, head_dim, rank, rope_dim,
+                 max_blocks_per_seq, num_blocks, out, workspace)
+    status = lib().ql_mla_attn_decode(q.data_ptr(), w_kv.data_ptr(), pool.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+                                      batch, n_heads, head_dim, rank, rope_dim, block_size, max_blocks_per_seq, num_blocks, scale,
+                                      out.data_ptr(), workspace.data_ptr(), workspace.nbytes, stream_ptr(stream))
+    if status:
+        check(status)
+
+
+def ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq):
+    return int(lib().ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq))
+
+
+def ql_mla_attn_chunk(q, w_kv, pool, block_table, position, n_tokens, n_heads, head_dim, rank, rope_dim, block_size,
+                      max_blocks_per_seq, num_blocks, scale, out, workspace, stream=None):
+    """Causal latent attention of a prompt chunk at positions ``position[0] + i`` (int32 [1] device) over the sequence's ``block_table``:
+    ``q`` f16 [n_tokens, n_heads, head_dim + rope_dim], ``out`` f16 [n_tokens, n_heads, head_dim]; the rest as for ql_mla_attn_decode,
+    ``workspace`` of ql_mla_chunk_workspace_bytes."""
+    _mla_tensors("ql_mla_attn_chunk", q, w_kv, pool, block_table, position, n_tokens, 1, 1, n_heads, head_dim, rank, rope_dim,
+                 max_blocks_per_seq, num_blocks, out, workspace)
+    status = lib().ql_mla_attn_chunk(q.data_ptr(), w_kv.data_ptr(), pool.data_ptr(), block_table.data_ptr(), position.data_ptr(),
+                                     n_tokens, n_heads, head_dim, rank, rope_dim, block_size, max_blocks_per_seq, num_blocks, scale,
+                                     out.data_ptr(), workspace.data_ptr(), workspace.nbytes, stream_ptr(stream))
     if status:
         check(status)
 

@@ -95,6 +95,14 @@ SIGNATURES = {
     "ql_paged_attn_kv4_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64]),
     "ql_paged_attn_decode_kv4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_int,
                                          c_int64, c_int64, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "ql_mla_append": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                              c_float, c_int64, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int64, c_int64, c_void_p]),
+    "ql_mla_decode_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64]),
+    "ql_mla_attn_decode": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_int,
+                                   c_int, c_int64, c_int64, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "ql_mla_chunk_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64]),
+    "ql_mla_attn_chunk": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_int,
+                                  c_int, c_int64, c_int64, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
     "ql_sample": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                           c_void_p, c_void_p, c_void_p, c_void_p]),
     "ql_paged_attn_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int, c_int64]),

@@ -52,6 +52,8 @@ enum DevErrWhere {
     kErrKvSlot = 13,
     kErrSampleArg = 14,
     kErrAttnStage = 15,
+    kErrLatentValue = 16,
+    kErrLatentStage = 17,
 };
 // The current device's record (allocated on first use, zero-filled).
 DevError* device_error_record();
