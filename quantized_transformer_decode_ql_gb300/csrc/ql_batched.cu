@@ -1252,6 +1252,23 @@ int f16_rows_tensor_map(const void* base, uint64_t inner, uint64_t outer, uint32
     return r == CUDA_SUCCESS ? QL_OK : set_error(QL_ECUDA, "tensor map: f16 rows encoding failed (" + std::to_string((int)r) + ")");
 }
 
+int f16_tensor_map(const void* base, int nd, const uint64_t* dims, const uint64_t* strides, const uint32_t* box, CUtensorMap* map) {
+    const EncodeTiledFn enc = encode_tiled();
+    if (enc == nullptr) return set_error(QL_ECUDA, "tensor map: cuTensorMapEncodeTiled is not available");
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < nd; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1u;
+        if (i + 1 < nd) st[i] = strides[i];
+    }
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)nd, const_cast<void*>(base), d, st, b, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QL_OK : set_error(QL_ECUDA, "tensor map: encoding failed (" + std::to_string((int)r) + ")");
+}
+
 // The tensor-core form of batch 3-32 (process-wide): mma.sync by default (measured faster on the
 // decode step), tcgen05 with ql_set_batched_gemv_form or QL_BATCHED_TC=1.
 static std::atomic<int> g_form{-1};

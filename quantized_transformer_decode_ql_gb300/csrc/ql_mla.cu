@@ -220,9 +220,10 @@ int simple(const __half* q, const __half* w, const __half* pool, const int32_t* 
     return e == cudaSuccess ? QL_OK : cuda_error(e, "latent attention");
 }
 
-int attn_check(const char* name, const void* q, const void* w, const void* pool, const void* table, const void* lens, int64_t rows,
-               int n_heads, int head_dim, int rank, int rope_dim, int block_size, int64_t maxb, int64_t num_blocks, const void* out,
-               const void* ws, size_t ws_bytes, size_t need) {
+}  // namespace
+
+int mla::attn_check(const char* name, const void* q, const void* w, const void* pool, const void* table, const void* lens, int head_dim,
+                    int rank, int rope_dim, int block_size, int64_t num_blocks, const void* out, const void* ws, size_t ws_bytes, size_t need) {
     const std::string nm(name);
     if (!q || !w || !pool || !table || !lens || !out || !ws) return set_error(QL_EINVAL, nm + ": null pointer");
     if (!mla::shape_ok(head_dim, rank) || rope_dim != kRope || block_size != mla::kBlock)
@@ -237,7 +238,6 @@ int attn_check(const char* name, const void* q, const void* w, const void* pool,
     return QL_OK;
 }
 
-}  // namespace
 }  // namespace ql
 
 extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride, int64_t kv_stride, const float* d_norm_w,
@@ -282,15 +282,11 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_append");
 }
 
-extern "C" size_t ql_mla_decode_workspace_bytes(int64_t batch, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
-    if (!ql::mla::shape_ok(head_dim, rank) || batch < 1 || batch > 65535 || n_heads < 1 || n_heads > 1024 || max_blocks_per_seq < 1 ||
-        max_blocks_per_seq > (1 << 22))
-        return 0;
-    return (size_t)batch * n_heads * (2 * rank + ql::mla::kRope) * 4;
-}
-
 extern "C" size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
-    return ql_mla_decode_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq);
+    if (!ql::mla::shape_ok(head_dim, rank) || n_tokens < 1 || n_tokens > 65535 || n_heads < 1 || n_heads > 1024 || max_blocks_per_seq < 1 ||
+        max_blocks_per_seq > (1 << 16))
+        return 0;
+    return (size_t)n_tokens * n_heads * (2 * rank + ql::mla::kRope) * 4;
 }
 
 namespace ql {
@@ -303,28 +299,12 @@ int simple_of(int D, int R, A... a) {
 }  // namespace
 }  // namespace ql
 
-extern "C" int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_tables,
-                                  const int32_t* d_context_lens, int64_t batch, int n_heads, int head_dim, int rank, int rope_dim,
-                                  int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
-                                  void* d_workspace, size_t workspace_bytes, void* stream) {
-    using namespace ql;
-    if (int rc = attn_check("ql_mla_attn_decode", d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, batch, n_heads, head_dim, rank,
-                            rope_dim, block_size, max_blocks_per_seq, num_blocks, d_out, d_workspace, workspace_bytes,
-                            ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq)))
-        return rc;
-    return simple_of(head_dim, rank, static_cast<const __half*>(d_q), static_cast<const __half*>(d_w_kv),
-                     static_cast<const __half*>(d_pool), d_block_tables, d_context_lens, (const int32_t*)nullptr, (long long)batch, n_heads,
-                     (long long)max_blocks_per_seq, (long long)num_blocks, scale, static_cast<__half*>(d_out), d_workspace,
-                     static_cast<cudaStream_t>(stream));
-}
-
 extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
                                  const int32_t* d_position, int64_t n_tokens, int n_heads, int head_dim, int rank, int rope_dim,
                                  int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
                                  void* d_workspace, size_t workspace_bytes, void* stream) {
     using namespace ql;
-    if (int rc = attn_check("ql_mla_attn_chunk", d_q, d_w_kv, d_pool, d_block_table, d_position, n_tokens, n_heads, head_dim, rank,
-                            rope_dim, block_size, max_blocks_per_seq, num_blocks, d_out, d_workspace, workspace_bytes,
+    if (int rc = mla::attn_check("ql_mla_attn_chunk", d_q, d_w_kv, d_pool, d_block_table, d_position, head_dim, rank, rope_dim, block_size, num_blocks, d_out, d_workspace, workspace_bytes,
                             ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq)))
         return rc;
     return simple_of(head_dim, rank, static_cast<const __half*>(d_q), static_cast<const __half*>(d_w_kv),

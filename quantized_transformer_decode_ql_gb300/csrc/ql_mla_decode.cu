@@ -1,0 +1,692 @@
+// Latent attention of one new token per sequence over the paged cache, in three launches:
+//
+//  1. mla_absorb_kernel: q'_h = Wk_h^T q_h (f16), the heads' queries against the latents themselves; one more CTA cuts the
+//     batch's tiles of 64 keys into equal windows, one per SM (the lengths are on the device only);
+//  2. mla_decode_kernel: a window's tiles on the 5th-generation tensor cores, each tile read once for up to 64 heads:
+//     S^T = K q'^T (64 keys x heads), the online softmax, O^T += V^T P (rank x heads), K the tile's rows and V their first
+//     `rank` values, the same bytes in shared memory;
+//  3. mla_join_kernel: a sequence's parts joined, o rounded to f16, out_h = Wv_h o_h.
+#include "ql_batched.h"
+#include "ql_mla_tc.cuh"
+
+namespace ql {
+namespace mla {
+
+constexpr int kTile = 64;       // keys of a tile
+constexpr int kEnter = 1;       // tiles that entering a sequence costs a window (its query, its part written): charged in the split
+constexpr int kMaxWin = 160;    // windows at most
+constexpr int kPlanWin = 16;    // plan: [0] places in all, [1] places of a window; the windows' first sequences; the sequences' first places
+constexpr int kPlanStart = kPlanWin + kMaxWin;
+
+__host__ __device__ inline int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// ---------------------------------------------------------------- the plan and the absorbed queries
+struct AbsorbParams {
+    const __half* q;       // [batch][H][D + 64]
+    const __half* w;       // [H][2 D][R]
+    __half* qc;            // [batch][H][R + 64]
+    const int32_t* lens;
+    int* plan;
+    int batch, H, windows;
+    long long cap;         // longest length
+    DevError* err;
+};
+
+// Tiles of a sequence; 0 for an idle slot and for a length outside the table.
+__device__ __forceinline__ int tiles_checked(int len, long long cap) { return len > 0 && len <= cap ? tiles_of(len) : 0; }
+
+__device__ void make_plan(const AbsorbParams& p) {
+    __shared__ int sums[128];
+    __shared__ int total;
+    const int t = threadIdx.x, per = (p.batch + 127) / 128;
+    const int b0 = t * per, b1 = min(b0 + per, p.batch);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int len = p.lens[b], n = tiles_checked(len, p.cap);
+        if (len != 0 && n == 0) record_device_error(p.err, kErrAttnLength, b, len);
+        sum += n ? n + kEnter : 0;
+    }
+    sums[t] = sum;
+    __syncthreads();
+    for (int o = 1; o < 128; o <<= 1) {
+        const int v = t >= o ? sums[t - o] : 0;
+        __syncthreads();
+        sums[t] += v;
+        __syncthreads();
+    }
+    if (t == 127) total = sums[127];
+    __syncthreads();
+    const int W = max(1, (total + p.windows - 1) / p.windows);
+    int at = sums[t] - sum;
+    for (int b = b0; b < b1; ++b) {
+        const int n = tiles_checked(p.lens[b], p.cap), e = at + (n ? n + kEnter : 0);
+        p.plan[kPlanStart + b] = at;
+        for (int w = (at + W - 1) / W; w < p.windows && w * W < e; ++w) p.plan[kPlanWin + w] = b;
+        at = e;
+    }
+    if (t == 0) {
+        p.plan[0] = total;
+        p.plan[1] = W;
+    }
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One head, 64 of the rank columns, up to 64 rows of the batch. 4 warps, 16 columns each. The weights (16 KB) are on their
+// way before the previous kernel's end.
+template <int D, int R>
+__global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__ AbsorbParams p) {
+    constexpr int WP = 72, QP = D + 8;    // row pitches in shared memory: 16-byte parts of 8 rows in different banks
+    __shared__ __align__(16) __half ws[D * WP];
+    __shared__ __align__(16) __half qs[64 * QP];
+    const int slices = R / 64, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int h = blockIdx.x / slices, r0 = (blockIdx.x % slices) * 64, b0 = blockIdx.y * 64;
+    if (h == p.H) {
+        pdl_wait();
+        pdl_trigger();
+        if (blockIdx.x == p.H * slices && blockIdx.y == 0) make_plan(p);
+        return;
+    }
+    const __half* w = p.w + (size_t)h * 2 * D * R + r0;
+    for (int i = t; i < D * 8; i += 128) cp16(su32(ws + (i >> 3) * WP + (i & 7) * 8), w + (size_t)(i >> 3) * R + (i & 7) * 8);
+    pdl_wait();
+    pdl_trigger();
+    const int rows = min(64, p.batch - b0);
+    constexpr int QC = D / 8;
+    for (int i = t; i < 64 * QC; i += 128) {
+        const int b = i / QC, c = i % QC;
+        if (b < rows) cp16(su32(qs + b * QP + c * 8), p.q + ((size_t)(b0 + b) * p.H + h) * (D + kRope) + c * 8);
+        else *reinterpret_cast<uint4*>(qs + b * QP + c * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (r0 == 0)   // the rotated part as it is
+        for (int i = t; i < rows * 8; i += 128) {
+            const size_t row = (size_t)(b0 + (i >> 3)) * p.H + h;
+            *reinterpret_cast<uint4*>(p.qc + row * (R + kRope) + R + (i & 7) * 8) =
+                __ldg(reinterpret_cast<const uint4*>(p.q + row * (D + kRope) + D + (i & 7) * 8));
+        }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    uint32_t b[D / 16][4];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)   // (k 0-7, n 0-7), (k 8-15, n 0-7), (k 0-7, n 8-15), (k 8-15, n 8-15)
+        ldsm4t(b[k], su32(ws + (16 * k + (lane & 15)) * WP + 16 * warp + 8 * (lane >> 4)));
+    for (int m = 0; m < rows; m += 16) {
+        float c[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4];
+            ldsm4(a, su32(qs + (m + (lane & 15)) * QP + 16 * k + 8 * (lane >> 4)));
+            mma16(c[0], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
+            mma16(c[1], a[0], a[1], a[2], a[3], b[k][2], b[k][3]);
+        }
+        bool large = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // n tile i / 2, row group i % 2
+            const int r = m + (lane >> 2) + 8 * (i & 1);
+            const float x = c[i >> 1][2 * (i & 1)], y = c[i >> 1][2 * (i & 1) + 1];
+            if (r < rows) {
+                *reinterpret_cast<__half2*>(p.qc + ((size_t)(b0 + r) * p.H + h) * (R + kRope) + r0 + 16 * warp + 8 * (i >> 1) + 2 * (lane & 3)) =
+                    __floats2half2_rn(x, y);
+                large |= !(fabsf(x) < 65520.f && fabsf(y) < 65520.f);
+            }
+        }
+        if (large) record_device_error(p.err, kErrLatentValue, b0 + m, h);
+    }
+}
+
+// ---------------------------------------------------------------- the attention
+template <int R, int NH>
+struct Cfg {
+    static constexpr int CH = (R + kRope) / 64;         // runs of 64 values (128 bytes) of a row
+    static constexpr int GROUP = CH * 1024;             // 8 rows: [run][row][128 bytes], swizzled
+    static constexpr int TILE = 8 * GROUP;
+    static constexpr int QB = CH * NH * 128;            // [run][head][128 bytes]
+    static constexpr int PB = kTile * NH * 2;           // [key][head]
+    static constexpr int STAGES = R == 512 ? 2 : 4;
+    static constexpr int PBUF = R == 512 && NH == 64 ? 1 : 2;
+    static constexpr int MT = R / 128;                  // blocks of 128 latent values
+    static constexpr uint32_t SCOL = MT * NH;           // tensor memory: O^T of each block, then two S^T
+    static constexpr uint32_t COLS = SCOL + 2 * NH <= 128 ? 128 : SCOL + 2 * NH <= 256 ? 256 : 512;
+    static constexpr size_t SMEM = (size_t)STAGES * TILE + QB + PBUF * PB;
+    static constexpr int kKFull = 0, kKEmpty = STAGES, kSFull = 2 * STAGES, kPReady = kSFull + 2, kQFull = kPReady + 2, kQEmpty = kQFull + 1,
+                         kDone = kQEmpty + 1, kBars = kDone + 1;
+    static constexpr uint32_t PSW = NH == 64 ? 2 : 4;   // P's rows of 2 NH bytes: 128- or 64-byte swizzle
+    static_assert(SCOL + 2 * NH <= 512, "tensor memory");
+    static_assert(SMEM + 2048 <= 232448, "shared memory");
+};
+
+struct DecodeParams {
+    CUtensorMap tk;        // the pool: [group of 8 rows][run][row][64 values]
+    CUtensorMap tq;        // absorbed queries: [sequence][run][head][64 values]
+    const int* plan;
+    const int32_t* tables;
+    const int32_t* lens;
+    float* parts;          // [head group][window + sequence][NH][R]
+    float2* stats;         // [head group][window + sequence][NH]: reference (log2) and sum of the weights
+    long long maxb, cap, num_blocks;
+    int batch, H, windows, groups;
+    float scale_log2;
+    DevError* err;
+    unsigned long long ns;
+};
+
+// The values of a warp's 32 lanes reduced column by column: lane j ends with column j's.
+template <bool MAX>
+__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            const float got = __shfl_xor_sync(0xffffffffu, give, o);
+            v[i] = MAX ? fmaxf(keep, got) : keep + got;
+        }
+    }
+    return v[0];
+}
+
+template <int R, int NH>
+__global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
+    using C = Cfg<R, NH>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(8) unsigned long long bars[C::kBars];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    __shared__ int live_blocks[C::STAGES];
+    __shared__ __align__(16) float ref[NH];          // the weights' reference of each head, log2
+    __shared__ float factor[NH], column[4][NH];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const uint32_t bar = su32(bars), ks = su32(smem), qs = ks + C::STAGES * C::TILE, ps = qs + C::QB;
+    if (t == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            bar_init(bar + (C::kKFull + s) * 8, 1);
+            bar_init(bar + (C::kKEmpty + s) * 8, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            bar_init(bar + (C::kSFull + s) * 8, 1);
+            bar_init(bar + (C::kPReady + s) * 8, 4);
+        }
+        bar_init(bar + C::kQFull * 8, 1);
+        bar_init(bar + C::kQEmpty * 8, 1);
+        bar_init(bar + C::kDone * 8, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tk);
+        prefetch_map(&p.tq);
+    }
+    if (warp == 5) tmem_alloc<C::COLS>(&tmem_at);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tb = tmem_at;
+    const Waits wt = {p.err, &abort_flag, p.ns};
+    pdl_wait();
+    pdl_trigger();
+    const int hg = blockIdx.x % p.groups, win = blockIdx.x / p.groups;
+    const int total = p.plan[0], W = p.plan[1];
+    const int lo = win * W, hi = min(lo + W, total);
+    const int first = lo < hi ? p.plan[kPlanWin + win] : 0;
+
+    // The window's sequences and their tiles [t0, t1); `each` returns false to stop.
+    auto sequences = [&](auto each) {
+        int start = lo < hi ? p.plan[kPlanStart + first] : hi;
+        for (int b = first; b < p.batch && start < hi; ++b) {
+            const int len = p.lens[b], n = tiles_checked(len, p.cap);
+            if (n == 0) continue;
+            const int t0 = max(lo - start - kEnter, 0), t1 = min(hi - start - kEnter, n);
+            start += n + kEnter;
+            if (t0 < t1 && !each(b, len, t0, t1)) return;
+        }
+    };
+
+    int it = 0, sg = 0;   // tiles and sequences so far
+    if (warp == 4) {
+        // ------------------------------------------------ copies: lanes 0-3 bring the tile's four blocks
+        bool ok = true;
+        sequences([&](int b, int len, int t0, int t1) {
+            if (sg > 0) ok = ok && warp_wait(bar + C::kQEmpty * 8, (uint32_t)(sg - 1) & 1u, wt, 100);
+            if (!ok) return false;
+            if (lane == 0) {
+                bar_expect(bar + C::kQFull * 8, C::QB);
+                copy_box4(qs, &p.tq, 0, hg * NH, 0, b, bar + C::kQFull * 8);
+            }
+            ++sg;
+            const int nblk = (len + kBlock - 1) / kBlock;
+            const int32_t* table = p.tables + (size_t)b * p.maxb;
+            auto load_id = [&](int tt) { return lane < 4 && 4 * tt + lane < nblk ? __ldg(table + 4 * tt + lane) : -1; };
+            int id = load_id(t0);
+            for (int tt = t0; tt < t1; ++tt, ++it) {
+                const int s = it % C::STAGES;
+                const bool in = lane < 4 && 4 * tt + lane < nblk, live = in && id >= 0 && id < p.num_blocks;
+                if (in && !live && hg == 0) record_device_error(p.err, kErrAttnBlock, (long long)b * p.maxb + 4 * tt + lane, id);
+                const unsigned mask = __ballot_sync(0xffffffffu, live) & 15u;
+                const int now = live ? 2 * id : 2 * (int)p.num_blocks;   // outside: zeros
+                if (tt + 1 < t1) id = load_id(tt + 1);
+                if (it >= C::STAGES && !warp_wait(bar + (C::kKEmpty + s) * 8, (uint32_t)(it / C::STAGES - 1) & 1u, wt, 200)) {
+                    ok = false;
+                    return false;
+                }
+                if (lane == 0) {
+                    live_blocks[s] = (int)mask;
+                    fence_async();   // rows cleared through the generic proxy before the copies into them
+                    bar_expect(bar + (C::kKFull + s) * 8, C::TILE);
+                }
+                __syncwarp();
+                if (lane < 4) copy_box4(ks + s * C::TILE + lane * 2 * C::GROUP, &p.tk, 0, 0, 0, now, bar + (C::kKFull + s) * 8);
+            }
+            return true;
+        });
+        // (only after an abort) the copies in flight land before the CTA leaves
+        if (!ok && lane == 0) {
+            const Waits alone = {p.err, nullptr, p.ns};
+            for (int i = max(0, it - C::STAGES); i < it; ++i) bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 300);
+            if (sg > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(sg - 1) & 1u, alone, 301);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------ products, issued by one lane
+        if (lane == 0) {
+            constexpr uint32_t IS = instr(64, NH, false, false), IO = instr(128, NH, true, true);
+            auto values = [&](int i, bool fresh) {   // O^T += V^T P of tile i; frees its stage
+                if (!bar_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 400)) return false;
+                fence_after();
+                const uint32_t vb = ks + (i % C::STAGES) * C::TILE, pb = ps + (i % C::PBUF) * C::PB;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int m = 0; m < C::MT; ++m)
+                        mma_ss(tb + m * NH, operand(vb + 2 * k * C::GROUP + 2 * m * 1024, 1024, C::GROUP, 2),
+                               operand(pb + k * 16 * NH * 2, 16, 8 * NH * 2, C::PSW), IO, !fresh || k > 0);
+                mma_commit(bar + (C::kKEmpty + i % C::STAGES) * 8);
+                return true;
+            };
+            sequences([&](int, int, int t0, int t1) {
+                if (!bar_wait(bar + C::kQFull * 8, (uint32_t)sg & 1u, wt, 401)) return false;
+                ++sg;
+                for (int tt = t0; tt < t1; ++tt, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!bar_wait(bar + (C::kKFull + s) * 8, (uint32_t)(it / C::STAGES) & 1u, wt, 402)) return false;
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4 * C::CH; ++k)
+                        mma_ss(tb + C::SCOL + (it & 1) * NH, operand(ks + s * C::TILE + (k >> 2) * 1024 + (k & 3) * 32, 16, C::GROUP, 2),
+                               operand(qs + (k >> 2) * NH * 128 + (k & 3) * 32, 16, 1024, 2), IS, k > 0);
+                    mma_commit(bar + (C::kSFull + (it & 1)) * 8);
+                    if (tt + 1 == t1) mma_commit(bar + C::kQEmpty * 8);
+                    if (tt > t0 && !values(it - 1, tt - 1 == t0)) return false;
+                }
+                return values(it - 1, t1 - 1 == t0);
+            });
+            mma_commit(bar + C::kDone * 8);   // every product has ended before the tensor memory is given back
+            const Waits alone = {p.err, nullptr, p.ns};
+            bar_wait(bar + C::kDone * 8, 0u, alone, 500);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax: warp w has keys 16 w .. 16 w + 15 of a tile, a lane a key
+        // The four warps run the same number of tiles whatever their waits return, so that their barriers always meet.
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const int key = 16 * warp + (lane & 15);
+        const bool mine = lane < 16;
+        sequences([&](int b, int len, int t0, int t1) {
+            float l[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) l[h] = 0.f;
+            for (int tt = t0; tt < t1; ++tt, ++it) {
+                const int s = it % C::STAGES;
+                warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(it / C::STAGES) & 1u, wt, 600);   // live_blocks, and the rows to clear
+                const int left = len - tt * kTile;                       // keys of this tile
+                const bool seen = mine && key < left && ((live_blocks[s] >> warp) & 1);
+                if (left < kTile && (left & 15)) {   // what the last block holds behind the sequence must not meet the products
+                    const int end = (left + 15) & ~15;
+                    for (int i = t; i < (end - left) * C::CH * 8; i += 128) {
+                        const int row = left + i / (C::CH * 8), c = i % (C::CH * 8);
+                        *reinterpret_cast<uint4*>(smem + s * C::TILE + (row >> 3) * C::GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                warp_wait(bar + (C::kSFull + (it & 1)) * 8, (uint32_t)(it >> 1) & 1u, wt, 601);
+                fence_after();
+                float x[NH];
+#pragma unroll
+                for (int c = 0; c < NH / 32; ++c) tmem_ld32(tb + lanes + C::SCOL + (it & 1) * NH + 32 * c, x + 32 * c);
+                wait_ld();
+#pragma unroll
+                for (int c = 0; c < NH / 32; ++c) tie32(x + 32 * c);
+                float over = -INFINITY;   // how far a score lies above its head's reference
+#pragma unroll
+                for (int h = 0; h < NH; h += 4) {
+                    const float4 r = *reinterpret_cast<const float4*>(ref + h);
+                    const float rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[h + i] = seen ? x[h + i] * p.scale_log2 : -INFINITY;
+                        over = fmaxf(over, x[h + i] - rr[i]);
+                    }
+                }
+                // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
+                // smaller ones, and O has to be scaled only when a score passes that.
+                unsigned raise;
+                asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
+                             : "=r"(raise) : "r"((unsigned)(tt == t0 || over > 8.f)) : "memory");
+                if (raise) {
+#pragma unroll
+                    for (int c = 0; c < NH / 32; ++c) {
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = x[32 * c + i];
+                        column[warp][32 * c + lane] = reduce_columns<true>(v, lane);
+                    }
+                    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+                    if (t < NH) {
+                        const float most = fmaxf(fmaxf(column[0][t], column[1][t]), fmaxf(column[2][t], column[3][t]));
+                        // a finite reference where no key is left, so that the next tile's weights stay numbers
+                        const float old = tt == t0 ? -1e30f : ref[t], now = fmaxf(old, most);
+                        factor[t] = tt == t0 ? 0.f : ex2(old - now);
+                        ref[t] = now;
+                    }
+                    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+                    if (tt > t0) {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) l[h] *= factor[h];
+                        // O holds the tiles before this one
+                        warp_wait(bar + (C::kKEmpty + (it - 1) % C::STAGES) * 8, (uint32_t)((it - 1) / C::STAGES) & 1u, wt, 602);
+                        fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < C::MT * NH / 32; ++c) {
+                            float v[32];
+                            uint32_t u[32];
+                            tmem_ld32(tb + lanes + 32 * c, v);
+                            wait_ld();
+                            tie32(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * factor[(32 * c + i) % NH]);
+                            tmem_st32(tb + lanes + 32 * c, u);
+                        }
+                        wait_st();
+                    }
+                }
+                // the tile before last (or, with one buffer, the last) has taken its weights
+                if (it >= C::PBUF)
+                    warp_wait(bar + (C::kKEmpty + (it - C::PBUF) % C::STAGES) * 8, (uint32_t)((it - C::PBUF) / C::STAGES) & 1u, wt, 603);
+                unsigned char* row = smem + C::STAGES * C::TILE + C::QB + (it % C::PBUF) * C::PB + key * NH * 2;
+                const int turn = NH == 64 ? key & 7 : (key >> 1) & 3;
+#pragma unroll
+                for (int h = 0; h < NH; h += 8) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 r = *reinterpret_cast<const float4*>(ref + h + i);
+                        const float a = ex2(x[h + i] - r.x), bb = ex2(x[h + i + 1] - r.y), c = ex2(x[h + i + 2] - r.z), d = ex2(x[h + i + 3] - r.w);
+                        l[h + i] += a;
+                        l[h + i + 1] += bb;
+                        l[h + i + 2] += c;
+                        l[h + i + 3] += d;
+                        u[i / 2] = pack_half(a, bb);
+                        u[i / 2 + 1] = pack_half(c, d);
+                    }
+                    if (mine) *reinterpret_cast<uint4*>(row + (((h >> 3) ^ turn) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                fence_async();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar + (C::kPReady + (it & 1)) * 8);
+            }
+            // the part: O^T's lanes are latent values, its columns heads
+            const int heads = min(NH, p.H - hg * NH);
+            const size_t part = ((size_t)hg * (p.windows + p.batch) + win + b) * NH;
+            warp_wait(bar + (C::kKEmpty + (it - 1) % C::STAGES) * 8, (uint32_t)((it - 1) / C::STAGES) & 1u, wt, 604);
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < C::MT * NH / 32; ++c) {
+                float v[32];
+                tmem_ld32(tb + lanes + 32 * c, v);
+                wait_ld();
+                tie32(v);
+                const int h0 = 32 * c % NH;
+                float* o = p.parts + (part + h0) * R + 128 * (32 * c / NH) + 32 * warp + lane;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (h0 + i < heads) o[i * R] = v[i];
+            }
+            fence_before();
+            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");   // `column` is free
+#pragma unroll
+            for (int c = 0; c < NH / 32; ++c) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = mine ? l[32 * c + i] : 0.f;
+                column[warp][32 * c + lane] = reduce_columns<false>(v, lane);
+            }
+            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+            if (t < heads) p.stats[part + t] = make_float2(ref[t], column[0][t] + column[1][t] + column[2][t] + column[3][t]);
+            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");   // before the next sequence's reference
+            return true;
+        });
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        fence_after();
+        tmem_free<C::COLS>(tb);
+    }
+}
+
+// ---------------------------------------------------------------- parts joined, values projected
+struct JoinParams {
+    const __half* w;       // [H][2 D][R]
+    const int* plan;
+    const int32_t* lens;
+    const float* parts;
+    const float2* stats;
+    __half* out;           // [batch][H][D]
+    long long cap;
+    int batch, H, windows, rows;   // rows of the batch per CTA: 16 at most
+};
+
+// One head, `rows` sequences. The head's value weights go to registers before the wait on the attention (they are B
+// fragments of m16n8k16: a lane's 16 bytes are 8 consecutive values of one row; which k they stand for is the
+// products' own business as long as A's are the same).
+template <int D, int R, int NH>
+__global__ void __launch_bounds__(256, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
+    constexpr int OP = R + 32, NT = D / 64, KS = R / 32;
+    __shared__ __align__(16) __half os[16 * OP];
+    __shared__ float scale[16][kMaxWin];
+    __shared__ int first[16], count[16];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, h = blockIdx.x, b0 = blockIdx.y * p.rows;
+    uint4 w[NT][KS];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+            w[n][k] = __ldg(reinterpret_cast<const uint4*>(p.w + ((size_t)h * 2 * D + D + 8 * (warp * NT + n) + (lane >> 2)) * R + 32 * k + 8 * (lane & 3)));
+    pdl_wait();
+    pdl_trigger();
+    const int W = p.plan[1], hg = h / NH;
+    const size_t base = (size_t)hg * (p.windows + p.batch);
+    for (int r = warp; r < 16; r += 8) {
+        const int b = b0 + r;
+        const int n = r < p.rows && b < p.batch ? tiles_checked(p.lens[b], p.cap) : 0;
+        int w0 = 0, c = 0;
+        if (n) {
+            const int at = p.plan[kPlanStart + b] + kEnter;
+            w0 = at / W;
+            c = (at + n - 1) / W - w0 + 1;
+            float m = -INFINITY, l = 0.f;
+            for (int i = lane; i < c; i += 32) m = fmaxf(m, p.stats[(base + w0 + i + b) * NH + h % NH].x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = lane; i < c; i += 32) {
+                const float2 s = p.stats[(base + w0 + i + b) * NH + h % NH];
+                const float f = ex2(s.x - m);
+                scale[r][i] = f;
+                l += s.y * f;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // no key left: 0; NaN stays
+            for (int i = lane; i < c; i += 32) scale[r][i] *= inv;
+        }
+        if (lane == 0) {
+            first[r] = w0 + b;
+            count[r] = c;
+        }
+    }
+    __syncthreads();
+    constexpr int PER = R / 4, STEP = 256 / PER;
+    for (int r = t / PER; r < 16; r += STEP) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r]) * NH + h % NH) * R) + t % PER;
+        const int c = count[r];
+#pragma unroll 4
+        for (int i = 0; i < c; ++i) {
+            const float4 v = __ldcg(src + (size_t)i * (NH * R / 4));
+            const float f = scale[r][i];
+            a.x = fmaf(v.x, f, a.x);
+            a.y = fmaf(v.y, f, a.y);
+            a.z = fmaf(v.z, f, a.z);
+            a.w = fmaf(v.w, f, a.w);
+        }
+        *reinterpret_cast<uint2*>(os + r * OP + 4 * (t % PER)) = make_uint2(pack_half(a.x, a.y), pack_half(a.z, a.w));
+    }
+    __syncthreads();
+    float c[NT][4] = {};
+    const int g = lane >> 2, j = lane & 3;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(os + g * OP + 32 * k + 8 * j);
+        const uint4 hi = *reinterpret_cast<const uint4*>(os + (g + 8) * OP + 32 * k + 8 * j);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            mma16(c[n], lo.x, hi.x, lo.y, hi.y, w[n][k].x, w[n][k].y);
+            mma16(c[n], lo.z, hi.z, lo.w, hi.w, w[n][k].z, w[n][k].w);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = g + 8 * i;
+            if (count[r])
+                *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + 8 * (warp * NT + n) + 2 * j) =
+                    __floats2half2_rn(c[n][2 * i], c[n][2 * i + 1]);
+        }
+}
+
+// ---------------------------------------------------------------- host
+struct DecodeShape {
+    int NH, groups;
+    size_t plan, qc, parts, stats, total;   // offsets in the workspace
+};
+static DecodeShape decode_shape(int64_t batch, int H, int R) {
+    DecodeShape s = {};
+    s.NH = H <= 32 ? 32 : 64;
+    s.groups = (H + s.NH - 1) / s.NH;
+    const size_t win = kMaxWin / s.groups + 1, rows = (size_t)s.groups * (batch + win) * s.NH;
+    auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    s.qc = up((size_t)(kPlanStart + batch) * 4);
+    s.parts = s.qc + up((size_t)batch * H * (R + kRope) * 2);
+    s.stats = s.parts + rows * R * 4;
+    s.total = s.stats + up(rows * 8);
+    return s;
+}
+
+struct DecodeArgs {
+    const void *q, *w, *pool;
+    const int32_t *tables, *lens;
+    int64_t batch, maxb, num_blocks;
+    int H;
+    float scale;
+    void *out, *ws;
+};
+
+template <int D, int R, int NH>
+static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s) {
+    using C = Cfg<R, NH>;
+    DevError* err = device_error_record();
+    if (!err) return set_error(QL_ECUDA, "ql_mla_attn_decode: no device error record");
+    static std::atomic<unsigned long long> done{0};
+    QL_TRY_CUDA(allow_smem_once(mla_decode_kernel<R, NH>, C::SMEM, done));
+    unsigned char* ws = static_cast<unsigned char*>(a.ws);
+    int windows = std::min(num_sms(), kMaxWin) / sh.groups;
+    if (windows < 1) windows = 1;
+    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws + sh.qc), a.lens,
+                       reinterpret_cast<int*>(ws), (int)a.batch, a.H, windows, (long long)a.maxb * kBlock, err};
+    DecodeParams dp = {};
+    const uint64_t row = (R + kRope) * 2;
+    const uint64_t kd[4] = {64, 8, (uint64_t)C::CH, (uint64_t)a.num_blocks * 2}, kst[3] = {row, 128, 8 * row};
+    const uint32_t kb[4] = {64, 8, (uint32_t)C::CH, 2};
+    if (int rc = f16_tensor_map(a.pool, 4, kd, kst, kb, &dp.tk)) return rc;
+    const uint64_t qd[4] = {64, (uint64_t)a.H, (uint64_t)C::CH, (uint64_t)a.batch}, qst[3] = {row, 128, a.H * row};
+    const uint32_t qb[4] = {64, (uint32_t)NH, (uint32_t)C::CH, 1};
+    if (int rc = f16_tensor_map(ws + sh.qc, 4, qd, qst, qb, &dp.tq)) return rc;
+    dp.plan = ap.plan;
+    dp.tables = a.tables;
+    dp.lens = a.lens;
+    dp.parts = reinterpret_cast<float*>(ws + sh.parts);
+    dp.stats = reinterpret_cast<float2*>(ws + sh.stats);
+    dp.maxb = a.maxb;
+    dp.cap = ap.cap;
+    dp.num_blocks = a.num_blocks;
+    dp.batch = (int)a.batch;
+    dp.H = a.H;
+    dp.windows = windows;
+    dp.groups = sh.groups;
+    dp.scale_log2 = a.scale * 1.44269504088896340736f;
+    dp.err = err;
+    dp.ns = 2000000000ull;
+    JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, 16};
+    // rows of a CTA: fewer where 16 would leave SMs without work (each CTA reads the head's weights again, from L2)
+    while (jp.rows > 1 && (int64_t)a.H * ((a.batch + jp.rows - 1) / jp.rows) < num_sms()) jp.rows /= 2;
+    cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64) + 1), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
+    if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(192), C::SMEM, s, true, dp);
+    if (e == cudaSuccess)
+        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)a.H, (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(256), 0, s, true, jp);
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_decode");
+}
+
+}  // namespace mla
+}  // namespace ql
+
+extern "C" size_t ql_mla_decode_workspace_bytes(int64_t batch, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
+    if (!ql::mla::shape_ok(head_dim, rank) || batch < 1 || batch > 65535 || n_heads < 1 || n_heads > 1024 || batch * n_heads >= (1 << 22) ||
+        max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 20) || batch * (max_blocks_per_seq / 4 + 2) >= (1ll << 30))
+        return 0;
+    return ql::mla::decode_shape(batch, n_heads, rank).total;
+}
+
+extern "C" int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_tables,
+                                  const int32_t* d_context_lens, int64_t batch, int n_heads, int head_dim, int rank, int rope_dim,
+                                  int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
+                                  void* d_workspace, size_t workspace_bytes, void* stream) {
+    using namespace ql;
+    using namespace ql::mla;
+    if (int rc = attn_check("ql_mla_attn_decode", d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, head_dim, rank, rope_dim, block_size,
+                            num_blocks, d_out, d_workspace, workspace_bytes,
+                            ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq)))
+        return rc;
+    const DecodeShape sh = decode_shape(batch, n_heads, rank);
+    const DecodeArgs a = {d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, batch, max_blocks_per_seq, num_blocks, n_heads, scale, d_out, d_workspace};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool small = sh.NH == 32;
+    if (head_dim == 128) {
+        if (rank == 512) return small ? decode_go<128, 512, 32>(a, sh, s) : decode_go<128, 512, 64>(a, sh, s);
+        return small ? decode_go<128, 256, 32>(a, sh, s) : decode_go<128, 256, 64>(a, sh, s);
+    }
+    if (rank == 512) return small ? decode_go<64, 512, 32>(a, sh, s) : decode_go<64, 512, 64>(a, sh, s);
+    return small ? decode_go<64, 256, 32>(a, sh, s) : decode_go<64, 256, 64>(a, sh, s);
+}

@@ -1,0 +1,146 @@
+// Building blocks of the latent attention's tensor-core kernels: bounded barrier waits, bulk tensor copies, tcgen05
+// products, tensor memory loads and stores.
+#pragma once
+
+#include <cuda.h>
+
+#include "ql_mla.h"
+#include "ql_persist.cuh"
+
+namespace ql {
+namespace mla {
+
+__device__ __forceinline__ uint32_t su32(const void* q) { return static_cast<uint32_t>(__cvta_generic_to_shared(q)); }
+
+__device__ __forceinline__ void bar_init(uint32_t mb, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t mb) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mb) : "memory"); }
+__device__ __forceinline__ void bar_expect(uint32_t mb, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+}
+// The MMAs issued so far arrive on the barrier as they complete.
+__device__ __forceinline__ void mma_commit(uint32_t mb) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mb) : "memory");
+}
+
+// What a bounded wait needs: an expiry records an error (index = CTA, value = where), raises the CTA's abort flag, which ends the
+// other roles' waits, and returns false.
+struct Waits {
+    DevError* err;
+    int* abort_flag;
+    unsigned long long ns;
+};
+__device__ __noinline__ bool wait_slow(uint32_t mb, uint32_t parity, const Waits& w, int where) {
+    const unsigned long long t0 = persist::global_ns();
+    for (unsigned int spin = 1;; ++spin) {
+        if (persist::mbar_test(mb, parity)) return true;
+        if ((spin & 63u) == 0) {
+            if (w.abort_flag != nullptr && *reinterpret_cast<volatile int*>(w.abort_flag)) return false;
+            if (persist::global_ns() - t0 > w.ns) break;
+        }
+    }
+    if (w.abort_flag == nullptr || atomicExch(w.abort_flag, 1) == 0) record_device_error(w.err, kErrLatentStage, blockIdx.x, where);
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
+    if (persist::mbar_test(mb, parity) || persist::mbar_test(mb, parity)) return true;
+    return wait_slow(mb, parity, w, where);
+}
+// by every lane, one answer for the warp
+__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
+    return __all_sync(0xffffffffu, bar_wait(mb, parity, w, where));
+}
+
+__device__ __forceinline__ void copy_box2(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t mb) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(mb) : "memory");
+}
+__device__ __forceinline__ void copy_box3(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t mb) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(mb) : "memory");
+}
+__device__ __forceinline__ void copy_box4(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int u, uint32_t mb) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(mb) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// Shared-memory operand descriptor: start address, leading and stride byte offsets, swizzle (2: 128 bytes, 4: 64 bytes).
+// K-major: stride = bytes between groups of 8 rows (leading unused). MN-major: leading = bytes between swizzle-wide runs of the
+// rows' dimension, stride = bytes between groups of 8 along K.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride, uint32_t swizzle) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46) |
+           ((uint64_t)swizzle << 61);
+}
+// Instruction descriptor: D f32, A and B f16; MN-major operands by their flags.
+__host__ __device__ constexpr uint32_t instr(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n .reg .pred pa;\n setp.ne.u32 pa, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pa;\n}" ::"r"(d), "l"(a),
+                 "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// A in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n .reg .pred pa;\n setp.ne.u32 pa, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pa;\n}" ::"r"(d), "r"(a),
+                 "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// generic-proxy writes to shared memory made visible to copies and MMAs
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 consecutive columns of the warp's 32 lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float* f) {
+    uint32_t v[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+                 "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+                   "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+                   "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+                   "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                 : "r"(a) : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+}
+// Between the wait for a load and the first use of what it brought: the uses stay behind the wait.
+__device__ __forceinline__ void tie32(float* f) {
+    asm volatile("" : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]), "+f"(f[8]), "+f"(f[9]),
+                 "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]));
+    asm volatile("" : "+f"(f[16]), "+f"(f[17]), "+f"(f[18]), "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]), "+f"(f[24]),
+                 "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30]), "+f"(f[31]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+                 "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
+                 "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+                 "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]) : "memory");
+}
+template <uint32_t COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t* at) {   // by one whole warp
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(at)), "r"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <uint32_t COLS>
+__device__ __forceinline__ void tmem_free(uint32_t base) {   // by the same warp
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(COLS) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace mla
+}  // namespace ql
