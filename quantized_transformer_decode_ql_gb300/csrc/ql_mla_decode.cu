@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
     __shared__ int live_blocks[C::STAGES];
     __shared__ __align__(16) float ref[NH];          // the weights' reference of each head, log2
     __shared__ float factor[NH], column[4][NH];
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t bar = su32(bars), ks = su32(smem), qs = ks + C::STAGES * C::TILE, ps = qs + C::QB;
     if (t == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -298,44 +298,61 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
         }
         __syncwarp();
     } else if (warp == 5) {
-        // ------------------------------------------------ products, issued by one lane
-        if (lane == 0) {
-            constexpr uint32_t IS = instr(64, NH, false, false), IO = instr(128, NH, true, true);
-            auto values = [&](int i, bool fresh) {   // O^T += V^T P of tile i; frees its stage
-                if (!bar_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 400)) return false;
-                fence_after();
-                const uint32_t vb = ks + (i % C::STAGES) * C::TILE, pb = ps + (i % C::PBUF) * C::PB;
+        // ------------------------------------------------ products
+        constexpr uint32_t IS = instr(64, NH, false, false), IO = instr(128, NH, true, true);
+        const uint32_t one = elect_one(), td = __shfl_sync(0xffffffffu, tb, 0);
+        const uint64_t kd = operand(ks, 16, C::GROUP, 2), qd = operand(qs, 16, 1024, 2), vd = operand(ks, 1024, C::GROUP, 2),
+                       pd = operand(ps, 16, 8 * NH * 2, C::PSW);
+        auto values = [&](int i, bool fresh) {   // O^T += V^T P of tile i; frees its stage
+            fence_after();
+            const uint64_t v = vd + (i % C::STAGES) * (C::TILE >> 4), w = pd + (i % C::PBUF) * (C::PB >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int m = 0; m < C::MT; ++m)
-                        mma_ss(tb + m * NH, operand(vb + 2 * k * C::GROUP + 2 * m * 1024, 1024, C::GROUP, 2),
-                               operand(pb + k * 16 * NH * 2, 16, 8 * NH * 2, C::PSW), IO, !fresh || k > 0);
-                mma_commit(bar + (C::kKEmpty + i % C::STAGES) * 8);
-                return true;
-            };
-            sequences([&](int, int, int t0, int t1) {
-                if (!bar_wait(bar + C::kQFull * 8, (uint32_t)sg & 1u, wt, 401)) return false;
-                ++sg;
-                for (int tt = t0; tt < t1; ++tt, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!bar_wait(bar + (C::kKFull + s) * 8, (uint32_t)(it / C::STAGES) & 1u, wt, 402)) return false;
-                    fence_after();
+                for (int m = 0; m < C::MT; ++m)
+                    mma_ss(one, td + m * NH, v + ((2 * k * C::GROUP + 2 * m * 1024) >> 4), w + ((k * 16 * NH * 2) >> 4), IO, !fresh || k > 0);
+            mma_commit(one, bar + (C::kKEmpty + i % C::STAGES) * 8);
+        };
+        auto scores = [&](int i) {               // S^T = K q'^T of tile i
+            fence_after();
+            const uint64_t k0 = kd + (i % C::STAGES) * (C::TILE >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4 * C::CH; ++k)
-                        mma_ss(tb + C::SCOL + (it & 1) * NH, operand(ks + s * C::TILE + (k >> 2) * 1024 + (k & 3) * 32, 16, C::GROUP, 2),
-                               operand(qs + (k >> 2) * NH * 128 + (k & 3) * 32, 16, 1024, 2), IS, k > 0);
-                    mma_commit(bar + (C::kSFull + (it & 1)) * 8);
-                    if (tt + 1 == t1) mma_commit(bar + C::kQEmpty * 8);
-                    if (tt > t0 && !values(it - 1, tt - 1 == t0)) return false;
+            for (int k = 0; k < 4 * C::CH; ++k)
+                mma_ss(one, td + C::SCOL + (i & 1) * NH, k0 + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                       qd + (((k >> 2) * NH * 128 + (k & 3) * 32) >> 4), IS, k > 0);
+            mma_commit(one, bar + (C::kSFull + (i & 1)) * 8);
+        };
+        auto weights = [&](int i) { return warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 400); };
+        sequences([&](int, int, int t0_, int t1_) {
+            const int t0 = __shfl_sync(0xffffffffu, t0_, 0), t1 = __shfl_sync(0xffffffffu, t1_, 0);
+            if (!warp_wait(bar + C::kQFull * 8, (uint32_t)sg & 1u, wt, 401)) return false;
+            ++sg;
+            for (int tt = t0; tt < t1; ++tt, ++it) {
+                const uint32_t full = bar + (C::kKFull + it % C::STAGES) * 8, fp = (uint32_t)(it / C::STAGES) & 1u;
+                // the values of the tile before and this tile's scores in the order in which they become ready: with two
+                // stages the next copy waits for the former
+                bool due = tt > t0;
+                while (due && !__all_sync(0xffffffffu, bar_ready(full, fp))) {
+                    if (__all_sync(0xffffffffu, bar_ready(bar + (C::kPReady + ((it - 1) & 1)) * 8, (uint32_t)((it - 1) >> 1) & 1u))) {
+                        values(it - 1, tt - 1 == t0);
+                        due = false;
+                    } else if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&abort_flag))) return false;   // (both come to an end: whoever waits for them has a bound)
                 }
-                return values(it - 1, t1 - 1 == t0);
-            });
-            mma_commit(bar + C::kDone * 8);   // every product has ended before the tensor memory is given back
-            const Waits alone = {p.err, nullptr, p.ns};
-            bar_wait(bar + C::kDone * 8, 0u, alone, 500);
-        }
-        __syncwarp();
+                if (!warp_wait(full, fp, wt, 402)) return false;
+                scores(it);
+                if (tt + 1 == t1) mma_commit(one, bar + C::kQEmpty * 8);
+                if (due) {
+                    if (!weights(it - 1)) return false;
+                    values(it - 1, tt - 1 == t0);
+                }
+            }
+            if (!weights(it - 1)) return false;
+            values(it - 1, t1 - 1 == t0);
+            return true;
+        });
+        mma_commit(one, bar + C::kDone * 8);   // every product has ended before the tensor memory is given back
+        const Waits alone = {p.err, nullptr, p.ns};
+        warp_wait(bar + C::kDone * 8, 0u, alone, 500);
     } else {
         // ------------------------------------------------ softmax: warp w has keys 16 w .. 16 w + 15 of a tile, a lane a key
         // The four warps run the same number of tiles whatever their waits return, so that their barriers always meet.
@@ -495,51 +512,61 @@ struct JoinParams {
     const float2* stats;
     __half* out;           // [batch][H][D]
     long long cap;
-    int batch, H, windows, rows;   // rows of the batch per CTA: 16 at most
+    int batch, H, windows, rows;   // rows of the batch per CTA: 1, 2, 4 or 8
 };
 
 // One head, `rows` sequences. The head's value weights go to registers before the wait on the attention (they are B
 // fragments of m16n8k16: a lane's 16 bytes are 8 consecutive values of one row; which k they stand for is the
-// products' own business as long as A's are the same).
+// products' own business as long as A's are the same). R / 4 threads add up a sequence's parts, or a share of them
+// where there are fewer sequences than such groups. o enters the product as two f16 numbers (22 bits): as one its rounding
+// alone would be as large as the output's.
+constexpr int kJoinThreads = 512;
 template <int D, int R, int NH>
-__global__ void __launch_bounds__(256, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
-    constexpr int OP = R + 32, NT = D / 64, KS = R / 32;
-    __shared__ __align__(16) __half os[16 * OP];
-    __shared__ float scale[16][kMaxWin];
-    __shared__ int first[16], count[16];
+__global__ void __launch_bounds__(kJoinThreads, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
+    constexpr int OP = R + 32, KS = R / 32, PER = R / 4, GROUPS = kJoinThreads / PER;
+    __shared__ __align__(16) __half os[2][8 * OP];   // the halves of o
+    __shared__ __align__(16) float4 share[GROUPS][PER];
+    __shared__ float scale[8][kMaxWin];
+    __shared__ int first[8], count[8];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, h = blockIdx.x, b0 = blockIdx.y * p.rows;
-    uint4 w[NT][KS];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
+    uint4 w[KS];
+    if (warp < D / 8)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-            w[n][k] = __ldg(reinterpret_cast<const uint4*>(p.w + ((size_t)h * 2 * D + D + 8 * (warp * NT + n) + (lane >> 2)) * R + 32 * k + 8 * (lane & 3)));
+            w[k] = __ldg(reinterpret_cast<const uint4*>(p.w + ((size_t)h * 2 * D + D + 8 * warp + (lane >> 2)) * R + 32 * k + 8 * (lane & 3)));
     pdl_wait();
     pdl_trigger();
     const int W = p.plan[1], hg = h / NH;
     const size_t base = (size_t)hg * (p.windows + p.batch);
-    for (int r = warp; r < 16; r += 8) {
-        const int b = b0 + r;
+    if (warp < 8) {
+        const int r = warp, b = b0 + r;
         const int n = r < p.rows && b < p.batch ? tiles_checked(p.lens[b], p.cap) : 0;
         int w0 = 0, c = 0;
         if (n) {
             const int at = p.plan[kPlanStart + b] + kEnter;
             w0 = at / W;
             c = (at + n - 1) / W - w0 + 1;
+            constexpr int MORE = kMaxWin / 32;
+            float2 s[MORE];
             float m = -INFINITY, l = 0.f;
-            for (int i = lane; i < c; i += 32) m = fmaxf(m, p.stats[(base + w0 + i + b) * NH + h % NH].x);
+#pragma unroll
+            for (int i = 0; i < MORE; ++i) {
+                s[i] = 32 * i + lane < c ? p.stats[(base + w0 + 32 * i + lane + b) * NH + h % NH] : make_float2(-INFINITY, 0.f);
+                m = fmaxf(m, s[i].x);
+            }
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            for (int i = lane; i < c; i += 32) {
-                const float2 s = p.stats[(base + w0 + i + b) * NH + h % NH];
-                const float f = ex2(s.x - m);
-                scale[r][i] = f;
-                l += s.y * f;
+#pragma unroll
+            for (int i = 0; i < MORE; ++i) {
+                s[i].x = ex2(s[i].x - m);
+                l += s[i].y * s[i].x;
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // no key left: 0; NaN stays
-            for (int i = lane; i < c; i += 32) scale[r][i] *= inv;
+#pragma unroll
+            for (int i = 0; i < MORE; ++i)
+                if (32 * i + lane < c) scale[r][32 * i + lane] = s[i].x * inv;
         }
         if (lane == 0) {
             first[r] = w0 + b;
@@ -547,44 +574,68 @@ __global__ void __launch_bounds__(256, 1) mla_join_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    constexpr int PER = R / 4, STEP = 256 / PER;
-    for (int r = t / PER; r < 16; r += STEP) {
+    const int g = t / PER, at = t % PER;
+    const int split = p.rows >= GROUPS ? 1 : GROUPS / p.rows;   // groups of a sequence (rows and GROUPS are powers of two)
+    auto put = [&](int r, float4 a) {
+        const float x[4] = {a.x, a.y, a.z, a.w};
+        float y[4];
+        uint32_t u[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = x[i] - __half2float(__float2half_rn(x[i]));
+        u[0] = pack_half(x[0], x[1]);
+        u[1] = pack_half(x[2], x[3]);
+        *reinterpret_cast<uint2*>(os[0] + r * OP + 4 * at) = make_uint2(u[0], u[1]);
+        *reinterpret_cast<uint2*>(os[1] + r * OP + 4 * at) = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+    };
+    for (int r = g / split; r < 8; r += GROUPS / split) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r]) * NH + h % NH) * R) + t % PER;
+        const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r]) * NH + h % NH) * R) + at;
         const int c = count[r];
-#pragma unroll 4
-        for (int i = 0; i < c; ++i) {
-            const float4 v = __ldcg(src + (size_t)i * (NH * R / 4));
-            const float f = scale[r][i];
-            a.x = fmaf(v.x, f, a.x);
-            a.y = fmaf(v.y, f, a.y);
-            a.z = fmaf(v.z, f, a.z);
-            a.w = fmaf(v.w, f, a.w);
+        for (int i0 = g % split; i0 < c; i0 += 8 * split) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = i0 + i * split < c ? __ldcg(src + (size_t)(i0 + i * split) * (NH * R / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = i0 + i * split < c ? scale[r][i0 + i * split] : 0.f;
+                a.x = fmaf(v[i].x, f, a.x);
+                a.y = fmaf(v[i].y, f, a.y);
+                a.z = fmaf(v[i].z, f, a.z);
+                a.w = fmaf(v[i].w, f, a.w);
+            }
         }
-        *reinterpret_cast<uint2*>(os + r * OP + 4 * (t % PER)) = make_uint2(pack_half(a.x, a.y), pack_half(a.z, a.w));
+        if (split == 1) put(r, a);
+        else if (r < p.rows) share[g][at] = a;
+        else if (g % split == 0) put(r, a);   // the rows that are not there: zeros
     }
     __syncthreads();
-    float c[NT][4] = {};
-    const int g = lane >> 2, j = lane & 3;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(os + g * OP + 32 * k + 8 * j);
-        const uint4 hi = *reinterpret_cast<const uint4*>(os + (g + 8) * OP + 32 * k + 8 * j);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            mma16(c[n], lo.x, hi.x, lo.y, hi.y, w[n][k].x, w[n][k].y);
-            mma16(c[n], lo.z, hi.z, lo.w, hi.w, w[n][k].z, w[n][k].w);
+    if (split > 1) {
+        for (int r = g; r < p.rows; r += GROUPS) {
+            float4 a = share[r * split][at];
+            for (int i = 1; i < split; ++i) {
+                const float4 v = share[r * split + i][at];
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            put(r, a);
         }
+        __syncthreads();
     }
+    if (warp >= D / 8) return;
+    float c[4] = {};
+    const int r = lane >> 2, j = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int half = 1; half >= 0; --half)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
-            if (count[r])
-                *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + 8 * (warp * NT + n) + 2 * j) =
-                    __floats2half2_rn(c[n][2 * i], c[n][2 * i + 1]);
+        for (int k = 0; k < KS; ++k) {   // rows 8-15 of the products are not used
+            const uint4 x = *reinterpret_cast<const uint4*>(os[half] + r * OP + 32 * k + 8 * j);
+            mma16(c, x.x, 0u, x.y, 0u, w[k].x, w[k].y);
+            mma16(c, x.z, 0u, x.w, 0u, w[k].z, w[k].w);
         }
+    if (count[r]) *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + 8 * warp + 2 * j) = __floats2half2_rn(c[0], c[1]);
 }
 
 // ---------------------------------------------------------------- host
@@ -649,13 +700,14 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, 16};
-    // rows of a CTA: fewer where 16 would leave SMs without work (each CTA reads the head's weights again, from L2)
+    JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, 8};
+    // rows of a CTA: fewer where 8 would leave SMs without work (each CTA reads the head's weights again, from L2)
     while (jp.rows > 1 && (int64_t)a.H * ((a.batch + jp.rows - 1) / jp.rows) < num_sms()) jp.rows /= 2;
     cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64) + 1), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
     if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(192), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
-        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)a.H, (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(256), 0, s, true, jp);
+        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)a.H, (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
+                   true, jp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_decode");
 }
 

@@ -19,11 +19,6 @@ __device__ __forceinline__ void bar_arrive(uint32_t mb) { asm volatile("mbarrier
 __device__ __forceinline__ void bar_expect(uint32_t mb, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
 }
-// The MMAs issued so far arrive on the barrier as they complete.
-__device__ __forceinline__ void mma_commit(uint32_t mb) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mb) : "memory");
-}
-
 // What a bounded wait needs: an expiry records an error (index = CTA, value = where), raises the CTA's abort flag, which ends the
 // other roles' waits, and returns false.
 struct Waits {
@@ -46,6 +41,13 @@ __device__ __noinline__ bool wait_slow(uint32_t mb, uint32_t parity, const Waits
 __device__ __forceinline__ bool bar_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
     if (persist::mbar_test(mb, parity) || persist::mbar_test(mb, parity)) return true;
     return wait_slow(mb, parity, w, where);
+}
+// no waiting
+__device__ __forceinline__ bool bar_ready(uint32_t mb, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred q;\n mbarrier.test_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(done) : "r"(mb), "r"(parity) : "memory");
+    return done != 0;
 }
 // by every lane, one answer for the warp
 __device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
@@ -79,14 +81,26 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uin
 __host__ __device__ constexpr uint32_t instr(int M, int N, bool a_mn, bool b_mn) {
     return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n .reg .pred pa;\n setp.ne.u32 pa, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pa;\n}" ::"r"(d), "l"(a),
-                 "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+// Products and commits are issued by a whole warp that runs converged, `one` true in its elected lane: descriptors that the
+// compiler knows to be the same in all lanes cost an addition each (computed in a branch of one lane, 65 cycles a product).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(one));
+    return one;
+}
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
+                 " @pe tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pa;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
 }
 // A in tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n .reg .pred pa;\n setp.ne.u32 pa, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pa;\n}" ::"r"(d), "r"(a),
-                 "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
+                 " @pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pa;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
+}
+// The MMAs issued so far arrive on the barrier as they complete.
+__device__ __forceinline__ void mma_commit(uint32_t one, uint32_t mb) {
+    asm volatile("{\n .reg .pred pe;\n setp.ne.u32 pe, %1, 0;\n"
+                 " @pe tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(mb), "r"(one) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
