@@ -415,7 +415,8 @@ int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride
  * that of a length outside the range (recorded). A block id outside the pool is recorded and its keys left out
  * of the softmax (an output of 0 where none is left). What a sequence's last block holds behind its length does
  * not matter. An absorbed query that f16 does not hold is recorded (its outputs are then not finite).
- * d_out f16 [batch][n_heads * head_dim]. batch <= 65535, batch * n_heads < 2^22, max_blocks_per_seq <= 2^20.
+ * d_out f16 [batch][n_heads * head_dim]. scale positive and finite. batch <= 65535, batch * n_heads < 2^22,
+ * max_blocks_per_seq <= 2^20, batch * max_blocks_per_seq < 2^32.
  * q, the weights, the pool and the output 16-byte aligned. d_workspace: ql_mla_decode_workspace_bytes(...)
  * bytes, 128-byte aligned, any contents; calls and captured graphs that may run at the same time need
  * workspaces of their own. The split of the work over the SMs is made from the lengths on the

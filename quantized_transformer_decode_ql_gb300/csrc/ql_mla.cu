@@ -115,121 +115,17 @@ __global__ void __launch_bounds__(256) mla_append_kernel(AppendParams p, DevErro
     if (nan || most >= 65520.f) record_device_error(err, kErrLatentValue, i, 0);
 }
 
-// ---------------------------------------------------------------- attention, one warp a token
-// scratch: q' f32 [rows][H][R + 64], o f32 [rows][H][R]
-template <int D, int R>
-__global__ void __launch_bounds__(256) mla_absorb_kernel(const __half* q, const __half* w, float* qc, int H, DevError* err) {
-    __shared__ float qs[D];
-    const long long row = (long long)blockIdx.x;
-    const int h = blockIdx.y;
-    const __half* src = q + (row * H + h) * (D + kRope);
-    for (int d = threadIdx.x; d < D; d += 256) qs[d] = __half2float(src[d]);
-    __syncthreads();
-    float* dst = qc + (row * H + h) * (R + kRope);
-    for (int r = threadIdx.x; r < R; r += 256) {
-        float a = 0.f;
-        for (int d = 0; d < D; ++d) a = fmaf(qs[d], __half2float(w[((long long)h * 2 * D + d) * R + r]), a);
-        dst[r] = a;
-        if (!(fabsf(a) < 65520.f)) record_device_error(err, kErrLatentValue, row, h);
-    }
-    for (int r = threadIdx.x; r < kRope; r += 256) dst[R + r] = __half2float(src[D + r]);
-}
-
-template <int R>
-__global__ void __launch_bounds__(256) mla_simple_kernel(const float* qc, const __half* pool, const int32_t* tables, const int32_t* lens,
-                                                         const int32_t* position, long long maxb, long long num_blocks, float scale,
-                                                         float* o, int H, DevError* err) {
-    constexpr int W = R + kRope, V = W / 32, VR = R / 32;
-    __shared__ float sm[8], sl[8], sa[8][R];
-    const long long row = blockIdx.x;
-    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t* table = tables + (position ? 0 : row * maxb);
-    const long long len = position ? (long long)*position + row + 1 : lens[row];
-    const bool bad = position ? *position < 0 || *position + (long long)gridDim.x > maxb * 16 : len <= 0 || len > maxb * 16;
-    if (bad) {
-        if (len != 0 && threadIdx.x == 0 && h == 0) record_device_error(err, kErrAttnLength, row, len);
-        return;
-    }
-    float x[V], acc[VR], m = -INFINITY, l = 0.f;
-    for (int k = 0; k < V; ++k) x[k] = qc[(row * H + h) * W + k * 32 + lane] * scale;
-    for (int k = 0; k < VR; ++k) acc[k] = 0.f;
-    for (long long t = warp; t < len; t += 8) {
-        const int blk = table[t >> 4];
-        if (blk < 0 || blk >= num_blocks) {
-            if (lane == 0) record_device_error(err, kErrAttnBlock, row * maxb + (t >> 4), blk);
-            continue;
-        }
-        const __half* src = pool + ((long long)blk * 16 + (t & 15)) * W;
-        float c[V], d = 0.f;
-        for (int k = 0; k < V; ++k) {
-            c[k] = __half2float(src[k * 32 + lane]);
-            d = fmaf(c[k], x[k], d);
-        }
-        for (int s = 16; s; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-        const float mn = fmaxf(m, d), f = m == -INFINITY ? 0.f : __expf(m - mn), e = __expf(d - mn);
-        m = mn;
-        l = l * f + e;
-        for (int k = 0; k < VR; ++k) acc[k] = acc[k] * f + e * c[k];
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    for (int k = 0; k < VR; ++k) sa[warp][k * 32 + lane] = acc[k];
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.f, f[8];
-    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sm[w]);
-    for (int w = 0; w < 8; ++w) {
-        f[w] = sm[w] == -INFINITY ? 0.f : __expf(sm[w] - mm);
-        ll += sl[w] * f[w];
-    }
-    for (int r = threadIdx.x; r < R; r += 256) {
-        float a = 0.f;
-        for (int w = 0; w < 8; ++w) a += sa[w][r] * f[w];
-        o[(row * H + h) * R + r] = ll > 0.f ? a / ll : 0.f;
-    }
-}
-
-template <int D, int R>
-__global__ void __launch_bounds__(128) mla_out_kernel(const float* o, const __half* w, const int32_t* lens, const int32_t* position, long long cap, __half* out, int H) {
-    __shared__ float os[R];
-    const long long row = blockIdx.x;
-    const int h = blockIdx.y;
-    if (lens ? lens[row] <= 0 || lens[row] > cap : *position < 0 || *position + (long long)gridDim.x > cap) return;
-    for (int r = threadIdx.x; r < R; r += 128) os[r] = o[(row * H + h) * R + r];
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float a = 0.f;
-        for (int r = 0; r < R; ++r) a = fmaf(os[r], __half2float(w[((long long)h * 2 * D + D + d) * R + r]), a);
-        out[(row * H + h) * D + d] = __float2half_rn(a);
-    }
-}
-
-template <int D, int R>
-int simple(const __half* q, const __half* w, const __half* pool, const int32_t* tables, const int32_t* lens, const int32_t* position,
-           long long rows, int H, long long maxb, long long num_blocks, float scale, __half* out, void* ws, cudaStream_t s) {
-    DevError* err = device_error_record();
-    if (!err) return set_error(QL_ECUDA, "latent attention: no device error record");
-    float* qc = static_cast<float*>(ws);
-    float* o = qc + rows * H * (R + kRope);
-    const dim3 grid((unsigned)rows, (unsigned)H);
-    mla_absorb_kernel<D, R><<<grid, 256, 0, s>>>(q, w, qc, H, err);
-    mla_simple_kernel<R><<<grid, 256, 0, s>>>(qc, pool, tables, lens, position, maxb, num_blocks, scale, o, H, err);
-    mla_out_kernel<D, R><<<grid, 128, 0, s>>>(o, w, lens, position, maxb * 16, out, H);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? QL_OK : cuda_error(e, "latent attention");
-}
-
 }  // namespace
 
 int mla::attn_check(const char* name, const void* q, const void* w, const void* pool, const void* table, const void* lens, int head_dim,
-                    int rank, int rope_dim, int block_size, int64_t num_blocks, const void* out, const void* ws, size_t ws_bytes, size_t need) {
+                    int rank, int rope_dim, int block_size, int64_t num_blocks, float scale, const void* out, const void* ws, size_t ws_bytes, size_t need) {
     const std::string nm(name);
     if (!q || !w || !pool || !table || !lens || !out || !ws) return set_error(QL_EINVAL, nm + ": null pointer");
     if (!mla::shape_ok(head_dim, rank) || rope_dim != kRope || block_size != mla::kBlock)
         return set_error(QL_EINVAL, nm + ": head_dim must be 64 or 128, rank 256 or 512, rope_dim 64, block_size 16");
     if (need == 0 || num_blocks < 1 || num_blocks >= (1ll << 27))
         return set_error(QL_EINVAL, nm + ": sizes out of range");
+    if (!(scale > 0.f && scale < INFINITY)) return set_error(QL_EINVAL, nm + ": the scale must be positive and finite");
     auto aligned = [](const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
     if (!aligned(q, 16) || !aligned(w, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(ws, 128))
         return set_error(QL_EINVAL, nm + ": q, the weights, the pool and the output must be 16-byte, the workspace 128-byte aligned");
@@ -280,35 +176,4 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
         e = rank == 512 ? (f32 ? go(mla_append_kernel<64, 512, float>) : go(mla_append_kernel<64, 512, __half>))
                         : (f32 ? go(mla_append_kernel<64, 256, float>) : go(mla_append_kernel<64, 256, __half>));
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_append");
-}
-
-extern "C" size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
-    if (!ql::mla::shape_ok(head_dim, rank) || n_tokens < 1 || n_tokens > 65535 || n_heads < 1 || n_heads > 1024 || max_blocks_per_seq < 1 ||
-        max_blocks_per_seq > (1 << 16))
-        return 0;
-    return (size_t)n_tokens * n_heads * (2 * rank + ql::mla::kRope) * 4;
-}
-
-namespace ql {
-namespace {
-template <typename... A>
-int simple_of(int D, int R, A... a) {
-    return D == 128 ? (R == 512 ? simple<128, 512>(a...) : simple<128, 256>(a...))
-                    : (R == 512 ? simple<64, 512>(a...) : simple<64, 256>(a...));
-}
-}  // namespace
-}  // namespace ql
-
-extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
-                                 const int32_t* d_position, int64_t n_tokens, int n_heads, int head_dim, int rank, int rope_dim,
-                                 int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
-                                 void* d_workspace, size_t workspace_bytes, void* stream) {
-    using namespace ql;
-    if (int rc = mla::attn_check("ql_mla_attn_chunk", d_q, d_w_kv, d_pool, d_block_table, d_position, head_dim, rank, rope_dim, block_size, num_blocks, d_out, d_workspace, workspace_bytes,
-                            ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq)))
-        return rc;
-    return simple_of(head_dim, rank, static_cast<const __half*>(d_q), static_cast<const __half*>(d_w_kv),
-                     static_cast<const __half*>(d_pool), d_block_table, (const int32_t*)nullptr, d_position, (long long)n_tokens, n_heads,
-                     (long long)max_blocks_per_seq, (long long)num_blocks, scale, static_cast<__half*>(d_out), d_workspace,
-                     static_cast<cudaStream_t>(stream));
 }

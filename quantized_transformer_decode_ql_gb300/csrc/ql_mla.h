@@ -13,7 +13,7 @@ inline bool shape_ok(int head_dim, int rank) { return (head_dim == 64 || head_di
 
 // The checks that the attention entry points share; `need`: the workspace's bytes, 0 where the sizes are out of range.
 int attn_check(const char* name, const void* q, const void* w, const void* pool, const void* table, const void* lens, int head_dim, int rank,
-               int rope_dim, int block_size, int64_t num_blocks, const void* out, const void* ws, size_t ws_bytes, size_t need);
+               int rope_dim, int block_size, int64_t num_blocks, float scale, const void* out, const void* ws, size_t ws_bytes, size_t need);
 
 }  // namespace mla
 }  // namespace ql

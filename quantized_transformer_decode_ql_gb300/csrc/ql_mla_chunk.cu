@@ -1,0 +1,573 @@
+// Latent attention of a prompt chunk over the paged cache, in the expanded form:
+//
+//  1. mla_expand_kernel: every head's keys k = Wk_h c and values v = Wv_h c of the whole context, f16, by a tcgen05 product over
+//     the cache's rows (128 tokens x 256 outputs a CTA), and the rotated key parts laid out beside them;
+//  2. mla_chunk_kernel: causal attention of 128 queries of one head, the online softmax over tiles of 128 keys in two
+//     independent halves of the tiles (even and odd), so that one half's products run beside the other's weights;
+//  3. mla_chunk_join_kernel, where the keys are split over CTAs: the parts joined.
+#include "ql_batched.h"
+#include "ql_mla_tc.cuh"
+
+#include <algorithm>
+
+namespace ql {
+namespace mla {
+
+constexpr int kQ = 128;     // queries of a CTA, keys of a tile
+
+// ---------------------------------------------------------------- keys and values
+struct ExpandParams {
+    CUtensorMap tc;         // the pool: [token][rank + 64]
+    CUtensorMap tw;         // weights: [head, row][rank]
+    const __half* pool;
+    const int32_t* table;
+    const int32_t* position;
+    __half* k;              // [H][cap][D]
+    __half* v;              // [H][cap][D]
+    __half* turned;         // [cap][64]
+    int* live;              // [cap / 128]: a bit per block of 16 tokens: it is in the pool
+    long long maxb, num_blocks, cap;
+    int n, H;
+    DevError* err;
+    unsigned long long ns;
+};
+
+// Tokens of the context with the chunk, 0 where the position does not fit the table.
+__device__ __forceinline__ long long context(const int32_t* position, int n, long long maxb) {
+    const long long p = __ldg(position);
+    return p >= 0 && p + n <= maxb * kBlock ? p + n : 0;
+}
+
+template <int D, int R>
+struct ExpandCfg {
+    static constexpr int HEADS = 128 / D;                  // heads of a CTA: 256 outputs
+    static constexpr int KC = R / 64;                      // runs of 64 latent values
+    static constexpr int STAGES = 2, AB = 128 * 128, BB = 256 * 128;
+    static constexpr size_t SMEM = (size_t)STAGES * (AB + BB);
+    static constexpr int kFull = 0, kEmpty = STAGES, kDone = 2 * STAGES, kBars = kDone + 1;
+};
+
+template <int D, int R>
+__global__ void __launch_bounds__(192, 2) mla_expand_kernel(const __grid_constant__ ExpandParams p) {
+    using C = ExpandCfg<D, R>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(8) unsigned long long bars[C::kBars];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
+    const int h0 = blockIdx.x * C::HEADS;
+    const long long t0 = (long long)blockIdx.y * 128;
+    const uint32_t bar = su32(bars), as = su32(smem), bs = as + C::STAGES * C::AB;
+    pdl_wait();
+    const long long L = context(p.position, p.n, p.maxb);
+    if (L == 0 && t == 0 && blockIdx.x == 0 && blockIdx.y == 0) record_device_error(p.err, kErrAttnLength, 0, __ldg(p.position));
+    if (t0 >= L) return;
+    if (t == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            bar_init(bar + (C::kFull + s) * 8, 1);
+            bar_init(bar + (C::kEmpty + s) * 8, 1);
+        }
+        bar_init(bar + C::kDone * 8, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5) tmem_alloc<256>(&tmem_at);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    pdl_trigger();   // not before this CTA has its tensor memory: the attention, which takes all of it, waits for this grid's end
+    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
+    const Waits wt = {p.err, &abort_flag, p.ns};
+    const Waits alone = {p.err, nullptr, p.ns};
+    if (warp == 4) {
+        // ------------------------------------------------ copies: a block of 16 tokens a lane, the weights by lane 8
+        const long long nblk = (L + kBlock - 1) / kBlock, at = t0 / kBlock + lane;
+        int id = -1;
+        bool live = false;
+        if (lane < 8 && at < nblk) {
+            id = __ldg(p.table + at);
+            live = id >= 0 && id < p.num_blocks;
+            if (!live && blockIdx.x == 0) record_device_error(p.err, kErrAttnBlock, at, id);
+        }
+        const unsigned mask = __ballot_sync(0xffffffffu, live);
+        if (blockIdx.x == 0 && lane == 0) p.live[blockIdx.y] = (int)mask;
+        const int row = live ? id * kBlock : (int)(p.num_blocks * kBlock);   // outside: zeros
+        int c = 0;
+        for (; c < C::KC; ++c) {
+            const int s = c % C::STAGES;
+            if (c >= C::STAGES && !warp_wait(bar + (C::kEmpty + s) * 8, (uint32_t)(c / C::STAGES - 1) & 1u, wt, 700)) break;
+            if (lane == 0) bar_expect(bar + (C::kFull + s) * 8, C::AB + C::BB);
+            __syncwarp();
+            if (lane < 8) copy_box2(as + s * C::AB + lane * 2048, &p.tc, 64 * c, row, bar + (C::kFull + s) * 8);
+            else if (lane == 8) copy_box2(bs + s * C::BB, &p.tw, 64 * c, h0 * 2 * D, bar + (C::kFull + s) * 8);
+        }
+        if (c < C::KC && lane == 0)   // after an abort: the copies in flight land
+            for (int i = max(0, c - C::STAGES); i < c; ++i) bar_wait(bar + (C::kFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 701);
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------ products
+        constexpr uint32_t I = instr(128, 256, false, false);
+        const uint32_t one = elect_one();
+        const uint64_t ad = operand(as, 16, 1024, 2), bd = operand(bs, 16, 1024, 2);
+        for (int c = 0; c < C::KC; ++c) {
+            const int s = c % C::STAGES;
+            if (!warp_wait(bar + (C::kFull + s) * 8, (uint32_t)(c / C::STAGES) & 1u, wt, 702)) break;
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_ss(one, tb, ad + ((s * C::AB + 32 * k) >> 4), bd + ((s * C::BB + 32 * k) >> 4), I, c > 0 || k > 0);
+            mma_commit(one, bar + (C::kEmpty + s) * 8);
+        }
+        mma_commit(one, bar + C::kDone * 8);
+        warp_wait(bar + C::kDone * 8, 0u, alone, 703);
+    } else {
+        // ------------------------------------------------ a token a thread: its 256 outputs rounded and stored
+        const long long tok = t0 + 32 * warp + lane;
+        const bool in = tok < L;   // rows behind the context are zeros: what its last block holds there must not meet the weights
+        if (blockIdx.x == 0) {     // the rotated part as it is
+            const long long at = tok / kBlock;
+            const int id = in ? __ldg(p.table + at) : -1;
+            const bool live = id >= 0 && id < p.num_blocks;
+            const uint4* src = reinterpret_cast<const uint4*>(p.pool + ((long long)(live ? id : 0) * kBlock + tok % kBlock) * (R + kRope) + R);
+            uint4* dst = reinterpret_cast<uint4*>(p.turned + tok * kRope);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        warp_wait(bar + C::kDone * 8, 0u, wt, 704);
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {   // 32 outputs
+            float f[32];
+            tmem_ld32(tb + ((uint32_t)(32 * warp) << 16) + 32 * c, f);
+            wait_ld();
+            tie32(f);
+            const int h = h0 + 32 * c / (2 * D), e = 32 * c % (2 * D);
+            if (h >= p.H) break;
+            __half* dst = (e < D ? p.k : p.v) + ((long long)h * p.cap + tok) * D + e % D;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(dst)[i] = in ? make_uint4(pack_half(f[8 * i], f[8 * i + 1]), pack_half(f[8 * i + 2], f[8 * i + 3]),
+                                                                   pack_half(f[8 * i + 4], f[8 * i + 5]), pack_half(f[8 * i + 6], f[8 * i + 7]))
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        fence_after();
+        tmem_free<256>(tb);
+    }
+}
+
+// ---------------------------------------------------------------- attention
+struct ChunkParams {
+    CUtensorMap tq;         // queries: [head][token][D + 64]
+    CUtensorMap tk;         // keys: [head, token][D]
+    CUtensorMap tv;         // values: [head, token][D]
+    CUtensorMap tt;         // rotated parts: [token][64]
+    const int* live;
+    const int32_t* position;
+    __half* out;            // [n][H][D]
+    float* parts;           // splits > 1: [split][n][H][D]
+    float2* stats;          // [split][n][H]: reference (log2), sum of the weights
+    long long maxb, cap;
+    int n, H, splits;
+    float scale_log2;
+    DevError* err;
+    unsigned long long ns;
+};
+
+template <int D>
+struct ChunkCfg {
+    static constexpr int CH = (D + kRope) / 64, RUN = kQ * 128;      // a run of 64 values of 128 rows
+    static constexpr int QB = CH * RUN, KB = CH * RUN, VB = D / 64 * RUN;
+    static constexpr size_t SMEM = QB + 2 * KB + 2 * VB;
+    static constexpr uint32_t OCOL = 256, COLS = 512;                // tensor memory: two S (P over them), two O
+    static constexpr int kQFull = 0, kKFull = 1, kKEmpty = 3, kVFull = 5, kVEmpty = 7, kSFull = 9, kPReady = 11, kDone = 13, kBars = 14;
+};
+
+template <int D>
+__global__ void __launch_bounds__(320, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using C = ChunkCfg<D>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(8) unsigned long long bars[C::kBars];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag, live[2];
+    __shared__ float2 half[2][kQ];
+    const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
+    const int split = blockIdx.x, h = blockIdx.y, q0 = (gridDim.z - 1 - blockIdx.z) * kQ;   // the longest rows first
+    const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + 2 * C::KB;
+    if (t == 0) {
+        bar_init(bar + C::kQFull * 8, 1);
+        for (int s = 0; s < 2; ++s) {
+            bar_init(bar + (C::kKFull + s) * 8, 1);
+            bar_init(bar + (C::kKEmpty + s) * 8, 1);
+            bar_init(bar + (C::kVFull + s) * 8, 1);
+            bar_init(bar + (C::kVEmpty + s) * 8, 1);
+            bar_init(bar + (C::kSFull + s) * 8, 1);
+            bar_init(bar + (C::kPReady + s) * 8, 4);
+        }
+        bar_init(bar + C::kDone * 8, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tq);
+        prefetch_map(&p.tk);
+        prefetch_map(&p.tv);
+        prefetch_map(&p.tt);
+    }
+    if (warp == 9) tmem_alloc<C::COLS>(&tmem_at);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
+    const Waits wt = {p.err, &abort_flag, p.ns};
+    const Waits alone = {p.err, nullptr, p.ns};
+    pdl_wait();
+    pdl_trigger();
+    const long long L = context(p.position, p.n, p.maxb);
+    const int before = (int)(L - p.n), rows = min(kQ, p.n - q0);
+    const int all = L ? (before + q0 + rows + kQ - 1) / kQ : 0;    // tiles that the last of these queries sees
+    const int per = (all + p.splits - 1) / p.splits, j0 = min(split * per, all);
+    const int tiles = __shfl_sync(0xffffffffu, min(per, all - j0), 0);
+
+    if (warp == 8) {
+        // ------------------------------------------------ copies
+        if (lane == 0 && tiles > 0) {
+            bar_expect(bar + C::kQFull * 8, C::QB);
+            for (int c = 0; c < C::CH; ++c) copy_box3(qs + c * C::RUN, &p.tq, 64 * c, q0, h, bar + C::kQFull * 8);
+            int j = 0, mask = __ldg(p.live + j0);
+            bool ok = true;
+            for (; j < tiles; ++j) {
+                const int s = j & 1, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
+                const uint32_t ph = (uint32_t)((j >> 1) - 1) & 1u;
+                if (j >= 2 && !bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800)) {
+                    ok = false;
+                    break;
+                }
+                bar_expect(bar + (C::kKFull + s) * 8, C::KB);
+                for (int c = 0; c < D / 64; ++c) copy_box2(ks + s * C::KB + c * C::RUN, &p.tk, 64 * c, row, bar + (C::kKFull + s) * 8);
+                copy_box2(ks + s * C::KB + D / 64 * C::RUN, &p.tt, 0, at, bar + (C::kKFull + s) * 8);
+                if (j >= 2 && !bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801)) {
+                    ok = false;
+                    break;
+                }
+                live[s] = mask;
+                if (j + 1 < tiles) mask = __ldg(p.live + j0 + j + 1);
+                bar_expect(bar + (C::kVFull + s) * 8, C::VB);
+                for (int c = 0; c < D / 64; ++c) copy_box2(vs + s * C::VB + c * C::RUN, &p.tv, 64 * c, row, bar + (C::kVFull + s) * 8);
+            }
+            if (!ok) {   // the copies in flight land before the CTA leaves
+                bar_wait(bar + C::kQFull * 8, 0u, alone, 802);
+                for (int i = max(0, j - 2); i < j; ++i) {
+                    bar_wait(bar + (C::kKFull + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, alone, 803);
+                    bar_wait(bar + (C::kVFull + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, alone, 804);
+                }
+                bar_wait(bar + (C::kKFull + (j & 1)) * 8, (uint32_t)(j >> 1) & 1u, alone, 805);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------ products: the scores of a tile before the values of the one before it
+        constexpr uint32_t IS = instr(128, kQ, false, false), IO = instr(128, D, false, true);
+        const uint32_t one = elect_one();
+        const uint64_t qd = operand(qs, 16, 1024, 2), kd = operand(ks, 16, 1024, 2), vd = operand(vs, C::RUN, 1024, 2);
+        bool ok = tiles > 0 && warp_wait(bar + C::kQFull * 8, 0u, wt, 810);
+        for (int j = 0; ok && j <= tiles; ++j) {
+            if (j < tiles) {
+                const int s = j & 1;
+                ok = warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(j >> 1) & 1u, wt, 811);
+                if (!ok) break;
+                fence_after();
+                const uint64_t k0 = kd + s * (C::KB >> 4);
+#pragma unroll
+                for (int k = 0; k < 4 * C::CH; ++k) {
+                    const uint32_t o = ((k >> 2) * C::RUN + (k & 3) * 32) >> 4;
+                    mma_ss(one, tb + s * kQ, qd + o, k0 + o, IS, k > 0);
+                }
+                mma_commit(one, bar + (C::kKEmpty + s) * 8);
+                mma_commit(one, bar + (C::kSFull + s) * 8);
+            }
+            if (j > 0) {
+                const int i = j - 1, s = i & 1;
+                ok = warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i >> 1) & 1u, wt, 812) &&
+                     warp_wait(bar + (C::kPReady + s) * 8, (uint32_t)(i >> 1) & 1u, wt, 813);
+                if (!ok) break;
+                fence_after();
+                const uint64_t v0 = vd + s * (C::VB >> 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(one, tb + C::OCOL + s * D, tb + s * kQ + 8 * k, v0 + ((k * 2048) >> 4), IO, i >= 2 || k > 0);
+                mma_commit(one, bar + (C::kVEmpty + s) * 8);
+            }
+        }
+        mma_commit(one, bar + C::kDone * 8);
+        warp_wait(bar + C::kDone * 8, 0u, alone, 814);
+    } else {
+        // ------------------------------------------------ softmax: four warps have the even tiles, four the odd ones, a thread a query
+        const int g = warp >> 2, q = 32 * (warp & 3) + lane, mine = (tiles + 1 - g) >> 1;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sc = tb + lanes + g * kQ, oc = tb + lanes + C::OCOL + g * D;
+        const int last = before + q0 + q;        // the last key this query sees
+        float m = -1e30f, l = 0.f;               // finite where no key is left: the weights stay numbers
+        for (int i = 0; i < mine; ++i) {
+            const int at = (j0 + 2 * i + g) * kQ;
+            warp_wait(bar + (C::kVFull + g) * 8, (uint32_t)i & 1u, wt, 820);   // `live`
+            const int mask = live[g];
+            warp_wait(bar + (C::kSFull + g) * 8, (uint32_t)i & 1u, wt, 821);
+            fence_after();
+            float x[kQ];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x + 32 * c);
+            wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tie32(x + 32 * c);
+            if (at + kQ - 1 > before + q0 || mask != 0xff) {   // the same for the CTA
+#pragma unroll
+                for (int c = 0; c < kQ; ++c)
+                    if (at + c > last || !((mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
+            }
+            float most = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kQ; ++c) most = fmaxf(most, x[c]);
+            most *= p.scale_log2;
+            // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
+            // smaller ones, and O has to be scaled only when a score passes that.
+            const bool raise = most > m + 8.f;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float now = raise ? most : m, f = ex2(m - now);
+                m = now;
+                l *= f;
+                if (i > 0) {
+                    warp_wait(bar + (C::kVEmpty + g) * 8, (uint32_t)(i - 1) & 1u, wt, 822);   // O holds this half's tiles before
+                    fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        uint32_t u[32];
+                        tmem_ld32(oc + 32 * c, v);
+                        wait_ld();
+                        tie32(v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(v[k] * f);
+                        tmem_st32(oc + 32 * c, u);
+                    }
+                }
+            }
+            float sum[4] = {};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t u[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float a = ex2(fmaf(x[64 * c + 2 * k], p.scale_log2, -m)), b = ex2(fmaf(x[64 * c + 2 * k + 1], p.scale_log2, -m));
+                    sum[(2 * k) & 3] += a;
+                    sum[(2 * k + 1) & 3] += b;
+                    u[k] = pack_half(a, b);
+                }
+                tmem_st32(sc + 32 * c, u);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar + (C::kPReady + g) * 8);
+        }
+        if (mine > 0) {
+            warp_wait(bar + (C::kVEmpty + g) * 8, (uint32_t)(mine - 1) & 1u, wt, 823);
+            fence_after();
+        }
+        half[g][q] = make_float2(m, l);
+        fence_before();
+        asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+        fence_after();
+        // both halves joined: these warps take half of the values each, of all their lanes' queries
+        const float2 a = half[0][q], b = half[1][q];
+        const float top = fmaxf(a.x, b.x), fa = ex2(a.x - top), fb = ex2(b.x - top), total = a.y * fa + b.y * fb;
+        const bool whole = p.splits == 1;
+        const float inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
+        const float ca = fa * inv, cb = fb * inv;
+#pragma unroll 1
+        for (int c = g * (D / 64); c < (g + 1) * (D / 64); ++c) {
+            float x[32], y[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = y[k] = 0.f;
+            if (tiles > 0) tmem_ld32(tb + lanes + C::OCOL + 32 * c, x);
+            if (tiles > 1) tmem_ld32(tb + lanes + C::OCOL + D + 32 * c, y);
+            wait_ld();
+            tie32(x);
+            tie32(y);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = x[k] * ca + y[k] * cb;
+            if (q < rows && L) {
+                const size_t o = ((size_t)(q0 + q) * p.H + h) * D + 32 * c;
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(p.out + o + 8 * k) = make_uint4(pack_half(x[8 * k], x[8 * k + 1]), pack_half(x[8 * k + 2], x[8 * k + 3]),
+                                                                                  pack_half(x[8 * k + 4], x[8 * k + 5]), pack_half(x[8 * k + 6], x[8 * k + 7]));
+                } else {
+                    float* dst = p.parts + (size_t)split * p.n * p.H * D + o;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                }
+            }
+        }
+        if (!whole && g == 0 && q < rows && L) p.stats[((size_t)split * p.n + q0 + q) * p.H + h] = make_float2(top, total);
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free<C::COLS>(tb);
+    }
+}
+
+// A warp a query and head.
+template <int D>
+__global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), all = (long long)p.n * p.H;
+    const int lane = threadIdx.x & 31;
+    if (i >= all || context(p.position, p.n, p.maxb) == 0) return;
+    constexpr int V = D / 32;
+    float top = -INFINITY, total = 0.f, x[V] = {};
+    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.stats[s * all + i].x);
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 st = p.stats[s * all + i];
+        const float f = ex2(st.x - top);
+        total += st.y * f;
+        const float* src = p.parts + (s * all + i) * D + lane * V;
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[k] = fmaf(src[k], f, x[k]);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+        *reinterpret_cast<__half2*>(p.out + i * D + lane * V + k) = __floats2half2_rn(x[k] * inv, x[k + 1] * inv);
+}
+
+// ---------------------------------------------------------------- host
+struct ChunkShape {
+    int splits;
+    long long cap;                                       // rows of the keys and values a head
+    size_t v, turned, live, stats, parts, total;         // offsets in the workspace
+};
+static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
+    ChunkShape s = {};
+    s.cap = (maxb * kBlock + kQ - 1) / kQ * kQ;
+    // keys split over CTAs where queries and heads give too few for the SMs: up to two a SM, at least 4 tiles each
+    const int64_t ctas = (n + kQ - 1) / kQ * H, tiles = s.cap / kQ;
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(ctas >= 152 ? 1 : 304 / ctas, tiles / 4));
+    auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
+    s.v = up((size_t)H * s.cap * D * 2);
+    s.turned = 2 * s.v;
+    s.live = s.turned + up((size_t)s.cap * kRope * 2);
+    s.stats = s.live + up((size_t)tiles * 4);
+    s.parts = s.stats + (s.splits > 1 ? up((size_t)s.splits * n * H * 8) : 0);
+    s.total = s.parts + (s.splits > 1 ? up((size_t)s.splits * n * H * D * 4) : 0);
+    return s;
+}
+
+struct ChunkArgs {
+    const void *q, *w, *pool;
+    const int32_t *table, *position;
+    int64_t n, maxb, num_blocks;
+    int H;
+    float scale;
+    void *out, *ws;
+};
+
+template <int D, int R>
+static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
+    using E = ExpandCfg<D, R>;
+    using C = ChunkCfg<D>;
+    DevError* err = device_error_record();
+    if (!err) return set_error(QL_ECUDA, "ql_mla_attn_chunk: no device error record");
+    static std::atomic<unsigned long long> done{0}, done2{0};
+    QL_TRY_CUDA(allow_smem_once(mla_expand_kernel<D, R>, E::SMEM, done));
+    QL_TRY_CUDA(allow_smem_once(mla_chunk_kernel<D>, C::SMEM, done2));
+    unsigned char* ws = static_cast<unsigned char*>(a.ws);
+    ExpandParams ep = {};
+    ChunkParams cp = {};
+    const uint64_t row = (R + kRope) * 2;
+    {
+        const uint64_t d[2] = {R + kRope, (uint64_t)a.num_blocks * kBlock}, st[1] = {row};
+        const uint32_t b[2] = {64, kBlock};
+        if (int rc = f16_tensor_map(a.pool, 2, d, st, b, &ep.tc)) return rc;
+    }
+    {
+        const uint64_t d[2] = {R, (uint64_t)a.H * 2 * D}, st[1] = {R * 2};
+        const uint32_t b[2] = {64, 256};
+        if (int rc = f16_tensor_map(a.w, 2, d, st, b, &ep.tw)) return rc;
+    }
+    {
+        const uint64_t w = (D + kRope) * 2, d[3] = {D + kRope, (uint64_t)a.n, (uint64_t)a.H}, st[2] = {a.H * w, w};
+        const uint32_t b[3] = {64, kQ, 1};
+        if (int rc = f16_tensor_map(a.q, 3, d, st, b, &cp.tq)) return rc;
+    }
+    {
+        const uint64_t d[2] = {D, (uint64_t)a.H * sh.cap}, st[1] = {D * 2};
+        const uint32_t b[2] = {64, kQ};
+        if (int rc = f16_tensor_map(ws, 2, d, st, b, &cp.tk)) return rc;
+        if (int rc = f16_tensor_map(ws + sh.v, 2, d, st, b, &cp.tv)) return rc;
+    }
+    {
+        const uint64_t d[2] = {kRope, (uint64_t)sh.cap}, st[1] = {kRope * 2};
+        const uint32_t b[2] = {64, kQ};
+        if (int rc = f16_tensor_map(ws + sh.turned, 2, d, st, b, &cp.tt)) return rc;
+    }
+    ep.pool = static_cast<const __half*>(a.pool);
+    ep.table = a.table;
+    ep.position = cp.position = a.position;
+    ep.k = reinterpret_cast<__half*>(ws);
+    ep.v = reinterpret_cast<__half*>(ws + sh.v);
+    ep.turned = reinterpret_cast<__half*>(ws + sh.turned);
+    ep.live = reinterpret_cast<int*>(ws + sh.live);
+    cp.live = ep.live;
+    ep.maxb = cp.maxb = a.maxb;
+    ep.num_blocks = a.num_blocks;
+    ep.cap = cp.cap = sh.cap;
+    ep.n = cp.n = (int)a.n;
+    ep.H = cp.H = a.H;
+    ep.err = cp.err = err;
+    ep.ns = cp.ns = 2000000000ull;
+    cp.out = static_cast<__half*>(a.out);
+    cp.parts = reinterpret_cast<float*>(ws + sh.parts);
+    cp.stats = reinterpret_cast<float2*>(ws + sh.stats);
+    cp.splits = sh.splits;
+    cp.scale_log2 = a.scale * 1.44269504088896340736f;
+    cudaError_t e = launch(mla_expand_kernel<D, R>, dim3((unsigned)((a.H + E::HEADS - 1) / E::HEADS), (unsigned)(sh.cap / 128)), dim3(192), E::SMEM, s,
+                           true, ep);
+    if (e == cudaSuccess)
+        e = launch(mla_chunk_kernel<D>, dim3((unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + kQ - 1) / kQ)), dim3(320), C::SMEM, s, true, cp);
+    if (e == cudaSuccess && sh.splits > 1)
+        e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.n * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");
+}
+
+}  // namespace mla
+}  // namespace ql
+
+extern "C" size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
+    if (!ql::mla::shape_ok(head_dim, rank) || n_tokens < 1 || n_tokens > 65535 || n_heads < 1 || n_heads > 1024 ||
+        n_tokens * n_heads >= (1 << 22) || max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 16))
+        return 0;
+    return ql::mla::chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq).total;
+}
+
+extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
+                                 const int32_t* d_position, int64_t n_tokens, int n_heads, int head_dim, int rank, int rope_dim,
+                                 int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
+                                 void* d_workspace, size_t workspace_bytes, void* stream) {
+    using namespace ql;
+    using namespace ql::mla;
+    if (int rc = attn_check("ql_mla_attn_chunk", d_q, d_w_kv, d_pool, d_block_table, d_position, head_dim, rank, rope_dim, block_size,
+                            num_blocks, scale, d_out, d_workspace, workspace_bytes,
+                            ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq)))
+        return rc;
+    const ChunkShape sh = chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq);
+    const ChunkArgs a = {d_q, d_w_kv, d_pool, d_block_table, d_position, n_tokens, max_blocks_per_seq, num_blocks, n_heads, scale, d_out, d_workspace};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (head_dim == 128) return rank == 512 ? chunk_go<128, 512>(a, sh, s) : chunk_go<128, 256>(a, sh, s);
+    return rank == 512 ? chunk_go<64, 512>(a, sh, s) : chunk_go<64, 256>(a, sh, s);
+}

@@ -625,17 +625,18 @@ __global__ void __launch_bounds__(kJoinThreads, 1) mla_join_kernel(const __grid_
         __syncthreads();
     }
     if (warp >= D / 8) return;
-    float c[4] = {};
+    float c[4][4] = {};   // four chains of products
     const int r = lane >> 2, j = lane & 3;
 #pragma unroll
-    for (int half = 1; half >= 0; --half)
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {   // rows 8-15 of the products are not used
+        for (int half = 0; half < 2; ++half) {   // rows 8-15 of the products are not used
             const uint4 x = *reinterpret_cast<const uint4*>(os[half] + r * OP + 32 * k + 8 * j);
-            mma16(c, x.x, 0u, x.y, 0u, w[k].x, w[k].y);
-            mma16(c, x.z, 0u, x.w, 0u, w[k].z, w[k].w);
+            mma16(c[half], x.x, 0u, x.y, 0u, w[k].x, w[k].y);
+            mma16(c[2 + half], x.z, 0u, x.w, 0u, w[k].z, w[k].w);
         }
-    if (count[r]) *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + 8 * warp + 2 * j) = __floats2half2_rn(c[0], c[1]);
+    const float y0 = (c[0][0] + c[2][0]) + (c[1][0] + c[3][0]), y1 = (c[0][1] + c[2][1]) + (c[1][1] + c[3][1]);
+    if (count[r]) *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + 8 * warp + 2 * j) = __floats2half2_rn(y0, y1);
 }
 
 // ---------------------------------------------------------------- host
@@ -701,8 +702,8 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     dp.err = err;
     dp.ns = 2000000000ull;
     JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, 8};
-    // rows of a CTA: fewer where 8 would leave SMs without work (each CTA reads the head's weights again, from L2)
-    while (jp.rows > 1 && (int64_t)a.H * ((a.batch + jp.rows - 1) / jp.rows) < num_sms()) jp.rows /= 2;
+    // sequences of a CTA: as few as give one CTA an SM at most (a second wave costs what the first does: 15 instead of 10 us)
+    while (jp.rows > 1 && (int64_t)a.H * ((a.batch + jp.rows / 2 - 1) / (jp.rows / 2)) <= num_sms()) jp.rows /= 2;
     cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64) + 1), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
     if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(192), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
@@ -716,7 +717,7 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
 
 extern "C" size_t ql_mla_decode_workspace_bytes(int64_t batch, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
     if (!ql::mla::shape_ok(head_dim, rank) || batch < 1 || batch > 65535 || n_heads < 1 || n_heads > 1024 || batch * n_heads >= (1 << 22) ||
-        max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 20) || batch * (max_blocks_per_seq / 4 + 2) >= (1ll << 30))
+        max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 20) || batch * max_blocks_per_seq >= (1ll << 32))
         return 0;
     return ql::mla::decode_shape(batch, n_heads, rank).total;
 }
@@ -728,7 +729,7 @@ extern "C" int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const voi
     using namespace ql;
     using namespace ql::mla;
     if (int rc = attn_check("ql_mla_attn_decode", d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, head_dim, rank, rope_dim, block_size,
-                            num_blocks, d_out, d_workspace, workspace_bytes,
+                            num_blocks, scale, d_out, d_workspace, workspace_bytes,
                             ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq)))
         return rc;
     const DecodeShape sh = decode_shape(batch, n_heads, rank);

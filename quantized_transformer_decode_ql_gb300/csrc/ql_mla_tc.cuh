@@ -26,7 +26,7 @@ struct Waits {
     int* abort_flag;
     unsigned long long ns;
 };
-__device__ __noinline__ bool wait_slow(uint32_t mb, uint32_t parity, const Waits& w, int where) {
+static __device__ __noinline__ bool wait_slow(uint32_t mb, uint32_t parity, const Waits& w, int where) {
     const unsigned long long t0 = persist::global_ns();
     for (unsigned int spin = 1;; ++spin) {
         if (persist::mbar_test(mb, parity)) return true;
