@@ -344,30 +344,33 @@ def ql_mla_append(q, kv, norm_w, cos_t, sin_t, positions, slots, eps, n_heads, h
     physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out), queries ``q`` ([n, n_heads, head_dim + rope_dim] of the same
     type, or None) rotated into ``q_out`` (f16, contiguous); ``positions`` int32 [n], the tables f32 [max_position, rope_dim / 2]."""
     name = "ql_mla_append"
-    n, row, width = slots.numel(), rank + rope_dim, head_dim + rope_dim
     half, whole, long = _types or _torch_types()
-    here, turns = device_index(), max_position * (rope_dim // 2)
-    for what, t, kind, size in (("norm_w", norm_w, norm_w.dtype, rank), ("cos_t", cos_t, norm_w.dtype, turns),
-                                ("sin_t", sin_t, norm_w.dtype, turns), ("positions", positions, whole, n), ("slots", slots, long, n),
-                                ("q_out", q_out, half, n * n_heads * width)):
-        if t is None and what == "q_out":
-            continue
-        if t.dtype is not kind or t.numel() < size or t.get_device() != here or not t.is_contiguous():
-            check_array(name, what, t, str(kind), size)
-            check_device(name, t)
-    if str(norm_w.dtype) != "torch.float32":
-        raise QLError(QL_EINVAL, f"{name}: norm_w must be float32")
-    if pool is None or pool.dtype is not half or pool.numel() < num_blocks * 16 * row or pool.get_device() != here or not pool.is_contiguous():
-        check_array(name, "pool", pool, "torch.float16", num_blocks * 16 * row)
-        check_device(name, pool)
-        raise QLError(QL_EINVAL, f"{name}: the pool must be a contiguous float16 tensor")
-    check_device(name, kv, q)
-    if (q is None) != (q_out is None):
+    here, row, width = device_index(), rank + rope_dim, head_dim + rope_dim
+    n, turns, kind = slots.numel(), max_position * rope_dim // 2, norm_w.dtype
+    if not (norm_w.get_device() == cos_t.get_device() == sin_t.get_device() == positions.get_device() == slots.get_device()
+            == pool.get_device() == kv.get_device() == here and _DTYPES.get(str(kind)) == QL_DTYPE_F32
+            and cos_t.dtype is kind and sin_t.dtype is kind and positions.dtype is whole and slots.dtype is long and pool.dtype is half
+            and norm_w.numel() >= rank and cos_t.numel() >= turns and sin_t.numel() >= turns and positions.numel() >= n
+            and pool.numel() >= num_blocks * 16 * row and norm_w.is_contiguous() and cos_t.is_contiguous() and sin_t.is_contiguous()
+            and positions.is_contiguous() and slots.is_contiguous() and pool.is_contiguous()):
+        for what, t, dtype, size in (("norm_w", norm_w, "torch.float32", rank), ("cos_t", cos_t, "torch.float32", turns),
+                                     ("sin_t", sin_t, "torch.float32", turns), ("positions", positions, "torch.int32", n),
+                                     ("slots", slots, "torch.int64", n), ("pool", pool, "torch.float16", num_blocks * 16 * row)):
+            check_array(name, what, t, dtype, size)
+        check_device(name, norm_w, cos_t, sin_t, positions, slots, pool, kv)
+    q_at = out_at = None
+    q_stride = 0
+    if q is not None and q_out is not None:
+        if not (q.get_device() == q_out.get_device() == here and q_out.dtype is half and q_out.numel() >= n * n_heads * width
+                and q_out.is_contiguous()):
+            check_array(name, "q_out", q_out, "torch.float16", n * n_heads * width)
+            check_device(name, q, q_out)
+        q_at, out_at, q_stride = q.data_ptr(), q_out.data_ptr(), _row_stride(name, q, n, n_heads, width)
+    elif q is not q_out:
         raise QLError(QL_EINVAL, f"{name}: q and q_out come together")
-    status = lib().ql_mla_append(ptr(q), kv.data_ptr(), _dtype_of(name, kv, q), _row_stride(name, q, n, n_heads, width) if q is not None else 0,
-                                 _row_stride(name, kv, n, 1, row), norm_w.data_ptr(), cos_t.data_ptr(), sin_t.data_ptr(),
-                                 positions.data_ptr(), slots.data_ptr(), eps, n, n_heads, head_dim, rank, rope_dim, ptr(q_out),
-                                 pool.data_ptr(), num_blocks, max_position, stream_ptr(stream))
+    status = lib().ql_mla_append(q_at, kv.data_ptr(), _dtype_of(name, kv, q), q_stride, _row_stride(name, kv, n, 1, row), norm_w.data_ptr(),
+                                 cos_t.data_ptr(), sin_t.data_ptr(), positions.data_ptr(), slots.data_ptr(), eps, n, n_heads, head_dim, rank,
+                                 rope_dim, out_at, pool.data_ptr(), num_blocks, max_position, stream_ptr(stream))
     if status:
         check(status)
 
@@ -377,17 +380,18 @@ def _mla_tensors(name, q, w_kv, pool, table, lens, rows, tables, n_lens, n_heads
     """The tensors of a latent attention checked."""
     half, whole, _ = _types or _torch_types()
     here = device_index()
-    arrays = (("q", q, half, rows * n_heads * (head_dim + rope_dim)), ("w_kv", w_kv, half, n_heads * 2 * head_dim * rank),
-              ("pool", pool, half, num_blocks * 16 * (rank + rope_dim)), ("table", table, whole, tables * max_blocks_per_seq),
-              ("lengths", lens, whole, n_lens), ("out", out, half, rows * n_heads * head_dim))
-    for what, t, kind, size in arrays:
-        if t is None or t.dtype is not kind or t.numel() < size or t.get_device() != here or not t.is_contiguous():
-            if t is None:
-                raise QLError(QL_EINVAL, f"{name}: {what} is missing")
-            check_array(name, what, t, str(kind), size)
-            check_device(name, t)
-    if workspace.get_device() != here or not workspace.is_contiguous():
-        check_device(name, workspace)
+    n_q, n_w, n_pool = rows * n_heads * (head_dim + rope_dim), n_heads * 2 * head_dim * rank, num_blocks * 16 * (rank + rope_dim)
+    n_table, n_out = tables * max_blocks_per_seq, rows * n_heads * head_dim
+    if not (q.get_device() == w_kv.get_device() == pool.get_device() == table.get_device() == lens.get_device() == out.get_device()
+            == workspace.get_device() == here and q.dtype is half and w_kv.dtype is half and pool.dtype is half and out.dtype is half
+            and table.dtype is whole and lens.dtype is whole and q.numel() >= n_q and w_kv.numel() >= n_w and pool.numel() >= n_pool
+            and table.numel() >= n_table and lens.numel() >= n_lens and out.numel() >= n_out and q.is_contiguous() and w_kv.is_contiguous()
+            and pool.is_contiguous() and table.is_contiguous() and lens.is_contiguous() and out.is_contiguous() and workspace.is_contiguous()):
+        for what, t, dtype, size in (("q", q, "torch.float16", n_q), ("w_kv", w_kv, "torch.float16", n_w), ("pool", pool, "torch.float16", n_pool),
+                                     ("the table", table, "torch.int32", n_table), ("the lengths", lens, "torch.int32", n_lens),
+                                     ("out", out, "torch.float16", n_out)):
+            check_array(name, what, t, dtype, size)
+        check_device(name, q, w_kv, pool, table, lens, out, workspace)
         raise QLError(QL_EINVAL, f"{name}: the workspace must be contiguous")
 
 

@@ -4,7 +4,8 @@
 //   row of the cache = f16( x[0:R] / sqrt(mean x[0:R]^2 + eps) * w | rot(x[R:R+64], p) )
 //   query head       = f16( q[0:D] | rot(q[D:D+64], p) )
 //
-// rot turns the pairs (i, i + 32) by the tables' angle of position p. A warp takes one head of a row, or its latent vector.
+// rot turns the pairs (i, i + 32) by the tables' angle of position p. A warp takes four heads of a row, all of their
+// loads in flight together (16 bytes a lane and more), or the row's latent vector.
 #include "ql_mla.h"
 
 namespace ql {
@@ -12,34 +13,50 @@ namespace {
 
 using mla::kRope;
 
-// N consecutive values (a multiple of 4) from a 16-byte (f32) or 8-byte (f16) boundary, in f32
+// N consecutive values in f32, the address a multiple of N * sizeof(T) up to 16 bytes
 template <int N>
 __device__ __forceinline__ void load_row(const float* p, float* x) {
+    if constexpr (N == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+        x[0] = v.x;
+        x[1] = v.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
-        x[i] = v.x;
-        x[i + 1] = v.y;
-        x[i + 2] = v.z;
-        x[i + 3] = v.w;
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+            x[i] = v.x;
+            x[i + 1] = v.y;
+            x[i + 2] = v.z;
+            x[i + 3] = v.w;
+        }
     }
 }
 template <int N>
 __device__ __forceinline__ void load_row(const __half* p, float* x) {
+    uint32_t u[N / 2];
+    if constexpr (N == 2) u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    else if constexpr (N == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        u[0] = v.x;
+        u[1] = v.y;
+    } else {
+        static_assert(N == 8, "");
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        u[0] = v.x;
+        u[1] = v.y;
+        u[2] = v.z;
+        u[3] = v.w;
+    }
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const float2 v = __half22float2(__ldg(reinterpret_cast<const __half2*>(p + i)));
-        x[i] = v.x;
-        x[i + 1] = v.y;
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i / 2]));
+        x[i] = f.x;
+        x[i + 1] = f.y;
     }
 }
-__device__ __forceinline__ float load_one(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load_one(const __half* p) { return __half2float(__ldg(p)); }
-
-template <int N>
-__device__ __forceinline__ void store_row(__half* p, const float* x) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) *reinterpret_cast<__half2*>(p + i) = __floats2half2_rn(x[i], x[i + 1]);
+__device__ __forceinline__ uint32_t two(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 struct AppendParams {
@@ -58,61 +75,98 @@ struct AppendParams {
     long long num_blocks, max_position;
 };
 
+constexpr int kHeads = 4;   // of a warp
+
 template <int D, int R, typename T>
-__global__ void __launch_bounds__(256) mla_append_kernel(AppendParams p, DevError* err) {
+__global__ void __launch_bounds__(512) mla_append_kernel(AppendParams p, DevError* err) {
     const long long i = blockIdx.x;
     const int lane = threadIdx.x & 31;
-    const int item = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);   // 0: the latent vector, 1 + h: head h
+    const int item = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);   // 0: the latent vector, 1 + k: heads 4 k ..
+    const int heads = p.q != nullptr ? p.n_heads : 0, h0 = (item - 1) * kHeads;
     pdl_wait();
     pdl_trigger();
-    if (item > (p.q != nullptr ? p.n_heads : 0)) return;
+    if (item > 0 && h0 >= heads) return;
     const long long slot = __ldg(p.slots + i);
     const int pos = __ldg(p.positions + i);
-    const bool head = item > 0;
-    const T* src = head ? static_cast<const T*>(p.q) + i * p.q_stride + (long long)(item - 1) * (D + kRope)
-                        : static_cast<const T*>(p.kv) + i * p.kv_stride;
     if (slot < 0 || slot >= 16 * p.num_blocks || pos < 0 || pos >= p.max_position) {
-        if (!head && lane == 0 && slot != -1) {
+        if (item == 0 && lane == 0 && slot != -1) {
             const bool bad_slot = slot < 0 || slot >= 16 * p.num_blocks;
             record_device_error(err, bad_slot ? kErrKvSlot : kErrRopePosition, i, bad_slot ? slot : pos);
         }
         return;
     }
-    const float c = __ldg(p.cos_t + (long long)pos * (kRope / 2) + lane), s = __ldg(p.sin_t + (long long)pos * (kRope / 2) + lane);
-    const T* tail = src + (head ? D : R);
-    const float a = load_one(tail + lane), b = load_one(tail + kRope / 2 + lane);
-    const float ra = a * c - b * s, rb = b * c + a * s;
-    if (head) {
-        float x[D / 32];
-        load_row<D / 32>(src + lane * (D / 32), x);
-        __half* o = p.q_out + (i * p.n_heads + item - 1) * (D + kRope);
-        store_row<D / 32>(o + lane * (D / 32), x);
-        o[D + lane] = __float2half_rn(ra);
-        o[D + kRope / 2 + lane] = __float2half_rn(rb);
+    // lanes 0-15 and 16-31 turn the pairs j, j + 1 of two heads
+    const int j = 2 * (lane & 15), sub = lane >> 4;
+    const float2 c = __ldg(reinterpret_cast<const float2*>(p.cos_t + (long long)pos * (kRope / 2) + j));
+    const float2 s = __ldg(reinterpret_cast<const float2*>(p.sin_t + (long long)pos * (kRope / 2) + j));
+    if (item > 0) {
+        constexpr int LANES = D / 8, AT = 32 / LANES;   // lanes of a head's first D values, heads of the warp at a time
+        const T* q = static_cast<const T*>(p.q) + i * p.q_stride + (long long)h0 * (D + kRope);
+        __half* o = p.q_out + (i * p.n_heads + h0) * (D + kRope);
+        float x[kHeads / AT][8], a[kHeads / 2][2], b[kHeads / 2][2];
+#pragma unroll
+        for (int k = 0; k < kHeads / AT; ++k) {
+            const int h = k * AT + lane / LANES;
+            if (h0 + h < heads) load_row<8>(q + h * (D + kRope) + lane % LANES * 8, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads / 2; ++k) {
+            const int h = 2 * k + sub;
+            if (h0 + h < heads) {
+                load_row<2>(q + h * (D + kRope) + D + j, a[k]);
+                load_row<2>(q + h * (D + kRope) + D + kRope / 2 + j, b[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads / AT; ++k) {
+            const int h = k * AT + lane / LANES;
+            if (h0 + h < heads)
+                *reinterpret_cast<uint4*>(o + h * (D + kRope) + lane % LANES * 8) =
+                    make_uint4(two(x[k][0], x[k][1]), two(x[k][2], x[k][3]), two(x[k][4], x[k][5]), two(x[k][6], x[k][7]));
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads / 2; ++k) {
+            const int h = 2 * k + sub;
+            if (h0 + h < heads) {
+                uint32_t* t = reinterpret_cast<uint32_t*>(o + h * (D + kRope) + D + j);
+                t[0] = two(a[k][0] * c.x - b[k][0] * s.x, a[k][1] * c.y - b[k][1] * s.y);
+                t[kRope / 4] = two(b[k][0] * c.x + a[k][0] * s.x, b[k][1] * c.y + a[k][1] * s.y);
+            }
+        }
         return;
     }
     constexpr int V = R / 32;
-    float x[V], w[V], ss = 0.f;
-    load_row<V>(src + lane * V, x);
-    load_row<V>(p.norm + lane * V, w);
+    const T* src = static_cast<const T*>(p.kv) + i * p.kv_stride;
+    float x[V], w[V], a[2], b[2], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; k += 4) load_row<4>(src + 32 * k + 4 * lane, x + k);
+    load_row<2>(src + R + j, a);
+    load_row<2>(src + R + kRope / 2 + j, b);
+#pragma unroll
+    for (int k = 0; k < V; k += 4) load_row<4>(p.norm + 32 * k + 4 * lane, w + k);
 #pragma unroll
     for (int k = 0; k < V; ++k) ss = fmaf(x[k], x[k], ss);
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = rsqrtf(fmaf(ss, 1.0f / (float)R, p.eps));
     __half* o = p.pool + slot * (R + kRope);
-    float most = fmaxf(fabsf(ra), fabsf(rb));
-    bool nan = !(most <= INFINITY) || ra != ra || rb != rb;
+    const float t[4] = {a[0] * c.x - b[0] * s.x, a[1] * c.y - b[1] * s.y, b[0] * c.x + a[0] * s.x, b[1] * c.y + a[1] * s.y};
+    bool held = true;   // by f16
+#pragma unroll
+    for (int k = 0; k < 4; ++k) held &= fabsf(t[k]) < 65520.f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         x[k] *= r * w[k];
-        nan |= x[k] != x[k];
-        most = fmaxf(most, fabsf(x[k]));
+        held &= fabsf(x[k]) < 65520.f;
     }
-    store_row<V>(o + lane * V, x);
-    o[R + lane] = __float2half_rn(ra);
-    o[R + kRope / 2 + lane] = __float2half_rn(rb);
-    if (nan || most >= 65520.f) record_device_error(err, kErrLatentValue, i, 0);
+#pragma unroll
+    for (int k = 0; k < V; k += 4) *reinterpret_cast<uint2*>(o + 32 * k + 4 * lane) = make_uint2(two(x[k], x[k + 1]), two(x[k + 2], x[k + 3]));
+    if (sub == 0) {
+        uint32_t* u = reinterpret_cast<uint32_t*>(o + R + j);
+        u[0] = two(t[0], t[1]);
+        u[kRope / 4] = two(t[2], t[3]);
+    }
+    if (!held) record_device_error(err, kErrLatentValue, i, 0);
 }
 
 }  // namespace
@@ -153,8 +207,8 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
     auto aligned = [](const void* p, int k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; };
     QL_REQUIRE(aligned(d_q, 16) && aligned(d_kv, 16) && aligned(d_norm_w, 16) && aligned(d_q_out, 16) && aligned(d_pool, 16),
                "ql_mla_append: rows, norm weights, the queries' output and the pool must be 16-byte aligned");
-    QL_REQUIRE(aligned(d_cos, 4) && aligned(d_sin, 4) && aligned(d_positions, 4) && aligned(d_slots, 8),
-               "ql_mla_append: tables and positions must be 4-byte, slots 8-byte aligned");
+    QL_REQUIRE(aligned(d_cos, 8) && aligned(d_sin, 8) && aligned(d_positions, 4) && aligned(d_slots, 8),
+               "ql_mla_append: the tables and the slots must be 8-byte, positions 4-byte aligned");
     const int64_t per = dtype == QL_DTYPE_F32 ? 4 : 8, q_row = (int64_t)n_heads * (head_dim + kRope);
     QL_REQUIRE(n == 1 || (kv_stride >= rank + kRope && kv_stride % per == 0 && kv_stride < (1ll << 31) &&
                           (!d_q || (q_stride >= q_row && q_stride % per == 0 && q_stride < (1ll << 31)))),
@@ -164,7 +218,7 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
     AppendParams p = {d_q, d_kv, q_stride, kv_stride, d_norm_w, d_cos, d_sin, d_positions,
                       reinterpret_cast<const long long*>(d_slots), eps, n_heads, static_cast<__half*>(d_q_out),
                       static_cast<__half*>(d_pool), (long long)num_blocks, (long long)max_position};
-    const int items = d_q ? n_heads + 1 : 1, gy = (items + 7) / 8, warps = (items + gy - 1) / gy;
+    const int items = d_q ? (n_heads + kHeads - 1) / kHeads + 1 : 1, gy = (items + 15) / 16, warps = (items + gy - 1) / gy;
     const dim3 grid((unsigned)n, (unsigned)gy), block((unsigned)(32 * warps));
     auto go = [&](auto kernel) { return launch(kernel, grid, block, 0, static_cast<cudaStream_t>(stream), true, p, err); };
     const bool f32 = dtype == QL_DTYPE_F32;
