@@ -512,38 +512,38 @@ struct JoinParams {
     const float2* stats;
     __half* out;           // [batch][H][D]
     long long cap;
-    int batch, H, windows, rows;   // rows of the batch per CTA: 1, 2, 4 or 8
+    int batch, H, windows, rows;   // rows: sequences of a cluster, 1, 2, 4 or 8
 };
 
-// One head, `rows` sequences. The head's value weights go to registers before the wait on the attention (they are B
-// fragments of m16n8k16: a lane's 16 bytes are 8 consecutive values of one row; which k they stand for is the
-// products' own business as long as A's are the same). R / 4 threads add up a sequence's parts, or a share of them
-// where there are fewer sequences than such groups. o enters the product as two f16 numbers (22 bits): as one its rounding
-// alone would be as large as the output's.
-constexpr int kJoinThreads = 512;
+// A cluster of four CTAs takes one head and `rows` sequences. Each CTA joins the parts of a quarter of the latent values, hands
+// them to the other three through distributed shared memory, and multiplies all of them with a quarter of the head's value
+// rows. Those weights go to registers before the wait on the attention (they are B fragments of m16n8k16: a lane's 16 bytes
+// are 8 consecutive values of one row; which k they stand for is the products' own business as long as A's are the same).
+// o enters the product as two f16 numbers (22 bits): as one, its rounding alone would be as large as the output's.
+constexpr int kJoinThreads = 256, kJoinCtas = 4, kJoinRows = 8;
 template <int D, int R, int NH>
-__global__ void __launch_bounds__(kJoinThreads, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
-    constexpr int OP = R + 32, KS = R / 32, PER = R / 4, GROUPS = kJoinThreads / PER;
-    __shared__ __align__(16) __half os[2][8 * OP];   // the halves of o
+__global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
+    constexpr int OP = R + 32, PER = R / kJoinCtas / 4, GROUPS = kJoinThreads / PER;   // threads of a sequence's quarter (4 values each)
+    constexpr int NT = D / kJoinCtas / 8, KW = 8 / NT, KS = R / 32 / KW;               // 8-row tiles of a CTA, warps and steps of one
+    __shared__ __align__(16) __half os[2][kJoinRows * OP];   // o, its upper and lower halves
     __shared__ __align__(16) float4 share[GROUPS][PER];
-    __shared__ float scale[8][kMaxWin];
-    __shared__ int first[8], count[8];
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, h = blockIdx.x, b0 = blockIdx.y * p.rows;
+    __shared__ float scale[kJoinRows][kMaxWin];
+    __shared__ float sums[8][kJoinRows][8];
+    __shared__ int first[kJoinRows], count[kJoinRows];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quarter = blockIdx.x % kJoinCtas, h = blockIdx.x / kJoinCtas;
+    const int b0 = blockIdx.y * p.rows, nt = warp / KW, kw = warp % KW;
     uint4 w[KS];
-    if (warp < D / 8)
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-            w[k] = __ldg(reinterpret_cast<const uint4*>(p.w + ((size_t)h * 2 * D + D + 8 * warp + (lane >> 2)) * R + 32 * k + 8 * (lane & 3)));
+    const int d0 = quarter * (D / kJoinCtas) + 8 * nt;       // this warp's value rows
     pdl_wait();
     pdl_trigger();
-    const int W = p.plan[1], hg = h / NH;
+    const int hg = h / NH;
     const size_t base = (size_t)hg * (p.windows + p.batch);
-    if (warp < 8) {
+    {
         const int r = warp, b = b0 + r;
-        const int n = r < p.rows && b < p.batch ? tiles_checked(p.lens[b], p.cap) : 0;
+        const bool in = r < p.rows && b < p.batch;
+        const int W = p.plan[1], n = in ? tiles_checked(p.lens[b], p.cap) : 0, at = in ? p.plan[kPlanStart + b] + kEnter : 0;
         int w0 = 0, c = 0;
         if (n) {
-            const int at = p.plan[kPlanStart + b] + kEnter;
             w0 = at / W;
             c = (at + n - 1) / W - w0 + 1;
             constexpr int MORE = kMaxWin / 32;
@@ -575,21 +575,30 @@ __global__ void __launch_bounds__(kJoinThreads, 1) mla_join_kernel(const __grid_
     }
     __syncthreads();
     const int g = t / PER, at = t % PER;
-    const int split = p.rows >= GROUPS ? 1 : GROUPS / p.rows;   // groups of a sequence (rows and GROUPS are powers of two)
-    auto put = [&](int r, float4 a) {
+    const int split = GROUPS / p.rows;   // groups of a sequence (powers of two; at least one)
+    auto put = [&](int r, float4 a) {    // 4 values of o to all four CTAs
         const float x[4] = {a.x, a.y, a.z, a.w};
         float y[4];
-        uint32_t u[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = x[i] - __half2float(__float2half_rn(x[i]));
-        u[0] = pack_half(x[0], x[1]);
-        u[1] = pack_half(x[2], x[3]);
-        *reinterpret_cast<uint2*>(os[0] + r * OP + 4 * at) = make_uint2(u[0], u[1]);
-        *reinterpret_cast<uint2*>(os[1] + r * OP + 4 * at) = make_uint2(pack_half(y[0], y[1]), pack_half(y[2], y[3]));
+        const uint32_t v[2][2] = {{pack_half(x[0], x[1]), pack_half(x[2], x[3])}, {pack_half(y[0], y[1]), pack_half(y[2], y[3])}};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t here = su32(os[i] + r * OP + quarter * (R / kJoinCtas) + 4 * at);
+#pragma unroll
+            for (int c = 0; c < kJoinCtas; ++c) {
+                uint32_t there;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(c));
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(there), "r"(v[i][0]), "r"(v[i][1]) : "memory");
+            }
+        }
     };
-    for (int r = g / split; r < 8; r += GROUPS / split) {
+    // every CTA of the cluster has started before another writes into it
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    {
+        const int r = g / split;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r]) * NH + h % NH) * R) + at;
+        const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r]) * NH + h % NH) * R + quarter * (R / kJoinCtas)) + at;
         const int c = count[r];
         for (int i0 = g % split; i0 < c; i0 += 8 * split) {
             float4 v[8];
@@ -606,37 +615,49 @@ __global__ void __launch_bounds__(kJoinThreads, 1) mla_join_kernel(const __grid_
             }
         }
         if (split == 1) put(r, a);
-        else if (r < p.rows) share[g][at] = a;
-        else if (g % split == 0) put(r, a);   // the rows that are not there: zeros
-    }
-    __syncthreads();
-    if (split > 1) {
-        for (int r = g; r < p.rows; r += GROUPS) {
-            float4 a = share[r * split][at];
-            for (int i = 1; i < split; ++i) {
-                const float4 v = share[r * split + i][at];
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
+        else {
+            share[g][at] = a;
+            __syncthreads();
+            if (g < p.rows) {
+                a = share[g * split][at];
+                for (int i = 1; i < split; ++i) {
+                    const float4 v = share[g * split + i][at];
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
+                }
+                put(g, a);
             }
-            put(r, a);
         }
-        __syncthreads();
     }
-    if (warp >= D / 8) return;
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+        w[k] = __ldg(reinterpret_cast<const uint4*>(p.w + ((size_t)h * 2 * D + D + d0 + (lane >> 2)) * R + 32 * (kw * KS + k) + 8 * (lane & 3)));
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     float c[4][4] = {};   // four chains of products
     const int r = lane >> 2, j = lane & 3;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {   // rows 8-15 of the products are not used
-            const uint4 x = *reinterpret_cast<const uint4*>(os[half] + r * OP + 32 * k + 8 * j);
+        for (int half = 0; half < 2; ++half) {   // rows 8-15 of the products are not used; rows that are not there keep to themselves
+            const uint4 x = *reinterpret_cast<const uint4*>(os[half] + r * OP + 32 * (kw * KS + k) + 8 * j);
             mma16(c[half], x.x, 0u, x.y, 0u, w[k].x, w[k].y);
             mma16(c[2 + half], x.z, 0u, x.w, 0u, w[k].z, w[k].w);
         }
-    const float y0 = (c[0][0] + c[2][0]) + (c[1][0] + c[3][0]), y1 = (c[0][1] + c[2][1]) + (c[1][1] + c[3][1]);
-    if (count[r]) *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + 8 * warp + 2 * j) = __floats2half2_rn(y0, y1);
+    sums[warp][r][2 * j] = (c[0][0] + c[2][0]) + (c[1][0] + c[3][0]);
+    sums[warp][r][2 * j + 1] = (c[0][1] + c[2][1]) + (c[1][1] + c[3][1]);
+    __syncthreads();
+    if (kw == 0 && count[r]) {
+        float y0 = sums[warp][r][2 * j], y1 = sums[warp][r][2 * j + 1];
+#pragma unroll
+        for (int i = 1; i < KW; ++i) {
+            y0 += sums[warp + i][r][2 * j];
+            y1 += sums[warp + i][r][2 * j + 1];
+        }
+        *reinterpret_cast<__half2*>(p.out + ((size_t)(b0 + r) * p.H + h) * D + d0 + 2 * j) = __floats2half2_rn(y0, y1);
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -701,13 +722,12 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, 8};
-    // sequences of a CTA: as few as give one CTA an SM at most (a second wave costs what the first does: 15 instead of 10 us)
-    while (jp.rows > 1 && (int64_t)a.H * ((a.batch + jp.rows / 2 - 1) / (jp.rows / 2)) <= num_sms()) jp.rows /= 2;
+    JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, kJoinRows};
+    while (jp.rows > 1 && jp.rows / 2 >= a.batch) jp.rows /= 2;
     cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64) + 1), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
     if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(192), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
-        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)a.H, (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
+        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)(a.H * kJoinCtas), (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
                    true, jp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_decode");
 }
