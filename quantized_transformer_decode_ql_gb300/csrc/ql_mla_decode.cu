@@ -1,10 +1,10 @@
 // Latent attention of one new token per sequence over the paged cache, in three launches:
 //
-//  1. mla_absorb_kernel: q'_h = Wk_h^T q_h (f16), the heads' queries against the latents themselves; one more CTA cuts the
-//     batch's tiles of 64 keys into equal windows, one per SM (the lengths are on the device only);
-//  2. mla_decode_kernel: a window's tiles on the 5th-generation tensor cores, each tile read once for up to 64 heads:
-//     S^T = K q'^T (64 keys x heads), the online softmax, O^T += V^T P (rank x heads), K the tile's rows and V their first
-//     `rank` values, the same bytes in shared memory;
+//  1. mla_absorb_kernel: q'_h = Wk_h^T q_h (f16), the heads' queries against the latents themselves;
+//  2. mla_decode_kernel: the batch's tiles of 64 keys cut into equal windows, one per SM (the lengths are on the device only), a
+//     window's tiles on the 5th-generation tensor cores, each tile read once for up to 64 heads: S^T = K q'^T (64 keys x heads),
+//     the online softmax, O^T += V^T P (rank x heads), K the tile's rows and V their first `rank` values, the same bytes in
+//     shared memory;
 //  3. mla_join_kernel: a sequence's parts joined, o rounded to f16, out_h = Wv_h o_h.
 #include "ql_batched.h"
 #include "ql_mla_tc.cuh"
@@ -15,60 +15,21 @@ namespace mla {
 constexpr int kTile = 64;       // keys of a tile
 constexpr int kEnter = 1;       // tiles that entering a sequence costs a window (its query, its part written): charged in the split
 constexpr int kMaxWin = 160;    // windows at most
-constexpr int kPlanWin = 16;    // plan: [0] places in all, [1] places of a window; the windows' first sequences; the sequences' first places
-constexpr int kPlanStart = kPlanWin + kMaxWin;
+constexpr int kPlanStart = 4;   // plan: [0] places of a window; from here the sequences' first places
 
 __host__ __device__ inline int tiles_of(int len) { return (len + kTile - 1) / kTile; }
-
-// ---------------------------------------------------------------- the plan and the absorbed queries
-struct AbsorbParams {
-    const __half* q;       // [batch][H][D + 64]
-    const __half* w;       // [H][2 D][R]
-    __half* qc;            // [batch][H][R + 64]
-    const int32_t* lens;
-    int* plan;
-    int batch, H, windows;
-    long long cap;         // longest length
-    DevError* err;
-};
 
 // Tiles of a sequence; 0 for an idle slot and for a length outside the table.
 __device__ __forceinline__ int tiles_checked(int len, long long cap) { return len > 0 && len <= cap ? tiles_of(len) : 0; }
 
-__device__ void make_plan(const AbsorbParams& p) {
-    __shared__ int sums[128];
-    __shared__ int total;
-    const int t = threadIdx.x, per = (p.batch + 127) / 128;
-    const int b0 = t * per, b1 = min(b0 + per, p.batch);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int len = p.lens[b], n = tiles_checked(len, p.cap);
-        if (len != 0 && n == 0) record_device_error(p.err, kErrAttnLength, b, len);
-        sum += n ? n + kEnter : 0;
-    }
-    sums[t] = sum;
-    __syncthreads();
-    for (int o = 1; o < 128; o <<= 1) {
-        const int v = t >= o ? sums[t - o] : 0;
-        __syncthreads();
-        sums[t] += v;
-        __syncthreads();
-    }
-    if (t == 127) total = sums[127];
-    __syncthreads();
-    const int W = max(1, (total + p.windows - 1) / p.windows);
-    int at = sums[t] - sum;
-    for (int b = b0; b < b1; ++b) {
-        const int n = tiles_checked(p.lens[b], p.cap), e = at + (n ? n + kEnter : 0);
-        p.plan[kPlanStart + b] = at;
-        for (int w = (at + W - 1) / W; w < p.windows && w * W < e; ++w) p.plan[kPlanWin + w] = b;
-        at = e;
-    }
-    if (t == 0) {
-        p.plan[0] = total;
-        p.plan[1] = W;
-    }
-}
+// ---------------------------------------------------------------- the absorbed queries
+struct AbsorbParams {
+    const __half* q;       // [batch][H][D + 64]
+    const __half* w;       // [H][2 D][R]
+    __half* qc;            // [batch][H][R + 64]
+    int batch, H;
+    DevError* err;
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -93,12 +54,6 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
     __shared__ __align__(16) __half qs[64 * QP];
     const int slices = R / 64, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int h = blockIdx.x / slices, r0 = (blockIdx.x % slices) * 64, b0 = blockIdx.y * 64;
-    if (h == p.H) {
-        pdl_wait();
-        pdl_trigger();
-        if (blockIdx.x == p.H * slices && blockIdx.y == 0) make_plan(p);
-        return;
-    }
     const __half* w = p.w + (size_t)h * 2 * D * R + r0;
     for (int i = t; i < D * 8; i += 128) cp16(su32(ws + (i >> 3) * WP + (i & 7) * 8), w + (size_t)(i >> 3) * R + (i & 7) * 8);
     pdl_wait();
@@ -161,17 +116,20 @@ struct Cfg {
     static constexpr uint32_t SCOL = MT * NH;           // tensor memory: O^T of each block, then two S^T
     static constexpr uint32_t COLS = SCOL + 2 * NH <= 128 ? 128 : SCOL + 2 * NH <= 256 ? 256 : 512;
     static constexpr size_t SMEM = (size_t)STAGES * TILE + QB + PBUF * PB;
-    static constexpr int kKFull = 0, kKEmpty = STAGES, kSFull = 2 * STAGES, kPReady = kSFull + 2, kQFull = kPReady + 2, kQEmpty = kQFull + 1,
+    // a stage is freed block by block (kKEmpty + 4 stage + block): the next copies start while the values are still multiplied
+    static constexpr int kKFull = 0, kKEmpty = STAGES, kSFull = 5 * STAGES, kPReady = kSFull + 2, kQFull = kPReady + 2, kQEmpty = kQFull + 1,
                          kDone = kQEmpty + 1, kBars = kDone + 1;
     static constexpr uint32_t PSW = NH == 64 ? 2 : 4;   // P's rows of 2 NH bytes: 128- or 64-byte swizzle
+    static constexpr int HN = NH / 2;                   // heads of a softmax group
     static_assert(SCOL + 2 * NH <= 512, "tensor memory");
     static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
+constexpr int kSoftWarps = 8, kCopyWarp = 8, kScoreWarp = 9, kValueWarp = 10, kDecodeThreads = 352;
 
 struct DecodeParams {
     CUtensorMap tk;        // the pool: [group of 8 rows][run][row][64 values]
     CUtensorMap tq;        // absorbed queries: [sequence][run][head][64 values]
-    const int* plan;
+    int* plan;
     const int32_t* tables;
     const int32_t* lens;
     float* parts;          // [head group][window + sequence][NH][R]
@@ -183,11 +141,12 @@ struct DecodeParams {
     unsigned long long ns;
 };
 
-// The values of a warp's 32 lanes reduced column by column: lane j ends with column j's.
-template <bool MAX>
-__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
+// N columns of a warp's lower 16 lanes reduced (N = 16: lanes 16-31 end with nothing of use; N = 32: they hold neutral values):
+// lane j < N ends with column j's.
+template <bool MAX, int N>
+__device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
+    for (int o = N / 2; o; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -199,9 +158,70 @@ __device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
     return v[0];
 }
 
+// The window: places [lo, hi) of all; `first` holds place lo, which starts at place `start`.
+struct Window {
+    int lo, hi, first, start;
+};
+
+// Every CTA cuts the batch by itself, from the lengths: it starts before the absorbed queries are there, and so this and its
+// first tiles' copies cost nothing. CTA 0 leaves the sequences' places to the join.
+__device__ Window make_window(const DecodeParams& p, int win) {
+    constexpr int WARPS = kDecodeThreads / 32;
+    __shared__ int sums[2][WARPS];
+    __shared__ int found[2];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const bool writer = blockIdx.x == 0;
+    auto places = [&](int b) {
+        const int n = b < p.batch ? tiles_checked(__ldg(p.lens + b), p.cap) : 0;
+        return n ? n + kEnter : 0;
+    };
+    int sum = 0;
+    for (int b = t; b < p.batch; b += kDecodeThreads) sum += places(b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sums[0][warp] = sum;
+    if (t == 0) found[0] = found[1] = 0;
+    __syncthreads();
+    int total = 0;
+    for (int i = 0; i < WARPS; ++i) total += sums[0][i];
+    const int W = max(1, (total + p.windows - 1) / p.windows);
+    const int lo = win * W, hi = min(lo + W, total);
+    int before = 0;
+    for (int b0 = 0, k = 1; b0 < p.batch && (writer || before <= lo); b0 += kDecodeThreads, k ^= 1) {
+        const int b = b0 + t, n = places(b);
+        int at = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, at, o);
+            at += lane >= o ? v : 0;
+        }
+        if (lane == 31) sums[k][warp] = at;
+        __syncthreads();   // (the sums of two steps ago, and the total, are read)
+        int all = 0;
+        for (int i = 0; i < WARPS; ++i) {
+            if (i == warp) at += before + all - n;
+            all += sums[k][i];
+        }
+        if (lo < hi && n && at <= lo && lo < at + n) {
+            found[0] = b;
+            found[1] = at;
+        }
+        if (writer && b < p.batch) {
+            p.plan[kPlanStart + b] = at;
+            const int len = p.lens[b];
+            if (len != 0 && n == 0) record_device_error(p.err, kErrAttnLength, b, len);
+        }
+        before += all;
+    }
+    if (writer && t == 0) p.plan[0] = W;
+    __syncthreads();
+    return {lo, hi, found[0], found[1]};
+}
+
 template <int R, int NH>
-__global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = Cfg<R, NH>;
+    constexpr int HN = C::HN;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
@@ -214,163 +234,176 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
     if (t == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             bar_init(bar + (C::kKFull + s) * 8, 1);
-            bar_init(bar + (C::kKEmpty + s) * 8, 1);
+            for (int k = 0; k < 4; ++k) bar_init(bar + (C::kKEmpty + 4 * s + k) * 8, 1);
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(bar + (C::kSFull + s) * 8, 1);
-            bar_init(bar + (C::kPReady + s) * 8, 4);
+            bar_init(bar + (C::kPReady + s) * 8, kSoftWarps);
         }
         bar_init(bar + C::kQFull * 8, 1);
         bar_init(bar + C::kQEmpty * 8, 1);
-        bar_init(bar + C::kDone * 8, 1);
+        bar_init(bar + C::kDone * 8, 2);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tk);
         prefetch_map(&p.tq);
     }
-    if (warp == 5) tmem_alloc<C::COLS>(&tmem_at);
+    if (warp == kScoreWarp) tmem_alloc<C::COLS>(&tmem_at);
     fence_before();
-    __syncthreads();
-    fence_after();
-    const uint32_t tb = tmem_at;
-    const Waits wt = {p.err, &abort_flag, p.ns};
-    pdl_wait();
-    pdl_trigger();
     const int hg = blockIdx.x % p.groups, win = blockIdx.x / p.groups;
-    const int total = p.plan[0], W = p.plan[1];
-    const int lo = win * W, hi = min(lo + W, total);
-    const int first = lo < hi ? p.plan[kPlanWin + win] : 0;
+    const Window window = make_window(p, win);   // (and a barrier of the CTA)
+    fence_after();
+    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
+    const Waits wt = {p.err, &abort_flag, p.ns};
+    const Waits alone = {p.err, nullptr, p.ns};
 
     // The window's sequences and their tiles [t0, t1); `each` returns false to stop.
     auto sequences = [&](auto each) {
-        int start = lo < hi ? p.plan[kPlanStart + first] : hi;
-        for (int b = first; b < p.batch && start < hi; ++b) {
-            const int len = p.lens[b], n = tiles_checked(len, p.cap);
+        int start = window.lo < window.hi ? window.start : window.hi;
+        for (int b = window.first; b < p.batch && start < window.hi; ++b) {
+            const int len = __ldg(p.lens + b), n = tiles_checked(len, p.cap);
             if (n == 0) continue;
-            const int t0 = max(lo - start - kEnter, 0), t1 = min(hi - start - kEnter, n);
+            const int t0 = max(window.lo - start - kEnter, 0), t1 = min(window.hi - start - kEnter, n);
             start += n + kEnter;
-            if (t0 < t1 && !each(b, len, t0, t1)) return;
+            if (t0 < t1 && !each(b, len, __shfl_sync(0xffffffffu, t0, 0), __shfl_sync(0xffffffffu, t1, 0))) return;
         }
     };
+    auto empty = [&](int i, int block) { return bar + (C::kKEmpty + 4 * (i % C::STAGES) + block) * 8; };
+    auto turn = [&](int i) { return (uint32_t)(i / C::STAGES) & 1u; };   // parity of tile i's stage
 
     int it = 0, sg = 0;   // tiles and sequences so far
-    if (warp == 4) {
+    if (warp == kCopyWarp) {
         // ------------------------------------------------ copies: lanes 0-3 bring the tile's four blocks
         bool ok = true;
         sequences([&](int b, int len, int t0, int t1) {
-            if (sg > 0) ok = ok && warp_wait(bar + C::kQEmpty * 8, (uint32_t)(sg - 1) & 1u, wt, 100);
-            if (!ok) return false;
-            if (lane == 0) {
-                bar_expect(bar + C::kQFull * 8, C::QB);
-                copy_box4(qs, &p.tq, 0, hg * NH, 0, b, bar + C::kQFull * 8);
+            auto query = [&] {
+                if (lane == 0) {
+                    bar_expect(bar + C::kQFull * 8, C::QB);
+                    copy_box4(qs, &p.tq, 0, hg * NH, 0, b, bar + C::kQFull * 8);
+                }
+                ++sg;
+            };
+            bool first = sg == 0;
+            if (!first) {
+                ok = warp_wait(bar + C::kQEmpty * 8, (uint32_t)(sg - 1) & 1u, wt, 100);
+                if (!ok) return false;
+                query();
             }
-            ++sg;
             const int nblk = (len + kBlock - 1) / kBlock;
             const int32_t* table = p.tables + (size_t)b * p.maxb;
             auto load_id = [&](int tt) { return lane < 4 && 4 * tt + lane < nblk ? __ldg(table + 4 * tt + lane) : -1; };
             int id = load_id(t0);
             for (int tt = t0; tt < t1; ++tt, ++it) {
+                if (first && it == C::STAGES) {   // the absorbed queries are the previous kernel's; what the cache holds is older
+                    pdl_wait();
+                    pdl_trigger();
+                    query();
+                    first = false;
+                }
                 const int s = it % C::STAGES;
                 const bool in = lane < 4 && 4 * tt + lane < nblk, live = in && id >= 0 && id < p.num_blocks;
                 if (in && !live && hg == 0) record_device_error(p.err, kErrAttnBlock, (long long)b * p.maxb + 4 * tt + lane, id);
                 const unsigned mask = __ballot_sync(0xffffffffu, live) & 15u;
                 const int now = live ? 2 * id : 2 * (int)p.num_blocks;   // outside: zeros
                 if (tt + 1 < t1) id = load_id(tt + 1);
-                if (it >= C::STAGES && !warp_wait(bar + (C::kKEmpty + s) * 8, (uint32_t)(it / C::STAGES - 1) & 1u, wt, 200)) {
-                    ok = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // (after an abort this tile's copies still go out, so that its barrier can be waited for)
+                    ok = ok && (it < C::STAGES || warp_wait(empty(it, k), turn(it - C::STAGES), wt, 200 + k));
+                    if (k == 0 && lane == 0) {
+                        live_blocks[s] = (int)mask;
+                        fence_async();   // rows cleared through the generic proxy before the copies into them
+                    }
+                    __syncwarp();
+                    if (lane == k) {
+                        if (k == 0) bar_expect(bar + (C::kKFull + s) * 8, C::TILE);
+                        copy_box4(ks + s * C::TILE + k * 2 * C::GROUP, &p.tk, 0, 0, 0, now, bar + (C::kKFull + s) * 8);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) {
+                    ++it;
                     return false;
                 }
-                if (lane == 0) {
-                    live_blocks[s] = (int)mask;
-                    fence_async();   // rows cleared through the generic proxy before the copies into them
-                    bar_expect(bar + (C::kKFull + s) * 8, C::TILE);
-                }
-                __syncwarp();
-                if (lane < 4) copy_box4(ks + s * C::TILE + lane * 2 * C::GROUP, &p.tk, 0, 0, 0, now, bar + (C::kKFull + s) * 8);
+            }
+            if (first) {
+                pdl_wait();
+                pdl_trigger();
+                query();
             }
             return true;
         });
-        // (only after an abort) the copies in flight land before the CTA leaves
-        if (!ok && lane == 0) {
-            const Waits alone = {p.err, nullptr, p.ns};
-            for (int i = max(0, it - C::STAGES); i < it; ++i) bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 300);
+        if (!ok && lane == 0) {   // (only after an abort)
+            for (int i = max(0, it - C::STAGES); i < it; ++i) bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, turn(i), alone, 300);
             if (sg > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(sg - 1) & 1u, alone, 301);
         }
         __syncwarp();
-    } else if (warp == 5) {
-        // ------------------------------------------------ products
-        constexpr uint32_t IS = instr(64, NH, false, false), IO = instr(128, NH, true, true);
-        const uint32_t one = elect_one(), td = __shfl_sync(0xffffffffu, tb, 0);
-        const uint64_t kd = operand(ks, 16, C::GROUP, 2), qd = operand(qs, 16, 1024, 2), vd = operand(ks, 1024, C::GROUP, 2),
-                       pd = operand(ps, 16, 8 * NH * 2, C::PSW);
-        auto values = [&](int i, bool fresh) {   // O^T += V^T P of tile i; frees its stage
-            fence_after();
-            const uint64_t v = vd + (i % C::STAGES) * (C::TILE >> 4), w = pd + (i % C::PBUF) * (C::PB >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int m = 0; m < C::MT; ++m)
-                    mma_ss(one, td + m * NH, v + ((2 * k * C::GROUP + 2 * m * 1024) >> 4), w + ((k * 16 * NH * 2) >> 4), IO, !fresh || k > 0);
-            mma_commit(one, bar + (C::kKEmpty + i % C::STAGES) * 8);
-        };
-        auto scores = [&](int i) {               // S^T = K q'^T of tile i
-            fence_after();
-            const uint64_t k0 = kd + (i % C::STAGES) * (C::TILE >> 4);
-#pragma unroll
-            for (int k = 0; k < 4 * C::CH; ++k)
-                mma_ss(one, td + C::SCOL + (i & 1) * NH, k0 + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
-                       qd + (((k >> 2) * NH * 128 + (k & 3) * 32) >> 4), IS, k > 0);
-            mma_commit(one, bar + (C::kSFull + (i & 1)) * 8);
-        };
-        auto weights = [&](int i) { return warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 400); };
-        sequences([&](int, int, int t0_, int t1_) {
-            const int t0 = __shfl_sync(0xffffffffu, t0_, 0), t1 = __shfl_sync(0xffffffffu, t1_, 0);
+    } else if (warp == kScoreWarp) {
+        // ------------------------------------------------ S^T = K q'^T, two tiles ahead of their values at most
+        constexpr uint32_t I = instr(64, NH, false, false);
+        const uint32_t one = elect_one();
+        const uint64_t kd = operand(ks, 16, C::GROUP, 2), qd = operand(qs, 16, 1024, 2);
+        sequences([&](int, int, int t0, int t1) {
             if (!warp_wait(bar + C::kQFull * 8, (uint32_t)sg & 1u, wt, 401)) return false;
             ++sg;
             for (int tt = t0; tt < t1; ++tt, ++it) {
-                const uint32_t full = bar + (C::kKFull + it % C::STAGES) * 8, fp = (uint32_t)(it / C::STAGES) & 1u;
-                // the values of the tile before and this tile's scores in the order in which they become ready: with two
-                // stages the next copy waits for the former
-                bool due = tt > t0;
-                while (due && !__all_sync(0xffffffffu, bar_ready(full, fp))) {
-                    if (__all_sync(0xffffffffu, bar_ready(bar + (C::kPReady + ((it - 1) & 1)) * 8, (uint32_t)((it - 1) >> 1) & 1u))) {
-                        values(it - 1, tt - 1 == t0);
-                        due = false;
-                    } else if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&abort_flag))) return false;   // (both come to an end: whoever waits for them has a bound)
-                }
-                if (!warp_wait(full, fp, wt, 402)) return false;
-                scores(it);
+                if (it >= 2 && !warp_wait(bar + (C::kPReady + (it & 1)) * 8, (uint32_t)((it >> 1) - 1) & 1u, wt, 402)) return false;   // its S is read
+                if (!warp_wait(bar + (C::kKFull + it % C::STAGES) * 8, turn(it), wt, 403)) return false;
+                fence_after();
+                const uint64_t k0 = kd + (it % C::STAGES) * (C::TILE >> 4);
+#pragma unroll
+                for (int k = 0; k < 4 * C::CH; ++k)
+                    mma_ss(one, tb + C::SCOL + (it & 1) * NH, k0 + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                           qd + (((k >> 2) * NH * 128 + (k & 3) * 32) >> 4), I, k > 0);
+                mma_commit(one, bar + (C::kSFull + (it & 1)) * 8);
                 if (tt + 1 == t1) mma_commit(one, bar + C::kQEmpty * 8);
-                if (due) {
-                    if (!weights(it - 1)) return false;
-                    values(it - 1, tt - 1 == t0);
-                }
             }
-            if (!weights(it - 1)) return false;
-            values(it - 1, t1 - 1 == t0);
             return true;
         });
         mma_commit(one, bar + C::kDone * 8);   // every product has ended before the tensor memory is given back
-        const Waits alone = {p.err, nullptr, p.ns};
         warp_wait(bar + C::kDone * 8, 0u, alone, 500);
-    } else {
-        // ------------------------------------------------ softmax: warp w has keys 16 w .. 16 w + 15 of a tile, a lane a key
-        // The four warps run the same number of tiles whatever their waits return, so that their barriers always meet.
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const int key = 16 * warp + (lane & 15);
-        const bool mine = lane < 16;
-        sequences([&](int b, int len, int t0, int t1) {
-            float l[NH];
+    } else if (warp == kValueWarp) {
+        // ------------------------------------------------ O^T += V^T P
+        constexpr uint32_t I = instr(128, NH, true, true);
+        const uint32_t one = elect_one();
+        const uint64_t vd = operand(ks, 1024, C::GROUP, 2), pd = operand(ps, 16, 8 * NH * 2, C::PSW);
+        sequences([&](int, int, int t0, int t1) {
+            for (int tt = t0; tt < t1; ++tt, ++it) {
+                if (!warp_wait(bar + (C::kPReady + (it & 1)) * 8, (uint32_t)(it >> 1) & 1u, wt, 404)) return false;
+                fence_after();
+                const uint64_t v = vd + (it % C::STAGES) * (C::TILE >> 4), w = pd + (it % C::PBUF) * (C::PB >> 4);
 #pragma unroll
-            for (int h = 0; h < NH; ++h) l[h] = 0.f;
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int m = 0; m < C::MT; ++m)
+                        mma_ss(one, tb + m * NH, v + ((2 * k * C::GROUP + 2 * m * 1024) >> 4), w + ((k * 16 * NH * 2) >> 4), I, tt > t0 || k > 0);
+                    mma_commit(one, empty(it, k));
+                }
+            }
+            return true;
+        });
+        mma_commit(one, bar + C::kDone * 8);
+        warp_wait(bar + C::kDone * 8, 0u, alone, 501);
+    } else {
+        // ------------------------------------------------ softmax: warps 4 g .. 4 g + 3 have half of the heads; a lane has a key, warp w
+        // of four the keys 16 w .. 16 w + 15 (M = 64: the scores fill 16 of a warp's 32 lanes).
+        // The four warps run the same number of tiles whatever their waits return, so that their barriers always meet.
+        const int g = warp >> 2, w4 = warp & 3, h0 = g * HN, tg = t & 127;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const int key = 16 * w4 + (lane & 15);
+        const bool mine = lane < 16;
+        auto meet = [&] { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + g) : "memory"); };
+        sequences([&](int b, int len, int t0, int t1) {
+            float l[HN];
+#pragma unroll
+            for (int h = 0; h < HN; ++h) l[h] = 0.f;
             for (int tt = t0; tt < t1; ++tt, ++it) {
                 const int s = it % C::STAGES;
-                warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(it / C::STAGES) & 1u, wt, 600);   // live_blocks, and the rows to clear
+                warp_wait(bar + (C::kKFull + s) * 8, turn(it), wt, 600);   // live_blocks, and the rows to clear
                 const int left = len - tt * kTile;                       // keys of this tile
-                const bool seen = mine && key < left && ((live_blocks[s] >> warp) & 1);
+                const bool seen = mine && key < left && ((live_blocks[s] >> w4) & 1);
                 if (left < kTile && (left & 15)) {   // what the last block holds behind the sequence must not meet the products
                     const int end = (left + 15) & ~15;
-                    for (int i = t; i < (end - left) * C::CH * 8; i += 128) {
+                    for (int i = t; i < (end - left) * C::CH * 8; i += 32 * kSoftWarps) {
                         const int row = left + i / (C::CH * 8), c = i % (C::CH * 8);
                         *reinterpret_cast<uint4*>(smem + s * C::TILE + (row >> 3) * C::GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
@@ -378,16 +411,12 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
                 }
                 warp_wait(bar + (C::kSFull + (it & 1)) * 8, (uint32_t)(it >> 1) & 1u, wt, 601);
                 fence_after();
-                float x[NH];
-#pragma unroll
-                for (int c = 0; c < NH / 32; ++c) tmem_ld32(tb + lanes + C::SCOL + (it & 1) * NH + 32 * c, x + 32 * c);
-                wait_ld();
-#pragma unroll
-                for (int c = 0; c < NH / 32; ++c) tie32(x + 32 * c);
+                float x[HN];
+                tmem_load<HN>(tb + lanes + C::SCOL + (it & 1) * NH + h0, x);
                 float over = -INFINITY;   // how far a score lies above its head's reference
 #pragma unroll
-                for (int h = 0; h < NH; h += 4) {
-                    const float4 r = *reinterpret_cast<const float4*>(ref + h);
+                for (int h = 0; h < HN; h += 4) {
+                    const float4 r = *reinterpret_cast<const float4*>(ref + h0 + h);
                     const float rr[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -398,56 +427,54 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
                 // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
                 // smaller ones, and O has to be scaled only when a score passes that.
                 unsigned raise;
-                asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
-                             : "=r"(raise) : "r"((unsigned)(tt == t0 || over > 8.f)) : "memory");
+                asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
+                             : "=r"(raise) : "r"((unsigned)(tt == t0 || over > 8.f)), "r"(1 + g) : "memory");
                 if (raise) {
+                    {
+                        float v[HN];
 #pragma unroll
-                    for (int c = 0; c < NH / 32; ++c) {
-                        float v[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = x[32 * c + i];
-                        column[warp][32 * c + lane] = reduce_columns<true>(v, lane);
+                        for (int i = 0; i < HN; ++i) v[i] = x[i];
+                        const float most = reduce_columns<true, HN>(v, lane);
+                        if (lane < HN) column[w4][h0 + lane] = most;
                     }
-                    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-                    if (t < NH) {
-                        const float most = fmaxf(fmaxf(column[0][t], column[1][t]), fmaxf(column[2][t], column[3][t]));
+                    meet();
+                    if (tg < HN) {
+                        const int h = h0 + tg;
+                        const float most = fmaxf(fmaxf(column[0][h], column[1][h]), fmaxf(column[2][h], column[3][h]));
                         // a finite reference where no key is left, so that the next tile's weights stay numbers
-                        const float old = tt == t0 ? -1e30f : ref[t], now = fmaxf(old, most);
-                        factor[t] = tt == t0 ? 0.f : ex2(old - now);
-                        ref[t] = now;
+                        const float old = tt == t0 ? -1e30f : ref[h], now = fmaxf(old, most);
+                        factor[h] = tt == t0 ? 0.f : ex2(old - now);
+                        ref[h] = now;
                     }
-                    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+                    meet();
                     if (tt > t0) {
 #pragma unroll
-                        for (int h = 0; h < NH; ++h) l[h] *= factor[h];
-                        // O holds the tiles before this one
-                        warp_wait(bar + (C::kKEmpty + (it - 1) % C::STAGES) * 8, (uint32_t)((it - 1) / C::STAGES) & 1u, wt, 602);
+                        for (int h = 0; h < HN; ++h) l[h] *= factor[h0 + h];
+                        warp_wait(empty(it - 1, 3), turn(it - 1), wt, 602);   // O holds the tiles before this one
                         fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < C::MT * NH / 32; ++c) {
-                            float v[32];
-                            uint32_t u[32];
-                            tmem_ld32(tb + lanes + 32 * c, v);
-                            wait_ld();
-                            tie32(v);
+                        for (int m = 0; m < C::MT; ++m) {
+                            float v[HN];
+                            uint32_t u[HN];
+                            tmem_load<HN>(tb + lanes + m * NH + h0, v);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * factor[(32 * c + i) % NH]);
-                            tmem_st32(tb + lanes + 32 * c, u);
+                            for (int i = 0; i < HN; ++i) u[i] = __float_as_uint(v[i] * factor[h0 + i]);
+                            if constexpr (HN == 32) tmem_st32(tb + lanes + m * NH + h0, u);
+                            else tmem_st16(tb + lanes + m * NH + h0, u);
                         }
                         wait_st();
                     }
                 }
                 // the tile before last (or, with one buffer, the last) has taken its weights
-                if (it >= C::PBUF)
-                    warp_wait(bar + (C::kKEmpty + (it - C::PBUF) % C::STAGES) * 8, (uint32_t)((it - C::PBUF) / C::STAGES) & 1u, wt, 603);
+                if (it >= C::PBUF) warp_wait(empty(it - C::PBUF, 3), turn(it - C::PBUF), wt, 603);
                 unsigned char* row = smem + C::STAGES * C::TILE + C::QB + (it % C::PBUF) * C::PB + key * NH * 2;
-                const int turn = NH == 64 ? key & 7 : (key >> 1) & 3;
+                const int sw = NH == 64 ? key & 7 : (key >> 1) & 3;
 #pragma unroll
-                for (int h = 0; h < NH; h += 8) {
+                for (int h = 0; h < HN; h += 8) {
                     uint32_t u[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 4) {
-                        const float4 r = *reinterpret_cast<const float4*>(ref + h + i);
+                        const float4 r = *reinterpret_cast<const float4*>(ref + h0 + h + i);
                         const float a = ex2(x[h + i] - r.x), bb = ex2(x[h + i + 1] - r.y), c = ex2(x[h + i + 2] - r.z), d = ex2(x[h + i + 3] - r.w);
                         l[h + i] += a;
                         l[h + i + 1] += bb;
@@ -456,7 +483,7 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
                         u[i / 2] = pack_half(a, bb);
                         u[i / 2 + 1] = pack_half(c, d);
                     }
-                    if (mine) *reinterpret_cast<uint4*>(row + (((h >> 3) ^ turn) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                    if (mine) *reinterpret_cast<uint4*>(row + ((((h0 + h) >> 3) ^ sw) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 fence_async();
                 fence_before();
@@ -466,38 +493,40 @@ __global__ void __launch_bounds__(192, 1) mla_decode_kernel(const __grid_constan
             // the part: O^T's lanes are latent values, its columns heads
             const int heads = min(NH, p.H - hg * NH);
             const size_t part = ((size_t)hg * (p.windows + p.batch) + win + b) * NH;
-            warp_wait(bar + (C::kKEmpty + (it - 1) % C::STAGES) * 8, (uint32_t)((it - 1) / C::STAGES) & 1u, wt, 604);
+            {
+                float v[HN];
+#pragma unroll
+                for (int i = 0; i < HN; ++i) v[i] = mine ? l[i] : 0.f;
+                const float sum = reduce_columns<false, HN>(v, lane);
+                if (lane < HN) column[w4][h0 + lane] = sum;
+            }
+            meet();
+            if (tg < HN && h0 + tg < heads) {
+                const int h = h0 + tg;
+                p.stats[part + h] = make_float2(ref[h], column[0][h] + column[1][h] + column[2][h] + column[3][h]);
+            }
+            warp_wait(empty(it - 1, 3), turn(it - 1), wt, 604);
             fence_after();
 #pragma unroll 1
-            for (int c = 0; c < C::MT * NH / 32; ++c) {
-                float v[32];
-                tmem_ld32(tb + lanes + 32 * c, v);
-                wait_ld();
-                tie32(v);
-                const int h0 = 32 * c % NH;
-                float* o = p.parts + (part + h0) * R + 128 * (32 * c / NH) + 32 * warp + lane;
+            for (int m = 0; m < C::MT; ++m) {
+                float v[HN];
+                tmem_load<HN>(tb + lanes + m * NH + h0, v);
+                float* o = p.parts + (part + h0) * R + 128 * m + 32 * w4 + lane;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < HN; ++i)
                     if (h0 + i < heads) o[i * R] = v[i];
             }
             fence_before();
-            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");   // `column` is free
-#pragma unroll
-            for (int c = 0; c < NH / 32; ++c) {
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = mine ? l[32 * c + i] : 0.f;
-                column[warp][32 * c + lane] = reduce_columns<false>(v, lane);
-            }
-            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-            if (t < heads) p.stats[part + t] = make_float2(ref[t], column[0][t] + column[1][t] + column[2][t] + column[3][t]);
-            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");   // before the next sequence's reference
+            meet();   // before the next sequence's reference and columns
             return true;
         });
     }
+    // (the copying warp of a window with tiles has waited already)
+    pdl_wait();
+    pdl_trigger();
     fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kScoreWarp) {
         fence_after();
         tmem_free<C::COLS>(tb);
     }
@@ -541,7 +570,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
     {
         const int r = warp, b = b0 + r;
         const bool in = r < p.rows && b < p.batch;
-        const int W = p.plan[1], n = in ? tiles_checked(p.lens[b], p.cap) : 0, at = in ? p.plan[kPlanStart + b] + kEnter : 0;
+        const int W = p.plan[0], n = in ? tiles_checked(p.lens[b], p.cap) : 0, at = in ? p.plan[kPlanStart + b] + kEnter : 0;
         int w0 = 0, c = 0;
         if (n) {
             w0 = at / W;
@@ -697,8 +726,7 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     int windows = std::min(num_sms(), kMaxWin) / sh.groups;
     if (windows < 1) windows = 1;
-    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws + sh.qc), a.lens,
-                       reinterpret_cast<int*>(ws), (int)a.batch, a.H, windows, (long long)a.maxb * kBlock, err};
+    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws + sh.qc), (int)a.batch, a.H, err};
     DecodeParams dp = {};
     const uint64_t row = (R + kRope) * 2;
     const uint64_t kd[4] = {64, 8, (uint64_t)C::CH, (uint64_t)a.num_blocks * 2}, kst[3] = {row, 128, 8 * row};
@@ -707,13 +735,13 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     const uint64_t qd[4] = {64, (uint64_t)a.H, (uint64_t)C::CH, (uint64_t)a.batch}, qst[3] = {row, 128, a.H * row};
     const uint32_t qb[4] = {64, (uint32_t)NH, (uint32_t)C::CH, 1};
     if (int rc = f16_tensor_map(ws + sh.qc, 4, qd, qst, qb, &dp.tq)) return rc;
-    dp.plan = ap.plan;
+    dp.plan = reinterpret_cast<int*>(ws);
     dp.tables = a.tables;
     dp.lens = a.lens;
     dp.parts = reinterpret_cast<float*>(ws + sh.parts);
     dp.stats = reinterpret_cast<float2*>(ws + sh.stats);
     dp.maxb = a.maxb;
-    dp.cap = ap.cap;
+    dp.cap = (long long)a.maxb * kBlock;
     dp.num_blocks = a.num_blocks;
     dp.batch = (int)a.batch;
     dp.H = a.H;
@@ -722,10 +750,10 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, ap.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), ap.cap, (int)a.batch, a.H, windows, kJoinRows};
+    JoinParams jp = {ap.w, dp.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.batch, a.H, windows, kJoinRows};
     while (jp.rows > 1 && jp.rows / 2 >= a.batch) jp.rows /= 2;
-    cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64) + 1), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
-    if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(192), C::SMEM, s, true, dp);
+    cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64)), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
+    if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(kDecodeThreads), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
         e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)(a.H * kJoinCtas), (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
                    true, jp);
