@@ -546,43 +546,91 @@ struct JoinParams {
 
 // A cluster of four CTAs takes one head and `rows` sequences. Each CTA joins the parts of a quarter of the latent values, hands
 // them to the other three through distributed shared memory, and multiplies all of them with a quarter of the head's value
-// rows. Those weights go to registers before the wait on the attention (they are B fragments of m16n8k16: a lane's 16 bytes
-// are 8 consecutive values of one row; which k they stand for is the products' own business as long as A's are the same).
+// rows (they are B fragments of m16n8k16: a lane's 16 bytes are 8 consecutive values of one row; which k they stand for is the
+// products' own business as long as A's are the same). What the lengths alone decide is worked out before the wait on the
+// attention; behind it the parts and their statistics are loaded at once.
 // o enters the product as two f16 numbers (22 bits): as one, its rounding alone would be as large as the output's.
 constexpr int kJoinThreads = 256, kJoinCtas = 4, kJoinRows = 8;
 template <int D, int R, int NH>
 __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
     constexpr int OP = R + 32, PER = R / kJoinCtas / 4, GROUPS = kJoinThreads / PER;   // threads of a sequence's quarter (4 values each)
     constexpr int NT = D / kJoinCtas / 8, KW = 8 / NT, KS = R / 32 / KW;               // 8-row tiles of a CTA, warps and steps of one
+    constexpr int AT_ONCE = 4;                                                         // parts a thread loads at a time
     __shared__ __align__(16) __half os[2][kJoinRows * OP];   // o, its upper and lower halves
     __shared__ __align__(16) float4 share[GROUPS][PER];
     __shared__ float scale[kJoinRows][kMaxWin];
     __shared__ float sums[8][kJoinRows][8];
-    __shared__ int first[kJoinRows], count[kJoinRows];
+    __shared__ int first[kJoinRows], count[kJoinRows], places[2][8];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, quarter = blockIdx.x % kJoinCtas, h = blockIdx.x / kJoinCtas;
     const int b0 = blockIdx.y * p.rows, nt = warp / KW, kw = warp % KW;
-    uint4 w[KS];
     const int d0 = quarter * (D / kJoinCtas) + 8 * nt;       // this warp's value rows
-    pdl_wait();
-    pdl_trigger();
     const int hg = h / NH;
     const size_t base = (size_t)hg * (p.windows + p.batch);
+    // every CTA of the cluster has started before another writes into it (waited for below)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     {
-        const int r = warp, b = b0 + r;
-        const bool in = r < p.rows && b < p.batch;
-        const int W = p.plan[0], n = in ? tiles_checked(p.lens[b], p.cap) : 0, at = in ? p.plan[kPlanStart + b] + kEnter : 0;
-        int w0 = 0, c = 0;
-        if (n) {
-            w0 = at / W;
-            c = (at + n - 1) / W - w0 + 1;
-            constexpr int MORE = kMaxWin / 32;
-            float2 s[MORE];
-            float m = -INFINITY, l = 0.f;
+        // the places of all sequences and of those before this cluster's, as the attention counts them
+        int all = 0, before = 0;
+        for (int b = t; b < p.batch; b += kJoinThreads) {
+            const int n = tiles_checked(__ldg(p.lens + b), p.cap);
+            all += n ? n + kEnter : 0;
+            before += n && b < b0 ? n + kEnter : 0;
+        }
 #pragma unroll
-            for (int i = 0; i < MORE; ++i) {
-                s[i] = 32 * i + lane < c ? p.stats[(base + w0 + 32 * i + lane + b) * NH + h % NH] : make_float2(-INFINITY, 0.f);
-                m = fmaxf(m, s[i].x);
+        for (int o = 16; o; o >>= 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        if (lane == 0) {
+            places[0][warp] = all;
+            places[1][warp] = before;
+        }
+        __syncthreads();
+        if (t < kJoinRows) {   // (lanes 0-7 of one warp)
+            all = before = 0;
+            for (int i = 0; i < 8; ++i) {
+                all += places[0][i];
+                before += places[1][i];
             }
+            const int W = max(1, (all + p.windows - 1) / p.windows), b = b0 + t;
+            const int n = t < p.rows && b < p.batch ? tiles_checked(__ldg(p.lens + b), p.cap) : 0, mine = n ? n + kEnter : 0;
+            int at = mine;
+#pragma unroll
+            for (int o = 1; o < kJoinRows; o <<= 1) {
+                const int v = __shfl_up_sync(0xffu, at, o);
+                at += t >= o ? v : 0;
+            }
+            at += before - mine + kEnter;
+            const int w0 = n ? at / W : 0;
+            first[t] = w0 + b;
+            count[t] = n ? (at + n - 1) / W - w0 + 1 : 0;
+        }
+        __syncthreads();
+    }
+    pdl_wait();
+    pdl_trigger();
+    const int g = t / PER, at = t % PER;
+    const int split = GROUPS / p.rows, r0 = g / split;   // groups of a sequence (powers of two; at least one)
+    const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r0]) * NH + h % NH) * R + quarter * (R / kJoinCtas)) + at;
+    const int c0 = count[r0];
+    float4 v[AT_ONCE];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+            v[i] = i0 + i * split < c0 ? __ldcg(src + (size_t)(i0 + i * split) * (NH * R / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(g % split);
+    {
+        const int r = warp, c = count[r];
+        constexpr int MORE = kMaxWin / 32;
+        float2 s[MORE];
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < MORE; ++i) {
+            s[i] = 32 * i + lane < c ? __ldcg(p.stats + (base + first[r] + 32 * i + lane) * NH + h % NH) : make_float2(-INFINITY, 0.f);
+            m = fmaxf(m, s[i].x);
+        }
+        if (c > 0) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
@@ -597,20 +645,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
             for (int i = 0; i < MORE; ++i)
                 if (32 * i + lane < c) scale[r][32 * i + lane] = s[i].x * inv;
         }
-        if (lane == 0) {
-            first[r] = w0 + b;
-            count[r] = c;
-        }
     }
     __syncthreads();
-    const int g = t / PER, at = t % PER;
-    const int split = GROUPS / p.rows;   // groups of a sequence (powers of two; at least one)
     auto put = [&](int r, float4 a) {    // 4 values of o to all four CTAs
         const float x[4] = {a.x, a.y, a.z, a.w};
         float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = x[i] - __half2float(__float2half_rn(x[i]));
-        const uint32_t v[2][2] = {{pack_half(x[0], x[1]), pack_half(x[2], x[3])}, {pack_half(y[0], y[1]), pack_half(y[2], y[3])}};
+        const uint32_t u[2][2] = {{pack_half(x[0], x[1]), pack_half(x[2], x[3])}, {pack_half(y[0], y[1]), pack_half(y[2], y[3])}};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t here = su32(os[i] + r * OP + quarter * (R / kJoinCtas) + 4 * at);
@@ -618,48 +660,37 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
             for (int c = 0; c < kJoinCtas; ++c) {
                 uint32_t there;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(c));
-                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(there), "r"(v[i][0]), "r"(v[i][1]) : "memory");
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(there), "r"(u[i][0]), "r"(u[i][1]) : "memory");
             }
         }
     };
-    // every CTA of the cluster has started before another writes into it
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    {
-        const int r = g / split;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r]) * NH + h % NH) * R + quarter * (R / kJoinCtas)) + at;
-        const int c = count[r];
-        for (int i0 = g % split; i0 < c; i0 += 8 * split) {
-            float4 v[8];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = g % split; i0 < c0; i0 += AT_ONCE * split) {
+        if (i0 >= AT_ONCE * split) load(i0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = i0 + i * split < c ? __ldcg(src + (size_t)(i0 + i * split) * (NH * R / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = i0 + i * split < c ? scale[r][i0 + i * split] : 0.f;
-                a.x = fmaf(v[i].x, f, a.x);
-                a.y = fmaf(v[i].y, f, a.y);
-                a.z = fmaf(v[i].z, f, a.z);
-                a.w = fmaf(v[i].w, f, a.w);
-            }
-        }
-        if (split == 1) put(r, a);
-        else {
-            share[g][at] = a;
-            __syncthreads();
-            if (g < p.rows) {
-                a = share[g * split][at];
-                for (int i = 1; i < split; ++i) {
-                    const float4 v = share[g * split + i][at];
-                    a.x += v.x;
-                    a.y += v.y;
-                    a.z += v.z;
-                    a.w += v.w;
-                }
-                put(g, a);
-            }
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const float f = i0 + i * split < c0 ? scale[r0][i0 + i * split] : 0.f;
+            a.x = fmaf(v[i].x, f, a.x);
+            a.y = fmaf(v[i].y, f, a.y);
+            a.z = fmaf(v[i].z, f, a.z);
+            a.w = fmaf(v[i].w, f, a.w);
         }
     }
+    if (split > 1) {
+        share[g][at] = a;
+        __syncthreads();
+        a = share[g < p.rows ? g * split : 0][at];
+        for (int i = 1; i < split; ++i) {
+            const float4 x = share[g < p.rows ? g * split + i : 0][at];
+            a.x += x.x;
+            a.y += x.y;
+            a.z += x.z;
+            a.w += x.w;
+        }
+    }
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (g < p.rows || split == 1) put(g, a);   // (with one group a sequence, g is the sequence)
+    uint4 w[KS];
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < KS; ++k)
