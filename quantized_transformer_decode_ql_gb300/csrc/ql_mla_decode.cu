@@ -15,7 +15,6 @@ namespace mla {
 constexpr int kTile = 64;       // keys of a tile
 constexpr int kEnter = 1;       // tiles that entering a sequence costs a window (its query, its part written): charged in the split
 constexpr int kMaxWin = 160;    // windows at most
-constexpr int kPlanStart = 4;   // plan: [0] places of a window; from here the sequences' first places
 
 __host__ __device__ inline int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
@@ -120,16 +119,16 @@ struct Cfg {
     static constexpr int kKFull = 0, kKEmpty = STAGES, kSFull = 5 * STAGES, kPReady = kSFull + 2, kQFull = kPReady + 2, kQEmpty = kQFull + 1,
                          kDone = kQEmpty + 1, kBars = kDone + 1;
     static constexpr uint32_t PSW = NH == 64 ? 2 : 4;   // P's rows of 2 NH bytes: 128- or 64-byte swizzle
-    static constexpr int HN = NH / 2;                   // heads of a softmax group
+    static constexpr int HN = NH / 2;                   // heads of a softmax group of four warps (four groups of 16 of 64: 61 instead of 57 us, many heads)
+    static constexpr int kSoftWarps = NH / HN * 4, kCopyWarp = kSoftWarps, kScoreWarp = kSoftWarps + 1, kValueWarp = kSoftWarps + 2,
+                         THREADS = (kSoftWarps + 3) * 32;
     static_assert(SCOL + 2 * NH <= 512, "tensor memory");
     static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
-constexpr int kSoftWarps = 8, kCopyWarp = 8, kScoreWarp = 9, kValueWarp = 10, kDecodeThreads = 352;
 
 struct DecodeParams {
     CUtensorMap tk;        // the pool: [group of 8 rows][run][row][64 values]
     CUtensorMap tq;        // absorbed queries: [sequence][run][head][64 values]
-    int* plan;
     const int32_t* tables;
     const int32_t* lens;
     float* parts;          // [head group][window + sequence][NH][R]
@@ -164,19 +163,21 @@ struct Window {
 };
 
 // Every CTA cuts the batch by itself, from the lengths: it starts before the absorbed queries are there, and so this and its
-// first tiles' copies cost nothing. CTA 0 leaves the sequences' places to the join.
+// first tiles' copies cost nothing.
+template <int THREADS>
 __device__ Window make_window(const DecodeParams& p, int win) {
-    constexpr int WARPS = kDecodeThreads / 32;
+    constexpr int WARPS = THREADS / 32;
     __shared__ int sums[2][WARPS];
     __shared__ int found[2];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const bool writer = blockIdx.x == 0;
     auto places = [&](int b) {
-        const int n = b < p.batch ? tiles_checked(__ldg(p.lens + b), p.cap) : 0;
+        const int len = b < p.batch ? __ldg(p.lens + b) : 0, n = tiles_checked(len, p.cap);
+        if (len != 0 && n == 0 && blockIdx.x == 0) record_device_error(p.err, kErrAttnLength, b, len);
         return n ? n + kEnter : 0;
     };
-    int sum = 0;
-    for (int b = t; b < p.batch; b += kDecodeThreads) sum += places(b);
+    const int mine = places(t);
+    int sum = mine;
+    for (int b = t + THREADS; b < p.batch; b += THREADS) sum += places(b);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) sums[0][warp] = sum;
@@ -187,8 +188,8 @@ __device__ Window make_window(const DecodeParams& p, int win) {
     const int W = max(1, (total + p.windows - 1) / p.windows);
     const int lo = win * W, hi = min(lo + W, total);
     int before = 0;
-    for (int b0 = 0, k = 1; b0 < p.batch && (writer || before <= lo); b0 += kDecodeThreads, k ^= 1) {
-        const int b = b0 + t, n = places(b);
+    for (int b0 = 0, k = 1; b0 < p.batch && before <= lo; b0 += THREADS, k ^= 1) {
+        const int b = b0 + t, n = b0 == 0 ? mine : places(b);
         int at = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -206,20 +207,14 @@ __device__ Window make_window(const DecodeParams& p, int win) {
             found[0] = b;
             found[1] = at;
         }
-        if (writer && b < p.batch) {
-            p.plan[kPlanStart + b] = at;
-            const int len = p.lens[b];
-            if (len != 0 && n == 0) record_device_error(p.err, kErrAttnLength, b, len);
-        }
         before += all;
     }
-    if (writer && t == 0) p.plan[0] = W;
     __syncthreads();
     return {lo, hi, found[0], found[1]};
 }
 
 template <int R, int NH>
-__global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = Cfg<R, NH>;
     constexpr int HN = C::HN;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -227,7 +222,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
     __shared__ int live_blocks[C::STAGES];
-    __shared__ __align__(16) float ref[NH];          // the weights' reference of each head, log2
+    __shared__ __align__(16) float ref[NH];          // the weights' reference of each head, log2, negated
     __shared__ float factor[NH], column[4][NH];
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t bar = su32(bars), ks = su32(smem), qs = ks + C::STAGES * C::TILE, ps = qs + C::QB;
@@ -238,7 +233,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(bar + (C::kSFull + s) * 8, 1);
-            bar_init(bar + (C::kPReady + s) * 8, kSoftWarps);
+            bar_init(bar + (C::kPReady + s) * 8, C::kSoftWarps);
         }
         bar_init(bar + C::kQFull * 8, 1);
         bar_init(bar + C::kQEmpty * 8, 1);
@@ -248,10 +243,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
         prefetch_map(&p.tk);
         prefetch_map(&p.tq);
     }
-    if (warp == kScoreWarp) tmem_alloc<C::COLS>(&tmem_at);
+    if (warp == C::kScoreWarp) tmem_alloc<C::COLS>(&tmem_at);
     fence_before();
     const int hg = blockIdx.x % p.groups, win = blockIdx.x / p.groups;
-    const Window window = make_window(p, win);   // (and a barrier of the CTA)
+    const Window window = make_window<C::THREADS>(p, win);   // (and a barrier of the CTA)
     fence_after();
     const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
     const Waits wt = {p.err, &abort_flag, p.ns};
@@ -272,7 +267,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
     auto turn = [&](int i) { return (uint32_t)(i / C::STAGES) & 1u; };   // parity of tile i's stage
 
     int it = 0, sg = 0;   // tiles and sequences so far
-    if (warp == kCopyWarp) {
+    if (warp == C::kCopyWarp) {
         // ------------------------------------------------ copies: lanes 0-3 bring the tile's four blocks
         bool ok = true;
         sequences([&](int b, int len, int t0, int t1) {
@@ -337,7 +332,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
             if (sg > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(sg - 1) & 1u, alone, 301);
         }
         __syncwarp();
-    } else if (warp == kScoreWarp) {
+    } else if (warp == C::kScoreWarp) {
         // ------------------------------------------------ S^T = K q'^T, two tiles ahead of their values at most
         constexpr uint32_t I = instr(64, NH, false, false);
         const uint32_t one = elect_one();
@@ -361,7 +356,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
         });
         mma_commit(one, bar + C::kDone * 8);   // every product has ended before the tensor memory is given back
         warp_wait(bar + C::kDone * 8, 0u, alone, 500);
-    } else if (warp == kValueWarp) {
+    } else if (warp == C::kValueWarp) {
         // ------------------------------------------------ O^T += V^T P
         constexpr uint32_t I = instr(128, NH, true, true);
         const uint32_t one = elect_one();
@@ -403,7 +398,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
                 const bool seen = mine && key < left && ((live_blocks[s] >> w4) & 1);
                 if (left < kTile && (left & 15)) {   // what the last block holds behind the sequence must not meet the products
                     const int end = (left + 15) & ~15;
-                    for (int i = t; i < (end - left) * C::CH * 8; i += 32 * kSoftWarps) {
+                    for (int i = t; i < (end - left) * C::CH * 8; i += 32 * C::kSoftWarps) {
                         const int row = left + i / (C::CH * 8), c = i % (C::CH * 8);
                         *reinterpret_cast<uint4*>(smem + s * C::TILE + (row >> 3) * C::GROUP + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
@@ -411,19 +406,27 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
                 }
                 warp_wait(bar + (C::kSFull + (it & 1)) * 8, (uint32_t)(it >> 1) & 1u, wt, 601);
                 fence_after();
+                const uint32_t sc = tb + lanes + C::SCOL + (it & 1) * NH + h0;
+                const float2 scale = make_float2(p.scale_log2, p.scale_log2);
                 float x[HN];
-                tmem_load<HN>(tb + lanes + C::SCOL + (it & 1) * NH + h0, x);
-                float over = -INFINITY;   // how far a score lies above its head's reference
+                float over = -INFINITY;
+                auto exponents = [&] {   // x: how far the scores lie above their heads' references
+                    tmem_load<HN>(sc, x);
+                    if (seen) {
 #pragma unroll
-                for (int h = 0; h < HN; h += 4) {
-                    const float4 r = *reinterpret_cast<const float4*>(ref + h0 + h);
-                    const float rr[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[h + i] = seen ? x[h + i] * p.scale_log2 : -INFINITY;
-                        over = fmaxf(over, x[h + i] - rr[i]);
+                        for (int h = 0; h < HN; h += 4) {
+                            const float4 r = *reinterpret_cast<const float4*>(ref + h0 + h);
+                            const float2 a = fma2(make_float2(x[h], x[h + 1]), scale, make_float2(r.x, r.y));
+                            const float2 c = fma2(make_float2(x[h + 2], x[h + 3]), scale, make_float2(r.z, r.w));
+                            x[h] = a.x;
+                            x[h + 1] = a.y;
+                            x[h + 2] = c.x;
+                            x[h + 3] = c.y;
+                            over = fmaxf(over, fmaxf(fmaxf(a.x, a.y), fmaxf(c.x, c.y)));
+                        }
                     }
-                }
+                };
+                exponents();
                 // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
                 // smaller ones, and O has to be scaled only when a score passes that.
                 unsigned raise;
@@ -432,8 +435,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
                 if (raise) {
                     {
                         float v[HN];
+                        tmem_load<HN>(sc, v);
 #pragma unroll
-                        for (int i = 0; i < HN; ++i) v[i] = x[i];
+                        for (int i = 0; i < HN; ++i) v[i] = seen ? v[i] * p.scale_log2 : -INFINITY;
                         const float most = reduce_columns<true, HN>(v, lane);
                         if (lane < HN) column[w4][h0 + lane] = most;
                     }
@@ -442,9 +446,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
                         const int h = h0 + tg;
                         const float most = fmaxf(fmaxf(column[0][h], column[1][h]), fmaxf(column[2][h], column[3][h]));
                         // a finite reference where no key is left, so that the next tile's weights stay numbers
-                        const float old = tt == t0 ? -1e30f : ref[h], now = fmaxf(old, most);
+                        const float old = tt == t0 ? -1e30f : -ref[h], now = fmaxf(old, most);
                         factor[h] = tt == t0 ? 0.f : ex2(old - now);
-                        ref[h] = now;
+                        ref[h] = -now;
                     }
                     meet();
                     if (tt > t0) {
@@ -464,26 +468,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
                         }
                         wait_st();
                     }
+                    exponents();
                 }
                 // the tile before last (or, with one buffer, the last) has taken its weights
                 if (it >= C::PBUF) warp_wait(empty(it - C::PBUF, 3), turn(it - C::PBUF), wt, 603);
                 unsigned char* row = smem + C::STAGES * C::TILE + C::QB + (it % C::PBUF) * C::PB + key * NH * 2;
                 const int sw = NH == 64 ? key & 7 : (key >> 1) & 3;
+                if (mine) {   // (a key that is not seen, its scores never looked at, weighs 0)
 #pragma unroll
-                for (int h = 0; h < HN; h += 8) {
-                    uint32_t u[4];
+                    for (int h = 0; h < HN; h += 8) {
+                        uint32_t u[4];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 r = *reinterpret_cast<const float4*>(ref + h0 + h + i);
-                        const float a = ex2(x[h + i] - r.x), bb = ex2(x[h + i + 1] - r.y), c = ex2(x[h + i + 2] - r.z), d = ex2(x[h + i + 3] - r.w);
-                        l[h + i] += a;
-                        l[h + i + 1] += bb;
-                        l[h + i + 2] += c;
-                        l[h + i + 3] += d;
-                        u[i / 2] = pack_half(a, bb);
-                        u[i / 2 + 1] = pack_half(c, d);
+                        for (int i = 0; i < 8; i += 2) {
+                            const float2 w = seen ? make_float2(ex2(x[h + i]), ex2(x[h + i + 1])) : make_float2(0.f, 0.f);
+                            const float2 sum = add2(make_float2(l[h + i], l[h + i + 1]), w);
+                            l[h + i] = sum.x;
+                            l[h + i + 1] = sum.y;
+                            u[i / 2] = pack_half(w.x, w.y);
+                        }
+                        *reinterpret_cast<uint4*>(row + ((((h0 + h) >> 3) ^ sw) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    if (mine) *reinterpret_cast<uint4*>(row + ((((h0 + h) >> 3) ^ sw) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 fence_async();
                 fence_before();
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
             meet();
             if (tg < HN && h0 + tg < heads) {
                 const int h = h0 + tg;
-                p.stats[part + h] = make_float2(ref[h], column[0][h] + column[1][h] + column[2][h] + column[3][h]);
+                p.stats[part + h] = make_float2(-ref[h], column[0][h] + column[1][h] + column[2][h] + column[3][h]);
             }
             warp_wait(empty(it - 1, 3), turn(it - 1), wt, 604);
             fence_after();
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
     pdl_trigger();
     fence_before();
     __syncthreads();
-    if (warp == kScoreWarp) {
+    if (warp == C::kScoreWarp) {
         fence_after();
         tmem_free<C::COLS>(tb);
     }
@@ -535,7 +539,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) mla_decode_kernel(const __g
 // ---------------------------------------------------------------- parts joined, values projected
 struct JoinParams {
     const __half* w;       // [H][2 D][R]
-    const int* plan;
     const int32_t* lens;
     const float* parts;
     const float2* stats;
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
 // ---------------------------------------------------------------- host
 struct DecodeShape {
     int NH, groups;
-    size_t plan, qc, parts, stats, total;   // offsets in the workspace
+    size_t parts, stats, total;   // offsets in the workspace; the absorbed queries come first
 };
 static DecodeShape decode_shape(int64_t batch, int H, int R) {
     DecodeShape s = {};
@@ -731,8 +734,7 @@ static DecodeShape decode_shape(int64_t batch, int H, int R) {
     s.groups = (H + s.NH - 1) / s.NH;
     const size_t win = kMaxWin / s.groups + 1, rows = (size_t)s.groups * (batch + win) * s.NH;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-    s.qc = up((size_t)(kPlanStart + batch) * 4);
-    s.parts = s.qc + up((size_t)batch * H * (R + kRope) * 2);
+    s.parts = up((size_t)batch * H * (R + kRope) * 2);
     s.stats = s.parts + rows * R * 4;
     s.total = s.stats + up(rows * 8);
     return s;
@@ -757,7 +759,7 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     int windows = std::min(num_sms(), kMaxWin) / sh.groups;
     if (windows < 1) windows = 1;
-    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws + sh.qc), (int)a.batch, a.H, err};
+    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws), (int)a.batch, a.H, err};
     DecodeParams dp = {};
     const uint64_t row = (R + kRope) * 2;
     const uint64_t kd[4] = {64, 8, (uint64_t)C::CH, (uint64_t)a.num_blocks * 2}, kst[3] = {row, 128, 8 * row};
@@ -765,8 +767,7 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     if (int rc = f16_tensor_map(a.pool, 4, kd, kst, kb, &dp.tk)) return rc;
     const uint64_t qd[4] = {64, (uint64_t)a.H, (uint64_t)C::CH, (uint64_t)a.batch}, qst[3] = {row, 128, a.H * row};
     const uint32_t qb[4] = {64, (uint32_t)NH, (uint32_t)C::CH, 1};
-    if (int rc = f16_tensor_map(ws + sh.qc, 4, qd, qst, qb, &dp.tq)) return rc;
-    dp.plan = reinterpret_cast<int*>(ws);
+    if (int rc = f16_tensor_map(ws, 4, qd, qst, qb, &dp.tq)) return rc;
     dp.tables = a.tables;
     dp.lens = a.lens;
     dp.parts = reinterpret_cast<float*>(ws + sh.parts);
@@ -781,10 +782,10 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, dp.plan, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.batch, a.H, windows, kJoinRows};
+    JoinParams jp = {ap.w, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.batch, a.H, windows, kJoinRows};
     while (jp.rows > 1 && jp.rows / 2 >= a.batch) jp.rows /= 2;
     cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64)), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
-    if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(kDecodeThreads), C::SMEM, s, true, dp);
+    if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(C::THREADS), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
         e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)(a.H * kJoinCtas), (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
                    true, jp);
