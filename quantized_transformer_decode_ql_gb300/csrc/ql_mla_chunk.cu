@@ -1,7 +1,7 @@
 // Latent attention of a prompt chunk over the paged cache, in the expanded form:
 //
 //  1. mla_expand_kernel: every head's keys k = Wk_h c and values v = Wv_h c of the whole context, f16, by a tcgen05 product over
-//     the cache's rows (128 tokens x 256 outputs a CTA), and the rotated key parts laid out beside them;
+//     the cache's rows (256 tokens x 256 outputs a pair of CTAs), and the rotated key parts laid out beside them;
 //  2. mla_chunk_kernel: causal attention of 128 queries of one head, the online softmax over tiles of 128 keys in two
 //     independent halves of the tiles (even and odd), so that one half's products run beside the other's weights;
 //  3. mla_chunk_join_kernel, where the keys are split over CTAs: the parts joined.
@@ -19,11 +19,10 @@ constexpr int kQ = 128;     // queries of a CTA, keys of a tile
 struct ExpandParams {
     CUtensorMap tc;         // the pool: [token][rank + 64]
     CUtensorMap tw;         // weights: [head, row][rank]
+    CUtensorMap tk, tv;     // keys, values: [head, token][D], boxes of 32 tokens x 64
     const __half* pool;
     const int32_t* table;
     const int32_t* position;
-    __half* k;              // [H][cap][D]
-    __half* v;              // [H][cap][D]
     __half* turned;         // [cap][64]
     int* live;              // [cap / 128]: a bit per block of 16 tokens: it is in the pool
     long long maxb, num_blocks, cap;
@@ -38,124 +37,191 @@ __device__ __forceinline__ long long context(const int32_t* position, int n, lon
     return p >= 0 && p + n <= maxb * kBlock ? p + n : 0;
 }
 
+// A pair of CTAs multiplies 256 tokens (128 in each) with 256 weight rows (half of them in each): 64 bytes a cycle and SM
+// of operands read from shared memory, where a CTA alone reads 96 beside the 128 that it would have to take in from L2 (one CTA a
+// product of 128 x 256: 53.6 us for 4096 tokens and 32 heads, bound by L2). The tokens stay in shared memory for all the heads of
+// a pair's share of the work; the weights stream through a ring.
 template <int D, int R>
 struct ExpandCfg {
-    static constexpr int HEADS = 128 / D;                  // heads of a CTA: 256 outputs
+    static constexpr int HEADS = 128 / D;                  // heads of a product: 256 outputs
     static constexpr int KC = R / 64;                      // runs of 64 latent values
-    static constexpr int STAGES = 2, AB = 128 * 128, BB = 256 * 128;
-    static constexpr size_t SMEM = (size_t)STAGES * (AB + BB);
-    static constexpr int kFull = 0, kEmpty = STAGES, kDone = 2 * STAGES, kBars = kDone + 1;
+    static constexpr int STAGES = R == 512 ? 5 : 8, AB = 128 * 128, BB = 128 * 128, OB = 32 * 128;   // OB: 64 outputs of a warp's 32 tokens
+    static constexpr size_t SMEM = (size_t)KC * AB + (size_t)STAGES * BB + 4 * OB;
+    // what has landed in either CTA is reported to rank 0's barriers, what has been read to both CTAs'
+    static constexpr int kAFull = 0, kBFull = KC, kBEmpty = kBFull + STAGES, kAEmpty = kBEmpty + STAGES, kDFull = kAEmpty + 1, kDEmpty = kDFull + 2, kDone = kDEmpty + 2, kBars = kDone + 1;
+    static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
 
 template <int D, int R>
-__global__ void __launch_bounds__(192, 2) mla_expand_kernel(const __grid_constant__ ExpandParams p) {
+__global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_kernel(const __grid_constant__ ExpandParams p) {
     using C = ExpandCfg<D, R>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
-    const int h0 = blockIdx.x * C::HEADS;
-    const long long t0 = (long long)blockIdx.y * 128;
-    const uint32_t bar = su32(bars), as = su32(smem), bs = as + C::STAGES * C::AB;
-    pdl_wait();
-    const long long L = context(p.position, p.n, p.maxb);
-    if (L == 0 && t == 0 && blockIdx.x == 0 && blockIdx.y == 0) record_device_error(p.err, kErrAttnLength, 0, __ldg(p.position));
-    if (t0 >= L) return;
+    const uint32_t rank = cluster_rank();
+    const uint32_t bar = su32(bars), as = su32(smem), bs = as + C::KC * C::AB;
     if (t == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            bar_init(bar + (C::kFull + s) * 8, 1);
-            bar_init(bar + (C::kEmpty + s) * 8, 1);
-        }
-        bar_init(bar + C::kDone * 8, 1);
+        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kDEmpty || i == C::kDEmpty + 1 ? 8 : 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.tc);
+        prefetch_map(&p.tw);
     }
-    if (warp == 5) tmem_alloc<256>(&tmem_at);
+    if (warp == 5) tmem_alloc2<512>(&tmem_at);
     fence_before();
     __syncthreads();
+    cluster_sync();
     fence_after();
-    pdl_trigger();   // not before this CTA has its tensor memory: the attention, which takes all of it, waits for this grid's end
     const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
     const Waits wt = {p.err, &abort_flag, p.ns};
     const Waits alone = {p.err, nullptr, p.ns};
+    pdl_wait();
+    pdl_trigger();   // not before this CTA has its tensor memory: the attention, which takes all of it, waits for this grid's end
+    const long long L = context(p.position, p.n, p.maxb);
+    if (L == 0 && t == 0 && blockIdx.x == 0) record_device_error(p.err, kErrAttnLength, 0, __ldg(p.position));
+    // this pair's run of (256 tokens, 256 outputs), the tokens outside
+    const int hgs = (p.H + C::HEADS - 1) / C::HEADS, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const long long units = (L + 255) / 256 * hgs;
+    const long long u0 = __shfl_sync(0xffffffffu, units * pair / pairs, 0), u1 = __shfl_sync(0xffffffffu, units * (pair + 1) / pairs, 0);
+
+    const uint32_t there = in_cta(bar, 0);
     if (warp == 4) {
-        // ------------------------------------------------ copies: a block of 16 tokens a lane, the weights by lane 8
-        const long long nblk = (L + kBlock - 1) / kBlock, at = t0 / kBlock + lane;
-        int id = -1;
-        bool live = false;
-        if (lane < 8 && at < nblk) {
-            id = __ldg(p.table + at);
-            live = id >= 0 && id < p.num_blocks;
-            if (!live && blockIdx.x == 0) record_device_error(p.err, kErrAttnBlock, at, id);
+        // ------------------------------------------------ copies: a block of 16 tokens a lane, the weights by lane 0
+        const long long nblk = (L + kBlock - 1) / kBlock;
+        long long held = -1;
+        int loads = 0, it = 0;
+        bool ok = true;
+        for (long long u = u0; u < u1 && ok; ++u) {
+            const long long tp = u / hgs;
+            const int hg = (int)(u - tp * hgs);
+            const bool fresh = tp != held;
+            int row = 0;
+            if (fresh) {
+                const long long at = tp * 16 + 8 * rank + lane;
+                bool live = false;
+                int id = -1;
+                if (lane < 8 && at < nblk) {
+                    id = __ldg(p.table + at);
+                    live = id >= 0 && id < p.num_blocks;
+                    if (!live && hg == 0) record_device_error(p.err, kErrAttnBlock, at, id);
+                }
+                const unsigned mask = __ballot_sync(0xffffffffu, live);
+                if (lane == 0 && hg == 0) p.live[2 * tp + rank] = (int)mask;
+                row = live ? id * kBlock : (int)(p.num_blocks * kBlock);   // outside: zeros
+                if (loads > 0) ok = warp_wait(bar + C::kAEmpty * 8, (uint32_t)(loads - 1) & 1u, wt, 700);
+                if (!ok) break;
+                held = tp;
+                ++loads;
+            }
+            for (int c = 0; c < C::KC; ++c, ++it) {
+                const int s = it % C::STAGES;
+                if (fresh) {
+                    if (lane == 0 && rank == 0) bar_expect(bar + (C::kAFull + c) * 8, 2 * C::AB);
+                    __syncwarp();
+                    if (lane < 8) copy2_box2(as + c * C::AB + lane * 2048, &p.tc, 64 * c, row, there + (C::kAFull + c) * 8);
+                }
+                ok = ok && (it < C::STAGES || warp_wait(bar + (C::kBEmpty + s) * 8, (uint32_t)(it / C::STAGES - 1) & 1u, wt, 701));
+                if (lane == 0) {   // (after an abort the unit's copies still go out, so that they can be waited for)
+                    if (rank == 0) bar_expect(bar + (C::kBFull + s) * 8, 2 * C::BB);
+                    copy2_box2(bs + s * C::BB, &p.tw, 64 * c, hg * 256 + 128 * rank, there + (C::kBFull + s) * 8);
+                }
+                __syncwarp();
+            }
         }
-        const unsigned mask = __ballot_sync(0xffffffffu, live);
-        if (blockIdx.x == 0 && lane == 0) p.live[blockIdx.y] = (int)mask;
-        const int row = live ? id * kBlock : (int)(p.num_blocks * kBlock);   // outside: zeros
-        int c = 0;
-        for (; c < C::KC; ++c) {
-            const int s = c % C::STAGES;
-            if (c >= C::STAGES && !warp_wait(bar + (C::kEmpty + s) * 8, (uint32_t)(c / C::STAGES - 1) & 1u, wt, 700)) break;
-            if (lane == 0) bar_expect(bar + (C::kFull + s) * 8, C::AB + C::BB);
-            __syncwarp();
-            if (lane < 8) copy_box2(as + s * C::AB + lane * 2048, &p.tc, 64 * c, row, bar + (C::kFull + s) * 8);
-            else if (lane == 8) copy_box2(bs + s * C::BB, &p.tw, 64 * c, h0 * 2 * D, bar + (C::kFull + s) * 8);
+        if (!ok && rank == 0) {   // (the barriers of rank 0 know of both CTAs' copies)
+            for (int c = 0; loads > 0 && c < C::KC; ++c) warp_wait(bar + (C::kAFull + c) * 8, (uint32_t)(loads - 1) & 1u, alone, 702);
+            for (int i = max(0, it - C::STAGES); i < it; ++i) warp_wait(bar + (C::kBFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 703);
         }
-        if (c < C::KC && lane == 0)   // after an abort: the copies in flight land
-            for (int i = max(0, c - C::STAGES); i < c; ++i) bar_wait(bar + (C::kFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 701);
-        __syncwarp();
     } else if (warp == 5) {
-        // ------------------------------------------------ products
-        constexpr uint32_t I = instr(128, 256, false, false);
+        // ------------------------------------------------ products of both CTAs, issued by rank 0
+        constexpr uint32_t I = instr(256, 256, false, false);
         const uint32_t one = elect_one();
         const uint64_t ad = operand(as, 16, 1024, 2), bd = operand(bs, 16, 1024, 2);
-        for (int c = 0; c < C::KC; ++c) {
-            const int s = c % C::STAGES;
-            if (!warp_wait(bar + (C::kFull + s) * 8, (uint32_t)(c / C::STAGES) & 1u, wt, 702)) break;
-            fence_after();
+        long long held = -1;
+        int loads = 0, it = 0, n = 0;
+        bool ok = rank == 0;
+        for (long long u = u0; u < u1 && ok; ++u, ++n) {
+            const long long tp = u / hgs;
+            const bool fresh = tp != held;
+            if (fresh) ++loads;
+            held = tp;
+            if (n >= 2) ok = warp_wait(bar + (C::kDEmpty + (n & 1)) * 8, (uint32_t)((n >> 1) - 1) & 1u, wt, 710);
+            for (int c = 0; c < C::KC && ok; ++c, ++it) {
+                const int s = it % C::STAGES;
+                if (fresh) ok = warp_wait(bar + (C::kAFull + c) * 8, (uint32_t)(loads - 1) & 1u, wt, 711);
+                ok = ok && warp_wait(bar + (C::kBFull + s) * 8, (uint32_t)(it / C::STAGES) & 1u, wt, 712);
+                if (!ok) break;
+                fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_ss(one, tb, ad + ((s * C::AB + 32 * k) >> 4), bd + ((s * C::BB + 32 * k) >> 4), I, c > 0 || k > 0);
-            mma_commit(one, bar + (C::kEmpty + s) * 8);
+                for (int k = 0; k < 4; ++k)
+                    mma2_ss(one, tb + 256 * (n & 1), ad + ((c * C::AB + 32 * k) >> 4), bd + ((s * C::BB + 32 * k) >> 4), I, c > 0 || k > 0);
+                mma2_commit(one, bar + (C::kBEmpty + s) * 8);
+            }
+            if (!ok) break;
+            mma2_commit(one, bar + (C::kDFull + (n & 1)) * 8);
+            if (u + 1 < u1 && (u + 1) / hgs != tp) mma2_commit(one, bar + C::kAEmpty * 8);
         }
-        mma_commit(one, bar + C::kDone * 8);
-        warp_wait(bar + C::kDone * 8, 0u, alone, 703);
+        if (rank == 0) {
+            mma2_commit(one, bar + C::kDone * 8);
+            warp_wait(bar + C::kDone * 8, 0u, alone, 715);
+        }
     } else {
         // ------------------------------------------------ a token a thread: its 256 outputs rounded and stored
-        const long long tok = t0 + 32 * warp + lane;
-        const bool in = tok < L;   // rows behind the context are zeros: what its last block holds there must not meet the weights
-        if (blockIdx.x == 0) {     // the rotated part as it is
-            const long long at = tok / kBlock;
-            const int id = in ? __ldg(p.table + at) : -1;
-            const bool live = id >= 0 && id < p.num_blocks;
-            const uint4* src = reinterpret_cast<const uint4*>(p.pool + ((long long)(live ? id : 0) * kBlock + tok % kBlock) * (R + kRope) + R);
-            uint4* dst = reinterpret_cast<uint4*>(p.turned + tok * kRope);
+        unsigned char* stage = smem + C::KC * C::AB + C::STAGES * C::BB + warp * C::OB + lane * 128;
+        int n = 0;
+        for (long long u = u0; u < u1; ++u, ++n) {
+            const long long tp = u / hgs, tok = tp * 256 + 128 * rank + 32 * warp + lane;
+            const int hg = (int)(u - tp * hgs), b = n & 1;
+            const bool in = tok < L;   // rows behind the context are zeros: what its last block holds there must not meet the weights
+            if (hg == 0) {             // the rotated part as it is
+                const long long at = tok / kBlock;
+                const int id = in ? __ldg(p.table + at) : -1;
+                const bool live = id >= 0 && id < p.num_blocks;
+                const uint4* src = reinterpret_cast<const uint4*>(p.pool + ((long long)(live ? id : 0) * kBlock + tok % kBlock) * (R + kRope) + R);
+                uint4* dst = reinterpret_cast<uint4*>(p.turned + tok * kRope);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        warp_wait(bar + C::kDone * 8, 0u, wt, 704);
-        fence_after();
+                for (int i = 0; i < 8; ++i) dst[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (!warp_wait(bar + (C::kDFull + b) * 8, (uint32_t)(n >> 1) & 1u, wt, 720)) break;
+            fence_after();
+            const uint32_t acc = tb + 256 * b + ((uint32_t)(32 * warp) << 16);
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {   // 32 outputs
-            float f[32];
-            tmem_ld32(tb + ((uint32_t)(32 * warp) << 16) + 32 * c, f);
-            wait_ld();
-            tie32(f);
-            const int h = h0 + 32 * c / (2 * D), e = 32 * c % (2 * D);
-            if (h >= p.H) break;
-            __half* dst = (e < D ? p.k : p.v) + ((long long)h * p.cap + tok) * D + e % D;
+            for (int c = 0; c < 4; ++c) {   // 64 outputs: rounded into shared memory, copied out from there
+                float f[64];
+                tmem_ld32(acc + 64 * c, f);
+                tmem_ld32(acc + 64 * c + 32, f + 32);
+                wait_ld();
+                tie32(f);
+                tie32(f + 32);
+                const int h = hg * C::HEADS + 64 * c / (2 * D), e = 64 * c % (2 * D);
+                if (h >= p.H) break;
+                if (lane == 0) stores_read();   // the copy before this one
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4*>(dst)[i] = in ? make_uint4(pack_half(f[8 * i], f[8 * i + 1]), pack_half(f[8 * i + 2], f[8 * i + 3]),
-                                                                   pack_half(f[8 * i + 4], f[8 * i + 5]), pack_half(f[8 * i + 6], f[8 * i + 7]))
-                                                      : make_uint4(0u, 0u, 0u, 0u);
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(stage + ((i ^ (lane & 7)) << 4)) =
+                        in ? make_uint4(pack_half(f[8 * i], f[8 * i + 1]), pack_half(f[8 * i + 2], f[8 * i + 3]), pack_half(f[8 * i + 4], f[8 * i + 5]),
+                                        pack_half(f[8 * i + 6], f[8 * i + 7]))
+                           : make_uint4(0u, 0u, 0u, 0u);
+                fence_async();
+                __syncwarp();
+                if (lane == 0) store_box2(e < D ? &p.tk : &p.tv, e % D, (int)((long long)h * p.cap + tok), su32(stage));
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_cluster(there + (C::kDEmpty + b) * 8);
         }
+        if (lane == 0) stores_done();
+        __syncwarp();
     }
     fence_before();
     __syncthreads();
+    cluster_sync();   // no product, report or commit is left that touches the other CTA
     if (warp == 5) {
         fence_after();
-        tmem_free<256>(tb);
+        tmem_free2<512>(tb);
     }
 }
 
@@ -454,7 +520,7 @@ struct ChunkShape {
 };
 static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     ChunkShape s = {};
-    s.cap = (maxb * kBlock + kQ - 1) / kQ * kQ;
+    s.cap = (maxb * kBlock + 255) / 256 * 256;
     // keys split over CTAs where queries and heads give too few for the SMs: up to two a SM, at least 4 tiles each
     const int64_t ctas = (n + kQ - 1) / kQ * H, tiles = s.cap / kQ;
     s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(ctas >= 152 ? 1 : 304 / ctas, tiles / 4));
@@ -497,7 +563,7 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     }
     {
         const uint64_t d[2] = {R, (uint64_t)a.H * 2 * D}, st[1] = {R * 2};
-        const uint32_t b[2] = {64, 256};
+        const uint32_t b[2] = {64, 128};
         if (int rc = f16_tensor_map(a.w, 2, d, st, b, &ep.tw)) return rc;
     }
     {
@@ -510,6 +576,9 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
         const uint32_t b[2] = {64, kQ};
         if (int rc = f16_tensor_map(ws, 2, d, st, b, &cp.tk)) return rc;
         if (int rc = f16_tensor_map(ws + sh.v, 2, d, st, b, &cp.tv)) return rc;
+        const uint32_t o[2] = {64, 32};
+        if (int rc = f16_tensor_map(ws, 2, d, st, o, &ep.tk)) return rc;
+        if (int rc = f16_tensor_map(ws + sh.v, 2, d, st, o, &ep.tv)) return rc;
     }
     {
         const uint64_t d[2] = {kRope, (uint64_t)sh.cap}, st[1] = {kRope * 2};
@@ -519,8 +588,6 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     ep.pool = static_cast<const __half*>(a.pool);
     ep.table = a.table;
     ep.position = cp.position = a.position;
-    ep.k = reinterpret_cast<__half*>(ws);
-    ep.v = reinterpret_cast<__half*>(ws + sh.v);
     ep.turned = reinterpret_cast<__half*>(ws + sh.turned);
     ep.live = reinterpret_cast<int*>(ws + sh.live);
     cp.live = ep.live;
@@ -536,8 +603,29 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     cp.stats = reinterpret_cast<float2*>(ws + sh.stats);
     cp.splits = sh.splits;
     cp.scale_log2 = a.scale * 1.44269504088896340736f;
-    cudaError_t e = launch(mla_expand_kernel<D, R>, dim3((unsigned)((a.H + E::HEADS - 1) / E::HEADS), (unsigned)(sh.cap / 128)), dim3(192), E::SMEM, s,
-                           true, ep);
+    // as many pairs as the GPU holds at once, and as there can be work for
+    static std::atomic<int> most[64];
+    int dev = 0, pairs = 0;
+    QL_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 64) pairs = most[dev].load();
+    if (pairs == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(192);
+        cfg.dynamicSmemBytes = E::SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        QL_TRY_CUDA(cudaOccupancyMaxActiveClusters(&pairs, mla_expand_kernel<D, R>, &cfg));
+        if (pairs < 1) return set_error(QL_ECUDA, "ql_mla_attn_chunk: the GPU holds no pair of CTAs of the product");
+        if (dev < 64) most[dev].store(pairs);
+    }
+    const int64_t work = sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS);
+    if (pairs > work) pairs = (int)work;
+    cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(192), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
         e = launch(mla_chunk_kernel<D>, dim3((unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + kQ - 1) / kQ)), dim3(320), C::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.splits > 1)

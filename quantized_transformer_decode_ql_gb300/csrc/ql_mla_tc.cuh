@@ -66,6 +66,14 @@ __device__ __forceinline__ void copy_box4(uint32_t dst, const CUtensorMap* m, in
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(mb) : "memory");
 }
+// from shared memory; the issuing thread's copies so far have been read, or have arrived
+__device__ __forceinline__ void store_box2(const CUtensorMap* m, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x),
+                 "r"(y), "r"(src) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
@@ -101,6 +109,46 @@ __device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uin
 __device__ __forceinline__ void mma_commit(uint32_t one, uint32_t mb) {
     asm volatile("{\n .reg .pred pe;\n setp.ne.u32 pe, %1, 0;\n"
                  " @pe tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(mb), "r"(one) : "memory");
+}
+// ---- pairs of CTAs (clusters of two): one product of 256 rows, 128 of them in each CTA, as is each half of B's rows and of the result
+template <uint32_t COLS>
+__device__ __forceinline__ void tmem_alloc2(uint32_t* at) {   // by one whole warp of both CTAs
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(at)), "r"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+template <uint32_t COLS>
+__device__ __forceinline__ void tmem_free2(uint32_t base) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(COLS) : "memory");
+}
+__device__ __forceinline__ void mma2_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
+                 " @pe tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, pa;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
+}
+// arrives on the barrier of this address in both CTAs
+__device__ __forceinline__ void mma2_commit(uint32_t one, uint32_t mb) {
+    asm volatile("{\n .reg .pred pe;\n .reg .b16 m;\n setp.ne.u32 pe, %1, 0;\n mov.b16 m, 3;\n"
+                 " @pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(mb), "r"(one) : "memory");
+}
+// a copy into this CTA that reports to a barrier of the pair
+__device__ __forceinline__ void copy2_box2(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t mb) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(mb) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t mb) {   // mb: an address in the cluster
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mb) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
