@@ -1253,6 +1253,7 @@ int f16_rows_tensor_map(const void* base, uint64_t inner, uint64_t outer, uint32
 }
 
 int f16_tensor_map(const void* base, int nd, const uint64_t* dims, const uint64_t* strides, const uint32_t* box, CUtensorMap* map) {
+    const bool narrow = box[0] == 32;
     const EncodeTiledFn enc = encode_tiled();
     if (enc == nullptr) return set_error(QL_ECUDA, "tensor map: cuTensorMapEncodeTiled is not available");
     cuuint64_t d[5], st[4];
@@ -1264,8 +1265,8 @@ int f16_tensor_map(const void* base, int nd, const uint64_t* dims, const uint64_
         if (i + 1 < nd) st[i] = strides[i];
     }
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)nd, const_cast<void*>(base), d, st, b, one,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? QL_OK : set_error(QL_ECUDA, "tensor map: encoding failed (" + std::to_string((int)r) + ")");
 }
 

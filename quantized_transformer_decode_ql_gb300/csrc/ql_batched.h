@@ -30,7 +30,7 @@ int f16_rows_tensor_map(const void* base, uint64_t inner, uint64_t outer, uint32
                         CUtensorMap* map, bool swizzle128);
 
 // An f16 tensor of nd <= 5 dimensions, the first contiguous, the others `strides` bytes apart (nd - 1 of them, any
-// order), in boxes whose inner 64 elements land with the 128-byte swizzle; reads outside return zero.
+// order), in boxes whose inner 64 (32) elements land with the 128-byte (64-byte) swizzle; reads outside return zero.
 int f16_tensor_map(const void* base, int nd, const uint64_t* dims, const uint64_t* strides, const uint32_t* box, CUtensorMap* map);
 
 // The prompt GEMM (ql_gemm.cu): y[t][r] = sum_k W[r][k] x16[t][k] for t < T over the tile stream

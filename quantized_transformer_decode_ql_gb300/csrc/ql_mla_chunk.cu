@@ -2,8 +2,8 @@
 //
 //  1. mla_expand_kernel: every head's keys k = Wk_h c and values v = Wv_h c of the whole context, f16, by a tcgen05 product over
 //     the cache's rows (256 tokens x 256 outputs a pair of CTAs), and the rotated key parts laid out beside them;
-//  2. mla_chunk_kernel: causal attention of 128 queries of one head, the online softmax over tiles of 128 keys in two
-//     independent halves of the tiles (even and odd), so that one half's products run beside the other's weights;
+//  2. mla_chunk_kernel: causal attention of 256 queries of one head by a pair of CTAs, the online softmax over tiles of 128 keys in
+//     two independent halves of the tiles (even and odd), so that one half's products run beside the other's weights;
 //  3. mla_chunk_join_kernel, where the keys are split over CTAs: the parts joined.
 #include "ql_batched.h"
 #include "ql_mla_tc.cuh"
@@ -243,37 +243,37 @@ struct ChunkParams {
     unsigned long long ns;
 };
 
+// A pair of CTAs takes 256 queries of one head, 128 in each, and shares every tile of keys and values: each CTA brings 64 of a
+// tile's 128 keys and half of its values' columns. A CTA alone takes 80 KB from L2 for every 10.5 MFLOP, and 152 of them
+// are held up by L2 (1.4 us a tile of 128 queries and 128 keys; its products take 0.66).
 template <int D>
 struct ChunkCfg {
     static constexpr int CH = (D + kRope) / 64, RUN = kQ * 128;      // a run of 64 values of 128 rows
-    static constexpr int QB = CH * RUN, KB = CH * RUN, VB = D / 64 * RUN;
-    static constexpr size_t SMEM = QB + 2 * KB + 2 * VB;
+    static constexpr int KRUN = 64 * 128, STAGES = 4;
+    static constexpr int QB = CH * RUN, KB = CH * KRUN, VB = kQ * D; // V: 128 keys x D / 2 columns
+    static constexpr size_t SMEM = QB + STAGES * (KB + VB);
     static constexpr uint32_t OCOL = 256, COLS = 512;                // tensor memory: two S (P over them), two O
-    static constexpr int kQFull = 0, kKFull = 1, kKEmpty = 3, kVFull = 5, kVEmpty = 7, kSFull = 9, kPReady = 11, kDone = 13, kBars = 14;
+    // what has landed in either CTA, and the weights of both, are reported to rank 0's barriers, what the products have read or
+    // written to both CTAs'
+    static constexpr int kQFull = 0, kKFull = 1, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
+                         kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kDone = kPReady + 2, kBars = kDone + 1;
 };
 
 template <int D>
-__global__ void __launch_bounds__(320, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = ChunkCfg<D>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
-    __shared__ int abort_flag, live[2];
+    __shared__ int abort_flag;
     __shared__ float2 half[2][kQ];
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
-    const int split = blockIdx.x, h = blockIdx.y, q0 = (gridDim.z - 1 - blockIdx.z) * kQ;   // the longest rows first
-    const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + 2 * C::KB;
+    const uint32_t rank = cluster_rank();
+    const int split = blockIdx.x / 2, h = blockIdx.y, pair0 = (gridDim.z - 1 - blockIdx.z) * 2 * kQ;   // the longest rows first
+    const int q0 = pair0 + rank * kQ;
+    const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + C::STAGES * C::KB;
     if (t == 0) {
-        bar_init(bar + C::kQFull * 8, 1);
-        for (int s = 0; s < 2; ++s) {
-            bar_init(bar + (C::kKFull + s) * 8, 1);
-            bar_init(bar + (C::kKEmpty + s) * 8, 1);
-            bar_init(bar + (C::kVFull + s) * 8, 1);
-            bar_init(bar + (C::kVEmpty + s) * 8, 1);
-            bar_init(bar + (C::kSFull + s) * 8, 1);
-            bar_init(bar + (C::kPReady + s) * 8, 4);
-        }
-        bar_init(bar + C::kDone * 8, 1);
+        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 ? 8 : 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tq);
@@ -281,103 +281,103 @@ __global__ void __launch_bounds__(320, 1) mla_chunk_kernel(const __grid_constant
         prefetch_map(&p.tv);
         prefetch_map(&p.tt);
     }
-    if (warp == 9) tmem_alloc<C::COLS>(&tmem_at);
+    if (warp == 9) tmem_alloc2<C::COLS>(&tmem_at);
     fence_before();
     __syncthreads();
+    cluster_sync();
     fence_after();
-    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
+    const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0), there = in_cta(bar, 0);
     const Waits wt = {p.err, &abort_flag, p.ns};
     const Waits alone = {p.err, nullptr, p.ns};
     pdl_wait();
     pdl_trigger();
     const long long L = context(p.position, p.n, p.maxb);
-    const int before = (int)(L - p.n), rows = min(kQ, p.n - q0);
-    const int all = L ? (before + q0 + rows + kQ - 1) / kQ : 0;    // tiles that the last of these queries sees
+    const int before = (int)(L - p.n), rows = min(kQ, p.n - q0);   // (none, or fewer, of the last pair)
+    const int all = L ? (before + min(pair0 + 2 * kQ, p.n) + kQ - 1) / kQ : 0;    // tiles that the last of the pair's queries sees
     const int per = (all + p.splits - 1) / p.splits, j0 = min(split * per, all);
     const int tiles = __shfl_sync(0xffffffffu, min(per, all - j0), 0);
 
     if (warp == 8) {
-        // ------------------------------------------------ copies
+        // ------------------------------------------------ copies: this CTA's queries and its halves of the tiles
         if (lane == 0 && tiles > 0) {
-            bar_expect(bar + C::kQFull * 8, C::QB);
-            for (int c = 0; c < C::CH; ++c) copy_box3(qs + c * C::RUN, &p.tq, 64 * c, q0, h, bar + C::kQFull * 8);
-            int j = 0, mask = __ldg(p.live + j0);
+            if (rank == 0) bar_expect(bar + C::kQFull * 8, 2 * C::QB);
+            for (int c = 0; c < C::CH; ++c) copy2_box3(qs + c * C::RUN, &p.tq, 64 * c, q0, h, there + C::kQFull * 8);
             bool ok = true;
-            for (; j < tiles; ++j) {
-                const int s = j & 1, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
-                const uint32_t ph = (uint32_t)((j >> 1) - 1) & 1u;
-                if (j >= 2 && !bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800)) {
-                    ok = false;
-                    break;
-                }
-                bar_expect(bar + (C::kKFull + s) * 8, C::KB);
-                for (int c = 0; c < D / 64; ++c) copy_box2(ks + s * C::KB + c * C::RUN, &p.tk, 64 * c, row, bar + (C::kKFull + s) * 8);
-                copy_box2(ks + s * C::KB + D / 64 * C::RUN, &p.tt, 0, at, bar + (C::kKFull + s) * 8);
-                if (j >= 2 && !bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801)) {
-                    ok = false;
-                    break;
-                }
-                live[s] = mask;
-                if (j + 1 < tiles) mask = __ldg(p.live + j0 + j + 1);
-                bar_expect(bar + (C::kVFull + s) * 8, C::VB);
-                for (int c = 0; c < D / 64; ++c) copy_box2(vs + s * C::VB + c * C::RUN, &p.tv, 64 * c, row, bar + (C::kVFull + s) * 8);
+            int j = 0;
+            for (; j < tiles && ok; ++j) {
+                const int s = j % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
+                const uint32_t ph = (uint32_t)(j / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
+                ok = j < C::STAGES || bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800);
+                if (rank == 0) bar_expect(bar + (C::kKFull + s) * 8, 2 * C::KB);
+                for (int c = 0; c < D / 64; ++c) copy2_box2(ks + s * C::KB + c * C::KRUN, &p.tk, 64 * c, row + 64 * rank, kf);
+                copy2_box2(ks + s * C::KB + D / 64 * C::KRUN, &p.tt, 0, at + 64 * rank, kf);
+                ok = ok && (j < C::STAGES || bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801));
+                if (rank == 0) bar_expect(bar + (C::kVFull + s) * 8, 2 * C::VB);
+                copy2_box2(vs + s * C::VB, &p.tv, D / 2 * rank, row, vf);
             }
-            if (!ok) {   // the copies in flight land before the CTA leaves
+            if (!ok && rank == 0) {   // (after an abort) the copies in flight land before the pair leaves; these barriers know of both CTAs'
                 bar_wait(bar + C::kQFull * 8, 0u, alone, 802);
-                for (int i = max(0, j - 2); i < j; ++i) {
-                    bar_wait(bar + (C::kKFull + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, alone, 803);
-                    bar_wait(bar + (C::kVFull + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, alone, 804);
+                for (int i = max(0, j - C::STAGES); i < j; ++i) {
+                    bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 803);
+                    bar_wait(bar + (C::kVFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 804);
                 }
-                bar_wait(bar + (C::kKFull + (j & 1)) * 8, (uint32_t)(j >> 1) & 1u, alone, 805);
             }
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ------------------------------------------------ products: the scores of a tile before the values of the one before it
-        constexpr uint32_t IS = instr(128, kQ, false, false), IO = instr(128, D, false, true);
-        const uint32_t one = elect_one();
-        const uint64_t qd = operand(qs, 16, 1024, 2), kd = operand(ks, 16, 1024, 2), vd = operand(vs, C::RUN, 1024, 2);
-        bool ok = tiles > 0 && warp_wait(bar + C::kQFull * 8, 0u, wt, 810);
-        for (int j = 0; ok && j <= tiles; ++j) {
-            if (j < tiles) {
-                const int s = j & 1;
-                ok = warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(j >> 1) & 1u, wt, 811);
-                if (!ok) break;
-                fence_after();
-                const uint64_t k0 = kd + s * (C::KB >> 4);
+        // ------------------------------------------------ products of both CTAs: the scores of a tile before the values of the one before it
+        if (rank == 0) {
+            constexpr uint32_t IS = instr(2 * kQ, kQ, false, false), IO = instr(2 * kQ, D, false, true);
+            const uint32_t one = elect_one();
+            const uint64_t qd = operand(qs, 16, 1024, 2), kd = operand(ks, 16, 1024, 2);
+            const uint64_t vd = operand(vs, 16, D * 8, D == 128 ? 2 : 4);   // a run of D / 2 columns
+            bool ok = tiles > 0 && warp_wait(bar + C::kQFull * 8, 0u, wt, 810);
+            for (int j = 0; ok && j <= tiles; ++j) {
+                if (j < tiles) {
+                    const int s = j % C::STAGES;
+                    ok = warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 811);
+                    if (!ok) break;
+                    fence_after();
 #pragma unroll
-                for (int k = 0; k < 4 * C::CH; ++k) {
-                    const uint32_t o = ((k >> 2) * C::RUN + (k & 3) * 32) >> 4;
-                    mma_ss(one, tb + s * kQ, qd + o, k0 + o, IS, k > 0);
+                    for (int k = 0; k < 4 * C::CH; ++k)
+                        mma2_ss(one, tb + (j & 1) * kQ, qd + (((k >> 2) * C::RUN + (k & 3) * 32) >> 4),
+                                kd + s * (C::KB >> 4) + (((k >> 2) * C::KRUN + (k & 3) * 32) >> 4), IS, k > 0);
+                    mma2_commit(one, bar + (C::kKEmpty + s) * 8);
+                    mma2_commit(one, bar + (C::kSFull + (j & 1)) * 8);
                 }
-                mma_commit(one, bar + (C::kKEmpty + s) * 8);
-                mma_commit(one, bar + (C::kSFull + s) * 8);
-            }
-            if (j > 0) {
-                const int i = j - 1, s = i & 1;
-                ok = warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i >> 1) & 1u, wt, 812) &&
-                     warp_wait(bar + (C::kPReady + s) * 8, (uint32_t)(i >> 1) & 1u, wt, 813);
-                if (!ok) break;
-                fence_after();
-                const uint64_t v0 = vd + s * (C::VB >> 4);
+                if (j > 0) {
+                    const int i = j - 1, s = i % C::STAGES;
+                    ok = warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i / C::STAGES) & 1u, wt, 812) &&
+                         warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 813);
+                    if (!ok) break;
+                    fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(one, tb + C::OCOL + s * D, tb + s * kQ + 8 * k, v0 + ((k * 2048) >> 4), IO, i >= 2 || k > 0);
-                mma_commit(one, bar + (C::kVEmpty + s) * 8);
+                    for (int k = 0; k < 8; ++k)
+                        mma2_ts(one, tb + C::OCOL + (i & 1) * D, tb + (i & 1) * kQ + 8 * k, vd + s * (C::VB >> 4) + ((k * 16 * D) >> 4), IO,
+                                i >= 2 || k > 0);
+                    mma2_commit(one, bar + (C::kVEmpty + s) * 8);
+                }
             }
+            mma2_commit(one, bar + C::kDone * 8);
+            warp_wait(bar + C::kDone * 8, 0u, alone, 814);
         }
-        mma_commit(one, bar + C::kDone * 8);
-        warp_wait(bar + C::kDone * 8, 0u, alone, 814);
     } else {
         // ------------------------------------------------ softmax: four warps have the even tiles, four the odd ones, a thread a query
         const int g = warp >> 2, q = 32 * (warp & 3) + lane, mine = (tiles + 1 - g) >> 1;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sc = tb + lanes + g * kQ, oc = tb + lanes + C::OCOL + g * D;
         const int last = before + q0 + q;        // the last key this query sees
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+        // the values of this half's tile i - 1 (tile 2 (i - 1) + g of the pair) are in O
+        auto done = [&](int i) {
+            const int j = 2 * (i - 1) + g;
+            warp_wait(bar + (C::kVEmpty + j % C::STAGES) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 822);
+            fence_after();
+        };
         float m = -1e30f, l = 0.f;               // finite where no key is left: the weights stay numbers
+        int mask = mine > 0 ? __ldg(p.live + j0 + g) : 0;
         for (int i = 0; i < mine; ++i) {
-            const int at = (j0 + 2 * i + g) * kQ;
-            warp_wait(bar + (C::kVFull + g) * 8, (uint32_t)i & 1u, wt, 820);   // `live`
-            const int mask = live[g];
+            const int at = (j0 + 2 * i + g) * kQ, now_mask = mask;
+            if (i + 1 < mine) mask = __ldg(p.live + j0 + 2 * i + 2 + g);
             warp_wait(bar + (C::kSFull + g) * 8, (uint32_t)i & 1u, wt, 821);
             fence_after();
             float x[kQ];
@@ -386,61 +386,57 @@ __global__ void __launch_bounds__(320, 1) mla_chunk_kernel(const __grid_constant
             wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) tie32(x + 32 * c);
-            if (at + kQ - 1 > before + q0 || mask != 0xff) {   // the same for the CTA
+            if (at + kQ - 1 > before + q0 || now_mask != 0xff) {   // the same for the CTA
 #pragma unroll
                 for (int c = 0; c < kQ; ++c)
-                    if (at + c > last || !((mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
+                    if (at + c > last || !((now_mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
             }
-            float most = -INFINITY;
+            float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 0; c < kQ; ++c) most = fmaxf(most, x[c]);
-            most *= p.scale_log2;
+            for (int c = 4; c < kQ; ++c) most[c & 3] = fmaxf(most[c & 3], x[c]);
+            const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * p.scale_log2;
             // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
             // smaller ones, and O has to be scaled only when a score passes that.
-            const bool raise = most > m + 8.f;
+            const bool raise = top > m + 8.f;
             if (__any_sync(0xffffffffu, raise)) {
-                const float now = raise ? most : m, f = ex2(m - now);
+                const float now = raise ? top : m, f = ex2(m - now);
                 m = now;
                 l *= f;
                 if (i > 0) {
-                    warp_wait(bar + (C::kVEmpty + g) * 8, (uint32_t)(i - 1) & 1u, wt, 822);   // O holds this half's tiles before
-                    fence_after();
+                    done(i);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         float v[32];
                         uint32_t u[32];
-                        tmem_ld32(oc + 32 * c, v);
-                        wait_ld();
-                        tie32(v);
+                        tmem_load<32>(oc + 32 * c, v);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(v[k] * f);
                         tmem_st32(oc + 32 * c, u);
                     }
                 }
             }
-            float sum[4] = {};
+            const float2 ref = make_float2(-m, -m);
+            float2 sum[4] = {};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t u[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    const float a = ex2(fmaf(x[64 * c + 2 * k], p.scale_log2, -m)), b = ex2(fmaf(x[64 * c + 2 * k + 1], p.scale_log2, -m));
-                    sum[(2 * k) & 3] += a;
-                    sum[(2 * k + 1) & 3] += b;
-                    u[k] = pack_half(a, b);
+                    const float2 e = fma2(make_float2(x[64 * c + 2 * k], x[64 * c + 2 * k + 1]), scale, ref);
+                    const float2 w = make_float2(ex2(e.x), ex2(e.y));
+                    sum[k & 3] = add2(sum[k & 3], w);
+                    u[k] = pack_half(w.x, w.y);
                 }
                 tmem_st32(sc + 32 * c, u);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += s2.x + s2.y;
             wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(bar + (C::kPReady + g) * 8);
+            if (lane == 0) bar_arrive_cluster(there + (C::kPReady + g) * 8);
         }
-        if (mine > 0) {
-            warp_wait(bar + (C::kVEmpty + g) * 8, (uint32_t)(mine - 1) & 1u, wt, 823);
-            fence_after();
-        }
+        if (mine > 0) done(mine);
         half[g][q] = make_float2(m, l);
         fence_before();
         asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
@@ -481,9 +477,10 @@ __global__ void __launch_bounds__(320, 1) mla_chunk_kernel(const __grid_constant
     }
     fence_before();
     __syncthreads();
+    cluster_sync();   // no product, report or commit is left that touches the other CTA
     if (warp == 9) {
         fence_after();
-        tmem_free<C::COLS>(tb);
+        tmem_free2<C::COLS>(tb);
     }
 }
 
@@ -521,9 +518,18 @@ struct ChunkShape {
 static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     ChunkShape s = {};
     s.cap = (maxb * kBlock + 255) / 256 * 256;
-    // keys split over CTAs where queries and heads give too few for the SMs: up to two a SM, at least 4 tiles each
-    const int64_t ctas = (n + kQ - 1) / kQ * H, tiles = s.cap / kQ;
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(ctas >= 152 ? 1 : 304 / ctas, tiles / 4));
+    // Keys split over pairs of CTAs where queries and heads alone give few: what the last wave of 76 pairs and the start of each
+    // (about 3 tiles) cost, for the longest context that the table holds.
+    const int64_t pairs = (n + 2 * kQ - 1) / (2 * kQ) * H, tiles = s.cap / kQ;
+    int64_t best = 0;
+    s.splits = 1;
+    for (int64_t k = 1; k <= 16 && k <= std::max<int64_t>(1, tiles / 4) && (k == 1 || pairs < 152); ++k) {
+        const int64_t cost = (pairs * k + 75) / 76 * ((tiles + k - 1) / k + 3);
+        if (k == 1 || cost < best) {
+            best = cost;
+            s.splits = (int)k;
+        }
+    }
     auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
     s.v = up((size_t)H * s.cap * D * 2);
     s.turned = 2 * s.v;
@@ -573,16 +579,16 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     }
     {
         const uint64_t d[2] = {D, (uint64_t)a.H * sh.cap}, st[1] = {D * 2};
-        const uint32_t b[2] = {64, kQ};
+        const uint32_t b[2] = {64, 64}, v[2] = {D / 2, kQ};
         if (int rc = f16_tensor_map(ws, 2, d, st, b, &cp.tk)) return rc;
-        if (int rc = f16_tensor_map(ws + sh.v, 2, d, st, b, &cp.tv)) return rc;
+        if (int rc = f16_tensor_map(ws + sh.v, 2, d, st, v, &cp.tv)) return rc;
         const uint32_t o[2] = {64, 32};
         if (int rc = f16_tensor_map(ws, 2, d, st, o, &ep.tk)) return rc;
         if (int rc = f16_tensor_map(ws + sh.v, 2, d, st, o, &ep.tv)) return rc;
     }
     {
         const uint64_t d[2] = {kRope, (uint64_t)sh.cap}, st[1] = {kRope * 2};
-        const uint32_t b[2] = {64, kQ};
+        const uint32_t b[2] = {64, 64};
         if (int rc = f16_tensor_map(ws + sh.turned, 2, d, st, b, &cp.tt)) return rc;
     }
     ep.pool = static_cast<const __half*>(a.pool);
@@ -627,7 +633,7 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     if (pairs > work) pairs = (int)work;
     cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(192), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
-        e = launch(mla_chunk_kernel<D>, dim3((unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + kQ - 1) / kQ)), dim3(320), C::SMEM, s, true, cp);
+        e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + 2 * kQ - 1) / (2 * kQ))), dim3(320), C::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.splits > 1)
         e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.n * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");

@@ -124,6 +124,10 @@ __device__ __forceinline__ void mma2_ss(uint32_t one, uint32_t d, uint64_t a, ui
     asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
                  " @pe tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, pa;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
 }
+__device__ __forceinline__ void mma2_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {   // A in tensor memory
+    asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
+                 " @pe tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, pa;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
+}
 // arrives on the barrier of this address in both CTAs
 __device__ __forceinline__ void mma2_commit(uint32_t one, uint32_t mb) {
     asm volatile("{\n .reg .pred pe;\n .reg .b16 m;\n setp.ne.u32 pe, %1, 0;\n mov.b16 m, 3;\n"
@@ -133,6 +137,10 @@ __device__ __forceinline__ void mma2_commit(uint32_t one, uint32_t mb) {
 __device__ __forceinline__ void copy2_box2(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t mb) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(mb) : "memory");
+}
+__device__ __forceinline__ void copy2_box3(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t mb) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(mb) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -144,8 +152,10 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void bar_arrive_cluster(uint32_t mb) {   // mb: an address in the cluster
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mb) : "memory");
+// mb: an address in the cluster. What the arrival reports lies in tensor memory, ordered by the tcgen05 fences around it: a release
+// of the whole cluster's memory is not needed (and takes 1500 cycles).
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t mb) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mb) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
