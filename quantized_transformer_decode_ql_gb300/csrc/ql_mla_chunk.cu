@@ -259,21 +259,23 @@ struct ChunkCfg {
                          kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kDone = kPReady + 2, kBars = kDone + 1;
 };
 
+constexpr int kSoft = 16, kCopy = 16, kProduct = 17, kChunkThreads = 18 * 32;   // warps: softmax, copies, products
+
 template <int D>
-__global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = ChunkCfg<D>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
-    __shared__ float2 half[2][kQ];
+    __shared__ float tops[2][2][kQ], sums[2][2][kQ], refs[2][kQ];
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t rank = cluster_rank();
     const int split = blockIdx.x / 2, h = blockIdx.y, pair0 = (gridDim.z - 1 - blockIdx.z) * 2 * kQ;   // the longest rows first
     const int q0 = pair0 + rank * kQ;
     const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + C::STAGES * C::KB;
     if (t == 0) {
-        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 ? 8 : 1);
+        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 ? kSoft : 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tq);
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
         prefetch_map(&p.tv);
         prefetch_map(&p.tt);
     }
-    if (warp == 9) tmem_alloc2<C::COLS>(&tmem_at);
+    if (warp == kProduct) tmem_alloc2<C::COLS>(&tmem_at);
     fence_before();
     __syncthreads();
     cluster_sync();
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
     const int per = (all + p.splits - 1) / p.splits, j0 = min(split * per, all);
     const int tiles = __shfl_sync(0xffffffffu, min(per, all - j0), 0);
 
-    if (warp == 8) {
+    if (warp == kCopy) {
         // ------------------------------------------------ copies: this CTA's queries and its halves of the tiles
         if (lane == 0 && tiles > 0) {
             if (rank == 0) bar_expect(bar + C::kQFull * 8, 2 * C::QB);
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
             }
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == kProduct) {
         // ------------------------------------------------ products of both CTAs: the scores of a tile before the values of the one before it
         if (rank == 0) {
             constexpr uint32_t IS = instr(2 * kQ, kQ, false, false), IO = instr(2 * kQ, D, false, true);
@@ -362,10 +364,12 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
             warp_wait(bar + C::kDone * 8, 0u, alone, 814);
         }
     } else {
-        // ------------------------------------------------ softmax: four warps have the even tiles, four the odd ones, a thread a query
-        const int g = warp >> 2, q = 32 * (warp & 3) + lane, mine = (tiles + 1 - g) >> 1;
+        // ------------------------------------------------ softmax: eight warps have the even tiles, eight the odd ones; of the eight, four
+        // have keys 0 - 63 of a tile and four the rest; a thread has one query. The eight run the same tiles whatever their waits
+        // return, so that their barriers always meet.
+        const int g = warp >> 3, hf = (warp >> 2) & 1, q = 32 * (warp & 3) + lane, mine = (tiles + 1 - g) >> 1;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sc = tb + lanes + g * kQ, oc = tb + lanes + C::OCOL + g * D;
-        const int last = before + q0 + q;        // the last key this query sees
+        const int last = before + q0 + q - 64 * hf;        // the last key this query sees, counted from this thread's first
         const float2 scale = make_float2(p.scale_log2, p.scale_log2);
         // the values of this half's tile i - 1 (tile 2 (i - 1) + g of the pair) are in O
         auto done = [&](int i) {
@@ -376,42 +380,49 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
         float m = -1e30f, l = 0.f;               // finite where no key is left: the weights stay numbers
         int mask = mine > 0 ? __ldg(p.live + j0 + g) : 0;
         for (int i = 0; i < mine; ++i) {
-            const int at = (j0 + 2 * i + g) * kQ, now_mask = mask;
+            const int at = (j0 + 2 * i + g) * kQ, now_mask = mask >> (4 * hf);
+            const bool whole = mask == 0xff;
             if (i + 1 < mine) mask = __ldg(p.live + j0 + 2 * i + 2 + g);
             warp_wait(bar + (C::kSFull + g) * 8, (uint32_t)i & 1u, wt, 821);
             fence_after();
-            float x[kQ];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x + 32 * c);
+            float x[64];
+            tmem_ld32(sc + 64 * hf, x);
+            tmem_ld32(sc + 64 * hf + 32, x + 32);
             wait_ld();
+            tie32(x);
+            tie32(x + 32);
+            if (at + kQ - 1 > before + q0 || !whole) {   // the same for the CTA
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tie32(x + 32 * c);
-            if (at + kQ - 1 > before + q0 || now_mask != 0xff) {   // the same for the CTA
-#pragma unroll
-                for (int c = 0; c < kQ; ++c)
+                for (int c = 0; c < 64; ++c)
                     if (at + c > last || !((now_mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
             }
             float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < kQ; ++c) most[c & 3] = fmaxf(most[c & 3], x[c]);
-            const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * p.scale_log2;
+            for (int c = 4; c < 64; ++c) most[c & 3] = fmaxf(most[c & 3], x[c]);
+            float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * p.scale_log2;
             // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
             // smaller ones, and O has to be scaled only when a score passes that.
-            const bool raise = top > m + 8.f;
-            if (__any_sync(0xffffffffu, raise)) {
-                const float now = raise ? top : m, f = ex2(m - now);
+            // (The barrier also keeps the weights, which take the scores' place, behind the other four warps' loads.)
+            unsigned raise;
+            asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 256, a;\n selp.u32 %0, 1, 0, b;\n}"
+                         : "=r"(raise) : "r"((unsigned)(top > m + 8.f)), "r"(1 + g) : "memory");
+            if (raise) {
+                tops[g][hf][q] = top;
+                asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + g) : "memory");
+                top = fmaxf(top, tops[g][hf ^ 1][q]);
+                const float now = top > m + 8.f ? top : m, f = ex2(m - now);
                 m = now;
                 l *= f;
                 if (i > 0) {
                     done(i);
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float v[32];
-                        uint32_t u[32];
-                        tmem_load<32>(oc + 32 * c, v);
+                    for (int c = hf * (D / 32); c < (hf + 1) * (D / 32); ++c) {
+                        float v[16];
+                        uint32_t u[16];
+                        tmem_load<16>(oc + 16 * c, v);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(v[k] * f);
-                        tmem_st32(oc + 32 * c, u);
+                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(v[k] * f);
+                        tmem_st16(oc + 16 * c, u);
                     }
                 }
             }
@@ -419,15 +430,15 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
             float2 sum[4] = {};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t u[32];
+                uint32_t u[16];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 e = fma2(make_float2(x[64 * c + 2 * k], x[64 * c + 2 * k + 1]), scale, ref);
+                for (int k = 0; k < 16; ++k) {
+                    const float2 e = fma2(make_float2(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]), scale, ref);
                     const float2 w = make_float2(ex2(e.x), ex2(e.y));
                     sum[k & 3] = add2(sum[k & 3], w);
                     u[k] = pack_half(w.x, w.y);
                 }
-                tmem_st32(sc + 32 * c, u);
+                tmem_st16(sc + 32 * hf + 16 * c, u);
             }
             const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += s2.x + s2.y;
@@ -437,48 +448,47 @@ __global__ void __launch_bounds__(320, 1) __cluster_dims__(2, 1, 1) mla_chunk_ke
             if (lane == 0) bar_arrive_cluster(there + (C::kPReady + g) * 8);
         }
         if (mine > 0) done(mine);
-        half[g][q] = make_float2(m, l);
+        sums[g][hf][q] = l;
+        refs[g][q] = m;          // (the same from both halves of the keys)
         fence_before();
-        asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+        asm volatile("barrier.cta.sync 3, 512;" ::: "memory");
         fence_after();
-        // both halves joined: these warps take half of the values each, of all their lanes' queries
-        const float2 a = half[0][q], b = half[1][q];
-        const float top = fmaxf(a.x, b.x), fa = ex2(a.x - top), fb = ex2(b.x - top), total = a.y * fa + b.y * fb;
+        // both halves of the tiles joined: these warps take a quarter of the values each, of all their lanes' queries
+        const float ma = refs[0][q], mb = refs[1][q], top = fmaxf(ma, mb), fa = ex2(ma - top), fb = ex2(mb - top);
+        const float total = (sums[0][0][q] + sums[0][1][q]) * fa + (sums[1][0][q] + sums[1][1][q]) * fb;
         const bool whole = p.splits == 1;
         const float inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
         const float ca = fa * inv, cb = fb * inv;
+        const int d0 = (2 * g + hf) * (D / 4);
 #pragma unroll 1
-        for (int c = g * (D / 64); c < (g + 1) * (D / 64); ++c) {
-            float x[32], y[32];
+        for (int c = 0; c < D / 64; ++c) {
+            float x[16], y[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = y[k] = 0.f;
-            if (tiles > 0) tmem_ld32(tb + lanes + C::OCOL + 32 * c, x);
-            if (tiles > 1) tmem_ld32(tb + lanes + C::OCOL + D + 32 * c, y);
-            wait_ld();
-            tie32(x);
-            tie32(y);
+            for (int k = 0; k < 16; ++k) x[k] = y[k] = 0.f;
+            if (tiles > 0) tmem_load<16>(tb + lanes + C::OCOL + d0 + 16 * c, x);
+            if (tiles > 1) tmem_load<16>(tb + lanes + C::OCOL + D + d0 + 16 * c, y);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = x[k] * ca + y[k] * cb;
+            for (int k = 0; k < 16; ++k) x[k] = x[k] * ca + y[k] * cb;
             if (q < rows && L) {
-                const size_t o = ((size_t)(q0 + q) * p.H + h) * D + 32 * c;
+                const size_t o = ((size_t)(q0 + q) * p.H + h) * D + d0 + 16 * c;
                 if (whole) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 2; ++k)
                         *reinterpret_cast<uint4*>(p.out + o + 8 * k) = make_uint4(pack_half(x[8 * k], x[8 * k + 1]), pack_half(x[8 * k + 2], x[8 * k + 3]),
                                                                                   pack_half(x[8 * k + 4], x[8 * k + 5]), pack_half(x[8 * k + 6], x[8 * k + 7]));
                 } else {
                     float* dst = p.parts + (size_t)split * p.n * p.H * D + o;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 }
             }
         }
-        if (!whole && g == 0 && q < rows && L) p.stats[((size_t)split * p.n + q0 + q) * p.H + h] = make_float2(top, total);
+        if (!whole && g == 0 && hf == 0 && q < rows && L) p.stats[((size_t)split * p.n + q0 + q) * p.H + h] = make_float2(top, total);
     }
     fence_before();
     __syncthreads();
     cluster_sync();   // no product, report or commit is left that touches the other CTA
-    if (warp == 9) {
+    if (warp == kProduct) {
         fence_after();
         tmem_free2<C::COLS>(tb);
     }
@@ -633,7 +643,7 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     if (pairs > work) pairs = (int)work;
     cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(192), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
-        e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + 2 * kQ - 1) / (2 * kQ))), dim3(320), C::SMEM, s, true, cp);
+        e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + 2 * kQ - 1) / (2 * kQ))), dim3(kChunkThreads), C::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.splits > 1)
         e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.n * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");
