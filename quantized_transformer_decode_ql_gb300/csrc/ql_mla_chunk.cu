@@ -246,6 +246,8 @@ struct ChunkParams {
 // A pair of CTAs takes 256 queries of one head, 128 in each, and shares every tile of keys and values: each CTA brings 64 of a
 // tile's 128 keys and half of its values' columns. A CTA alone takes 80 KB from L2 for every 10.5 MFLOP, and 152 of them
 // are held up by L2 (1.4 us a tile of 128 queries and 128 keys; its products take 0.66).
+// The pairs stay for the whole grid's work. A unit of it is (256 queries, head, part of the keys); units are ordered by their length and
+// dealt out to and fro, so that all pairs end together, and a unit's queries, first tiles and scores arrive while the one before is finished.
 template <int D>
 struct ChunkCfg {
     static constexpr int CH = (D + kRope) / 64, RUN = kQ * 128;      // a run of 64 values of 128 rows
@@ -255,7 +257,7 @@ struct ChunkCfg {
     static constexpr uint32_t OCOL = 256, COLS = 512;                // tensor memory: two S (P over them), two O
     // what has landed in either CTA, and the weights of both, are reported to rank 0's barriers, what the products have read or
     // written to both CTAs'
-    static constexpr int kQFull = 0, kKFull = 1, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
+    static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
                          kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kDone = kPReady + 2, kBars = kDone + 1;
 };
 
@@ -271,8 +273,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     __shared__ float tops[2][2][kQ], sums[2][2][kQ], refs[2][kQ];
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t rank = cluster_rank();
-    const int split = blockIdx.x / 2, h = blockIdx.y, pair0 = (gridDim.z - 1 - blockIdx.z) * 2 * kQ;   // the longest rows first
-    const int q0 = pair0 + rank * kQ;
     const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + C::STAGES * C::KB;
     if (t == 0) {
         for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 ? kSoft : 1);
@@ -294,32 +294,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     pdl_wait();
     pdl_trigger();
     const long long L = context(p.position, p.n, p.maxb);
-    const int before = (int)(L - p.n), rows = min(kQ, p.n - q0);   // (none, or fewer, of the last pair)
-    const int all = L ? (before + min(pair0 + 2 * kQ, p.n) + kQ - 1) / kQ : 0;    // tiles that the last of the pair's queries sees
-    const int per = (all + p.splits - 1) / p.splits, j0 = min(split * per, all);
-    const int tiles = __shfl_sync(0xffffffffu, min(per, all - j0), 0);
+    const int before = (int)(L - p.n);
+    const int blocks = (p.n + 2 * kQ - 1) / (2 * kQ), units = L ? blocks * p.H * p.splits : 0, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+
+    // The units of this pair: `each` gets the head, the first query, the part of the keys, its first tile and their number, and returns
+    // false to stop.
+    auto work = [&](auto each) {
+        for (int k = 0;; ++k) {
+            const int u = k * pairs + (k & 1 ? pairs - 1 - pair : pair);
+            if (u >= units) {
+                if (k * pairs >= units) return;
+                continue;
+            }
+            const int split = u % p.splits, h = u / p.splits % p.H, first = (blocks - 1 - u / p.splits / p.H) * 2 * kQ;
+            const int all = (before + min(first + 2 * kQ, p.n) + kQ - 1) / kQ;    // tiles that the last of the unit's queries sees
+            const int per = (all + p.splits - 1) / p.splits, j0 = min(split * per, all);
+            if (!each(h, first, split, j0, min(per, all - j0))) return;
+        }
+    };
+    int jt = 0, un = 0;   // tiles and units with tiles so far
 
     if (warp == kCopy) {
         // ------------------------------------------------ copies: this CTA's queries and its halves of the tiles
-        if (lane == 0 && tiles > 0) {
-            if (rank == 0) bar_expect(bar + C::kQFull * 8, 2 * C::QB);
-            for (int c = 0; c < C::CH; ++c) copy2_box3(qs + c * C::RUN, &p.tq, 64 * c, q0, h, there + C::kQFull * 8);
+        if (lane == 0) {
             bool ok = true;
-            int j = 0;
-            for (; j < tiles && ok; ++j) {
-                const int s = j % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
-                const uint32_t ph = (uint32_t)(j / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
-                ok = j < C::STAGES || bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800);
-                if (rank == 0) bar_expect(bar + (C::kKFull + s) * 8, 2 * C::KB);
-                for (int c = 0; c < D / 64; ++c) copy2_box2(ks + s * C::KB + c * C::KRUN, &p.tk, 64 * c, row + 64 * rank, kf);
-                copy2_box2(ks + s * C::KB + D / 64 * C::KRUN, &p.tt, 0, at + 64 * rank, kf);
-                ok = ok && (j < C::STAGES || bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801));
-                if (rank == 0) bar_expect(bar + (C::kVFull + s) * 8, 2 * C::VB);
-                copy2_box2(vs + s * C::VB, &p.tv, D / 2 * rank, row, vf);
-            }
+            work([&](int h, int first, int, int j0, int tiles) {
+                if (tiles <= 0) return true;
+                ok = un == 0 || bar_wait(bar + C::kQEmpty * 8, (uint32_t)(un - 1) & 1u, wt, 799);
+                if (!ok) return false;
+                if (rank == 0) bar_expect(bar + C::kQFull * 8, 2 * C::QB);
+                for (int c = 0; c < C::CH; ++c) copy2_box3(qs + c * C::RUN, &p.tq, 64 * c, first + kQ * rank, h, there + C::kQFull * 8);
+                ++un;
+                for (int j = 0; j < tiles && ok; ++j, ++jt) {
+                    const int s = jt % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
+                    const uint32_t ph = (uint32_t)(jt / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
+                    ok = jt < C::STAGES || bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800);
+                    if (rank == 0) bar_expect(bar + (C::kKFull + s) * 8, 2 * C::KB);
+                    for (int c = 0; c < D / 64; ++c) copy2_box2(ks + s * C::KB + c * C::KRUN, &p.tk, 64 * c, row + 64 * rank, kf);
+                    copy2_box2(ks + s * C::KB + D / 64 * C::KRUN, &p.tt, 0, at + 64 * rank, kf);
+                    ok = ok && (jt < C::STAGES || bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801));
+                    if (rank == 0) bar_expect(bar + (C::kVFull + s) * 8, 2 * C::VB);
+                    copy2_box2(vs + s * C::VB, &p.tv, D / 2 * rank, row, vf);
+                }
+                return ok;
+            });
             if (!ok && rank == 0) {   // (after an abort) the copies in flight land before the pair leaves; these barriers know of both CTAs'
-                bar_wait(bar + C::kQFull * 8, 0u, alone, 802);
-                for (int i = max(0, j - C::STAGES); i < j; ++i) {
+                if (un > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(un - 1) & 1u, alone, 802);
+                for (int i = max(0, jt - C::STAGES); i < jt; ++i) {
                     bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 803);
                     bar_wait(bar + (C::kVFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 804);
                 }
@@ -333,33 +354,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
             const uint32_t one = elect_one();
             const uint64_t qd = operand(qs, 16, 1024, 2), kd = operand(ks, 16, 1024, 2);
             const uint64_t vd = operand(vs, 16, D * 8, D == 128 ? 2 : 4);   // a run of D / 2 columns
-            bool ok = tiles > 0 && warp_wait(bar + C::kQFull * 8, 0u, wt, 810);
-            for (int j = 0; ok && j <= tiles; ++j) {
-                if (j < tiles) {
-                    const int s = j % C::STAGES;
-                    ok = warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 811);
-                    if (!ok) break;
-                    fence_after();
+            work([&](int, int, int, int, int tiles_) {
+                const int tiles = __shfl_sync(0xffffffffu, tiles_, 0);
+                if (tiles <= 0) return true;
+                if (!warp_wait(bar + C::kQFull * 8, (uint32_t)un & 1u, wt, 810)) return false;
+                ++un;
+                for (int j = 0; j <= tiles; ++j) {
+                    if (j < tiles) {
+                        const int s = jt % C::STAGES;
+                        if (!warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(jt / C::STAGES) & 1u, wt, 811)) return false;
+                        fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4 * C::CH; ++k)
-                        mma2_ss(one, tb + (j & 1) * kQ, qd + (((k >> 2) * C::RUN + (k & 3) * 32) >> 4),
-                                kd + s * (C::KB >> 4) + (((k >> 2) * C::KRUN + (k & 3) * 32) >> 4), IS, k > 0);
-                    mma2_commit(one, bar + (C::kKEmpty + s) * 8);
-                    mma2_commit(one, bar + (C::kSFull + (j & 1)) * 8);
-                }
-                if (j > 0) {
-                    const int i = j - 1, s = i % C::STAGES;
-                    ok = warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i / C::STAGES) & 1u, wt, 812) &&
-                         warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 813);
-                    if (!ok) break;
-                    fence_after();
+                        for (int k = 0; k < 4 * C::CH; ++k)
+                            mma2_ss(one, tb + (jt & 1) * kQ, qd + (((k >> 2) * C::RUN + (k & 3) * 32) >> 4),
+                                    kd + s * (C::KB >> 4) + (((k >> 2) * C::KRUN + (k & 3) * 32) >> 4), IS, k > 0);
+                        mma2_commit(one, bar + (C::kKEmpty + s) * 8);
+                        mma2_commit(one, bar + (C::kSFull + (jt & 1)) * 8);
+                        if (j + 1 == tiles) mma2_commit(one, bar + C::kQEmpty * 8);
+                        ++jt;
+                    }
+                    if (j > 0) {   // (the tile before: jt - 2, or the last, jt - 1)
+                        const int i = j < tiles ? jt - 2 : jt - 1, s = i % C::STAGES;
+                        if (!warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i / C::STAGES) & 1u, wt, 812)) return false;
+                        if (!warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 813)) return false;
+                        fence_after();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma2_ts(one, tb + C::OCOL + (i & 1) * D, tb + (i & 1) * kQ + 8 * k, vd + s * (C::VB >> 4) + ((k * 16 * D) >> 4), IO,
-                                i >= 2 || k > 0);
-                    mma2_commit(one, bar + (C::kVEmpty + s) * 8);
+                        for (int k = 0; k < 8; ++k)
+                            mma2_ts(one, tb + C::OCOL + (i & 1) * D, tb + (i & 1) * kQ + 8 * k, vd + s * (C::VB >> 4) + ((k * 16 * D) >> 4), IO,
+                                    j > 2 || k > 0);
+                        mma2_commit(one, bar + (C::kVEmpty + s) * 8);
+                    }
                 }
-            }
+                return true;
+            });
             mma2_commit(one, bar + C::kDone * 8);
             warp_wait(bar + C::kDone * 8, 0u, alone, 814);
         }
@@ -367,123 +394,141 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
         // ------------------------------------------------ softmax: eight warps have the even tiles, eight the odd ones; of the eight, four
         // have keys 0 - 63 of a tile and four the rest; a thread has one query. The eight run the same tiles whatever their waits
         // return, so that their barriers always meet.
-        const int g = warp >> 3, hf = (warp >> 2) & 1, q = 32 * (warp & 3) + lane, mine = (tiles + 1 - g) >> 1;
+        const int g = warp >> 3, hf = (warp >> 2) & 1, q = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sc = tb + lanes + g * kQ, oc = tb + lanes + C::OCOL + g * D;
-        const int last = before + q0 + q - 64 * hf;        // the last key this query sees, counted from this thread's first
         const float2 scale = make_float2(p.scale_log2, p.scale_log2);
-        // the values of this half's tile i - 1 (tile 2 (i - 1) + g of the pair) are in O
-        auto done = [&](int i) {
-            const int j = 2 * (i - 1) + g;
-            warp_wait(bar + (C::kVEmpty + j % C::STAGES) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 822);
-            fence_after();
-        };
-        float m = -1e30f, l = 0.f;               // finite where no key is left: the weights stay numbers
-        int mask = mine > 0 ? __ldg(p.live + j0 + g) : 0;
-        for (int i = 0; i < mine; ++i) {
-            const int at = (j0 + 2 * i + g) * kQ, now_mask = mask >> (4 * hf);
-            const bool whole = mask == 0xff;
-            if (i + 1 < mine) mask = __ldg(p.live + j0 + 2 * i + 2 + g);
-            warp_wait(bar + (C::kSFull + g) * 8, (uint32_t)i & 1u, wt, 821);
-            fence_after();
-            float x[64];
-            tmem_ld32(sc + 64 * hf, x);
-            tmem_ld32(sc + 64 * hf + 32, x + 32);
-            wait_ld();
-            tie32(x);
-            tie32(x + 32);
-            if (at + kQ - 1 > before + q0 || !whole) {   // the same for the CTA
+        work([&](int h, int first, int split, int j0, int tiles) {
+            const int q0 = first + kQ * (int)rank, rows = p.n - q0;   // (some, all or none of 128)
+            const int last = before + q0 + q - 64 * hf;        // the last key this query sees, counted from this thread's first
+            const int off = (jt & 1) ^ g;                      // this half's first tile of the unit
+            const int mine = tiles > off ? (tiles - off + 1) >> 1 : 0;
+            // the values up to this half's tile i are in O
+            auto done = [&](int i) {
+                const int j = jt + off + 2 * i;
+                warp_wait(bar + (C::kVEmpty + j % C::STAGES) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 822);
+                fence_after();
+            };
+            float m = -1e30f, l = 0.f;               // finite where no key is left: the weights stay numbers
+            int mask = mine > 0 ? __ldg(p.live + j0 + off) : 0;
+            for (int i = 0; i < mine; ++i) {
+                const int at = (j0 + off + 2 * i) * kQ, now_mask = mask >> (4 * hf), j = jt + off + 2 * i;
+                const bool whole = mask == 0xff;
+                if (i + 1 < mine) mask = __ldg(p.live + j0 + off + 2 * i + 2);
+                warp_wait(bar + (C::kSFull + g) * 8, (uint32_t)(j >> 1) & 1u, wt, 821);
+                fence_after();
+                float x[64];
+                tmem_ld32(sc + 64 * hf, x);
+                tmem_ld32(sc + 64 * hf + 32, x + 32);
+                wait_ld();
+                tie32(x);
+                tie32(x + 32);
+                if (at + kQ - 1 > before + q0 || !whole) {   // the same for the CTA
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (at + c > last || !((now_mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
-            }
-            float most[4] = {x[0], x[1], x[2], x[3]};
+                    for (int c = 0; c < 64; ++c)
+                        if (at + c > last || !((now_mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
+                }
+                float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < 64; ++c) most[c & 3] = fmaxf(most[c & 3], x[c]);
-            float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * p.scale_log2;
-            // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
-            // smaller ones, and O has to be scaled only when a score passes that.
-            // (The barrier also keeps the weights, which take the scores' place, behind the other four warps' loads.)
-            unsigned raise;
-            asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 256, a;\n selp.u32 %0, 1, 0, b;\n}"
-                         : "=r"(raise) : "r"((unsigned)(top > m + 8.f)), "r"(1 + g) : "memory");
-            if (raise) {
-                tops[g][hf][q] = top;
-                asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + g) : "memory");
-                top = fmaxf(top, tops[g][hf ^ 1][q]);
-                const float now = top > m + 8.f ? top : m, f = ex2(m - now);
-                m = now;
-                l *= f;
-                if (i > 0) {
-                    done(i);
+                for (int c = 4; c < 64; ++c) most[c & 3] = fmaxf(most[c & 3], x[c]);
+                float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * p.scale_log2;
+                // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
+                // smaller ones, and O has to be scaled only when a score passes that.
+                // (The barrier also keeps the weights, which take the scores' place, behind the other four warps' loads.)
+                unsigned raise;
+                asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 256, a;\n selp.u32 %0, 1, 0, b;\n}"
+                             : "=r"(raise) : "r"((unsigned)(top > m + 8.f)), "r"(1 + g) : "memory");
+                if (raise) {
+                    tops[g][hf][q] = top;
+                    asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + g) : "memory");
+                    top = fmaxf(top, tops[g][hf ^ 1][q]);
+                    const float now = top > m + 8.f ? top : m, f = ex2(m - now);
+                    m = now;
+                    l *= f;
+                    if (i > 0) {
+                        done(i - 1);
 #pragma unroll 1
-                    for (int c = hf * (D / 32); c < (hf + 1) * (D / 32); ++c) {
-                        float v[16];
-                        uint32_t u[16];
-                        tmem_load<16>(oc + 16 * c, v);
+                        for (int c = hf * (D / 32); c < (hf + 1) * (D / 32); ++c) {
+                            float v[16];
+                            uint32_t u[16];
+                            tmem_load<16>(oc + 16 * c, v);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(v[k] * f);
-                        tmem_st16(oc + 16 * c, u);
+                            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(v[k] * f);
+                            tmem_st16(oc + 16 * c, u);
+                        }
                     }
                 }
-            }
-            const float2 ref = make_float2(-m, -m);
-            float2 sum[4] = {};
+                const float2 ref = make_float2(-m, -m);
+                float2 sum[4] = {};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t u[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t u[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 e = fma2(make_float2(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]), scale, ref);
-                    const float2 w = make_float2(ex2(e.x), ex2(e.y));
-                    sum[k & 3] = add2(sum[k & 3], w);
-                    u[k] = pack_half(w.x, w.y);
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 e = fma2(make_float2(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]), scale, ref);
+                        const float2 w = make_float2(ex2(e.x), ex2(e.y));
+                        sum[k & 3] = add2(sum[k & 3], w);
+                        u[k] = pack_half(w.x, w.y);
+                    }
+                    tmem_st16(sc + 32 * hf + 16 * c, u);
                 }
-                tmem_st16(sc + 32 * hf + 16 * c, u);
+                const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                l += s2.x + s2.y;
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_cluster(there + (C::kPReady + g) * 8);
             }
-            const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += s2.x + s2.y;
-            wait_st();
+            if (mine > 0) done(mine - 1);
+            sums[g][hf][q] = l;
+            refs[g][q] = m;          // (the same from both halves of the keys)
             fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive_cluster(there + (C::kPReady + g) * 8);
-        }
-        if (mine > 0) done(mine);
-        sums[g][hf][q] = l;
-        refs[g][q] = m;          // (the same from both halves of the keys)
-        fence_before();
-        asm volatile("barrier.cta.sync 3, 512;" ::: "memory");
-        fence_after();
-        // both halves of the tiles joined: these warps take a quarter of the values each, of all their lanes' queries
-        const float ma = refs[0][q], mb = refs[1][q], top = fmaxf(ma, mb), fa = ex2(ma - top), fb = ex2(mb - top);
-        const float total = (sums[0][0][q] + sums[0][1][q]) * fa + (sums[1][0][q] + sums[1][1][q]) * fb;
-        const bool whole = p.splits == 1;
-        const float inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
-        const float ca = fa * inv, cb = fb * inv;
-        const int d0 = (2 * g + hf) * (D / 4);
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-            float x[16], y[16];
+            asm volatile("barrier.cta.sync 3, 512;" ::: "memory");
+            fence_after();
+            // both halves of the tiles joined: these warps take a quarter of the values each, of all their lanes' queries
+            const float ma = refs[0][q], mb = refs[1][q], top = fmaxf(ma, mb), fa = ex2(ma - top), fb = ex2(mb - top);
+            const float total = (sums[0][0][q] + sums[0][1][q]) * fa + (sums[1][0][q] + sums[1][1][q]) * fb;
+            const bool whole = p.splits == 1;
+            const float inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
+            const float ca = fa * inv, cb = fb * inv;
+            const int d0 = (2 * g + hf) * (D / 4);
+            const bool even = tiles > (jt & 1), odd = tiles > (1 ^ (jt & 1));   // which of the two O hold something of this unit
+            float x[D / 4];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = y[k] = 0.f;
-            if (tiles > 0) tmem_load<16>(tb + lanes + C::OCOL + d0 + 16 * c, x);
-            if (tiles > 1) tmem_load<16>(tb + lanes + C::OCOL + D + d0 + 16 * c, y);
+            for (int c = 0; c < D / 64; ++c) {
+                float y[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = x[k] * ca + y[k] * cb;
-            if (q < rows && L) {
-                const size_t o = ((size_t)(q0 + q) * p.H + h) * D + d0 + 16 * c;
+                for (int k = 0; k < 16; ++k) x[16 * c + k] = 0.f;
+                if (even) {
+                    tmem_load<16>(tb + lanes + C::OCOL + d0 + 16 * c, y);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[16 * c + k] = y[k] * ca;
+                }
+                if (odd) {
+                    tmem_load<16>(tb + lanes + C::OCOL + D + d0 + 16 * c, y);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[16 * c + k] = fmaf(y[k], cb, x[16 * c + k]);
+                }
+            }
+            fence_before();
+            asm volatile("barrier.cta.sync 3, 512;" ::: "memory");   // both O, and what was exchanged, are read: the next unit's weights may go out
+            fence_after();
+            if (q < rows) {
+                const size_t o = ((size_t)(q0 + q) * p.H + h) * D + d0;
                 if (whole) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < D / 32; ++k)
                         *reinterpret_cast<uint4*>(p.out + o + 8 * k) = make_uint4(pack_half(x[8 * k], x[8 * k + 1]), pack_half(x[8 * k + 2], x[8 * k + 3]),
                                                                                   pack_half(x[8 * k + 4], x[8 * k + 5]), pack_half(x[8 * k + 6], x[8 * k + 7]));
                 } else {
                     float* dst = p.parts + (size_t)split * p.n * p.H * D + o;
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                    for (int k = 0; k < D / 4; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                    if (g == 0 && hf == 0) p.stats[((size_t)split * p.n + q0 + q) * p.H + h] = make_float2(top, total);
                 }
             }
-        }
-        if (!whole && g == 0 && hf == 0 && q < rows && L) p.stats[((size_t)split * p.n + q0 + q) * p.H + h] = make_float2(top, total);
+            jt += max(tiles, 0);
+            return true;
+        });
     }
     fence_before();
     __syncthreads();
@@ -528,13 +573,13 @@ struct ChunkShape {
 static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     ChunkShape s = {};
     s.cap = (maxb * kBlock + 255) / 256 * 256;
-    // Keys split over pairs of CTAs where queries and heads alone give few: what the last wave of 76 pairs and the start of each
-    // (about 3 tiles) cost, for the longest context that the table holds.
+    // Keys split over pairs of CTAs where queries and heads alone give few: what the last round of 76 pairs and the end of each unit
+    // (about 2 tiles) cost, for the longest context that the table holds.
     const int64_t pairs = (n + 2 * kQ - 1) / (2 * kQ) * H, tiles = s.cap / kQ;
     int64_t best = 0;
     s.splits = 1;
     for (int64_t k = 1; k <= 16 && k <= std::max<int64_t>(1, tiles / 4) && (k == 1 || pairs < 152); ++k) {
-        const int64_t cost = (pairs * k + 75) / 76 * ((tiles + k - 1) / k + 3);
+        const int64_t cost = (pairs * k + 75) / 76 * ((tiles + k - 1) / k + 2);
         if (k == 1 || cost < best) {
             best = cost;
             s.splits = (int)k;
@@ -558,6 +603,29 @@ struct ChunkArgs {
     float scale;
     void *out, *ws;
 };
+
+// Clusters of two CTAs of a kernel that the current device holds at once, looked up once.
+template <typename K>
+static int pairs_at_once(K kernel, int threads, size_t smem, std::atomic<int>* known, int* out) {
+    int dev = 0;
+    QL_TRY_CUDA(cudaGetDevice(&dev));
+    *out = dev < 64 ? known[dev].load() : 0;
+    if (*out > 0) return QL_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    QL_TRY_CUDA(cudaOccupancyMaxActiveClusters(out, kernel, &cfg));
+    if (*out < 1) return set_error(QL_ECUDA, "ql_mla_attn_chunk: the GPU does not hold a pair of its CTAs");
+    if (dev < 64) known[dev].store(*out);
+    return QL_OK;
+}
 
 template <int D, int R>
 static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
@@ -620,30 +688,15 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     cp.splits = sh.splits;
     cp.scale_log2 = a.scale * 1.44269504088896340736f;
     // as many pairs as the GPU holds at once, and as there can be work for
-    static std::atomic<int> most[64];
-    int dev = 0, pairs = 0;
-    QL_TRY_CUDA(cudaGetDevice(&dev));
-    if (dev < 64) pairs = most[dev].load();
-    if (pairs == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(192);
-        cfg.dynamicSmemBytes = E::SMEM;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 2;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        QL_TRY_CUDA(cudaOccupancyMaxActiveClusters(&pairs, mla_expand_kernel<D, R>, &cfg));
-        if (pairs < 1) return set_error(QL_ECUDA, "ql_mla_attn_chunk: the GPU holds no pair of CTAs of the product");
-        if (dev < 64) most[dev].store(pairs);
-    }
-    const int64_t work = sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS);
-    if (pairs > work) pairs = (int)work;
+    static std::atomic<int> most[64], most2[64];
+    int pairs = 0, pairs2 = 0;
+    if (int rc = pairs_at_once(mla_expand_kernel<D, R>, 192, E::SMEM, most, &pairs)) return rc;
+    if (int rc = pairs_at_once(mla_chunk_kernel<D>, kChunkThreads, C::SMEM, most2, &pairs2)) return rc;
+    pairs = (int)std::min<int64_t>(pairs, sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS));
+    pairs2 = (int)std::min<int64_t>(pairs2, (a.n + 2 * kQ - 1) / (2 * kQ) * a.H * sh.splits);
     cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(192), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
-        e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)sh.splits, (unsigned)a.H, (unsigned)((a.n + 2 * kQ - 1) / (2 * kQ))), dim3(kChunkThreads), C::SMEM, s, true, cp);
+        e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), C::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.splits > 1)
         e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.n * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");
