@@ -48,7 +48,8 @@ def keys_values(rows, w, h, hd):
 def attention(q, rows, w, scale, before=None):
     """q [n, heads, hd + 64] over rows [L, rank + 64] -> out [n, heads, hd] and a bound of the error of a kernel that
     makes keys and values as f16, weighs them with f16 weights and rounds the output to f16. Query i sees rows 0 .. before + i
-    (all of them where before is None)."""
+    (all of them where before is None). A weight is kept relative to a reference that makes a row's largest 2^-1 or more, so that half
+    a step of f16's subnormals is 2 TINY of the largest at most."""
     q = q.astype(np.float64)
     n, heads, width = q.shape
     hd, L = width - ROPE, len(rows)
@@ -63,7 +64,7 @@ def attention(q, rows, w, scale, before=None):
         delta = np.max(np.where(seen, size * (U + (len(rows[0]) + width) * E) + 8 * E, 0), -1, keepdims=True)
         av = np.abs(v) * (1 + U)
         bound[:, h] = ((2 * delta + 2 * U + (len(rows[0]) + L) * E) * (p @ av) + U * np.abs(out[:, h]) + TINY
-                       + TINY * p.max(-1, keepdims=True) * (seen @ av))
+                       + 2 * TINY * p.max(-1, keepdims=True) * (seen @ av))
     return out, bound
 
 

@@ -8,6 +8,7 @@ namespace mla {
 
 constexpr int kRope = 64;    // rotated values of a cache row and of a query head
 constexpr int kBlock = 16;   // tokens of a pool block
+constexpr float kLag = 14.f; // log2 of how far a weight may lie above its reference: f16 holds 2^15, and O is scaled rarely
 
 inline bool shape_ok(int head_dim, int rank) { return (head_dim == 64 || head_dim == 128) && (rank == 256 || rank == 512); }
 

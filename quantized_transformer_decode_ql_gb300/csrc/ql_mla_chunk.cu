@@ -232,11 +232,12 @@ struct ChunkParams {
     CUtensorMap tv;         // values: [head, token][D]
     CUtensorMap tt;         // rotated parts: [token][64]
     const int* live;
+    const int32_t* table;
     const int32_t* position;
     __half* out;            // [n][H][D]
     float* parts;           // splits > 1: [split][n][H][D]
     float2* stats;          // [split][n][H]: reference (log2), sum of the weights
-    long long maxb, cap;
+    long long maxb, num_blocks, cap;
     int n, H, splits;
     float scale_log2;
     DevError* err;
@@ -258,8 +259,28 @@ struct ChunkCfg {
     // what has landed in either CTA, and the weights of both, are reported to rank 0's barriers, what the products have read or
     // written to both CTAs'
     static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
-                         kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kDone = kPReady + 2, kBars = kDone + 1;
+                         kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kOFree = kPReady + 2, kDone = kOFree + 1, kBars = kDone + 1;
 };
+
+// Four lanes' four 16-byte units each, transposed: unit r of lane i becomes what was unit i of lane r.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & o) continue;
+            const uint4 give = up ? u[k] : u[k + o];
+            uint4 got;
+            got.x = __shfl_xor_sync(0xffffffffu, give.x, o);
+            got.y = __shfl_xor_sync(0xffffffffu, give.y, o);
+            got.z = __shfl_xor_sync(0xffffffffu, give.z, o);
+            got.w = __shfl_xor_sync(0xffffffffu, give.w, o);
+            if (up) u[k] = got;
+            else u[k + o] = got;
+        }
+    }
+}
 
 constexpr int kSoft = 16, kCopy = 16, kProduct = 17, kChunkThreads = 18 * 32;   // warps: softmax, copies, products
 
@@ -270,12 +291,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
-    __shared__ float tops[2][2][kQ], sums[2][2][kQ], refs[2][kQ];
+    __shared__ float tops[2][2][kQ], sums[2][2][2][kQ], refs[2][2][kQ];   // (sums and refs of two units in turn)
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + C::STAGES * C::KB;
     if (t == 0) {
-        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 ? kSoft : 1);
+        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 || i == C::kOFree ? kSoft : 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tq);
@@ -291,26 +312,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0), there = in_cta(bar, 0);
     const Waits wt = {p.err, &abort_flag, p.ns};
     const Waits alone = {p.err, nullptr, p.ns};
+    const long long L = context(p.position, p.n, p.maxb);
+    // whether a block of the context is missing (its keys are then left out): the rare case is told apart here, once, beside the
+    // kernel before this one, and not at every tile
+    bool gap = false;
+    for (long long i = t; i < (L + kBlock - 1) / kBlock; i += kChunkThreads) {
+        const int id = __ldg(p.table + i);
+        gap |= id < 0 || id >= p.num_blocks;
+    }
+    gap = __syncthreads_or(gap);
     pdl_wait();
     pdl_trigger();
-    const long long L = context(p.position, p.n, p.maxb);
     const int before = (int)(L - p.n);
     const int blocks = (p.n + 2 * kQ - 1) / (2 * kQ), units = L ? blocks * p.H * p.splits : 0, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
-    // The units of this pair: `each` gets the head, the first query, the part of the keys, its first tile and their number, and returns
-    // false to stop.
+    // u / d for u < 2^22, `by` the rounded 1 / d
+    const float by_splits = 1.f / (float)p.splits, by_heads = 1.f / (float)p.H;
+    auto quotient = [](int u, int d, float by) {
+        int k = (int)((float)u * by);
+        k -= k * d > u;
+        return k + ((k + 1) * d <= u);
+    };
+    // The k-th unit of this pair: the head, the first query, the part of the keys, its first tile and their number; false behind the last.
+    struct Unit {
+        int h, first, split, j0, tiles;
+    };
+    auto unit = [&](int k, Unit& w) {
+        const int u = k * pairs + (k & 1 ? pairs - 1 - pair : pair);
+        if (u >= units) return false;
+        const int bh = quotient(u, p.splits, by_splits), b = quotient(bh, p.H, by_heads);
+        w.split = u - bh * p.splits;
+        w.h = bh - b * p.H;
+        w.first = (blocks - 1 - b) * 2 * kQ;
+        const int all = (before + min(w.first + 2 * kQ, p.n) + kQ - 1) / kQ;    // tiles that the last of the unit's queries sees
+        const int per = quotient(all + p.splits - 1, p.splits, by_splits);
+        w.j0 = min(w.split * per, all);
+        w.tiles = min(per, all - w.j0);
+        return true;
+    };
+    // (to and fro: where the last row of units is short, the pairs that have one there are those of the row's end)
     auto work = [&](auto each) {
-        for (int k = 0;; ++k) {
-            const int u = k * pairs + (k & 1 ? pairs - 1 - pair : pair);
-            if (u >= units) {
-                if (k * pairs >= units) return;
-                continue;
-            }
-            const int split = u % p.splits, h = u / p.splits % p.H, first = (blocks - 1 - u / p.splits / p.H) * 2 * kQ;
-            const int all = (before + min(first + 2 * kQ, p.n) + kQ - 1) / kQ;    // tiles that the last of the unit's queries sees
-            const int per = (all + p.splits - 1) / p.splits, j0 = min(split * per, all);
-            if (!each(h, first, split, j0, min(per, all - j0))) return;
-        }
+        Unit w;
+        for (int k = 0; k * pairs < units; ++k)
+            if (unit(k, w) && !each(w, k)) return;
     };
     int jt = 0, un = 0;   // tiles and units with tiles so far
 
@@ -318,13 +362,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
         // ------------------------------------------------ copies: this CTA's queries and its halves of the tiles
         if (lane == 0) {
             bool ok = true;
-            work([&](int h, int first, int, int j0, int tiles) {
+            work([&](const Unit& w, int k) {
+                const int h = w.h, first = w.first, j0 = w.j0, tiles = w.tiles;
                 if (tiles <= 0) return true;
                 ok = un == 0 || bar_wait(bar + C::kQEmpty * 8, (uint32_t)(un - 1) & 1u, wt, 799);
                 if (!ok) return false;
                 if (rank == 0) bar_expect(bar + C::kQFull * 8, 2 * C::QB);
                 for (int c = 0; c < C::CH; ++c) copy2_box3(qs + c * C::RUN, &p.tq, 64 * c, first + kQ * rank, h, there + C::kQFull * 8);
                 ++un;
+                Unit next;
+                if (unit(k + 1, next))   // its queries, spread over the rows of all heads, come from far
+                    for (int c = 0; c < C::CH; ++c) ask_box3(&p.tq, 64 * c, next.first + kQ * rank, next.h);
                 for (int j = 0; j < tiles && ok; ++j, ++jt) {
                     const int s = jt % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
                     const uint32_t ph = (uint32_t)(jt / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
@@ -354,8 +402,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
             const uint32_t one = elect_one();
             const uint64_t qd = operand(qs, 16, 1024, 2), kd = operand(ks, 16, 1024, 2);
             const uint64_t vd = operand(vs, 16, D * 8, D == 128 ? 2 : 4);   // a run of D / 2 columns
-            work([&](int, int, int, int, int tiles_) {
-                const int tiles = __shfl_sync(0xffffffffu, tiles_, 0);
+            work([&](const Unit& w, int) {
+                const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
                 if (tiles <= 0) return true;
                 if (!warp_wait(bar + C::kQFull * 8, (uint32_t)un & 1u, wt, 810)) return false;
                 ++un;
@@ -377,6 +425,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                         const int i = j < tiles ? jt - 2 : jt - 1, s = i % C::STAGES;
                         if (!warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i / C::STAGES) & 1u, wt, 812)) return false;
                         if (!warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 813)) return false;
+                        if (j == 1 && un > 1 && !warp_wait(bar + C::kOFree * 8, (uint32_t)un & 1u, wt, 815)) return false;   // (un - 2: the unit before)
                         fence_after();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -397,23 +446,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
         const int g = warp >> 3, hf = (warp >> 2) & 1, q = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sc = tb + lanes + g * kQ, oc = tb + lanes + C::OCOL + g * D;
         const float2 scale = make_float2(p.scale_log2, p.scale_log2);
-        work([&](int h, int first, int split, int j0, int tiles) {
-            const int q0 = first + kQ * (int)rank, rows = p.n - q0;   // (some, all or none of 128)
+        work([&](const Unit& w, int) {
+            const int tiles = max(w.tiles, 0), q0 = w.first + kQ * (int)rank, rows = p.n - q0;   // (some, all or none of 128)
             const int last = before + q0 + q - 64 * hf;        // the last key this query sees, counted from this thread's first
             const int off = (jt & 1) ^ g;                      // this half's first tile of the unit
             const int mine = tiles > off ? (tiles - off + 1) >> 1 : 0;
-            // the values up to this half's tile i are in O
+            // the values up to the unit's tile i are in O
             auto done = [&](int i) {
-                const int j = jt + off + 2 * i;
+                const int j = jt + i;
                 warp_wait(bar + (C::kVEmpty + j % C::STAGES) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 822);
                 fence_after();
             };
-            float m = -1e30f, l = 0.f;               // finite where no key is left: the weights stay numbers
-            int mask = mine > 0 ? __ldg(p.live + j0 + off) : 0;
+            // The weights' reference: 0 where the row's first scores allow it (the largest weight of a tile lies between 2^-1 and 2^kLag then),
+            // else their largest, and from then on a running maximum that lags by up to 2^kLag: weights of up to 16384 are as exact in f16
+            // as smaller ones, and O has to be scaled only when a score passes that.
+            float m = 0.f, l = 0.f;
+            bool set = false;
             for (int i = 0; i < mine; ++i) {
-                const int at = (j0 + off + 2 * i) * kQ, now_mask = mask >> (4 * hf), j = jt + off + 2 * i;
-                const bool whole = mask == 0xff;
-                if (i + 1 < mine) mask = __ldg(p.live + j0 + off + 2 * i + 2);
+                const int at = (w.j0 + off + 2 * i) * kQ, j = jt + off + 2 * i;
                 warp_wait(bar + (C::kSFull + g) * 8, (uint32_t)(j >> 1) & 1u, wt, 821);
                 fence_after();
                 float x[64];
@@ -422,30 +472,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 wait_ld();
                 tie32(x);
                 tie32(x + 32);
-                if (at + kQ - 1 > before + q0 || !whole) {   // the same for the CTA
+                if (at + kQ - 1 > before + q0 || gap) {   // the same for the CTA
+                    const int mask = gap ? __ldg(p.live + w.j0 + off + 2 * i) >> (4 * hf) : 0xf;
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
-                        if (at + c > last || !((now_mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
+                        if (at + c > last || !((mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
                 }
                 float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                 for (int c = 4; c < 64; ++c) most[c & 3] = fmaxf(most[c & 3], x[c]);
                 float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * p.scale_log2;
-                // The reference is a running maximum that lags by up to 2^8: weights of up to 256 are as exact in f16 as
-                // smaller ones, and O has to be scaled only when a score passes that.
-                // (The barrier also keeps the weights, which take the scores' place, behind the other four warps' loads.)
+                // (The barrier also keeps the weights, which take the scores' place, behind the other four warps' loads. Whether a row is
+                // set is known to both halves of its keys only as far as each has seen it: they settle it together where either asks.)
                 unsigned raise;
                 asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 256, a;\n selp.u32 %0, 1, 0, b;\n}"
-                             : "=r"(raise) : "r"((unsigned)(top > m + 8.f)), "r"(1 + g) : "memory");
+                             : "=r"(raise) : "r"((unsigned)(top > m + kLag || (!set && top < -1.f))), "r"(1 + g) : "memory");
                 if (raise) {
                     tops[g][hf][q] = top;
                     asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + g) : "memory");
                     top = fmaxf(top, tops[g][hf ^ 1][q]);
-                    const float now = top > m + 8.f ? top : m, f = ex2(m - now);
+                    const bool move = top > -INFINITY && (top > m + kLag || (!set && top < -1.f));
+                    const float now = move ? top : m, f = set ? ex2(m - now) : 0.f;
                     m = now;
+                    set |= top > -INFINITY;
                     l *= f;
                     if (i > 0) {
-                        done(i - 1);
+                        done(off + 2 * i - 2);
 #pragma unroll 1
                         for (int c = hf * (D / 32); c < (hf + 1) * (D / 32); ++c) {
                             float v[16];
@@ -456,7 +508,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                             tmem_st16(oc + 16 * c, u);
                         }
                     }
-                }
+                } else set = true;
                 const float2 ref = make_float2(-m, -m);
                 float2 sum[4] = {};
 #pragma unroll
@@ -478,55 +530,79 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 __syncwarp();
                 if (lane == 0) bar_arrive_cluster(there + (C::kPReady + g) * 8);
             }
-            if (mine > 0) done(mine - 1);
-            sums[g][hf][q] = l;
-            refs[g][q] = m;          // (the same from both halves of the keys)
-            fence_before();
-            asm volatile("barrier.cta.sync 3, 512;" ::: "memory");
-            fence_after();
-            // both halves of the tiles joined: these warps take a quarter of the values each, of all their lanes' queries
-            const float ma = refs[0][q], mb = refs[1][q], top = fmaxf(ma, mb), fa = ex2(ma - top), fb = ex2(mb - top);
-            const float total = (sums[0][0][q] + sums[0][1][q]) * fa + (sums[1][0][q] + sums[1][1][q]) * fb;
+            // Both halves of the tiles joined by the eight warps that had the last tile, half of the values each four; the other
+            // eight leave what they know and go on to the next unit.
             const bool whole = p.splits == 1;
-            const float inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
-            const float ca = fa * inv, cb = fb * inv;
-            const int d0 = (2 * g + hf) * (D / 4);
+            float ma = -1e30f, mb = -1e30f, total = 0.f;
+            if (tiles > 0) {
+                const int lastg = (jt + tiles - 1) & 1, turn = un & 1;
+                sums[turn][g][hf][q] = l;
+                refs[turn][g][q] = set ? m : -1e30f;          // (the same from both halves of the keys)
+                ++un;
+                if (g != lastg) {
+                    asm volatile("barrier.cta.arrive %0, 512;" ::"r"(3 + turn) : "memory");
+                    jt += tiles;
+                    return true;
+                }
+                asm volatile("barrier.cta.sync %0, 512;" ::"r"(3 + turn) : "memory");
+                ma = refs[turn][0][q];
+                mb = refs[turn][1][q];
+                const float top = fmaxf(ma, mb);
+                total = (sums[turn][0][0][q] + sums[turn][0][1][q]) * ex2(ma - top) + (sums[turn][1][0][q] + sums[turn][1][1][q]) * ex2(mb - top);
+                if (tiles > 1) done(tiles - 2);
+                done(tiles - 1);
+            } else if (g != 0) return true;
+            const float top = fmaxf(ma, mb), inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
+            const float ca = ex2(ma - top) * inv, cb = ex2(mb - top) * inv;
             const bool even = tiles > (jt & 1), odd = tiles > (1 ^ (jt & 1));   // which of the two O hold something of this unit
-            float x[D / 4];
+            // Four lanes store 64 bytes of one query together (one lane a query: rows far apart, which held up the warps for 3500 cycles).
+            const int r0 = q & ~3, part = q & 3;
+            const size_t step = (size_t)p.H * D, row0 = (size_t)(q0 + r0) * step + (size_t)w.h * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {   // 32 values
+                float x[32], y[32];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                float y[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) x[16 * c + k] = 0.f;
-                if (even) {
-                    tmem_load<16>(tb + lanes + C::OCOL + d0 + 16 * c, y);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) x[16 * c + k] = y[k] * ca;
+                for (int k = 0; k < 32; ++k) x[k] = y[k] = 0.f;
+                const int d0 = hf * (D / 2) + 32 * c;
+                if (even) tmem_raw<32>(tb + lanes + C::OCOL + d0, x);
+                if (odd) tmem_raw<32>(tb + lanes + C::OCOL + D + d0, y);
+                wait_ld();
+                tie<32>(x);
+                tie<32>(y);
+                if (c == D / 64 - 1 && tiles > 0) {   // both O are read: the next unit's values may go there
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(there + C::kOFree * 8);
                 }
-                if (odd) {
-                    tmem_load<16>(tb + lanes + C::OCOL + D + d0 + 16 * c, y);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[16 * c + k] = fmaf(y[k], cb, x[16 * c + k]);
-                }
-            }
-            fence_before();
-            asm volatile("barrier.cta.sync 3, 512;" ::: "memory");   // both O, and what was exchanged, are read: the next unit's weights may go out
-            fence_after();
-            if (q < rows) {
-                const size_t o = ((size_t)(q0 + q) * p.H + h) * D + d0;
+                for (int k = 0; k < 32; ++k) x[k] = fmaf(y[k], cb, x[k] * ca);
+                uint4 u[4];
                 if (whole) {
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        *reinterpret_cast<uint4*>(p.out + o + 8 * k) = make_uint4(pack_half(x[8 * k], x[8 * k + 1]), pack_half(x[8 * k + 2], x[8 * k + 3]),
-                                                                                  pack_half(x[8 * k + 4], x[8 * k + 5]), pack_half(x[8 * k + 6], x[8 * k + 7]));
-                } else {
-                    float* dst = p.parts + (size_t)split * p.n * p.H * D + o;
+                    for (int k = 0; k < 4; ++k)
+                        u[k] = make_uint4(pack_half(x[8 * k], x[8 * k + 1]), pack_half(x[8 * k + 2], x[8 * k + 3]), pack_half(x[8 * k + 4], x[8 * k + 5]),
+                                          pack_half(x[8 * k + 6], x[8 * k + 7]));
+                    transpose4(u, lane);
 #pragma unroll
-                    for (int k = 0; k < D / 4; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-                    if (g == 0 && hf == 0) p.stats[((size_t)split * p.n + q0 + q) * p.H + h] = make_float2(top, total);
+                    for (int r = 0; r < 4; ++r)
+                        if (r0 + r < rows) *reinterpret_cast<uint4*>(p.out + row0 + r * step + d0 + 8 * part) = u[r];
+                } else {
+                    float* dst = p.parts + (size_t)w.split * p.n * p.H * D;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            u[k] = make_uint4(__float_as_uint(x[16 * b + 4 * k]), __float_as_uint(x[16 * b + 4 * k + 1]), __float_as_uint(x[16 * b + 4 * k + 2]),
+                                              __float_as_uint(x[16 * b + 4 * k + 3]));
+                        transpose4(u, lane);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (r0 + r < rows) *reinterpret_cast<uint4*>(dst + row0 + r * step + d0 + 16 * b + 4 * part) = u[r];
+                    }
                 }
             }
-            jt += max(tiles, 0);
+            if (!whole && hf == 0 && q < rows) p.stats[((size_t)w.split * p.n + q0 + q) * p.H + w.h] = make_float2(top, total);
+            jt += tiles;
             return true;
         });
     }
@@ -670,13 +746,13 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
         if (int rc = f16_tensor_map(ws + sh.turned, 2, d, st, b, &cp.tt)) return rc;
     }
     ep.pool = static_cast<const __half*>(a.pool);
-    ep.table = a.table;
+    ep.table = cp.table = a.table;
     ep.position = cp.position = a.position;
     ep.turned = reinterpret_cast<__half*>(ws + sh.turned);
     ep.live = reinterpret_cast<int*>(ws + sh.live);
     cp.live = ep.live;
     ep.maxb = cp.maxb = a.maxb;
-    ep.num_blocks = a.num_blocks;
+    ep.num_blocks = cp.num_blocks = a.num_blocks;
     ep.cap = cp.cap = sh.cap;
     ep.n = cp.n = (int)a.n;
     ep.H = cp.H = a.H;

@@ -66,6 +66,10 @@ __device__ __forceinline__ void copy_box4(uint32_t dst, const CUtensorMap* m, in
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(mb) : "memory");
 }
+// into L2 only
+__device__ __forceinline__ void ask_box3(const CUtensorMap* m, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z) : "memory");
+}
 // from shared memory; the issuing thread's copies so far have been read, or have arrived
 __device__ __forceinline__ void store_box2(const CUtensorMap* m, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x),
@@ -193,13 +197,21 @@ __device__ __forceinline__ void tie32(float* f) {
     tie16(f + 16);
 }
 template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t a, float* f) {   // and wait
+__device__ __forceinline__ void tmem_raw(uint32_t a, float* f) {
     static_assert(N == 16 || N == 32, "");
     if constexpr (N == 32) tmem_ld32(a, f);
     else tmem_ld16(a, f);
+}
+template <int N>
+__device__ __forceinline__ void tie(float* f) {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) tie16(f + i);
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t a, float* f) {   // and wait
+    tmem_raw<N>(a, f);
     wait_ld();
-    tie16(f);
-    if constexpr (N == 32) tie16(f + 16);
+    tie<N>(f);
 }
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
