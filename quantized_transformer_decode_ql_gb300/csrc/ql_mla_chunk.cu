@@ -46,14 +46,16 @@ struct ExpandCfg {
     static constexpr int HEADS = 128 / D;                  // heads of a product: 256 outputs
     static constexpr int KC = R / 64;                      // runs of 64 latent values
     static constexpr int STAGES = R == 512 ? 5 : 8, AB = 128 * 128, BB = 128 * 128, OB = 32 * 128;   // OB: 64 outputs of a warp's 32 tokens
-    static constexpr size_t SMEM = (size_t)KC * AB + (size_t)STAGES * BB + 4 * OB;
+    // (with rank 512 a fifth stage is worth more than eight storing warps' room: 49.7 instead of 52.6 us; with 256, 11.5 instead of 13)
+    static constexpr int kOut = R == 512 ? 4 : 8, kCopy = kOut, kProduct = kOut + 1, THREADS = (kOut + 2) * 32;   // warps
+    static constexpr size_t SMEM = (size_t)KC * AB + (size_t)STAGES * BB + kOut * OB;
     // what has landed in either CTA is reported to rank 0's barriers, what has been read to both CTAs'
     static constexpr int kAFull = 0, kBFull = KC, kBEmpty = kBFull + STAGES, kAEmpty = kBEmpty + STAGES, kDFull = kAEmpty + 1, kDEmpty = kDFull + 2, kDone = kDEmpty + 2, kBars = kDone + 1;
     static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
 
 template <int D, int R>
-__global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_kernel(const __grid_constant__ ExpandParams p) {
+__global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(2, 1, 1) mla_expand_kernel(const __grid_constant__ ExpandParams p) {
     using C = ExpandCfg<D, R>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) unsigned long long bars[C::kBars];
@@ -63,13 +65,13 @@ __global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_k
     const uint32_t rank = cluster_rank();
     const uint32_t bar = su32(bars), as = su32(smem), bs = as + C::KC * C::AB;
     if (t == 0) {
-        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kDEmpty || i == C::kDEmpty + 1 ? 8 : 1);
+        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kDEmpty || i == C::kDEmpty + 1 ? 2 * C::kOut : 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tc);
         prefetch_map(&p.tw);
     }
-    if (warp == 5) tmem_alloc2<512>(&tmem_at);
+    if (warp == C::kProduct) tmem_alloc2<512>(&tmem_at);
     fence_before();
     __syncthreads();
     cluster_sync();
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_k
     const long long u0 = __shfl_sync(0xffffffffu, units * pair / pairs, 0), u1 = __shfl_sync(0xffffffffu, units * (pair + 1) / pairs, 0);
 
     const uint32_t there = in_cta(bar, 0);
-    if (warp == 4) {
+    if (warp == C::kCopy) {
         // ------------------------------------------------ copies: a block of 16 tokens a lane, the weights by lane 0
         const long long nblk = (L + kBlock - 1) / kBlock;
         long long held = -1;
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_k
             for (int c = 0; loads > 0 && c < C::KC; ++c) warp_wait(bar + (C::kAFull + c) * 8, (uint32_t)(loads - 1) & 1u, alone, 702);
             for (int i = max(0, it - C::STAGES); i < it; ++i) warp_wait(bar + (C::kBFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 703);
         }
-    } else if (warp == 5) {
+    } else if (warp == C::kProduct) {
         // ------------------------------------------------ products of both CTAs, issued by rank 0
         constexpr uint32_t I = instr(256, 256, false, false);
         const uint32_t one = elect_one();
@@ -168,14 +170,14 @@ __global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_k
             warp_wait(bar + C::kDone * 8, 0u, alone, 715);
         }
     } else {
-        // ------------------------------------------------ a token a thread: its 256 outputs rounded and stored
+        // ------------------------------------------------ a token a thread: its 256 outputs, or 128 of them, rounded and stored
         unsigned char* stage = smem + C::KC * C::AB + C::STAGES * C::BB + warp * C::OB + lane * 128;
         int n = 0;
         for (long long u = u0; u < u1; ++u, ++n) {
-            const long long tp = u / hgs, tok = tp * 256 + 128 * rank + 32 * warp + lane;
+            const long long tp = u / hgs, tok = tp * 256 + 128 * rank + 32 * (warp & 3) + lane;
             const int hg = (int)(u - tp * hgs), b = n & 1;
             const bool in = tok < L;   // rows behind the context are zeros: what its last block holds there must not meet the weights
-            if (hg == 0) {             // the rotated part as it is
+            if (hg == 0 && warp < 4) { // the rotated part as it is
                 const long long at = tok / kBlock;
                 const int id = in ? __ldg(p.table + at) : -1;
                 const bool live = id >= 0 && id < p.num_blocks;
@@ -186,9 +188,9 @@ __global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_k
             }
             if (!warp_wait(bar + (C::kDFull + b) * 8, (uint32_t)(n >> 1) & 1u, wt, 720)) break;
             fence_after();
-            const uint32_t acc = tb + 256 * b + ((uint32_t)(32 * warp) << 16);
+            const uint32_t acc = tb + 256 * b + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {   // 64 outputs: rounded into shared memory, copied out from there
+            for (int c = warp >> 2; c < 4; c += C::kOut / 4) {   // 64 outputs: rounded into shared memory, copied out from there
                 float f[64];
                 tmem_ld32(acc + 64 * c, f);
                 tmem_ld32(acc + 64 * c + 32, f + 32);
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(192, 1) __cluster_dims__(2, 1, 1) mla_expand_k
     fence_before();
     __syncthreads();
     cluster_sync();   // no product, report or commit is left that touches the other CTA
-    if (warp == 5) {
+    if (warp == C::kProduct) {
         fence_after();
         tmem_free2<512>(tb);
     }
@@ -551,7 +553,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 total = (sums[turn][0][0][q] + sums[turn][0][1][q]) * ex2(ma - top) + (sums[turn][1][0][q] + sums[turn][1][1][q]) * ex2(mb - top);
                 if (tiles > 1) done(tiles - 2);
                 done(tiles - 1);
-            } else if (g != 0) return true;
+            } else {   // (a split without keys: the join does not look at its part)
+                if (g == 0 && hf == 0 && q < rows) p.stats[((size_t)w.split * p.n + q0 + q) * p.H + w.h] = make_float2(-1e30f, 0.f);
+                return true;
+            }
             const float top = fmaxf(ma, mb), inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
             const float ca = ex2(ma - top) * inv, cb = ex2(mb - top) * inv;
             const bool even = tiles > (jt & 1), odd = tiles > (1 ^ (jt & 1));   // which of the two O hold something of this unit
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 wait_ld();
                 tie<32>(x);
                 tie<32>(y);
-                if (c == D / 64 - 1 && tiles > 0) {   // both O are read: the next unit's values may go there
+                if (c == D / 64 - 1) {   // both O are read: the next unit's values may go there
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive_cluster(there + C::kOFree * 8);
@@ -623,16 +628,37 @@ __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_consta
     const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), all = (long long)p.n * p.H;
     const int lane = threadIdx.x & 31;
     if (i >= all || context(p.position, p.n, p.maxb) == 0) return;
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, AT_ONCE = 4;
     float top = -INFINITY, total = 0.f, x[V] = {};
-    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.stats[s * all + i].x);
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 st = p.stats[s * all + i];
-        const float f = ex2(st.x - top);
-        total += st.y * f;
-        const float* src = p.parts + (s * all + i) * D + lane * V;
+    for (int s0 = 0; s0 < p.splits; s0 += AT_ONCE) {   // the parts of four splits at a time
+        float2 st[AT_ONCE];
+        float v[AT_ONCE][V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[k] = fmaf(src[k], f, x[k]);
+        for (int s = 0; s < AT_ONCE; ++s) {
+            st[s] = s0 + s < p.splits ? __ldcg(p.stats + (s0 + s) * all + i) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+                const float2 a = s0 + s < p.splits ? __ldcg(reinterpret_cast<const float2*>(p.parts + ((s0 + s) * all + i) * D + lane * V + k)) : make_float2(0.f, 0.f);
+                v[s][k] = a.x;
+                v[s][k + 1] = a.y;
+            }
+        }
+        float now = top;
+#pragma unroll
+        for (int s = 0; s < AT_ONCE; ++s) now = fmaxf(now, st[s].x);
+        const float f0 = top == now ? 1.f : ex2(top - now);
+        total *= f0;
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[k] *= f0;
+        top = now;
+#pragma unroll
+        for (int s = 0; s < AT_ONCE; ++s) {
+            if (st[s].y == 0.f) continue;   // no key, and no part
+            const float f = ex2(st[s].x - top);
+            total += st[s].y * f;
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[k] = fmaf(v[s][k], f, x[k]);
+        }
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
@@ -766,11 +792,11 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     // as many pairs as the GPU holds at once, and as there can be work for
     static std::atomic<int> most[64], most2[64];
     int pairs = 0, pairs2 = 0;
-    if (int rc = pairs_at_once(mla_expand_kernel<D, R>, 192, E::SMEM, most, &pairs)) return rc;
+    if (int rc = pairs_at_once(mla_expand_kernel<D, R>, E::THREADS, E::SMEM, most, &pairs)) return rc;
     if (int rc = pairs_at_once(mla_chunk_kernel<D>, kChunkThreads, C::SMEM, most2, &pairs2)) return rc;
     pairs = (int)std::min<int64_t>(pairs, sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS));
     pairs2 = (int)std::min<int64_t>(pairs2, (a.n + 2 * kQ - 1) / (2 * kQ) * a.H * sh.splits);
-    cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(192), E::SMEM, s, true, ep);
+    cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(E::THREADS), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
         e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), C::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.splits > 1)
