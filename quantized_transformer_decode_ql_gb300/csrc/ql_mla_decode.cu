@@ -1,6 +1,7 @@
 // Latent attention of one new token per sequence over the paged cache, in three launches:
 //
-//  1. mla_absorb_kernel: q'_h = Wk_h^T q_h (f16), the heads' queries against the latents themselves;
+//  1. mla_absorb_kernel: q'_h = Wk_h^T q_h, the heads' queries against the latents themselves, as f16 (up to 32 heads: as a
+//     pair of f16, 22 bits, which enter the scores' product as 64 heads);
 //  2. mla_decode_kernel: the batch's tiles of 64 keys cut into equal windows, one per SM (the lengths are on the device only), a
 //     window's tiles on the 5th-generation tensor cores, each tile read once for up to 64 heads: S^T = K q'^T (64 keys x heads),
 //     the online softmax, O^T += V^T P (rank x heads), K the tile's rows and V their first `rank` values, the same bytes in
@@ -25,8 +26,8 @@ __device__ __forceinline__ int tiles_checked(int len, long long cap) { return le
 struct AbsorbParams {
     const __half* q;       // [batch][H][D + 64]
     const __half* w;       // [H][2 D][R]
-    __half* qc;            // [batch][H][R + 64]
-    int batch, H;
+    __half* qc;            // [batch][halves][H][R + 64]
+    int batch, H, halves;  // halves: 2 where the rest of each rounding is kept, too
     DevError* err;
 };
 
@@ -65,11 +66,13 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
         else *reinterpret_cast<uint4*>(qs + b * QP + c * 8) = make_uint4(0u, 0u, 0u, 0u);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    const size_t rest = (size_t)p.H * (R + kRope);         // from a value to the rest of its rounding
     if (r0 == 0)   // the rotated part as it is
         for (int i = t; i < rows * 8; i += 128) {
-            const size_t row = (size_t)(b0 + (i >> 3)) * p.H + h;
-            *reinterpret_cast<uint4*>(p.qc + row * (R + kRope) + R + (i & 7) * 8) =
-                __ldg(reinterpret_cast<const uint4*>(p.q + row * (D + kRope) + D + (i & 7) * 8));
+            const int b = b0 + (i >> 3);
+            __half* dst = p.qc + ((size_t)b * p.halves * p.H + h) * (R + kRope) + R + (i & 7) * 8;
+            *reinterpret_cast<uint4*>(dst) = __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.H + h) * (D + kRope) + D + (i & 7) * 8));
+            if (p.halves == 2) *reinterpret_cast<uint4*>(dst + rest) = make_uint4(0u, 0u, 0u, 0u);
         }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
@@ -92,8 +95,10 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
             const int r = m + (lane >> 2) + 8 * (i & 1);
             const float x = c[i >> 1][2 * (i & 1)], y = c[i >> 1][2 * (i & 1) + 1];
             if (r < rows) {
-                *reinterpret_cast<__half2*>(p.qc + ((size_t)(b0 + r) * p.H + h) * (R + kRope) + r0 + 16 * warp + 8 * (i >> 1) + 2 * (lane & 3)) =
-                    __floats2half2_rn(x, y);
+                __half* dst = p.qc + ((size_t)(b0 + r) * p.halves * p.H + h) * (R + kRope) + r0 + 16 * warp + 8 * (i >> 1) + 2 * (lane & 3);
+                const __half2 v = __floats2half2_rn(x, y);
+                *reinterpret_cast<__half2*>(dst) = v;
+                if (p.halves == 2) *reinterpret_cast<__half2*>(dst + rest) = __floats2half2_rn(x - __low2float(v), y - __high2float(v));
                 large |= !(fabsf(x) < 65520.f && fabsf(y) < 65520.f);
             }
         }
@@ -107,13 +112,14 @@ struct Cfg {
     static constexpr int CH = (R + kRope) / 64;         // runs of 64 values (128 bytes) of a row
     static constexpr int GROUP = CH * 1024;             // 8 rows: [run][row][128 bytes], swizzled
     static constexpr int TILE = 8 * GROUP;
-    static constexpr int QB = CH * NH * 128;            // [run][head][128 bytes]
+    static constexpr int HALVES = NH == 32 ? 2 : 1, NQ = NH * HALVES;   // of the queries: 64 columns of scores either way
+    static constexpr int QB = CH * NQ * 128;            // [run][half][head][128 bytes]
     static constexpr int PB = kTile * NH * 2;           // [key][head]
     static constexpr int STAGES = R == 512 ? 2 : 4;
     static constexpr int PBUF = R == 512 && NH == 64 ? 1 : 2;
     static constexpr int MT = R / 128;                  // blocks of 128 latent values
     static constexpr uint32_t SCOL = MT * NH;           // tensor memory: O^T of each block, then two S^T
-    static constexpr uint32_t COLS = SCOL + 2 * NH <= 128 ? 128 : SCOL + 2 * NH <= 256 ? 256 : 512;
+    static constexpr uint32_t COLS = SCOL + 2 * NQ <= 128 ? 128 : SCOL + 2 * NQ <= 256 ? 256 : 512;
     static constexpr size_t SMEM = (size_t)STAGES * TILE + QB + PBUF * PB;
     // a stage is freed block by block (kKEmpty + 4 stage + block): the next copies start while the values are still multiplied
     static constexpr int kKFull = 0, kKEmpty = STAGES, kSFull = 5 * STAGES, kPReady = kSFull + 2, kQFull = kPReady + 2, kQEmpty = kQFull + 1,
@@ -122,13 +128,13 @@ struct Cfg {
     static constexpr int HN = NH / 2;                   // heads of a softmax group of four warps (four groups of 16 of 64: 61 instead of 57 us, many heads)
     static constexpr int kSoftWarps = NH / HN * 4, kCopyWarp = kSoftWarps, kScoreWarp = kSoftWarps + 1, kValueWarp = kSoftWarps + 2,
                          THREADS = (kSoftWarps + 3) * 32;
-    static_assert(SCOL + 2 * NH <= 512, "tensor memory");
+    static_assert(SCOL + 2 * NQ <= 512, "tensor memory");
     static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
 
 struct DecodeParams {
     CUtensorMap tk;        // the pool: [group of 8 rows][run][row][64 values]
-    CUtensorMap tq;        // absorbed queries: [sequence][run][head][64 values]
+    CUtensorMap tq;        // absorbed queries: [sequence][run][half][head][64 values]
     const int32_t* tables;
     const int32_t* lens;
     float* parts;          // [head group][window + sequence][NH][R]
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
             auto query = [&] {
                 if (lane == 0) {
                     bar_expect(bar + C::kQFull * 8, C::QB);
-                    copy_box4(qs, &p.tq, 0, hg * NH, 0, b, bar + C::kQFull * 8);
+                    copy_box5(qs, &p.tq, 0, hg * NH, 0, 0, b, bar + C::kQFull * 8);
                 }
                 ++sg;
             };
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
         __syncwarp();
     } else if (warp == C::kScoreWarp) {
         // ------------------------------------------------ S^T = K q'^T, two tiles ahead of their values at most
-        constexpr uint32_t I = instr(64, NH, false, false);
+        constexpr uint32_t I = instr(64, C::NQ, false, false);
         const uint32_t one = elect_one();
         const uint64_t kd = operand(ks, 16, C::GROUP, 2), qd = operand(qs, 16, 1024, 2);
         sequences([&](int, int, int t0, int t1) {
@@ -347,8 +353,8 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                 const uint64_t k0 = kd + (it % C::STAGES) * (C::TILE >> 4);
 #pragma unroll
                 for (int k = 0; k < 4 * C::CH; ++k)
-                    mma_ss(one, tb + C::SCOL + (it & 1) * NH, k0 + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
-                           qd + (((k >> 2) * NH * 128 + (k & 3) * 32) >> 4), I, k > 0);
+                    mma_ss(one, tb + C::SCOL + (it & 1) * C::NQ, k0 + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                           qd + (((k >> 2) * C::NQ * 128 + (k & 3) * 32) >> 4), I, k > 0);
                 mma_commit(one, bar + (C::kSFull + (it & 1)) * 8);
                 if (tt + 1 == t1) mma_commit(one, bar + C::kQEmpty * 8);
             }
@@ -406,12 +412,28 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                 }
                 warp_wait(bar + (C::kSFull + (it & 1)) * 8, (uint32_t)(it >> 1) & 1u, wt, 601);
                 fence_after();
-                const uint32_t sc = tb + lanes + C::SCOL + (it & 1) * NH + h0;
+                const uint32_t sc = tb + lanes + C::SCOL + (it & 1) * C::NQ + h0;
                 const float2 scale = make_float2(p.scale_log2, p.scale_log2);
                 float x[HN];
                 float over = -INFINITY;
+                auto scores = [&](float* s) {
+                    if constexpr (C::HALVES == 2) {
+                        float r[HN];
+                        tmem_raw<HN>(sc, s);
+                        tmem_raw<HN>(sc + NH, r);
+                        wait_ld();
+                        tie<HN>(s);
+                        tie<HN>(r);
+#pragma unroll
+                        for (int h = 0; h < HN; h += 2) {
+                            const float2 a = add2(make_float2(s[h], s[h + 1]), make_float2(r[h], r[h + 1]));
+                            s[h] = a.x;
+                            s[h + 1] = a.y;
+                        }
+                    } else tmem_load<HN>(sc, s);
+                };
                 auto exponents = [&] {   // x: how far the scores lie above their heads' references
-                    tmem_load<HN>(sc, x);
+                    scores(x);
                     if (seen) {
 #pragma unroll
                         for (int h = 0; h < HN; h += 4) {
@@ -435,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                 if (raise) {
                     {
                         float v[HN];
-                        tmem_load<HN>(sc, v);
+                        scores(v);
 #pragma unroll
                         for (int i = 0; i < HN; ++i) v[i] = seen ? v[i] * p.scale_log2 : -INFINITY;
                         const float most = reduce_columns<true, HN>(v, lane);
@@ -734,7 +756,7 @@ static DecodeShape decode_shape(int64_t batch, int H, int R) {
     s.groups = (H + s.NH - 1) / s.NH;
     const size_t win = kMaxWin / s.groups + 1, rows = (size_t)s.groups * (batch + win) * s.NH;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-    s.parts = up((size_t)batch * H * (R + kRope) * 2);
+    s.parts = up((size_t)batch * H * (R + kRope) * 2 * (s.NH == 32 ? 2 : 1));
     s.stats = s.parts + rows * R * 4;
     s.total = s.stats + up(rows * 8);
     return s;
@@ -759,15 +781,15 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     int windows = std::min(num_sms(), kMaxWin) / sh.groups;
     if (windows < 1) windows = 1;
-    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws), (int)a.batch, a.H, err};
+    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws), (int)a.batch, a.H, C::HALVES, err};
     DecodeParams dp = {};
     const uint64_t row = (R + kRope) * 2;
     const uint64_t kd[4] = {64, 8, (uint64_t)C::CH, (uint64_t)a.num_blocks * 2}, kst[3] = {row, 128, 8 * row};
     const uint32_t kb[4] = {64, 8, (uint32_t)C::CH, 2};
     if (int rc = f16_tensor_map(a.pool, 4, kd, kst, kb, &dp.tk)) return rc;
-    const uint64_t qd[4] = {64, (uint64_t)a.H, (uint64_t)C::CH, (uint64_t)a.batch}, qst[3] = {row, 128, a.H * row};
-    const uint32_t qb[4] = {64, (uint32_t)NH, (uint32_t)C::CH, 1};
-    if (int rc = f16_tensor_map(ws, 4, qd, qst, qb, &dp.tq)) return rc;
+    const uint64_t qd[5] = {64, (uint64_t)a.H, C::HALVES, (uint64_t)C::CH, (uint64_t)a.batch}, qst[4] = {row, a.H * row, 128, C::HALVES * a.H * row};
+    const uint32_t qb[5] = {64, (uint32_t)NH, C::HALVES, (uint32_t)C::CH, 1};
+    if (int rc = f16_tensor_map(ws, 5, qd, qst, qb, &dp.tq)) return rc;
     dp.tables = a.tables;
     dp.lens = a.lens;
     dp.parts = reinterpret_cast<float*>(ws + sh.parts);
