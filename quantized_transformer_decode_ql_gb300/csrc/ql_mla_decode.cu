@@ -181,6 +181,21 @@ __device__ Window make_window(const DecodeParams& p, int win) {
         if (len != 0 && n == 0 && blockIdx.x == 0) record_device_error(p.err, kErrAttnLength, b, len);
         return n ? n + kEnter : 0;
     };
+    if (p.batch <= 32) {   // every warp by itself
+        const int n = places(lane);
+        int end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            end += lane >= o ? v : 0;
+        }
+        const int total = __shfl_sync(0xffffffffu, end, 31), W = max(1, (total + p.windows - 1) / p.windows);
+        const int lo = win * W, hi = min(lo + W, total);
+        const unsigned in = __ballot_sync(0xffffffffu, n && end - n <= lo && lo < end);
+        const int first = in ? __ffs(in) - 1 : 0;
+        __syncthreads();
+        return {lo, hi, first, __shfl_sync(0xffffffffu, end - n, first)};
+    }
     const int mine = places(t);
     int sum = mine;
     for (int b = t + THREADS; b < p.batch; b += THREADS) sum += places(b);
