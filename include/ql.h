@@ -400,7 +400,7 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  * cache row nor its query is written. Any other slot outside the pool, or a position outside the tables, leaves
  * the row out too and is recorded in the device error record, as is a cache row with a value that f16 does
  * not hold (the row is written). The slots of one call must differ from one another (-1 may repeat).
- * d_q_out overlaps no input. Rows, norm weights, d_q_out and the pool 16-byte, tables and slots 8-byte aligned, strides multiples
+ * d_q_out and the pool overlap neither each other nor an input (QL_EINVAL). Rows, norm weights, d_q_out and the pool 16-byte, tables and slots 8-byte aligned, strides multiples
  * of 16 bytes and at least a row (any when n is 1), below 2^31 elements. n = 0 is allowed, n < 2^31. Asynchronous on stream. */
 int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride, int64_t kv_stride, const float* d_norm_w,
                   const float* d_cos, const float* d_sin, const int32_t* d_positions, const int64_t* d_slots, float eps,
@@ -417,7 +417,8 @@ int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride
  * not matter. An absorbed query that f16 does not hold is recorded (its outputs are then not finite).
  * d_out f16 [batch][n_heads * head_dim]. scale positive and finite. batch <= 65535, batch * n_heads < 2^22,
  * max_blocks_per_seq <= 2^20, batch * max_blocks_per_seq < 2^32.
- * q, the weights, the pool and the output 16-byte aligned. d_workspace: ql_mla_decode_workspace_bytes(...)
+ * q, the weights, the pool and the output 16-byte aligned; output and workspace overlap neither each other nor an
+ * input (QL_EINVAL). d_workspace: ql_mla_decode_workspace_bytes(...)
  * bytes, 128-byte aligned, any contents; calls and captured graphs that may run at the same time need
  * workspaces of their own. The split of the work over the SMs is made from the lengths on the
  * device, so that a captured call serves any lengths. */

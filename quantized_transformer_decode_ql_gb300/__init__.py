@@ -368,9 +368,10 @@ def ql_mla_append(q, kv, norm_w, cos_t, sin_t, positions, slots, eps, n_heads, h
         q_at, out_at, q_stride = q.data_ptr(), q_out.data_ptr(), _row_stride(name, q, n, n_heads, width)
     elif q is not q_out:
         raise QLError(QL_EINVAL, f"{name}: q and q_out come together")
-    status = lib().ql_mla_append(q_at, kv.data_ptr(), _dtype_of(name, kv, q), q_stride, _row_stride(name, kv, n, 1, row), norm_w.data_ptr(),
-                                 cos_t.data_ptr(), sin_t.data_ptr(), positions.data_ptr(), slots.data_ptr(), eps, n, n_heads, head_dim, rank,
-                                 rope_dim, out_at, pool.data_ptr(), num_blocks, max_position, stream_ptr(stream))
+    dtype, kv_stride = _dtype_of(name, kv, q), _row_stride(name, kv, n, 1, row)
+    status = lib().ql_mla_append(q_at, kv.data_ptr(), dtype, q_stride, kv_stride, norm_w.data_ptr(), cos_t.data_ptr(), sin_t.data_ptr(),
+                                 positions.data_ptr(), slots.data_ptr(), eps, n, n_heads, head_dim, rank, rope_dim, out_at, pool.data_ptr(),
+                                 num_blocks, max_position, stream_ptr(stream))
     if status:
         check(status)
 

@@ -171,23 +171,36 @@ __global__ void __launch_bounds__(512) mla_append_kernel(AppendParams p, DevErro
 
 }  // namespace
 
-int mla::attn_check(const char* name, const void* q, const void* w, const void* pool, const void* table, const void* lens, int head_dim,
-                    int rank, int rope_dim, int block_size, int64_t num_blocks, float scale, const void* out, const void* ws, size_t ws_bytes, size_t need) {
+// Whether [a, a + an) and [b, b + bn) share a byte.
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return an && bn && x < y + bn && y < x + an;
+}
+static bool aligned(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int mla::attn_check(const char* name, const AttnIn& a, size_t need) {
     const std::string nm(name);
-    if (!q || !w || !pool || !table || !lens || !out || !ws) return set_error(QL_EINVAL, nm + ": null pointer");
-    if (!mla::shape_ok(head_dim, rank) || rope_dim != kRope || block_size != mla::kBlock)
+    if (!a.q || !a.w || !a.pool || !a.table || !a.lens || !a.out || !a.ws) return set_error(QL_EINVAL, nm + ": null pointer");
+    if (!shape_ok(a.D, a.R) || a.rope != kRope || a.block != kBlock)
         return set_error(QL_EINVAL, nm + ": head_dim must be 64 or 128, rank 256 or 512, rope_dim 64, block_size 16");
-    if (need == 0 || num_blocks < 1 || num_blocks >= (1ll << 27))
-        return set_error(QL_EINVAL, nm + ": sizes out of range");
-    if (!(scale > 0.f && scale < INFINITY)) return set_error(QL_EINVAL, nm + ": the scale must be positive and finite");
-    auto aligned = [](const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
-    if (!aligned(q, 16) || !aligned(w, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(ws, 128))
+    if (need == 0 || a.num_blocks < 1 || a.num_blocks >= (1ll << 27)) return set_error(QL_EINVAL, nm + ": sizes out of range");
+    if (!(a.scale > 0.f && a.scale < INFINITY)) return set_error(QL_EINVAL, nm + ": the scale must be positive and finite");
+    if (!aligned(a.q, 16) || !aligned(a.w, 16) || !aligned(a.pool, 16) || !aligned(a.out, 16) || !aligned(a.ws, 128))
         return set_error(QL_EINVAL, nm + ": q, the weights, the pool and the output must be 16-byte, the workspace 128-byte aligned");
-    if (!aligned(table, 4) || !aligned(lens, 4)) return set_error(QL_EINVAL, nm + ": the table and the lengths must be 4-byte aligned");
-    if (ws_bytes < need) return set_error(QL_EINVAL, nm + ": the workspace is too small");
+    if (!aligned(a.table, 4) || !aligned(a.lens, 4)) return set_error(QL_EINVAL, nm + ": misaligned table or lengths");
+    if (a.ws_bytes < need) return set_error(QL_EINVAL, nm + ": the workspace is too small");
+    const size_t row = (size_t)a.rows * a.H;
+    const struct {
+        const void* p;
+        size_t n;
+    } in[] = {{a.q, row * (a.D + kRope) * 2}, {a.w, (size_t)a.H * 2 * a.D * a.R * 2}, {a.pool, (size_t)a.num_blocks * kBlock * (a.R + kRope) * 2},
+              {a.table, (size_t)a.tables * a.maxb * 4}, {a.lens, (size_t)a.tables * 4}};
+    for (const auto& i : in)
+        if (overlap(a.out, row * a.D * 2, i.p, i.n) || overlap(a.ws, need, i.p, i.n))
+            return set_error(QL_EINVAL, nm + ": the output or the workspace overlaps an input");
+    if (overlap(a.out, row * a.D * 2, a.ws, need)) return set_error(QL_EINVAL, nm + ": the output overlaps the workspace");
     return QL_OK;
 }
-
 }  // namespace ql
 
 extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride, int64_t kv_stride, const float* d_norm_w,
@@ -204,7 +217,6 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
     if (n == 0) return QL_OK;
     QL_REQUIRE(d_kv && d_norm_w && d_cos && d_sin && d_positions && d_slots && d_pool && (d_q == nullptr) == (d_q_out == nullptr),
                "ql_mla_append: null pointer");
-    auto aligned = [](const void* p, int k) { return (reinterpret_cast<uintptr_t>(p) & (k - 1)) == 0; };
     QL_REQUIRE(aligned(d_q, 16) && aligned(d_kv, 16) && aligned(d_norm_w, 16) && aligned(d_q_out, 16) && aligned(d_pool, 16),
                "ql_mla_append: rows, norm weights, the queries' output and the pool must be 16-byte aligned");
     QL_REQUIRE(aligned(d_cos, 8) && aligned(d_sin, 8) && aligned(d_positions, 4) && aligned(d_slots, 8),
@@ -213,6 +225,13 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
     QL_REQUIRE(n == 1 || (kv_stride >= rank + kRope && kv_stride % per == 0 && kv_stride < (1ll << 31) &&
                           (!d_q || (q_stride >= q_row && q_stride % per == 0 && q_stride < (1ll << 31)))),
                "ql_mla_append: row strides must be multiples of 16 bytes, at least a row and below 2^31");
+    const size_t size = dtype == QL_DTYPE_F32 ? 4 : 2, q_bytes = d_q ? ((n - 1) * (n > 1 ? q_stride : 0) + q_row) * size : 0;
+    const size_t kv_bytes = ((n - 1) * (n > 1 ? kv_stride : 0) + rank + kRope) * size, out_bytes = d_q ? (size_t)n * q_row * 2 : 0;
+    const size_t pool_bytes = (size_t)num_blocks * mla::kBlock * (rank + kRope) * 2;
+    QL_REQUIRE(!overlap(d_q_out, out_bytes, d_q, q_bytes) && !overlap(d_q_out, out_bytes, d_kv, kv_bytes) &&
+                   !overlap(d_q_out, out_bytes, d_pool, pool_bytes) && !overlap(d_pool, pool_bytes, d_q, q_bytes) &&
+                   !overlap(d_pool, pool_bytes, d_kv, kv_bytes),
+               "ql_mla_append: the queries' output and the pool overlap each other or an input");
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "ql_mla_append: no device error record");
     AppendParams p = {d_q, d_kv, q_stride, kv_stride, d_norm_w, d_cos, d_sin, d_positions,

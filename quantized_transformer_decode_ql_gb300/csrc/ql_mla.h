@@ -12,9 +12,18 @@ constexpr float kLag = 14.f; // log2 of how far a weight may lie above its refer
 
 inline bool shape_ok(int head_dim, int rank) { return (head_dim == 64 || head_dim == 128) && (rank == 256 || rank == 512); }
 
-// The checks that the attention entry points share; `need`: the workspace's bytes, 0 where the sizes are out of range.
-int attn_check(const char* name, const void* q, const void* w, const void* pool, const void* table, const void* lens, int head_dim, int rank,
-               int rope_dim, int block_size, int64_t num_blocks, float scale, const void* out, const void* ws, size_t ws_bytes, size_t need);
+// The arguments that the attention entry points share.
+struct AttnIn {
+    const void *q, *w, *pool;
+    const int32_t *table, *lens;      // lens: the lengths, or a chunk's position
+    int64_t rows, tables, maxb, num_blocks;   // rows of q and the output, rows of the table
+    int H, D, R, rope, block;
+    float scale;
+    void *out, *ws;
+    size_t ws_bytes;
+};
+// Their checks; `need`: the workspace's bytes, 0 where the sizes are out of range.
+int attn_check(const char* name, const AttnIn& a, size_t need);
 
 }  // namespace mla
 }  // namespace ql

@@ -33,7 +33,7 @@ struct ExpandParams {
 
 // Tokens of the context with the chunk, 0 where the position does not fit the table.
 __device__ __forceinline__ long long context(const int32_t* position, int n, long long maxb) {
-    const long long p = __ldg(position);
+    const long long p = __ldcg(position);
     return p >= 0 && p + n <= maxb * kBlock ? p + n : 0;
 }
 
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     // kernel before this one, and not at every tile
     bool gap = false;
     for (long long i = t; i < (L + kBlock - 1) / kBlock; i += kChunkThreads) {
-        const int id = __ldg(p.table + i);
+        const int id = __ldcg(p.table + i);
         gap |= id < 0 || id >= p.num_blocks;
     }
     gap = __syncthreads_or(gap);
@@ -697,15 +697,6 @@ static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     return s;
 }
 
-struct ChunkArgs {
-    const void *q, *w, *pool;
-    const int32_t *table, *position;
-    int64_t n, maxb, num_blocks;
-    int H;
-    float scale;
-    void *out, *ws;
-};
-
 // Clusters of two CTAs of a kernel that the current device holds at once, looked up once.
 template <typename K>
 static int pairs_at_once(K kernel, int threads, size_t smem, std::atomic<int>* known, int* out) {
@@ -730,7 +721,7 @@ static int pairs_at_once(K kernel, int threads, size_t smem, std::atomic<int>* k
 }
 
 template <int D, int R>
-static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
+static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
     using E = ExpandCfg<D, R>;
     using C = ChunkCfg<D>;
     DevError* err = device_error_record();
@@ -753,7 +744,7 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
         if (int rc = f16_tensor_map(a.w, 2, d, st, b, &ep.tw)) return rc;
     }
     {
-        const uint64_t w = (D + kRope) * 2, d[3] = {D + kRope, (uint64_t)a.n, (uint64_t)a.H}, st[2] = {a.H * w, w};
+        const uint64_t w = (D + kRope) * 2, d[3] = {D + kRope, (uint64_t)a.rows, (uint64_t)a.H}, st[2] = {a.H * w, w};
         const uint32_t b[3] = {64, kQ, 1};
         if (int rc = f16_tensor_map(a.q, 3, d, st, b, &cp.tq)) return rc;
     }
@@ -773,14 +764,14 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     }
     ep.pool = static_cast<const __half*>(a.pool);
     ep.table = cp.table = a.table;
-    ep.position = cp.position = a.position;
+    ep.position = cp.position = a.lens;
     ep.turned = reinterpret_cast<__half*>(ws + sh.turned);
     ep.live = reinterpret_cast<int*>(ws + sh.live);
     cp.live = ep.live;
     ep.maxb = cp.maxb = a.maxb;
     ep.num_blocks = cp.num_blocks = a.num_blocks;
     ep.cap = cp.cap = sh.cap;
-    ep.n = cp.n = (int)a.n;
+    ep.n = cp.n = (int)a.rows;
     ep.H = cp.H = a.H;
     ep.err = cp.err = err;
     ep.ns = cp.ns = 2000000000ull;
@@ -795,12 +786,12 @@ static int chunk_go(const ChunkArgs& a, const ChunkShape& sh, cudaStream_t s) {
     if (int rc = pairs_at_once(mla_expand_kernel<D, R>, E::THREADS, E::SMEM, most, &pairs)) return rc;
     if (int rc = pairs_at_once(mla_chunk_kernel<D>, kChunkThreads, C::SMEM, most2, &pairs2)) return rc;
     pairs = (int)std::min<int64_t>(pairs, sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS));
-    pairs2 = (int)std::min<int64_t>(pairs2, (a.n + 2 * kQ - 1) / (2 * kQ) * a.H * sh.splits);
+    pairs2 = (int)std::min<int64_t>(pairs2, (a.rows + 2 * kQ - 1) / (2 * kQ) * a.H * sh.splits);
     cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(E::THREADS), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
         e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), C::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.splits > 1)
-        e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.n * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
+        e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.rows * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");
 }
 
@@ -820,12 +811,10 @@ extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void
                                  void* d_workspace, size_t workspace_bytes, void* stream) {
     using namespace ql;
     using namespace ql::mla;
-    if (int rc = attn_check("ql_mla_attn_chunk", d_q, d_w_kv, d_pool, d_block_table, d_position, head_dim, rank, rope_dim, block_size,
-                            num_blocks, scale, d_out, d_workspace, workspace_bytes,
-                            ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq)))
-        return rc;
+    const AttnIn a = {d_q, d_w_kv, d_pool, d_block_table, d_position, n_tokens, 1, max_blocks_per_seq, num_blocks, n_heads, head_dim, rank,
+                      rope_dim, block_size, scale, d_out, d_workspace, workspace_bytes};
+    if (int rc = attn_check("ql_mla_attn_chunk", a, ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq))) return rc;
     const ChunkShape sh = chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq);
-    const ChunkArgs a = {d_q, d_w_kv, d_pool, d_block_table, d_position, n_tokens, max_blocks_per_seq, num_blocks, n_heads, scale, d_out, d_workspace};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (head_dim == 128) return rank == 512 ? chunk_go<128, 512>(a, sh, s) : chunk_go<128, 256>(a, sh, s);
     return rank == 512 ? chunk_go<64, 512>(a, sh, s) : chunk_go<64, 256>(a, sh, s);

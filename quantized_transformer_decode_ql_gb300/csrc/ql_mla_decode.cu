@@ -169,7 +169,8 @@ struct Window {
 };
 
 // Every CTA cuts the batch by itself, from the lengths: it starts before the absorbed queries are there, and so this and its
-// first tiles' copies cost nothing.
+// first tiles' copies cost nothing. (Lengths, tables and the cache are older than the kernel that makes the queries, which lets this
+// one start only once it has waited for what came before it; they are read from L2, past whatever an SM may still hold.)
 template <int THREADS>
 __device__ Window make_window(const DecodeParams& p, int win) {
     constexpr int WARPS = THREADS / 32;
@@ -177,7 +178,7 @@ __device__ Window make_window(const DecodeParams& p, int win) {
     __shared__ int found[2];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     auto places = [&](int b) {
-        const int len = b < p.batch ? __ldg(p.lens + b) : 0, n = tiles_checked(len, p.cap);
+        const int len = b < p.batch ? __ldcg(p.lens + b) : 0, n = tiles_checked(len, p.cap);
         if (len != 0 && n == 0 && blockIdx.x == 0) record_device_error(p.err, kErrAttnLength, b, len);
         return n ? n + kEnter : 0;
     };
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     auto sequences = [&](auto each) {
         int start = window.lo < window.hi ? window.start : window.hi;
         for (int b = window.first; b < p.batch && start < window.hi; ++b) {
-            const int len = __ldg(p.lens + b), n = tiles_checked(len, p.cap);
+            const int len = __ldcg(p.lens + b), n = tiles_checked(len, p.cap);
             if (n == 0) continue;
             const int t0 = max(window.lo - start - kEnter, 0), t1 = min(window.hi - start - kEnter, n);
             start += n + kEnter;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
             }
             const int nblk = (len + kBlock - 1) / kBlock;
             const int32_t* table = p.tables + (size_t)b * p.maxb;
-            auto load_id = [&](int tt) { return lane < 4 && 4 * tt + lane < nblk ? __ldg(table + 4 * tt + lane) : -1; };
+            auto load_id = [&](int tt) { return lane < 4 && 4 * tt + lane < nblk ? __ldcg(table + 4 * tt + lane) : -1; };
             int id = load_id(t0);
             for (int tt = t0; tt < t1; ++tt, ++it) {
                 if (first && it == C::STAGES) {   // the absorbed queries are the previous kernel's; what the cache holds is older
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
         // the places of all sequences and of those before this cluster's, as the attention counts them
         int all = 0, before = 0;
         for (int b = t; b < p.batch; b += kJoinThreads) {
-            const int n = tiles_checked(__ldg(p.lens + b), p.cap);
+            const int n = tiles_checked(__ldcg(p.lens + b), p.cap);
             all += n ? n + kEnter : 0;
             before += n && b < b0 ? n + kEnter : 0;
         }
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
                 before += places[1][i];
             }
             const int W = max(1, (all + p.windows - 1) / p.windows), b = b0 + t;
-            const int n = t < p.rows && b < p.batch ? tiles_checked(__ldg(p.lens + b), p.cap) : 0, mine = n ? n + kEnter : 0;
+            const int n = t < p.rows && b < p.batch ? tiles_checked(__ldcg(p.lens + b), p.cap) : 0, mine = n ? n + kEnter : 0;
             int at = mine;
 #pragma unroll
             for (int o = 1; o < kJoinRows; o <<= 1) {
@@ -777,17 +778,8 @@ static DecodeShape decode_shape(int64_t batch, int H, int R) {
     return s;
 }
 
-struct DecodeArgs {
-    const void *q, *w, *pool;
-    const int32_t *tables, *lens;
-    int64_t batch, maxb, num_blocks;
-    int H;
-    float scale;
-    void *out, *ws;
-};
-
 template <int D, int R, int NH>
-static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s) {
+static int decode_go(const AttnIn& a, const DecodeShape& sh, cudaStream_t s) {
     using C = Cfg<R, NH>;
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "ql_mla_attn_decode: no device error record");
@@ -796,35 +788,35 @@ static int decode_go(const DecodeArgs& a, const DecodeShape& sh, cudaStream_t s)
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     int windows = std::min(num_sms(), kMaxWin) / sh.groups;
     if (windows < 1) windows = 1;
-    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws), (int)a.batch, a.H, C::HALVES, err};
+    AbsorbParams ap = {static_cast<const __half*>(a.q), static_cast<const __half*>(a.w), reinterpret_cast<__half*>(ws), (int)a.rows, a.H, C::HALVES, err};
     DecodeParams dp = {};
     const uint64_t row = (R + kRope) * 2;
     const uint64_t kd[4] = {64, 8, (uint64_t)C::CH, (uint64_t)a.num_blocks * 2}, kst[3] = {row, 128, 8 * row};
     const uint32_t kb[4] = {64, 8, (uint32_t)C::CH, 2};
     if (int rc = f16_tensor_map(a.pool, 4, kd, kst, kb, &dp.tk)) return rc;
-    const uint64_t qd[5] = {64, (uint64_t)a.H, C::HALVES, (uint64_t)C::CH, (uint64_t)a.batch}, qst[4] = {row, a.H * row, 128, C::HALVES * a.H * row};
+    const uint64_t qd[5] = {64, (uint64_t)a.H, C::HALVES, (uint64_t)C::CH, (uint64_t)a.rows}, qst[4] = {row, a.H * row, 128, C::HALVES * a.H * row};
     const uint32_t qb[5] = {64, (uint32_t)NH, C::HALVES, (uint32_t)C::CH, 1};
     if (int rc = f16_tensor_map(ws, 5, qd, qst, qb, &dp.tq)) return rc;
-    dp.tables = a.tables;
+    dp.tables = a.table;
     dp.lens = a.lens;
     dp.parts = reinterpret_cast<float*>(ws + sh.parts);
     dp.stats = reinterpret_cast<float2*>(ws + sh.stats);
     dp.maxb = a.maxb;
     dp.cap = (long long)a.maxb * kBlock;
     dp.num_blocks = a.num_blocks;
-    dp.batch = (int)a.batch;
+    dp.batch = (int)a.rows;
     dp.H = a.H;
     dp.windows = windows;
     dp.groups = sh.groups;
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.batch, a.H, windows, kJoinRows};
-    while (jp.rows > 1 && jp.rows / 2 >= a.batch) jp.rows /= 2;
-    cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64)), (unsigned)((a.batch + 63) / 64)), dim3(128), 0, s, true, ap);
+    JoinParams jp = {ap.w, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.rows, a.H, windows, kJoinRows};
+    while (jp.rows > 1 && jp.rows / 2 >= a.rows) jp.rows /= 2;
+    cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64)), (unsigned)((a.rows + 63) / 64)), dim3(128), 0, s, true, ap);
     if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(C::THREADS), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
-        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)(a.H * kJoinCtas), (unsigned)((a.batch + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
+        e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)(a.H * kJoinCtas), (unsigned)((a.rows + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
                    true, jp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_decode");
 }
@@ -845,12 +837,10 @@ extern "C" int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const voi
                                   void* d_workspace, size_t workspace_bytes, void* stream) {
     using namespace ql;
     using namespace ql::mla;
-    if (int rc = attn_check("ql_mla_attn_decode", d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, head_dim, rank, rope_dim, block_size,
-                            num_blocks, scale, d_out, d_workspace, workspace_bytes,
-                            ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq)))
-        return rc;
+    const AttnIn a = {d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, batch, batch, max_blocks_per_seq, num_blocks, n_heads, head_dim, rank,
+                      rope_dim, block_size, scale, d_out, d_workspace, workspace_bytes};
+    if (int rc = attn_check("ql_mla_attn_decode", a, ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq))) return rc;
     const DecodeShape sh = decode_shape(batch, n_heads, rank);
-    const DecodeArgs a = {d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, batch, max_blocks_per_seq, num_blocks, n_heads, scale, d_out, d_workspace};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool small = sh.NH == 32;
     if (head_dim == 128) {

@@ -180,6 +180,17 @@ def test_decode_many_short_sequences(rank):
     check_decode(c, decode(c))
 
 
+def test_decode_a_full_sequence_among_5000_empty_ones():
+    """More sequences than a CTA has threads, most of them idle or of one token."""
+    lens = np.zeros(5000, np.int64)
+    lens[::371] = 1
+    lens[4321] = 3000
+    c = latent_case(list(lens), 2, 64, 256, seed=8, stale=np.nan)
+    got = decode(c)
+    assert np.all(got[lens == 0] == 5.0)
+    check_decode(c, got, skip=set(np.flatnonzero(lens == 0)))
+
+
 @pytest.mark.parametrize("order", ["rising", "falling", "one", "small", "large"])
 def test_decode_scores(order):
     """Scores that rise along the context (each tile's largest far above the last one's), fall, hold one key that
@@ -391,6 +402,75 @@ def test_chunk_bad_blocks_and_positions():
 
 
 # ---------------------------------------------------------------- together
+@pytest.mark.parametrize("graph", [False, True])
+def test_steps_without_a_pause(graph):
+    """60 steps of three sequences issued one after the other: each step's rows, slots, lengths and table entries are written on the
+    stream right before the kernels that read them, while the kernels of the step before may still run."""
+    ql = lib()
+    heads, hd, rank, B, steps, start = 9, 64, 256, 3, 60, (1, 250, 63)
+    g = np.random.default_rng(11)
+    cos, sin = (dev(x) for x in tables(512))
+    w = (g.standard_normal((heads, 2 * hd, rank)) / math.sqrt(rank)).astype(np.float16)
+    maxb, blocks = 20, 70
+    ids = g.permutation(blocks)[:B * maxb].reshape(B, maxb).astype(np.int32)
+    pool = torch.full((blocks, 16, rank + 64), math.nan, dtype=torch.float16, device="cuda")
+    first = [g.standard_normal((n, rank + 64)).astype(np.float16) for n in start]
+    for b in range(B):
+        for t in range(start[b]):
+            pool[int(ids[b, t // 16]), t % 16] = dev(first[b][t])
+    whole = dev(ids)
+    table = torch.full((B, maxb), -1, dtype=torch.int32, device="cuda")
+    lens = dev(np.array(start, np.int32))
+    q = dev(g.standard_normal((steps, B, heads, hd + 64)).astype(np.float32))
+    kv = dev(g.standard_normal((steps, B, rank + 64)).astype(np.float32))
+    at = torch.zeros(1, dtype=torch.int64, device="cuda")
+    norm, wd = torch.ones(rank, device="cuda"), dev(w)
+    q_out = torch.zeros((B, heads, hd + 64), dtype=torch.float16, device="cuda")
+    out = torch.zeros((B, heads, hd), dtype=torch.float16, device="cuda")
+    ws = torch.empty(ql.ql_mla_decode_workspace_bytes(B, heads, hd, rank, maxb), dtype=torch.uint8, device="cuda")
+    outs, qs = torch.zeros((steps, *out.shape), dtype=torch.float16, device="cuda"), torch.zeros((steps, *q_out.shape), dtype=torch.float16, device="cuda")
+    blk = torch.arange(maxb, device="cuda")
+
+    def step():
+        pos = lens.clone()
+        slots = whole.gather(1, (pos // 16).long()[:, None])[:, 0].long() * 16 + pos % 16
+        table.copy_(torch.where(blk[None] <= (pos // 16)[:, None], whole, torch.full_like(whole, -1)))
+        ql.ql_mla_append(q.index_select(0, at)[0], kv.index_select(0, at)[0], norm, cos, sin, pos, slots, EPS, heads, hd, rank, 64, q_out, pool,
+                         blocks, 512)
+        lens.add_(1)
+        ql.ql_mla_attn_decode(q_out, wd, pool, table, lens, B, heads, hd, rank, 64, 16, maxb, blocks, 0.1, out, ws)
+        outs.index_copy_(0, at, out[None])
+        qs.index_copy_(0, at, q_out[None])
+        at.add_(1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        if graph:
+            keep = (lens.clone(), at.clone(), pool.clone())
+            step()
+            for t, k in zip((lens, at, pool), keep):
+                t.copy_(k)
+            torch.cuda.synchronize()
+            recorded = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(recorded, stream=s):
+                step()
+            for _ in range(steps):
+                recorded.replay()
+        else:
+            for _ in range(steps):
+                step()
+    torch.cuda.synchronize()
+    ql.ql_check_device_error()
+    rows = pool.cpu().numpy()
+    got, qn = outs.cpu().numpy().astype(np.float64), qs.cpu().numpy()
+    for b in range(B):
+        seq = rows[ids[b]].reshape(-1, rank + 64)
+        assert np.array_equal(seq[:start[b]], first[b])
+        for i in range(0, steps, 7):
+            want, bound = mla.absorbed(qn[i, b], seq[:start[b] + i + 1], w, 0.1)
+            assert np.all(np.abs(got[i, b] - want) <= bound), (b, i)
+
+
 @pytest.mark.parametrize("heads,hd,rank", [(6, 64, 256), (34, 128, 512)])
 def test_prompt_then_tokens(heads, hd, rank):
     """Two sequences: a prompt in two chunks each, then single tokens of both, each step's rows appended by the operator
