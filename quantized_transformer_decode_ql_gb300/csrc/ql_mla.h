@@ -22,6 +22,9 @@ struct AttnIn {
     void *out, *ws;
     size_t ws_bytes;
 };
+// The absorbed form of a's rows: sequences with a length each, or (chunk) one sequence's queries from the position on (ql_mla_decode.cu).
+int absorbed_launch(const AttnIn& a, bool chunk, cudaStream_t s);
+size_t absorbed_workspace(int64_t rows, int H, int R);
 // Their checks; `need`: the workspace's bytes, 0 where the sizes are out of range.
 int attn_check(const char* name, const AttnIn& a, size_t need);
 

@@ -667,6 +667,13 @@ __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- host
+// Few queries go through the absorbed form, each for itself over the cache: a query costs it the context's rows once per 64 heads,
+// where the expanded form first makes every head's keys and values. Both grow with the context, which the host does not know.
+// Expanded / absorbed in us, 32 heads of 128, rank 512, after 8000 tokens: 84 / 18 (1 token), 84 / 27 (8), 85 / 55 (32), 85 / 80 (48);
+// with no context 18 / 12, 19 / 13, 19 / 18, 20 / 25. 128 heads after 8000: 333 / 123 (32), 344 / 339 (96); with no context
+// 24 / 27 (16), 24 / 41 (32). 8 heads of 64, rank 256, after 8000: 24 / 15 (4), 24 / 24 (16).
+static bool few(int64_t n, int H, int D) { return n <= 32 && n * 128 <= (int64_t)H * D; }
+
 struct ChunkShape {
     int splits;
     long long cap;                                       // rows of the keys and values a head
@@ -695,6 +702,12 @@ static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     s.parts = s.stats + (s.splits > 1 ? up((size_t)s.splits * n * H * 8) : 0);
     s.total = s.parts + (s.splits > 1 ? up((size_t)s.splits * n * H * D * 4) : 0);
     return s;
+}
+
+// Bytes of the workspace that a call uses; 0 where its sizes are out of range.
+static size_t chunk_need(int64_t n, int H, int D, int R, int64_t maxb) {
+    if (!shape_ok(D, R) || n < 1 || n > 65535 || H < 1 || H > 1024 || n * H >= (1 << 22) || maxb < 1 || maxb > (1 << 16)) return 0;
+    return few(n, H, D) ? absorbed_workspace(n, H, R) : chunk_shape(n, H, D, maxb).total;
 }
 
 // Clusters of two CTAs of a kernel that the current device holds at once, looked up once.
@@ -799,10 +812,14 @@ static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
 }  // namespace ql
 
 extern "C" size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
-    if (!ql::mla::shape_ok(head_dim, rank) || n_tokens < 1 || n_tokens > 65535 || n_heads < 1 || n_heads > 1024 ||
-        n_tokens * n_heads >= (1 << 22) || max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 16))
-        return 0;
-    return ql::mla::chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq).total;
+    // Fewer tokens may split their keys further, or take the other form: the most that any number up to n_tokens needs.
+    size_t most = ql::mla::chunk_need(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq);
+    if (most == 0) return 0;
+    for (int64_t n = 2 * ql::mla::kQ; n < n_tokens && n / (2 * ql::mla::kQ) * n_heads < 152; n += 2 * ql::mla::kQ)
+        most = std::max(most, ql::mla::chunk_need(n, n_heads, head_dim, rank, max_blocks_per_seq));
+    for (int64_t n = std::min<int64_t>(n_tokens, 32); n > 0; --n)
+        most = std::max(most, ql::mla::chunk_need(n, n_heads, head_dim, rank, max_blocks_per_seq));
+    return most;
 }
 
 extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
@@ -813,9 +830,10 @@ extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void
     using namespace ql::mla;
     const AttnIn a = {d_q, d_w_kv, d_pool, d_block_table, d_position, n_tokens, 1, max_blocks_per_seq, num_blocks, n_heads, head_dim, rank,
                       rope_dim, block_size, scale, d_out, d_workspace, workspace_bytes};
-    if (int rc = attn_check("ql_mla_attn_chunk", a, ql_mla_chunk_workspace_bytes(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq))) return rc;
-    const ChunkShape sh = chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq);
+    if (int rc = attn_check("ql_mla_attn_chunk", a, chunk_need(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (few(n_tokens, n_heads, head_dim)) return absorbed_launch(a, true, s);
+    const ChunkShape sh = chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq);
     if (head_dim == 128) return rank == 512 ? chunk_go<128, 512>(a, sh, s) : chunk_go<128, 256>(a, sh, s);
     return rank == 512 ? chunk_go<64, 512>(a, sh, s) : chunk_go<64, 256>(a, sh, s);
 }

@@ -22,6 +22,20 @@ __host__ __device__ inline int tiles_of(int len) { return (len + kTile - 1) / kT
 // Tiles of a sequence; 0 for an idle slot and for a length outside the table.
 __device__ __forceinline__ int tiles_checked(int len, long long cap) { return len > 0 && len <= cap ? tiles_of(len) : 0; }
 
+// The lengths of the batch's rows: an array, or those of a chunk's queries (row b sees one key more than row b - 1; -1 where
+// the chunk does not fit the table).
+struct Lengths {
+    const int32_t* lens;
+    const int32_t* position;   // null: lens
+    int batch;
+    long long cap;             // longest length
+    __device__ int operator()(int b) const {
+        if (position == nullptr) return __ldcg(lens + b);
+        const long long p = __ldcg(position);
+        return p >= 0 && p + batch <= cap ? (int)p + b + 1 : -1;
+    }
+};
+
 // ---------------------------------------------------------------- the absorbed queries
 struct AbsorbParams {
     const __half* q;       // [batch][H][D + 64]
@@ -136,10 +150,10 @@ struct DecodeParams {
     CUtensorMap tk;        // the pool: [group of 8 rows][run][row][64 values]
     CUtensorMap tq;        // absorbed queries: [sequence][run][half][head][64 values]
     const int32_t* tables;
-    const int32_t* lens;
+    Lengths lens;
     float* parts;          // [head group][window + sequence][NH][R]
     float2* stats;         // [head group][window + sequence][NH]: reference (log2) and sum of the weights
-    long long maxb, cap, num_blocks;
+    long long maxb, cap, num_blocks;   // maxb: entries from a row's table to the next (0: one table)
     int batch, H, windows, groups;
     float scale_log2;
     DevError* err;
@@ -178,7 +192,7 @@ __device__ Window make_window(const DecodeParams& p, int win) {
     __shared__ int found[2];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     auto places = [&](int b) {
-        const int len = b < p.batch ? __ldcg(p.lens + b) : 0, n = tiles_checked(len, p.cap);
+        const int len = b < p.batch ? p.lens(b) : 0, n = tiles_checked(len, p.cap);
         if (len != 0 && n == 0 && blockIdx.x == 0) record_device_error(p.err, kErrAttnLength, b, len);
         return n ? n + kEnter : 0;
     };
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     auto sequences = [&](auto each) {
         int start = window.lo < window.hi ? window.start : window.hi;
         for (int b = window.first; b < p.batch && start < window.hi; ++b) {
-            const int len = __ldcg(p.lens + b), n = tiles_checked(len, p.cap);
+            const int len = p.lens(b), n = tiles_checked(len, p.cap);
             if (n == 0) continue;
             const int t0 = max(window.lo - start - kEnter, 0), t1 = min(window.hi - start - kEnter, n);
             start += n + kEnter;
@@ -319,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                 }
                 const int s = it % C::STAGES;
                 const bool in = lane < 4 && 4 * tt + lane < nblk, live = in && id >= 0 && id < p.num_blocks;
-                if (in && !live && hg == 0) record_device_error(p.err, kErrAttnBlock, (long long)b * p.maxb + 4 * tt + lane, id);
+                if (in && !live && hg == 0) record_device_error(p.err, kErrAttnBlock, b * p.maxb + 4 * tt + lane, id);
                 const unsigned mask = __ballot_sync(0xffffffffu, live) & 15u;
                 const int now = live ? 2 * id : 2 * (int)p.num_blocks;   // outside: zeros
                 if (tt + 1 < t1) id = load_id(tt + 1);
@@ -577,7 +591,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
 // ---------------------------------------------------------------- parts joined, values projected
 struct JoinParams {
     const __half* w;       // [H][2 D][R]
-    const int32_t* lens;
+    Lengths lens;
     const float* parts;
     const float2* stats;
     __half* out;           // [batch][H][D]
@@ -613,7 +627,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
         // the places of all sequences and of those before this cluster's, as the attention counts them
         int all = 0, before = 0;
         for (int b = t; b < p.batch; b += kJoinThreads) {
-            const int n = tiles_checked(__ldcg(p.lens + b), p.cap);
+            const int n = tiles_checked(p.lens(b), p.cap);
             all += n ? n + kEnter : 0;
             before += n && b < b0 ? n + kEnter : 0;
         }
@@ -634,7 +648,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
                 before += places[1][i];
             }
             const int W = max(1, (all + p.windows - 1) / p.windows), b = b0 + t;
-            const int n = t < p.rows && b < p.batch ? tiles_checked(__ldcg(p.lens + b), p.cap) : 0, mine = n ? n + kEnter : 0;
+            const int n = t < p.rows && b < p.batch ? tiles_checked(p.lens(b), p.cap) : 0, mine = n ? n + kEnter : 0;
             int at = mine;
 #pragma unroll
             for (int o = 1; o < kJoinRows; o <<= 1) {
@@ -779,10 +793,10 @@ static DecodeShape decode_shape(int64_t batch, int H, int R) {
 }
 
 template <int D, int R, int NH>
-static int decode_go(const AttnIn& a, const DecodeShape& sh, cudaStream_t s) {
+static int decode_go(const AttnIn& a, bool chunk, const DecodeShape& sh, cudaStream_t s) {
     using C = Cfg<R, NH>;
     DevError* err = device_error_record();
-    if (!err) return set_error(QL_ECUDA, "ql_mla_attn_decode: no device error record");
+    if (!err) return set_error(QL_ECUDA, "latent attention: no device error record");
     static std::atomic<unsigned long long> done{0};
     QL_TRY_CUDA(allow_smem_once(mla_decode_kernel<R, NH>, C::SMEM, done));
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
@@ -798,10 +812,10 @@ static int decode_go(const AttnIn& a, const DecodeShape& sh, cudaStream_t s) {
     const uint32_t qb[5] = {64, (uint32_t)NH, C::HALVES, (uint32_t)C::CH, 1};
     if (int rc = f16_tensor_map(ws, 5, qd, qst, qb, &dp.tq)) return rc;
     dp.tables = a.table;
-    dp.lens = a.lens;
+    dp.lens = {chunk ? nullptr : a.lens, chunk ? a.lens : nullptr, (int)a.rows, (long long)a.maxb * kBlock};
     dp.parts = reinterpret_cast<float*>(ws + sh.parts);
     dp.stats = reinterpret_cast<float2*>(ws + sh.stats);
-    dp.maxb = a.maxb;
+    dp.maxb = chunk ? 0 : a.maxb;
     dp.cap = (long long)a.maxb * kBlock;
     dp.num_blocks = a.num_blocks;
     dp.batch = (int)a.rows;
@@ -811,14 +825,27 @@ static int decode_go(const AttnIn& a, const DecodeShape& sh, cudaStream_t s) {
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, a.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.rows, a.H, windows, kJoinRows};
+    JoinParams jp = {ap.w, dp.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.rows, a.H, windows, kJoinRows};
     while (jp.rows > 1 && jp.rows / 2 >= a.rows) jp.rows /= 2;
     cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64)), (unsigned)((a.rows + 63) / 64)), dim3(128), 0, s, true, ap);
     if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(C::THREADS), C::SMEM, s, true, dp);
     if (e == cudaSuccess)
         e = launch(mla_join_kernel<D, R, NH>, dim3((unsigned)(a.H * kJoinCtas), (unsigned)((a.rows + jp.rows - 1) / jp.rows)), dim3(kJoinThreads), 0, s,
                    true, jp);
-    return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_decode");
+    return e == cudaSuccess ? QL_OK : cuda_error(e, "latent attention, absorbed form");
+}
+
+size_t absorbed_workspace(int64_t rows, int H, int R) { return decode_shape(rows, H, R).total; }
+
+int absorbed_launch(const AttnIn& a, bool chunk, cudaStream_t s) {
+    const DecodeShape sh = decode_shape(a.rows, a.H, a.R);
+    const bool small = sh.NH == 32;
+    if (a.D == 128) {
+        if (a.R == 512) return small ? decode_go<128, 512, 32>(a, chunk, sh, s) : decode_go<128, 512, 64>(a, chunk, sh, s);
+        return small ? decode_go<128, 256, 32>(a, chunk, sh, s) : decode_go<128, 256, 64>(a, chunk, sh, s);
+    }
+    if (a.R == 512) return small ? decode_go<64, 512, 32>(a, chunk, sh, s) : decode_go<64, 512, 64>(a, chunk, sh, s);
+    return small ? decode_go<64, 256, 32>(a, chunk, sh, s) : decode_go<64, 256, 64>(a, chunk, sh, s);
 }
 
 }  // namespace mla
@@ -828,7 +855,7 @@ extern "C" size_t ql_mla_decode_workspace_bytes(int64_t batch, int n_heads, int 
     if (!ql::mla::shape_ok(head_dim, rank) || batch < 1 || batch > 65535 || n_heads < 1 || n_heads > 1024 || batch * n_heads >= (1 << 22) ||
         max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 20) || batch * max_blocks_per_seq >= (1ll << 32))
         return 0;
-    return ql::mla::decode_shape(batch, n_heads, rank).total;
+    return ql::mla::absorbed_workspace(batch, n_heads, rank);
 }
 
 extern "C" int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_tables,
@@ -840,13 +867,5 @@ extern "C" int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const voi
     const AttnIn a = {d_q, d_w_kv, d_pool, d_block_tables, d_context_lens, batch, batch, max_blocks_per_seq, num_blocks, n_heads, head_dim, rank,
                       rope_dim, block_size, scale, d_out, d_workspace, workspace_bytes};
     if (int rc = attn_check("ql_mla_attn_decode", a, ql_mla_decode_workspace_bytes(batch, n_heads, head_dim, rank, max_blocks_per_seq))) return rc;
-    const DecodeShape sh = decode_shape(batch, n_heads, rank);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool small = sh.NH == 32;
-    if (head_dim == 128) {
-        if (rank == 512) return small ? decode_go<128, 512, 32>(a, sh, s) : decode_go<128, 512, 64>(a, sh, s);
-        return small ? decode_go<128, 256, 32>(a, sh, s) : decode_go<128, 256, 64>(a, sh, s);
-    }
-    if (rank == 512) return small ? decode_go<64, 512, 32>(a, sh, s) : decode_go<64, 512, 64>(a, sh, s);
-    return small ? decode_go<64, 256, 32>(a, sh, s) : decode_go<64, 256, 64>(a, sh, s);
+    return absorbed_launch(a, false, static_cast<cudaStream_t>(stream));
 }

@@ -332,7 +332,18 @@ def chunk(c, n, before, out=None, table=None, position=None):
     return out.cpu().numpy().astype(np.float64)
 
 
-CHUNK = [(1, 0, 1, 64, 256), (1, 0, 32, 128, 512), (17, 0, 4, 64, 256), (16, 1, 2, 128, 512), (128, 0, 3, 128, 256), (129, 0, 2, 64, 512),
+def chunk_bound(c, n, before):
+    """The oracle's answer and its bound for the form that the call takes: up to 32 tokens, and n_heads * head_dim / 128, go through the
+    absorbed one."""
+    rows = rows_of(c, 0, before + n)
+    if n > 32 or n * 128 > c["heads"] * c["hd"]:
+        return mla.attention(c["q"], rows, c["w"], c["scale"], before=before)
+    both = [mla.absorbed(c["q"][i], rows[:before + i + 1], c["w"], c["scale"]) for i in range(n)]
+    return np.stack([x for x, _ in both]), np.stack([x for _, x in both])
+
+
+CHUNK = [(5, 300, 5, 128, 256), (6, 300, 5, 128, 256), (32, 1000, 64, 64, 512), (33, 1000, 64, 64, 512), (20, 0, 33, 128, 512),
+         (32, 500, 96, 128, 256), (33, 500, 96, 128, 256), (1, 0, 1, 64, 256), (1, 0, 32, 128, 512), (17, 0, 4, 64, 256), (16, 1, 2, 128, 512), (128, 0, 3, 128, 256), (129, 0, 2, 64, 512),
          (1, 700, 5, 128, 512), (7, 121, 3, 64, 256), (100, 1000, 2, 128, 512), (300, 333, 7, 64, 256), (513, 0, 2, 128, 512),
          (64, 2500, 1, 64, 512), (200, 57, 33, 64, 256), (40, 3, 70, 64, 512)]
 
@@ -341,7 +352,7 @@ CHUNK = [(1, 0, 1, 64, 256), (1, 0, 32, 128, 512), (17, 0, 4, 64, 256), (16, 1, 
 def test_chunk(n, before, heads, hd, rank):
     c = latent_case([before + n], heads, hd, rank, rows=n, seed=n + heads, stale=np.nan)
     got = chunk(c, n, before)
-    want, bound = mla.attention(c["q"], rows_of(c, 0, before + n), c["w"], c["scale"], before=before)
+    want, bound = chunk_bound(c, n, before)
     assert np.all(np.abs(got - want) <= bound), float(np.max(np.abs(got - want) / bound))
     lib().ql_check_device_error()
 
@@ -373,10 +384,12 @@ def test_chunk_scores(order):
     assert np.all(np.abs(got - want) <= bound)
 
 
-def test_chunk_bad_blocks_and_positions():
+@pytest.mark.parametrize("heads", [3, 90])
+def test_chunk_bad_blocks_and_positions(heads):
+    """(The second in the absorbed form: 24 tokens are few for 90 heads of 128.)"""
     ql = lib()
-    n, before = 40, 100
-    c = latent_case([n + before], 3, 64, 256, rows=n, seed=5)
+    n, before = 40 if heads == 3 else 24, 100
+    c = latent_case([n + before], heads, 64 if heads == 3 else 128, 256, rows=n, seed=5)
     table = c["table"].copy()
     table[0, 1], table[0, 7] = c["blocks"], -3
     got = chunk(c, n, before, table=table)
@@ -386,8 +399,9 @@ def test_chunk_bad_blocks_and_positions():
     keep = np.concatenate([np.arange(16), np.arange(32, 112), np.arange(128, 140)])
     for i in range(n):
         some = keep[keep <= before + i]
-        want, bound = mla.attention(c["q"][i:i + 1], rows[some], c["w"], c["scale"])
-        assert np.all(np.abs(got[i:i + 1] - want) <= bound)
+        want, bound = mla.attention(c["q"][i:i + 1], rows[some], c["w"], c["scale"]) if heads == 3 else mla.absorbed(
+            c["q"][i], rows[some], c["w"], c["scale"])
+        assert np.all(np.abs(got[i] - want.reshape(got[i].shape)) <= bound.reshape(got[i].shape))
     # the first queries see only keys of a bad block
     table = c["table"].copy()
     table[0, 0] = -1

@@ -161,3 +161,9 @@ def test_append_refusals():
         assert L.ql_mla_append(*{**good, **bad}.values()) == ql.QL_EINVAL, bad
         assert "ql_mla_append" in L.ql_last_error().decode()
     assert L.ql_mla_append(*{**good, "n": 0}.values()) == ql.QL_OK
+
+
+@pytest.mark.parametrize("heads,hd,rank,maxb", [(1, 64, 256, 4096), (3, 128, 512, 2048), (32, 128, 512, 512), (90, 64, 256, 64), (1024, 128, 256, 8)])
+def test_chunk_workspace_is_enough_for_fewer_tokens(heads, hd, rank, maxb):
+    need = [ql.ql_mla_chunk_workspace_bytes(n, heads, hd, rank, maxb) for n in range(1, 2000)]
+    assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))
