@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
+    __shared__ int rows_now;    // read once, so that all warps run the same tiles
     __shared__ float tops[2][2][kQ], sums[2][2][2][kQ], refs[2][2][kQ];   // (sums and refs of two units in turn)
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t rank = cluster_rank();
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     if (t == 0) {
         for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 || i == C::kOFree ? kSoft : 1);
         abort_flag = 0;
+        rows_now = (int)context(p.position, p.n, p.maxb);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.tq);
         prefetch_map(&p.tk);
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0), there = in_cta(bar, 0);
     const Waits wt = {p.err, &abort_flag, p.ns};
     const Waits alone = {p.err, nullptr, p.ns};
-    const long long L = context(p.position, p.n, p.maxb);
+    const long long L = rows_now;
     // whether a block of the context is missing (its keys are then left out): the rare case is told apart here, once, beside the
     // kernel before this one, and not at every tile
     bool gap = false;

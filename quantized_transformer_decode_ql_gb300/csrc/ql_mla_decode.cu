@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     __shared__ int live_blocks[C::STAGES];
     __shared__ __align__(16) float ref[NH];          // the weights' reference of each head, log2, negated
     __shared__ float factor[NH], column[4][NH];
+    __shared__ __align__(16) int4 turns[2];          // the softmax groups' sequence
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t bar = su32(bars), ks = su32(smem), qs = ks + C::STAGES * C::TILE, ps = qs + C::QB;
     if (t == 0) {
@@ -288,16 +289,24 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     const Waits wt = {p.err, &abort_flag, p.ns};
     const Waits alone = {p.err, nullptr, p.ns};
 
-    // The window's sequences and their tiles [t0, t1); `each` returns false to stop.
-    auto sequences = [&](auto each) {
-        int start = window.lo < window.hi ? window.start : window.hi;
-        for (int b = window.first; b < p.batch && start < window.hi; ++b) {
-            const int len = p.lens(b), n = tiles_checked(len, p.cap);
+    // The window's next sequence and its tiles [t0, t1); false behind the last.
+    int next_b = window.first, start = window.lo < window.hi ? window.start : window.hi;
+    auto next = [&](int4& s) {
+        while (next_b < p.batch && start < window.hi) {
+            const int b = next_b++, len = p.lens(b), n = tiles_checked(len, p.cap);
             if (n == 0) continue;
             const int t0 = max(window.lo - start - kEnter, 0), t1 = min(window.hi - start - kEnter, n);
             start += n + kEnter;
-            if (t0 < t1 && !each(b, len, __shfl_sync(0xffffffffu, t0, 0), __shfl_sync(0xffffffffu, t1, 0))) return;
+            if (t0 < t1) {
+                s = make_int4(b, len, __shfl_sync(0xffffffffu, t0, 0), __shfl_sync(0xffffffffu, t1, 0));
+                return true;
+            }
         }
+        return false;
+    };
+    auto sequences = [&](auto each) {   // `each` returns false to stop
+        int4 s;
+        while (next(s) && each(s.x, s.y, s.z, s.w)) {}
     };
     auto empty = [&](int i, int block) { return bar + (C::kKEmpty + 4 * (i % C::STAGES) + block) * 8; };
     auto turn = [&](int i) { return (uint32_t)(i / C::STAGES) & 1u; };   // parity of tile i's stage
@@ -417,13 +426,23 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     } else {
         // ------------------------------------------------ softmax: warps 4 g .. 4 g + 3 have half of the heads; a lane has a key, warp w
         // of four the keys 16 w .. 16 w + 15 (M = 64: the scores fill 16 of a warp's 32 lanes).
-        // The four warps run the same number of tiles whatever their waits return, so that their barriers always meet.
+        // The four warps run the same tiles whatever their waits return, and take them from one of them (lengths that change during the
+        // launch, an error of the caller's, would else tell them apart), so that their barriers always meet.
         const int g = warp >> 2, w4 = warp & 3, h0 = g * HN, tg = t & 127;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int key = 16 * w4 + (lane & 15);
         const bool mine = lane < 16;
         auto meet = [&] { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + g) : "memory"); };
-        sequences([&](int b, int len, int t0, int t1) {
+        for (;;) {
+            if (w4 == 0) {
+                int4 s;
+                if (!next(s)) s.x = -1;
+                if (lane == 0) turns[g] = s;
+            }
+            meet();
+            const int4 now = turns[g];
+            const int b = now.x, len = now.y, t0 = __shfl_sync(0xffffffffu, now.z, 0), t1 = __shfl_sync(0xffffffffu, now.w, 0);
+            if (b < 0) break;
             float l[HN];
 #pragma unroll
             for (int h = 0; h < HN; ++h) l[h] = 0.f;
@@ -574,8 +593,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
             }
             fence_before();
             meet();   // before the next sequence's reference and columns
-            return true;
-        });
+        }
     }
     // (the copying warp of a window with tiles has waited already)
     pdl_wait();
@@ -656,9 +674,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
                 at += t >= o ? v : 0;
             }
             at += before - mine + kEnter;
-            const int w0 = n ? at / W : 0;
+            // (inside the workspace whatever the lengths do meanwhile)
+            const int w0 = n ? min(at / W, p.windows - 1) : 0;
             first[t] = w0 + b;
-            count[t] = n ? (at + n - 1) / W - w0 + 1 : 0;
+            count[t] = n ? min((at + n - 1) / W, p.windows - 1) - w0 + 1 : 0;
         }
         __syncthreads();
     }
