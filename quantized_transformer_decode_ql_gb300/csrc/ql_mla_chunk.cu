@@ -50,7 +50,7 @@ struct ExpandCfg {
     static constexpr int kOut = R == 512 ? 4 : 8, kCopy = kOut, kProduct = kOut + 1, THREADS = (kOut + 2) * 32;   // warps
     static constexpr size_t SMEM = (size_t)KC * AB + (size_t)STAGES * BB + kOut * OB;
     // what has landed in either CTA is reported to rank 0's barriers, what has been read to both CTAs'
-    static constexpr int kAFull = 0, kBFull = KC, kBEmpty = kBFull + STAGES, kAEmpty = kBEmpty + STAGES, kDFull = kAEmpty + 1, kDEmpty = kDFull + 2, kDone = kDEmpty + 2, kBars = kDone + 1;
+    static constexpr int kAFull = 0, kBFull = KC, kBEmpty = kBFull + STAGES, kAEmpty = kBEmpty + STAGES, kDFull = kAEmpty + KC, kDEmpty = kDFull + 2, kDone = kDEmpty + 2, kBars = kDone + 1;
     static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
 
@@ -85,23 +85,21 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
     if (L == 0 && t == 0 && blockIdx.x == 0) record_device_error(p.err, kErrAttnLength, 0, __ldg(p.position));
     // this pair's run of (256 tokens, 256 outputs), the tokens outside
     const int hgs = (p.H + C::HEADS - 1) / C::HEADS, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
-    const long long units = (L + 255) / 256 * hgs;
-    const long long u0 = __shfl_sync(0xffffffffu, units * pair / pairs, 0), u1 = __shfl_sync(0xffffffffu, units * (pair + 1) / pairs, 0);
+    const int units = (int)((L + 255) / 256) * hgs, each = units / pairs, more = units % pairs;   // (below 2^22)
+    const int u0 = __shfl_sync(0xffffffffu, pair * each + min(pair, more), 0), u1 = __shfl_sync(0xffffffffu, u0 + each + (pair < more), 0);
 
     const uint32_t there = in_cta(bar, 0);
     if (warp == C::kCopy) {
         // ------------------------------------------------ copies: a block of 16 tokens a lane, the weights by lane 0
         const long long nblk = (L + kBlock - 1) / kBlock;
-        long long held = -1;
-        int loads = 0, it = 0;
+        int held = -1, loads = 0, it = 0;
         bool ok = true;
-        for (long long u = u0; u < u1 && ok; ++u) {
-            const long long tp = u / hgs;
-            const int hg = (int)(u - tp * hgs);
+        int tp = u0 / hgs, hg = u0 - tp * hgs;
+        for (int u = u0; u < u1 && ok; ++u, hg = hg + 1 == hgs ? 0 : hg + 1, tp += hg == 0) {
             const bool fresh = tp != held;
             int row = 0;
             if (fresh) {
-                const long long at = tp * 16 + 8 * rank + lane;
+                const long long at = (long long)tp * 16 + 8 * rank + lane;
                 bool live = false;
                 int id = -1;
                 if (lane < 8 && at < nblk) {
@@ -112,14 +110,13 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
                 const unsigned mask = __ballot_sync(0xffffffffu, live);
                 if (lane == 0 && hg == 0) p.live[2 * tp + rank] = (int)mask;
                 row = live ? id * kBlock : (int)(p.num_blocks * kBlock);   // outside: zeros
-                if (loads > 0) ok = warp_wait(bar + C::kAEmpty * 8, (uint32_t)(loads - 1) & 1u, wt, 700);
-                if (!ok) break;
                 held = tp;
                 ++loads;
             }
             for (int c = 0; c < C::KC; ++c, ++it) {
                 const int s = it % C::STAGES;
-                if (fresh) {
+                if (fresh) {   // a run of the tokens' values makes room as its last product ends
+                    ok = ok && (loads < 2 || warp_wait(bar + (C::kAEmpty + c) * 8, (uint32_t)loads & 1u, wt, 700));
                     if (lane == 0 && rank == 0) bar_expect(bar + (C::kAFull + c) * 8, 2 * C::AB);
                     __syncwarp();
                     if (lane < 8) copy2_box2(as + c * C::AB + lane * 2048, &p.tc, 64 * c, row, there + (C::kAFull + c) * 8);
@@ -141,29 +138,32 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
         constexpr uint32_t I = instr(256, 256, false, false);
         const uint32_t one = elect_one();
         const uint64_t ad = operand(as, 16, 1024, 2), bd = operand(bs, 16, 1024, 2);
-        long long held = -1;
-        int loads = 0, it = 0, n = 0;
+        int hg = u0 % hgs, loads = 0, s = 0;
+        uint32_t phase = 0;                     // of the ring's stage s
         bool ok = rank == 0;
-        for (long long u = u0; u < u1 && ok; ++u, ++n) {
-            const long long tp = u / hgs;
-            const bool fresh = tp != held;
-            if (fresh) ++loads;
-            held = tp;
-            if (n >= 2) ok = warp_wait(bar + (C::kDEmpty + (n & 1)) * 8, (uint32_t)((n >> 1) - 1) & 1u, wt, 710);
-            for (int c = 0; c < C::KC && ok; ++c, ++it) {
-                const int s = it % C::STAGES;
+        for (int n = 0; n < u1 - u0 && ok; ++n) {
+            const bool fresh = n == 0 || hg == 0;
+            hg = hg + 1 == hgs ? 0 : hg + 1;
+            const bool last = hg == 0 && n + 1 < u1 - u0;
+            loads += fresh;
+            for (int c = 0; c < C::KC; ++c) {
                 if (fresh) ok = warp_wait(bar + (C::kAFull + c) * 8, (uint32_t)(loads - 1) & 1u, wt, 711);
-                ok = ok && warp_wait(bar + (C::kBFull + s) * 8, (uint32_t)(it / C::STAGES) & 1u, wt, 712);
+                ok = ok && warp_wait(bar + (C::kBFull + s) * 8, phase, wt, 712);
+                if (c == 0 && n >= 2) ok = ok && warp_wait(bar + (C::kDEmpty + (n & 1)) * 8, (uint32_t)((n >> 1) - 1) & 1u, wt, 710);
                 if (!ok) break;
                 fence_after();
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma2_ss(one, tb + 256 * (n & 1), ad + ((c * C::AB + 32 * k) >> 4), bd + ((s * C::BB + 32 * k) >> 4), I, c > 0 || k > 0);
                 mma2_commit(one, bar + (C::kBEmpty + s) * 8);
+                if (last) mma2_commit(one, bar + (C::kAEmpty + c) * 8);
+                if (++s == C::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
             if (!ok) break;
             mma2_commit(one, bar + (C::kDFull + (n & 1)) * 8);
-            if (u + 1 < u1 && (u + 1) / hgs != tp) mma2_commit(one, bar + C::kAEmpty * 8);
         }
         if (rank == 0) {
             mma2_commit(one, bar + C::kDone * 8);
@@ -173,9 +173,10 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
         // ------------------------------------------------ a token a thread: its 256 outputs, or 128 of them, rounded and stored
         unsigned char* stage = smem + C::KC * C::AB + C::STAGES * C::BB + warp * C::OB + lane * 128;
         int n = 0;
-        for (long long u = u0; u < u1; ++u, ++n) {
-            const long long tp = u / hgs, tok = tp * 256 + 128 * rank + 32 * (warp & 3) + lane;
-            const int hg = (int)(u - tp * hgs), b = n & 1;
+        int tp = u0 / hgs, hg = u0 - tp * hgs;
+        for (int u = u0; u < u1; ++u, ++n, hg = hg + 1 == hgs ? 0 : hg + 1, tp += hg == 0) {
+            const int b = n & 1;
+            const long long tok = (long long)tp * 256 + 128 * rank + 32 * (warp & 3) + lane;
             const bool in = tok < L;   // rows behind the context are zeros: what its last block holds there must not meet the weights
             if (hg == 0 && warp < 4) { // the rotated part as it is
                 const long long at = tok / kBlock;
@@ -190,15 +191,23 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
             fence_after();
             const uint32_t acc = tb + 256 * b + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-            for (int c = warp >> 2; c < 4; c += C::kOut / 4) {   // 64 outputs: rounded into shared memory, copied out from there
-                float f[64];
-                tmem_ld32(acc + 64 * c, f);
-                tmem_ld32(acc + 64 * c + 32, f + 32);
-                wait_ld();
-                tie32(f);
-                tie32(f + 32);
+            for (int c = warp >> 2;; c += C::kOut / 4) {   // 64 outputs: rounded into shared memory, copied out from there
                 const int h = hg * C::HEADS + 64 * c / (2 * D), e = 64 * c % (2 * D);
-                if (h >= p.H) break;
+                const bool is = c < 4 && h < p.H, last = !is || c + C::kOut / 4 >= 4;
+                float f[64];
+                if (is) {
+                    tmem_ld32(acc + 64 * c, f);
+                    tmem_ld32(acc + 64 * c + 32, f + 32);
+                    wait_ld();
+                    tie32(f);
+                    tie32(f + 32);
+                }
+                if (last) {   // the sums are free for the next unit but one
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(there + (C::kDEmpty + b) * 8);
+                }
+                if (!is) break;
                 if (lane == 0) stores_read();   // the copy before this one
                 __syncwarp();
 #pragma unroll
@@ -210,10 +219,8 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
                 fence_async();
                 __syncwarp();
                 if (lane == 0) store_box2(e < D ? &p.tk : &p.tv, e % D, (int)((long long)h * p.cap + tok), su32(stage));
+                if (last) break;
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive_cluster(there + (C::kDEmpty + b) * 8);
         }
         if (lane == 0) stores_done();
         __syncwarp();
