@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
     const int slices = R / 64, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int h = blockIdx.x / slices, r0 = (blockIdx.x % slices) * 64, b0 = blockIdx.y * 64;
     const __half* w = p.w + (size_t)h * 2 * D * R + r0;
-    for (int i = t; i < D * 8; i += 128) cp16(su32(ws + (i >> 3) * WP + (i & 7) * 8), w + (size_t)(i >> 3) * R + (i & 7) * 8);
+    for (int i = t; i < D; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + (size_t)i * R));
     pdl_wait();
     pdl_trigger();
+    for (int i = t; i < D * 8; i += 128) cp16(su32(ws + (i >> 3) * WP + (i & 7) * 8), w + (size_t)(i >> 3) * R + (i & 7) * 8);
     const int rows = min(64, p.batch - b0);
     constexpr int QC = D / 8;
     for (int i = t; i < 64 * QC; i += 128) {
