@@ -59,8 +59,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// One head, 64 of the rank columns, up to 64 rows of the batch. 4 warps, 16 columns each. The weights (16 KB) are on their
-// way before the previous kernel's end.
+// One head, 64 of the rank columns, up to 64 rows of the batch. 4 warps, 16 columns each, f16 products with f32 sums (a batch's few rows
+// fill no larger tile). The weights (16 KB) are asked into L2 before the previous kernel's end and read behind it, since that kernel may be
+// what wrote them (read before it: 0.7 us less at one row). Bound by their way from L2 and the launch: about 3.5 us for 32 heads of 128,
+// rank 512, at 1 to 32 rows (without shared memory, each lane its own rows: 3 us longer at 32).
 template <int D, int R>
 __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__ AbsorbParams p) {
     constexpr int WP = 72, QP = D + 8;    // row pitches in shared memory: 16-byte parts of 8 rows in different banks
@@ -250,6 +252,12 @@ __device__ Window make_window(const DecodeParams& p, int win) {
     return {lo, hi, found[0], found[1]};
 }
 
+// One CTA an SM, a window of the batch's tiles each. Two stages of 64 keys (73.7 KB each at rank 512) and the queries fill shared memory; a
+// stage is freed a block of 16 keys at a time. Scores have the keys as rows and the heads as columns, so that a softmax thread keeps one key's
+// heads in registers and stores its weights as the value product's B operand.
+//  16 x 20000 - 40960, 64 heads, rank 512: 105 us of the call's 120, 5.5 TB/s. A tile takes 2.0 us, 1.75 where the cache is in L2: HBM's latency
+//    and the chain of scores, softmax and values through two stages bound it together.
+//  32 x 128 - 8192, 32 heads: 38 us of 52; 5.5 - 5.9 TB/s in the loop, where copies of such tiles alone reach 6.6.
 template <int R, int NH>
 __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = Cfg<R, NH>;
@@ -624,6 +632,8 @@ struct JoinParams {
 // products' own business as long as A's are the same). What the lengths alone decide is worked out before the wait on the
 // attention; behind it the parts and their statistics are loaded at once.
 // o enters the product as two f16 numbers (22 bits): as one, its rounding alone would be as large as the output's.
+// Bound by latency (lengths, statistics, parts, the cluster's barrier, weights): 4 us for one sequence of 32 heads, 6 for 32 (a CTA a head
+// instead of a cluster: 3 us more at one).
 constexpr int kJoinThreads = 256, kJoinCtas = 4, kJoinRows = 8;
 template <int D, int R, int NH>
 __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1, 1) mla_join_kernel(const __grid_constant__ JoinParams p) {
