@@ -37,6 +37,28 @@ __device__ __forceinline__ long long context(const int32_t* position, int n, lon
     return p >= 0 && p + n <= maxb * kBlock ? p + n : 0;
 }
 
+// A warp's 32 tokens, a lane each (`live`: its block is in the pool): whether a value of the lane's latent vector is NaN or an infinity.
+template <int R>
+__device__ __forceinline__ bool latent_broken(const __half* pool, bool live, int id, long long tok, int lane) {
+    bool broken = false;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {   // a row at a time, by the whole warp
+        const bool is = __shfl_sync(0xffffffffu, live, i);
+        const long long row = (long long)__shfl_sync(0xffffffffu, id, i) * kBlock + __shfl_sync(0xffffffffu, (int)(tok % kBlock), i);
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < R / 256; ++k) {
+            const uint4 v = is ? __ldg(reinterpret_cast<const uint4*>(pool + row * (R + kRope)) + 32 * k + lane) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bad |= (u[j] & 0x7c00u) == 0x7c00u || (u[j] & 0x7c000000u) == 0x7c000000u;
+        }
+        const bool any = __any_sync(0xffffffffu, bad);
+        if (lane == i) broken = any;
+    }
+    return broken;
+}
+
 // A pair of CTAs multiplies 256 tokens (128 in each) with 256 weight rows (half of them in each): 64 bytes a cycle and SM
 // of operands read from shared memory, where a CTA alone reads 96 beside the 128 that it would have to take in from L2 (one CTA a
 // product of 128 x 256: 53.6 us for 4096 tokens and 32 heads, bound by L2). The tokens stay in shared memory for all the heads of
@@ -176,15 +198,19 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
         // ------------------------------------------------ a token a thread: its 256 outputs, or 128 of them, rounded and stored
         unsigned char* stage = smem + C::KC * C::AB + C::STAGES * C::BB + warp * C::OB + lane * 128;
         int n = 0;
+        bool broken = false;   // A token of the chunk whose latent vector holds NaN or an infinity: NaN as key for those who see it, 0 as value
+                               // for those whose weight of it is 0.
         int tp = u0 / hgs, hg = u0 - tp * hgs;
         for (int u = u0; u < u1; ++u, ++n, hg = hg + 1 == hgs ? 0 : hg + 1, tp += hg == 0) {
             const int b = n & 1;
             const long long tok = (long long)tp * 256 + 128 * rank + 32 * (warp & 3) + lane;
             const bool in = tok < L;   // rows behind the context are zeros: what its last block holds there must not meet the weights
+            const bool fresh = n == 0 || hg == 0;
+            int id = -1;
+            if (fresh && in) id = __ldg(p.table + tok / kBlock);
+            const bool live = id >= 0 && id < p.num_blocks;
+            if (fresh) broken = __any_sync(0xffffffffu, live && tok > L - p.n) && latent_broken<R>(p.pool, live, id, tok, lane);
             if (hg == 0 && warp < 4) { // the rotated part as it is
-                const long long at = tok / kBlock;
-                const int id = in ? __ldg(p.table + at) : -1;
-                const bool live = id >= 0 && id < p.num_blocks;
                 const uint4* src = reinterpret_cast<const uint4*>(p.pool + ((long long)(live ? id : 0) * kBlock + tok % kBlock) * (R + kRope) + R);
                 uint4* dst = reinterpret_cast<uint4*>(p.turned + tok * kRope);
 #pragma unroll
@@ -211,6 +237,14 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
                     if (lane == 0) bar_arrive_cluster(there + (C::kDEmpty + b) * 8);
                 }
                 if (!is) break;
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) most = fmaxf(most, fabsf(f[i]));
+                if (in && most >= 65520.f) record_device_error(p.err, kErrLatentValue, tok, h);
+                if (broken) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) f[i] = e < D ? NAN : 0.f;
+                }
                 if (lane == 0) stores_read();   // the copy before this one
                 __syncwarp();
 #pragma unroll

@@ -415,6 +415,45 @@ def test_chunk_bad_blocks_and_positions(heads):
             ql.ql_check_device_error()
 
 
+@pytest.mark.parametrize("n,before,heads,hd,rank", [(300, 50, 3, 64, 256), (300, 50, 3, 128, 512), (600, 0, 5, 64, 512), (129, 700, 2, 128, 256),
+                                                    (20, 100, 32, 128, 512)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("at", ["latent", "rotated"])
+def test_chunk_broken_rows_stay_behind_the_mask(n, before, heads, hd, rank, value, at):
+    """A token whose cache row holds NaN or an infinity is seen by the queries from it on, and by none before it."""
+    c = latent_case([before + n], heads, hd, rank, rows=n, seed=n + heads)
+    broken = n - n // 3
+    row = before + broken
+    c["pool"][c["table"][0, row // 16], row % 16, rank - 7 if at == "latent" else rank + 5] = value
+    got = chunk(c, n, before)
+    if at == "latent" or math.isnan(value):
+        assert not np.any(np.isfinite(got[broken:]))
+    sound = dict(c, q=c["q"][:broken])
+    lens = before + broken
+    rows = rows_of(c, 0, lens)
+    if n > 32:
+        want, bound = mla.attention(sound["q"], rows, c["w"], c["scale"], before=before)
+    else:
+        both = [mla.absorbed(c["q"][i], rows[:before + i + 1], c["w"], c["scale"]) for i in range(broken)]
+        want, bound = np.stack([x for x, _ in both]), np.stack([x for _, x in both])
+    assert np.all(np.abs(got[:broken] - want) <= bound)
+    lib()
+
+
+@pytest.mark.parametrize("hd,rank", [(64, 256), (128, 512)])
+def test_chunk_keys_beyond_f16_are_recorded(hd, rank):
+    ql = lib()
+    c = latent_case([90], 3, hd, rank, rows=90, seed=4)
+    c["w"][1, 3] = 300.0       # a key row of the second head
+    c["pool"][:, :, :rank] = 1.0
+    chunk(c, 90, 0)
+    with pytest.raises(ql.QLError):
+        ql.ql_check_device_error()
+    c["w"][1, 3] = 0.0
+    chunk(c, 90, 0)
+    ql.ql_check_device_error()
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("graph", [False, True])
 def test_steps_without_a_pause(graph):
