@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(512) mla_append_kernel(AppendParams p, DevErro
     const float r = rsqrtf(fmaf(ss, 1.0f / (float)R, p.eps));
     __half* o = p.pool + slot * (R + kRope);
     const float t[4] = {a[0] * c.x - b[0] * s.x, a[1] * c.y - b[1] * s.y, b[0] * c.x + a[0] * s.x, b[1] * c.y + a[1] * s.y};
-    bool held = true;   // by f16
+    bool held = ss < INFINITY;   // by f16, and the squares' sum by f32
 #pragma unroll
     for (int k = 0; k < 4; ++k) held &= fabsf(t[k]) < 65520.f;
 #pragma unroll

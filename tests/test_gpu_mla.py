@@ -82,7 +82,7 @@ def test_append_without_queries_and_no_rows():
     assert torch.equal(pool, before)
 
 
-@pytest.mark.parametrize("what", ["slot", "negative slot", "position", "negative position", "value", "nan"])
+@pytest.mark.parametrize("what", ["slot", "negative slot", "position", "negative position", "value", "nan", "squares"])
 def test_append_bad_rows_are_recorded(what):
     ql = lib()
     cos, sin = (dev(x) for x in tables(64))
@@ -96,12 +96,12 @@ def test_append_bad_rows_are_recorded(what):
     elif what.endswith("position"):
         pos[1] = 64 if what == "position" else -1
     else:
-        kv[1, 300] = 1e5 if what == "value" else math.nan
+        kv[1, 7 if what == "squares" else 300] = 1e5 if what == "value" else 1e25 if what == "squares" else math.nan
     ql.ql_mla_append(q, kv, torch.ones(256, device="cuda"), cos, sin, pos, slots, EPS, 2, 64, 256, 64, q_out, pool, 2, 64)
     with pytest.raises(ql.QLError) as e:
         ql.ql_check_device_error()
     assert e.value.status == ql.QL_EDEVICE
-    wrote = what in ("value", "nan")
+    wrote = what in ("value", "nan", "squares")
     assert int((pool.abs().sum(-1) != 0).sum()) == (3 if wrote else 2)
     assert bool((q_out[1] == 9).all()) == (not wrote) and not bool((q_out[0] == 9).any())
 
@@ -163,7 +163,7 @@ def check_decode(c, got, skip=()):
 
 DECODE = [([1], 1, 64, 256), ([1], 32, 128, 512), ([16, 15, 17], 4, 64, 512), ([63, 64, 65, 0, 1, 128], 3, 128, 256),
           ([2048], 32, 128, 512), ([0, 0, 700, 0], 20, 64, 256), ([1000, 3, 129, 640], 33, 64, 512), ([200, 90], 64, 128, 512),
-          ([333, 1, 77], 65, 64, 256), ([129], 96, 128, 512), ([70, 4000], 100, 64, 512), ([12000], 8, 128, 512), ([500] * 40, 2, 64, 256)]
+          ([333, 1, 77], 65, 64, 256), ([129], 96, 128, 512), ([40, 5], 1024, 64, 256), ([70, 4000], 100, 64, 512), ([12000], 8, 128, 512), ([500] * 40, 2, 64, 256)]
 
 
 @pytest.mark.parametrize("lens,heads,hd,rank", DECODE)
@@ -452,6 +452,58 @@ def test_chunk_keys_beyond_f16_are_recorded(hd, rank):
     c["w"][1, 3] = 0.0
     chunk(c, 90, 0)
     ql.ql_check_device_error()
+
+
+def test_chunk_offsets_past_32_bits():
+    """Keys and values of the last heads start beyond 2^32 bytes of the workspace, blocks of the cache beyond 2^32 bytes of the pool."""
+    ql = lib()
+    n, before, heads, hd, rank, maxb = 70, 30, 20, 128, 512, 1 << 16
+    blocks = (1 << 32) // (16 * 576) + 5
+    c = latent_case([before + n], heads, hd, rank, rows=n, seed=6)
+    pool = torch.empty((blocks, 16, 576), dtype=torch.float16, device="cuda")
+    ids = [blocks - 1, 3, blocks - 2, (1 << 31) // (16 * 576) + 1, 0, 7, blocks - 3]
+    for i, b in enumerate(ids):
+        pool[b] = dev(c["pool"][c["table"][0, i]])
+    table = torch.full((maxb,), -1, dtype=torch.int32, device="cuda")
+    table[:len(ids)] = torch.tensor(ids, dtype=torch.int32)
+    out = torch.full((n, heads, hd), 5.0, dtype=torch.float16, device="cuda")
+    ws = torch.empty(ql.ql_mla_chunk_workspace_bytes(n, heads, hd, rank, maxb), dtype=torch.uint8, device="cuda")
+    assert heads * maxb * 16 * hd * 2 > 1 << 32
+    ql.ql_mla_attn_chunk(dev(c["q"]), dev(c["w"]), pool, table, torch.tensor([before], dtype=torch.int32, device="cuda"), n, heads, hd, rank, 64, 16,
+                         maxb, blocks, c["scale"], out, ws)
+    torch.cuda.synchronize()
+    want, bound = mla.attention(c["q"], rows_of(c, 0, before + n), c["w"], c["scale"], before=before)
+    assert np.all(np.abs(out.cpu().numpy().astype(np.float64) - want) <= bound)
+    ql.ql_check_device_error()
+
+
+@pytest.mark.parametrize("n,before", [(3, 37), (40, 0), (260, 20)])
+def test_chunk_1024_heads(n, before):
+    c = latent_case([before + n], 1024, 64, 256, rows=n, seed=n)
+    got = chunk(c, n, before)
+    for heads in (slice(0, 3), slice(510, 514), slice(1020, 1024)):
+        part = dict(c, q=c["q"][:, heads], w=c["w"][heads])
+        rows = rows_of(c, 0, before + n)
+        if n > 32:
+            want, bound = mla.attention(part["q"], rows, part["w"], c["scale"], before=before)
+        else:
+            both = [mla.absorbed(part["q"][i], rows[:before + i + 1], part["w"], c["scale"]) for i in range(n)]
+            want, bound = np.stack([x for x, _ in both]), np.stack([x for _, x in both])
+        assert np.all(np.abs(got[:, heads] - want) <= bound)
+    lib().ql_check_device_error()
+
+
+@pytest.mark.parametrize("what,sizes", [("decode", ([3000, 1, 700, 64], 32, 128, 512)), ("decode", ([900, 5000], 70, 64, 256)),
+                                        ("chunk", (200, 3000, 4, 128, 512)), ("chunk", (30, 2000, 32, 128, 256)), ("chunk", (600, 100, 6, 64, 512))])
+def test_repeats_are_bit_identical(what, sizes):
+    if what == "decode":
+        c = latent_case(*sizes, seed=3)
+        runs = [decode(c) for _ in range(4)]
+    else:
+        n, before, heads, hd, rank = sizes
+        c = latent_case([before + n], heads, hd, rank, rows=n, seed=3)
+        runs = [chunk(c, n, before) for _ in range(4)]
+    assert all(np.array_equal(runs[0], r) for r in runs[1:])
 
 
 # ---------------------------------------------------------------- together
