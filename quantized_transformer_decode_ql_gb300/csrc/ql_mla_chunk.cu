@@ -62,7 +62,7 @@ __device__ __forceinline__ bool latent_broken(const __half* pool, bool live, int
 // A pair of CTAs multiplies 256 tokens (128 in each) with 256 weight rows (half of them in each): 64 bytes a cycle and SM
 // of operands read from shared memory, where a CTA alone reads 96 beside the 128 that it would have to take in from L2 (one CTA a
 // product of 128 x 256: 53.6 us for 4096 tokens and 32 heads, bound by L2). The tokens stay in shared memory for all the heads of
-// a pair's share of the work; the weights stream through a ring. 32 heads of 128, rank 512: 8192 tokens 44 us (1.55 PFLOP/s), 4096 tokens 28 us.
+// a pair's share of the work; the weights stream through a ring. 32 heads of 128, rank 512: 8192 tokens 46 us (1.49 PFLOP/s), 4096 tokens 31 us.
 // A product of 256 x 256 x 512 takes 4700 cycles of the 4100 that its instructions need; the first one's operands arrive 5 us after the launch,
 // and 14 (or 7) rounds of 76 pairs do not come out even. Not bound by the weights' reads (without half of them: 1.5 us less) nor by the stores
 // alone (6 us less without any). Keys and values are rounded to f16, as the attention's operands have to be; sums are f32.
@@ -295,7 +295,7 @@ struct ChunkParams {
 // are held up by L2 (1.4 us a tile of 128 queries and 128 keys; its products take 0.66).
 // The pairs stay for the whole grid's work. A unit of it is (256 queries, head, part of the keys); units are ordered by their length and
 // dealt out to and fro, so that all pairs end together, and a unit's queries, first tiles and scores arrive while the one before is finished.
-// A causal prompt of 4096 tokens, 32 heads of 128: 127 us, 1.35 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
+// A causal prompt of 4096 tokens, 32 heads of 128: 132 us, 1.30 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
 // warps (600) for two tiles. A unit's end takes 3 us. The weights are f16 (the product's operand, up to 2^14), their sums f32.
 // Without gain: weights before their maximum is known, judged by their sum (registers spill: 156 -> 170 us a prompt).
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     }
 }
 
-// A warp a query and head, the parts' loads together. Bound by latency: 3 us for 256 queries of 32 heads in two parts.
+// A warp a query and head, the parts' loads together. Bound by latency: 3 us behind the attention (7 alone) for 256 queries of 32 heads in two parts.
 template <int D>
 __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
     pdl_wait();
