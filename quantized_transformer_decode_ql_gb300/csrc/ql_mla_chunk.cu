@@ -295,7 +295,7 @@ struct ChunkParams {
 // are held up by L2 (1.4 us a tile of 128 queries and 128 keys; its products take 0.66).
 // The pairs stay for the whole grid's work. A unit of it is (256 queries, head, part of the keys); units are ordered by their length and
 // dealt out to and fro, so that all pairs end together, and a unit's queries, first tiles and scores arrive while the one before is finished.
-// A causal prompt of 4096 tokens, 32 heads of 128: 132 us, 1.30 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
+// A causal prompt of 4096 tokens, 32 heads of 128: 130 us, 1.32 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
 // warps (600) for two tiles. A unit's end takes 3 us. The weights are f16 (the product's operand, up to 2^14), their sums f32.
 // Without gain: weights before their maximum is known, judged by their sum (registers spill: 156 -> 170 us a prompt).
@@ -525,10 +525,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 tie32(x);
                 tie32(x + 32);
                 if (at + kQ - 1 > before + q0 || gap) {   // the same for the CTA
-                    const int mask = gap ? __ldg(p.live + w.j0 + off + 2 * i) >> (4 * hf) : 0xf;
+                    const int seen = last - at;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (at + c > last || !((mask >> (c >> 4)) & 1)) x[c] = -INFINITY;
+                    for (int c = 0; c < 64; ++c) x[c] = c > seen ? -INFINITY : x[c];
+                    if (gap) {
+                        const int live = __ldg(p.live + w.j0 + off + 2 * i) >> (4 * hf);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (!((live >> b) & 1)) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) x[16 * b + c] = -INFINITY;
+                            }
+                    }
                 }
                 float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
