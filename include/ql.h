@@ -430,12 +430,14 @@ int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, 
 /* A chunk of a prompt (the expanded form): query i of d_q, f16 [n_tokens][n_heads][head_dim + rope_dim], is at
  * position p + i, p = *d_position (int32 [1], device), and attends to rows 0 .. p + i of the sequence whose table is
  * d_block_table (int32 [max_blocks_per_seq]); all of them are in the cache already. Keys and values are made from the
- * latents of the whole context, as f16, in the workspace; up to 32 tokens (and n_heads * head_dim / 128) are taken
- * through the absorbed form instead. d_out f16 [n_tokens][n_heads * head_dim]. Block ids as for ql_mla_attn_decode (an
- * output of 0 for a query that no key is left for); a position below 0 or a chunk that ends behind the table is recorded
- * and leaves the output as it was. A row that holds NaN or an infinity spoils the outputs of the queries that see it, and
- * no others; a key or value that f16 does not hold is recorded. 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22, max_blocks_per_seq <= 2^16.
- * Alignments and workspace (ql_mla_chunk_workspace_bytes, enough for fewer tokens too) as for ql_mla_attn_decode. */
+ * latents of the whole context, as f16, in the workspace. Up to 32 tokens are taken through the absorbed form instead where
+ * that costs less: n_tokens <= n_heads * head_dim / 128, or n_tokens * n_heads <= 512 under a table of at most 64 blocks.
+ * d_out f16 [n_tokens][n_heads * head_dim]. Block ids as for ql_mla_attn_decode (an output of 0 for a query that no key is
+ * left for); a position below 0 or a chunk that ends behind the table is recorded and leaves the output as it was. A row
+ * that holds NaN or an infinity spoils the outputs of the queries that see it, and no others; a key or value (in the
+ * absorbed form: an absorbed query) that f16 does not hold is recorded. 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22,
+ * max_blocks_per_seq <= 2^16. Alignments and workspace as for ql_mla_attn_decode; ql_mla_chunk_workspace_bytes(...) bytes
+ * are enough for fewer tokens under the same table too. */
 size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq);
 int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
                       const int32_t* d_position, int64_t n_tokens, int n_heads, int head_dim, int rank, int rope_dim,

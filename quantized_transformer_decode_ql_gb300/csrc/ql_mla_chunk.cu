@@ -730,7 +730,9 @@ __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_consta
 // Expanded / absorbed in us, 32 heads of 128, rank 512, after 8000 tokens: 84 / 18 (1 token), 84 / 27 (8), 85 / 55 (32), 85 / 80 (48);
 // with no context 18 / 12, 19 / 13, 19 / 18, 20 / 25. 128 heads after 8000: 333 / 123 (32), 344 / 339 (96); with no context
 // 24 / 27 (16), 24 / 41 (32). 8 heads of 64, rank 256, after 8000: 24 / 15 (4), 24 / 24 (16).
-static bool few(int64_t n, int H, int D) { return n <= 32 && n * 128 <= (int64_t)H * D; }
+// Under a table of at most 1024 tokens the context cannot grow dear: 4 heads of 64, rank 256, after 0 and 900 tokens 12 / 10 and 16 / 13 (16),
+// 16 of 128, rank 512, 15 / 15 and 21 / 20 (32), 32 of 64 14 / 14 and 20 / 17 (16).
+static bool few(int64_t n, int H, int D, int64_t maxb) { return n <= 32 && (n * 128 <= (int64_t)H * D || (maxb <= 64 && n * H <= 512)); }
 
 struct ChunkShape {
     int splits;
@@ -765,7 +767,7 @@ static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
 // Bytes of the workspace that a call uses; 0 where its sizes are out of range.
 static size_t chunk_need(int64_t n, int H, int D, int R, int64_t maxb) {
     if (!shape_ok(D, R) || n < 1 || n > 65535 || H < 1 || H > 1024 || n * H >= (1 << 22) || maxb < 1 || maxb > (1 << 16)) return 0;
-    return few(n, H, D) ? absorbed_workspace(n, H, R) : chunk_shape(n, H, D, maxb).total;
+    return few(n, H, D, maxb) ? absorbed_workspace(n, H, R) : chunk_shape(n, H, D, maxb).total;
 }
 
 // Clusters of two CTAs of a kernel that the current device holds at once, looked up once.
@@ -890,7 +892,7 @@ extern "C" int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void
                       rope_dim, block_size, scale, d_out, d_workspace, workspace_bytes};
     if (int rc = attn_check("ql_mla_attn_chunk", a, chunk_need(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (few(n_tokens, n_heads, head_dim)) return absorbed_launch(a, true, s);
+    if (few(n_tokens, n_heads, head_dim, max_blocks_per_seq)) return absorbed_launch(a, true, s);
     const ChunkShape sh = chunk_shape(n_tokens, n_heads, head_dim, max_blocks_per_seq);
     if (head_dim == 128) return rank == 512 ? chunk_go<128, 512>(a, sh, s) : chunk_go<128, 256>(a, sh, s);
     return rank == 512 ? chunk_go<64, 512>(a, sh, s) : chunk_go<64, 256>(a, sh, s);
