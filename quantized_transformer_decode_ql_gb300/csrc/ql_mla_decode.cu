@@ -506,12 +506,14 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                         }
                     }
                 };
-                exponents();
                 // The reference is a running maximum that lags by up to 2^kLag: weights of up to 16384 are as exact in f16 as
                 // smaller ones, and O has to be scaled only when a score passes that.
-                unsigned raise;
-                asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
-                             : "=r"(raise) : "r"((unsigned)(tt == t0 || over > kLag)), "r"(1 + g) : "memory");
+                unsigned raise = 1;
+                if (tt > t0) {
+                    exponents();
+                    asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
+                                 : "=r"(raise) : "r"((unsigned)(over > kLag)), "r"(1 + g) : "memory");
+                }
                 if (raise) {
                     {
                         float v[HN];
