@@ -66,7 +66,7 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 template <int D, int R>
 __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__ AbsorbParams p) {
     constexpr int WP = 72, QP = D + 8;    // row pitches in shared memory: 16-byte parts of 8 rows in different banks
-    __shared__ __align__(16) __half ws[D * WP];
+    __shared__ __align__(16) __half ws[128 * WP];      // weights, then the outputs: [half][row]
     __shared__ __align__(16) __half qs[64 * QP];
     const int slices = R / 64, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int h = blockIdx.x / slices, r0 = (blockIdx.x % slices) * 64, b0 = blockIdx.y * 64;
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)   // (k 0-7, n 0-7), (k 8-15, n 0-7), (k 0-7, n 8-15), (k 8-15, n 8-15)
         ldsm4t(b[k], su32(ws + (16 * k + (lane & 15)) * WP + 16 * warp + 8 * (lane >> 4)));
+    __syncthreads();
     for (int m = 0; m < rows; m += 16) {
         float c[2][4] = {};
 #pragma unroll
@@ -112,14 +113,20 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
             const int r = m + (lane >> 2) + 8 * (i & 1);
             const float x = c[i >> 1][2 * (i & 1)], y = c[i >> 1][2 * (i & 1) + 1];
             if (r < rows) {
-                __half* dst = p.qc + ((size_t)(b0 + r) * p.halves * p.H + h) * (R + kRope) + r0 + 16 * warp + 8 * (i >> 1) + 2 * (lane & 3);
+                __half* dst = ws + r * WP + 16 * warp + 8 * (i >> 1) + 2 * (lane & 3);
                 const __half2 v = __floats2half2_rn(x, y);
                 *reinterpret_cast<__half2*>(dst) = v;
-                if (p.halves == 2) *reinterpret_cast<__half2*>(dst + rest) = __floats2half2_rn(x - __low2float(v), y - __high2float(v));
+                if (p.halves == 2) *reinterpret_cast<__half2*>(dst + 64 * WP) = __floats2half2_rn(x - __low2float(v), y - __high2float(v));
                 large |= !(fabsf(x) < 65520.f && fabsf(y) < 65520.f);
             }
         }
         if (large) record_device_error(p.err, kErrLatentValue, b0 + m, h);
+    }
+    __syncthreads();
+    for (int i = t; i < rows * 8 * p.halves; i += 128) {   // 128 bytes a row and half
+        const int half = i >= rows * 8, r = (i - half * rows * 8) >> 3, c = i & 7;
+        *reinterpret_cast<uint4*>(p.qc + ((size_t)(b0 + r) * p.halves * p.H + h) * (R + kRope) + half * rest + r0 + 8 * c) =
+            *reinterpret_cast<const uint4*>(ws + (64 * half + r) * WP + 8 * c);
     }
 }
 
