@@ -659,6 +659,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
     const int d0 = quarter * (D / kJoinCtas) + 8 * nt;       // this warp's value rows
     const int hg = h / NH;
     const size_t base = (size_t)hg * (p.windows + p.batch);
+    // this CTA's value rows into L2 while the attention still runs
+    for (int i = t; i < D / kJoinCtas * (R / 64); i += kJoinThreads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w + ((size_t)h * 2 * D + D + quarter * (D / kJoinCtas)) * R + (size_t)i * 64));
     // every CTA of the cluster has started before another writes into it (waited for below)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     {
