@@ -4,7 +4,7 @@
 //     the cache's rows (256 tokens x 256 outputs a pair of CTAs), and the rotated key parts laid out beside them;
 //  2. mla_chunk_kernel: causal attention of 256 queries of one head by a pair of CTAs, the online softmax over tiles of 128 keys in
 //     two independent halves of the tiles (even and odd), so that one half's products run beside the other's weights;
-//  3. mla_chunk_join_kernel, where the keys are split over CTAs: the parts joined.
+//  3. mla_chunk_join_kernel, where units are cut: their parts joined.
 #include "ql_batched.h"
 #include "ql_mla_tc.cuh"
 
@@ -281,10 +281,10 @@ struct ChunkParams {
     const int32_t* table;
     const int32_t* position;
     __half* out;            // [n][H][D]
-    float* parts;           // splits > 1: [split][n][H][D]
-    float2* stats;          // [split][n][H]: reference (log2), sum of the weights
+    float* parts;           // cut: [window + unit][query of the unit][D]
+    float2* stats;          // [window + unit][query]: reference (log2), sum of the weights
     long long maxb, num_blocks, cap;
-    int n, H, splits;
+    int n, H, pairs, cut;
     float scale_log2;
     DevError* err;
     unsigned long long ns;
@@ -293,8 +293,11 @@ struct ChunkParams {
 // A pair of CTAs takes 256 queries of one head, 128 in each, and shares every tile of keys and values: each CTA brings 64 of a
 // tile's 128 keys and half of its values' columns. A CTA alone takes 80 KB from L2 for every 10.5 MFLOP, and 152 of them
 // are held up by L2 (1.4 us a tile of 128 queries and 128 keys; its products take 0.66).
-// The pairs stay for the whole grid's work. A unit of it is (256 queries, head, part of the keys); units are ordered by their length and
+// The pairs stay for the whole grid's work. A unit of it is (256 queries, head); units are ordered by their length and
 // dealt out to and fro, so that all pairs end together, and a unit's queries, first tiles and scores arrive while the one before is finished.
+// Where there are few (cut), all units' tiles in a row are cut into a window a pair instead, and parts of a unit joined afterwards (against a number
+// of parts that is the same for all units: 777 tokens after 1234, 20 heads of 64, 37.1 -> 32.8 us; 256 after 30000, 32 heads of 128, 284 -> 275;
+// 256 after 7936, 40 heads, 116.5 -> 105; 1000 after 1000, 8 heads, 27.3 -> 28.4).
 // A causal prompt of 4096 tokens, 32 heads of 128: 130 us, 1.32 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
 // warps (600) for two tiles. A unit's end takes 3 us. The weights are f16 (the product's operand, up to 2^14), their sums f32.
@@ -333,6 +336,29 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
 }
 
 constexpr int kSoft = 16, kCopy = 16, kProduct = 17, kChunkThreads = 18 * 32;   // warps: softmax, copies, products
+
+// The units' tiles in a row, for `cut`: unit b H + h has the block of queries that is the b-th from the end, and `enter` places before its tiles for
+// what it costs to enter and leave it. From one block to the one before it there are two tiles less.
+constexpr int kLeast = 8;   // tiles of a window at least: shorter ones make more parts than they save (4 heads after 16000: 39.9 us with 8, 42 with 4)
+struct Row {
+    int H, blocks, past, longest, enter, window;
+    __device__ Row(int n, int H, int before, int pairs)
+        : H(H), blocks((n + 2 * kQ - 1) / (2 * kQ)), past((before + kQ - 1) / kQ), longest((before + n + kQ - 1) / kQ), enter(4) {
+        window = max((start(blocks) + pairs - 1) / pairs, kLeast);
+        // One block of queries: windows that end where heads end, if they are little longer (256 queries after 7936, 32 heads: 32 tiles of one
+        // head each are 1.2 us shorter than 28 of two).
+        if (blocks == 1 && H <= pairs) {
+            const int k = pairs / H, even = max((longest + k - 1) / k, kLeast);
+            if (even <= window + 6) {
+                window = even;
+                enter = k * even - longest;
+            }
+        }
+    }
+    __device__ int tiles(int b) const { return b == 0 ? longest : 2 * (blocks - b) + past; }
+    __device__ int start(int b) const { return b == 0 ? 0 : H * (longest + enter + (b - 1) * (past + enter + 2 * blocks - b)); }   // of the block's first head
+    __device__ int start(int b, int h) const { return start(b) + h * (tiles(b) + enter); }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
@@ -373,40 +399,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
         gap |= id < 0 || id >= p.num_blocks;
     }
     gap = __syncthreads_or(gap);
-    pdl_wait();
-    pdl_trigger();
-    const int before = (int)(L - p.n);
-    const int blocks = (p.n + 2 * kQ - 1) / (2 * kQ), units = L ? blocks * p.H * p.splits : 0, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int before = L ? (int)(L - p.n) : 0;
+    const int blocks = (p.n + 2 * kQ - 1) / (2 * kQ), units = L ? blocks * p.H : 0, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
     // u / d for u < 2^22, `by` the rounded 1 / d
-    const float by_splits = 1.f / (float)p.splits, by_heads = 1.f / (float)p.H;
+    const float by_heads = 1.f / (float)p.H;
     auto quotient = [](int u, int d, float by) {
         int k = (int)((float)u * by);
         k -= k * d > u;
         return k + ((k + 1) * d <= u);
     };
-    // The k-th unit of this pair: the head, the first query, the part of the keys, its first tile and their number; false behind the last.
+    const Row in_a_row(p.n, p.H, before, pairs);
+    const int lo = pair * in_a_row.window, hi = lo + in_a_row.window;
+    int first_unit = 0;
+    if (p.cut) {   // the one that holds place lo
+        int b = 0;
+        while (b + 1 < blocks && in_a_row.start(b + 1) <= lo) ++b;
+        first_unit = b * p.H + min((lo - in_a_row.start(b)) / (in_a_row.tiles(b) + in_a_row.enter), p.H);
+    }
+    pdl_wait();
+    pdl_trigger();
+    // The k-th unit of this pair: the head, the first query, where a part of it goes (-1: the whole unit), its first tile and their number
+    // (of a part: possibly none); false behind the last.
     struct Unit {
-        int h, first, split, j0, tiles;
+        int h, first, slot, j0, tiles;
     };
     auto unit = [&](int k, Unit& w) {
-        const int u = k * pairs + (k & 1 ? pairs - 1 - pair : pair);
+        // (to and fro: where the last row of units is short, the pairs that have one there are those of the row's end)
+        const int u = p.cut ? first_unit + k : k * pairs + (k & 1 ? pairs - 1 - pair : pair);
         if (u >= units) return false;
-        const int bh = quotient(u, p.splits, by_splits), b = quotient(bh, p.H, by_heads);
-        w.split = u - bh * p.splits;
-        w.h = bh - b * p.H;
+        const int b = quotient(u, p.H, by_heads);
+        w.h = u - b * p.H;
         w.first = (blocks - 1 - b) * 2 * kQ;
-        const int all = (before + min(w.first + 2 * kQ, p.n) + kQ - 1) / kQ;    // tiles that the last of the unit's queries sees
-        const int per = quotient(all + p.splits - 1, p.splits, by_splits);
-        w.j0 = min(w.split * per, all);
-        w.tiles = min(per, all - w.j0);
+        w.slot = -1;
+        w.j0 = 0;
+        w.tiles = in_a_row.tiles(b);    // that the last of the unit's queries sees
+        if (p.cut) {
+            const int start = in_a_row.start(b, w.h);
+            if (start >= hi) return false;
+            const int all = w.tiles, j1 = min(hi - start - in_a_row.enter, all);
+            w.j0 = max(lo - start - in_a_row.enter, 0);
+            w.tiles = j1 - w.j0;
+            if (w.tiles < all) w.slot = pair + u;
+        }
         return true;
     };
-    // (to and fro: where the last row of units is short, the pairs that have one there are those of the row's end)
     auto work = [&](auto each) {
         Unit w;
-        for (int k = 0; k * pairs < units; ++k)
-            if (unit(k, w) && !each(w, k)) return;
+        for (int k = 0; unit(k, w) && each(w, k); ++k) {}
     };
     int jt = 0, un = 0;   // tiles and units with tiles so far
 
@@ -592,7 +632,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
             }
             // Both halves of the tiles joined by the eight warps that had the last tile, half of the values each four; the other
             // eight leave what they know and go on to the next unit.
-            const bool whole = p.splits == 1;
+            const bool whole = w.slot < 0;
             float ma = -1e30f, mb = -1e30f, total = 0.f;
             if (tiles > 0) {
                 const int lastg = (jt + tiles - 1) & 1, turn = un & 1;
@@ -611,10 +651,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 total = (sums[turn][0][0][q] + sums[turn][0][1][q]) * ex2(ma - top) + (sums[turn][1][0][q] + sums[turn][1][1][q]) * ex2(mb - top);
                 if (tiles > 1) done(tiles - 2);
                 done(tiles - 1);
-            } else {   // (a split without keys: the join does not look at its part)
-                if (g == 0 && hf == 0 && q < rows) p.stats[((size_t)w.split * p.n + q0 + q) * p.H + w.h] = make_float2(-1e30f, 0.f);
-                return true;
-            }
+            } else return true;   // (the join does not look for a part here)
             const float top = fmaxf(ma, mb), inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
             const float ca = ex2(ma - top) * inv, cb = ex2(mb - top) * inv;
             const bool even = tiles > (jt & 1), odd = tiles > (1 ^ (jt & 1));   // which of the two O hold something of this unit
@@ -650,7 +687,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                     for (int r = 0; r < 4; ++r)
                         if (r0 + r < rows) *reinterpret_cast<uint4*>(p.out + row0 + r * step + d0 + 8 * part) = u[r];
                 } else {
-                    float* dst = p.parts + (size_t)w.split * p.n * p.H * D;
+                    float* dst = p.parts + ((size_t)w.slot * 2 * kQ + kQ * rank + r0) * D;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -660,11 +697,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                         transpose4(u, lane);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (r0 + r < rows) *reinterpret_cast<uint4*>(dst + row0 + r * step + d0 + 16 * b + 4 * part) = u[r];
+                            if (r0 + r < rows) *reinterpret_cast<uint4*>(dst + r * D + d0 + 16 * b + 4 * part) = u[r];
                     }
                 }
             }
-            if (!whole && hf == 0 && q < rows) p.stats[((size_t)w.split * p.n + q0 + q) * p.H + w.h] = make_float2(top, total);
+            if (!whole && hf == 0 && q < rows) p.stats[(size_t)w.slot * 2 * kQ + kQ * rank + q] = make_float2(top, total);
             jt += tiles;
             return true;
         });
@@ -678,25 +715,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     }
 }
 
-// A warp a query and head, the parts' loads together. Bound by latency: 3 us behind the attention (7 alone) for 256 queries of 32 heads in two parts.
+// A warp a query and head, four parts' loads together; which parts there are is worked out before the wait. Bound by latency: 3 us behind the
+// attention (7 alone) for 256 queries of 32 heads in two parts.
 template <int D>
 __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+    const int i = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;   // (below 2^22)
+    const int L = (int)context(p.position, p.n, p.maxb);
+    const int row = i / p.H, h = i - row * p.H;
+    const Row in_a_row(p.n, p.H, max(L - p.n, 0), p.pairs);
+    const int b = in_a_row.blocks - 1 - row / (2 * kQ), start = in_a_row.start(b, h) + in_a_row.enter;
+    const int w0 = start / in_a_row.window, count = (start + in_a_row.tiles(b) - 1) / in_a_row.window - w0 + 1;
+    const size_t at = (size_t)(w0 + b * p.H + h) * 2 * kQ + row % (2 * kQ);
     pdl_wait();
     pdl_trigger();
-    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), all = (long long)p.n * p.H;
-    const int lane = threadIdx.x & 31;
-    if (i >= all || context(p.position, p.n, p.maxb) == 0) return;
+    if (row >= p.n || L == 0 || count == 1) return;   // (a whole unit is in its place)
     constexpr int V = D / 32, AT_ONCE = 4;
     float top = -INFINITY, total = 0.f, x[V] = {};
-    for (int s0 = 0; s0 < p.splits; s0 += AT_ONCE) {   // the parts of four splits at a time
+    for (int s0 = 0; s0 < count; s0 += AT_ONCE) {   // four parts at a time
         float2 st[AT_ONCE];
         float v[AT_ONCE][V];
 #pragma unroll
         for (int s = 0; s < AT_ONCE; ++s) {
-            st[s] = s0 + s < p.splits ? __ldcg(p.stats + (s0 + s) * all + i) : make_float2(-INFINITY, 0.f);
+            const size_t part = at + (size_t)(s0 + s) * 2 * kQ;
+            st[s] = s0 + s < count ? __ldcg(p.stats + part) : make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int k = 0; k < V; k += 2) {
-                const float2 a = s0 + s < p.splits ? __ldcg(reinterpret_cast<const float2*>(p.parts + ((s0 + s) * all + i) * D + lane * V + k)) : make_float2(0.f, 0.f);
+                const float2 a = s0 + s < count ? __ldcg(reinterpret_cast<const float2*>(p.parts + part * D + lane * V + k)) : make_float2(0.f, 0.f);
                 v[s][k] = a.x;
                 v[s][k + 1] = a.y;
             }
@@ -721,7 +765,7 @@ __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_consta
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
     for (int k = 0; k < V; k += 2)
-        *reinterpret_cast<__half2*>(p.out + i * D + lane * V + k) = __floats2half2_rn(x[k] * inv, x[k + 1] * inv);
+        *reinterpret_cast<__half2*>(p.out + (size_t)i * D + lane * V + k) = __floats2half2_rn(x[k] * inv, x[k + 1] * inv);
 }
 
 // ---------------------------------------------------------------- host
@@ -734,33 +778,26 @@ __global__ void __launch_bounds__(256) mla_chunk_join_kernel(const __grid_consta
 // 16 of 128, rank 512, 15 / 15 and 21 / 20 (32), 32 of 64 14 / 14 and 20 / 17 (16).
 static bool few(int64_t n, int H, int D, int64_t maxb) { return n <= 32 && (n * 128 <= (int64_t)H * D || (maxb <= 64 && n * H <= 512)); }
 
+constexpr int kMostPairs = 80;   // pairs of CTAs with a window each
 struct ChunkShape {
-    int splits;
+    bool cut;
     long long cap;                                       // rows of the keys and values a head
     size_t v, turned, live, stats, parts, total;         // offsets in the workspace
 };
 static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     ChunkShape s = {};
     s.cap = (maxb * kBlock + 255) / 256 * 256;
-    // Keys split over pairs of CTAs where queries and heads alone give few: what the last round of 76 pairs and the end of each unit
-    // (about 2 tiles) cost, for the longest context that the table holds.
-    const int64_t pairs = (n + 2 * kQ - 1) / (2 * kQ) * H, tiles = s.cap / kQ;
-    int64_t best = 0;
-    s.splits = 1;
-    for (int64_t k = 1; k <= 16 && k <= std::max<int64_t>(1, tiles / 4) && (k == 1 || pairs < 152); ++k) {
-        const int64_t cost = (pairs * k + 75) / 76 * ((tiles + k - 1) / k + 2);
-        if (k == 1 || cost < best) {
-            best = cost;
-            s.splits = (int)k;
-        }
-    }
+    // Few units are cut evenly over the pairs where that costs less, for the longest context that the table holds: rounds of 76 units and the
+    // end of each (about 2 tiles), against their share, a second entry and the join.
+    const int64_t units = (n + 2 * kQ - 1) / (2 * kQ) * H, tiles = s.cap / kQ;
+    s.cut = units < 152 && (units * (tiles + 2) + 75) / 76 + 5 < (units + 75) / 76 * (tiles + 2);
     auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
     s.v = up((size_t)H * s.cap * D * 2);
     s.turned = 2 * s.v;
     s.live = s.turned + up((size_t)s.cap * kRope * 2);
     s.stats = s.live + up((size_t)tiles * 4);
-    s.parts = s.stats + (s.splits > 1 ? up((size_t)s.splits * n * H * 8) : 0);
-    s.total = s.parts + (s.splits > 1 ? up((size_t)s.splits * n * H * D * 4) : 0);
+    s.parts = s.stats + (s.cut ? up((size_t)(kMostPairs + units) * 2 * kQ * 8) : 0);
+    s.total = s.parts + (s.cut ? up((size_t)(kMostPairs + units) * 2 * kQ * D * 4) : 0);
     return s;
 }
 
@@ -851,7 +888,7 @@ static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
     cp.out = static_cast<__half*>(a.out);
     cp.parts = reinterpret_cast<float*>(ws + sh.parts);
     cp.stats = reinterpret_cast<float2*>(ws + sh.stats);
-    cp.splits = sh.splits;
+    cp.cut = sh.cut;
     cp.scale_log2 = a.scale * 1.44269504088896340736f;
     // as many pairs as the GPU holds at once, and as there can be work for
     static std::atomic<int> most[64], most2[64];
@@ -859,11 +896,12 @@ static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
     if (int rc = pairs_at_once(mla_expand_kernel<D, R>, E::THREADS, E::SMEM, most, &pairs)) return rc;
     if (int rc = pairs_at_once(mla_chunk_kernel<D>, kChunkThreads, C::SMEM, most2, &pairs2)) return rc;
     pairs = (int)std::min<int64_t>(pairs, sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS));
-    pairs2 = (int)std::min<int64_t>(pairs2, (a.rows + 2 * kQ - 1) / (2 * kQ) * a.H * sh.splits);
+    pairs2 = sh.cut ? std::min(pairs2, kMostPairs) : (int)std::min<int64_t>(pairs2, (a.rows + 2 * kQ - 1) / (2 * kQ) * a.H);
+    cp.pairs = pairs2;
     cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(E::THREADS), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
         e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), C::SMEM, s, true, cp);
-    if (e == cudaSuccess && sh.splits > 1)
+    if (e == cudaSuccess && sh.cut)
         e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.rows * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");
 }
@@ -872,7 +910,7 @@ static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
 }  // namespace ql
 
 extern "C" size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq) {
-    // Fewer tokens may split their keys further, or take the other form: the most that any number up to n_tokens needs.
+    // Fewer tokens may be cut, or take the other form: the most that any number up to n_tokens needs.
     size_t most = ql::mla::chunk_need(n_tokens, n_heads, head_dim, rank, max_blocks_per_seq);
     if (most == 0) return 0;
     for (int64_t n = 2 * ql::mla::kQ; n < n_tokens && n / (2 * ql::mla::kQ) * n_heads < 152; n += 2 * ql::mla::kQ)

@@ -342,7 +342,8 @@ def chunk_bound(c, n, before):
     return np.stack([x for x, _ in both]), np.stack([x for _, x in both])
 
 
-CHUNK = [(17, 0, 4, 64, 256), (32, 900, 16, 64, 512), (17, 1100, 4, 64, 256), (30, 900, 18, 64, 512), (5, 300, 5, 128, 256), (6, 300, 5, 128, 256), (32, 1000, 64, 64, 512), (33, 1000, 64, 64, 512), (20, 0, 33, 128, 512),
+CHUNK = [(256, 5000, 2, 64, 256), (300, 2500, 7, 64, 256), (700, 900, 13, 64, 256), (40, 9000, 1, 128, 256), (1030, 0, 11, 64, 256), (600, 600, 50, 64, 256),
+         (17, 0, 4, 64, 256), (32, 900, 16, 64, 512), (17, 1100, 4, 64, 256), (30, 900, 18, 64, 512), (5, 300, 5, 128, 256), (6, 300, 5, 128, 256), (32, 1000, 64, 64, 512), (33, 1000, 64, 64, 512), (20, 0, 33, 128, 512),
          (32, 500, 96, 128, 256), (33, 500, 96, 128, 256), (1, 0, 1, 64, 256), (1, 0, 32, 128, 512), (17, 0, 4, 64, 256), (16, 1, 2, 128, 512), (128, 0, 3, 128, 256), (129, 0, 2, 64, 512),
          (1, 700, 5, 128, 512), (7, 121, 3, 64, 256), (100, 1000, 2, 128, 512), (300, 333, 7, 64, 256), (513, 0, 2, 128, 512),
          (64, 2500, 1, 64, 512), (200, 57, 33, 64, 256), (40, 3, 70, 64, 512)]
