@@ -658,47 +658,59 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
             // Four lanes store 64 bytes of one query together (one lane a query: rows far apart, which held up the warps for 3500 cycles).
             const int r0 = q & ~3, part = q & 3;
             const size_t step = (size_t)p.H * D, row0 = (size_t)(q0 + r0) * step + (size_t)w.h * D;
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {   // 32 values
-                float x[32], y[32];
+            auto values = [&](int d0, float* x, float* y) {   // 16 of them, both halves of the tiles together
+                constexpr int N = 16;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = y[k] = 0.f;
-                const int d0 = hf * (D / 2) + 32 * c;
-                if (even) tmem_raw<32>(tb + lanes + C::OCOL + d0, x);
-                if (odd) tmem_raw<32>(tb + lanes + C::OCOL + D + d0, y);
+                for (int k = 0; k < N; ++k) x[k] = y[k] = 0.f;
+                if (even) tmem_raw<N>(tb + lanes + C::OCOL + d0, x);
+                if (odd) tmem_raw<N>(tb + lanes + C::OCOL + D + d0, y);
                 wait_ld();
-                tie<32>(x);
-                tie<32>(y);
-                if (c == D / 64 - 1) {   // both O are read: the next unit's values may go there
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_cluster(there + C::kOFree * 8);
+                tie<N>(x);
+                tie<N>(y);
+#pragma unroll
+                for (int k = 0; k < N; ++k) x[k] = fmaf(y[k], cb, x[k] * ca);
+            };
+            auto read = [&] {   // both O are read: the next unit's values may go there
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_cluster(there + C::kOFree * 8);
+            };
+            if (whole) {
+                uint32_t packed[D / 4];   // (all of them before the first store: the next unit waits for O)
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float x[16], y[16];
+                    values(hf * (D / 2) + 16 * c, x, y);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) packed[8 * c + k] = pack_half(x[2 * k], x[2 * k + 1]);
                 }
+                read();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = fmaf(y[k], cb, x[k] * ca);
-                uint4 u[4];
-                if (whole) {
+                for (int c = 0; c < D / 64; ++c) {
+                    uint4 u[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        u[k] = make_uint4(pack_half(x[8 * k], x[8 * k + 1]), pack_half(x[8 * k + 2], x[8 * k + 3]), pack_half(x[8 * k + 4], x[8 * k + 5]),
-                                          pack_half(x[8 * k + 6], x[8 * k + 7]));
+                    for (int k = 0; k < 4; ++k) u[k] = make_uint4(packed[16 * c + 4 * k], packed[16 * c + 4 * k + 1], packed[16 * c + 4 * k + 2], packed[16 * c + 4 * k + 3]);
                     transpose4(u, lane);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (r0 + r < rows) *reinterpret_cast<uint4*>(p.out + row0 + r * step + d0 + 8 * part) = u[r];
-                } else {
-                    float* dst = p.parts + ((size_t)w.slot * 2 * kQ + kQ * rank + r0) * D;
+                        if (r0 + r < rows) *reinterpret_cast<uint4*>(p.out + row0 + r * step + hf * (D / 2) + 32 * c + 8 * part) = u[r];
+                }
+            } else {
+                float* dst = p.parts + ((size_t)w.slot * 2 * kQ + kQ * rank + r0) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float x[16], y[16];
+                    const int d0 = hf * (D / 2) + 16 * c;
+                    values(d0, x, y);
+                    if (c == D / 32 - 1) read();
+                    uint4 u[4];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                    for (int k = 0; k < 4; ++k)
+                        u[k] = make_uint4(__float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]), __float_as_uint(x[4 * k + 2]), __float_as_uint(x[4 * k + 3]));
+                    transpose4(u, lane);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            u[k] = make_uint4(__float_as_uint(x[16 * b + 4 * k]), __float_as_uint(x[16 * b + 4 * k + 1]), __float_as_uint(x[16 * b + 4 * k + 2]),
-                                              __float_as_uint(x[16 * b + 4 * k + 3]));
-                        transpose4(u, lane);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (r0 + r < rows) *reinterpret_cast<uint4*>(dst + r * D + d0 + 16 * b + 4 * part) = u[r];
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        if (r0 + r < rows) *reinterpret_cast<uint4*>(dst + r * D + d0 + 4 * part) = u[r];
                 }
             }
             if (!whole && hf == 0 && q < rows) p.stats[(size_t)w.slot * 2 * kQ + kQ * rank + q] = make_float2(top, total);
