@@ -298,20 +298,22 @@ struct ChunkParams {
 // Where there are few (cut), all units' tiles in a row are cut into a window a pair instead, and parts of a unit joined afterwards (against a number
 // of parts that is the same for all units: 777 tokens after 1234, 20 heads of 64, 37.1 -> 32.8 us; 256 after 30000, 32 heads of 128, 284 -> 275;
 // 256 after 7936, 40 heads, 116.5 -> 105; 1000 after 1000, 8 heads, 27.3 -> 28.4).
-// A causal prompt of 4096 tokens, 32 heads of 128: 130 us, 1.32 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
+// A causal prompt of 4096 tokens, 32 heads of 128: 127 us, 1.35 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
-// warps (600) for two tiles. A unit's end takes 3 us. The weights are f16 (the product's operand, up to 2^14), their sums f32.
+// warps (600) for two tiles. From unit to unit go 2 - 3 thousand cycles more. The weights are f16 (the product's operand, up to 2^14), their sums f32.
 // Without gain: weights before their maximum is known, judged by their sum (registers spill: 156 -> 170 us a prompt).
-template <int D>
+template <int D, int NQ>
 struct ChunkCfg {
     static constexpr int CH = (D + kRope) / 64, RUN = kQ * 128;      // a run of 64 values of 128 rows
-    static constexpr int KRUN = 64 * 128, STAGES = 4;
+    // Buffers of queries (NQ) and tiles in flight share the room. With units in turn a second buffer is worth a tile with 128 values (a 4096-token
+    // prompt 151.9 -> 150.5 us), with a window or two a pair it is not (256 tokens after 7936 83.2 -> 85.2); with 64 there is room for both.
+    static constexpr int KRUN = 64 * 128, STAGES = D == 128 && NQ == 2 ? 3 : 4;
     static constexpr int QB = CH * RUN, KB = CH * KRUN, VB = kQ * D; // V: 128 keys x D / 2 columns
-    static constexpr size_t SMEM = QB + STAGES * (KB + VB);
+    static constexpr size_t SMEM = NQ * QB + STAGES * (KB + VB);
     static constexpr uint32_t OCOL = 256, COLS = 512;                // tensor memory: two S (P over them), two O
     // what has landed in either CTA, and the weights of both, are reported to rank 0's barriers, what the products have read or
     // written to both CTAs'
-    static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
+    static constexpr int kQFull = 0, kQEmpty = NQ, kKFull = 2 * NQ, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
                          kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kOFree = kPReady + 2, kDone = kOFree + 1, kBars = kDone + 1;
 };
 
@@ -360,9 +362,9 @@ struct Row {
     __device__ int start(int b, int h) const { return start(b) + h * (tiles(b) + enter); }
 };
 
-template <int D>
+template <int D, int NQ>
 __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
-    using C = ChunkCfg<D>;
+    using C = ChunkCfg<D, NQ>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     __shared__ float tops[2][2][kQ], sums[2][2][2][kQ], refs[2][2][kQ];   // (sums and refs of two units in turn)
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t rank = cluster_rank();
-    const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + C::QB, vs = ks + C::STAGES * C::KB;
+    const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + NQ * C::QB, vs = ks + C::STAGES * C::KB;
     if (t == 0) {
         for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 || i == C::kOFree ? kSoft : 1);
         abort_flag = 0;
@@ -454,17 +456,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
         // ------------------------------------------------ copies: this CTA's queries and its halves of the tiles
         if (lane == 0) {
             bool ok = true;
+            int asked = 0;                    // units whose queries have been asked for
+            auto queries = [&](const Unit& w) {
+                const int b = asked % NQ;
+                ok = asked < NQ || bar_wait(bar + (C::kQEmpty + b) * 8, (uint32_t)(asked / NQ - 1) & 1u, wt, 799);
+                if (!ok) return;
+                if (rank == 0) bar_expect(bar + (C::kQFull + b) * 8, 2 * C::QB);
+                for (int c = 0; c < C::CH; ++c)
+                    copy2_box3(qs + b * C::QB + c * C::RUN, &p.tq, 64 * c, w.first + kQ * rank, w.h, there + (C::kQFull + b) * 8);
+                ++asked;
+            };
             work([&](const Unit& w, int k) {
-                const int h = w.h, first = w.first, j0 = w.j0, tiles = w.tiles;
+                const int h = w.h, j0 = w.j0, tiles = w.tiles;
                 if (tiles <= 0) return true;
-                ok = un == 0 || bar_wait(bar + C::kQEmpty * 8, (uint32_t)(un - 1) & 1u, wt, 799);
-                if (!ok) return false;
-                if (rank == 0) bar_expect(bar + C::kQFull * 8, 2 * C::QB);
-                for (int c = 0; c < C::CH; ++c) copy2_box3(qs + c * C::RUN, &p.tq, 64 * c, first + kQ * rank, h, there + C::kQFull * 8);
-                ++un;
-                Unit next;
-                if (unit(k + 1, next))   // its queries, spread over the rows of all heads, come from far
-                    for (int c = 0; c < C::CH; ++c) ask_box3(&p.tq, 64 * c, next.first + kQ * rank, next.h);
+                if (asked == 0) queries(w);
                 for (int j = 0; j < tiles && ok; ++j, ++jt) {
                     const int s = jt % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
                     const uint32_t ph = (uint32_t)(jt / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
@@ -475,11 +480,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                     ok = ok && (jt < C::STAGES || bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801));
                     if (rank == 0) bar_expect(bar + (C::kVFull + s) * 8, 2 * C::VB);
                     copy2_box2(vs + s * C::VB, &p.tv, D / 2 * rank, row, vf);
+                    if (ok && j == (NQ == 2 ? min(1, tiles - 1) : tiles - 1)) {   // the next unit's queries, spread over the rows of all heads, come from far
+                        Unit next;
+                        int i = k + 1;
+                        bool is;
+                        while ((is = unit(i, next)) && next.tiles <= 0) ++i;
+                        if (is) queries(next);
+                    }
                 }
                 return ok;
             });
             if (!ok && rank == 0) {   // (after an abort) the copies in flight land before the pair leaves; these barriers know of both CTAs'
-                if (un > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(un - 1) & 1u, alone, 802);
+                for (int i = max(0, asked - NQ); i < asked; ++i) bar_wait(bar + (C::kQFull + i % NQ) * 8, (uint32_t)(i / NQ) & 1u, alone, 802);
                 for (int i = max(0, jt - C::STAGES); i < jt; ++i) {
                     bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 803);
                     bar_wait(bar + (C::kVFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 804);
@@ -494,40 +506,55 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
             const uint32_t one = elect_one();
             const uint64_t qd = operand(qs, 16, 1024, 2), kd = operand(ks, 16, 1024, 2);
             const uint64_t vd = operand(vs, 16, D * 8, D == 128 ? 2 : 4);   // a run of D / 2 columns
+            // The values of tile i, the j-th of unit u - 1: behind the next tile's scores, be they another unit's (with one buffer of queries those
+            // have to wait, and the values do not).
+            auto values = [&](int i, int j, int u) {
+                const int s = i % C::STAGES;
+                if (!warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i / C::STAGES) & 1u, wt, 812)) return false;
+                if (!warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 813)) return false;
+                if (j == 0 && u > 1 && !warp_wait(bar + C::kOFree * 8, (uint32_t)u & 1u, wt, 815)) return false;   // (u - 2: the unit before)
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma2_ts(one, tb + C::OCOL + (i & 1) * D, tb + (i & 1) * kQ + 8 * k, vd + s * (C::VB >> 4) + ((k * 16 * D) >> 4), IO, j > 1 || k > 0);
+                mma2_commit(one, bar + (C::kVEmpty + s) * 8);
+                return true;
+            };
+            int last_j = 0;
+            bool ok = true;
             work([&](const Unit& w, int) {
                 const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
                 if (tiles <= 0) return true;
-                if (!warp_wait(bar + C::kQFull * 8, (uint32_t)un & 1u, wt, 810)) return false;
+                const int b = un % NQ;
+                bool held = jt > 0;   // the tile before's values
+                if (NQ == 1 && held) {
+                    ok = values(jt - 1, last_j, un);
+                    held = false;
+                }
+                ok = ok && warp_wait(bar + (C::kQFull + b) * 8, (uint32_t)(un / NQ) & 1u, wt, 810);
+                if (!ok) return false;
                 ++un;
-                for (int j = 0; j <= tiles; ++j) {
-                    if (j < tiles) {
-                        const int s = jt % C::STAGES;
-                        if (!warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(jt / C::STAGES) & 1u, wt, 811)) return false;
-                        fence_after();
+                for (int j = 0; j < tiles; ++j) {
+                    const int s = jt % C::STAGES;
+                    ok = warp_wait(bar + (C::kKFull + s) * 8, (uint32_t)(jt / C::STAGES) & 1u, wt, 811);
+                    if (!ok) return false;
+                    fence_after();
 #pragma unroll
-                        for (int k = 0; k < 4 * C::CH; ++k)
-                            mma2_ss(one, tb + (jt & 1) * kQ, qd + (((k >> 2) * C::RUN + (k & 3) * 32) >> 4),
-                                    kd + s * (C::KB >> 4) + (((k >> 2) * C::KRUN + (k & 3) * 32) >> 4), IS, k > 0);
-                        mma2_commit(one, bar + (C::kKEmpty + s) * 8);
-                        mma2_commit(one, bar + (C::kSFull + (jt & 1)) * 8);
-                        if (j + 1 == tiles) mma2_commit(one, bar + C::kQEmpty * 8);
-                        ++jt;
-                    }
-                    if (j > 0) {   // (the tile before: jt - 2, or the last, jt - 1)
-                        const int i = j < tiles ? jt - 2 : jt - 1, s = i % C::STAGES;
-                        if (!warp_wait(bar + (C::kVFull + s) * 8, (uint32_t)(i / C::STAGES) & 1u, wt, 812)) return false;
-                        if (!warp_wait(bar + (C::kPReady + (i & 1)) * 8, (uint32_t)(i >> 1) & 1u, wt, 813)) return false;
-                        if (j == 1 && un > 1 && !warp_wait(bar + C::kOFree * 8, (uint32_t)un & 1u, wt, 815)) return false;   // (un - 2: the unit before)
-                        fence_after();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma2_ts(one, tb + C::OCOL + (i & 1) * D, tb + (i & 1) * kQ + 8 * k, vd + s * (C::VB >> 4) + ((k * 16 * D) >> 4), IO,
-                                    j > 2 || k > 0);
-                        mma2_commit(one, bar + (C::kVEmpty + s) * 8);
-                    }
+                    for (int k = 0; k < 4 * C::CH; ++k)
+                        mma2_ss(one, tb + (jt & 1) * kQ, qd + b * (C::QB >> 4) + (((k >> 2) * C::RUN + (k & 3) * 32) >> 4),
+                                kd + s * (C::KB >> 4) + (((k >> 2) * C::KRUN + (k & 3) * 32) >> 4), IS, k > 0);
+                    mma2_commit(one, bar + (C::kKEmpty + s) * 8);
+                    mma2_commit(one, bar + (C::kSFull + (jt & 1)) * 8);
+                    if (j + 1 == tiles) mma2_commit(one, bar + (C::kQEmpty + b) * 8);
+                    ok = !held || values(jt - 1, last_j, j > 0 ? un : un - 1);
+                    if (!ok) return false;
+                    held = true;
+                    last_j = j;
+                    ++jt;
                 }
                 return true;
             });
+            if (ok && jt > 0) values(jt - 1, last_j, un);
             mma2_commit(one, bar + C::kDone * 8);
             warp_wait(bar + C::kDone * 8, 0u, alone, 814);
         }
@@ -842,15 +869,22 @@ static int pairs_at_once(K kernel, int threads, size_t smem, std::atomic<int>* k
     return QL_OK;
 }
 
+// The attention's shared memory allowed and its pairs counted, once.
+template <int D, int NQ>
+static int attention_ready(int* pairs) {
+    static std::atomic<unsigned long long> done{0};
+    static std::atomic<int> most[64];
+    QL_TRY_CUDA(allow_smem_once(mla_chunk_kernel<D, NQ>, ChunkCfg<D, NQ>::SMEM, done));
+    return pairs_at_once(mla_chunk_kernel<D, NQ>, kChunkThreads, ChunkCfg<D, NQ>::SMEM, most, pairs);
+}
+
 template <int D, int R>
 static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
     using E = ExpandCfg<D, R>;
-    using C = ChunkCfg<D>;
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "ql_mla_attn_chunk: no device error record");
-    static std::atomic<unsigned long long> done{0}, done2{0};
+    static std::atomic<unsigned long long> done{0};
     QL_TRY_CUDA(allow_smem_once(mla_expand_kernel<D, R>, E::SMEM, done));
-    QL_TRY_CUDA(allow_smem_once(mla_chunk_kernel<D>, C::SMEM, done2));
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     ExpandParams ep = {};
     ChunkParams cp = {};
@@ -903,16 +937,18 @@ static int chunk_go(const AttnIn& a, const ChunkShape& sh, cudaStream_t s) {
     cp.cut = sh.cut;
     cp.scale_log2 = a.scale * 1.44269504088896340736f;
     // as many pairs as the GPU holds at once, and as there can be work for
-    static std::atomic<int> most[64], most2[64];
+    static std::atomic<int> most[64];
     int pairs = 0, pairs2 = 0;
     if (int rc = pairs_at_once(mla_expand_kernel<D, R>, E::THREADS, E::SMEM, most, &pairs)) return rc;
-    if (int rc = pairs_at_once(mla_chunk_kernel<D>, kChunkThreads, C::SMEM, most2, &pairs2)) return rc;
+    constexpr int ONE = D == 128 ? 1 : 2;   // buffers of queries where units are cut
+    if (int rc = sh.cut ? attention_ready<D, ONE>(&pairs2) : attention_ready<D, 2>(&pairs2)) return rc;
     pairs = (int)std::min<int64_t>(pairs, sh.cap / 256 * ((a.H + E::HEADS - 1) / E::HEADS));
     pairs2 = sh.cut ? std::min(pairs2, kMostPairs) : (int)std::min<int64_t>(pairs2, (a.rows + 2 * kQ - 1) / (2 * kQ) * a.H);
     cp.pairs = pairs2;
     cudaError_t e = launch(mla_expand_kernel<D, R>, dim3(2 * (unsigned)pairs), dim3(E::THREADS), E::SMEM, s, true, ep);
     if (e == cudaSuccess)
-        e = launch(mla_chunk_kernel<D>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), C::SMEM, s, true, cp);
+        e = sh.cut ? launch(mla_chunk_kernel<D, ONE>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), ChunkCfg<D, ONE>::SMEM, s, true, cp)
+                   : launch(mla_chunk_kernel<D, 2>, dim3(2 * (unsigned)pairs2), dim3(kChunkThreads), ChunkCfg<D, 2>::SMEM, s, true, cp);
     if (e == cudaSuccess && sh.cut)
         e = launch(mla_chunk_join_kernel<D>, dim3((unsigned)((a.rows * a.H + 7) / 8)), dim3(256), 0, s, true, cp);
     return e == cudaSuccess ? QL_OK : cuda_error(e, "ql_mla_attn_chunk");
