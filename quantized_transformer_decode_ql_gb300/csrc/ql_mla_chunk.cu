@@ -300,7 +300,7 @@ struct ChunkParams {
 // 256 after 7936, 40 heads, 116.5 -> 105; 1000 after 1000, 8 heads, 27.3 -> 28.4).
 // A causal prompt of 4096 tokens, 32 heads of 128: 127 us, 1.35 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
-// warps (600) for two tiles. From unit to unit go 2 - 3 thousand cycles more. The weights are f16 (the product's operand, up to 2^14), their sums f32.
+// warps (600) for two tiles. From unit to unit go 4 thousand cycles more. The weights are f16 (the product's operand, up to 2^14), their sums f32.
 // Without gain: weights before their maximum is known, judged by their sum (registers spill: 156 -> 170 us a prompt).
 template <int D, int NQ>
 struct ChunkCfg {
