@@ -42,33 +42,14 @@ __device__ __forceinline__ bool bar_wait(uint32_t mb, uint32_t parity, const Wai
     if (persist::mbar_test(mb, parity) || persist::mbar_test(mb, parity)) return true;
     return wait_slow(mb, parity, w, where);
 }
-// no waiting
-__device__ __forceinline__ bool bar_ready(uint32_t mb, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{\n .reg .pred q;\n mbarrier.test_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 %0, 1, 0, q;\n}"
-                 : "=r"(done) : "r"(mb), "r"(parity) : "memory");
-    return done != 0;
-}
 // by every lane, one answer for the warp
 __device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
     return __all_sync(0xffffffffu, bar_wait(mb, parity, w, where));
 }
 
-__device__ __forceinline__ void copy_box2(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t mb) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(mb) : "memory");
-}
-__device__ __forceinline__ void copy_box3(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t mb) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(mb) : "memory");
-}
 __device__ __forceinline__ void copy_box4(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int u, uint32_t mb) {
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(mb) : "memory");
-}
-// into L2 only
-__device__ __forceinline__ void ask_box3(const CUtensorMap* m, int x, int y, int z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 // from shared memory; the issuing thread's copies so far have been read, or have arrived
 __device__ __forceinline__ void store_box2(const CUtensorMap* m, int x, int y, uint32_t src) {
@@ -107,11 +88,6 @@ __device__ __forceinline__ uint32_t elect_one() {
 __device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
                  " @pe tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pa;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
-}
-// A in tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n .reg .pred pa, pe;\n setp.ne.u32 pa, %4, 0;\n setp.ne.u32 pe, %5, 0;\n"
-                 " @pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pa;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one) : "memory");
 }
 // The MMAs issued so far arrive on the barrier as they complete.
 __device__ __forceinline__ void mma_commit(uint32_t one, uint32_t mb) {
