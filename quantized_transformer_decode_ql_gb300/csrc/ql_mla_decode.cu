@@ -262,9 +262,9 @@ __device__ Window make_window(const DecodeParams& p, int win) {
 // One CTA an SM, a window of the batch's tiles each. Two stages of 64 keys (73.7 KB each at rank 512) and the queries fill shared memory; a
 // stage is freed a block of 16 keys at a time. Scores have the keys as rows and the heads as columns, so that a softmax thread keeps one key's
 // heads in registers and stores its weights as the value product's B operand.
-//  16 x 20000 - 40960, 64 heads, rank 512: 105 us of the call's 120, 5.5 TB/s. A tile takes 2.0 us, 1.75 where the cache is in L2: HBM's latency
+//  16 x 20000 - 40960, 64 heads, rank 512: 105 us of the call's 119, 5.5 TB/s. A tile takes 2.0 us, 1.75 where the cache is in L2: HBM's latency
 //    and the chain of scores, softmax and values through two stages bound it together.
-//  32 x 128 - 8192, 32 heads: 38 us of 52; 5.5 - 5.9 TB/s in the loop, where copies of such tiles alone reach 6.6.
+//  32 x 128 - 8192, 32 heads: 38 us of 51; 5.5 - 5.9 TB/s in the loop, where copies of such tiles alone reach 6.6.
 template <int R, int NH>
 __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = Cfg<R, NH>;
