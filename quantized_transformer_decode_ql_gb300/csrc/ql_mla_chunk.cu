@@ -298,7 +298,7 @@ struct ChunkParams {
 // Where there are few (cut), all units' tiles in a row are cut into a window a pair instead, and parts of a unit joined afterwards (against a number
 // of parts that is the same for all units: 777 tokens after 1234, 20 heads of 64, 37.1 -> 32.8 us; 256 after 30000, 32 heads of 128, 284 -> 275;
 // 256 after 7936, 40 heads, 116.5 -> 105; 1000 after 1000, 8 heads, 27.3 -> 28.4).
-// A causal prompt of 4096 tokens, 32 heads of 128: 124 us, 1.39 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
+// A causal prompt of 4096 tokens, 32 heads of 128: 129 us, 1.33 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
 // warps (600) for two tiles. From unit to unit go 4 thousand cycles more. The weights are f16 (the product's operand, up to 2^14), their sums f32.
 // Without gain: weights before their maximum is known, judged by their sum (registers spill: 156 -> 170 us a prompt).
