@@ -79,6 +79,18 @@ struct ExpandCfg {
     static_assert(SMEM + 2048 <= 232448, "shared memory");
 };
 
+// The pair's copies in flight, after an abort.
+template <typename C>
+__device__ __noinline__ void settle_expand(uint32_t bar, uint32_t issued, DevError* err, unsigned long long ns) {
+    if (cluster_rank() == 0 && threadIdx.x == 32 * C::kCopy) {
+        const Waits alone = {err, nullptr, ns};
+        settle_ring(bar + C::kAFull * 8, C::KC, issued, C::AB, alone, 702);
+        settle_ring(bar + C::kBFull * 8, C::STAGES, issued + 4, C::BB, alone, 703);
+    }
+    __syncthreads();
+    cluster_sync();
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(2, 1, 1) mla_expand_kernel(const __grid_constant__ ExpandParams p) {
     using C = ExpandCfg<D, R>;
@@ -86,6 +98,7 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
+    __shared__ int issued[2];   // copies of the tokens' runs, of the weights
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t bar = su32(bars), as = su32(smem), bs = as + C::KC * C::AB;
@@ -102,7 +115,7 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
     cluster_sync();
     fence_after();
     const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0);
-    const Waits wt = {p.err, &abort_flag, p.ns};
+    const PairWaits wt = {{p.err, &abort_flag, p.ns}};
     const Waits alone = {p.err, nullptr, p.ns};
     pdl_wait();
     pdl_trigger();   // not before this CTA has its tensor memory: the attention, which takes all of it, waits for this grid's end
@@ -117,7 +130,7 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
     if (warp == C::kCopy) {
         // ------------------------------------------------ copies: a block of 16 tokens a lane, the weights by lane 0
         const long long nblk = (L + kBlock - 1) / kBlock;
-        int held = -1, loads = 0, it = 0;
+        int held = -1, loads = 0, it = 0, runs = 0;
         bool ok = true;
         int tp = u0 / hgs, hg = u0 - tp * hgs;
         for (int u = u0; u < u1 && ok; ++u, hg = hg + 1 == hgs ? 0 : hg + 1, tp += hg == 0) {
@@ -138,25 +151,29 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
                 held = tp;
                 ++loads;
             }
-            for (int c = 0; c < C::KC; ++c, ++it) {
+            for (int c = 0; c < C::KC; ++c) {   // (behind a wait that failed nothing is armed or issued)
                 const int s = it % C::STAGES;
                 if (fresh) {   // a run of the tokens' values makes room as its last product ends
-                    ok = ok && (loads < 2 || warp_wait(bar + (C::kAEmpty + c) * 8, (uint32_t)loads & 1u, wt, 700));
+                    ok = loads < 2 || warp_wait(bar + (C::kAEmpty + c) * 8, (uint32_t)loads & 1u, wt, 700);
+                    if (!ok) break;
+                    ++runs;
                     if (lane == 0 && rank == 0) bar_expect(bar + (C::kAFull + c) * 8, 2 * C::AB);
                     __syncwarp();
                     if (lane < 8) copy2_box2(as + c * C::AB + lane * 2048, &p.tc, 64 * c, row, there + (C::kAFull + c) * 8);
                 }
-                ok = ok && (it < C::STAGES || warp_wait(bar + (C::kBEmpty + s) * 8, (uint32_t)(it / C::STAGES - 1) & 1u, wt, 701));
-                if (lane == 0) {   // (after an abort the unit's copies still go out, so that they can be waited for)
+                ok = it < C::STAGES || warp_wait(bar + (C::kBEmpty + s) * 8, (uint32_t)(it / C::STAGES - 1) & 1u, wt, 701);
+                if (!ok) break;
+                ++it;
+                if (lane == 0) {
                     if (rank == 0) bar_expect(bar + (C::kBFull + s) * 8, 2 * C::BB);
                     copy2_box2(bs + s * C::BB, &p.tw, 64 * c, hg * 256 + 128 * rank, there + (C::kBFull + s) * 8);
                 }
                 __syncwarp();
             }
         }
-        if (!ok && rank == 0) {   // (the barriers of rank 0 know of both CTAs' copies)
-            for (int c = 0; loads > 0 && c < C::KC; ++c) warp_wait(bar + (C::kAFull + c) * 8, (uint32_t)(loads - 1) & 1u, alone, 702);
-            for (int i = max(0, it - C::STAGES); i < it; ++i) warp_wait(bar + (C::kBFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 703);
+        if (lane == 0) {
+            issued[0] = runs;
+            issued[1] = it;
         }
     } else if (warp == C::kProduct) {
         // ------------------------------------------------ products of both CTAs, issued by rank 0
@@ -265,6 +282,7 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
     fence_before();
     __syncthreads();
     cluster_sync();   // no product, report or commit is left that touches the other CTA
+    if (abort_flag) settle_expand<C>(su32(bars), su32(issued), p.err, p.ns);   // (the same in both)
     if (warp == C::kProduct) {
         fence_after();
         tmem_free2<512>(tb);
@@ -362,6 +380,19 @@ struct Row {
     __device__ int start(int b, int h) const { return start(b) + h * (tiles(b) + enter); }
 };
 
+// The pair's copies in flight, after an abort.
+template <typename C, int NQ>
+__device__ __noinline__ void settle_chunk(uint32_t bar, uint32_t issued, DevError* err, unsigned long long ns) {
+    if (cluster_rank() == 0 && threadIdx.x == 32 * kCopy) {
+        const Waits alone = {err, nullptr, ns};
+        settle_ring(bar + C::kQFull * 8, NQ, issued, C::QB, alone, 802);
+        settle_ring(bar + C::kKFull * 8, C::STAGES, issued + 4, C::KB, alone, 803);
+        settle_ring(bar + C::kVFull * 8, C::STAGES, issued + 8, C::VB, alone, 804);
+    }
+    __syncthreads();
+    cluster_sync();
+}
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = ChunkCfg<D, NQ>;
@@ -369,6 +400,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
+    __shared__ int issued[3];   // copies of queries, keys, values
     __shared__ int rows_now;    // read once, so that all warps run the same tiles
     __shared__ float tops[2][2][kQ], sums[2][2][2][kQ], refs[2][2][kQ];   // (sums and refs of two units in turn)
     const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
@@ -390,7 +422,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     cluster_sync();
     fence_after();
     const uint32_t tb = __shfl_sync(0xffffffffu, tmem_at, 0), there = in_cta(bar, 0);
-    const Waits wt = {p.err, &abort_flag, p.ns};
+    const PairWaits wt = {{p.err, &abort_flag, p.ns}};
     const Waits alone = {p.err, nullptr, p.ns};
     const long long L = rows_now;
     // whether a block of the context is missing (its keys are then left out): the rare case is told apart here, once, beside the
@@ -456,7 +488,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
         // ------------------------------------------------ copies: this CTA's queries and its halves of the tiles
         if (lane == 0) {
             bool ok = true;
-            int asked = 0;                    // units whose queries have been asked for
+            int asked = 0, keys = 0, vals = 0;   // units whose queries have been asked for, tiles (behind a wait that failed nothing is armed or issued)
             auto queries = [&](const Unit& w) {
                 const int b = asked % NQ;
                 ok = asked < NQ || bar_wait(bar + (C::kQEmpty + b) * 8, (uint32_t)(asked / NQ - 1) & 1u, wt, 799);
@@ -470,17 +502,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 const int h = w.h, j0 = w.j0, tiles = w.tiles;
                 if (tiles <= 0) return true;
                 if (asked == 0) queries(w);
-                for (int j = 0; j < tiles && ok; ++j, ++jt) {
-                    const int s = jt % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
-                    const uint32_t ph = (uint32_t)(jt / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
-                    ok = jt < C::STAGES || bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800);
+                for (int j = 0; j < tiles && ok; ++j) {
+                    const int s = vals % C::STAGES, at = (j0 + j) * kQ, row = (int)((long long)h * p.cap) + at;
+                    const uint32_t ph = (uint32_t)(vals / C::STAGES - 1) & 1u, kf = there + (C::kKFull + s) * 8, vf = there + (C::kVFull + s) * 8;
+                    ok = vals < C::STAGES || bar_wait(bar + (C::kKEmpty + s) * 8, ph, wt, 800);
+                    if (!ok) break;
+                    ++keys;
                     if (rank == 0) bar_expect(bar + (C::kKFull + s) * 8, 2 * C::KB);
                     for (int c = 0; c < D / 64; ++c) copy2_box2(ks + s * C::KB + c * C::KRUN, &p.tk, 64 * c, row + 64 * rank, kf);
                     copy2_box2(ks + s * C::KB + D / 64 * C::KRUN, &p.tt, 0, at + 64 * rank, kf);
-                    ok = ok && (jt < C::STAGES || bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801));
+                    ok = vals < C::STAGES || bar_wait(bar + (C::kVEmpty + s) * 8, ph, wt, 801);
+                    if (!ok) break;
+                    ++vals;
                     if (rank == 0) bar_expect(bar + (C::kVFull + s) * 8, 2 * C::VB);
                     copy2_box2(vs + s * C::VB, &p.tv, D / 2 * rank, row, vf);
-                    if (ok && j == (NQ == 2 ? min(1, tiles - 1) : tiles - 1)) {   // the next unit's queries, spread over the rows of all heads, come from far
+                    if (j == (NQ == 2 ? min(1, tiles - 1) : tiles - 1)) {   // the next unit's queries, spread over the rows of all heads, come from far
                         Unit next;
                         int i = k + 1;
                         bool is;
@@ -490,13 +526,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 }
                 return ok;
             });
-            if (!ok && rank == 0) {   // (after an abort) the copies in flight land before the pair leaves; these barriers know of both CTAs'
-                for (int i = max(0, asked - NQ); i < asked; ++i) bar_wait(bar + (C::kQFull + i % NQ) * 8, (uint32_t)(i / NQ) & 1u, alone, 802);
-                for (int i = max(0, jt - C::STAGES); i < jt; ++i) {
-                    bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 803);
-                    bar_wait(bar + (C::kVFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 804);
-                }
-            }
+            issued[0] = asked;
+            issued[1] = keys;
+            issued[2] = vals;
         }
         __syncwarp();
     } else if (warp == kProduct) {
@@ -748,6 +780,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     fence_before();
     __syncthreads();
     cluster_sync();   // no product, report or commit is left that touches the other CTA
+    if (abort_flag) settle_chunk<C, NQ>(su32(bars), su32(issued), p.err, p.ns);   // (the same in both)
     if (warp == kProduct) {
         fence_after();
         tmem_free2<C::COLS>(tb);

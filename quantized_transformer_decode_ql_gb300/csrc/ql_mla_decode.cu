@@ -259,6 +259,18 @@ __device__ Window make_window(const DecodeParams& p, int win) {
     return {lo, hi, found[0], found[1]};
 }
 
+// After an abort, behind a barrier of the CTA: whoever gave up, the copies in flight land before the CTA leaves.
+template <typename C>
+__device__ __noinline__ void settle_decode(uint32_t bar, const int* issued, DevError* err, unsigned long long ns) {
+    if (threadIdx.x != 32 * C::kCopyWarp) return;
+    const Waits alone = {err, nullptr, ns};
+    const int it = issued[0], sg = issued[2];
+    if (issued[1]) bar_forgo(bar + (C::kKFull + (it - 1) % C::STAGES) * 8, issued[1] * 2 * C::GROUP);
+    for (int i = max(0, it - C::STAGES); i < it; ++i)
+        bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, (uint32_t)(i / C::STAGES) & 1u, alone, 300);
+    if (sg > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(sg - 1) & 1u, alone, 301);
+}
+
 // One CTA an SM, a window of the batch's tiles each. Two stages of 64 keys (73.7 KB each at rank 512) and the queries fill shared memory; a
 // stage is freed a block of 16 keys at a time. Scores have the keys as rows and the heads as columns, so that a softmax thread keeps one key's
 // heads in registers and stores its weights as the value product's B operand.
@@ -273,6 +285,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     __shared__ __align__(8) unsigned long long bars[C::kBars];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
+    __shared__ int issued[3];   // tiles, blocks that the last one lacks, queries
     __shared__ int live_blocks[C::STAGES];
     __shared__ __align__(16) float ref[NH];          // the weights' reference of each head, log2, negated
     __shared__ float factor[NH], column[4][NH];
@@ -330,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     int it = 0, sg = 0;   // tiles and sequences so far
     if (warp == C::kCopyWarp) {
         // ------------------------------------------------ copies: lanes 0-3 bring the tile's four blocks
-        bool ok = true;
+        int missing = 0;   // blocks of the last tile whose bytes are expected and not asked for
         sequences([&](int b, int len, int t0, int t1) {
             auto query = [&] {
                 if (lane == 0) {
@@ -341,8 +354,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
             };
             bool first = sg == 0;
             if (!first) {
-                ok = warp_wait(bar + C::kQEmpty * 8, (uint32_t)(sg - 1) & 1u, wt, 100);
-                if (!ok) return false;
+                if (!warp_wait(bar + C::kQEmpty * 8, (uint32_t)(sg - 1) & 1u, wt, 100)) return false;
                 query();
             }
             const int nblk = (len + kBlock - 1) / kBlock;
@@ -362,22 +374,28 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                 const unsigned mask = __ballot_sync(0xffffffffu, live) & 15u;
                 const int now = live ? 2 * id : 2 * (int)p.num_blocks;   // outside: zeros
                 if (tt + 1 < t1) id = load_id(tt + 1);
+                // The stage's last phase is complete before it is armed again, also where a wait has failed (weights of its tile are then
+                // reported, and its blocks given back, whatever has arrived).
+                bool ok = it < C::STAGES || warp_wait(bar + (C::kKFull + s) * 8, turn(it - C::STAGES), wt, 204), sent = false;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {   // (after an abort this tile's copies still go out, so that its barrier can be waited for)
+                for (int k = 0; k < 4; ++k) {   // (behind a wait that failed nothing is armed or asked for)
                     ok = ok && (it < C::STAGES || warp_wait(empty(it, k), turn(it - C::STAGES), wt, 200 + k));
                     if (k == 0 && lane == 0) {
                         live_blocks[s] = (int)mask;
                         fence_async();   // rows cleared through the generic proxy before the copies into them
                     }
                     __syncwarp();
-                    if (lane == k) {
+                    if (lane == k && ok) {
                         if (k == 0) bar_expect(bar + (C::kKFull + s) * 8, C::TILE);
                         copy_box4(ks + s * C::TILE + k * 2 * C::GROUP, &p.tk, 0, 0, 0, now, bar + (C::kKFull + s) * 8);
+                        sent = true;
                     }
                     __syncwarp();
                 }
                 if (!ok) {
-                    ++it;
+                    const int blocks = __popc(__ballot_sync(0xffffffffu, sent));
+                    missing = blocks ? 4 - blocks : 0;
+                    it += blocks > 0;
                     return false;
                 }
             }
@@ -388,11 +406,11 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
             }
             return true;
         });
-        if (!ok && lane == 0) {   // (only after an abort)
-            for (int i = max(0, it - C::STAGES); i < it; ++i) bar_wait(bar + (C::kKFull + i % C::STAGES) * 8, turn(i), alone, 300);
-            if (sg > 0) bar_wait(bar + C::kQFull * 8, (uint32_t)(sg - 1) & 1u, alone, 301);
+        if (lane == 0) {
+            issued[0] = it;
+            issued[1] = missing;
+            issued[2] = sg;
         }
-        __syncwarp();
     } else if (warp == C::kScoreWarp) {
         // ------------------------------------------------ S^T = K q'^T, two tiles ahead of their values at most
         constexpr uint32_t I = instr(64, C::NQ, false, false);
@@ -618,6 +636,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
     pdl_trigger();
     fence_before();
     __syncthreads();
+    if (abort_flag) settle_decode<C>(su32(bars), issued, p.err, p.ns);
     if (warp == C::kScoreWarp) {
         fence_after();
         tmem_free<C::COLS>(tb);

@@ -19,6 +19,10 @@ __device__ __forceinline__ void bar_arrive(uint32_t mb) { asm volatile("mbarrier
 __device__ __forceinline__ void bar_expect(uint32_t mb, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
 }
+// expected bytes whose copy is not going to be issued
+__device__ __forceinline__ void bar_forgo(uint32_t mb, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
+}
 // What a bounded wait needs: an expiry records an error (index = CTA, value = where), raises the CTA's abort flag, which ends the
 // other roles' waits, and returns false.
 struct Waits {
@@ -26,6 +30,9 @@ struct Waits {
     int* abort_flag;
     unsigned long long ns;
 };
+// In a pair of CTAs it raises the other's flag, too, so that both know once they have met.
+struct PairWaits : Waits {};
+template <bool PAIR>
 static __device__ __noinline__ bool wait_slow(uint32_t mb, uint32_t parity, Waits w, int where) {
     const unsigned long long t0 = persist::global_ns();
     for (unsigned int spin = 1;; ++spin) {
@@ -35,15 +42,25 @@ static __device__ __noinline__ bool wait_slow(uint32_t mb, uint32_t parity, Wait
             if (persist::global_ns() - t0 > w.ns) break;
         }
     }
+    if constexpr (PAIR) {
+        uint32_t other;
+        asm volatile("{\n .reg .u32 r;\n mov.u32 r, %%cluster_ctarank;\n xor.b32 r, r, 1;\n mapa.shared::cluster.u32 %0, %1, r;\n"
+                     " st.shared::cluster.u32 [%0], %2;\n}" : "=&r"(other) : "r"(su32(w.abort_flag)), "r"(1) : "memory");
+    }
     if (w.abort_flag == nullptr || atomicExch(w.abort_flag, 1) == 0) record_device_error(w.err, kErrLatentStage, blockIdx.x, where);
     return false;
 }
 __device__ __forceinline__ bool bar_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
     if (persist::mbar_test(mb, parity) || persist::mbar_test(mb, parity)) return true;
-    return wait_slow(mb, parity, w, where);
+    return wait_slow<false>(mb, parity, w, where);
+}
+__device__ __forceinline__ bool bar_wait(uint32_t mb, uint32_t parity, const PairWaits& w, int where) {
+    if (persist::mbar_test(mb, parity) || persist::mbar_test(mb, parity)) return true;
+    return wait_slow<true>(mb, parity, w, where);
 }
 // by every lane, one answer for the warp
-__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, const Waits& w, int where) {
+template <typename W>
+__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, const W& w, int where) {
     return __all_sync(0xffffffffu, bar_wait(mb, parity, w, where));
 }
 
@@ -143,6 +160,23 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t mb) {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int load_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// After an abort, by one thread of rank 0, behind a barrier of the pair: no copy is issued any more. Every copy into a ring of n stages, of
+// which each CTA brings `bytes`, reports to rank 0's barriers at mb, and each CTA has noted at `issued` how many it has asked for (rank 0 has
+// armed the barrier for its own). Each waited for its stage first, so that they are a ring apart at most and the phase before is complete.
+// What only one of them has asked for is armed, or given up, for the other, and the copies in flight are waited for.
+__device__ __forceinline__ void settle_ring(uint32_t mb, int n, uint32_t issued, uint32_t bytes, const Waits& alone, int where) {
+    const int mine = load_cluster(in_cta(issued, 0)), other = load_cluster(in_cta(issued, 1)), all = max(mine, other);
+    for (int i = min(mine, other); i < all; ++i) {
+        if (i >= mine) bar_expect(mb + i % n * 8, bytes);
+        else bar_forgo(mb + i % n * 8, bytes);
+    }
+    for (int i = max(0, all - n); i < all; ++i) bar_wait(mb + i % n * 8, (uint32_t)(i / n) & 1u, alone, where);
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
