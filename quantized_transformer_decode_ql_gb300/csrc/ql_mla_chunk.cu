@@ -330,9 +330,9 @@ struct ChunkCfg {
     static constexpr size_t SMEM = NQ * QB + STAGES * (KB + VB);
     static constexpr uint32_t OCOL = 256, COLS = 512;                // tensor memory: two S (P over them), two O
     // what has landed in either CTA, and the weights of both, are reported to rank 0's barriers, what the products have read or
-    // written to both CTAs'
+    // written to both CTAs'; a unit's sums are left to its own CTA's
     static constexpr int kQFull = 0, kQEmpty = NQ, kKFull = 2 * NQ, kKEmpty = kKFull + STAGES, kVFull = kKEmpty + STAGES, kVEmpty = kVFull + STAGES,
-                         kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kOFree = kPReady + 2, kDone = kOFree + 1, kBars = kDone + 1;
+                         kSFull = kVEmpty + STAGES, kPReady = kSFull + 2, kOFree = kPReady + 2, kSums = kOFree + 1, kDone = kSums + 2, kBars = kDone + 1;
 };
 
 // Four lanes' four 16-byte units each, transposed: unit r of lane i becomes what was unit i of lane r.
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     const uint32_t rank = cluster_rank();
     const uint32_t bar = su32(bars), qs = su32(smem), ks = qs + NQ * C::QB, vs = ks + C::STAGES * C::KB;
     if (t == 0) {
-        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, i == C::kPReady || i == C::kPReady + 1 || i == C::kOFree ? kSoft : 1);
+        for (int i = 0; i < C::kBars; ++i) bar_init(bar + i * 8, (i >= C::kPReady && i <= C::kOFree) || i == C::kSums || i == C::kSums + 1 ? kSoft : 1);
         abort_flag = 0;
         rows_now = (int)context(p.position, p.n, p.maxb);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
     } else {
         // ------------------------------------------------ softmax: eight warps have the even tiles, eight the odd ones; of the eight, four
         // have keys 0 - 63 of a tile and four the rest; a thread has one query. The eight run the same tiles whatever their waits
-        // return, so that their barriers always meet.
+        // return, so that their named barriers always meet. The two eights meet on mbarriers, by bounded waits: once one has failed nothing
+        // keeps them within a unit of each other.
         const int g = warp >> 3, hf = (warp >> 2) & 1, q = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, sc = tb + lanes + g * kQ, oc = tb + lanes + C::OCOL + g * D;
         const float2 scale = make_float2(p.scale_log2, p.scale_log2);
@@ -695,15 +696,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
             float ma = -1e30f, mb = -1e30f, total = 0.f;
             if (tiles > 0) {
                 const int lastg = (jt + tiles - 1) & 1, turn = un & 1;
+                const uint32_t left = bar + (C::kSums + turn) * 8, phase = (uint32_t)(un >> 1) & 1u;
                 sums[turn][g][hf][q] = l;
                 refs[turn][g][q] = set ? m : -1e30f;          // (the same from both halves of the keys)
                 ++un;
+                __syncwarp();
+                if (lane == 0) bar_arrive(left);
                 if (g != lastg) {
-                    asm volatile("barrier.cta.arrive %0, 512;" ::"r"(3 + turn) : "memory");
                     jt += tiles;
                     return true;
                 }
-                asm volatile("barrier.cta.sync %0, 512;" ::"r"(3 + turn) : "memory");
+                warp_wait(left, phase, wt, 823);
                 ma = refs[turn][0][q];
                 mb = refs[turn][1][q];
                 const float top = fmaxf(ma, mb);

@@ -342,13 +342,14 @@ def expand(units, hgs, u0, KC, STAGES, seed, broken=False, old=False):
     return sim.expired
 
 
-def chunk(units, NQ, STAGES, seed, broken=False, old=False, raises=0.0):
+def chunk(units, NQ, STAGES, seed, broken=False, old=False, named=False, raises=0.0):
     """`units`: tiles of each."""
     sim = Sim(seed, broken, 2)
     qfull, kfull, vfull = ([Bar(1, f"{x}{s}") for s in range(n)] for x, n in (("QFull", NQ), ("KFull", STAGES), ("VFull", STAGES)))
     qempty, kempty, vempty, sfull = pairs_of(NQ, "QEmpty"), pairs_of(STAGES, "KEmpty"), pairs_of(STAGES, "VEmpty"), pairs_of(2, "SFull")
     pready, ofree, done = [Bar(2, f"PReady{g}") for g in range(2)], Bar(2, "OFree"), Bar(1, "Done")
     q, k, v = ([[Stage() for _ in range(n)] for _ in range(2)] for n in (NQ, STAGES, STAGES))
+    sums = pairs_of(2, "Sums", 2)
     issued = [[0, 0, 0], [0, 0, 0]]
 
     def copies(rank):
@@ -440,7 +441,7 @@ def chunk(units, NQ, STAGES, seed, broken=False, old=False, raises=0.0):
 
     def softmax(rank, g):
         jt = 0
-        for tiles in units:
+        for un, tiles in enumerate(units):
             off = (jt & 1) ^ g
             for i, j in enumerate(range(jt + off, jt + tiles, 2)):
                 yield from sim.wait(sfull[g][rank], j >> 1, rank)
@@ -448,7 +449,16 @@ def chunk(units, NQ, STAGES, seed, broken=False, old=False, raises=0.0):
                     yield from sim.wait(vempty[(j - 2) % STAGES][rank], (j - 2) // STAGES, rank)
                 pready[g].arrive()
                 yield True
+            left = sums[un & 1][rank]
+            at = left.phase
+            left.arrive()
+            yield True
             if g == (jt + tiles - 1) & 1:
+                if named:       # a named barrier: no limit, and whoever arrives counts
+                    while left.phase == at:
+                        yield False
+                else:
+                    yield from sim.wait(left, un >> 1, rank)
                 for j in range(max(jt, jt + tiles - 2), jt + tiles):
                     yield from sim.wait(vempty[j % STAGES][rank], j // STAGES, rank)
                 ofree.arrive()
@@ -491,3 +501,18 @@ def test_model_sees_copies_behind_a_failed_wait(kernel, sizes):
             except AssertionError as e:
                 seen |= {m for m in ("armed for phase", "over a stage", "in flight") if m in str(e)}
     assert "armed for phase" in seen and "in flight" in seen, seen
+
+
+def test_model_sees_a_named_barrier_behind_a_failed_wait():
+    """The half of the softmax that only arrives runs ahead once no wait holds it, completes the other's barrier by itself, and the
+    other's last wait, which has no limit, never ends."""
+    stuck = 0
+    for seed in range(40):
+        for some in CHUNK:
+            try:
+                chunk(*some, seed, broken=True, named=True)
+            except AssertionError as e:
+                assert "no role can move" in str(e)
+                stuck += 1
+        assert chunk(*CHUNK[3], seed, named=True) == 0
+    assert stuck
