@@ -434,8 +434,9 @@ int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, 
  * that costs less: n_tokens <= n_heads * head_dim / 128, or n_tokens * n_heads <= 512 under a table of at most 64 blocks.
  * d_out f16 [n_tokens][n_heads * head_dim]. Block ids as for ql_mla_attn_decode (an output of 0 for a query that no key is
  * left for); a position below 0 or a chunk that ends behind the table is recorded and leaves the output as it was. A row
- * that holds NaN or an infinity spoils the outputs of the queries that see it, and no others; a key or value (in the
- * absorbed form: an absorbed query) that f16 does not hold is recorded. 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22,
+ * that holds NaN or an infinity spoils the outputs of the queries that see it, and no others. A key or value (in the
+ * absorbed form: an absorbed query) that f16 does not hold is recorded; only queries that see such a row are then wrong (a value is
+ * taken as the largest f16). 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22,
  * max_blocks_per_seq <= 2^16. Alignments and workspace as for ql_mla_attn_decode; ql_mla_chunk_workspace_bytes(...) bytes
  * are enough for fewer tokens under the same table too. */
 size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq);

@@ -257,7 +257,14 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
                 float most = 0.f;
 #pragma unroll
                 for (int i = 0; i < 64; ++i) most = fmaxf(most, fabsf(f[i]));
-                if (in && most >= 65520.f) record_device_error(p.err, kErrLatentValue, tok, h);
+                if (in && most >= 65520.f) {
+                    record_device_error(p.err, kErrLatentValue, tok, h);
+                    // a value as the largest that f16 holds: an infinity would meet the weights of 0 of queries that do not see it
+                    if (e >= D) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) f[i] = fabsf(f[i]) < INFINITY ? fminf(fmaxf(f[i], -65504.f), 65504.f) : f[i];
+                    }
+                }
                 if (broken) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) f[i] = e < D ? NAN : 0.f;
