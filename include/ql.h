@@ -398,8 +398,8 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  * elements apart) is written to row i of d_q_out, f16, contiguous, the last rope_dim values of each head rotated alike. d_q and
  * d_q_out may both be NULL. A slot of -1 marks a row to leave out (a padded batch): neither its
  * cache row nor its query is written. Any other slot outside the pool, or a position outside the tables, leaves
- * the row out too and is recorded in the device error record, as is a cache row with a value that f16 does
- * not hold or whose squares' sum f32 does not (the row is written). The slots of one call must differ from one another (-1 may repeat).
+ * the row out too and is recorded in the device error record, as is a cache row or a query with a value that f16 does
+ * not hold, or a cache row whose squares' sum f32 does not (the row is written). The slots of one call must differ from one another (-1 may repeat).
  * d_q_out and the pool overlap neither each other nor an input (QL_EINVAL). Rows, norm weights, d_q_out and the pool 16-byte, tables and slots 8-byte aligned, strides multiples
  * of 16 bytes and at least a row (any when n is 1), below 2^31 elements. n = 0 is allowed, n < 2^31. Asynchronous on stream. */
 int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride, int64_t kv_stride, const float* d_norm_w,

@@ -49,3 +49,33 @@ def test_chunk_value_beyond_f16_stays_behind_the_mask(n, before, heads, hd, rank
         assert np.all(np.abs(got[:at] - want) <= bound)
     # heads whose values f16 holds answer for every query that does not see the row, and for the others as well
     assert np.all(np.isfinite(got[:, 0]))
+
+
+@pytest.mark.parametrize("hd,heads", [(128, 7), (64, 130)])
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("what", ["value", "rotated", "nan"])
+def test_append_query_beyond_f16_is_recorded(hd, heads, f16, what):
+    """One head of one row; written all the same, and no other row or head is spoilt."""
+    ql = lib()
+    n, row, head, rank = 5, 3, heads - 2, 256
+    cos, sin = np.empty((9, 32), np.float32), np.empty((9, 32), np.float32)
+    ql.ql_rope_tables(cos, sin, 1e4)
+    q = torch.randn((n, heads, hd + 64), device="cuda")
+    q[row, head, 11 if what != "rotated" else hd + 5] = math.nan if what == "nan" else 7e4 if what == "value" else 6e4
+    if what == "rotated":       # each half is held, their turn by 45 degrees is not
+        q[row, head, hd + 37] = 6e4
+        cos[4, 5] = sin[4, 5] = math.sqrt(0.5)
+    q = q.half() if f16 else q
+    kv = torch.randn((n, rank + 64), device="cuda").to(q.dtype)
+    pos, slots = torch.tensor([0, 1, 2, 4, 3], dtype=torch.int32, device="cuda"), torch.arange(n, device="cuda")
+    pool = torch.zeros((1, 16, rank + 64), dtype=torch.float16, device="cuda")
+    q_out = torch.full((n, heads, hd + 64), 9.0, dtype=torch.float16, device="cuda")
+    args = (torch.ones(rank, device="cuda"), dev(cos), dev(sin), pos, slots, 1e-6, heads, hd, rank, 64, q_out, pool, 1, 9)
+    ql.ql_mla_append(q, kv, *args)
+    said = recorded()
+    assert f"(index {row}, value {1 + head})" in said, said
+    broken = ~torch.isfinite(q_out).all(-1)
+    assert broken.sum() == 1 and bool(broken[row, head])
+    q[row, head] = 1.0
+    ql.ql_mla_append(q, kv, *args)
+    ql.ql_check_device_error()
