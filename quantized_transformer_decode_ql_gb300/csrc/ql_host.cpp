@@ -85,7 +85,9 @@ static const char* where_name(int w) {
         case kErrKvOverflow: return "KV rows: a block scale or minimum, or a value read back for a prompt chunk, overflows f16 (index = row, value = block or kv head)";
         case kErrKvSlot: return "KV rows: slot outside the pool (index = row, value = slot)";
         case kErrAttnStage: return "4-bit attention: a staged record did not arrive (bounded wait expired; index = sequence, value = block)";
-        case kErrLatentValue: return "latent attention: a value that f16 does not hold (a cache row: index = row, value = 0; a query: index = row, value = 1 + head; an absorbed query: index = sequence, value = head)";
+        case kErrLatentValue: return "latent rows: a value that f16 does not hold (index = row, value = 0 for the cache row, 1 + head for a query)";
+        case kErrLatentQuery: return "latent attention: an absorbed query that f16 does not hold (index = sequence, or token of the chunk, value = head)";
+        case kErrLatentKey: return "latent attention: a key or value that f16 does not hold (index = position in the sequence, value = head)";
         case kErrLatentStage: return "latent attention: a staged copy or product did not arrive (bounded wait expired; index = CTA, value = where)";
         case kErrSampleArg: return "sampling: temperature, top-p, min-p or uniform number out of range (index = row)";
         default: return "unknown";

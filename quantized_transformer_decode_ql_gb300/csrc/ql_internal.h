@@ -54,6 +54,8 @@ enum DevErrWhere {
     kErrAttnStage = 15,
     kErrLatentValue = 16,
     kErrLatentStage = 17,
+    kErrLatentQuery = 18,
+    kErrLatentKey = 19,
 };
 // The current device's record (allocated on first use, zero-filled).
 DevError* device_error_record();

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(ExpandCfg<D, R>::THREADS, 1) __cluster_dims__(
 #pragma unroll
                 for (int i = 0; i < 64; ++i) most = fmaxf(most, fabsf(f[i]));
                 if (in && most >= 65520.f) {
-                    record_device_error(p.err, kErrLatentValue, tok, h);
+                    record_device_error(p.err, kErrLatentKey, tok, h);
                     // a value as the largest that f16 holds: an infinity would meet the weights of 0 of queries that do not see it
                     if (e >= D) {
 #pragma unroll

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
             mma16(c[0], a[0], a[1], a[2], a[3], b[k][0], b[k][1]);
             mma16(c[1], a[0], a[1], a[2], a[3], b[k][2], b[k][3]);
         }
-        bool large = false;
+        bool large[2] = {};             // in the lane's two rows
 #pragma unroll
         for (int i = 0; i < 4; ++i) {   // n tile i / 2, row group i % 2
             const int r = m + (lane >> 2) + 8 * (i & 1);
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const __grid_constant__
                 const __half2 v = __floats2half2_rn(x, y);
                 *reinterpret_cast<__half2*>(dst) = v;
                 if (p.halves == 2) *reinterpret_cast<__half2*>(dst + 64 * WP) = __floats2half2_rn(x - __low2float(v), y - __high2float(v));
-                large |= !(fabsf(x) < 65520.f && fabsf(y) < 65520.f);
+                large[i & 1] |= !(fabsf(x) < 65520.f && fabsf(y) < 65520.f);
             }
         }
-        if (large) record_device_error(p.err, kErrLatentValue, b0 + m, h);
+        if (large[0] || large[1]) record_device_error(p.err, kErrLatentQuery, b0 + m + (lane >> 2) + (large[0] ? 0 : 8), h);
     }
     __syncthreads();
     for (int i = t; i < rows * 8 * p.halves; i += 128) {   // 128 bytes a row and half

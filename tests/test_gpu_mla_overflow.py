@@ -7,7 +7,7 @@ import torch
 
 from gpu_util import dev, lib
 from oracle import mla
-from test_gpu_mla import chunk, latent_case, rows_of
+from test_gpu_mla import chunk, decode, latent_case, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -43,7 +43,8 @@ def test_chunk_value_beyond_f16_stays_behind_the_mask(n, before, heads, hd, rank
     c["pool"][c["table"][0, row // 16], row % 16, :rank] = big
     assert 70000 < big @ w and np.abs(c["w"][:, :hd].astype(np.float64) @ big).max() < 65000
     got = chunk(c, n, before)
-    assert "f16" in recorded()
+    said = recorded()
+    assert "key or value" in said and f"(index {row}, value 1)" in said, said
     if at:
         want, bound = mla.attention(c["q"][:at], rows_of(c, 0, row), c["w"], c["scale"], before=before)
         assert np.all(np.abs(got[:at] - want) <= bound)
@@ -79,3 +80,50 @@ def test_append_query_beyond_f16_is_recorded(hd, heads, f16, what):
     q[row, head] = 1.0
     ql.ql_mla_append(q, kv, *args)
     ql.ql_check_device_error()
+
+
+@pytest.mark.parametrize("hd,rank", [(64, 256), (128, 512)])
+@pytest.mark.parametrize("at,head,heads", [(1, 1, 2), (13, 0, 3), (31, 30, 32), (70, 39, 40)])
+def test_decode_absorbed_query_beyond_f16_names_its_sequence(hd, rank, at, head, heads):
+    c = latent_case([5] * (at + 2), heads, hd, rank, seed=at)
+    c["q"][at, head, :hd] = 6e4
+    c["w"][head, :hd, 7] = np.where(np.arange(hd) < hd // 2, 6e4, 0)
+    c["q"][np.arange(at + 2) != at, head, :hd] = 0
+    decode(c)
+    said = recorded()
+    assert "absorbed query" in said and f"(index {at}, value {head})" in said, said
+
+
+def test_chunk_absorbed_query_beyond_f16_names_its_token():
+    c = latent_case([60 + 20], 32, 128, 512, rows=20, seed=1)
+    c["q"][:, 9, :128] = 0
+    c["q"][17, 9, :128] = 6e4
+    c["w"][9, :128, 300] = 6e4
+    chunk(c, 20, 60)
+    said = recorded()
+    assert "absorbed query" in said and "(index 17, value 9)" in said, said
+
+
+@pytest.mark.parametrize("hd,rank", [(64, 256), (128, 512)])
+def test_chunk_key_beyond_f16_names_its_position(hd, rank):
+    c = latent_case([90], 3, hd, rank, rows=90, seed=4)
+    c["w"][1, 3] = 300.0
+    c["pool"][:, :, :rank] = 0.01
+    c["pool"][c["table"][0, 4], 9, :rank] = 1.0
+    chunk(c, 90, 0)
+    said = recorded()
+    assert "key or value" in said and "(index 73, value 1)" in said, said
+
+
+@pytest.mark.parametrize("value,at,form,records", [(math.nan, "latent", "expanded", False), (math.inf, "latent", "expanded", True), (math.inf, "rotated", "expanded", False),
+                                                   (math.nan, "latent", "absorbed", False), (math.inf, "latent", "absorbed", False)])
+def test_what_a_broken_row_records(value, at, form, records):
+    """An infinite latent makes infinite keys, which are recorded; NaN, or a rotated part, is not a number beyond f16."""
+    heads, hd, rank, n, before = (3, 64, 256, 60, 50) if form == "expanded" else (32, 128, 512, 20, 50)
+    c = latent_case([before + n], heads, hd, rank, rows=n, seed=n)
+    row = before + 10
+    c["pool"][c["table"][0, row // 16], row % 16, rank - 7 if at == "latent" else rank + 5] = value
+    got = chunk(c, n, before)
+    assert np.all(np.isfinite(got[:10]))
+    if records:
+        assert "key or value" in recorded()
