@@ -10,6 +10,8 @@
 // 48 us, 6.7 TB/s of what is read and written (a head a warp, narrower loads: 97 us); a step's rows take 1.6 us.
 #include "ql_mla.h"
 
+#include <algorithm>
+
 namespace ql {
 namespace {
 
@@ -251,10 +253,15 @@ extern "C" int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64
     const size_t size = dtype == QL_DTYPE_F32 ? 4 : 2, q_bytes = d_q ? ((n - 1) * (n > 1 ? q_stride : 0) + q_row) * size : 0;
     const size_t kv_bytes = ((n - 1) * (n > 1 ? kv_stride : 0) + rank + kRope) * size, out_bytes = d_q ? (size_t)n * q_row * 2 : 0;
     const size_t pool_bytes = (size_t)num_blocks * mla::kBlock * (rank + kRope) * 2;
-    QL_REQUIRE(!overlap(d_q_out, out_bytes, d_q, q_bytes) && !overlap(d_q_out, out_bytes, d_kv, kv_bytes) &&
-                   !overlap(d_q_out, out_bytes, d_pool, pool_bytes) && !overlap(d_pool, pool_bytes, d_q, q_bytes) &&
-                   !overlap(d_pool, pool_bytes, d_kv, kv_bytes),
-               "ql_mla_append: the queries' output and the pool overlap each other or an input");
+    // (rows of the tables that an int32 position reaches)
+    const size_t turns = (size_t)std::min<int64_t>(max_position, 1ll << 31) * (kRope / 2) * 4;
+    const struct {
+        const void* p;
+        size_t n;
+    } in[] = {{d_q, q_bytes}, {d_kv, kv_bytes}, {d_norm_w, (size_t)rank * 4}, {d_cos, turns}, {d_sin, turns}, {d_positions, (size_t)n * 4}, {d_slots, (size_t)n * 8}};
+    bool apart = !overlap(d_q_out, out_bytes, d_pool, pool_bytes);
+    for (const auto& i : in) apart = apart && !overlap(d_q_out, out_bytes, i.p, i.n) && !overlap(d_pool, pool_bytes, i.p, i.n);
+    QL_REQUIRE(apart, "ql_mla_append: the queries' output and the pool overlap each other or an input");
     DevError* err = device_error_record();
     if (!err) return set_error(QL_ECUDA, "ql_mla_append: no device error record");
     AppendParams p = {d_q, d_kv, q_stride, kv_stride, d_norm_w, d_cos, d_sin, d_positions,
