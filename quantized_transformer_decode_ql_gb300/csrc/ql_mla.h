@@ -8,7 +8,10 @@ namespace mla {
 
 constexpr int kRope = 64;    // rotated values of a cache row and of a query head
 constexpr int kBlock = 16;   // tokens of a pool block
-constexpr float kLag = 14.f; // log2 of how far a weight may lie above its reference: f16 holds 2^15, and O is scaled rarely
+// The weights of the softmax are f16 numbers relative to a running reference, log2 of which lies kLift below the largest score when it is
+// set: half a step of f16's subnormals is then 2^-31 of the largest weight, so that many keys far below it still count (2^20 keys, each
+// 2^-25.2 of the largest, weigh 2.6% together; with the reference at the largest they were 0). It is moved when a score lies kLag above it.
+constexpr float kLift = 6.f, kLag = 15.f;   // f16 holds 2^15
 
 inline bool shape_ok(int head_dim, int rank) { return (head_dim == 64 || head_dim == 128) && (rank == 256 || rank == 512); }
 

@@ -14,6 +14,7 @@ namespace ql {
 namespace mla {
 
 constexpr int kQ = 128;     // queries of a CTA, keys of a tile
+constexpr float kLow = 5.f; // log2 of the least that a row's largest weight may be with the reference that most rows begin with
 
 // ---------------------------------------------------------------- keys and values
 struct ExpandParams {
@@ -616,10 +617,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 warp_wait(bar + (C::kVEmpty + j % C::STAGES) * 8, (uint32_t)(j / C::STAGES) & 1u, wt, 822);
                 fence_after();
             };
-            // The weights' reference: 0 where the row's first scores allow it (the largest weight of a tile lies between 2^-1 and 2^kLag then),
-            // else their largest, and from then on a running maximum that lags by up to 2^kLag: weights of up to 16384 are as exact in f16
-            // as smaller ones, and O has to be scaled only when a score passes that.
-            float m = 0.f, l = 0.f;
+            // The weights' reference, log2: -kLow where the row's first scores allow it (the largest lies between 0 and kLag - kLow then), else
+            // kLift below their largest; from then on it is moved where a score passes kLag above it. Weights of up to 2^kLag are as exact in f16 as
+            // smaller ones, and O has to be scaled only then.
+            float m = -kLow, l = 0.f;
             bool set = false;
             for (int i = 0; i < mine; ++i) {
                 const int at = (w.j0 + off + 2 * i) * kQ, j = jt + off + 2 * i;
@@ -653,13 +654,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) __cluster_dims__(2, 1, 1) ml
                 // set is known to both halves of its keys only as far as each has seen it: they settle it together where either asks.)
                 unsigned raise;
                 asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %2, 256, a;\n selp.u32 %0, 1, 0, b;\n}"
-                             : "=r"(raise) : "r"((unsigned)(top > m + kLag || (!set && top < -1.f))), "r"(1 + g) : "memory");
+                             : "=r"(raise) : "r"((unsigned)(top > m + kLag || (!set && top < 0.f))), "r"(1 + g) : "memory");
                 if (raise) {
                     tops[g][hf][q] = top;
                     asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + g) : "memory");
                     top = fmaxf(top, tops[g][hf ^ 1][q]);
-                    const bool move = top > -INFINITY && (top > m + kLag || (!set && top < -1.f));
-                    const float now = move ? top : m, f = set ? ex2(m - now) : 0.f;
+                    // (O is scaled for all of the rows, so that each may as well have its reference where it would be set)
+                    const bool move = top > -INFINITY && (top > m + kLift || (!set && top < 0.f));
+                    const float now = move ? top - kLift : m, f = set ? ex2(m - now) : 0.f;
                     m = now;
                     set |= top > -INFINITY;
                     l *= f;

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                         }
                     }
                 };
-                // The reference is a running maximum that lags by up to 2^kLag: weights of up to 16384 are as exact in f16 as
+                // The reference follows the running maximum by steps: weights of up to 2^kLag are as exact in f16 as
                 // smaller ones, and O has to be scaled only when a score passes that.
                 unsigned raise = 1;
                 if (tt > t0) {
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
                         const int h = h0 + tg;
                         const float most = fmaxf(fmaxf(column[0][h], column[1][h]), fmaxf(column[2][h], column[3][h]));
                         // a finite reference where no key is left, so that the next tile's weights stay numbers
-                        const float old = tt == t0 ? -1e30f : -ref[h], now = fmaxf(old, most);
+                        const float old = tt == t0 ? -1e30f : -ref[h], now = fmaxf(old, most - kLift);
                         factor[h] = tt == t0 ? 0.f : ex2(old - now);
                         ref[h] = -now;
                     }
