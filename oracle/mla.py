@@ -4,6 +4,10 @@ A token's cache row is f16(norm(x[:rank]) * w | rot(x[rank:], p)). Head h of a q
 (Wk_h^T q[:hd] . c + q[hd:] . r) * scale with a row (c | r) and value Wv_h c; ``w[h]`` holds the hd rows of Wk_h, then
 those of Wv_h. :func:`attention` makes keys and values of every head (the definition); :func:`absorbed` multiplies the
 weights into the query and into the sum, and is pinned equal to it.
+
+Both give an elementwise bound, every rounding at its worst; it grows with the rank and the context past the answer itself.
+:func:`attention_spread` and :func:`absorbed_spread` give the variance that independent roundings leave instead, from the steps of f16 at
+the very numbers that are rounded, and :func:`off` says how many times that an answer is away.
 """
 from __future__ import annotations
 
@@ -87,3 +91,62 @@ def absorbed(q, rows, w, scale):
           + TINY * p.max(-1, keepdims=True) * np.abs(c).sum(0))
     bound = np.einsum("hr,hdr->hd", do + R * E * np.abs(o), np.abs(w[:, hd:])) + U * np.abs(out) + TINY
     return out, bound
+
+
+# ---------------------------------------------------------------- what independent roundings add up to
+# A rounding is off by something between half a step down and half a step up: step^2 / 12 on average. A weight of the softmax is rounded relative to
+# a reference that is not known here; over mantissas of all sizes alike its step^2 is 2^-20 of its square times 3 / (8 ln 2).
+WEIGHT = 3 / (8 * np.log(2)) * 2.0 ** -20 / 12
+
+
+def rounding(x):
+    """The variance of rounding x to f16."""
+    _, e = np.frexp(x)
+    return 2.0 ** (2 * np.maximum(e - 11, -24)) / 12
+
+
+def attention_spread(q, rows, w, scale, before):
+    """:func:`attention`'s answer and the variance of its error: keys and values as f16, f16 weights, the output as f16."""
+    q = q.astype(np.float64)
+    n, heads, width = q.shape
+    hd, L = width - ROPE, len(rows)
+    seen = np.arange(L)[None] <= before + np.arange(n)[:, None]
+    out, var = np.zeros((n, heads, hd)), np.zeros((n, heads, hd))
+    for h in range(heads):
+        k, v = keys_values(rows, w, h, hd)
+        p = _weights(np.where(seen, q[:, h] @ k.T * scale, -np.inf))
+        o = out[:, h] = p @ v
+        score = scale ** 2 * q[:, h, :hd] ** 2 @ rounding(k[:, :hd]).T           # (the rotated part is f16 already)
+        s2 = p * p * score
+        var[:, h] = (s2 @ v ** 2 - 2 * o * (s2 @ v) + s2.sum(-1, keepdims=True) * o ** 2 + (p * p) @ (rounding(v) + WEIGHT * v ** 2)
+                     + rounding(o))
+    return out, var
+
+
+def absorbed_spread(q, rows, w, scale, pair):
+    """:func:`absorbed`'s answer and the variance of its error: f16 weights, the output as f16, and (not `pair`) the absorbed query as one f16
+    number; as two, and the sum over the rows as two, they are exact beside the rest."""
+    q = q.astype(np.float64)
+    heads, hd = q.shape[0], q.shape[1] - ROPE
+    rows, w = rows.astype(np.float64), w.astype(np.float64)
+    c = rows[:, :-ROPE]
+    qc = np.einsum("hd,hdr->hr", q[:, :hd], w[:, :hd])
+    p = _weights(np.concatenate([qc, q[:, hd:]], -1) @ rows.T * scale)
+    o = p @ c
+    out = np.einsum("hr,hdr->hd", o, w[:, hd:])
+    var = rounding(out)
+    for h in range(heads):
+        v = c @ w[h, hd:].T
+        var[h] += WEIGHT * (p[h] ** 2 @ v ** 2)
+        if not pair:        # one error for all rows: it moves the answer by the values' covariance with the latents
+            m = scale * ((p[h][:, None] * (v - out[h])).T @ c)
+            var[h] += m ** 2 @ rounding(qc[h])
+    return out, var
+
+
+def off(got, want, var):
+    """How many times the spread an answer is away: the root mean square of its error over the last two axes (heads and values), and the
+    largest head's."""
+    e = (got.astype(np.float64) - want) ** 2
+    e, var = e.reshape(-1, *e.shape[-2:]), var.reshape(-1, *e.shape[-2:])
+    return float(np.sqrt(e.mean() / var.mean())), float(np.sqrt(np.max(e.mean(-1) / var.mean(-1))))

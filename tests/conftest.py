@@ -26,3 +26,25 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True)
+def latent_attention_record(request):
+    """The latent attention's GPU tests each start with an empty device error record, so that what one expects is its own, and none may end
+    with a wait that ran out; the other errors of a test are the test's to read."""
+    if not request.module.__name__.startswith("test_gpu_mla") or "gpu" not in request.node.keywords:
+        yield
+        return
+    from gpu_util import lib
+    ql = lib()
+
+    def message():
+        try:
+            ql.ql_check_device_error()
+        except ql.QLError as e:
+            return str(e)
+        return ""
+    message()
+    yield
+    left = message()
+    assert "did not arrive" not in left, left
