@@ -161,10 +161,10 @@ struct DecodeParams {
     CUtensorMap tq;        // absorbed queries: [sequence][run][half][head][64 values]
     const int32_t* tables;
     Lengths lens;
-    float* parts;          // [head group][window + sequence][NH][R]
-    float2* stats;         // [head group][window + sequence][NH]: reference (log2) and sum of the weights
+    float* parts;          // [head group][window + sequence][per][R]
+    float2* stats;         // [head group][window + sequence][per]: reference (log2) and sum of the weights
     long long maxb, cap, num_blocks;   // maxb: entries from a row's table to the next (0: one table)
-    int batch, H, windows, groups;
+    int batch, H, windows, groups, per;   // per: heads of a part, NH or all that there are
     float scale_log2;
     DevError* err;
     unsigned long long ns;
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(cons
             }
             // the part: O^T's lanes are latent values, its columns heads
             const int heads = min(NH, p.H - hg * NH);
-            const size_t part = ((size_t)hg * (p.windows + p.batch) + win + b) * NH;
+            const size_t part = ((size_t)hg * (p.windows + p.batch) + win + b) * p.per;
             {
                 float v[HN];
 #pragma unroll
@@ -651,7 +651,7 @@ struct JoinParams {
     const float2* stats;
     __half* out;           // [batch][H][D]
     long long cap;
-    int batch, H, windows, rows;   // rows: sequences of a cluster, 1, 2, 4 or 8
+    int batch, H, windows, per, rows;   // rows: sequences of a cluster, 1, 2, 4 or 8
 };
 
 // A cluster of four CTAs takes one head and `rows` sequences. Each CTA joins the parts of a quarter of the latent values, hands
@@ -723,17 +723,19 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
         }
         __syncthreads();
     }
-    pdl_wait();
-    pdl_trigger();
     const int g = t / PER, at = t % PER;
     const int split = GROUPS / p.rows, r0 = g / split;   // groups of a sequence (powers of two; at least one)
-    const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r0]) * NH + h % NH) * R + quarter * (R / kJoinCtas)) + at;
+    const float4* src = reinterpret_cast<const float4*>(p.parts + ((base + first[r0]) * p.per + h % NH) * R + quarter * (R / kJoinCtas)) + at;
+    const float2* stats = p.stats + (base + first[warp] + lane) * p.per + h % NH;
+    const size_t next = (size_t)split * (p.per * (R / 4));
     const int c0 = count[r0];
+    pdl_wait();
+    pdl_trigger();
     float4 v[AT_ONCE];
     auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i)
-            v[i] = i0 + i * split < c0 ? __ldcg(src + (size_t)(i0 + i * split) * (NH * R / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = i0 + i * split < c0 ? __ldcg(src + (size_t)i0 * (p.per * (R / 4)) + i * next) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(g % split);
     {
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
         float m = -INFINITY, l = 0.f;
 #pragma unroll
         for (int i = 0; i < MORE; ++i) {
-            s[i] = 32 * i + lane < c ? __ldcg(p.stats + (base + first[r] + 32 * i + lane) * NH + h % NH) : make_float2(-INFINITY, 0.f);
+            s[i] = 32 * i + lane < c ? __ldcg(stats + 32 * i * p.per) : make_float2(-INFINITY, 0.f);
             m = fmaxf(m, s[i].x);
         }
         if (c > 0) {
@@ -838,14 +840,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) __cluster_dims__(kJoinCtas, 1
 
 // ---------------------------------------------------------------- host
 struct DecodeShape {
-    int NH, groups;
+    int NH, groups, per;
     size_t parts, stats, total;   // offsets in the workspace; the absorbed queries come first
 };
 static DecodeShape decode_shape(int64_t batch, int H, int R) {
     DecodeShape s = {};
     s.NH = H <= 32 ? 32 : 64;
     s.groups = (H + s.NH - 1) / s.NH;
-    const size_t win = kMaxWin / s.groups + 1, rows = (size_t)s.groups * (batch + win) * s.NH;
+    s.per = std::min(H, s.NH);
+    const size_t win = kMaxWin / s.groups + 1, rows = (size_t)s.groups * (batch + win) * s.per;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     s.parts = up((size_t)batch * H * (R + kRope) * 2 * (s.NH == 32 ? 2 : 1));
     s.stats = s.parts + rows * R * 4;
@@ -883,10 +886,11 @@ static int decode_go(const AttnIn& a, bool chunk, const DecodeShape& sh, cudaStr
     dp.H = a.H;
     dp.windows = windows;
     dp.groups = sh.groups;
+    dp.per = sh.per;
     dp.scale_log2 = a.scale * 1.44269504088896340736f;
     dp.err = err;
     dp.ns = 2000000000ull;
-    JoinParams jp = {ap.w, dp.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.rows, a.H, windows, kJoinRows};
+    JoinParams jp = {ap.w, dp.lens, dp.parts, dp.stats, static_cast<__half*>(a.out), dp.cap, (int)a.rows, a.H, windows, sh.per, kJoinRows};
     while (jp.rows > 1 && jp.rows / 2 >= a.rows) jp.rows /= 2;
     cudaError_t e = launch(mla_absorb_kernel<D, R>, dim3((unsigned)(a.H * (R / 64)), (unsigned)((a.rows + 63) / 64)), dim3(128), 0, s, true, ap);
     if (e == cudaSuccess) e = launch(mla_decode_kernel<R, NH>, dim3((unsigned)(windows * sh.groups)), dim3(C::THREADS), C::SMEM, s, true, dp);
