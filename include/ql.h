@@ -389,56 +389,75 @@ int ql_paged_attn_decode_kv4(const void* d_q, const void* d_pool, const int32_t*
  * [n_heads][2 head_dim][rank], a head's key rows before its value rows; a query is f16
  * [n_heads][head_dim + rope_dim], the rotated part last. num_blocks < 2^27.
  *
+ * Pairs: a rotation turns value j of a rotated part with value j + rope_dim / 2, as everywhere in
+ * this library. Projections that keep the two numbers of a pair next to each other, (2 j, 2 j + 1),
+ * give wrong answers without an error: the last rope_dim rows of the cache's projection, and those of
+ * each head of the queries' projection, have to be reordered first, row 2 j to place j and row 2 j + 1
+ * to place j + rope_dim / 2.
+ *
  * ql_mla_append: n tokens' projections into the cache and the queries made ready. Row i of d_kv
- * ([rank + rope_dim] of dtype, QL_DTYPE_F32 or QL_DTYPE_F16, kv_stride elements after the row before) goes to slot
- * d_slots[i] % 16 of block d_slots[i] / 16 as f16( x / sqrt(mean x^2 + eps) * d_norm_w | rot ), the mean over
- * the first rank values, rot the rotation of the last rope_dim: pairs (j, j + rope_dim / 2) by the angle of
- * position d_positions[i] (int32 [n]) in the tables d_cos / d_sin, f32 [max_position][rope_dim / 2]
- * (ql_rope_tables with head_dim = rope_dim). Row i of d_q ([n_heads][head_dim + rope_dim] of dtype, q_stride
- * elements apart) is written to row i of d_q_out, f16, contiguous, the last rope_dim values of each head rotated alike. d_q and
- * d_q_out may both be NULL. A slot of -1 marks a row to leave out (a padded batch): neither its
- * cache row nor its query is written. Any other slot outside the pool, or a position outside the tables, leaves
- * the row out too and is recorded in the device error record, as is a cache row or a query with a value that f16 does
- * not hold, or a cache row whose squares' sum f32 does not (the row is written). The slots of one call must differ from one another (-1 may repeat).
- * d_q_out and the pool overlap neither each other nor an input (QL_EINVAL). Rows, norm weights, d_q_out and the pool 16-byte, tables and slots 8-byte aligned, strides multiples
- * of 16 bytes and at least a row (any when n is 1), below 2^31 elements. n = 0 is allowed, n < 2^31. Asynchronous on stream. */
+ * ([rank + rope_dim] of dtype, QL_DTYPE_F32 or QL_DTYPE_F16, kv_stride elements after the row before)
+ * goes to slot d_slots[i] % 16 of block d_slots[i] / 16 as
+ * f16( x / sqrt(mean x^2 + eps) * d_norm_w | rot ), the mean over the first rank values, rot the
+ * rotation of the last rope_dim: pairs (j, j + rope_dim / 2) by the angle of position d_positions[i]
+ * (int32 [n]) in the tables d_cos / d_sin, f32 [max_position][rope_dim / 2] (ql_rope_tables with
+ * head_dim = rope_dim). Row i of d_q ([n_heads][head_dim + rope_dim] of dtype, q_stride elements
+ * apart) is written to row i of d_q_out, f16, contiguous, the last rope_dim values of each head
+ * rotated alike. d_q and d_q_out may both be NULL. A slot of -1 marks a row to leave out (a padded
+ * batch): neither its cache row nor its query is written. Any other slot outside the pool, or a
+ * position outside the tables, leaves the row out too and is recorded in the device error record, as
+ * is a cache row or a query with a value that f16 does not hold, or a cache row whose squares' sum f32
+ * does not (the row is written). The slots of one call must differ from one another (-1 may repeat).
+ * d_q_out and the pool overlap neither each other nor an input (QL_EINVAL). Rows, norm weights,
+ * d_q_out and the pool 16-byte, tables and slots 8-byte aligned, strides multiples of 16 bytes and at
+ * least a row (any when n is 1), below 2^31 elements. n = 0 is allowed, n < 2^31. Asynchronous on
+ * stream. */
 int ql_mla_append(const void* d_q, const void* d_kv, int dtype, int64_t q_stride, int64_t kv_stride, const float* d_norm_w,
                   const float* d_cos, const float* d_sin, const int32_t* d_positions, const int64_t* d_slots, float eps,
                   int64_t n, int n_heads, int head_dim, int rank, int rope_dim, void* d_q_out, void* d_pool,
                   int64_t num_blocks, int64_t max_position, void* stream);
 /* One new token of each sequence (the absorbed form):
- *   out[b][h] = Wv_h sum_{t < context_lens[b]} softmax_t((Wk_h^T q[b][h][0:head_dim] . c_t + q[b][h][head_dim:] . r_t) scale) c_t
- * with row t of sequence b in slot t % 16 of block d_block_tables[b][t / 16]. The weights are multiplied into the query
- * (rounded to f16) and into the sum (rounded to f16), so that the cache is read once, as it is, for up to 64 heads.
- * d_q f16 [batch][n_heads][head_dim + rope_dim]; d_block_tables int32 [batch][max_blocks_per_seq]; d_context_lens int32
- * [batch], each in [0, max_blocks_per_seq * 16]: 0 marks an idle slot, whose output row is left as it was, as is
- * that of a length outside the range (recorded). A block id outside the pool is recorded and its keys left out
- * of the softmax (an output of 0 where none is left). What a sequence's last block holds behind its length does
- * not matter. An absorbed query that f16 does not hold is recorded (its outputs are then not finite).
- * d_out f16 [batch][n_heads * head_dim]. scale positive and finite. batch <= 65535, batch * n_heads < 2^22,
- * max_blocks_per_seq <= 2^20, batch * max_blocks_per_seq < 2^32.
- * q, the weights, the pool and the output 16-byte aligned; output and workspace overlap neither each other nor an
- * input (QL_EINVAL). d_workspace: ql_mla_decode_workspace_bytes(...)
- * bytes, 128-byte aligned, any contents; calls and captured graphs that may run at the same time need
- * workspaces of their own. The split of the work over the SMs is made from the lengths on the
- * device, so that a captured call serves any lengths. */
+ *   out[b][h] = Wv_h sum_{t < context_lens[b]}
+ *               softmax_t((Wk_h^T q[b][h][0:head_dim] . c_t + q[b][h][head_dim:] . r_t) scale) c_t
+ * with row t of sequence b in slot t % 16 of block d_block_tables[b][t / 16]. The weights are
+ * multiplied into the query and into the sum, so that the cache is read once, as it is, for up to 64
+ * heads. The absorbed query enters the scores as two f16 numbers (22 bits) up to 32 heads, as one
+ * above; the sum enters the last product as two, the softmax's weights are one f16 number each.
+ * Against exact arithmetic the outputs are off by 0.0002 - 0.0003 of their root mean square up to 32
+ * heads (a last rounding to f16 alone: 0.0002), by 0.0003 above.
+ * d_q f16 [batch][n_heads][head_dim + rope_dim]; d_block_tables int32 [batch][max_blocks_per_seq];
+ * d_context_lens int32 [batch], each in [0, max_blocks_per_seq * 16]: 0 marks an idle slot, whose
+ * output row is left as it was, as is that of a length outside the range (recorded). A block id outside
+ * the pool is recorded and its keys left out of the softmax (an output of 0 where none is left). What a
+ * sequence's last block holds behind its length does not matter. An absorbed query that f16 does not
+ * hold is recorded (its outputs are then not finite). d_out f16 [batch][n_heads * head_dim]. scale
+ * positive and finite. batch <= 65535, batch * n_heads < 2^22, max_blocks_per_seq <= 2^20,
+ * batch * max_blocks_per_seq < 2^32. q, the weights, the pool and the output 16-byte aligned; output
+ * and workspace overlap neither each other nor an input (QL_EINVAL). d_workspace:
+ * ql_mla_decode_workspace_bytes(...) bytes, 128-byte aligned, any contents; calls and captured graphs
+ * that may run at the same time need workspaces of their own. The split of the work over the SMs is
+ * made from the lengths on the device, so that a captured call serves any lengths. */
 size_t ql_mla_decode_workspace_bytes(int64_t batch, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq);
 int ql_mla_attn_decode(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_tables,
                        const int32_t* d_context_lens, int64_t batch, int n_heads, int head_dim, int rank, int rope_dim,
                        int block_size, int64_t max_blocks_per_seq, int64_t num_blocks, float scale, void* d_out,
                        void* d_workspace, size_t workspace_bytes, void* stream);
-/* A chunk of a prompt (the expanded form): query i of d_q, f16 [n_tokens][n_heads][head_dim + rope_dim], is at
- * position p + i, p = *d_position (int32 [1], device), and attends to rows 0 .. p + i of the sequence whose table is
- * d_block_table (int32 [max_blocks_per_seq]); all of them are in the cache already. Keys and values are made from the
- * latents of the whole context, as f16, in the workspace. Up to 32 tokens are taken through the absorbed form instead where
- * that costs less: n_tokens <= n_heads * head_dim / 128, or n_tokens * n_heads <= 512 under a table of at most 64 blocks.
- * d_out f16 [n_tokens][n_heads * head_dim]. Block ids as for ql_mla_attn_decode (an output of 0 for a query that no key is
- * left for); a position below 0 or a chunk that ends behind the table is recorded and leaves the output as it was. A row
- * that holds NaN or an infinity spoils the outputs of the queries that see it, and no others. A key or value (in the
- * absorbed form: an absorbed query) that f16 does not hold is recorded; only queries that see such a row are then wrong (a value is
- * taken as the largest f16). 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22,
- * max_blocks_per_seq <= 2^16. Alignments and workspace as for ql_mla_attn_decode; ql_mla_chunk_workspace_bytes(...) bytes
- * are enough for fewer tokens under the same table too. */
+/* A chunk of a prompt (the expanded form): query i of d_q, f16 [n_tokens][n_heads][head_dim + rope_dim],
+ * is at position p + i, p = *d_position (int32 [1], device), and attends to rows 0 .. p + i of the
+ * sequence whose table is d_block_table (int32 [max_blocks_per_seq]); all of them are in the cache
+ * already. Keys and values are made from the latents of the whole context, as f16, in the workspace:
+ * outputs are off by 0.0003 - 0.0005 of their root mean square. Up to 32 tokens are taken through the
+ * absorbed form instead where that costs less: n_tokens <= n_heads * head_dim / 128, or
+ * n_tokens * n_heads <= 512 under a table of at most 64 blocks. The same chunk under a longer table
+ * may so take the other form, which has other bits and another error.
+ * d_out f16 [n_tokens][n_heads * head_dim]. Block ids as for ql_mla_attn_decode (an output of 0 for a
+ * query that no key is left for); a position below 0 or a chunk that ends behind the table is recorded
+ * and leaves the output as it was. A row that holds NaN or an infinity spoils the outputs of the
+ * queries that see it, and no others. A key or value (in the absorbed form: an absorbed query) that f16
+ * does not hold is recorded; only queries that see such a row are then wrong (a value is taken as the
+ * largest f16). 1 <= n_tokens <= 65535, n_tokens * n_heads < 2^22, max_blocks_per_seq <= 2^16.
+ * Alignments and workspace as for ql_mla_attn_decode; ql_mla_chunk_workspace_bytes(...) bytes are
+ * enough for fewer tokens under the same table too. */
 size_t ql_mla_chunk_workspace_bytes(int64_t n_tokens, int n_heads, int head_dim, int rank, int64_t max_blocks_per_seq);
 int ql_mla_attn_chunk(const void* d_q, const void* d_w_kv, const void* d_pool, const int32_t* d_block_table,
                       const int32_t* d_position, int64_t n_tokens, int n_heads, int head_dim, int rank, int rope_dim,

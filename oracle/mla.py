@@ -74,7 +74,8 @@ def attention(q, rows, w, scale, before=None):
 
 def absorbed(q, rows, w, scale):
     """The single-token form: q [heads, hd + 64] -> out [heads, hd] and a bound of the error of a kernel that rounds the
-    absorbed query, the weights, the sum over the rows and the output to f16."""
+    absorbed query, the weights, the sum over the rows and the output to f16. (The kernels keep the sum, and up to 32 heads the query, as two
+    f16 numbers: the bound allows for one.)"""
     q = q.astype(np.float64)
     heads, hd, L = q.shape[0], q.shape[1] - ROPE, len(rows)
     rows = rows.astype(np.float64)

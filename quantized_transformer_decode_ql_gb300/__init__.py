@@ -342,7 +342,8 @@ def ql_mla_append(q, kv, norm_w, cos_t, sin_t, positions, slots, eps, n_heads, h
                   max_position, stream=None):
     """Latent rows ``kv`` (f32 or f16 [n, rank + rope_dim], rows may be strided) normalised and rotated into the paged ``pool`` (f16) at
     physical ``slots`` (int64 [n], block * 16 + offset; -1: leave the row out), queries ``q`` ([n, n_heads, head_dim + rope_dim] of the same
-    type, or None) rotated into ``q_out`` (f16, contiguous); ``positions`` int32 [n], the tables f32 [max_position, rope_dim / 2]."""
+    type, or None) rotated into ``q_out`` (f16, contiguous); ``positions`` int32 [n], the tables f32 [max_position, rope_dim / 2]. Pairs of the
+    rotation are (j, j + rope_dim / 2): projections whose pairs lie next to each other have their rows reordered first."""
     name = "ql_mla_append"
     half, whole, long = _types or _torch_types()
     here, row, width = device_index(), rank + rope_dim, head_dim + rope_dim

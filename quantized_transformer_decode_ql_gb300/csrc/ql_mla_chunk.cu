@@ -326,7 +326,7 @@ struct ChunkParams {
 // 256 after 7936, 40 heads, 116.5 -> 105; 1000 after 1000, 8 heads, 27.3 -> 28.4).
 // A causal prompt of 4096 tokens, 32 heads of 128: 129 us, 1.33 PFLOP/s of what the mask leaves. A tile of 256 x 128 takes 1640 - 1740 cycles, its
 // products 1280: with two halves in turn each has a chain of scores (800), maximum (450), exponentials (800), values (600) and the way between the
-// warps (600) for two tiles. From unit to unit go 4 thousand cycles more. The weights are f16 (the product's operand, up to 2^14), their sums f32.
+// warps (600) for two tiles. From unit to unit go 4 thousand cycles more. The weights are f16 (the product's operand, up to 2^15), their sums f32.
 // Without gain: weights before their maximum is known, judged by their sum (registers spill: 156 -> 170 us a prompt).
 template <int D, int NQ>
 struct ChunkCfg {
@@ -374,7 +374,7 @@ struct Row {
         : H(H), blocks((n + 2 * kQ - 1) / (2 * kQ)), past((before + kQ - 1) / kQ), longest((before + n + kQ - 1) / kQ), enter(4) {
         window = max((start(blocks) + pairs - 1) / pairs, kLeast);
         // One block of queries: windows that end where heads end, if they are little longer (256 queries after 7936, 32 heads: 32 tiles of one
-        // head each are 1.2 us shorter than 28 of two).
+        // head each are 1.2 us shorter than 28 of two; the 6 tiles that "little" stands for rest on this one shape).
         if (blocks == 1 && H <= pairs) {
             const int k = pairs / H, even = max((longest + k - 1) / k, kLeast);
             if (even <= window + 6) {
@@ -872,7 +872,8 @@ static ChunkShape chunk_shape(int64_t n, int H, int D, int64_t maxb) {
     ChunkShape s = {};
     s.cap = (maxb * kBlock + 255) / 256 * 256;
     // Few units are cut evenly over the pairs where that costs less, for the longest context that the table holds: rounds of 76 units and the
-    // end of each (about 2 tiles), against their share, a second entry and the join.
+    // end of each (about 2 tiles), against their share, a second entry and the join. (76 pairs: 152 SMs. The workspace's size, which this decides,
+    // is asked for without a device; where another number of pairs is launched the cut is a worse one, not a wrong one.)
     const int64_t units = (n + 2 * kQ - 1) / (2 * kQ) * H, tiles = s.cap / kQ;
     s.cut = units < 152 && (units * (tiles + 2) + 75) / 76 + 5 < (units + 75) / 76 * (tiles + 2);
     auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };

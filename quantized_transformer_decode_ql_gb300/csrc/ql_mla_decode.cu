@@ -6,7 +6,7 @@
 //     window's tiles on the 5th-generation tensor cores, each tile read once for up to 64 heads: S^T = K q'^T (64 keys x heads),
 //     the online softmax, O^T += V^T P (rank x heads), K the tile's rows and V their first `rank` values, the same bytes in
 //     shared memory;
-//  3. mla_join_kernel: a sequence's parts joined, o rounded to f16, out_h = Wv_h o_h.
+//  3. mla_join_kernel: a sequence's parts joined, o as a pair of f16, out_h = Wv_h o_h.
 #include "ql_batched.h"
 #include "ql_mla_tc.cuh"
 
@@ -149,7 +149,7 @@ struct Cfg {
     static constexpr int kKFull = 0, kKEmpty = STAGES, kSFull = 5 * STAGES, kPReady = kSFull + 2, kQFull = kPReady + 2, kQEmpty = kQFull + 1,
                          kDone = kQEmpty + 1, kBars = kDone + 1;
     static constexpr uint32_t PSW = NH == 64 ? 2 : 4;   // P's rows of 2 NH bytes: 128- or 64-byte swizzle
-    static constexpr int HN = NH / 2;                   // heads of a softmax group of four warps (four groups of 16 of 64: 61 instead of 57 us, many heads)
+    static constexpr int HN = NH / 2;                   // heads of a softmax group of four warps (four groups of 16 for 64 heads: 4 us longer, 8 x 4000 - 16000 with 96 heads)
     static constexpr int kSoftWarps = NH / HN * 4, kCopyWarp = kSoftWarps, kScoreWarp = kSoftWarps + 1, kValueWarp = kSoftWarps + 2,
                          THREADS = (kSoftWarps + 3) * 32;
     static_assert(SCOL + 2 * NQ <= 512, "tensor memory");
@@ -274,9 +274,9 @@ __device__ __noinline__ void settle_decode(uint32_t bar, const int* issued, DevE
 // One CTA an SM, a window of the batch's tiles each. Two stages of 64 keys (73.7 KB each at rank 512) and the queries fill shared memory; a
 // stage is freed a block of 16 keys at a time. Scores have the keys as rows and the heads as columns, so that a softmax thread keeps one key's
 // heads in registers and stores its weights as the value product's B operand.
-//  16 x 20000 - 40960, 64 heads, rank 512: 105 us of the call's 119, 5.5 TB/s. A tile takes 2.0 us, 1.75 where the cache is in L2: HBM's latency
+//  16 x 20000 - 40960, 64 heads, rank 512: 106 us of the call's 116, 5.3 TB/s. A tile takes 2.0 us, 1.75 where the cache is in L2: HBM's latency
 //    and the chain of scores, softmax and values through two stages bound it together.
-//  32 x 128 - 8192, 32 heads: 38 us of 51; 5.5 - 5.9 TB/s in the loop, where copies of such tiles alone reach 6.6.
+//  32 x 128 - 8192, 32 heads: 38.6 us of 47.7; 5.5 - 5.9 TB/s in the loop, where copies of such tiles alone reach 6.6.
 template <int R, int NH>
 __global__ void __launch_bounds__(Cfg<R, NH>::THREADS, 1) mla_decode_kernel(const __grid_constant__ DecodeParams p) {
     using C = Cfg<R, NH>;
